@@ -1,9 +1,15 @@
 """Kaczmarz Linear Attention (KLA) for NVIDIA GB300 (sm_103a).
 
 The compute path is the CUDA library ``libkla_gb300.so`` (C ABI in
-``include/kla.h``); ``binding`` is its thin ctypes binding.  ``workloads``
-draws seeded synthetic inputs.
+``include/kla.h``); ``binding`` is its thin ctypes binding, ``attention`` that
+of query and key conditioning.  ``workloads`` draws seeded synthetic inputs.
 """
+from .attention import (  # noqa: F401
+    kla_qk_norm_rope,
+    kla_qk_norm_rope_bwd,
+    kla_qk_norm_rope_bwd_workspace_size,
+    kla_qk_norm_rope_fwd,
+)
 from .binding import (  # noqa: F401
     KlaError,
     kla_ccq_query,

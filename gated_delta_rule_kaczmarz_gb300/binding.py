@@ -110,6 +110,16 @@ def load(build_if_stale: bool = True) -> ctypes.CDLL:
                                               I, I, I, I, I, I, I, vp]
         lib.kla_chunk_fwd_noalloc_status.restype = I
         lib.kla_chunk_fwd_noalloc_status.argtypes = [vp]
+        L = ctypes.c_longlong
+        lib.kla_qk_norm_rope_fwd.restype = I
+        lib.kla_qk_norm_rope_fwd.argtypes = [vp, L, vp, L, fp, fp, ip, fp, vp, L, vp, L,
+                                             I, I, I, I, I, vp, I, I, I, I, F, I, vp]
+        lib.kla_qk_norm_rope_bwd_workspace_size.restype = Z
+        lib.kla_qk_norm_rope_bwd_workspace_size.argtypes = [I, I, I, I]
+        lib.kla_qk_norm_rope_bwd.restype = I
+        lib.kla_qk_norm_rope_bwd.argtypes = [vp, L, vp, L, fp, fp, ip, fp, vp, L, vp, L, vp, L,
+                                             vp, L, fp, fp, I, I, I, I, I, vp, I, I, I, I, F, I,
+                                             vp, Z, vp]
         lib.kla_workspace_status.restype = I
         lib.kla_workspace_status.argtypes = [vp, Z, vp]
         _lib = lib

@@ -210,6 +210,72 @@ int run_bwd(const void *q, const void *k, const void *v, const float *alpha, con
 }
 }  // namespace
 
+namespace {
+// Checks of the conditioning calls; the pointers of q, k and their outputs
+// are given with their strides.
+struct Rows {
+    const void *p;
+    long long stride;
+    int heads;
+    const char *name;
+};
+kla_status check_rows(const Rows &r, int d, int dtype) {
+    const long long es = dtype == KLA_DTYPE_BF16 ? 2 : 4;
+    if (r.heads == 0) return KLA_OK;
+    if (!r.p) return fail(KLA_ERR_INVALID_ARG, "%s must be non-null", r.name);
+    if (!aligned16(r.p)) return fail(KLA_ERR_INVALID_ARG, "%s must be 16-byte aligned", r.name);
+    if (r.stride < (long long)r.heads * d || r.stride * es % 16 != 0)
+        return fail(KLA_ERR_INVALID_ARG,
+                    "%s: the row stride must be at least heads * d elements and a multiple of "
+                    "16 bytes (got %lld)", r.name, r.stride);
+    return KLA_OK;
+}
+
+kla_status check_qk(kla::QkProblem &p, const int *sections) {
+    if (p.tokens < 0 || p.Hq <= 0 || p.Hk < 0)
+        return fail(KLA_ERR_INVALID_ARG, "tokens and Hk must not be negative, Hq positive "
+                    "(tokens=%d Hq=%d Hk=%d)", p.tokens, p.Hq, p.Hk);
+    if (p.dtype != KLA_DTYPE_F32 && p.dtype != KLA_DTYPE_BF16)
+        return fail(KLA_ERR_INVALID_ARG, "unknown dtype %d", p.dtype);
+    if (p.d != 64 && p.d != 128)
+        return fail(KLA_ERR_UNSUPPORTED, "supported head sizes: 64 and 128 (got %d)", p.d);
+    if (p.rot < 0 || p.rot > p.d || p.rot % 16 != 0)
+        return fail(KLA_ERR_UNSUPPORTED,
+                    "the rotated part must be a multiple of 16 in 0..d (got %d)", p.rot);
+    if (p.Hq > 1024 || p.Hk > 1024)
+        return fail(KLA_ERR_UNSUPPORTED, "at most 1024 heads (Hq=%d Hk=%d)", p.Hq, p.Hk);
+    if (p.style != KLA_ROPE_HALF && p.style != KLA_ROPE_PAIRS)
+        return fail(KLA_ERR_INVALID_ARG, "unknown rotation style %d", p.style);
+    if (p.norm_q < KLA_NORM_NONE || p.norm_q > KLA_NORM_L2 || p.norm_k < KLA_NORM_NONE ||
+        p.norm_k > KLA_NORM_L2)
+        return fail(KLA_ERR_INVALID_ARG, "unknown norm mode (%d, %d)", p.norm_q, p.norm_k);
+    if (!(p.eps >= 0.f)) return fail(KLA_ERR_INVALID_ARG, "eps must be >= 0");
+    if (!aligned16(p.wq) || !aligned16(p.wk) || !aligned4(p.positions) || !aligned4(p.inv_freq))
+        return fail(KLA_ERR_INVALID_ARG, "the weights must be 16-byte aligned, positions and "
+                    "inv_freq 4-byte");
+    if (p.rot > 0) {
+        if (p.n_axes < 1 || p.n_axes > 4 || !sections)
+            return fail(KLA_ERR_INVALID_ARG, "1 to 4 position axes with their sections "
+                        "(n_axes=%d)", p.n_axes);
+        long sum = 0;
+        for (int i = 0; i < p.n_axes; ++i) {
+            if (sections[i] < 0 || sections[i] > p.rot / 2)
+                return fail(KLA_ERR_INVALID_ARG, "section %d out of range (%d)", i, sections[i]);
+            p.sections[i] = sections[i];
+            sum += sections[i];
+        }
+        if (sum != p.rot / 2)
+            return fail(KLA_ERR_INVALID_ARG, "the sections must sum to rot / 2 = %d (got %ld)",
+                        p.rot / 2, sum);
+        if (p.tokens > 0 && (!p.positions || !p.inv_freq))
+            return fail(KLA_ERR_INVALID_ARG, "positions and inv_freq must be non-null");
+    } else {
+        p.n_axes = 1;
+    }
+    return KLA_OK;
+}
+}  // namespace
+
 extern "C" {
 
 const char *kla_status_str(int status) {
@@ -474,6 +540,90 @@ int kla_ccq_query_step(const void *q, const void *k, const float *lambda, float 
     cudaError_t e = kla::launch_ccq_step(q, k, lambda, Ms, ms, ns, q_clean, B * H, dk, dtype,
                                          static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "ccq step launch");
+    return ok();
+}
+
+int kla_qk_norm_rope_fwd(const void *q, long long q_stride, const void *k, long long k_stride,
+                         const float *wq, const float *wk, const int *positions,
+                         const float *inv_freq, void *q_out, long long q_out_stride, void *k_out,
+                         long long k_out_stride, int tokens, int Hq, int Hk, int d, int rot,
+                         const int *sections, int n_axes, int style, int norm_q, int norm_k,
+                         float eps, int dtype, void *stream) {
+    kla::QkProblem p{};
+    p.q = q; p.k = k; p.q_stride = q_stride; p.k_stride = k_stride; p.wq = wq; p.wk = wk;
+    p.positions = positions; p.inv_freq = inv_freq; p.q_out = q_out; p.k_out = k_out;
+    p.qo_stride = q_out_stride; p.ko_stride = k_out_stride; p.tokens = tokens; p.Hq = Hq;
+    p.Hk = Hk; p.d = d; p.rot = rot; p.n_axes = n_axes; p.style = style; p.norm_q = norm_q;
+    p.norm_k = norm_k; p.eps = eps; p.dtype = dtype;
+    kla_status st = check_qk(p, sections);
+    if (st != KLA_OK) return st;
+    if (tokens == 0) return ok();
+    const Rows rows[] = {{q, q_stride, Hq, "q"}, {k, k_stride, Hk, "k"},
+                         {q_out, q_out_stride, Hq, "q_out"}, {k_out, k_out_stride, Hk, "k_out"}};
+    for (const Rows &r : rows)
+        if ((st = check_rows(r, d, dtype)) != KLA_OK) return st;
+    if (inject_launch_fault()) return fail(KLA_ERR_CUDA, "injected launch fault (KLA_FAULT_INJECT)");
+    cudaError_t e = kla::launch_qk_fwd(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "conditioning launch");
+    return ok();
+}
+
+size_t kla_qk_norm_rope_bwd_workspace_size(int tokens, int Hq, int Hk, int d) {
+    if (tokens <= 0 || Hq <= 0 || Hk < 0 || (d != 64 && d != 128)) return 0;
+    kla::QkProblem p{};
+    p.tokens = tokens; p.Hq = Hq; p.Hk = Hk; p.d = d; p.n_axes = 1;
+    return kla::qk_bwd_workspace_bytes(p);
+}
+
+int kla_qk_norm_rope_bwd(const void *q, long long q_stride, const void *k, long long k_stride,
+                         const float *wq, const float *wk, const int *positions,
+                         const float *inv_freq, const void *dq_out, long long dq_out_stride,
+                         const void *dk_out, long long dk_out_stride, void *dq,
+                         long long dq_stride, void *dk, long long dk_stride, float *dwq,
+                         float *dwk, int tokens, int Hq, int Hk, int d, int rot,
+                         const int *sections, int n_axes, int style, int norm_q, int norm_k,
+                         float eps, int dtype, void *workspace, size_t workspace_bytes,
+                         void *stream) {
+    kla::QkProblem p{};
+    p.q = q; p.k = k; p.q_stride = q_stride; p.k_stride = k_stride; p.wq = wq; p.wk = wk;
+    p.positions = positions; p.inv_freq = inv_freq; p.gq = dq_out; p.gk = dk_out;
+    p.gq_stride = dq_out_stride; p.gk_stride = dk_out_stride; p.q_out = dq; p.k_out = dk;
+    p.qo_stride = dq_stride; p.ko_stride = dk_stride; p.dwq = dwq; p.dwk = dwk;
+    p.tokens = tokens; p.Hq = Hq; p.Hk = Hk; p.d = d; p.rot = rot; p.n_axes = n_axes;
+    p.style = style; p.norm_q = norm_q; p.norm_k = norm_k; p.eps = eps; p.dtype = dtype;
+    kla_status st = check_qk(p, sections);
+    if (st != KLA_OK) return st;
+    if ((dwq && !wq) || (dwk && (!wk || Hk == 0)))
+        return fail(KLA_ERR_INVALID_ARG, "a weight's gradient requires that weight and its rows");
+    if (!aligned4(dwq) || !aligned4(dwk))
+        return fail(KLA_ERR_INVALID_ARG, "dwq and dwk must be 4-byte aligned");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (tokens > 0) {
+        const Rows rows[] = {{q, q_stride, Hq, "q"}, {k, k_stride, Hk, "k"},
+                             {dq_out, dq_out_stride, Hq, "dq_out"},
+                             {dk_out, dk_out_stride, Hk, "dk_out"}, {dq, dq_stride, Hq, "dq"},
+                             {dk, dk_stride, Hk, "dk"}};
+        for (const Rows &r : rows)
+            if ((st = check_rows(r, d, dtype)) != KLA_OK) return st;
+        if (dwq || dwk) {
+            const size_t need = kla::qk_bwd_workspace_bytes(p);
+            if (workspace == nullptr || workspace_bytes < need)
+                return fail(KLA_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need,
+                            workspace ? workspace_bytes : (size_t)0);
+            if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+                return fail(KLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+            p.ws = workspace;
+        }
+    }
+    if (inject_launch_fault()) return fail(KLA_ERR_CUDA, "injected launch fault (KLA_FAULT_INJECT)");
+    cudaError_t e = cudaSuccess;
+    if (tokens == 0) {      // no rows: the weights' gradients are zero
+        if (dwq) e = cudaMemsetAsync(dwq, 0, d * sizeof(float), s);
+        if (dwk && e == cudaSuccess) e = cudaMemsetAsync(dwk, 0, d * sizeof(float), s);
+    } else {
+        e = kla::launch_qk_bwd(p, s);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "conditioning backward launch");
     return ok();
 }
 

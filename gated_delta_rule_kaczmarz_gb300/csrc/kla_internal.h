@@ -80,6 +80,28 @@ cudaError_t launch_ccq_step(const void *q, const void *k, const float *lambda, f
                             float *ms, float *ns, void *q_clean, int BH, int d, int dtype,
                             cudaStream_t s);
 
+// Query and key conditioning (kla_qk_norm_rope.cu).  Strides are elements
+// between token rows; the heads of a row are d apart.
+struct QkProblem {
+    const void *q, *k;              // k may be null with Hk = 0
+    const void *gq, *gk;            // backward: gradients of q_out and k_out
+    void *q_out, *k_out;            // backward: dq, dk
+    long long q_stride, k_stride, gq_stride, gk_stride, qo_stride, ko_stride;
+    const float *wq, *wk;           // [d] or nullptr
+    float *dwq, *dwk;               // backward: [d] or nullptr
+    const int *positions;           // [n_axes][tokens]
+    const float *inv_freq;          // [rot / 2]
+    int tokens, Hq, Hk, d, rot;
+    int sections[4], n_axes;        // frequency pairs of each axis, in order
+    int style, norm_q, norm_k;      // kla_rope_style, kla_norm_mode
+    float eps;
+    int dtype;
+    void *ws;                       // backward: qk_bwd_workspace_bytes(p)
+};
+size_t qk_bwd_workspace_bytes(const QkProblem &p);
+cudaError_t launch_qk_fwd(const QkProblem &p, cudaStream_t s);
+cudaError_t launch_qk_bwd(const QkProblem &p, cudaStream_t s);
+
 // Backward of the chunkwise forward (kla_chunk_bwd.cu), fixed length or varlen.
 struct BwdProblem {
     const void *q, *k, *v, *dout;

@@ -83,6 +83,17 @@ typedef enum {
     KLA_BETA_GIVEN = 1         /* beta_t = eta_t */
 } kla_beta_mode;
 
+typedef enum {
+    KLA_NORM_NONE = 0,         /* the row as it is */
+    KLA_NORM_RMS = 1,          /* x / sqrt(mean(x^2) + eps) */
+    KLA_NORM_L2 = 2            /* x / sqrt(sum(x^2) + eps) */
+} kla_norm_mode;
+
+typedef enum {
+    KLA_ROPE_HALF = 0,         /* pair i of rot/2: features i and i + rot/2 */
+    KLA_ROPE_PAIRS = 1         /* pair i: features 2i and 2i + 1 */
+} kla_rope_style;
+
 /* Static string for a status code; never NULL. */
 KLA_API const char *kla_status_str(int status);
 
@@ -343,6 +354,67 @@ KLA_API int kla_ccq_query(const void *q, const void *k, const float *lambda,
 KLA_API int kla_ccq_query_step(const void *q, const void *k, const float *lambda, float *Ms,
                                float *ms, float *ns, void *q_clean, int B, int H, int dk,
                                int dtype, void *stream);
+
+/*
+ * Query and key conditioning in one pass over q and k, before the token mixer
+ * (kla_chunk_fwd, kla_decode_step, kla_attn_fwd): a norm of every head's row
+ * and the rotary positions.  Per token t and head,
+ *
+ *     y = x r w,   r by kla_norm_mode over the d features (a row of sum 0 with
+ *                  eps = 0 stays 0), w = wq / wk or none
+ *     pair i of rot/2 is turned by positions[axis(i)][t] * inv_freq[i]:
+ *     (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin)
+ *
+ * and the features from rot on pass through.  KLA's write coefficient takes
+ * the key's norm, which a rotation keeps: keys for KLA_BETA_KACZMARZ go with
+ * KLA_NORM_NONE, keys for a given beta usually with KLA_NORM_L2.
+ *   q, k          : `tokens` rows of Hq and Hk heads of d (dtype), rows
+ *                   q_stride / k_stride elements apart, so that both may lie
+ *                   in a fused projection's output.  Hk = 0 with k and k_out
+ *                   NULL: q alone.
+ *   wq, wk        : [d] fp32 or NULL (no weight), 16-byte aligned
+ *   positions     : [n_axes][tokens] int32, any values
+ *   inv_freq      : [rot / 2] fp32, in radians per position.  The angle is
+ *                   the exact product, reduced in integer arithmetic, so far
+ *                   positions lose nothing.
+ *   sections      : host array of n_axes (1 to 4) counts of frequency pairs:
+ *                   the first sections[0] pairs take axis 0 and so on (time,
+ *                   height, width); they sum to rot / 2.
+ *   q_out, k_out  : written, rows q_out_stride / k_out_stride elements apart;
+ *                   may be q and k themselves (same stride: in place), and
+ *                   may not overlap them otherwise
+ * d in {64, 128}; rot a multiple of 16 in 0..d (0: norm only, positions,
+ * inv_freq and sections unused); at most 1024 heads; strides a multiple of 16
+ * bytes and at least heads * d.  tokens == 0 is valid.  Arithmetic is fp32,
+ * rounded once.  One launch, no workspace.
+ */
+KLA_API int kla_qk_norm_rope_fwd(const void *q, long long q_stride, const void *k,
+                                 long long k_stride, const float *wq, const float *wk,
+                                 const int *positions, const float *inv_freq, void *q_out,
+                                 long long q_out_stride, void *k_out, long long k_out_stride,
+                                 int tokens, int Hq, int Hk, int d, int rot, const int *sections,
+                                 int n_axes, int style, int norm_q, int norm_k, float eps,
+                                 int dtype, void *stream);
+
+/*
+ * Backward of kla_qk_norm_rope_fwd on the same inputs: from the gradients of
+ * its outputs (dq_out, dk_out: dtype, strided rows) those of q, k (dq, dk,
+ * written, strided; dq may be dq_out itself) and of the weights (dwq, dwk: [d]
+ * fp32, written unless NULL; NULL where there is no weight).  The weights'
+ * gradients are summed in a fixed order.  workspace:
+ * kla_qk_norm_rope_bwd_workspace_size(...) bytes, 256-byte aligned, scratch
+ * (unused without dwq and dwk).  It carries no status word.
+ */
+KLA_API size_t kla_qk_norm_rope_bwd_workspace_size(int tokens, int Hq, int Hk, int d);
+KLA_API int kla_qk_norm_rope_bwd(const void *q, long long q_stride, const void *k,
+                                 long long k_stride, const float *wq, const float *wk,
+                                 const int *positions, const float *inv_freq, const void *dq_out,
+                                 long long dq_out_stride, const void *dk_out,
+                                 long long dk_out_stride, void *dq, long long dq_stride, void *dk,
+                                 long long dk_stride, float *dwq, float *dwk, int tokens, int Hq,
+                                 int Hk, int d, int rot, const int *sections, int n_axes,
+                                 int style, int norm_q, int norm_k, float eps, int dtype,
+                                 void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Synchronises `stream` and returns the status that the last prefill call
