@@ -2,9 +2,18 @@
 
 The compute path is the CUDA library ``libkla_gb300.so`` (C ABI in
 ``include/kla.h``); ``binding`` is its thin ctypes binding, ``attention`` that
-of query and key conditioning.  ``workloads`` draws seeded synthetic inputs.
+of query and key conditioning and of causal attention.  ``workloads`` draws seeded synthetic inputs.
 """
 from .attention import (  # noqa: F401
+    kla_attn,
+    kla_attn_bwd,
+    kla_attn_bwd_varlen,
+    kla_attn_bwd_varlen_workspace_size,
+    kla_attn_bwd_workspace_size,
+    kla_attn_fwd,
+    kla_attn_fwd_varlen,
+    kla_attn_fwd_varlen_workspace_size,
+    kla_attn_fwd_workspace_size,
     kla_qk_norm_rope,
     kla_qk_norm_rope_bwd,
     kla_qk_norm_rope_bwd_workspace_size,

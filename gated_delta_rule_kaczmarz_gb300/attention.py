@@ -231,3 +231,176 @@ def kla_qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, norm
     k is None, with gradients for q, k, wq and wk."""
     how = dict(eps=float(eps), norm_q=norm_q, norm_k=norm_k, sections=sections, style=style)
     return _QkNormRope.apply(q, k, positions, inv_freq, wq, wk, how)
+
+
+# ------------------------------------------------------------------ attention
+def kla_attn_fwd_workspace_size(B, Tq, Tk, Hq, Hk, d, dtype=1) -> int:
+    return int(load().kla_attn_fwd_workspace_size(B, Tq, Tk, Hq, Hk, d, dtype))
+
+
+def kla_attn_fwd_varlen_workspace_size(N, total_q, total_k, Hq, Hk, d, dtype=1) -> int:
+    return int(load().kla_attn_fwd_varlen_workspace_size(N, total_q, total_k, Hq, Hk, d, dtype))
+
+
+def kla_attn_bwd_workspace_size(B, Tq, Tk, Hq, Hk, d, dtype=1) -> int:
+    return int(load().kla_attn_bwd_workspace_size(B, Tq, Tk, Hq, Hk, d, dtype))
+
+
+def kla_attn_bwd_varlen_workspace_size(N, total_q, total_k, Hq, Hk, d, dtype=1) -> int:
+    return int(load().kla_attn_bwd_varlen_workspace_size(N, total_q, total_k, Hq, Hk, d, dtype))
+
+
+def _qkv(q, k, v, dims):
+    """Checks q, k, v of `dims` dimensions; returns their row strides, the
+    dtype code and (Hq, Hk, d)."""
+    if q.dim() != dims:
+        raise ValueError(f"q must have {dims} dimensions, got {tuple(q.shape)}")
+    dt = _dtype_code(q)
+    qs = _rows(q, "q")
+    hq, d = q.shape[-2:]
+    if k.dim() != dims or (dims == 4 and k.shape[0] != q.shape[0]):
+        raise ValueError(f"k must have q's batch, got {tuple(k.shape)}")
+    ks = _rows(k, "k", q, None, None, d)
+    vs = _rows(v, "v", q, k.shape[:-2], k.shape[-2], d)
+    return (_ptr(q), qs, _ptr(k), ks, _ptr(v), vs), dt, (hq, k.shape[-2], d)
+
+
+def _out(t, name, shape, dtype, device, want=True):
+    if t is None and want:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, name, device, dtype, shape)
+    return t
+
+
+def _scale(scale, d):
+    return 1.0 / math.sqrt(d) if scale is None else float(scale)
+
+
+def kla_attn_fwd(q, k, v, scale=None, k_lens=None, o=None, lse=None, return_lse=True,
+                 workspace=None, stream=None):
+    """Causal attention with grouped heads.  q: [B,Tq,Hq,d], k, v: [B,Tk,Hk,d];
+    query i sees the keys j <= i + Tk - Tq (one token over a cache: Tq = 1);
+    k_lens: int32 [B], the keys of each sequence of a padded cache, or None
+    (all Tk); scale: 1/sqrt(d) unless given.  Returns (o, lse), o dense, lse
+    [B,Tq,Hq] fp32 (None with return_lse=False)."""
+    rows, dt, (hq, hk, d) = _qkv(q, k, v, 4)
+    B, Tq, Tk = q.shape[0], q.shape[1], k.shape[1]
+    _need(k_lens, "k_lens", q.device, torch.int32, (B,))
+    o = _out(o, "o", q.shape, q.dtype, q.device)
+    lse = _out(lse, "lse", (B, Tq, hq), torch.float32, q.device, return_lse)
+    lib = load()
+    with _device(q.device):
+        need = int(lib.kla_attn_fwd_workspace_size(B, Tq, Tk, hq, hk, d, dt))
+    workspace, wsb = _workspace(need, q.device, workspace)
+    _call(q.device, stream, lib.kla_attn_fwd, *rows, _ptr(k_lens), _scale(scale, d), _ptr(o),
+          _ptr(lse), B, Tq, Tk, hq, hk, d, dt, _ptr(workspace), wsb)
+    return o, lse
+
+
+def _tables(q, cu_q, cu_k):
+    if cu_k is None:
+        cu_k = cu_q
+    _need(cu_q, "cu_seqlens_q", q.device, torch.int32, (cu_q.numel(),))
+    _need(cu_k, "cu_seqlens_k", q.device, torch.int32, (cu_q.numel(),))
+    if cu_q.numel() < 1:
+        raise ValueError("cu_seqlens_q must have N + 1 entries")
+    return cu_k, cu_q.numel() - 1
+
+
+def kla_attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, o=None, lse=None,
+                        return_lse=True, workspace=None, stream=None, check_status=False):
+    """kla_attn_fwd over packed sequences: q [total_q,Hq,d], k, v [total_k,Hk,d],
+    cu_seqlens_q, cu_seqlens_k: int32 [N+1] on the device (cu_seqlens_k None:
+    the same table).  Returns (o, lse)."""
+    rows, dt, (hq, hk, d) = _qkv(q, k, v, 3)
+    cu_k, N = _tables(q, cu_seqlens_q, cu_seqlens_k)
+    nq, nk = q.shape[0], k.shape[0]
+    o = _out(o, "o", q.shape, q.dtype, q.device)
+    lse = _out(lse, "lse", (nq, hq), torch.float32, q.device, return_lse)
+    lib = load()
+    with _device(q.device):
+        need = int(lib.kla_attn_fwd_varlen_workspace_size(N, nq, nk, hq, hk, d, dt))
+    workspace, wsb = _workspace(need, q.device, workspace)
+    _call(q.device, stream, lib.kla_attn_fwd_varlen, *rows, _ptr(cu_seqlens_q), _ptr(cu_k),
+          _scale(scale, d), _ptr(o), _ptr(lse), N, nq, nk, hq, hk, d, dt, _ptr(workspace), wsb)
+    if check_status:
+        _call(q.device, stream, lib.kla_workspace_status, _ptr(workspace), wsb)
+    return o, lse
+
+
+def _grads(q, k, v, o, lse, d_o, dq, dk, dv):
+    """Checks what the backward takes and allocates what it writes."""
+    gs = _rows(d_o, "d_o", q, q.shape[:-2], *q.shape[-2:])
+    _need(o, "o", q.device, q.dtype, q.shape)
+    _need(lse, "lse", q.device, torch.float32, q.shape[:-1])
+    dq = _out(dq, "dq", q.shape, q.dtype, q.device)
+    dk = _out(dk, "dk", k.shape, k.dtype, k.device)
+    dv = _out(dv, "dv", v.shape, v.dtype, v.device)
+    return gs, dq, dk, dv
+
+
+def kla_attn_bwd(q, k, v, o, lse, d_o, scale=None, dq=None, dk=None, dv=None, workspace=None,
+                 stream=None):
+    """Backward of kla_attn_fwd (without k_lens): the gradients of sum <d_o, o>
+    from the forward's inputs and its o and lse.  Returns (dq, dk, dv), dense."""
+    rows, dt, (hq, hk, d) = _qkv(q, k, v, 4)
+    B, Tq, Tk = q.shape[0], q.shape[1], k.shape[1]
+    gs, dq, dk, dv = _grads(q, k, v, o, lse, d_o, dq, dk, dv)
+    lib = load()
+    with _device(q.device):
+        need = int(lib.kla_attn_bwd_workspace_size(B, Tq, Tk, hq, hk, d, dt))
+    workspace, wsb = _workspace(need, q.device, workspace)
+    _call(q.device, stream, lib.kla_attn_bwd, *rows, _ptr(o), _ptr(lse), _ptr(d_o), gs,
+          _scale(scale, d), _ptr(dq), _ptr(dk), _ptr(dv), B, Tq, Tk, hq, hk, d, dt,
+          _ptr(workspace), wsb)
+    return dq, dk, dv
+
+
+def kla_attn_bwd_varlen(q, k, v, o, lse, d_o, cu_seqlens_q, cu_seqlens_k=None, scale=None,
+                        dq=None, dk=None, dv=None, workspace=None, stream=None,
+                        check_status=False):
+    """Backward of kla_attn_fwd_varlen; otherwise as kla_attn_bwd."""
+    rows, dt, (hq, hk, d) = _qkv(q, k, v, 3)
+    cu_k, N = _tables(q, cu_seqlens_q, cu_seqlens_k)
+    nq, nk = q.shape[0], k.shape[0]
+    gs, dq, dk, dv = _grads(q, k, v, o, lse, d_o, dq, dk, dv)
+    lib = load()
+    with _device(q.device):
+        need = int(lib.kla_attn_bwd_varlen_workspace_size(N, nq, nk, hq, hk, d, dt))
+    workspace, wsb = _workspace(need, q.device, workspace)
+    _call(q.device, stream, lib.kla_attn_bwd_varlen, *rows, _ptr(o), _ptr(lse), _ptr(d_o), gs,
+          _ptr(cu_seqlens_q), _ptr(cu_k), _scale(scale, d), _ptr(dq), _ptr(dk), _ptr(dv), N, nq,
+          nk, hq, hk, d, dt, _ptr(workspace), wsb)
+    if check_status:
+        _call(q.device, stream, lib.kla_workspace_status, _ptr(workspace), wsb)
+    return dq, dk, dv
+
+
+class _KlaAttn(torch.autograd.Function):
+    """Causal attention under autograd: kla_attn_fwd[_varlen] and its backward."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, scale, cu_q, cu_k):
+        if cu_q is None:
+            o, lse = kla_attn_fwd(q, k, v, scale)
+        else:
+            o, lse = kla_attn_fwd_varlen(q, k, v, cu_q, cu_k, scale)
+        ctx.save_for_backward(q, k, v, o, lse, cu_q, cu_k)
+        ctx.scale = scale
+        return o
+
+    @staticmethod
+    def backward(ctx, d_o):
+        q, k, v, o, lse, cu_q, cu_k = ctx.saved_tensors
+        d_o = _dense_rows(d_o, o)
+        if cu_q is None:
+            grads = kla_attn_bwd(q, k, v, o, lse, d_o, ctx.scale)
+        else:
+            grads = kla_attn_bwd_varlen(q, k, v, o, lse, d_o, cu_q, cu_k, ctx.scale)
+        return *grads, None, None, None
+
+
+def kla_attn(q, k, v, scale=None, cu_seqlens_q=None, cu_seqlens_k=None):
+    """Differentiable causal attention: o, with gradients for q, k and v.  A
+    batch [B,T,H,d], or packed sequences [total,H,d] with their tables."""
+    return _KlaAttn.apply(q, k, v, scale, cu_seqlens_q, cu_seqlens_k)

@@ -120,6 +120,17 @@ def load(build_if_stale: bool = True) -> ctypes.CDLL:
         lib.kla_qk_norm_rope_bwd.argtypes = [vp, L, vp, L, fp, fp, ip, fp, vp, L, vp, L, vp, L,
                                              vp, L, fp, fp, I, I, I, I, I, vp, I, I, I, I, F, I,
                                              vp, Z, vp]
+        for name in ("kla_attn_fwd", "kla_attn_fwd_varlen", "kla_attn_bwd",
+                     "kla_attn_bwd_varlen"):
+            size = getattr(lib, name + "_workspace_size")
+            size.restype = Z
+            size.argtypes = [I, I, I, I, I, I, I]
+            getattr(lib, name).restype = I
+        rows, end = [vp, L, vp, L, vp, L], [I, I, I, I, I, I, I, vp, Z, vp]
+        lib.kla_attn_fwd.argtypes = [*rows, ip, F, vp, fp, *end]
+        lib.kla_attn_fwd_varlen.argtypes = [*rows, ip, ip, F, vp, fp, *end]
+        lib.kla_attn_bwd.argtypes = [*rows, vp, fp, vp, L, F, vp, vp, vp, *end]
+        lib.kla_attn_bwd_varlen.argtypes = [*rows, vp, fp, vp, L, ip, ip, F, vp, vp, vp, *end]
         lib.kla_workspace_status.restype = I
         lib.kla_workspace_status.argtypes = [vp, Z, vp]
         _lib = lib

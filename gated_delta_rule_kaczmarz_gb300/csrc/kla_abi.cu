@@ -627,6 +627,186 @@ int kla_qk_norm_rope_bwd(const void *q, long long q_stride, const void *k, long 
     return ok();
 }
 
+}  // extern "C"
+
+namespace {
+// Checks and runs a forward or backward attention request whose sizes and
+// pointers are in p.
+kla_status run_attn(kla::AttnProblem &p, bool backward, void *workspace, size_t workspace_bytes,
+                    void *stream) {
+    kla_status st;
+    const Rows rows[] = {{p.q, p.q_stride, p.total_q ? p.Hq : 0, "q"},
+                         {p.k, p.k_stride, p.total_k ? p.Hk : 0, "k"},
+                         {p.v, p.v_stride, p.total_k ? p.Hk : 0, "v"},
+                         {p.go, p.go_stride, backward && p.total_q ? p.Hq : 0, "d_o"}};
+    for (const Rows &r : rows)
+        if ((st = check_rows(r, p.d, p.dtype)) != KLA_OK) return st;
+    if (p.total_q > 0 && (backward ? (!p.o || !p.lse_in || !p.dq) : !p.out))
+        return fail(KLA_ERR_INVALID_ARG, "o (backward: o, lse and dq) must be non-null");
+    if (backward && p.total_k > 0 && (!p.dk || !p.dv))
+        return fail(KLA_ERR_INVALID_ARG, "dk and dv must be non-null");
+    if (!aligned16(p.o) || !aligned16(p.out) || !aligned16(p.dq) || !aligned16(p.dk) ||
+        !aligned16(p.dv) || !aligned4(p.lse) || !aligned4(p.lse_in) || !aligned4(p.cu_q) ||
+        !aligned4(p.cu_k) || !aligned4(p.k_lens))
+        return fail(KLA_ERR_INVALID_ARG, "o and the gradients must be 16-byte aligned, lse and "
+                    "the length tables 4-byte");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (p.total_q == 0) {      // no queries: the keys' gradients are zero
+        if (inject_launch_fault()) return fail(KLA_ERR_CUDA, "injected launch fault (KLA_FAULT_INJECT)");
+        const size_t n = (size_t)p.total_k * p.Hk * p.d * (p.dtype == KLA_DTYPE_BF16 ? 2 : 4);
+        cudaError_t e = cudaSuccess;
+        if (backward && n) e = cudaMemsetAsync(p.dk, 0, n, s);
+        if (backward && n && e == cudaSuccess) e = cudaMemsetAsync(p.dv, 0, n, s);
+        return e == cudaSuccess ? ok() : cuda_fail(e, "gradient reset");
+    }
+    const size_t need = backward ? kla::attn_bwd_workspace_bytes(p) : kla::attn_fwd_workspace_bytes(p);
+    if (workspace == nullptr || workspace_bytes < need)
+        return fail(KLA_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need,
+                    workspace ? workspace_bytes : (size_t)0);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(KLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (inject_launch_fault()) return fail(KLA_ERR_CUDA, "injected launch fault (KLA_FAULT_INJECT)");
+    p.ws = workspace;
+    cudaError_t e = backward ? kla::launch_attn_bwd(p, s) : kla::launch_attn_fwd(p, s);
+    if (e != cudaSuccess) return cuda_fail(e, backward ? "attention backward launch" : "attention launch");
+    return ok();
+}
+
+// Sizes of a request; total_k and total_q come with it.
+kla_status check_attn(const kla::AttnProblem &p) {
+    if (p.Hq <= 0 || p.Hk <= 0 || p.Hq % p.Hk != 0)
+        return fail(KLA_ERR_INVALID_ARG, "Hq must be a positive multiple of Hk (Hq=%d Hk=%d)",
+                    p.Hq, p.Hk);
+    if (p.dtype != KLA_DTYPE_F32 && p.dtype != KLA_DTYPE_BF16)
+        return fail(KLA_ERR_INVALID_ARG, "unknown dtype %d", p.dtype);
+    if (p.d != 64 && p.d != 128)
+        return fail(KLA_ERR_UNSUPPORTED, "supported head sizes: 64 and 128 (got %d)", p.d);
+    if (p.Hq > 1024) return fail(KLA_ERR_UNSUPPORTED, "at most 1024 heads (Hq=%d)", p.Hq);
+    if (p.n_seq > 0 && p.total_q > 0 && kla::attn_too_large(p))
+        return fail(KLA_ERR_UNSUPPORTED, "problem too large (tiles must fit in int32)");
+    return KLA_OK;
+}
+kla_status fixed_attn(kla::AttnProblem &p, int B, int Tq, int Tk) {
+    if (B < 0 || Tq < 0 || Tk < 0)
+        return fail(KLA_ERR_INVALID_ARG, "negative size (B=%d Tq=%d Tk=%d)", B, Tq, Tk);
+    if ((long long)B * Tq > INT32_MAX || (long long)B * Tk > INT32_MAX)
+        return fail(KLA_ERR_UNSUPPORTED, "problem too large (B*Tq and B*Tk must fit in int32)");
+    p.n_seq = B; p.Tq = Tq; p.Tk = Tk; p.total_q = B * Tq; p.total_k = B * Tk;
+    return check_attn(p);
+}
+kla_status packed_attn(kla::AttnProblem &p, int N, int total_q, int total_k, const int *cu_q,
+                       const int *cu_k) {
+    if (N < 0 || total_q < 0 || total_k < 0)
+        return fail(KLA_ERR_INVALID_ARG, "negative size (N=%d total_q=%d total_k=%d)", N, total_q,
+                    total_k);
+    if (N == 0 && (total_q != 0 || total_k != 0))
+        return fail(KLA_ERR_INVALID_ARG, "N == 0 requires no tokens");
+    p.n_seq = N; p.total_q = total_q; p.total_k = total_k; p.cu_q = cu_q; p.cu_k = cu_k;
+    return check_attn(p);
+}
+kla_status check_scale(float scale) {
+    if (!(scale > 0.f) || scale > 3e38f)
+        return fail(KLA_ERR_INVALID_ARG, "scale must be positive and finite");
+    return KLA_OK;
+}
+}  // namespace
+
+extern "C" {
+
+size_t kla_attn_fwd_workspace_size(int B, int Tq, int Tk, int Hq, int Hk, int d, int dtype) {
+    kla::AttnProblem p{};
+    p.Hq = Hq; p.Hk = Hk; p.d = d; p.dtype = dtype;
+    if (fixed_attn(p, B, Tq, Tk) != KLA_OK || p.total_q == 0) return 0;
+    return kla::attn_fwd_workspace_bytes(p);
+}
+
+size_t kla_attn_fwd_varlen_workspace_size(int N, int total_q, int total_k, int Hq, int Hk, int d,
+                                          int dtype) {
+    kla::AttnProblem p{};
+    p.Hq = Hq; p.Hk = Hk; p.d = d; p.dtype = dtype;
+    static const int some = 0;      // packed: the tables' contents are not read here
+    if (packed_attn(p, N, total_q, total_k, &some, &some) != KLA_OK || total_q == 0) return 0;
+    return kla::attn_fwd_workspace_bytes(p);
+}
+
+size_t kla_attn_bwd_workspace_size(int B, int Tq, int Tk, int Hq, int Hk, int d, int dtype) {
+    kla::AttnProblem p{};
+    p.Hq = Hq; p.Hk = Hk; p.d = d; p.dtype = dtype;
+    if (fixed_attn(p, B, Tq, Tk) != KLA_OK || p.total_q == 0) return 0;
+    return kla::attn_bwd_workspace_bytes(p);
+}
+
+size_t kla_attn_bwd_varlen_workspace_size(int N, int total_q, int total_k, int Hq, int Hk, int d,
+                                          int dtype) {
+    kla::AttnProblem p{};
+    p.Hq = Hq; p.Hk = Hk; p.d = d; p.dtype = dtype;
+    static const int some = 0;
+    if (packed_attn(p, N, total_q, total_k, &some, &some) != KLA_OK || total_q == 0) return 0;
+    return kla::attn_bwd_workspace_bytes(p);
+}
+
+int kla_attn_fwd(const void *q, long long q_stride, const void *k, long long k_stride,
+                 const void *v, long long v_stride, const int *k_lens, float scale, void *o,
+                 float *lse, int B, int Tq, int Tk, int Hq, int Hk, int d, int dtype,
+                 void *workspace, size_t workspace_bytes, void *stream) {
+    kla::AttnProblem p{};
+    p.q = q; p.k = k; p.v = v; p.q_stride = q_stride; p.k_stride = k_stride;
+    p.v_stride = v_stride; p.k_lens = k_lens; p.scale = scale; p.out = o; p.lse = lse;
+    p.Hq = Hq; p.Hk = Hk; p.d = d; p.dtype = dtype;
+    kla_status st = fixed_attn(p, B, Tq, Tk);
+    if (st != KLA_OK || (st = check_scale(scale)) != KLA_OK) return st;
+    return run_attn(p, false, workspace, workspace_bytes, stream);
+}
+
+int kla_attn_fwd_varlen(const void *q, long long q_stride, const void *k, long long k_stride,
+                        const void *v, long long v_stride, const int *cu_seqlens_q,
+                        const int *cu_seqlens_k, float scale, void *o, float *lse, int N,
+                        int total_q, int total_k, int Hq, int Hk, int d, int dtype,
+                        void *workspace, size_t workspace_bytes, void *stream) {
+    kla::AttnProblem p{};
+    p.q = q; p.k = k; p.v = v; p.q_stride = q_stride; p.k_stride = k_stride;
+    p.v_stride = v_stride; p.scale = scale; p.out = o; p.lse = lse;
+    p.Hq = Hq; p.Hk = Hk; p.d = d; p.dtype = dtype;
+    kla_status st = packed_attn(p, N, total_q, total_k, cu_seqlens_q, cu_seqlens_k);
+    if (st != KLA_OK || (st = check_scale(scale)) != KLA_OK) return st;
+    if (N > 0 && (!cu_seqlens_q || !cu_seqlens_k))
+        return fail(KLA_ERR_INVALID_ARG, "cu_seqlens_q and cu_seqlens_k must be non-null");
+    return run_attn(p, false, workspace, workspace_bytes, stream);
+}
+
+int kla_attn_bwd(const void *q, long long q_stride, const void *k, long long k_stride,
+                 const void *v, long long v_stride, const void *o, const float *lse,
+                 const void *d_o, long long d_o_stride, float scale, void *dq, void *dk, void *dv,
+                 int B, int Tq, int Tk, int Hq, int Hk, int d, int dtype, void *workspace,
+                 size_t workspace_bytes, void *stream) {
+    kla::AttnProblem p{};
+    p.q = q; p.k = k; p.v = v; p.q_stride = q_stride; p.k_stride = k_stride;
+    p.v_stride = v_stride; p.o = o; p.lse_in = lse; p.go = d_o; p.go_stride = d_o_stride;
+    p.scale = scale; p.dq = dq; p.dk = dk; p.dv = dv; p.Hq = Hq; p.Hk = Hk; p.d = d;
+    p.dtype = dtype;
+    kla_status st = fixed_attn(p, B, Tq, Tk);
+    if (st != KLA_OK || (st = check_scale(scale)) != KLA_OK) return st;
+    return run_attn(p, true, workspace, workspace_bytes, stream);
+}
+
+int kla_attn_bwd_varlen(const void *q, long long q_stride, const void *k, long long k_stride,
+                        const void *v, long long v_stride, const void *o, const float *lse,
+                        const void *d_o, long long d_o_stride, const int *cu_seqlens_q,
+                        const int *cu_seqlens_k, float scale, void *dq, void *dk, void *dv, int N,
+                        int total_q, int total_k, int Hq, int Hk, int d, int dtype,
+                        void *workspace, size_t workspace_bytes, void *stream) {
+    kla::AttnProblem p{};
+    p.q = q; p.k = k; p.v = v; p.q_stride = q_stride; p.k_stride = k_stride;
+    p.v_stride = v_stride; p.o = o; p.lse_in = lse; p.go = d_o; p.go_stride = d_o_stride;
+    p.scale = scale; p.dq = dq; p.dk = dk; p.dv = dv; p.Hq = Hq; p.Hk = Hk; p.d = d;
+    p.dtype = dtype;
+    kla_status st = packed_attn(p, N, total_q, total_k, cu_seqlens_q, cu_seqlens_k);
+    if (st != KLA_OK || (st = check_scale(scale)) != KLA_OK) return st;
+    if (N > 0 && (!cu_seqlens_q || !cu_seqlens_k))
+        return fail(KLA_ERR_INVALID_ARG, "cu_seqlens_q and cu_seqlens_k must be non-null");
+    return run_attn(p, true, workspace, workspace_bytes, stream);
+}
+
 int kla_workspace_status(const void *workspace, size_t workspace_bytes, void *stream) {
     if (workspace == nullptr || workspace_bytes < kla::kWsHeader) return ok();
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -1,0 +1,183 @@
+// Causal attention, host side: which kernels a call runs, its workspace and
+// its launches.  The kernels and their reasons are in kla_attn_simt.cu.
+#include "kla_attn.cuh"
+
+namespace kla {
+namespace {
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+        cudaGetLastError();     // no device: sizes are still wanted
+        return 152;
+    }
+    return n;
+}
+
+// Items of one side: tiles of ceil(len * mult / per) per sequence.
+struct Side {
+    int mult, per, tiles;
+    long long items;
+};
+Side side(const AttnProblem &p, bool keys, int mult, int per) {
+    Side r{mult, per, 0, 0};
+    const int len = keys ? p.Tk : p.Tq, total = keys ? p.total_k : p.total_q;
+    if (p.cu_q) {
+        // a sequence adds at most one partial tile, and has none without tokens
+        r.items = (long long)total * mult / per + (p.n_seq < total ? p.n_seq : total);
+    } else {
+        r.tiles = (int)ceil_div((long long)len * mult, per);
+        r.items = (long long)p.n_seq * r.tiles;
+    }
+    return r;
+}
+
+// Rows of a CUDA-core tile: 64 reuses a loaded key four times as often as 16,
+// but leaves SMs empty where there are few rows and wastes them where a
+// sequence has fewer (a decode batch).
+int simt_rows(const AttnProblem &p, bool keys) {
+    const int mult = keys ? 1 : p.Hq / p.Hk, total = keys ? p.total_k : p.total_q;
+    const long long each = ceil_div((long long)total * mult, p.n_seq);
+    return each <= 16 || side(p, keys, mult, 64).items * p.Hk < sm_count() ? 16 : 64;
+}
+
+// Parts of the key axis: enough that every SM has a block, each at least 4
+// tiles of 64 keys, so that the join's traffic stays small beside the keys'.
+int key_splits(const AttnProblem &p, long long blocks, int wanted, int tile) {
+    if (blocks >= wanted) return 1;
+    const long long tiles = ceil_div(p.total_k, (long long)p.n_seq * tile);
+    long long n = ceil_div(wanted, blocks < 1 ? 1 : blocks);
+    if (n > tiles / 4) n = tiles / 4;
+    return n < 1 ? 1 : (int)n;
+}
+
+struct FwdPlan {
+    Side q;
+    int rows, splits;
+    size_t table, o_part, lse_part, bytes;    // offsets and size of the workspace
+};
+FwdPlan fwd_plan(const AttnProblem &p) {
+    FwdPlan f{};
+    const int G = p.Hq / p.Hk;
+    f.rows = simt_rows(p, false);
+    f.q = side(p, false, G, f.rows);
+    f.splits = key_splits(p, f.q.items * p.Hk, 2 * sm_count(), 64);
+    size_t at = kWsHeader;
+    f.table = at;
+    if (p.cu_q) at = up256(at + f.q.items * sizeof(int2));
+    f.o_part = at;
+    if (f.splits > 1) {
+        const size_t rows = (size_t)f.splits * p.total_q * p.Hq;
+        at = up256(at + rows * p.d * sizeof(float));
+        f.lse_part = at;
+        at = up256(at + rows * sizeof(float));
+    }
+    f.bytes = at;
+    return f;
+}
+
+struct BwdPlan {
+    Side q, k;
+    int rows, keys;
+    size_t table_q, table_k, delta, bytes;
+};
+BwdPlan bwd_plan(const AttnProblem &p) {
+    BwdPlan b{};
+    const int G = p.Hq / p.Hk;
+    b.rows = simt_rows(p, false);
+    b.keys = p.total_k > 0 ? simt_rows(p, true) : 16;
+    b.q = side(p, false, G, b.rows);
+    b.k = side(p, true, 1, b.keys);
+    size_t at = kWsHeader;
+    b.table_q = at;
+    if (p.cu_q) at = up256(at + b.q.items * sizeof(int2));
+    b.table_k = at;
+    if (p.cu_q) at = up256(at + b.k.items * sizeof(int2));
+    b.delta = at;
+    b.bytes = up256(at + (size_t)p.total_q * p.Hq * sizeof(float));
+    return b;
+}
+
+attn::Args make_args(const AttnProblem &p) {
+    attn::Args a{};
+    a.q = p.q; a.k = p.k; a.v = p.v; a.o = p.o; a.go = p.go; a.out = p.out;
+    a.dq = p.dq; a.dk = p.dk; a.dv = p.dv; a.lse_in = p.lse_in; a.lse = p.lse;
+    a.q_stride = p.q_stride; a.k_stride = p.k_stride; a.v_stride = p.v_stride;
+    a.go_stride = p.go_stride; a.cu_q = p.cu_q; a.cu_k = p.cu_k; a.k_lens = p.k_lens;
+    a.status = static_cast<const unsigned *>(p.ws);
+    a.n_seq = p.n_seq; a.Tq = p.Tq; a.Tk = p.Tk; a.Hq = p.Hq; a.Hk = p.Hk; a.G = p.Hq / p.Hk;
+    a.splits = 1; a.total_q = p.total_q; a.scale = p.scale;
+    a.scale_log2 = p.scale * 1.4426950408889634f;
+    return a;
+}
+
+unsigned char *at(const AttnProblem &p, size_t offset) {
+    return static_cast<unsigned char *>(p.ws) + offset;
+}
+
+// The status word, and of packed sequences the check and the item tables.
+cudaError_t prepare(const AttnProblem &p, const AttnTable &t0, const AttnTable &t1,
+                    cudaStream_t s) {
+    if (!p.cu_q) return cudaMemsetAsync(p.ws, 0, sizeof(unsigned), s);
+    return launch_attn_prep(p.cu_q, p.cu_k, p.n_seq, p.total_q, p.total_k, t0, t1,
+                            static_cast<unsigned *>(p.ws), s);
+}
+
+void take(attn::Args &a, const Side &x, int2 *table) {
+    a.items = (int)x.items;
+    a.tiles = x.tiles;
+    a.table = table;
+}
+
+}  // namespace
+
+size_t attn_fwd_workspace_bytes(const AttnProblem &p) { return fwd_plan(p).bytes; }
+size_t attn_bwd_workspace_bytes(const AttnProblem &p) { return bwd_plan(p).bytes; }
+
+bool attn_too_large(const AttnProblem &p) {
+    const int G = p.Hq / p.Hk;
+    const long long q = side(p, false, G, 16).items, k = side(p, true, 1, 16).items;
+    const long long rows = ((long long)p.total_q * p.Hq + 15) / 16;
+    return q * p.Hk > INT32_MAX || k * p.Hk > INT32_MAX || rows > INT32_MAX;
+}
+
+cudaError_t launch_attn_fwd(const AttnProblem &p, cudaStream_t s) {
+    const FwdPlan f = fwd_plan(p);
+    attn::Args a = make_args(p);
+    int2 *table = p.cu_q ? reinterpret_cast<int2 *>(at(p, f.table)) : nullptr;
+    cudaError_t e = prepare(p, {table, p.cu_q, f.q.mult, f.q.per, (int)f.q.items, true}, {}, s);
+    if (e != cudaSuccess) return e;
+    take(a, f.q, table);
+    a.splits = f.splits;
+    if (f.splits > 1) {
+        a.o_part = reinterpret_cast<float *>(at(p, f.o_part));
+        a.lse_part = reinterpret_cast<float *>(at(p, f.lse_part));
+    }
+    e = launch_attn_simt_fwd(a, f.rows, p.d, p.dtype, s);
+    if (e != cudaSuccess || f.splits == 1) return e;
+    return launch_attn_join(a, p.d, p.dtype, s);
+}
+
+cudaError_t launch_attn_bwd(const AttnProblem &p, cudaStream_t s) {
+    const BwdPlan b = bwd_plan(p);
+    attn::Args a = make_args(p);
+    int2 *tq = p.cu_q ? reinterpret_cast<int2 *>(at(p, b.table_q)) : nullptr;
+    int2 *tk = p.cu_q ? reinterpret_cast<int2 *>(at(p, b.table_k)) : nullptr;
+    cudaError_t e = prepare(p, {tq, p.cu_q, b.q.mult, b.q.per, (int)b.q.items, true},
+                            {tk, p.cu_k, b.k.mult, b.k.per, (int)b.k.items, false}, s);
+    if (e != cudaSuccess) return e;
+    a.delta = reinterpret_cast<float *>(at(p, b.delta));
+    e = launch_attn_delta(a, p.d, p.dtype, s);
+    if (e != cudaSuccess) return e;
+    take(a, b.k, tk);
+    e = launch_attn_simt_dkv(a, b.keys, p.d, p.dtype, s);
+    if (e != cudaSuccess) return e;
+    take(a, b.q, tq);
+    return launch_attn_simt_dq(a, b.rows, p.d, p.dtype, s);
+}
+
+}  // namespace kla

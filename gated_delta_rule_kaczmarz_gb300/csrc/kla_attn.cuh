@@ -1,0 +1,121 @@
+// What the attention kernels share: the request, where a sequence's rows are,
+// the tables that map a launch's blocks to tiles, and the join of partial
+// results over a split key axis.
+//
+// Rows are packed: the G = Hq / Hk query heads of a key head read the same
+// keys and values, so a tile's row r is token r / G, head r % G of the group,
+// and one load of a key tile serves all of them, in a prompt as for the single
+// tokens of a decode batch.  Query i of lq sees the keys j <= i + lk - lq.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "kla_internal.h"
+
+namespace kla {
+namespace attn {
+
+// One launch's tables and problem, passed by value to every kernel.
+struct Args {
+    const void *q, *k, *v, *o, *go;       // o, go: backward
+    void *out, *dq, *dk, *dv;
+    const float *lse_in;
+    float *lse;
+    float *delta;                         // backward: rows of sum_d go o, [total_q][Hq]
+    long long q_stride, k_stride, v_stride, go_stride;
+    const int *cu_q, *cu_k, *k_lens;      // device; cu_*: packed, k_lens: padded keys
+    const unsigned *status;               // packed: the tables' check; not 0: nothing is done
+    const int2 *table;                    // packed: (sequence, tile) of every item
+    int n_seq, Tq, Tk, Hq, Hk, G;
+    int items;                            // fixed: n_seq * tiles, packed: table entries
+    int tiles;                            // fixed: tiles of a sequence
+    int splits;
+    float *o_part, *lse_part;             // splits > 1: [splits][total_q][Hq][d], [..][Hq]
+    int total_q;
+    float scale, scale_log2;
+};
+
+struct Seq {
+    long long q0, k0;    // first row
+    int lq, lk;
+};
+
+__device__ __forceinline__ Seq sequence(const Args &a, int s) {
+    Seq r;
+    if (a.cu_q) {
+        r.q0 = a.cu_q[s];
+        r.lq = a.cu_q[s + 1] - a.cu_q[s];
+        r.k0 = a.cu_k[s];
+        r.lk = a.cu_k[s + 1] - a.cu_k[s];
+    } else {
+        r.q0 = (long long)s * a.Tq;
+        r.lq = a.Tq;
+        r.k0 = (long long)s * a.Tk;
+        r.lk = a.Tk;
+        if (a.k_lens) {          // outside 0..Tk: clamped, every access stays in bounds
+            const int n = a.k_lens[s];
+            r.lk = n < 0 ? 0 : (n < a.Tk ? n : a.Tk);
+        }
+    }
+    return r;
+}
+
+// The item of a block: sequence, tile, key head and split.  Fixed lengths:
+// the last tiles first (they see the most keys, so the longest blocks start
+// first), key heads and sequences innermost.  False: nothing to do.
+struct Item {
+    int seq, tile, head, split;
+};
+__device__ __forceinline__ bool item_of(const Args &a, int block, bool last_first, Item &it) {
+    if (a.status && *a.status != 0) return false;
+    it.head = block % a.Hk;
+    int x = block / a.Hk;
+    if (a.table) {
+        it.split = x % a.splits;
+        const int2 e = a.table[x / a.splits];
+        it.seq = e.x;
+        it.tile = e.y;
+        return e.x >= 0;
+    }
+    it.seq = x % a.n_seq;
+    x /= a.n_seq;
+    it.split = x % a.splits;
+    x /= a.splits;
+    it.tile = last_first ? a.tiles - 1 - x : x;
+    return true;
+}
+
+// The key tiles of a split: [begin, end) of those of `n` that it takes.
+__device__ __forceinline__ void split_range(int n, int splits, int split, int &begin, int &end) {
+    const int per = (n + splits - 1) / splits;
+    begin = split * per;
+    end = begin + per < n ? begin + per : n;
+    if (begin > end) begin = end;
+}
+
+}  // namespace attn
+
+// A table that maps items to (sequence, tile): sequence n has
+// ceil(len * mult / per) tiles; entries past the last item hold -1.
+struct AttnTable {
+    int2 *items;
+    const int *cu;
+    int mult, per, entries;
+    bool last_first;      // a sequence's last tile first
+};
+// Checks the packed sequences' tables (writes *status) and fills up to two
+// item tables (items nullptr: none).
+cudaError_t launch_attn_prep(const int *cu_q, const int *cu_k, int n, int total_q, int total_k,
+                             const AttnTable &t0, const AttnTable &t1, unsigned *status,
+                             cudaStream_t s);
+cudaError_t launch_attn_join(const attn::Args &a, int d, int dtype, cudaStream_t s);
+cudaError_t launch_attn_delta(const attn::Args &a, int d, int dtype, cudaStream_t s);
+
+// CUDA-core kernels: any G.  rows / keys: rows of a tile, 16 or 64.
+cudaError_t launch_attn_simt_fwd(const attn::Args &a, int rows, int d, int dtype, cudaStream_t s);
+cudaError_t launch_attn_simt_dq(const attn::Args &a, int rows, int d, int dtype, cudaStream_t s);
+cudaError_t launch_attn_simt_dkv(const attn::Args &a, int keys, int d, int dtype, cudaStream_t s);
+
+}  // namespace kla

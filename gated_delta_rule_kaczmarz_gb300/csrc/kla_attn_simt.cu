@@ -1,0 +1,570 @@
+// Causal softmax attention on the CUDA cores (fp32 arithmetic throughout):
+// fp32 inputs, and bf16 inputs whose groups are too large for a tensor-core
+// tile.  Also the kernels that every path uses: the check and item tables of
+// packed sequences, the join of a split key axis, the backward pass's row
+// sums.
+//
+//   forward   s = scale q k^T, p = exp(s - m), o = p v / l, lse = m + log l,
+//             with the running maximum m and sum l over tiles of 64 keys
+//   backward  p = exp(s - lse), dp = go v^T, ds = p (dp - sum go o) scale,
+//             dv = p^T go, dk = ds^T q (a block per key tile), dq = ds k (a
+//             block per query tile): no atomics, a result does not depend on
+//             the order of blocks
+//
+// 256 threads as 16 x 16; thread (ty, tx) holds the scores of rows ty + 16 i
+// and keys tx + 16 j, and of the outputs rows ty + 16 i, features 4 tx + 64 j.
+// Rows in shared memory are 4 floats longer than d, so that the 16-byte reads
+// of 8 neighbouring keys fall into different banks.
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "kla_attn.cuh"
+
+namespace kla {
+namespace {
+
+using attn::Args;
+using attn::Item;
+using attn::Seq;
+
+constexpr int kT = 256;
+constexpr float kLn2 = 0.69314718055994531f;
+
+__device__ __forceinline__ float4 ld4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16 *p) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+}
+__device__ __forceinline__ void st4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
+__device__ __forceinline__ void st4(__nv_bfloat16 *p, float4 x) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(reinterpret_cast<const uint32_t &>(a),
+                                               reinterpret_cast<const uint32_t &>(b));
+}
+
+// ROWS query-side rows (packed) of a tile into dst[ROWS][D + 4]; rows past the
+// sequence's last are zero.
+template <typename T, int D, int ROWS>
+__device__ __forceinline__ void load_rows(float *dst, const T *src, long long stride,
+                                          const Args &a, const Seq &q, int head, long long row0) {
+    for (int i = threadIdx.x; i < ROWS * D / 4; i += kT) {
+        const int r = i / (D / 4), c = i % (D / 4) * 4;
+        const long long row = row0 + r;
+        const int tok = (int)(row / a.G), g = (int)(row % a.G);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (tok < q.lq) x = ld4(src + (q.q0 + tok) * stride + (long long)(head * a.G + g) * D + c);
+        *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) = x;
+    }
+}
+// ROWS keys or values from j0 into dst[ROWS][D + 4]; zero past the last.
+template <typename T, int D, int ROWS>
+__device__ __forceinline__ void load_keys(float *dst, const T *src, long long stride, const Seq &q,
+                                          int head, int j0) {
+    for (int i = threadIdx.x; i < ROWS * D / 4; i += kT) {
+        const int r = i / (D / 4), c = i % (D / 4) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j0 + r < q.lk) x = ld4(src + (q.k0 + j0 + r) * stride + (long long)head * D + c);
+        *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) = x;
+    }
+}
+
+// acc[i][j] += sum_c A[ty + 16 i][c] B[tx + 16 j][c] over the D features.
+template <int D, int MI, int NJ>
+__device__ __forceinline__ void dots(const float *A, const float *B, float (&acc)[MI][NJ]) {
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+        float4 x[MI], y[NJ];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) x[i] = ld4(A + (ty + 16 * i) * (D + 4) + c);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) y[j] = ld4(B + (tx + 16 * j) * (D + 4) + c);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                acc[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y,
+                                 fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, acc[i][j]))));
+    }
+}
+// acc[i][:] += sum_n W[ty + 16 i][n] X[n][:], features 4 tx + 64 j; W has LD
+// floats a row, N terms.
+template <int D, int MI, int N, int LD>
+__device__ __forceinline__ void mix(const float *W, const float *X, float4 (&acc)[MI][D / 64]) {
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+#pragma unroll 2
+    for (int n = 0; n < N; n += 4) {
+        float4 w[MI];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) w[i] = ld4(W + (ty + 16 * i) * LD + n);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                const float4 x = ld4(X + (n + m) * (D + 4) + 4 * tx + 64 * j);
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    const float f = m == 0 ? w[i].x : m == 1 ? w[i].y : m == 2 ? w[i].z : w[i].w;
+                    acc[i][j].x = fmaf(f, x.x, acc[i][j].x);
+                    acc[i][j].y = fmaf(f, x.y, acc[i][j].y);
+                    acc[i][j].z = fmaf(f, x.z, acc[i][j].z);
+                    acc[i][j].w = fmaf(f, x.w, acc[i][j].w);
+                }
+            }
+        }
+    }
+}
+
+template <int D, int BM>
+constexpr size_t fwd_smem() {
+    return ((size_t)BM * (D + 4) + 64 * (D + 4) + BM * 68) * 4;
+}
+
+template <typename T, int D, int BM>
+__global__ void __launch_bounds__(kT) attn_simt_fwd_kernel(const __grid_constant__ Args a) {
+    constexpr int MI = BM / 16;
+    extern __shared__ __align__(16) float sm[];
+    float *Q = sm, *KV = Q + BM * (D + 4), *P = KV + 64 * (D + 4);
+    Item it;
+    if (!attn::item_of(a, blockIdx.x, true, it)) return;
+    const Seq s = attn::sequence(a, it.seq);
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const long long row0 = (long long)it.tile * BM, rows = (long long)s.lq * a.G;
+    load_rows<T, D, BM>(Q, static_cast<const T *>(a.q), a.q_stride, a, s, it.head, row0);
+    const long long last = row0 + BM < rows ? row0 + BM - 1 : rows - 1;
+    const int seen = (int)(last / a.G) + 1 + s.lk - s.lq;      // keys of the last row
+    int begin, end;
+    attn::split_range(seen > 0 ? (seen + 63) / 64 : 0, a.splits, it.split, begin, end);
+    int limit[MI];                                             // last key of each row
+    float m[MI], l[MI];
+    float4 acc[MI][D / 64];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const long long r = row0 + ty + 16 * i;
+        limit[i] = r < rows ? (int)(r / a.G) + s.lk - s.lq : -1;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) acc[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int kb = begin; kb < end; ++kb) {
+        __syncthreads();
+        load_keys<T, D, 64>(KV, static_cast<const T *>(a.k), a.k_stride, s, it.head, kb * 64);
+        __syncthreads();
+        float x[MI][4];
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+        dots<D, MI, 4>(Q, KV, x);
+        __syncthreads();
+        load_keys<T, D, 64>(KV, static_cast<const T *>(a.v), a.v_stride, s, it.head, kb * 64);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            float mx = m[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool on = kb * 64 + tx + 16 * j <= limit[i];
+                x[i][j] = on ? x[i][j] * a.scale_log2 : -INFINITY;
+                mx = fmaxf(mx, x[i][j]);
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float base = mx == -INFINITY ? 0.f : mx;     // nothing seen yet
+            const float shrink = exp2f(m[i] - base);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = exp2f(x[i][j] - base);
+                sum += p;
+                P[(ty + 16 * i) * 68 + tx + 16 * j] = p;
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            l[i] = l[i] * shrink + sum;
+            m[i] = mx;
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                acc[i][j].x *= shrink; acc[i][j].y *= shrink;
+                acc[i][j].z *= shrink; acc[i][j].w *= shrink;
+            }
+        }
+        __syncthreads();
+        mix<D, MI, 64, 68>(P, KV, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const long long r = row0 + ty + 16 * i;
+        if (r >= rows) continue;
+        const long long tok = s.q0 + r / a.G;
+        const int head = it.head * a.G + (int)(r % a.G);
+        const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
+        const float lse = l[i] == 0.f ? -INFINITY : m[i] * kLn2 + logf(l[i]);
+        long long at = (tok * a.Hq + head) * D;
+        if (a.splits > 1) at += (long long)it.split * a.total_q * a.Hq * D;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+            float4 x = acc[i][j];
+            x.x *= inv; x.y *= inv; x.z *= inv; x.w *= inv;
+            if (a.splits > 1) st4(a.o_part + at + 4 * tx + 64 * j, x);
+            else st4(static_cast<T *>(a.out) + at + 4 * tx + 64 * j, x);
+        }
+        if (tx == 0) {
+            if (a.splits > 1)
+                a.lse_part[((long long)it.split * a.total_q + tok) * a.Hq + head] = lse;
+            else if (a.lse)
+                a.lse[tok * a.Hq + head] = lse;
+        }
+    }
+}
+
+// Scores and their gradients of BM rows by BN keys into P (p) and S (ds); the
+// caller has the four tiles in shared memory.  Row r's lse and delta.
+template <int D, int MI, int NJ>
+__device__ __forceinline__ void grads_tile(const float *Q, const float *K, const float *G,
+                                           const float *V, const int (&limit)[MI],
+                                           const float (&lse2)[MI], const float (&delta)[MI],
+                                           int j0, const Args &a, float (&p)[MI][NJ],
+                                           float (&ds)[MI][NJ]) {
+    const int tx = threadIdx.x % 16;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) p[i][j] = ds[i][j] = 0.f;
+    dots<D, MI, NJ>(Q, K, p);
+    dots<D, MI, NJ>(G, V, ds);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const bool on = j0 + tx + 16 * j <= limit[i];
+            p[i][j] = on ? exp2f(p[i][j] * a.scale_log2 - lse2[i]) : 0.f;
+            ds[i][j] = on ? p[i][j] * (ds[i][j] - delta[i]) * a.scale : 0.f;
+        }
+}
+
+template <int D, int BM>
+constexpr size_t dq_smem() {
+    return ((size_t)2 * BM * (D + 4) + 2 * 32 * (D + 4) + BM * 36) * 4;
+}
+
+template <typename T, int D, int BM>
+__global__ void __launch_bounds__(kT) attn_simt_dq_kernel(const __grid_constant__ Args a) {
+    constexpr int MI = BM / 16;
+    extern __shared__ __align__(16) float sm[];
+    float *Q = sm, *G = Q + BM * (D + 4), *K = G + BM * (D + 4), *V = K + 32 * (D + 4),
+          *S = V + 32 * (D + 4);
+    Item it;
+    if (!attn::item_of(a, blockIdx.x, true, it)) return;
+    const Seq s = attn::sequence(a, it.seq);
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const long long row0 = (long long)it.tile * BM, rows = (long long)s.lq * a.G;
+    load_rows<T, D, BM>(Q, static_cast<const T *>(a.q), a.q_stride, a, s, it.head, row0);
+    load_rows<T, D, BM>(G, static_cast<const T *>(a.go), a.go_stride, a, s, it.head, row0);
+    const long long last = row0 + BM < rows ? row0 + BM - 1 : rows - 1;
+    const int seen = (int)(last / a.G) + 1 + s.lk - s.lq;
+    const int tiles = seen > 0 ? (seen + 31) / 32 : 0;
+    int limit[MI];
+    float lse2[MI], delta[MI];
+    float4 acc[MI][D / 64];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const long long r = row0 + ty + 16 * i;
+        const bool on = r < rows;
+        limit[i] = on ? (int)(r / a.G) + s.lk - s.lq : -1;
+        const long long at = (s.q0 + r / a.G) * a.Hq + it.head * a.G + (int)(r % a.G);
+        lse2[i] = on ? a.lse_in[at] / kLn2 : 0.f;
+        delta[i] = on ? a.delta[at] : 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) acc[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int kb = 0; kb < tiles; ++kb) {
+        __syncthreads();
+        load_keys<T, D, 32>(K, static_cast<const T *>(a.k), a.k_stride, s, it.head, kb * 32);
+        load_keys<T, D, 32>(V, static_cast<const T *>(a.v), a.v_stride, s, it.head, kb * 32);
+        __syncthreads();
+        float p[MI][2], ds[MI][2];
+        grads_tile<D, MI, 2>(Q, K, G, V, limit, lse2, delta, kb * 32, a, p, ds);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) S[(ty + 16 * i) * 36 + tx + 16 * j] = ds[i][j];
+        __syncthreads();
+        mix<D, MI, 32, 36>(S, K, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const long long r = row0 + ty + 16 * i;
+        if (r >= rows) continue;
+        const long long at = ((s.q0 + r / a.G) * a.Hq + it.head * a.G + (int)(r % a.G)) * D;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+            st4(static_cast<T *>(a.dq) + at + 4 * tx + 64 * j, acc[i][j]);
+    }
+}
+
+template <int D, int BN>
+constexpr size_t dkv_smem() {
+    return ((size_t)2 * BN * (D + 4) + 2 * 32 * (D + 4) + 2 * BN * 36) * 4;
+}
+
+// A block per key tile: all rows of the group that see one of its keys.  Here
+// the tile's keys are the 16-row side: thread (ty, tx) has keys ty + 16 i and
+// rows tx + 16 j.
+template <typename T, int D, int BN>
+__global__ void __launch_bounds__(kT) attn_simt_dkv_kernel(const __grid_constant__ Args a) {
+    constexpr int MI = BN / 16;
+    extern __shared__ __align__(16) float sm[];
+    float *K = sm, *V = K + BN * (D + 4), *Q = V + BN * (D + 4), *G = Q + 32 * (D + 4),
+          *P = G + 32 * (D + 4), *S = P + BN * 36;
+    Item it;
+    if (!attn::item_of(a, blockIdx.x, false, it)) return;
+    const Seq s = attn::sequence(a, it.seq);
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int j0 = it.tile * BN;
+    load_keys<T, D, BN>(K, static_cast<const T *>(a.k), a.k_stride, s, it.head, j0);
+    load_keys<T, D, BN>(V, static_cast<const T *>(a.v), a.v_stride, s, it.head, j0);
+    float4 dk[MI][D / 64], dv[MI][D / 64];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) dk[i][j] = dv[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const long long rows = (long long)s.lq * a.G;
+    const int first = j0 + s.lq - s.lk;          // the first query that sees key j0
+    for (long long row0 = (long long)(first > 0 ? first : 0) * a.G / 32 * 32; row0 < rows;
+         row0 += 32) {
+        __syncthreads();
+        load_rows<T, D, 32>(Q, static_cast<const T *>(a.q), a.q_stride, a, s, it.head, row0);
+        load_rows<T, D, 32>(G, static_cast<const T *>(a.go), a.go_stride, a, s, it.head, row0);
+        __syncthreads();
+        float p[MI][2], ds[MI][2];
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) p[i][j] = ds[i][j] = 0.f;
+        dots<D, MI, 2>(K, Q, p);
+        dots<D, MI, 2>(V, G, ds);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const long long r = row0 + tx + 16 * j;
+            const bool on_r = r < rows;
+            const int limit = on_r ? (int)(r / a.G) + s.lk - s.lq : -1;
+            const long long at = (s.q0 + r / a.G) * a.Hq + it.head * a.G + (int)(r % a.G);
+            const float lse2 = on_r ? a.lse_in[at] / kLn2 : 0.f;
+            const float delta = on_r ? a.delta[at] : 0.f;
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const int key = j0 + ty + 16 * i;
+                const bool on = key <= limit && key < s.lk;
+                const float pv = on ? exp2f(p[i][j] * a.scale_log2 - lse2) : 0.f;
+                P[(ty + 16 * i) * 36 + tx + 16 * j] = pv;
+                S[(ty + 16 * i) * 36 + tx + 16 * j] =
+                    on ? pv * (ds[i][j] - delta) * a.scale : 0.f;
+            }
+        }
+        __syncthreads();
+        mix<D, MI, 32, 36>(P, G, dv);
+        mix<D, MI, 32, 36>(S, Q, dk);
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int key = j0 + ty + 16 * i;
+        if (key >= s.lk) continue;
+        const long long at = ((s.k0 + key) * a.Hk + it.head) * D;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+            st4(static_cast<T *>(a.dk) + at + 4 * tx + 64 * j, dk[i][j]);
+            st4(static_cast<T *>(a.dv) + at + 4 * tx + 64 * j, dv[i][j]);
+        }
+    }
+}
+
+// ------------------------------------------------------- shared by all paths
+// Row sums of go o: a warp per (token, head).
+template <typename T, int D>
+__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ Args a) {
+    if (a.status && *a.status != 0) return;
+    const long long n = (long long)a.total_q * a.Hq;
+    const long long i = (long long)blockIdx.x * 16 + threadIdx.x / 16;
+    const int lane = threadIdx.x % 16;
+    float sum = 0.f;
+    if (i < n) {
+        const T *o = static_cast<const T *>(a.o) + i * D;
+        const T *g = static_cast<const T *>(a.go) + i / a.Hq * a.go_stride + i % a.Hq * D;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+            const float4 x = ld4(o + 4 * lane + 64 * j), y = ld4(g + 4 * lane + 64 * j);
+            sum += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+        }
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (i < n && lane == 0) a.delta[i] = sum;
+}
+
+// o = sum_s exp(lse_s - lse) o_s, lse = log sum_s exp(lse_s): 16 lanes a row.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ Args a) {
+    if (a.status && *a.status != 0) return;
+    const long long n = (long long)a.total_q * a.Hq;
+    const long long i = (long long)blockIdx.x * 16 + threadIdx.x / 16;
+    const int lane = threadIdx.x % 16;
+    if (i >= n) return;
+    float top = -INFINITY;
+    for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.lse_part[s * n + i]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float4 acc[D / 64];
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int s = 0; s < a.splits; ++s) {
+        const float w = exp2f((a.lse_part[s * n + i] - base) / kLn2);
+        sum += w;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+            const float4 x = ld4(a.o_part + (s * n + i) * D + 4 * lane + 64 * j);
+            acc[j].x = fmaf(w, x.x, acc[j].x); acc[j].y = fmaf(w, x.y, acc[j].y);
+            acc[j].z = fmaf(w, x.z, acc[j].z); acc[j].w = fmaf(w, x.w, acc[j].w);
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+        acc[j].x *= inv; acc[j].y *= inv; acc[j].z *= inv; acc[j].w *= inv;
+        st4(static_cast<T *>(a.out) + i * D + 4 * lane + 64 * j, acc[j]);
+    }
+    if (lane == 0 && a.lse) a.lse[i] = sum == 0.f ? -INFINITY : base + logf(sum);
+}
+
+// One block: the check of both tables, then the items of up to two.
+__global__ void __launch_bounds__(1024)
+attn_prep_kernel(const int *cu_q, const int *cu_k, int n, int total_q, int total_k, AttnTable t0,
+                 AttnTable t1, unsigned *status) {
+    __shared__ int bad, base, warp_sum[32], off[1024], cnt[1024];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    if (tid == 0) bad = cu_q[0] != 0 || cu_k[0] != 0 || cu_q[n] != total_q || cu_k[n] != total_k;
+    __syncthreads();
+    for (int i = tid; i < n; i += 1024)
+        if (cu_q[i] > cu_q[i + 1] || cu_k[i] > cu_k[i + 1]) bad = 1;
+    __syncthreads();
+    if (tid == 0) *status = bad ? (unsigned)kDevBadSeqlens : (unsigned)kDevOk;
+    if (bad) return;
+    for (int z = 0; z < 2; ++z) {
+        const AttnTable t = z == 0 ? t0 : t1;
+        if (t.items == nullptr) continue;
+        __syncthreads();
+        if (tid == 0) base = 0;
+        __syncthreads();
+        for (int c = 0; c < n; c += 1024) {
+            const int i = c + tid;
+            int tiles = 0;
+            if (i < n) {
+                const long long len = t.cu[i + 1] - t.cu[i];
+                tiles = (int)((len * t.mult + t.per - 1) / t.per);
+            }
+            int sum = tiles;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += up;
+            }
+            if (lane == 31) warp_sum[warp] = sum;
+            __syncthreads();
+            if (warp == 0) {
+                int w = warp_sum[lane];
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int up = __shfl_up_sync(0xffffffffu, w, o);
+                    if (lane >= o) w += up;
+                }
+                warp_sum[lane] = w;
+            }
+            __syncthreads();
+            off[tid] = base + sum - tiles + (warp ? warp_sum[warp - 1] : 0);
+            cnt[tid] = tiles;
+            __syncthreads();
+            if (tid == 0) base += warp_sum[31];
+            for (int x = warp; x < 1024 && c + x < n; x += 32)
+                for (int j = lane; j < cnt[x]; j += 32)
+                    if (off[x] + j < t.entries)
+                        t.items[off[x] + j] = make_int2(c + x, t.last_first ? cnt[x] - 1 - j : j);
+            __syncthreads();
+        }
+        for (int j = base + tid; j < t.entries; j += 1024) t.items[j] = make_int2(-1, 0);
+    }
+}
+
+template <typename K>
+cudaError_t launch(K *kernel, const Args &a, size_t smem, cudaStream_t s) {
+    const long long blocks = (long long)a.items * a.splits * a.Hk;
+    if (blocks == 0) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)blocks, kT, smem, s>>>(a);
+    note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+#define KLA_BY_TYPE(d, dtype, CALL)                                        \
+    do {                                                                   \
+        if ((dtype) == 1) {                                                \
+            if ((d) == 128) { using T = __nv_bfloat16; constexpr int D = 128; CALL; } \
+            else { using T = __nv_bfloat16; constexpr int D = 64; CALL; }  \
+        } else {                                                           \
+            if ((d) == 128) { using T = float; constexpr int D = 128; CALL; } \
+            else { using T = float; constexpr int D = 64; CALL; }          \
+        }                                                                  \
+    } while (0)
+
+cudaError_t launch_attn_simt_fwd(const Args &a, int rows, int d, int dtype, cudaStream_t s) {
+    if (rows == 16)
+        KLA_BY_TYPE(d, dtype, return launch((attn_simt_fwd_kernel<T, D, 16>), a,
+                                            (fwd_smem<D, 16>()), s));
+    KLA_BY_TYPE(d, dtype, return launch((attn_simt_fwd_kernel<T, D, 64>), a,
+                                        (fwd_smem<D, 64>()), s));
+}
+
+cudaError_t launch_attn_simt_dq(const Args &a, int rows, int d, int dtype, cudaStream_t s) {
+    if (rows == 16)
+        KLA_BY_TYPE(d, dtype, return launch((attn_simt_dq_kernel<T, D, 16>), a,
+                                            (dq_smem<D, 16>()), s));
+    KLA_BY_TYPE(d, dtype, return launch((attn_simt_dq_kernel<T, D, 64>), a,
+                                        (dq_smem<D, 64>()), s));
+}
+
+cudaError_t launch_attn_simt_dkv(const Args &a, int keys, int d, int dtype, cudaStream_t s) {
+    if (keys == 16)
+        KLA_BY_TYPE(d, dtype, return launch((attn_simt_dkv_kernel<T, D, 16>), a,
+                                            (dkv_smem<D, 16>()), s));
+    KLA_BY_TYPE(d, dtype, return launch((attn_simt_dkv_kernel<T, D, 64>), a,
+                                        (dkv_smem<D, 64>()), s));
+}
+
+cudaError_t launch_attn_delta(const Args &a, int d, int dtype, cudaStream_t s) {
+    const long long blocks = ((long long)a.total_q * a.Hq + 15) / 16;
+    KLA_BY_TYPE(d, dtype, (attn_delta_kernel<T, D><<<(unsigned)blocks, 256, 0, s>>>(a)));
+    note_launch();
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_join(const Args &a, int d, int dtype, cudaStream_t s) {
+    const long long blocks = ((long long)a.total_q * a.Hq + 15) / 16;
+    KLA_BY_TYPE(d, dtype, (attn_join_kernel<T, D><<<(unsigned)blocks, 256, 0, s>>>(a)));
+    note_launch();
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_prep(const int *cu_q, const int *cu_k, int n, int total_q, int total_k,
+                             const AttnTable &t0, const AttnTable &t1, unsigned *status,
+                             cudaStream_t s) {
+    attn_prep_kernel<<<1, 1024, 0, s>>>(cu_q, cu_k, n, total_q, total_k, t0, t1, status);
+    note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace kla

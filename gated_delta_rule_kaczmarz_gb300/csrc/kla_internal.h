@@ -102,6 +102,29 @@ size_t qk_bwd_workspace_bytes(const QkProblem &p);
 cudaError_t launch_qk_fwd(const QkProblem &p, cudaStream_t s);
 cudaError_t launch_qk_bwd(const QkProblem &p, cudaStream_t s);
 
+// Causal attention (kla_attn.cu), fixed length (cu_q nullptr) or packed.
+struct AttnProblem {
+    const void *q, *k, *v;
+    const void *o, *go;             // backward
+    const float *lse_in;            // backward
+    void *out;                      // forward: o
+    float *lse;                     // forward, or nullptr
+    void *dq, *dk, *dv;             // backward
+    long long q_stride, k_stride, v_stride, go_stride;   // elements between token rows
+    const int *cu_q, *cu_k;         // device [n_seq + 1], packed only
+    const int *k_lens;              // device [n_seq], fixed length only, or nullptr
+    int n_seq, Tq, Tk;              // Tq, Tk: fixed length only
+    int total_q, total_k;
+    int Hq, Hk, d, dtype;
+    float scale;
+    void *ws;                       // attn_*_workspace_bytes(p), the status word first
+};
+size_t attn_fwd_workspace_bytes(const AttnProblem &p);
+size_t attn_bwd_workspace_bytes(const AttnProblem &p);
+bool attn_too_large(const AttnProblem &p);   // more blocks than a launch may have
+cudaError_t launch_attn_fwd(const AttnProblem &p, cudaStream_t s);
+cudaError_t launch_attn_bwd(const AttnProblem &p, cudaStream_t s);
+
 // Backward of the chunkwise forward (kla_chunk_bwd.cu), fixed length or varlen.
 struct BwdProblem {
     const void *q, *k, *v, *dout;

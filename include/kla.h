@@ -417,6 +417,92 @@ KLA_API int kla_qk_norm_rope_bwd(const void *q, long long q_stride, const void *
                                  void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Causal softmax attention with grouped heads: the other mixer of a hybrid
+ * stack, over whole prompts, packed sequences, and single tokens or chunks of
+ * a prompt over a cache.  Per (sequence, query head h), with the keys of head
+ * h / (Hq / Hk), lq queries and lk keys:
+ *
+ *     S_ij = scale <q_i, k_j>   for j <= i + lk - lq  (the last query sees all)
+ *     o_i  = sum_j exp(S_ij - lse_i) v_j,   lse_i = log sum_j exp(S_ij)
+ *
+ * A query that sees no key (i + lk - lq < 0) has o = 0 and lse = -infinity.
+ *   q, o     : [B, Tq, Hq, d]; k, v: [B, Tk, Hk, d], dtype.  Token rows of q, k
+ *              and v are q_stride, k_stride, v_stride elements apart (at least
+ *              heads * d, a multiple of 16 bytes), sequence b's rows start at
+ *              row b * Tq (b * Tk): parts of a fused projection's output are
+ *              read where they lie.  o is dense.
+ *   k_lens   : device int32 [B] or NULL: sequence b has its first k_lens[b]
+ *              keys (clamped to 0..Tk; the rest of a padded cache is not
+ *              read into a result), its queries are the last Tq of them
+ *   lse      : [B, Tq, Hq] fp32, written unless NULL (kla_attn_bwd wants it)
+ *   scale    : positive and finite
+ *   workspace: kla_attn_fwd_workspace_size(...) bytes, 256-byte aligned; it
+ *              starts with the device status word (kla_workspace_status), the
+ *              rest is scratch.  The size depends on the SM count of the
+ *              current device.  One workspace must not be shared by calls that
+ *              may run concurrently.
+ * Hq a multiple of Hk, at most 1024; d in {64, 128}.  B, Tq or Tk may be 0.
+ * Scores, statistics and sums are fp32.  Keys and values of rows that are not
+ * the sequence's own (behind its length, of its neighbours) may hold anything;
+ * its own must be finite for the queries before them to stay finite.
+ * Few rows over many keys (a decode batch) run split over the key axis, and
+ * a second kernel joins the parts.
+ */
+KLA_API size_t kla_attn_fwd_workspace_size(int B, int Tq, int Tk, int Hq, int Hk, int d,
+                                           int dtype);
+KLA_API int kla_attn_fwd(const void *q, long long q_stride, const void *k, long long k_stride,
+                         const void *v, long long v_stride, const int *k_lens, float scale,
+                         void *o, float *lse, int B, int Tq, int Tk, int Hq, int Hk, int d,
+                         int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kla_attn_fwd over N packed sequences: q, o [total_q, Hq, d], k, v [total_k,
+ * Hk, d], lse [total_q, Hq]; sequence n has the rows cu_seqlens_q[n] ..
+ * cu_seqlens_q[n+1]-1 and the keys cu_seqlens_k[n] .. cu_seqlens_k[n+1]-1
+ * (device int32 [N + 1]; the two may be the same array).  Both tables must
+ * start with 0, not decrease and end with the totals; the device checks this,
+ * and a violation skips all work and is reported by kla_workspace_status() as
+ * KLA_ERR_INVALID_ARG.  Sequences may be empty on either side.
+ */
+KLA_API size_t kla_attn_fwd_varlen_workspace_size(int N, int total_q, int total_k, int Hq, int Hk,
+                                                  int d, int dtype);
+KLA_API int kla_attn_fwd_varlen(const void *q, long long q_stride, const void *k,
+                                long long k_stride, const void *v, long long v_stride,
+                                const int *cu_seqlens_q, const int *cu_seqlens_k, float scale,
+                                void *o, float *lse, int N, int total_q, int total_k, int Hq,
+                                int Hk, int d, int dtype, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/*
+ * Backward of kla_attn_fwd (without k_lens) and kla_attn_fwd_varlen: the
+ * gradients of sum <d_o, o> from the same inputs, the forward's o and lse, and
+ * d_o (rows d_o_stride elements apart):
+ *
+ *     P = exp(S - lse),  dS = P (d_o v^T - rowsum(d_o o)) scale
+ *     dq = dS k,  dk = dS^T q,  dv = P^T d_o  (summed over a group's heads)
+ *
+ * dq [B, Tq, Hq, d], dk, dv [B, Tk, Hk, d] (dtype, dense) are written whole;
+ * keys that no query sees get 0.  No atomics: a result does not depend on the
+ * order of blocks.  workspace as for the forward, of its own size.
+ */
+KLA_API size_t kla_attn_bwd_workspace_size(int B, int Tq, int Tk, int Hq, int Hk, int d,
+                                           int dtype);
+KLA_API int kla_attn_bwd(const void *q, long long q_stride, const void *k, long long k_stride,
+                         const void *v, long long v_stride, const void *o, const float *lse,
+                         const void *d_o, long long d_o_stride, float scale, void *dq, void *dk,
+                         void *dv, int B, int Tq, int Tk, int Hq, int Hk, int d, int dtype,
+                         void *workspace, size_t workspace_bytes, void *stream);
+KLA_API size_t kla_attn_bwd_varlen_workspace_size(int N, int total_q, int total_k, int Hq, int Hk,
+                                                  int d, int dtype);
+KLA_API int kla_attn_bwd_varlen(const void *q, long long q_stride, const void *k,
+                                long long k_stride, const void *v, long long v_stride,
+                                const void *o, const float *lse, const void *d_o,
+                                long long d_o_stride, const int *cu_seqlens_q,
+                                const int *cu_seqlens_k, float scale, void *dq, void *dk,
+                                void *dv, int N, int total_q, int total_k, int Hq, int Hk, int d,
+                                int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Synchronises `stream` and returns the status that the last prefill call
  * using `workspace` recorded on the device: KLA_OK, KLA_ERR_INVALID_ARG
  * (cu_seqlens rejected) or KLA_ERR_TIMEOUT.  A workspace of 0 bytes (NULL)
