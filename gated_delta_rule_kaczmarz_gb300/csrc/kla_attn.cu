@@ -1,6 +1,6 @@
 // Causal attention, host side: which kernels a call runs, its workspace and
 // its launches.  The kernels and their reasons are in kla_attn_simt.cu.
-#include "kla_attn.cuh"
+#include "kla_attn_tc.cuh"
 
 namespace kla {
 namespace {
@@ -55,7 +55,34 @@ int key_splits(const AttnProblem &p, long long blocks, int wanted, int tile) {
     return n < 1 ? 1 : (int)n;
 }
 
+// The tensor cores take bf16 with groups that fit into a tile's 128 rows.
+bool on_tensor_cores(const AttnProblem &p) {
+    return p.dtype == 1 && p.Hq / p.Hk <= attn::kTile && p.total_k > 0 && attn_tc_ready();
+}
+
+// Parts of the key axis on the tensor cores, one CTA per SM: the number that
+// makes the whole launch shortest, counted in key tiles walked one after
+// another (waves of CTAs times the tiles of each, and 4 tiles' time for a
+// CTA's start and end).  Only where the unsplit launch has under two waves of
+// CTAs that all walk about the same tiles, that is few query rows.
+int tc_splits(const AttnProblem &p, long long blocks) {
+    const int sms = sm_count();
+    const long long tiles = ceil_div(p.total_k, (long long)p.n_seq * attn::kTile);
+    if (blocks < 1 || blocks >= 2 * sms) return 1;
+    int best = 1;
+    long long least = 0;
+    for (int n = 1; n <= 64 && n <= (tiles + 1) / 2; ++n) {
+        const long long cost = ceil_div(blocks * n, sms) * (ceil_div(tiles, n) + 4) + (n > 1 ? 4 : 0);
+        if (n == 1 || cost < least) {
+            least = cost;
+            best = n;
+        }
+    }
+    return best;
+}
+
 struct FwdPlan {
+    bool tc;
     Side q;
     int rows, splits;
     size_t table, o_part, lse_part, bytes;    // offsets and size of the workspace
@@ -63,9 +90,15 @@ struct FwdPlan {
 FwdPlan fwd_plan(const AttnProblem &p) {
     FwdPlan f{};
     const int G = p.Hq / p.Hk;
-    f.rows = simt_rows(p, false);
-    f.q = side(p, false, G, f.rows);
-    f.splits = key_splits(p, f.q.items * p.Hk, 2 * sm_count(), 64);
+    f.tc = on_tensor_cores(p);
+    if (f.tc) {
+        f.q = side(p, false, 1, 2 * attn::tile_tokens(G));
+        f.splits = tc_splits(p, f.q.items * p.Hk);
+    } else {
+        f.rows = simt_rows(p, false);
+        f.q = side(p, false, G, f.rows);
+        f.splits = key_splits(p, f.q.items * p.Hk, 2 * sm_count(), 64);
+    }
     size_t at = kWsHeader;
     f.table = at;
     if (p.cu_q) at = up256(at + f.q.items * sizeof(int2));
@@ -157,7 +190,8 @@ cudaError_t launch_attn_fwd(const AttnProblem &p, cudaStream_t s) {
         a.o_part = reinterpret_cast<float *>(at(p, f.o_part));
         a.lse_part = reinterpret_cast<float *>(at(p, f.lse_part));
     }
-    e = launch_attn_simt_fwd(a, f.rows, p.d, p.dtype, s);
+    e = f.tc ? launch_attn_tc_fwd(a, p.d, p.total_k, s)
+             : launch_attn_simt_fwd(a, f.rows, p.d, p.dtype, s);
     if (e != cudaSuccess || f.splits == 1) return e;
     return launch_attn_join(a, p.d, p.dtype, s);
 }

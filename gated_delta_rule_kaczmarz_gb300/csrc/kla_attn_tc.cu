@@ -1,0 +1,411 @@
+// Causal softmax attention, forward, on the tensor cores (bf16, head sizes 64
+// and 128).
+//
+//   s = q k^T,  p = exp2(c (s - m)),  o = (sum p v) / l,  l = sum p,
+//   lse = (c m + log2 l) ln 2,  c = scale log2 e
+//
+// One CTA takes two tiles of up to 128 packed rows (token x group head) of one
+// key head and walks the keys in tiles of 128.  Scores, probabilities and
+// outputs stay in tensor memory: S_t = Q_t K^T (128 columns each), P_t as bf16
+// over S_t's columns, from where it is the A operand of O_t += P_t V.  A warp
+// loads (TMA, a ring of 32 KB slots that holds K and V tiles in the order of
+// their use), a warp issues the products, and each tile has four softmax warps
+// with one row per thread.  The two tiles alternate: while one's softmax runs,
+// the tensor cores work on the other's products.
+//
+// The running maximum m is raised only where a row's grew by more than 8 (in
+// log2 units): p then stays below 2^8, which costs no accuracy in fp32 sums
+// and bf16 mantissas, and the rescaling of O in tensor memory, a round trip of
+// its whole row, happens in the first tiles only.  p is rounded to bf16 as an
+// operand; the sum l is of the unrounded values.
+//
+// Bound: the tensor cores over a prompt (4 d flops a pair and head), HBM for
+// single tokens over a cache (the key tiles pass once for all heads of a
+// group).
+#include "kla_attn_tc.cuh"
+
+namespace kla {
+namespace {
+
+using namespace tc;
+using attn::Args;
+using attn::Item;
+using attn::kSlab;
+using attn::kTile;
+using attn::Seq;
+
+constexpr int kThreads = 320;            // 8 softmax warps, products, loads
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kGrow = 8.f;             // see above
+
+template <int D>
+struct Cfg {
+    static constexpr int SLABS = D / 64;
+    static constexpr uint32_t TILE = SLABS * kSlab;
+    static constexpr int SLOTS = D == 128 ? 4 : 6;
+    static constexpr size_t SMEM = (size_t)TILE * (2 + SLOTS) + 1024;
+    static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
+};
+
+struct Shared {
+    uint64_t full[8], empty[8];          // ring slots
+    uint64_t q[2];                       // Q tiles landed
+    uint64_t s[2], p[2], o[2];           // scores ready, probabilities ready, product done
+    uint64_t fin;
+    uint32_t tmem;
+    volatile int abort;
+};
+
+// Maps of a launch and its row tiling.
+struct Maps {
+    CUtensorMap q, k, v;
+    int tokens;                          // of a tile
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
+    using C = Cfg<D>;
+    extern __shared__ unsigned char raw[];
+    __shared__ Shared sh;
+    unsigned char *base = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    unsigned char *sQ = base, *sKV = base + 2 * C::TILE;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    Item it;
+    if (!attn::item_of(a, blockIdx.x, true, it)) return;
+    const Seq seq = attn::sequence(a, it.seq);
+    const int TT = maps.tokens, R = TT * a.G;
+    const int tok0 = it.tile * 2 * TT;
+    // key tiles of the two row tiles; a tile without tokens has none
+    const int shift = seq.lk - seq.lq;
+    int blocks[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int first = tok0 + t * TT, last = min(first + TT, seq.lq);
+        const int seen = last > first ? last + shift : 0;      // keys of the last token
+        blocks[t] = seen > 0 ? (seen + kTile - 1) / kTile : 0;
+    }
+    int b0, b1;
+    attn::split_range(max(blocks[0], blocks[1]), a.splits, it.split, b0, b1);
+    const int e0 = min(blocks[0], b1), e1 = min(blocks[1], b1);   // tile t: keys b0 .. e_t
+    const int nb = b1 - b0;
+
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int i = 0; i < C::SLOTS; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&sh.q[t], 1);
+            mbar_init(&sh.s[t], 1);
+            mbar_init(&sh.p[t], 4);
+            mbar_init(&sh.o[t], 1);
+        }
+        mbar_init(&sh.fin, 1);
+        sh.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) tmem_alloc(&sh.tmem, C::TM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = sh.tmem;
+    const auto give_up = [&] {
+        sh.abort = 1;
+        if (a.status) *const_cast<unsigned *>(a.status) = kDevTimeout;
+    };
+
+    if (warp == 9) {
+        // ------------------------------------------------------------- loads
+        if (lane == 0 && nb > 0) {
+            const uint32_t box = (uint32_t)R * 128u;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if ((t ? e1 : e0) <= b0) continue;
+                mbar_expect_tx(&sh.q[t], box * C::SLABS);
+                for (int c = 0; c < C::SLABS; ++c)
+                    tma_load_3d(sQ + t * C::TILE + c * kSlab, &maps.q, &sh.q[t], c * 64,
+                                it.head * a.G, (int)(seq.q0 + tok0 + t * TT));
+            }
+            int j = 0;
+            for (; j < 2 * nb; ++j) {
+                const int slot = j % C::SLOTS, use = j / C::SLOTS;
+                if (use > 0 &&
+                    !mbar_wait_or_abort(&sh.empty[slot], (uint32_t)((use - 1) & 1), &sh.abort)) {
+                    give_up();
+                    break;
+                }
+                mbar_expect_tx(&sh.full[slot], C::TILE);
+                const int row = (int)(seq.k0 + (long long)(b0 + j / 2) * kTile);
+                for (int c = 0; c < C::SLABS; ++c)
+                    tma_load_3d(sKV + slot * C::TILE + c * kSlab, j % 2 ? &maps.v : &maps.k,
+                                &sh.full[slot], c * 64, it.head, row);
+            }
+            if (j < 2 * nb) {      // given up: the copies in flight land before the CTA leaves
+                for (int i = max(0, j - C::SLOTS); i < j; ++i)
+                    (void)mbar_wait(&sh.full[i % C::SLOTS], (uint32_t)((i / C::SLOTS) & 1));
+                for (int t = 0; t < 2; ++t)
+                    if ((t ? e1 : e0) > b0) (void)mbar_wait(&sh.q[t], 0u);
+            }
+        }
+    } else if (warp == 8) {
+        // ---------------------------------------------------------- products
+        constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true);
+        const uint32_t aQ = smem_u32(sQ), aKV = smem_u32(sKV);
+        const auto scores = [&](int t, int slot) {
+            if (lane == 0) {
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_bf16(tb + C::TM_S + 128u * t, attn::kdesc(aQ + t * C::TILE, ks),
+                             attn::kdesc(aKV + slot * C::TILE, ks), id_s, ks > 0);
+                mma_commit(&sh.s[t]);
+            }
+            __syncwarp();
+        };
+        const auto landed = [&](int j) {
+            return __all_sync(0xffffffffu,
+                              mbar_wait_or_abort(&sh.full[j % C::SLOTS],
+                                                 (uint32_t)((j / C::SLOTS) & 1), &sh.abort));
+        };
+        bool ok = true;
+        if (nb > 0) {
+            ok = landed(0);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if ((t ? e1 : e0) <= b0) continue;
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_or_abort(&sh.q[t], 0u, &sh.abort));
+                if (ok) {
+                    tc_fence_after();
+                    scores(t, 0);
+                }
+            }
+            if (ok && lane == 0) mma_commit(&sh.empty[0]);
+            __syncwarp();
+        }
+        for (int n = 0; ok && n < nb; ++n) {
+            const int jv = 2 * n + 1, jk = 2 * n + 2, sv = jv % C::SLOTS;
+            ok = landed(jv);
+            if (!ok) break;
+            const int valid = seq.lk - (b0 + n) * kTile;
+            if (valid < kTile) attn::zero_rows<C::SLABS>(sKV + sv * C::TILE, valid, lane);
+            if (n + 1 < nb) ok = landed(jk);
+            if (!ok) break;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int e = t ? e1 : e0;
+                if (b0 + n >= e) continue;
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_or_abort(&sh.p[t], (uint32_t)(n & 1),
+                                                                      &sh.abort));
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_bf16_ts(tb + C::TM_O + (uint32_t)(D * t),
+                                    tb + C::TM_S + 128u * t + 8u * ks,
+                                    attn::mdesc(aKV + sv * C::TILE, ks), id_o, n > 0 || ks > 0);
+                    mma_commit(&sh.o[t]);
+                }
+                __syncwarp();
+                if (b0 + n + 1 < e) scores(t, jk % C::SLOTS);
+            }
+            if (ok && lane == 0) {
+                mma_commit(&sh.empty[sv]);
+                if (n + 1 < nb) mma_commit(&sh.empty[jk % C::SLOTS]);
+            }
+            __syncwarp();
+        }
+        if (!ok) give_up();
+        // every product issued has completed before the tensor memory is released
+        if (lane == 0) mma_commit(&sh.fin);
+        __syncwarp();
+        (void)mbar_wait(&sh.fin, 0u);
+    } else {
+        // ----------------------------------------------------------- softmax
+        const int t = warp / 4, w = warp % 4, r = 32 * w + lane;
+        const int e = t ? e1 : e0;
+        const int tok = tok0 + t * TT + r / a.G, head = it.head * a.G + r % a.G;
+        const bool row = r < R && tok < seq.lq;
+        const int limit = row ? tok + shift : -1;             // last key of the row
+        const int full = tok0 + t * TT + shift;               // last key that every row sees
+        const uint32_t lanes = (uint32_t)(32 * w) << 16;
+        const uint32_t tS = tb + C::TM_S + 128u * t + lanes, tO = tb + C::TM_O + (uint32_t)(D * t) + lanes;
+        const float c = a.scale_log2;
+        const bool work = __any_sync(0xffffffffu, row);       // a warp without rows only arrives
+        float m = -INFINITY, l = 0.f, mc = 0.f;               // mc = c m (0 while m is -inf)
+        bool ok = true;
+        for (int n = b0; n < e; ++n) {
+            const int i = n - b0;
+            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&sh.s[t], (uint32_t)(i & 1), &sh.abort));
+            if (!ok) break;
+            tc_fence_after();
+            if (work) {
+                uint32_t x[4][32];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) tmem_ld32(tS + 32u * j, x[j]);
+                tmem_ld_wait();
+                if (n * kTile + kTile - 1 > full) {
+                    const int rel = limit - n * kTile;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * j + k > rel) x[j][k] = 0xff800000u;      // -infinity
+                }
+                float mx[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    mx[j] = __uint_as_float(x[j][0]);
+#pragma unroll
+                    for (int k = 1; k < 32; ++k) mx[j] = fmaxf(mx[j], __uint_as_float(x[j][k]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const bool grow = row && (top - m) * c > kGrow;
+                if (i == 0) {
+                    m = top;
+                    mc = top == -INFINITY ? 0.f : top * c;
+                } else if (__any_sync(0xffffffffu, grow)) {
+                    // O holds the products up to the last tile: they have to be complete
+                    ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&sh.o[t], (uint32_t)((i - 1) & 1),
+                                                                    &sh.abort));
+                    if (!ok) break;
+                    tc_fence_after();
+                    float f = 1.f;
+                    if (grow) {
+                        f = m == -INFINITY ? 0.f : attn::ex2((m - top) * c);
+                        m = top;
+                        mc = top * c;
+                    }
+                    __syncwarp();
+                    l *= f;
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        uint32_t y[16];
+                        tmem_ld16(tO + 16u * j, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+                        tmem_st16(tO + 16u * j, y);
+                    }
+                }
+                float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t y[32];
+#pragma unroll
+                    for (int k = 0; k < 64; k += 4) {
+                        float p[4];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            p[z] = __uint_as_float(x[2 * h + (k + z) / 32][(k + z) % 32]);
+                        attn::fma2(p[0], p[1], c, -mc);
+                        attn::fma2(p[2], p[3], c, -mc);
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) p[z] = attn::ex2(p[z]);
+                        attn::add2(s0, s1, p[0], p[1]);
+                        attn::add2(s2, s3, p[2], p[3]);
+                        y[k / 2] = attn::pack2(p[0], p[1]);
+                        y[k / 2 + 1] = attn::pack2(p[2], p[3]);
+                    }
+                    attn::tmem_st32(tS + 32u * h, y);
+                }
+                l += (s0 + s1) + (s2 + s3);
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p[t]);
+        }
+        if (ok && e > b0) {
+            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&sh.o[t], (uint32_t)((e - b0 - 1) & 1),
+                                                            &sh.abort));
+            tc_fence_after();
+        }
+        if (!ok) {
+            give_up();
+        } else if (work) {
+            // a row that saw no key has l = 0: o = 0 and lse = -infinity
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const long long at = (seq.q0 + tok) * a.Hq + head;
+            const bool parts = a.splits > 1;
+            const long long n_rows = (long long)a.total_q * a.Hq;
+            if (row) {
+                const float lse = l == 0.f ? -INFINITY : (mc + log2f(l)) * kLn2;
+                if (parts) a.lse_part[it.split * n_rows + at] = lse;
+                else if (a.lse) a.lse[at] = lse;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                uint32_t y[16];
+                if (e > b0) {
+                    tmem_ld16(tO + 16u * j, y);
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) y[k] = 0;
+                }
+                float f[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) f[k] = l == 0.f ? 0.f : __uint_as_float(y[k]) * inv;
+                if (row && parts) {
+                    float4 *dst = reinterpret_cast<float4 *>(a.o_part + (it.split * n_rows + at) * D + 16 * j);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        dst[k] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+                } else if (row) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                                           at * D + 16 * j);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        dst[k] = make_uint4(attn::pack2(f[8 * k], f[8 * k + 1]),
+                                            attn::pack2(f[8 * k + 2], f[8 * k + 3]),
+                                            attn::pack2(f[8 * k + 4], f[8 * k + 5]),
+                                            attn::pack2(f[8 * k + 6], f[8 * k + 7]));
+                }
+                __syncwarp();
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) {
+        tmem_relinquish();
+        tmem_dealloc(tb, C::TM_COLS);
+    }
+}
+
+template <int D>
+cudaError_t launch_fwd(const Args &a, const Maps &maps, cudaStream_t s) {
+    const long long blocks = (long long)a.items * a.splits * a.Hk;
+    if (blocks == 0) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(attn_tc_fwd_kernel<D>),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Cfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    attn_tc_fwd_kernel<D><<<(unsigned)blocks, kThreads, Cfg<D>::SMEM, s>>>(a, maps);
+    note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool attn_tc_ready() { return tmap::encode_fn() != nullptr; }
+
+cudaError_t launch_attn_tc_fwd(const Args &a, int d, int total_k, cudaStream_t s) {
+    Maps maps;
+    maps.tokens = attn::tile_tokens(a.G);
+    if (!attn::map_rows(&maps.q, a.q, d, a.Hq, a.total_q, a.q_stride, a.G, maps.tokens) ||
+        !attn::map_rows(&maps.k, a.k, d, a.Hk, total_k, a.k_stride, 1, kTile) ||
+        !attn::map_rows(&maps.v, a.v, d, a.Hk, total_k, a.v_stride, 1, kTile))
+        return cudaErrorInvalidValue;
+    return d == 128 ? launch_fwd<128>(a, maps, s) : launch_fwd<64>(a, maps, s);
+}
+
+}  // namespace kla
