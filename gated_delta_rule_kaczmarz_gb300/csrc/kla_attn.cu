@@ -114,6 +114,7 @@ FwdPlan fwd_plan(const AttnProblem &p) {
 }
 
 struct BwdPlan {
+    bool tc;
     Side q, k;
     int rows, keys;
     size_t table_q, table_k, delta, bytes;
@@ -121,10 +122,16 @@ struct BwdPlan {
 BwdPlan bwd_plan(const AttnProblem &p) {
     BwdPlan b{};
     const int G = p.Hq / p.Hk;
-    b.rows = simt_rows(p, false);
-    b.keys = p.total_k > 0 ? simt_rows(p, true) : 16;
-    b.q = side(p, false, G, b.rows);
-    b.k = side(p, true, 1, b.keys);
+    b.tc = on_tensor_cores(p);
+    if (b.tc) {
+        b.q = side(p, false, 1, attn::tile_tokens(G));
+        b.k = side(p, true, 1, attn::kTile);
+    } else {
+        b.rows = simt_rows(p, false);
+        b.keys = p.total_k > 0 ? simt_rows(p, true) : 16;
+        b.q = side(p, false, G, b.rows);
+        b.k = side(p, true, 1, b.keys);
+    }
     size_t at = kWsHeader;
     b.table_q = at;
     if (p.cu_q) at = up256(at + b.q.items * sizeof(int2));
@@ -207,6 +214,12 @@ cudaError_t launch_attn_bwd(const AttnProblem &p, cudaStream_t s) {
     a.delta = reinterpret_cast<float *>(at(p, b.delta));
     e = launch_attn_delta(a, p.d, p.dtype, s);
     if (e != cudaSuccess) return e;
+    if (b.tc) {
+        attn::Args keys = a;
+        take(keys, b.k, tk);
+        take(a, b.q, tq);
+        return launch_attn_tc_bwd(keys, a, p.d, p.total_k, s);
+    }
     take(a, b.k, tk);
     e = launch_attn_simt_dkv(a, b.keys, p.d, p.dtype, s);
     if (e != cudaSuccess) return e;
