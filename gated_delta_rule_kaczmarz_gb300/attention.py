@@ -15,84 +15,105 @@ import math
 
 import torch
 
-from .binding import _check, _dtype_code, _ptr, _workspace, load
+from .binding import KlaError, load
 
 _NORMS = {"none": 0, "rms": 1, "l2": 2}
 _STYLES = {"half": 0, "pairs": 1}
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+# A small call takes about as long as its checks do, so these go straight: no
+# object is made that the library call does not take.
 
 
-def _rows(t, name, like=None, lead=None, heads=None, d=None):
-    """Checks a [..., H, d] tensor whose token rows may be a stride apart;
-    returns that stride in elements."""
+def _type_code(q):
+    code = _TYPES.get(q.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {q.dtype}; use bfloat16 or float32")
+    return code
+
+
+def _refuse(t, name, dtype, device, shape):
+    """Says what is wrong with a tensor that is not as it has to be."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() < 3:
-        raise ValueError(f"{name} must have shape [..., heads, d], got {tuple(t.shape)}")
-    if like is not None:
-        if t.dtype != like.dtype:
-            raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-        if t.device != like.device:
-            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    shape = tuple(t.shape)
-    if (lead is not None and shape[:-2] != tuple(lead)) or \
-            (heads is not None and shape[-2] != heads) or (d is not None and shape[-1] != d):
-        raise ValueError(f"{name} must have shape {tuple(lead or shape[:-2])} + "
-                         f"({heads or shape[-2]}, {d or shape[-1]}), got {shape}")
-    dense = shape[-2] * shape[-1]
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows(t, name, dtype, device, shape):
+    """Checks a [..., H, d] tensor whose token rows may be a stride apart;
+    returns that stride in elements."""
+    size = t.shape
+    if t.dtype != dtype or t.get_device() != device or device < 0 or size != shape:
+        _refuse(t, name, dtype, device, shape)
     if t.is_contiguous():
-        return dense
+        return size[-2] * size[-1]
     st = t.stride()
-    if (shape[-1] > 1 and st[-1] != 1) or (shape[-2] > 1 and st[-2] != shape[-1]):
+    if (size[-1] > 1 and st[-1] != 1) or (size[-2] > 1 and st[-2] != size[-1]):
         raise ValueError(f"{name}: the heads of a token row must be dense (strides {st})")
     row, step = None, None               # the leading dimensions walk one row at a time
-    for n, s in zip(reversed(shape[:-2]), reversed(st[:-2])):
+    for n, x in zip(reversed(size[:-2]), reversed(st[:-2])):
         if n == 1:
             continue
         if row is None:
-            row, step = s, s
-        elif s != step:
+            row = x
+        elif x != step:
             raise ValueError(f"{name}: the token rows must be evenly spaced (strides {st})")
-        step = s * n
-    return dense if row is None else row
+        step = x * n
+    return size[-2] * size[-1] if row is None else row
 
 
-def _need(t, name, device, dtype, shape):
-    """Checks a dense tensor (or None)."""
+def _dense(t, name, dtype, device, shape):
+    """Checks a dense tensor; returns its address (None: None)."""
     if t is None:
-        return
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        return None
+    if t.dtype != dtype or t.get_device() != device or t.shape != shape:
+        _refuse(t, name, dtype, device, shape)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _call(device, stream, fn, *args):
     """Runs a library call with the tensors' device current and its stream
     last in the arguments; raises on a non-OK status."""
-    with _device(device):
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        _check(fn(*args, ctypes.c_void_p(s)))
+    if torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            return _call(device, stream, fn, *args)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    status = fn(*args, stream)
+    if status:
+        lib = load()
+        raise KlaError(status, lib.kla_last_error_message().decode() or
+                       lib.kla_status_str(status).decode())
 
 
-class _Nothing:
-    def __enter__(self):
-        return None
+def _workspace(device, size, args, t, workspace):
+    """The workspace that the library asks for, on t's device: its address and
+    size in bytes."""
+    if torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            return _workspace(device, size, args, t, workspace)
+    need = size(*args)
+    if workspace is None:
+        # kept by the caller's variable until the call is enqueued
+        return torch.empty(need, dtype=torch.uint8, device=t.device) if need else None, need
+    have = workspace.numel() * workspace.element_size()
+    if workspace.get_device() != device:
+        raise ValueError(f"workspace must be on cuda:{device}, got {workspace.device}")
+    if have < need:
+        raise ValueError(f"workspace needs {need} bytes")
+    return workspace, have
 
-    def __exit__(self, *a):
-        return False
 
-
-_nothing = _Nothing()
-
-
-def _device(device):
-    return _nothing if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 @functools.lru_cache(maxsize=64)
@@ -107,32 +128,46 @@ def _option(table, value, name):
 
 
 def _conditioning(q, k, positions, inv_freq, wq, wk, sections, norm_q, norm_k, style):
-    """The checks that forward and backward share."""
-    dt = _dtype_code(q)
-    qs = _rows(q, "q")
-    lead, (hq, d) = q.shape[:-2], q.shape[-2:]
-    hk, ks = 0, 0
+    """The checks that forward and backward share; returns the arguments up to
+    the outputs and those behind them."""
+    dt, dev, kind = _type_code(q), q.get_device(), q.dtype
+    shape = q.shape
+    if len(shape) < 3:
+        raise ValueError(f"q must have shape [..., heads, d], got {tuple(shape)}")
+    lead, hq, d = shape[:-2], shape[-2], shape[-1]
+    qs, hk, ks = _rows(q, "q", kind, dev, shape), 0, 0
     if k is not None:
-        ks = _rows(k, "k", q, lead, None, d)
-        hk = k.shape[-2]
+        hk = k.shape[-2] if k.dim() > 1 else 0
+        ks = _rows(k, "k", kind, dev, lead + (hk, d))
     elif wk is not None:
         raise ValueError("wk needs k")
-    _need(wq, "wq", q.device, torch.float32, (d,))
-    _need(wk, "wk", q.device, torch.float32, (d,))
-    pairs = 0 if inv_freq is None else inv_freq.numel()
-    tokens = math.prod(lead)
-    axes = 1
-    if pairs:
-        sections = (pairs,) if sections is None else tuple(int(n) for n in sections)
-        axes = len(sections)
-        _need(inv_freq, "inv_freq", q.device, torch.float32, (pairs,))
+    w = (d,)
+    pairs, sec, axes, pos, freq = 0, None, 1, None, None
+    if inv_freq is not None and inv_freq.numel():
+        pairs = inv_freq.numel()
+        sec = (pairs,) if sections is None else tuple(sections)
+        axes = len(sec)
+        sec = _sections(sec)
+        freq = _dense(inv_freq, "inv_freq", torch.float32, dev, (pairs,))
         if positions is None:
             raise ValueError("inv_freq needs positions")
-        one = axes == 1 and tuple(positions.shape) == tuple(lead)
-        _need(positions, "positions", q.device, torch.int32, lead if one else (axes, *lead))
-    return (dt, qs, ks, tokens, hq, hk, d, 2 * pairs, _sections(sections) if pairs else None, axes,
-            _option(_STYLES, style, "style"), _option(_NORMS, norm_q, "norm_q"),
-            _option(_NORMS, norm_k, "norm_k"))
+        one = axes == 1 and positions.shape == lead
+        pos = _dense(positions, "positions", torch.int32, dev, lead if one else (axes, *lead))
+    ins = (q.data_ptr(), qs, _at(k), ks, _dense(wq, "wq", torch.float32, dev, w),
+           _dense(wk, "wk", torch.float32, dev, w), pos, freq)
+    end = (lead.numel(), hq, hk, d, 2 * pairs, sec, axes, _option(_STYLES, style, "style"),
+           _option(_NORMS, norm_q, "norm_q"), _option(_NORMS, norm_k, "norm_k"))
+    return dev, dt, ins, end
+
+
+def _out_rows(t, name, like):
+    """An output of like's shape, made dense where there is none; with its row
+    stride."""
+    if t is None:
+        shape = like.shape
+        return (torch.empty(shape, dtype=like.dtype, device=like.device),
+                shape[-2] * shape[-1])
+    return t, _rows(t, name, like.dtype, like.get_device(), like.shape)
 
 
 def kla_qk_norm_rope_fwd(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, norm_q="rms",
@@ -146,19 +181,16 @@ def kla_qk_norm_rope_fwd(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, 
     norm_k: "rms", "l2" or "none"; style "half" (features i, i + rot/2) or
     "pairs" (2i, 2i + 1).  q_out, k_out may be q and k (in place).  Returns
     (q_out, k_out)."""
-    dt, qs, ks, n, hq, hk, d, rot, sec, axes, st, nq, nk = _conditioning(
-        q, k, positions, inv_freq, wq, wk, sections, norm_q, norm_k, style)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    qo = _rows(q_out, "q_out", q, q.shape[:-2], hq, d)
+    dev, dt, ins, end = _conditioning(q, k, positions, inv_freq, wq, wk, sections, norm_q,
+                                      norm_k, style)
+    q_out, qo = _out_rows(q_out, "q_out", q)
     ko = 0
-    if k is not None:
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        ko = _rows(k_out, "k_out", q, k.shape[:-2], hk, d)
-    _call(q.device, stream, load().kla_qk_norm_rope_fwd, _ptr(q), qs, _ptr(k), ks, _ptr(wq),
-          _ptr(wk), _ptr(positions), _ptr(inv_freq), _ptr(q_out), qo, _ptr(k_out), ko, n, hq, hk,
-          d, rot, sec, axes, st, nq, nk, float(eps), dt)
+    if k is None:
+        k_out = None
+    else:
+        k_out, ko = _out_rows(k_out, "k_out", k)
+    _call(dev, stream, load().kla_qk_norm_rope_fwd, *ins, q_out.data_ptr(), qo, _at(k_out), ko,
+          *end, eps, dt)
     return q_out, k_out
 
 
@@ -172,30 +204,29 @@ def kla_qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, wq=None, wk=
     """Backward of kla_qk_norm_rope_fwd on the same inputs: dq_out, dk_out are
     the gradients of its outputs.  Returns (dq, dk, dwq, dwk), None for what is
     not there (k, a weight)."""
-    dt, qs, ks, n, hq, hk, d, rot, sec, axes, st, nq, nk = _conditioning(
-        q, k, positions, inv_freq, wq, wk, sections, norm_q, norm_k, style)
-    gqs = _rows(dq_out, "dq_out", q, q.shape[:-2], hq, d)
-    if dq is None:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dqs = _rows(dq, "dq", q, q.shape[:-2], hq, d)
+    dev, dt, ins, end = _conditioning(q, k, positions, inv_freq, wq, wk, sections, norm_q,
+                                      norm_k, style)
+    gqs = _rows(dq_out, "dq_out", q.dtype, dev, q.shape)
+    dq, dqs = _out_rows(dq, "dq", q)
     gks = dks = 0
-    if k is not None:
-        gks = _rows(dk_out, "dk_out", q, k.shape[:-2], hk, d)
-        if dk is None:
-            dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        dks = _rows(dk, "dk", q, k.shape[:-2], hk, d)
-    else:
+    if k is None:
         dk_out = dk = None
+    elif dk_out is None:
+        raise ValueError("dk_out must be given with k")
+    else:
+        gks = _rows(dk_out, "dk_out", q.dtype, dev, k.shape)
+        dk, dks = _out_rows(dk, "dk", k)
     dwq = None if wq is None else torch.empty_like(wq)
     dwk = None if wk is None else torch.empty_like(wk)
-    need = 0
+    lib, wsb = load(), 0
     if dwq is not None or dwk is not None:
-        need = kla_qk_norm_rope_bwd_workspace_size(n, hq, hk, d)
-    workspace, wsb = _workspace(need, q.device, workspace)
-    _call(q.device, stream, load().kla_qk_norm_rope_bwd, _ptr(q), qs, _ptr(k), ks, _ptr(wq),
-          _ptr(wk), _ptr(positions), _ptr(inv_freq), _ptr(dq_out), gqs, _ptr(dk_out), gks,
-          _ptr(dq), dqs, _ptr(dk), dks, _ptr(dwq), _ptr(dwk), n, hq, hk, d, rot, sec, axes, st,
-          nq, nk, float(eps), dt, _ptr(workspace), wsb)
+        workspace, wsb = _workspace(dev, lib.kla_qk_norm_rope_bwd_workspace_size, end[:4], q,
+                                    workspace)
+    else:
+        workspace = None
+    _call(dev, stream, lib.kla_qk_norm_rope_bwd, *ins, dq_out.data_ptr(), gqs, _at(dk_out), gks,
+          dq.data_ptr(), dqs, _at(dk), dks, _at(dwq), _at(dwk), *end, eps, dt, _at(workspace),
+          wsb)
     return dq, dk, dwq, dwk
 
 
@@ -251,29 +282,29 @@ def kla_attn_bwd_varlen_workspace_size(N, total_q, total_k, Hq, Hk, d, dtype=1) 
 
 
 def _qkv(q, k, v, dims):
-    """Checks q, k, v of `dims` dimensions; returns their row strides, the
-    dtype code and (Hq, Hk, d)."""
-    if q.dim() != dims:
-        raise ValueError(f"q must have {dims} dimensions, got {tuple(q.shape)}")
-    dt = _dtype_code(q)
-    qs = _rows(q, "q")
-    hq, d = q.shape[-2:]
-    if k.dim() != dims or (dims == 4 and k.shape[0] != q.shape[0]):
-        raise ValueError(f"k must have q's batch, got {tuple(k.shape)}")
-    ks = _rows(k, "k", q, None, None, d)
-    vs = _rows(v, "v", q, k.shape[:-2], k.shape[-2], d)
-    return (_ptr(q), qs, _ptr(k), ks, _ptr(v), vs), dt, (hq, k.shape[-2], d)
+    """Checks q, k, v of `dims` dimensions; returns the device, the dtype code,
+    their addresses and row strides, and (Hq, Hk, d)."""
+    if q.dim() != dims or k.dim() != dims:
+        raise ValueError(f"q and k must have {dims} dimensions, got {tuple(q.shape)} and "
+                         f"{tuple(k.shape)}")
+    dt, dev, kind = _type_code(q), q.get_device(), q.dtype
+    qs, hq, d = _rows(q, "q", kind, dev, q.shape), q.shape[-2], q.shape[-1]
+    nk, hk = k.shape[-3], k.shape[-2]
+    shape = (q.shape[0], nk, hk, d) if dims == 4 else (nk, hk, d)
+    ks, vs = _rows(k, "k", kind, dev, shape), _rows(v, "v", kind, dev, shape)
+    return dev, dt, (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs), (hq, hk, d)
 
 
-def _out(t, name, shape, dtype, device, want=True):
-    if t is None and want:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(t, name, device, dtype, shape)
-    return t
+def _out(t, name, shape, dtype, like):
+    """A dense output, made where there is none; and its address."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+        return t, t.data_ptr()
+    return t, _dense(t, name, dtype, like.get_device(), shape)
 
 
 def _scale(scale, d):
-    return 1.0 / math.sqrt(d) if scale is None else float(scale)
+    return 1.0 / math.sqrt(d) if scale is None else scale
 
 
 def kla_attn_fwd(q, k, v, scale=None, k_lens=None, o=None, lse=None, return_lse=True,
@@ -283,28 +314,26 @@ def kla_attn_fwd(q, k, v, scale=None, k_lens=None, o=None, lse=None, return_lse=
     k_lens: int32 [B], the keys of each sequence of a padded cache, or None
     (all Tk); scale: 1/sqrt(d) unless given.  Returns (o, lse), o dense, lse
     [B,Tq,Hq] fp32 (None with return_lse=False)."""
-    rows, dt, (hq, hk, d) = _qkv(q, k, v, 4)
+    dev, dt, rows, (hq, hk, d) = _qkv(q, k, v, 4)
     B, Tq, Tk = q.shape[0], q.shape[1], k.shape[1]
-    _need(k_lens, "k_lens", q.device, torch.int32, (B,))
-    o = _out(o, "o", q.shape, q.dtype, q.device)
-    lse = _out(lse, "lse", (B, Tq, hq), torch.float32, q.device, return_lse)
-    lib = load()
-    with _device(q.device):
-        need = int(lib.kla_attn_fwd_workspace_size(B, Tq, Tk, hq, hk, d, dt))
-    workspace, wsb = _workspace(need, q.device, workspace)
-    _call(q.device, stream, lib.kla_attn_fwd, *rows, _ptr(k_lens), _scale(scale, d), _ptr(o),
-          _ptr(lse), B, Tq, Tk, hq, hk, d, dt, _ptr(workspace), wsb)
+    lens = _dense(k_lens, "k_lens", torch.int32, dev, (B,))
+    o, at = _out(o, "o", q.shape, q.dtype, q)
+    stats = None
+    if return_lse or lse is not None:
+        lse, stats = _out(lse, "lse", (B, Tq, hq), torch.float32, q)
+    lib, sizes = load(), (B, Tq, Tk, hq, hk, d, dt)
+    workspace, wsb = _workspace(dev, lib.kla_attn_fwd_workspace_size, sizes, q, workspace)
+    _call(dev, stream, lib.kla_attn_fwd, *rows, lens, _scale(scale, d), at, stats, *sizes,
+          _at(workspace), wsb)
     return o, lse
 
 
-def _tables(q, cu_q, cu_k):
-    if cu_k is None:
-        cu_k = cu_q
-    _need(cu_q, "cu_seqlens_q", q.device, torch.int32, (cu_q.numel(),))
-    _need(cu_k, "cu_seqlens_k", q.device, torch.int32, (cu_q.numel(),))
-    if cu_q.numel() < 1:
+def _tables(q, dev, cu_q, cu_k):
+    n = cu_q.numel()
+    if n < 1:
         raise ValueError("cu_seqlens_q must have N + 1 entries")
-    return cu_k, cu_q.numel() - 1
+    at = _dense(cu_q, "cu_seqlens_q", torch.int32, dev, (n,))
+    return at, at if cu_k is None else _dense(cu_k, "cu_seqlens_k", torch.int32, dev, (n,)), n - 1
 
 
 def kla_attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, o=None, lse=None,
@@ -312,68 +341,65 @@ def kla_attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, o=
     """kla_attn_fwd over packed sequences: q [total_q,Hq,d], k, v [total_k,Hk,d],
     cu_seqlens_q, cu_seqlens_k: int32 [N+1] on the device (cu_seqlens_k None:
     the same table).  Returns (o, lse)."""
-    rows, dt, (hq, hk, d) = _qkv(q, k, v, 3)
-    cu_k, N = _tables(q, cu_seqlens_q, cu_seqlens_k)
-    nq, nk = q.shape[0], k.shape[0]
-    o = _out(o, "o", q.shape, q.dtype, q.device)
-    lse = _out(lse, "lse", (nq, hq), torch.float32, q.device, return_lse)
-    lib = load()
-    with _device(q.device):
-        need = int(lib.kla_attn_fwd_varlen_workspace_size(N, nq, nk, hq, hk, d, dt))
-    workspace, wsb = _workspace(need, q.device, workspace)
-    _call(q.device, stream, lib.kla_attn_fwd_varlen, *rows, _ptr(cu_seqlens_q), _ptr(cu_k),
-          _scale(scale, d), _ptr(o), _ptr(lse), N, nq, nk, hq, hk, d, dt, _ptr(workspace), wsb)
+    dev, dt, rows, (hq, hk, d) = _qkv(q, k, v, 3)
+    cu_q, cu_k, N = _tables(q, dev, cu_seqlens_q, cu_seqlens_k)
+    o, at = _out(o, "o", q.shape, q.dtype, q)
+    stats = None
+    if return_lse or lse is not None:
+        lse, stats = _out(lse, "lse", q.shape[:-1], torch.float32, q)
+    lib, sizes = load(), (N, q.shape[0], k.shape[0], hq, hk, d, dt)
+    workspace, wsb = _workspace(dev, lib.kla_attn_fwd_varlen_workspace_size, sizes, q, workspace)
+    _call(dev, stream, lib.kla_attn_fwd_varlen, *rows, cu_q, cu_k, _scale(scale, d), at, stats,
+          *sizes, _at(workspace), wsb)
     if check_status:
-        _call(q.device, stream, lib.kla_workspace_status, _ptr(workspace), wsb)
+        _call(dev, None, _status, workspace, wsb, stream)
     return o, lse
 
 
-def _grads(q, k, v, o, lse, d_o, dq, dk, dv):
-    """Checks what the backward takes and allocates what it writes."""
-    gs = _rows(d_o, "d_o", q, q.shape[:-2], *q.shape[-2:])
-    _need(o, "o", q.device, q.dtype, q.shape)
-    _need(lse, "lse", q.device, torch.float32, q.shape[:-1])
-    dq = _out(dq, "dq", q.shape, q.dtype, q.device)
-    dk = _out(dk, "dk", k.shape, k.dtype, k.device)
-    dv = _out(dv, "dv", v.shape, v.dtype, v.device)
-    return gs, dq, dk, dv
+def _status(workspace, wsb, stream, current):
+    stream = current if stream is None else getattr(stream, "cuda_stream", stream)
+    return load().kla_workspace_status(_at(workspace), wsb, stream)
+
+
+def _grads(q, k, v, o, lse, d_o, dev, dq, dk, dv):
+    """Checks what the backward takes and makes what it writes: the arguments
+    of the forward's results and of the gradients, and those."""
+    gs = _rows(d_o, "d_o", q.dtype, dev, q.shape)
+    ins = (_dense(o, "o", q.dtype, dev, q.shape),
+           _dense(lse, "lse", torch.float32, dev, q.shape[:-1]), d_o.data_ptr(), gs)
+    dq, a = _out(dq, "dq", q.shape, q.dtype, q)
+    dk, b = _out(dk, "dk", k.shape, q.dtype, q)
+    dv, c = _out(dv, "dv", v.shape, q.dtype, q)
+    return ins, (a, b, c), (dq, dk, dv)
 
 
 def kla_attn_bwd(q, k, v, o, lse, d_o, scale=None, dq=None, dk=None, dv=None, workspace=None,
                  stream=None):
     """Backward of kla_attn_fwd (without k_lens): the gradients of sum <d_o, o>
     from the forward's inputs and its o and lse.  Returns (dq, dk, dv), dense."""
-    rows, dt, (hq, hk, d) = _qkv(q, k, v, 4)
-    B, Tq, Tk = q.shape[0], q.shape[1], k.shape[1]
-    gs, dq, dk, dv = _grads(q, k, v, o, lse, d_o, dq, dk, dv)
-    lib = load()
-    with _device(q.device):
-        need = int(lib.kla_attn_bwd_workspace_size(B, Tq, Tk, hq, hk, d, dt))
-    workspace, wsb = _workspace(need, q.device, workspace)
-    _call(q.device, stream, lib.kla_attn_bwd, *rows, _ptr(o), _ptr(lse), _ptr(d_o), gs,
-          _scale(scale, d), _ptr(dq), _ptr(dk), _ptr(dv), B, Tq, Tk, hq, hk, d, dt,
-          _ptr(workspace), wsb)
-    return dq, dk, dv
+    dev, dt, rows, (hq, hk, d) = _qkv(q, k, v, 4)
+    ins, at, grads = _grads(q, k, v, o, lse, d_o, dev, dq, dk, dv)
+    lib, sizes = load(), (q.shape[0], q.shape[1], k.shape[1], hq, hk, d, dt)
+    workspace, wsb = _workspace(dev, lib.kla_attn_bwd_workspace_size, sizes, q, workspace)
+    _call(dev, stream, lib.kla_attn_bwd, *rows, *ins, _scale(scale, d), *at, *sizes,
+          _at(workspace), wsb)
+    return grads
 
 
 def kla_attn_bwd_varlen(q, k, v, o, lse, d_o, cu_seqlens_q, cu_seqlens_k=None, scale=None,
                         dq=None, dk=None, dv=None, workspace=None, stream=None,
                         check_status=False):
     """Backward of kla_attn_fwd_varlen; otherwise as kla_attn_bwd."""
-    rows, dt, (hq, hk, d) = _qkv(q, k, v, 3)
-    cu_k, N = _tables(q, cu_seqlens_q, cu_seqlens_k)
-    nq, nk = q.shape[0], k.shape[0]
-    gs, dq, dk, dv = _grads(q, k, v, o, lse, d_o, dq, dk, dv)
-    lib = load()
-    with _device(q.device):
-        need = int(lib.kla_attn_bwd_varlen_workspace_size(N, nq, nk, hq, hk, d, dt))
-    workspace, wsb = _workspace(need, q.device, workspace)
-    _call(q.device, stream, lib.kla_attn_bwd_varlen, *rows, _ptr(o), _ptr(lse), _ptr(d_o), gs,
-          _ptr(cu_seqlens_q), _ptr(cu_k), _scale(scale, d), _ptr(dq), _ptr(dk), _ptr(dv), N, nq,
-          nk, hq, hk, d, dt, _ptr(workspace), wsb)
+    dev, dt, rows, (hq, hk, d) = _qkv(q, k, v, 3)
+    cu_q, cu_k, N = _tables(q, dev, cu_seqlens_q, cu_seqlens_k)
+    ins, at, grads = _grads(q, k, v, o, lse, d_o, dev, dq, dk, dv)
+    lib, sizes = load(), (N, q.shape[0], k.shape[0], hq, hk, d, dt)
+    workspace, wsb = _workspace(dev, lib.kla_attn_bwd_varlen_workspace_size, sizes, q, workspace)
+    _call(dev, stream, lib.kla_attn_bwd_varlen, *rows, *ins, cu_q, cu_k, _scale(scale, d), *at,
+          *sizes, _at(workspace), wsb)
     if check_status:
-        _call(q.device, stream, lib.kla_workspace_status, _ptr(workspace), wsb)
-    return dq, dk, dv
+        _call(dev, None, _status, workspace, wsb, stream)
+    return grads
 
 
 class _KlaAttn(torch.autograd.Function):

@@ -50,6 +50,8 @@ def load(build_if_stale: bool = True) -> ctypes.CDLL:
     """Load libkla_gb300.so (compiling it first when sources are newer and
     nvcc is present).  Raises if the library is unavailable."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -1,5 +1,7 @@
 // Causal attention, host side: which kernels a call runs, its workspace and
 // its launches.  The kernels and their reasons are in kla_attn_simt.cu.
+#include <mutex>
+
 #include "kla_attn_tc.cuh"
 
 namespace kla {
@@ -148,7 +150,7 @@ attn::Args make_args(const AttnProblem &p) {
     a.dq = p.dq; a.dk = p.dk; a.dv = p.dv; a.lse_in = p.lse_in; a.lse = p.lse;
     a.q_stride = p.q_stride; a.k_stride = p.k_stride; a.v_stride = p.v_stride;
     a.go_stride = p.go_stride; a.cu_q = p.cu_q; a.cu_k = p.cu_k; a.k_lens = p.k_lens;
-    a.status = static_cast<const unsigned *>(p.ws);
+    a.status = static_cast<unsigned *>(p.ws);
     a.n_seq = p.n_seq; a.Tq = p.Tq; a.Tk = p.Tk; a.Hq = p.Hq; a.Hk = p.Hk; a.G = p.Hq / p.Hk;
     a.splits = 1; a.total_q = p.total_q; a.scale = p.scale;
     a.scale_log2 = p.scale * 1.4426950408889634f;
@@ -159,10 +161,10 @@ unsigned char *at(const AttnProblem &p, size_t offset) {
     return static_cast<unsigned char *>(p.ws) + offset;
 }
 
-// The status word, and of packed sequences the check and the item tables.
+// Of packed sequences: the check, the status word and the item tables.
 cudaError_t prepare(const AttnProblem &p, const AttnTable &t0, const AttnTable &t1,
                     cudaStream_t s) {
-    if (!p.cu_q) return cudaMemsetAsync(p.ws, 0, sizeof(unsigned), s);
+    if (!p.cu_q) return cudaSuccess;
     return launch_attn_prep(p.cu_q, p.cu_k, p.n_seq, p.total_q, p.total_k, t0, t1,
                             static_cast<unsigned *>(p.ws), s);
 }
@@ -174,6 +176,28 @@ void take(attn::Args &a, const Side &x, int2 *table) {
 }
 
 }  // namespace
+
+// The setting stays with the device's context, so each kernel asks once per
+// device (a few kernels: a short list of what was asked for).
+cudaError_t attn_allow_smem(const void *kernel, size_t bytes) {
+    struct Asked {
+        const void *kernel;
+        int device;
+    };
+    constexpr int kMost = 256;
+    static Asked asked[kMost];
+    static int n = 0;
+    static std::mutex lock;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> hold(lock);
+    for (int i = 0; i < n; ++i)
+        if (asked[i].kernel == kernel && asked[i].device == dev) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && n < kMost) asked[n++] = {kernel, dev};
+    return e;
+}
 
 size_t attn_fwd_workspace_bytes(const AttnProblem &p) { return fwd_plan(p).bytes; }
 size_t attn_bwd_workspace_bytes(const AttnProblem &p) { return bwd_plan(p).bytes; }

@@ -26,7 +26,7 @@ struct Args {
     float *delta;                         // backward: rows of sum_d go o, [total_q][Hq]
     long long q_stride, k_stride, v_stride, go_stride;
     const int *cu_q, *cu_k, *k_lens;      // device; cu_*: packed, k_lens: padded keys
-    const unsigned *status;               // packed: the tables' check; not 0: nothing is done
+    unsigned *status;                     // device status word
     const int2 *table;                    // packed: (sequence, tile) of every item
     int n_seq, Tq, Tk, Hq, Hk, G;
     int items;                            // fixed: n_seq * tiles, packed: table entries
@@ -62,6 +62,16 @@ __device__ __forceinline__ Seq sequence(const Args &a, int s) {
     return r;
 }
 
+// Packed sequences whose tables the check refused: nothing is done.
+__device__ __forceinline__ bool rejected(const Args &a) { return a.cu_q && *a.status != kDevOk; }
+
+// Fixed lengths have no check before them: the first block of a call's first
+// kernel clears the status word.  What else writes it is a wait that ran out,
+// a second and more after that block started.
+__device__ __forceinline__ void clear_status(const Args &a) {
+    if (!a.cu_q && blockIdx.x == 0 && threadIdx.x == 0) *a.status = kDevOk;
+}
+
 // The item of a block: sequence, tile, key head and split.  Fixed lengths:
 // the last tiles first (they see the most keys, so the longest blocks start
 // first), key heads and sequences innermost.  False: nothing to do.
@@ -69,7 +79,7 @@ struct Item {
     int seq, tile, head, split;
 };
 __device__ __forceinline__ bool item_of(const Args &a, int block, bool last_first, Item &it) {
-    if (a.status && *a.status != 0) return false;
+    if (rejected(a)) return false;
     it.head = block % a.Hk;
     int x = block / a.Hk;
     if (a.table) {
@@ -110,6 +120,8 @@ struct AttnTable {
 cudaError_t launch_attn_prep(const int *cu_q, const int *cu_k, int n, int total_q, int total_k,
                              const AttnTable &t0, const AttnTable &t1, unsigned *status,
                              cudaStream_t s);
+// Lets a kernel use this much dynamic shared memory on the current device.
+cudaError_t attn_allow_smem(const void *kernel, size_t bytes);
 cudaError_t launch_attn_join(const attn::Args &a, int d, int dtype, cudaStream_t s);
 cudaError_t launch_attn_delta(const attn::Args &a, int d, int dtype, cudaStream_t s);
 

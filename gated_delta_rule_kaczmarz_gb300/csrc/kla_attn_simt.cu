@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(kT) attn_simt_fwd_kernel(const __grid_constant
     constexpr int MI = BM / 16;
     extern __shared__ __align__(16) float sm[];
     float *Q = sm, *KV = Q + BM * (D + 4), *P = KV + 64 * (D + 4);
+    attn::clear_status(a);
     Item it;
     if (!attn::item_of(a, blockIdx.x, true, it)) return;
     const Seq s = attn::sequence(a, it.seq);
@@ -385,7 +386,8 @@ __global__ void __launch_bounds__(kT) attn_simt_dkv_kernel(const __grid_constant
 // Row sums of go o: a warp per (token, head).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ Args a) {
-    if (a.status && *a.status != 0) return;
+    attn::clear_status(a);
+    if (attn::rejected(a)) return;
     const long long n = (long long)a.total_q * a.Hq;
     const long long i = (long long)blockIdx.x * 16 + threadIdx.x / 16;
     const int lane = threadIdx.x % 16;
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
 // o = sum_s exp(lse_s - lse) o_s, lse = log sum_s exp(lse_s): 16 lanes a row.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ Args a) {
-    if (a.status && *a.status != 0) return;
+    if (attn::rejected(a)) return;
     const long long n = (long long)a.total_q * a.Hq;
     const long long i = (long long)blockIdx.x * 16 + threadIdx.x / 16;
     const int lane = threadIdx.x % 16;
@@ -500,8 +502,7 @@ template <typename K>
 cudaError_t launch(K *kernel, const Args &a, size_t smem, cudaStream_t s) {
     const long long blocks = (long long)a.items * a.splits * a.Hk;
     if (blocks == 0) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = attn_allow_smem(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)blocks, kT, smem, s>>>(a);
     note_launch();

@@ -73,6 +73,7 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
     unsigned char *sQ = base, *sKV = base + 2 * C::TILE;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
+    attn::clear_status(a);
     Item it;
     if (!attn::item_of(a, blockIdx.x, true, it)) return;
     const Seq seq = attn::sequence(a, it.seq);
@@ -116,7 +117,7 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
     const uint32_t tb = sh.tmem;
     const auto give_up = [&] {
         sh.abort = 1;
-        if (a.status) *const_cast<unsigned *>(a.status) = kDevTimeout;
+        *a.status = kDevTimeout;
     };
 
     if (warp == 9) {
@@ -385,9 +386,7 @@ template <int D>
 cudaError_t launch_fwd(const Args &a, const Maps &maps, cudaStream_t s) {
     const long long blocks = (long long)a.items * a.splits * a.Hk;
     if (blocks == 0) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(attn_tc_fwd_kernel<D>),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)Cfg<D>::SMEM);
+    cudaError_t e = attn_allow_smem(reinterpret_cast<const void *>(attn_tc_fwd_kernel<D>), Cfg<D>::SMEM);
     if (e != cudaSuccess) return e;
     attn_tc_fwd_kernel<D><<<(unsigned)blocks, kThreads, Cfg<D>::SMEM, s>>>(a, maps);
     note_launch();
