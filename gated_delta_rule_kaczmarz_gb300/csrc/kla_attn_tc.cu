@@ -34,7 +34,7 @@ using attn::kSlab;
 using attn::kTile;
 using attn::Seq;
 
-constexpr int kThreads = 320;            // 8 softmax warps, products, loads
+constexpr int kThreads = 384;            // 8 softmax warps, products, loads, two idle
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kGrow = 8.f;             // see above
 
@@ -120,114 +120,119 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
         *a.status = kDevTimeout;
     };
 
-    if (warp == 9) {
-        // ------------------------------------------------------------- loads
-        if (lane == 0 && nb > 0) {
-            const uint32_t box = (uint32_t)R * 128u;
+    // Registers of a thread: 128 x 88 + 256 x 208 = 384 x 168.
+    if (warp >= 8) {
+        attn::fewer_registers<88>();
+        if (warp == 9) {
+            // ------------------------------------------------------------- loads
+            if (lane == 0 && nb > 0) {
+                const uint32_t box = (uint32_t)R * 128u;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if ((t ? e1 : e0) <= b0) continue;
-                mbar_expect_tx(&sh.q[t], box * C::SLABS);
-                for (int c = 0; c < C::SLABS; ++c)
-                    tma_load_3d(sQ + t * C::TILE + c * kSlab, &maps.q, &sh.q[t], c * 64,
-                                it.head * a.G, (int)(seq.q0 + tok0 + t * TT));
-            }
-            int j = 0;
-            for (; j < 2 * nb; ++j) {
-                const int slot = j % C::SLOTS, use = j / C::SLOTS;
-                if (use > 0 &&
-                    !mbar_wait_or_abort(&sh.empty[slot], (uint32_t)((use - 1) & 1), &sh.abort)) {
-                    give_up();
-                    break;
+                for (int t = 0; t < 2; ++t) {
+                    if ((t ? e1 : e0) <= b0) continue;
+                    mbar_expect_tx(&sh.q[t], box * C::SLABS);
+                    for (int c = 0; c < C::SLABS; ++c)
+                        tma_load_3d(sQ + t * C::TILE + c * kSlab, &maps.q, &sh.q[t], c * 64,
+                                    it.head * a.G, (int)(seq.q0 + tok0 + t * TT));
                 }
-                mbar_expect_tx(&sh.full[slot], C::TILE);
-                const int row = (int)(seq.k0 + (long long)(b0 + j / 2) * kTile);
-                for (int c = 0; c < C::SLABS; ++c)
-                    tma_load_3d(sKV + slot * C::TILE + c * kSlab, j % 2 ? &maps.v : &maps.k,
-                                &sh.full[slot], c * 64, it.head, row);
-            }
-            if (j < 2 * nb) {      // given up: the copies in flight land before the CTA leaves
-                for (int i = max(0, j - C::SLOTS); i < j; ++i)
-                    (void)mbar_wait(&sh.full[i % C::SLOTS], (uint32_t)((i / C::SLOTS) & 1));
-                for (int t = 0; t < 2; ++t)
-                    if ((t ? e1 : e0) > b0) (void)mbar_wait(&sh.q[t], 0u);
-            }
-        }
-    } else if (warp == 8) {
-        // ---------------------------------------------------------- products
-        constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
-        constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true);
-        const uint32_t aQ = smem_u32(sQ), aKV = smem_u32(sKV);
-        const auto scores = [&](int t, int slot) {
-            if (lane == 0) {
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    mma_bf16(tb + C::TM_S + 128u * t, attn::kdesc(aQ + t * C::TILE, ks),
-                             attn::kdesc(aKV + slot * C::TILE, ks), id_s, ks > 0);
-                mma_commit(&sh.s[t]);
-            }
-            __syncwarp();
-        };
-        const auto landed = [&](int j) {
-            return __all_sync(0xffffffffu,
-                              mbar_wait_or_abort(&sh.full[j % C::SLOTS],
-                                                 (uint32_t)((j / C::SLOTS) & 1), &sh.abort));
-        };
-        bool ok = true;
-        if (nb > 0) {
-            ok = landed(0);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if ((t ? e1 : e0) <= b0) continue;
-                ok = ok && __all_sync(0xffffffffu, mbar_wait_or_abort(&sh.q[t], 0u, &sh.abort));
-                if (ok) {
-                    tc_fence_after();
-                    scores(t, 0);
+                int j = 0;
+                for (; j < 2 * nb; ++j) {
+                    const int slot = j % C::SLOTS, use = j / C::SLOTS;
+                    if (use > 0 &&
+                        !mbar_wait_or_abort(&sh.empty[slot], (uint32_t)((use - 1) & 1), &sh.abort)) {
+                        give_up();
+                        break;
+                    }
+                    mbar_expect_tx(&sh.full[slot], C::TILE);
+                    const int row = (int)(seq.k0 + (long long)(b0 + j / 2) * kTile);
+                    for (int c = 0; c < C::SLABS; ++c)
+                        tma_load_3d(sKV + slot * C::TILE + c * kSlab, j % 2 ? &maps.v : &maps.k,
+                                    &sh.full[slot], c * 64, it.head, row);
+                }
+                if (j < 2 * nb) {      // given up: the copies in flight land before the CTA leaves
+                    for (int i = max(0, j - C::SLOTS); i < j; ++i)
+                        (void)mbar_wait(&sh.full[i % C::SLOTS], (uint32_t)((i / C::SLOTS) & 1));
+                    for (int t = 0; t < 2; ++t)
+                        if ((t ? e1 : e0) > b0) (void)mbar_wait(&sh.q[t], 0u);
                 }
             }
-            if (ok && lane == 0) mma_commit(&sh.empty[0]);
-            __syncwarp();
-        }
-        for (int n = 0; ok && n < nb; ++n) {
-            const int jv = 2 * n + 1, jk = 2 * n + 2, sv = jv % C::SLOTS;
-            ok = landed(jv);
-            if (!ok) break;
-            const int valid = seq.lk - (b0 + n) * kTile;
-            if (valid < kTile) attn::zero_rows<C::SLABS>(sKV + sv * C::TILE, valid, lane);
-            if (n + 1 < nb) ok = landed(jk);
-            if (!ok) break;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int e = t ? e1 : e0;
-                if (b0 + n >= e) continue;
-                ok = ok && __all_sync(0xffffffffu, mbar_wait_or_abort(&sh.p[t], (uint32_t)(n & 1),
-                                                                      &sh.abort));
-                if (!ok) break;
-                tc_fence_after();
+        } else if (warp == 8) {
+            // ---------------------------------------------------------- products
+            constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
+            constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true);
+            const uint32_t aQ = smem_u32(sQ), aKV = smem_u32(sKV);
+            const auto scores = [&](int t, int slot) {
                 if (lane == 0) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_bf16_ts(tb + C::TM_O + (uint32_t)(D * t),
-                                    tb + C::TM_S + 128u * t + 8u * ks,
-                                    attn::mdesc(aKV + sv * C::TILE, ks), id_o, n > 0 || ks > 0);
-                    mma_commit(&sh.o[t]);
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_bf16(tb + C::TM_S + 128u * t, attn::kdesc(aQ + t * C::TILE, ks),
+                                 attn::kdesc(aKV + slot * C::TILE, ks), id_s, ks > 0);
+                    mma_commit(&sh.s[t]);
                 }
                 __syncwarp();
-                if (b0 + n + 1 < e) scores(t, jk % C::SLOTS);
+            };
+            const auto landed = [&](int j) {
+                return __all_sync(0xffffffffu,
+                                  mbar_wait_or_abort(&sh.full[j % C::SLOTS],
+                                                     (uint32_t)((j / C::SLOTS) & 1), &sh.abort));
+            };
+            bool ok = true;
+            if (nb > 0) {
+                ok = landed(0);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if ((t ? e1 : e0) <= b0) continue;
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait_or_abort(&sh.q[t], 0u, &sh.abort));
+                    if (ok) {
+                        tc_fence_after();
+                        scores(t, 0);
+                    }
+                }
+                if (ok && lane == 0) mma_commit(&sh.empty[0]);
+                __syncwarp();
             }
-            if (ok && lane == 0) {
-                mma_commit(&sh.empty[sv]);
-                if (n + 1 < nb) mma_commit(&sh.empty[jk % C::SLOTS]);
+            for (int n = 0; ok && n < nb; ++n) {
+                const int jv = 2 * n + 1, jk = 2 * n + 2, sv = jv % C::SLOTS;
+                ok = landed(jv);
+                if (!ok) break;
+                const int valid = seq.lk - (b0 + n) * kTile;
+                if (valid < kTile) attn::zero_rows<C::SLABS>(sKV + sv * C::TILE, valid, lane);
+                if (n + 1 < nb) ok = landed(jk);
+                if (!ok) break;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int e = t ? e1 : e0;
+                    if (b0 + n >= e) continue;
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait_or_abort(&sh.p[t], (uint32_t)(n & 1),
+                                                                          &sh.abort));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_bf16_ts(tb + C::TM_O + (uint32_t)(D * t),
+                                        tb + C::TM_S + 128u * t + 8u * ks,
+                                        attn::mdesc(aKV + sv * C::TILE, ks), id_o, n > 0 || ks > 0);
+                        mma_commit(&sh.o[t]);
+                    }
+                    __syncwarp();
+                    if (b0 + n + 1 < e) scores(t, jk % C::SLOTS);
+                }
+                if (ok && lane == 0) {
+                    mma_commit(&sh.empty[sv]);
+                    if (n + 1 < nb) mma_commit(&sh.empty[jk % C::SLOTS]);
+                }
+                __syncwarp();
             }
+            if (!ok) give_up();
+            // every product issued has completed before the tensor memory is released
+            if (lane == 0) mma_commit(&sh.fin);
             __syncwarp();
+            (void)mbar_wait(&sh.fin, 0u);
         }
-        if (!ok) give_up();
-        // every product issued has completed before the tensor memory is released
-        if (lane == 0) mma_commit(&sh.fin);
-        __syncwarp();
-        (void)mbar_wait(&sh.fin, 0u);
     } else {
         // ----------------------------------------------------------- softmax
+        attn::more_registers<208>();
         const int t = warp / 4, w = warp % 4, r = 32 * w + lane;
         const int e = t ? e1 : e0;
         const int tok = tok0 + t * TT + r / a.G, head = it.head * a.G + r % a.G;
@@ -258,14 +263,19 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                         for (int k = 0; k < 32; ++k)
                             if (32 * j + k > rel) x[j][k] = 0xff800000u;      // -infinity
                 }
-                float mx[4];
+                float mx[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    mx[j] = __uint_as_float(x[j][0]);
+                for (int j = 0; j < 8; ++j) mx[j] = __uint_as_float(x[0][j]);
 #pragma unroll
-                    for (int k = 1; k < 32; ++k) mx[j] = fmaxf(mx[j], __uint_as_float(x[j][k]));
-                }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                for (int k = 8; k < 128; k += 16)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        mx[j] = k + 8 + j < 128
+                                    ? attn::max3(mx[j], __uint_as_float(x[(k + j) / 32][(k + j) % 32]),
+                                                 __uint_as_float(x[(k + 8 + j) / 32][(k + 8 + j) % 32]))
+                                    : fmaxf(mx[j], __uint_as_float(x[(k + j) / 32][(k + j) % 32]));
+                const float top = fmaxf(attn::max3(mx[0], mx[1], mx[2]),
+                                        attn::max3(attn::max3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
                 const bool grow = row && (top - m) * c > kGrow;
                 if (i == 0) {
                     m = top;
