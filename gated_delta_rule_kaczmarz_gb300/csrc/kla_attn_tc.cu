@@ -50,8 +50,8 @@ struct Cfg {
 struct Shared {
     uint64_t full[8], empty[8];          // ring slots
     uint64_t q[2];                       // Q tiles landed
-    uint64_t s[2], p[2], o[2];           // scores ready, probabilities ready, product done
-    uint64_t fin;
+    uint64_t s[2], p[2][2], o[2];        // scores ready, halves of the probabilities, product done
+    uint64_t tail, fin;
     uint32_t tmem;
     volatile int abort;
 };
@@ -103,9 +103,11 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sh.q[t], 1);
             mbar_init(&sh.s[t], 1);
-            mbar_init(&sh.p[t], 4);
+            mbar_init(&sh.p[t][0], 4);
+            mbar_init(&sh.p[t][1], 4);
             mbar_init(&sh.o[t], 1);
         }
+        mbar_init(&sh.tail, 1);
         mbar_init(&sh.fin, 1);
         sh.abort = 0;
         fence_mbar_init();
@@ -125,6 +127,7 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
         attn::fewer_registers<88>();
         if (warp == 9) {
             // ------------------------------------------------------------- loads
+            bool ok = true;
             if (lane == 0 && nb > 0) {
                 const uint32_t box = (uint32_t)R * 128u;
 #pragma unroll
@@ -149,82 +152,80 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                         tma_load_3d(sKV + slot * C::TILE + c * kSlab, j % 2 ? &maps.v : &maps.k,
                                     &sh.full[slot], c * 64, it.head, row);
                 }
-                if (j < 2 * nb) {      // given up: the copies in flight land before the CTA leaves
+                ok = j == 2 * nb;
+                if (!ok) {      // given up: the copies in flight land before the CTA leaves
                     for (int i = max(0, j - C::SLOTS); i < j; ++i)
                         (void)mbar_wait(&sh.full[i % C::SLOTS], (uint32_t)((i / C::SLOTS) & 1));
                     for (int t = 0; t < 2; ++t)
                         if ((t ? e1 : e0) > b0) (void)mbar_wait(&sh.q[t], 0u);
                 }
             }
+            const int valid = seq.lk - (b1 - 1) * kTile;
+            if (__all_sync(0xffffffffu, ok) && nb > 0 && valid < kTile) {
+                const int j = 2 * nb - 1, slot = j % C::SLOTS;
+                if (__all_sync(0xffffffffu, mbar_wait(&sh.full[slot], (uint32_t)((j / C::SLOTS) & 1)))) {
+                    attn::zero_rows<C::SLABS>(sKV + slot * C::TILE, valid, lane);
+                    if (lane == 0) mbar_arrive(&sh.tail);
+                }
+            }
         } else if (warp == 8) {
             // ---------------------------------------------------------- products
+            // One lane waits and issues: a warp-wide vote after every wait
+            // costs more than the queue of products holds (about 300 cycles).
             constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true);
             const uint32_t aQ = smem_u32(sQ), aKV = smem_u32(sKV);
+            const auto wait = [&](uint64_t *bar, int phase) {
+                return mbar_wait_or_abort(bar, (uint32_t)(phase & 1), &sh.abort);
+            };
+            const auto landed = [&](int j) { return wait(&sh.full[j % C::SLOTS], j / C::SLOTS); };
             const auto scores = [&](int t, int slot) {
-                if (lane == 0) {
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        mma_bf16(tb + C::TM_S + 128u * t, attn::kdesc(aQ + t * C::TILE, ks),
-                                 attn::kdesc(aKV + slot * C::TILE, ks), id_s, ks > 0);
-                    mma_commit(&sh.s[t]);
-                }
-                __syncwarp();
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_bf16(tb + C::TM_S + 128u * t, attn::kdesc(aQ + t * C::TILE, ks),
+                             attn::kdesc(aKV + slot * C::TILE, ks), id_s, ks > 0);
+                mma_commit(&sh.s[t]);
             };
-            const auto landed = [&](int j) {
-                return __all_sync(0xffffffffu,
-                                  mbar_wait_or_abort(&sh.full[j % C::SLOTS],
-                                                     (uint32_t)((j / C::SLOTS) & 1), &sh.abort));
-            };
-            bool ok = true;
-            if (nb > 0) {
-                ok = landed(0);
+            if (lane == 0 && nb > 0) {
+                bool ok = landed(0);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if ((t ? e1 : e0) <= b0) continue;
-                    ok = ok && __all_sync(0xffffffffu, mbar_wait_or_abort(&sh.q[t], 0u, &sh.abort));
-                    if (ok) {
-                        tc_fence_after();
-                        scores(t, 0);
-                    }
+                    ok = ok && wait(&sh.q[t], 0);
+                    if (ok) scores(t, 0);
                 }
-                if (ok && lane == 0) mma_commit(&sh.empty[0]);
-                __syncwarp();
-            }
-            for (int n = 0; ok && n < nb; ++n) {
-                const int jv = 2 * n + 1, jk = 2 * n + 2, sv = jv % C::SLOTS;
-                ok = landed(jv);
-                if (!ok) break;
-                const int valid = seq.lk - (b0 + n) * kTile;
-                if (valid < kTile) attn::zero_rows<C::SLABS>(sKV + sv * C::TILE, valid, lane);
-                if (n + 1 < nb) ok = landed(jk);
-                if (!ok) break;
+                if (ok) mma_commit(&sh.empty[0]);
+                // the last V tile may hold a neighbour's rows: they are zeroed first
+                const bool ragged = b1 * kTile > seq.lk;
+                for (int n = 0; ok && n < nb; ++n) {
+                    const int jv = 2 * n + 1, jk = 2 * n + 2, sv = jv % C::SLOTS;
+                    ok = landed(jv) && (n + 1 >= nb ? !ragged || wait(&sh.tail, 0) : landed(jk));
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int e = t ? e1 : e0;
-                    if (b0 + n >= e) continue;
-                    ok = ok && __all_sync(0xffffffffu, mbar_wait_or_abort(&sh.p[t], (uint32_t)(n & 1),
-                                                                          &sh.abort));
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (lane == 0) {
+                    for (int t = 0; t < 2; ++t) {
+                        const int e = t ? e1 : e0;
+                        if (b0 + n >= e) continue;
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            mma_bf16_ts(tb + C::TM_O + (uint32_t)(D * t),
-                                        tb + C::TM_S + 128u * t + 8u * ks,
-                                        attn::mdesc(aKV + sv * C::TILE, ks), id_o, n > 0 || ks > 0);
+                        for (int h = 0; h < 2; ++h) {      // as the halves of P come
+                            ok = ok && wait(&sh.p[t][h], n);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                                mma_bf16_ts(tb + C::TM_O + (uint32_t)(D * t),
+                                            tb + C::TM_S + 128u * t + 8u * ks,
+                                            attn::mdesc(aKV + sv * C::TILE, ks), id_o,
+                                            n > 0 || ks > 0);
+                        }
+                        if (!ok) break;
                         mma_commit(&sh.o[t]);
+                        if (b0 + n + 1 < e) scores(t, jk % C::SLOTS);
                     }
-                    __syncwarp();
-                    if (b0 + n + 1 < e) scores(t, jk % C::SLOTS);
-                }
-                if (ok && lane == 0) {
+                    if (!ok) break;
                     mma_commit(&sh.empty[sv]);
                     if (n + 1 < nb) mma_commit(&sh.empty[jk % C::SLOTS]);
                 }
-                __syncwarp();
+                if (!ok) give_up();
             }
-            if (!ok) give_up();
             // every product issued has completed before the tensor memory is released
             if (lane == 0) mma_commit(&sh.fin);
             __syncwarp();
@@ -325,13 +326,16 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                         y[k / 2 + 1] = attn::pack2(p[2], p[3]);
                     }
                     attn::tmem_st32(tS + 32u * h, y);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.p[t][h]);
                 }
                 l += (s0 + s1) + (s2 + s3);
-                tmem_st_wait();
+            } else if (lane == 0) {
+                mbar_arrive(&sh.p[t][0]);
+                mbar_arrive(&sh.p[t][1]);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p[t]);
         }
         if (ok && e > b0) {
             ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&sh.o[t], (uint32_t)((e - b0 - 1) & 1),
