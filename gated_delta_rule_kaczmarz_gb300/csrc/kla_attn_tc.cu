@@ -4,8 +4,10 @@
 //   s = q k^T,  p = exp2(c (s - m)),  o = (sum p v) / l,  l = sum p,
 //   lse = (c m + log2 l) ln 2,  c = scale log2 e
 //
-// One CTA takes two tiles of up to 128 packed rows (token x group head) of one
-// key head and walks the keys in tiles of 128.  Scores, probabilities and
+// An item is two tiles of up to 128 packed rows (token x group head) of one key
+// head, walked over the keys in tiles of 128.  There is a block per item, the
+// longest first; a running CTA takes over blocks that have not started, so
+// that one item's start runs under the end of the one before.  Scores, probabilities and
 // outputs stay in tensor memory: S_t = Q_t K^T (128 columns each), P_t as bf16
 // over S_t's columns, from where it is the A operand of O_t += P_t V.  A warp
 // loads (TMA, a ring of 32 KB slots that holds K and V tiles in the order of
@@ -47,11 +49,22 @@ struct Cfg {
     static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
 };
 
+// An item's rows, its key tiles and where they lie.
+struct Work {
+    int q0, k0, lq, lk;                  // the sequence: first rows and lengths
+    int tok0, head, split;               // first token of the two row tiles, key head
+    int b0, b1, e[2];                    // key tiles b0 .. b1; row tile t: b0 .. e[t]
+    int any;                             // 0: there is no more work
+};
+
 struct Shared {
     uint64_t full[8], empty[8];          // ring slots
-    uint64_t q[2];                       // Q tiles landed
+    uint64_t q[2], q_read[2];            // Q tiles landed, and no longer read
     uint64_t s[2], p[2][2], o[2];        // scores ready, halves of the probabilities, product done
-    uint64_t tail, fin;
+    uint64_t work[2], work_read[2];      // items published, and read
+    uint64_t tail, asked, fin;
+    uint4 answer;
+    Work item[2];
     uint32_t tmem;
     volatile int abort;
 };
@@ -72,26 +85,9 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
         (reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     unsigned char *sQ = base, *sKV = base + 2 * C::TILE;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-
     attn::clear_status(a);
-    Item it;
-    if (!attn::item_of(a, blockIdx.x, true, it)) return;
-    const Seq seq = attn::sequence(a, it.seq);
+    if (attn::rejected(a)) return;
     const int TT = maps.tokens, R = TT * a.G;
-    const int tok0 = it.tile * 2 * TT;
-    // key tiles of the two row tiles; a tile without tokens has none
-    const int shift = seq.lk - seq.lq;
-    int blocks[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int first = tok0 + t * TT, last = min(first + TT, seq.lq);
-        const int seen = last > first ? last + shift : 0;      // keys of the last token
-        blocks[t] = seen > 0 ? (seen + kTile - 1) / kTile : 0;
-    }
-    int b0, b1;
-    attn::split_range(max(blocks[0], blocks[1]), a.splits, it.split, b0, b1);
-    const int e0 = min(blocks[0], b1), e1 = min(blocks[1], b1);   // tile t: keys b0 .. e_t
-    const int nb = b1 - b0;
 
     if (threadIdx.x == 0) {
 #pragma unroll
@@ -102,12 +98,16 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sh.q[t], 1);
+            mbar_init(&sh.q_read[t], 1);
             mbar_init(&sh.s[t], 1);
             mbar_init(&sh.p[t][0], 4);
             mbar_init(&sh.p[t][1], 4);
             mbar_init(&sh.o[t], 1);
+            mbar_init(&sh.work[t], 1);
+            mbar_init(&sh.work_read[t], 9);      // the products' lane and eight softmax warps
         }
         mbar_init(&sh.tail, 1);
+        mbar_init(&sh.asked, 1);
         mbar_init(&sh.fin, 1);
         sh.abort = 0;
         fence_mbar_init();
@@ -121,52 +121,106 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
         sh.abort = 1;
         *a.status = kDevTimeout;
     };
+    const auto wait = [&](uint64_t *bar, int phase) {
+        return mbar_wait_or_abort(bar, (uint32_t)(phase & 1), &sh.abort);
+    };
+    const auto wait_warp = [&](uint64_t *bar, int phase) {
+        return __all_sync(0xffffffffu, wait(bar, phase));
+    };
 
     // Registers of a thread: 128 x 88 + 256 x 208 = 384 x 168.
     if (warp >= 8) {
         attn::fewer_registers<88>();
         if (warp == 9) {
-            // ------------------------------------------------------------- loads
+            // ------------------------------------------- items and their loads
+            int j = 0, used[2] = {0, 0}, block = blockIdx.x;
             bool ok = true;
-            if (lane == 0 && nb > 0) {
-                const uint32_t box = (uint32_t)R * 128u;
+            for (int m = 0; ok; ++m) {
+                // publish item m (the consumers may be an item behind)
+                if (lane == 0) {
+                    Work w{};
+                    Item it;
+                    if (block >= 0 && attn::item_of(a, block, true, it)) {
+                        const Seq seq = attn::sequence(a, it.seq);
+                        const int shift = seq.lk - seq.lq;
+                        w.q0 = (int)seq.q0; w.k0 = (int)seq.k0; w.lq = seq.lq; w.lk = seq.lk;
+                        w.tok0 = it.tile * 2 * TT; w.head = it.head; w.split = it.split;
+                        int n[2];      // key tiles of a row tile; none without tokens
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if ((t ? e1 : e0) <= b0) continue;
-                    mbar_expect_tx(&sh.q[t], box * C::SLABS);
-                    for (int c = 0; c < C::SLABS; ++c)
-                        tma_load_3d(sQ + t * C::TILE + c * kSlab, &maps.q, &sh.q[t], c * 64,
-                                    it.head * a.G, (int)(seq.q0 + tok0 + t * TT));
-                }
-                int j = 0;
-                for (; j < 2 * nb; ++j) {
-                    const int slot = j % C::SLOTS, use = j / C::SLOTS;
-                    if (use > 0 &&
-                        !mbar_wait_or_abort(&sh.empty[slot], (uint32_t)((use - 1) & 1), &sh.abort)) {
-                        give_up();
-                        break;
+                        for (int t = 0; t < 2; ++t) {
+                            const int first = w.tok0 + t * TT, last = min(first + TT, seq.lq);
+                            const int seen = last > first ? last + shift : 0;
+                            n[t] = seen > 0 ? (seen + kTile - 1) / kTile : 0;
+                        }
+                        attn::split_range(max(n[0], n[1]), a.splits, it.split, w.b0, w.b1);
+                        w.e[0] = min(n[0], w.b1);
+                        w.e[1] = min(n[1], w.b1);
+                        w.any = 1;
                     }
-                    mbar_expect_tx(&sh.full[slot], C::TILE);
-                    const int row = (int)(seq.k0 + (long long)(b0 + j / 2) * kTile);
-                    for (int c = 0; c < C::SLABS; ++c)
-                        tma_load_3d(sKV + slot * C::TILE + c * kSlab, j % 2 ? &maps.v : &maps.k,
-                                    &sh.full[slot], c * 64, it.head, row);
+                    ok = m < 2 || wait(&sh.work_read[m & 1], m / 2 - 1);
+                    sh.item[m & 1] = w;
+                    mbar_arrive(&sh.work[m & 1]);
                 }
-                ok = j == 2 * nb;
-                if (!ok) {      // given up: the copies in flight land before the CTA leaves
-                    for (int i = max(0, j - C::SLOTS); i < j; ++i)
-                        (void)mbar_wait(&sh.full[i % C::SLOTS], (uint32_t)((i / C::SLOTS) & 1));
-                    for (int t = 0; t < 2; ++t)
-                        if ((t ? e1 : e0) > b0) (void)mbar_wait(&sh.q[t], 0u);
+                ok = __all_sync(0xffffffffu, ok);
+                __syncwarp();
+                const Work w = sh.item[m & 1];
+                if (!ok || !w.any) break;
+                const int nb = w.b1 - w.b0;
+                if (lane == 0 && nb > 0) {
+                    const uint32_t box = (uint32_t)R * 128u;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (w.e[t] <= w.b0) continue;
+                        ok = ok && (used[t] == 0 || wait(&sh.q_read[t], used[t] - 1));
+                        if (!ok) break;
+                        ++used[t];
+                        mbar_expect_tx(&sh.q[t], box * C::SLABS);
+                        for (int c = 0; c < C::SLABS; ++c)
+                            tma_load_3d(sQ + t * C::TILE + c * kSlab, &maps.q, &sh.q[t], c * 64,
+                                        w.head * a.G, w.q0 + w.tok0 + t * TT);
+                    }
+                    for (int i = 0; ok && i < 2 * nb; ++i) {
+                        const int slot = j % C::SLOTS, use = j / C::SLOTS;
+                        ok = use == 0 || wait(&sh.empty[slot], use - 1);
+                        if (!ok) break;
+                        ++j;
+                        mbar_expect_tx(&sh.full[slot], C::TILE);
+                        const int row = w.k0 + (w.b0 + i / 2) * kTile;
+                        for (int c = 0; c < C::SLABS; ++c)
+                            tma_load_3d(sKV + slot * C::TILE + c * kSlab, i % 2 ? &maps.v : &maps.k,
+                                        &sh.full[slot], c * 64, w.head, row);
+                    }
                 }
+                // the next block is asked for late, so that one CTA does not
+                // hold what another could start
+                const bool asked = ok;
+                if (lane == 0 && asked) {
+                    mbar_expect_tx(&sh.asked, 16);
+                    attn::ask_block(&sh.answer, &sh.asked);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                j = __shfl_sync(0xffffffffu, j, 0);
+                const int valid = w.lk - (w.b1 - 1) * kTile;
+                if (ok && nb > 0 && valid < kTile) {     // rows behind the sequence's last
+                    const int slot = (j - 1) % C::SLOTS;
+                    ok = wait_warp(&sh.full[slot], (j - 1) / C::SLOTS);
+                    if (ok) attn::zero_rows<C::SLABS>(sKV + slot * C::TILE, valid, lane);
+                    if (ok && lane == 0) mbar_arrive(&sh.tail);
+                }
+                if (lane == 0 && asked) {
+                    ok = mbar_wait(&sh.asked, (uint32_t)(m & 1)) && ok;
+                    block = attn::answered_block(&sh.answer);
+                    fence_async_smem();        // read before the next answer is written
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                block = __shfl_sync(0xffffffffu, block, 0);
             }
-            const int valid = seq.lk - (b1 - 1) * kTile;
-            if (__all_sync(0xffffffffu, ok) && nb > 0 && valid < kTile) {
-                const int j = 2 * nb - 1, slot = j % C::SLOTS;
-                if (__all_sync(0xffffffffu, mbar_wait(&sh.full[slot], (uint32_t)((j / C::SLOTS) & 1)))) {
-                    attn::zero_rows<C::SLABS>(sKV + slot * C::TILE, valid, lane);
-                    if (lane == 0) mbar_arrive(&sh.tail);
-                }
+            if (!ok && lane == 0) {    // given up: the copies in flight land before the CTA leaves
+                give_up();
+                for (int i = max(0, j - C::SLOTS); i < j; ++i)
+                    (void)mbar_wait(&sh.full[i % C::SLOTS], (uint32_t)((i / C::SLOTS) & 1));
+                for (int t = 0; t < 2; ++t)
+                    if (used[t] > 0) (void)mbar_wait(&sh.q[t], (uint32_t)((used[t] - 1) & 1));
             }
         } else if (warp == 8) {
             // ---------------------------------------------------------- products
@@ -175,217 +229,240 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
             constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true);
             const uint32_t aQ = smem_u32(sQ), aKV = smem_u32(sKV);
-            const auto wait = [&](uint64_t *bar, int phase) {
-                return mbar_wait_or_abort(bar, (uint32_t)(phase & 1), &sh.abort);
-            };
             const auto landed = [&](int j) { return wait(&sh.full[j % C::SLOTS], j / C::SLOTS); };
-            const auto scores = [&](int t, int slot) {
+            const auto scores = [&](int t, int j, bool last) {
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
                     mma_bf16(tb + C::TM_S + 128u * t, attn::kdesc(aQ + t * C::TILE, ks),
-                             attn::kdesc(aKV + slot * C::TILE, ks), id_s, ks > 0);
+                             attn::kdesc(aKV + (j % C::SLOTS) * C::TILE, ks), id_s, ks > 0);
                 mma_commit(&sh.s[t]);
+                if (last) mma_commit(&sh.q_read[t]);
             };
-            if (lane == 0 && nb > 0) {
-                bool ok = landed(0);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if ((t ? e1 : e0) <= b0) continue;
-                    ok = ok && wait(&sh.q[t], 0);
-                    if (ok) scores(t, 0);
-                }
-                if (ok) mma_commit(&sh.empty[0]);
-                // the last V tile may hold a neighbour's rows: they are zeroed first
-                const bool ragged = b1 * kTile > seq.lk;
-                for (int n = 0; ok && n < nb; ++n) {
-                    const int jv = 2 * n + 1, jk = 2 * n + 2, sv = jv % C::SLOTS;
-                    ok = landed(jv) && (n + 1 >= nb ? !ragged || wait(&sh.tail, 0) : landed(jk));
+            if (lane == 0) {
+                int j = 0, used[2] = {0, 0}, steps[2] = {0, 0}, tails = 0;
+                bool ok = true;
+                for (int m = 0; ok; ++m) {
+                    ok = wait(&sh.work[m & 1], m / 2);
+                    if (!ok) break;
+                    const Work w = sh.item[m & 1];
+                    mbar_arrive(&sh.work_read[m & 1]);
+                    if (!w.any) break;
+                    const int nb = w.b1 - w.b0;
+                    if (nb == 0) continue;
+                    ok = landed(j);
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const int e = t ? e1 : e0;
-                        if (b0 + n >= e) continue;
+                        if (w.e[t] <= w.b0) continue;
+                        ok = ok && wait(&sh.q[t], used[t]++);
+                        if (ok) scores(t, j, w.e[t] == w.b0 + 1);
+                    }
+                    if (ok) mma_commit(&sh.empty[j % C::SLOTS]);
+                    // the last V tile may hold a neighbour's rows: they are zeroed first
+                    const bool ragged = w.b1 * kTile > w.lk;
+                    for (int n = 0; ok && n < nb; ++n) {
+                        const int jv = j + 2 * n + 1, jk = j + 2 * n + 2, sv = jv % C::SLOTS;
+                        ok = landed(jv) &&
+                             (n + 1 < nb ? landed(jk) : !ragged || wait(&sh.tail, tails));
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {      // as the halves of P come
-                            ok = ok && wait(&sh.p[t][h], n);
+                        for (int t = 0; t < 2; ++t) {
+                            if (w.b0 + n >= w.e[t]) continue;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {      // as the halves of P come
+                                ok = ok && wait(&sh.p[t][h], steps[t]);
+                                if (!ok) break;
+                                tc_fence_after();
+#pragma unroll
+                                for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                                    mma_bf16_ts(tb + C::TM_O + (uint32_t)(D * t),
+                                                tb + C::TM_S + 128u * t + 8u * ks,
+                                                attn::mdesc(aKV + sv * C::TILE, ks), id_o,
+                                                n > 0 || ks > 0);
+                            }
                             if (!ok) break;
-                            tc_fence_after();
-#pragma unroll
-                            for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-                                mma_bf16_ts(tb + C::TM_O + (uint32_t)(D * t),
-                                            tb + C::TM_S + 128u * t + 8u * ks,
-                                            attn::mdesc(aKV + sv * C::TILE, ks), id_o,
-                                            n > 0 || ks > 0);
+                            ++steps[t];
+                            mma_commit(&sh.o[t]);
+                            if (w.b0 + n + 1 < w.e[t]) scores(t, jk, w.b0 + n + 2 == w.e[t]);
                         }
                         if (!ok) break;
-                        mma_commit(&sh.o[t]);
-                        if (b0 + n + 1 < e) scores(t, jk % C::SLOTS);
+                        mma_commit(&sh.empty[sv]);
+                        if (n + 1 < nb) mma_commit(&sh.empty[jk % C::SLOTS]);
                     }
-                    if (!ok) break;
-                    mma_commit(&sh.empty[sv]);
-                    if (n + 1 < nb) mma_commit(&sh.empty[jk % C::SLOTS]);
+                    j += 2 * nb;
+                    tails += ragged;
                 }
                 if (!ok) give_up();
+                // every product issued has completed before the tensor memory is released
+                mma_commit(&sh.fin);
+                (void)mbar_wait(&sh.fin, 0u);
             }
-            // every product issued has completed before the tensor memory is released
-            if (lane == 0) mma_commit(&sh.fin);
             __syncwarp();
-            (void)mbar_wait(&sh.fin, 0u);
         }
     } else {
         // ----------------------------------------------------------- softmax
         attn::more_registers<208>();
         const int t = warp / 4, w = warp % 4, r = 32 * w + lane;
-        const int e = t ? e1 : e0;
-        const int tok = tok0 + t * TT + r / a.G, head = it.head * a.G + r % a.G;
-        const bool row = r < R && tok < seq.lq;
-        const int limit = row ? tok + shift : -1;             // last key of the row
-        const int full = tok0 + t * TT + shift;               // last key that every row sees
         const uint32_t lanes = (uint32_t)(32 * w) << 16;
-        const uint32_t tS = tb + C::TM_S + 128u * t + lanes, tO = tb + C::TM_O + (uint32_t)(D * t) + lanes;
+        const uint32_t tS = tb + C::TM_S + 128u * t + lanes;
+        const uint32_t tO = tb + C::TM_O + (uint32_t)(D * t) + lanes;
+        const int tok_r = t * TT + r / a.G, head_r = r % a.G;
         const float c = a.scale_log2;
-        const bool work = __any_sync(0xffffffffu, row);       // a warp without rows only arrives
-        float m = -INFINITY, l = 0.f, mc = 0.f;               // mc = c m (0 while m is -inf)
+        int step = 0;                                         // of this row tile, over all items
         bool ok = true;
-        for (int n = b0; n < e; ++n) {
-            const int i = n - b0;
-            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&sh.s[t], (uint32_t)(i & 1), &sh.abort));
+        for (int it = 0; ok; ++it) {
+            ok = wait_warp(&sh.work[it & 1], it / 2);
             if (!ok) break;
-            tc_fence_after();
-            if (work) {
-                uint32_t x[4][32];
+            const Work k = sh.item[it & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.work_read[it & 1]);
+            if (!k.any) break;
+            const int shift = k.lk - k.lq, e = k.e[t];
+            const int tok = k.tok0 + tok_r, head = k.head * a.G + head_r;
+            const bool row = r < R && tok < k.lq;
+            const int limit = row ? tok + shift : -1;         // last key of the row
+            const int full = k.tok0 + t * TT + shift;         // last key that every row sees
+            const bool work = __any_sync(0xffffffffu, row);   // a warp without rows only arrives
+            float m = -INFINITY, l = 0.f, mc = 0.f;           // mc = c m (0 while m is -inf)
+            for (int n = k.b0; n < e; ++n, ++step) {
+                ok = wait_warp(&sh.s[t], step);
+                if (!ok) break;
+                tc_fence_after();
+                if (work) {
+                    uint32_t x[4][32];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) tmem_ld32(tS + 32u * j, x[j]);
-                tmem_ld_wait();
-                if (n * kTile + kTile - 1 > full) {
-                    const int rel = limit - n * kTile;
+                    for (int j = 0; j < 4; ++j) tmem_ld32(tS + 32u * j, x[j]);
+                    tmem_ld_wait();
+                    if (n * kTile + kTile - 1 > full) {
+                        const int rel = limit - n * kTile;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                        for (int j = 0; j < 4; ++j)
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (32 * j + k > rel) x[j][k] = 0xff800000u;      // -infinity
-                }
-                float mx[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) mx[j] = __uint_as_float(x[0][j]);
-#pragma unroll
-                for (int k = 8; k < 128; k += 16)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        mx[j] = k + 8 + j < 128
-                                    ? attn::max3(mx[j], __uint_as_float(x[(k + j) / 32][(k + j) % 32]),
-                                                 __uint_as_float(x[(k + 8 + j) / 32][(k + 8 + j) % 32]))
-                                    : fmaxf(mx[j], __uint_as_float(x[(k + j) / 32][(k + j) % 32]));
-                const float top = fmaxf(attn::max3(mx[0], mx[1], mx[2]),
-                                        attn::max3(attn::max3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
-                const bool grow = row && (top - m) * c > kGrow;
-                if (i == 0) {
-                    m = top;
-                    mc = top == -INFINITY ? 0.f : top * c;
-                } else if (__any_sync(0xffffffffu, grow)) {
-                    // O holds the products up to the last tile: they have to be complete
-                    ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&sh.o[t], (uint32_t)((i - 1) & 1),
-                                                                    &sh.abort));
-                    if (!ok) break;
-                    tc_fence_after();
-                    float f = 1.f;
-                    if (grow) {
-                        f = m == -INFINITY ? 0.f : attn::ex2((m - top) * c);
-                        m = top;
-                        mc = top * c;
+                            for (int i = 0; i < 32; ++i)
+                                if (32 * j + i > rel) x[j][i] = 0xff800000u;      // -infinity
                     }
-                    __syncwarp();
-                    l *= f;
+                    float mx[8];
 #pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        uint32_t y[16];
+                    for (int j = 0; j < 8; ++j) mx[j] = __uint_as_float(x[0][j]);
+#pragma unroll
+                    for (int i = 8; i < 128; i += 16)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int u = i + j, v = i + 8 + j;
+                            const float f = __uint_as_float(x[u / 32][u % 32]);
+                            mx[j] = v < 128
+                                        ? attn::max3(mx[j], f, __uint_as_float(x[v / 32 % 4][v % 32]))
+                                        : fmaxf(mx[j], f);
+                        }
+                    const float top = fmaxf(attn::max3(mx[0], mx[1], mx[2]),
+                                            attn::max3(attn::max3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
+                    const bool grow = row && (top - m) * c > kGrow;
+                    if (n == k.b0) {
+                        m = top;
+                        mc = top == -INFINITY ? 0.f : top * c;
+                    } else if (__any_sync(0xffffffffu, grow)) {
+                        // O holds the products up to the last tile: they have to be complete
+                        ok = wait_warp(&sh.o[t], step - 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        float f = 1.f;
+                        if (grow) {
+                            f = m == -INFINITY ? 0.f : attn::ex2((m - top) * c);
+                            m = top;
+                            mc = top * c;
+                        }
+                        __syncwarp();
+                        l *= f;
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            uint32_t y[16];
+                            tmem_ld16(tO + 16u * j, y);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+                            tmem_st16(tO + 16u * j, y);
+                        }
+                    }
+                    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t y[32];
+#pragma unroll
+                        for (int i = 0; i < 64; i += 4) {
+                            float p[4];
+#pragma unroll
+                            for (int z = 0; z < 4; ++z)
+                                p[z] = __uint_as_float(x[2 * h + (i + z) / 32][(i + z) % 32]);
+                            attn::fma2(p[0], p[1], c, -mc);
+                            attn::fma2(p[2], p[3], c, -mc);
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) p[z] = attn::ex2(p[z]);
+                            attn::add2(s0, s1, p[0], p[1]);
+                            attn::add2(s2, s3, p[2], p[3]);
+                            y[i / 2] = attn::pack2(p[0], p[1]);
+                            y[i / 2 + 1] = attn::pack2(p[2], p[3]);
+                        }
+                        attn::tmem_st32(tS + 32u * h, y);
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.p[t][h]);
+                    }
+                    l += (s0 + s1) + (s2 + s3);
+                } else if (lane == 0) {
+                    mbar_arrive(&sh.p[t][0]);
+                    mbar_arrive(&sh.p[t][1]);
+                }
+            }
+            if (ok && e > k.b0) {
+                ok = wait_warp(&sh.o[t], step - 1);
+                tc_fence_after();
+            }
+            if (!ok) break;
+            if (work) {
+                // a row that saw no key has l = 0: o = 0 and lse = -infinity
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const long long at = (long long)(k.q0 + tok) * a.Hq + head;
+                const bool parts = a.splits > 1;
+                const long long n_rows = (long long)a.total_q * a.Hq;
+                if (row) {
+                    const float lse = l == 0.f ? -INFINITY : (mc + log2f(l)) * kLn2;
+                    if (parts) a.lse_part[k.split * n_rows + at] = lse;
+                    else if (a.lse) a.lse[at] = lse;
+                }
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    uint32_t y[16];
+                    if (e > k.b0) {
                         tmem_ld16(tO + 16u * j, y);
                         tmem_ld_wait();
+                    } else {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
-                        tmem_st16(tO + 16u * j, y);
+                        for (int i = 0; i < 16; ++i) y[i] = 0;
                     }
-                }
-                float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+                    float f[16];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t y[32];
+                    for (int i = 0; i < 16; ++i) f[i] = l == 0.f ? 0.f : __uint_as_float(y[i]) * inv;
+                    if (row && parts) {
+                        float4 *dst = reinterpret_cast<float4 *>(
+                            a.o_part + (k.split * n_rows + at) * D + 16 * j);
 #pragma unroll
-                    for (int k = 0; k < 64; k += 4) {
-                        float p[4];
+                        for (int i = 0; i < 4; ++i)
+                            dst[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                    } else if (row) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(
+                            static_cast<__nv_bfloat16 *>(a.out) + at * D + 16 * j);
 #pragma unroll
-                        for (int z = 0; z < 4; ++z)
-                            p[z] = __uint_as_float(x[2 * h + (k + z) / 32][(k + z) % 32]);
-                        attn::fma2(p[0], p[1], c, -mc);
-                        attn::fma2(p[2], p[3], c, -mc);
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) p[z] = attn::ex2(p[z]);
-                        attn::add2(s0, s1, p[0], p[1]);
-                        attn::add2(s2, s3, p[2], p[3]);
-                        y[k / 2] = attn::pack2(p[0], p[1]);
-                        y[k / 2 + 1] = attn::pack2(p[2], p[3]);
+                        for (int i = 0; i < 2; ++i)
+                            dst[i] = make_uint4(attn::pack2(f[8 * i], f[8 * i + 1]),
+                                                attn::pack2(f[8 * i + 2], f[8 * i + 3]),
+                                                attn::pack2(f[8 * i + 4], f[8 * i + 5]),
+                                                attn::pack2(f[8 * i + 6], f[8 * i + 7]));
                     }
-                    attn::tmem_st32(tS + 32u * h, y);
-                    tmem_st_wait();
-                    tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.p[t][h]);
                 }
-                l += (s0 + s1) + (s2 + s3);
-            } else if (lane == 0) {
-                mbar_arrive(&sh.p[t][0]);
-                mbar_arrive(&sh.p[t][1]);
             }
         }
-        if (ok && e > b0) {
-            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&sh.o[t], (uint32_t)((e - b0 - 1) & 1),
-                                                            &sh.abort));
-            tc_fence_after();
-        }
-        if (!ok) {
-            give_up();
-        } else if (work) {
-            // a row that saw no key has l = 0: o = 0 and lse = -infinity
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const long long at = (seq.q0 + tok) * a.Hq + head;
-            const bool parts = a.splits > 1;
-            const long long n_rows = (long long)a.total_q * a.Hq;
-            if (row) {
-                const float lse = l == 0.f ? -INFINITY : (mc + log2f(l)) * kLn2;
-                if (parts) a.lse_part[it.split * n_rows + at] = lse;
-                else if (a.lse) a.lse[at] = lse;
-            }
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-                uint32_t y[16];
-                if (e > b0) {
-                    tmem_ld16(tO + 16u * j, y);
-                    tmem_ld_wait();
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) y[k] = 0;
-                }
-                float f[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) f[k] = l == 0.f ? 0.f : __uint_as_float(y[k]) * inv;
-                if (row && parts) {
-                    float4 *dst = reinterpret_cast<float4 *>(a.o_part + (it.split * n_rows + at) * D + 16 * j);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        dst[k] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
-                } else if (row) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                                           at * D + 16 * j);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        dst[k] = make_uint4(attn::pack2(f[8 * k], f[8 * k + 1]),
-                                            attn::pack2(f[8 * k + 2], f[8 * k + 3]),
-                                            attn::pack2(f[8 * k + 4], f[8 * k + 5]),
-                                            attn::pack2(f[8 * k + 6], f[8 * k + 7]));
-                }
-                __syncwarp();
-            }
-        }
+        if (!ok) give_up();
     }
     tc_fence_before();
     __syncthreads();

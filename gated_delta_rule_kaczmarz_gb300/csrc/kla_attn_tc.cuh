@@ -91,6 +91,31 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
                  : "memory");
 }
 
+// Asks for a block of this launch that has not started: the answer lands in
+// *answer (16 bytes of shared memory, 16-byte aligned) and completes 16 bytes
+// on *bar.  Not asked again once the answer was that there is none.
+__device__ __forceinline__ void ask_block(uint4 *answer, uint64_t *bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+        " [%0], [%1];" ::"r"(tc::smem_u32(answer)), "r"(tc::smem_u32(bar))
+        : "memory");
+}
+// The block of an answer, or -1.
+__device__ __forceinline__ int answered_block(const uint4 *answer) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t"
+        "mov.b32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(tc::smem_u32(answer))
+        : "memory");
+    return got ? (int)x : -1;
+}
+
 // Zeroes rows from..127 of a tile's slabs (one warp) and makes the writes
 // visible to the tensor cores: rows behind a sequence's last are a
 // neighbour's, and 0 times what they hold need not be 0.
