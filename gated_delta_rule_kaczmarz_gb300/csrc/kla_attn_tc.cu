@@ -36,7 +36,7 @@ using attn::kSlab;
 using attn::kTile;
 using attn::Seq;
 
-constexpr int kThreads = 384;            // 8 softmax warps, products, loads, two idle
+constexpr int kThreads = 384;            // 8 softmax warps, 2 of products, loads, one idle
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kGrow = 8.f;             // see above
 
@@ -62,7 +62,7 @@ struct Shared {
     uint64_t q[2], q_read[2];            // Q tiles landed, and no longer read
     uint64_t s[2], p[2][2], o[2];        // scores ready, halves of the probabilities, product done
     uint64_t work[2], work_read[2];      // items published, and read
-    uint64_t tail, asked, fin;
+    uint64_t turn[2], tail, asked, fin;
     uint4 answer;
     Work item[2];
     uint32_t tmem;
@@ -93,7 +93,7 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
 #pragma unroll
         for (int i = 0; i < C::SLOTS; ++i) {
             mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], 1);
+            mbar_init(&sh.empty[i], 2);          // both tiles' products
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -104,11 +104,12 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
             mbar_init(&sh.p[t][1], 4);
             mbar_init(&sh.o[t], 1);
             mbar_init(&sh.work[t], 1);
-            mbar_init(&sh.work_read[t], 9);      // the products' lane and eight softmax warps
+            mbar_init(&sh.work_read[t], 10);     // two lanes of products and eight softmax warps
+            mbar_init(&sh.turn[t], 1);
         }
         mbar_init(&sh.tail, 1);
         mbar_init(&sh.asked, 1);
-        mbar_init(&sh.fin, 1);
+        mbar_init(&sh.fin, 2);
         sh.abort = 0;
         fence_mbar_init();
     }
@@ -222,24 +223,29 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                 for (int t = 0; t < 2; ++t)
                     if (used[t] > 0) (void)mbar_wait(&sh.q[t], (uint32_t)((used[t] - 1) & 1));
             }
-        } else if (warp == 8) {
+        } else if (warp == 8 || warp == 10) {
             // ---------------------------------------------------------- products
-            // One lane waits and issues: a warp-wide vote after every wait
-            // costs more than the queue of products holds (about 300 cycles).
+            // A warp per row tile, one lane of which waits and issues: a wait
+            // takes about 100 cycles even where there is nothing to wait for,
+            // and the queue of issued products is shorter than the six of a
+            // step, so one tile's waits have to run under the other's issue.
+            // The tiles' batches (O += P V, then the next scores) take turns;
+            // without them both tiles' products run at the same time and
+            // their softmax too, with the tensor cores idle.
             constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true);
-            const uint32_t aQ = smem_u32(sQ), aKV = smem_u32(sKV);
+            const int t = warp == 8 ? 0 : 1;
+            const uint32_t aQ = smem_u32(sQ) + t * C::TILE, aKV = smem_u32(sKV);
+            const uint32_t tS = tb + C::TM_S + 128u * t, tO = tb + C::TM_O + (uint32_t)(D * t);
             const auto landed = [&](int j) { return wait(&sh.full[j % C::SLOTS], j / C::SLOTS); };
-            const auto scores = [&](int t, int j, bool last) {
+            const auto scores = [&](int j, int ks0, int ks1) {
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    mma_bf16(tb + C::TM_S + 128u * t, attn::kdesc(aQ + t * C::TILE, ks),
+                for (int ks = ks0; ks < ks1; ++ks)
+                    mma_bf16(tS, attn::kdesc(aQ, ks),
                              attn::kdesc(aKV + (j % C::SLOTS) * C::TILE, ks), id_s, ks > 0);
-                mma_commit(&sh.s[t]);
-                if (last) mma_commit(&sh.q_read[t]);
             };
             if (lane == 0) {
-                int j = 0, used[2] = {0, 0}, steps[2] = {0, 0}, tails = 0;
+                int j = 0, used = 0, step = 0, tails = 0, turns = 0;
                 bool ok = true;
                 for (int m = 0; ok; ++m) {
                     ok = wait(&sh.work[m & 1], m / 2);
@@ -249,43 +255,61 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                     if (!w.any) break;
                     const int nb = w.b1 - w.b0;
                     if (nb == 0) continue;
+                    const int mine = max(0, w.e[t] - w.b0), other = max(0, w.e[1 - t] - w.b0);
                     ok = landed(j);
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (w.e[t] <= w.b0) continue;
-                        ok = ok && wait(&sh.q[t], used[t]++);
-                        if (ok) scores(t, j, w.e[t] == w.b0 + 1);
+                    if (ok && mine > 0) {
+                        ok = wait(&sh.q[t], used++);
+                        if (!ok) break;
+                        scores(j, 0, D / 16);
+                        mma_commit(&sh.s[t]);
+                        if (mine == 1) mma_commit(&sh.q_read[t]);
+                        mma_commit(&sh.empty[j % C::SLOTS]);
+                    } else if (ok) {
+                        mbar_arrive(&sh.empty[j % C::SLOTS]);
                     }
-                    if (ok) mma_commit(&sh.empty[j % C::SLOTS]);
                     // the last V tile may hold a neighbour's rows: they are zeroed first
                     const bool ragged = w.b1 * kTile > w.lk;
                     for (int n = 0; ok && n < nb; ++n) {
                         const int jv = j + 2 * n + 1, jk = j + 2 * n + 2, sv = jv % C::SLOTS;
-                        ok = landed(jv) &&
-                             (n + 1 < nb ? landed(jk) : !ragged || wait(&sh.tail, tails));
+                        ok = landed(jv) && (n + 1 < nb ? landed(jk) : !ragged || wait(&sh.tail, tails));
+                        if (!ok) break;
+                        if (n >= mine) {       // the other tile's keys
+                            mbar_arrive(&sh.empty[sv]);
+                            if (n + 1 < nb) mbar_arrive(&sh.empty[jk % C::SLOTS]);
+                            continue;
+                        }
+                        ok = wait(&sh.p[t][0], step);
+                        // strictly in turn over all items, where both tiles have a batch
+                        const bool both = n < other;
+                        if (both && (t == 1 || turns > 0))
+                            ok = ok && wait(&sh.turn[t], t == 1 ? turns : turns - 1);
+                        turns += both;
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (w.b0 + n >= w.e[t]) continue;
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {      // as the halves of P come
-                                ok = ok && wait(&sh.p[t][h], steps[t]);
-                                if (!ok) break;
-                                tc_fence_after();
-#pragma unroll
-                                for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-                                    mma_bf16_ts(tb + C::TM_O + (uint32_t)(D * t),
-                                                tb + C::TM_S + 128u * t + 8u * ks,
-                                                attn::mdesc(aKV + sv * C::TILE, ks), id_o,
-                                                n > 0 || ks > 0);
-                            }
+                        for (int h = 0; h < 2; ++h) {      // as the halves of P come
+                            if (h == 1) ok = ok && wait(&sh.p[t][1], step);
                             if (!ok) break;
-                            ++steps[t];
-                            mma_commit(&sh.o[t]);
-                            if (w.b0 + n + 1 < w.e[t]) scores(t, jk, w.b0 + n + 2 == w.e[t]);
+                            tc_fence_after();
+#pragma unroll
+                            for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                                mma_bf16_ts(tO, tS + 8u * ks, attn::mdesc(aKV + sv * C::TILE, ks),
+                                            id_o, n > 0 || ks > 0);
                         }
                         if (!ok) break;
+                        ++step;
+                        mma_commit(&sh.o[t]);
                         mma_commit(&sh.empty[sv]);
-                        if (n + 1 < nb) mma_commit(&sh.empty[jk % C::SLOTS]);
+                        // the turn passes on while the queue still holds products
+                        if (n + 1 < mine) {
+                            scores(jk, 0, D / 32);
+                            if (both) mbar_arrive(&sh.turn[1 - t]);
+                            scores(jk, D / 32, D / 16);
+                            mma_commit(&sh.s[t]);
+                            if (n + 2 == mine) mma_commit(&sh.q_read[t]);
+                            mma_commit(&sh.empty[jk % C::SLOTS]);
+                        } else {
+                            if (both) mbar_arrive(&sh.turn[1 - t]);
+                            if (n + 1 < nb) mbar_arrive(&sh.empty[jk % C::SLOTS]);
+                        }
                     }
                     j += 2 * nb;
                     tails += ragged;
