@@ -54,7 +54,7 @@ struct Shared {
     uint64_t full[5], empty[5];          // ring slots
     uint64_t s[2], dp, p, ds;            // products ready; operands ready
     uint64_t st[2], read[2];             // row statistics ready, and read
-    uint64_t fin;
+    uint64_t tail[2], fin;
     uint32_t tmem;
     volatile int abort;
 };
@@ -76,10 +76,6 @@ __device__ __forceinline__ Blocks blocks_of(int i) {
         case 2: return {128, 192, 0, 64, 192, 0};
         default: return {64, 128, 0, 192, 128, 192};
     }
-}
-
-__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, const volatile int *abort) {
-    return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity & 1u, abort));
 }
 
 __device__ __forceinline__ void mul2(float &x0, float &x1, float y0, float y1) {
@@ -146,8 +142,12 @@ struct Cta {
         sh.abort = 1;
         *a.status = kDevTimeout;
     }
+    // One lane's wait, and a warp's.
     __device__ bool wait(uint64_t *bar, int phase) {
-        return wait_all(bar, (uint32_t)phase, &sh.abort);
+        return mbar_wait_or_abort(bar, (uint32_t)phase & 1u, &sh.abort);
+    }
+    __device__ bool wait_warp(uint64_t *bar, int phase) {
+        return __all_sync(0xffffffffu, wait(bar, phase));
     }
     __device__ void load(int tile, const CUtensorMap *m, uint64_t *bar, int y, int z) {
         for (int c = 0; c < C::SLABS; ++c)
@@ -166,6 +166,7 @@ struct Cta {
         float *stats = reinterpret_cast<float *>(base + 6 * C::TILE);   // [2][2][128]
         constexpr uint32_t TM_V = 256, TM_K = 256 + D;
         if (n > 0 && warp == 9) {
+            bool ok = true;
             if (lane == 0) {
                 mbar_expect_tx(&sh.fix, 2 * C::TILE);
                 load(0, &maps.k, &sh.fix, it.head, (int)(seq.k0 + j0));
@@ -182,59 +183,60 @@ struct Cta {
                     load(2 + slot, j % 2 ? &maps.go : &maps.q, &sh.full[slot], it.head * a.G,
                          (int)(seq.q0 + (long long)(first + j / 2) * TT));
                 }
-                if (j < 2 * n) {
+                ok = j == 2 * n;
+                if (!ok) {
                     for (int i = max(0, j - 4); i < j; ++i)
                         (void)mbar_wait(&sh.full[i % 4], (uint32_t)((i / 4) & 1));
                     (void)mbar_wait(&sh.fix, 0u);
                 }
             }
+            const int valid = (seq.lq - (last - 1) * TT) * a.G;
+            if (__all_sync(0xffffffffu, ok) && valid < R)
+                for (int j = 2 * n - 2; j < 2 * n; ++j) {
+                    (void)mbar_wait(&sh.full[j % 4], (uint32_t)((j / 4) & 1));
+                    attn::zero_rows<C::SLABS>(base + (2 + j % 4) * C::TILE, valid, lane);
+                    if (lane == 0) mbar_arrive(&sh.tail[j & 1]);
+                }
         } else if (n > 0 && warp == 8) {
             constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t id_h = idesc_bf16_f32(128, 64, false, false);
             constexpr uint32_t id_g = idesc_bf16_f32(128, D, false, true);
             // D (two halves of 64 columns) = tile A x rows of the slot
             const auto product = [&](int A, int slot, uint32_t c0, uint32_t c1, uint64_t *bar) {
-                if (lane == 0) {
-                    const uint32_t x = addr(A), y = addr(2 + slot);
-                    if (c1 == c0 + 64) {
+                const uint32_t x = addr(A), y = addr(2 + slot);
+                if (c1 == c0 + 64) {
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks)
-                            mma_bf16(tb + c0, attn::kdesc(x, ks), attn::kdesc(y, ks), id_s, ks > 0);
-                    } else {
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_bf16(tb + c0, attn::kdesc(x, ks), attn::kdesc(y, ks), id_s, ks > 0);
+                } else {
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks)
-                            mma_bf16(tb + c0, attn::kdesc(x, ks), attn::kdesc(y, ks), id_h, ks > 0);
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_bf16(tb + c0, attn::kdesc(x, ks), attn::kdesc(y, ks), id_h, ks > 0);
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks)     // rows 64 .. 127 of each slab
-                            mma_bf16(tb + c1, attn::kdesc(x, ks), attn::kdesc(y + 8192, ks), id_h,
-                                     ks > 0);
-                    }
-                    mma_commit(bar);
+                    for (int ks = 0; ks < D / 16; ++ks)         // rows 64 .. 127 of each slab
+                        mma_bf16(tb + c1, attn::kdesc(x, ks), attn::kdesc(y + 8192, ks), id_h,
+                                 ks > 0);
                 }
-                __syncwarp();
+                mma_commit(bar);
             };
             const auto gather = [&](uint32_t out, uint32_t block, int slot, bool acc) {
-                if (lane == 0) {
-                    const uint32_t y = addr(2 + slot);
+                const uint32_t y = addr(2 + slot);
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_bf16_ts(tb + out, tb + block + 8u * ks, attn::mdesc(y, ks), id_g,
-                                    acc || ks > 0);
-                    mma_commit(&sh.empty[slot]);
-                }
-                __syncwarp();
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_bf16_ts(tb + out, tb + block + 8u * ks, attn::mdesc(y, ks), id_g,
+                                acc || ks > 0);
+                mma_commit(&sh.empty[slot]);
             };
-            // the last row tile may end inside: what follows is a neighbour's
+            // the last row tile may end inside: the loads' warp zeroes what
+            // follows, which is a neighbour's
+            const bool ragged = last * TT > seq.lq;
             const auto landed = [&](int j) {
-                if (!wait(&sh.full[j % 4], j / 4)) return false;
-                const int valid = (seq.lq - (first + j / 2) * TT) * a.G;
-                if (valid < R)
-                    attn::zero_rows<C::SLABS>(base + (2 + j % 4) * C::TILE, valid, lane);
-                return true;
+                return wait(&sh.full[j % 4], j / 4) &&
+                       (!ragged || j < 2 * n - 2 || wait(&sh.tail[j & 1], 0));
             };
+            if (lane == 0) {
             bool ok = wait(&sh.fix, 0) && landed(0);
             if (ok) {
-                tc_fence_after();
                 const Blocks b = blocks_of(0);
                 product(0, 0, b.s0, b.s1, &sh.s[0]);
                 ok = landed(1);
@@ -264,14 +266,15 @@ struct Cta {
                 }
             }
             if (!ok) give_up();
-            if (lane == 0) mma_commit(&sh.fin);
-            __syncwarp();
+            mma_commit(&sh.fin);
             (void)mbar_wait(&sh.fin, 0u);
+            }
+            __syncwarp();
         } else if (n > 0 && warp == 10) {
             // -lse log2 e and -delta of the tile's rows; a row that is none, or
             // saw no key, gets p = exp2(-inf) = 0
             for (int i = 0; i < n; ++i) {
-                if (i >= 2 && !wait(&sh.read[i & 1], i / 2 - 1)) break;
+                if (i >= 2 && !wait_warp(&sh.read[i & 1], i / 2 - 1)) break;
                 float *dst = stats + (i & 1) * 256;
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
@@ -298,7 +301,7 @@ struct Cta {
                 const Blocks b = blocks_of(i);
                 float p[64];
                 const float *st = stats + (i & 1) * 256 + 64 * half;
-                ok = ok && wait(&sh.st[i & 1], i / 2) && wait(&sh.s[0], i);
+                ok = ok && wait_warp(&sh.st[i & 1], i / 2) && wait_warp(&sh.s[0], i);
                 if (ok) {
                     tc_fence_after();
                     uint32_t x[2][32];
@@ -339,7 +342,7 @@ struct Cta {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.p);
-                    ok = wait(&sh.dp, i);
+                    ok = wait_warp(&sh.dp, i);
                 }
                 if (ok) {
                     tc_fence_after();
@@ -377,7 +380,7 @@ struct Cta {
                     }
                 }
             }
-            if (n > 0) ok = ok && wait(&sh.fin, 0);
+            if (n > 0) ok = ok && wait_warp(&sh.fin, 0);
             if (!ok) {
                 give_up();
             } else {
@@ -400,12 +403,12 @@ struct Cta {
         const int n = seen > 0 ? (seen + kTile - 1) / kTile : 0;
         constexpr uint32_t TM_P = 256, TM_Q = 384;
         if (n > 0 && warp == 9) {
+            bool ok = true;
             if (lane == 0) {
                 const uint32_t box = (uint32_t)R * 128u * C::SLABS;
                 mbar_expect_tx(&sh.fix, 2 * box);
                 load(0, &maps.q, &sh.fix, it.head * a.G, (int)(seq.q0 + tok0));
                 load(1, &maps.go, &sh.fix, it.head * a.G, (int)(seq.q0 + tok0));
-                bool ok = true;
                 int nk = 0, nv = 0;           // tiles asked for
                 const auto next = [&](bool value, int i) {
                     const int slot = value ? 3 + i % 2 : i % 3, use = value ? i / 2 : i / 3;
@@ -433,57 +436,58 @@ struct Cta {
                     (void)mbar_wait(&sh.fix, 0u);
                 }
             }
+            const int valid = seq.lk - (n - 1) * kTile;
+            if (__all_sync(0xffffffffu, ok) && valid < kTile) {
+                const int slot = (n - 1) % 3;
+                (void)mbar_wait(&sh.full[slot], (uint32_t)(((n - 1) / 3) & 1));
+                attn::zero_rows<C::SLABS>(base + (2 + slot) * C::TILE, valid, lane);
+                if (lane == 0) mbar_arrive(&sh.tail[0]);
+            }
         } else if (n > 0 && warp == 8) {
             constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t id_g = idesc_bf16_f32(128, D, false, true);
             const auto product = [&](int A, int tile, uint32_t out, uint64_t *bar) {
-                if (lane == 0) {
-                    const uint32_t x = addr(A), y = addr(tile);
+                const uint32_t x = addr(A), y = addr(tile);
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        mma_bf16(tb + out, attn::kdesc(x, ks), attn::kdesc(y, ks), id_s, ks > 0);
-                    mma_commit(bar);
-                }
-                __syncwarp();
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_bf16(tb + out, attn::kdesc(x, ks), attn::kdesc(y, ks), id_s, ks > 0);
+                mma_commit(bar);
             };
+            // the keys' rows are summed over in dQ: those behind the last are a
+            // neighbour's, and the loads' warp zeroes them
+            const bool ragged = n * kTile > seq.lk;
             const auto scores = [&](int i) {
                 if (!wait(&sh.full[i % 3], i / 3)) return false;
-                // the keys' rows are summed over in dQ: those behind the last are a neighbour's
-                const int valid = seq.lk - i * kTile;
-                if (valid < kTile)
-                    attn::zero_rows<C::SLABS>(base + (2 + i % 3) * C::TILE, valid, lane);
-                tc_fence_after();
+                if (ragged && i == n - 1 && !wait(&sh.tail[0], 0)) return false;
                 product(0, 2 + i % 3, 128u * (i & 1), &sh.s[i & 1]);
                 return true;
             };
             const auto grads = [&](int i) {
                 if (!wait(&sh.full[3 + i % 2], i / 2)) return false;
-                tc_fence_after();
                 product(1, 5 + i % 2, TM_P, &sh.dp);
-                if (lane == 0) mma_commit(&sh.empty[3 + i % 2]);
-                __syncwarp();
+                mma_commit(&sh.empty[3 + i % 2]);
                 return true;
             };
+            if (lane == 0) {
             bool ok = wait(&sh.fix, 0) && scores(0) && grads(0) && (n < 2 || scores(1));
             for (int i = 0; ok && i < n; ++i) {
-                ok = wait(&sh.ds, i) && (i + 1 >= n || grads(i + 1));
-                if (!ok) break;
+                ok = wait(&sh.ds, i);
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t y = addr(2 + i % 3);
+                ok = ok && (i + 1 >= n || grads(i + 1));
+                if (!ok) break;
+                const uint32_t y = addr(2 + i % 3);
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)      // dS: 32 columns in each half of S's
-                        mma_bf16_ts(tb + TM_Q, tb + 128u * (i & 1) + 64u * (ks / 4) + 8u * (ks % 4),
-                                    attn::mdesc(y, ks), id_g, i > 0 || ks > 0);
-                    mma_commit(&sh.empty[i % 3]);
-                }
-                __syncwarp();
+                for (int ks = 0; ks < 8; ++ks)          // dS: 32 columns in each half of S's
+                    mma_bf16_ts(tb + TM_Q, tb + 128u * (i & 1) + 64u * (ks / 4) + 8u * (ks % 4),
+                                attn::mdesc(y, ks), id_g, i > 0 || ks > 0);
+                mma_commit(&sh.empty[i % 3]);
                 if (i + 2 < n) ok = scores(i + 2);
             }
             if (!ok) give_up();
-            if (lane == 0) mma_commit(&sh.fin);
-            __syncwarp();
+            mma_commit(&sh.fin);
             (void)mbar_wait(&sh.fin, 0u);
+            }
+            __syncwarp();
         } else if (warp < 8) {
             const int half = warp / 4, w = warp % 4, r = 32 * w + lane;
             const int tok = tok0 + r / a.G;
@@ -500,7 +504,7 @@ struct Cta {
             }
             bool ok = true;
             for (int i = 0; ok && i < n; ++i) {
-                ok = wait(&sh.s[i & 1], i / 2);
+                ok = wait_warp(&sh.s[i & 1], i / 2);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t tS = tb + 128u * (i & 1) + 64u * half + lanes;
@@ -519,7 +523,7 @@ struct Cta {
                         p[k + 1] = attn::ex2(p[k + 1]);
                     }
                 }
-                ok = wait(&sh.dp, i);
+                ok = wait_warp(&sh.dp, i);
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t x[2][32];
@@ -549,7 +553,7 @@ struct Cta {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.ds);
             }
-            if (n > 0) ok = ok && wait(&sh.fin, 0);
+            if (n > 0) ok = ok && wait_warp(&sh.fin, 0);
             if (!ok) {
                 give_up();
             } else {
@@ -589,6 +593,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Args ak, const __grid_constant__ Args
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s[i], 1);
+            mbar_init(&sh.tail[i], 1);
             mbar_init(&sh.st[i], 1);
             mbar_init(&sh.read[i], 8);
         }

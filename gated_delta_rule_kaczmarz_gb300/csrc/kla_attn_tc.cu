@@ -60,7 +60,7 @@ struct Work {
 struct Shared {
     uint64_t full[8], empty[8];          // ring slots
     uint64_t q[2], q_read[2];            // Q tiles landed, and no longer read
-    uint64_t s[2], p[2][2], o[2];        // scores ready, halves of the probabilities, product done
+    uint64_t s[2], p[2], o[2];           // scores ready, probabilities ready, product done
     uint64_t work[2], work_read[2];      // items published, and read
     uint64_t turn[2], tail, asked, fin;
     uint4 answer;
@@ -100,8 +100,7 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
             mbar_init(&sh.q[t], 1);
             mbar_init(&sh.q_read[t], 1);
             mbar_init(&sh.s[t], 1);
-            mbar_init(&sh.p[t][0], 4);
-            mbar_init(&sh.p[t][1], 4);
+            mbar_init(&sh.p[t], 4);
             mbar_init(&sh.o[t], 1);
             mbar_init(&sh.work[t], 1);
             mbar_init(&sh.work_read[t], 10);     // two lanes of products and eight softmax warps
@@ -278,23 +277,18 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                             if (n + 1 < nb) mbar_arrive(&sh.empty[jk % C::SLOTS]);
                             continue;
                         }
-                        ok = wait(&sh.p[t][0], step);
                         // strictly in turn over all items, where both tiles have a batch
                         const bool both = n < other;
                         if (both && (t == 1 || turns > 0))
                             ok = ok && wait(&sh.turn[t], t == 1 ? turns : turns - 1);
                         turns += both;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {      // as the halves of P come
-                            if (h == 1) ok = ok && wait(&sh.p[t][1], step);
-                            if (!ok) break;
-                            tc_fence_after();
-#pragma unroll
-                            for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-                                mma_bf16_ts(tO, tS + 8u * ks, attn::mdesc(aKV + sv * C::TILE, ks),
-                                            id_o, n > 0 || ks > 0);
-                        }
+                        ok = ok && wait(&sh.p[t], step);
                         if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_bf16_ts(tO, tS + 8u * ks, attn::mdesc(aKV + sv * C::TILE, ks),
+                                        id_o, n > 0 || ks > 0);
                         ++step;
                         mma_commit(&sh.o[t]);
                         mma_commit(&sh.empty[sv]);
@@ -426,16 +420,13 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                             y[i / 2 + 1] = attn::pack2(p[2], p[3]);
                         }
                         attn::tmem_st32(tS + 32u * h, y);
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.p[t][h]);
                     }
                     l += (s0 + s1) + (s2 + s3);
-                } else if (lane == 0) {
-                    mbar_arrive(&sh.p[t][0]);
-                    mbar_arrive(&sh.p[t][1]);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
                 }
+                if (lane == 0) mbar_arrive(&sh.p[t]);
             }
             if (ok && e > k.b0) {
                 ok = wait_warp(&sh.o[t], step - 1);
