@@ -19,10 +19,9 @@
 // issues the products, the loads (TMA) and, for key tiles, the rows' lse and
 // delta.  p and ds are rounded to bf16 as operands; sums are fp32.
 //
-// Tensor memory, key tiles: four blocks of 64 columns hold S^T and dP^T (two
-// each) while P^T and dS^T of the same tile take one block of each once they
-// are read; the two blocks left take the next S^T.  By this the product dV
-// runs under the dS step and dK, dP^T of the next under the exponentials:
+// Order of a key tile's products (one thread issues them, so they run in this
+// order): dV runs under the dS step, dK and the next dP^T under the
+// exponentials.  P^T takes the columns of S^T, dS^T those of dP^T:
 //
 //     S' (next)   dK   dP'   dV'
 //     [ds done]        [exp: P']   [ds']
@@ -39,7 +38,6 @@ using attn::kTile;
 using attn::Seq;
 
 constexpr int kThreads = 384;            // 8 softmax warps, products, loads, row statistics
-constexpr int kSoftmax = 256;
 
 template <int D>
 struct Cfg {
@@ -63,20 +61,6 @@ struct Maps {
     CUtensorMap q, go, k, v;
     int tokens;                          // of a row tile
 };
-
-// Blocks of 64 columns of iteration i of a key tile: S^T's halves, dP^T's
-// halves, and the block of each that P^T and dS^T take.
-struct Blocks {
-    uint32_t s0, s1, d0, d1, p, ds;
-};
-__device__ __forceinline__ Blocks blocks_of(int i) {
-    switch (i & 3) {
-        case 0: return {0, 64, 128, 192, 0, 192};
-        case 1: return {64, 128, 0, 192, 64, 0};
-        case 2: return {128, 192, 0, 64, 192, 0};
-        default: return {64, 128, 0, 192, 128, 192};
-    }
-}
 
 __device__ __forceinline__ void mul2(float &x0, float &x1, float y0, float y1) {
     asm("{\n\t.reg .b64 x, y;\n\t"
@@ -137,7 +121,35 @@ struct Cta {
     int warp, lane;
     Item it;
     Seq seq;
+    int TT, R, shift;         // tokens and rows of a row tile; lk - lq
+    int j0, tok0;             // key tile: its first key; row tile: its first token
+    int first, last, n;       // tiles of the other side: first .. last, how many
+    float *stats;             // key tiles: [2][-lse log2 e, -delta][128]
 
+    // Tensor memory of a key tile: S^T, dP^T, dV, dK; of a row tile: S twice, dP, dQ.
+    static constexpr uint32_t TM_S = 0, TM_P = 128, TM_V = 256, TM_K = 256 + D;
+    static constexpr uint32_t TM_DP = 256, TM_Q = 384;
+
+    __device__ Cta(const Args &a_, const Maps &maps_, Shared &sh_, unsigned char *base_, int warp_,
+                   int lane_, const Item &it_, const Seq &seq_, bool key_tile)
+        : a(a_), maps(maps_), sh(sh_), base(base_), tb(sh_.tmem), warp(warp_), lane(lane_),
+          it(it_), seq(seq_) {
+        TT = maps.tokens;
+        R = TT * a.G;
+        shift = seq.lk - seq.lq;
+        j0 = it.tile * kTile;
+        tok0 = it.tile * TT;
+        stats = reinterpret_cast<float *>(base + 6 * C::TILE);
+        first = 0;
+        if (key_tile) {
+            first = max(0, j0 - shift) / TT;
+            last = (seq.lq + TT - 1) / TT;
+        } else {
+            const int seen = min(tok0 + TT, seq.lq) + shift;
+            last = seen > 0 ? (seen + kTile - 1) / kTile : 0;
+        }
+        n = max(0, last - first);
+    }
     __device__ void give_up() {
         sh.abort = 1;
         *a.status = kDevTimeout;
@@ -153,19 +165,20 @@ struct Cta {
         for (int c = 0; c < C::SLABS; ++c)
             tma_load_3d(base + tile * C::TILE + c * kSlab, m, bar, c * 64, y, z);
     }
+    // K step ks of an operand in the columns of the product it came from, 32
+    // columns in each half (a warpgroup's own).
+    static __device__ uint32_t operand(uint32_t col, int ks) {
+        return col + 64u * (ks / 4) + 8u * (ks % 4);
+    }
     __device__ uint32_t addr(int tile) { return smem_u32(base + tile * C::TILE); }
 
     // ------------------------------------------------------------- key tile
     // Tiles: 0 K, 1 V; ring slots 2 + i: Q_0 dO_0 Q_1 dO_1 ..; statistics in
     // the seventh.
-    __device__ void keys() {
-        const int j0 = it.tile * kTile, TT = maps.tokens, R = TT * a.G;
-        const int shift = seq.lk - seq.lq;
-        const int first = max(0, j0 - shift) / TT, last = (seq.lq + TT - 1) / TT;
-        const int n = max(0, last - first);
-        float *stats = reinterpret_cast<float *>(base + 6 * C::TILE);   // [2][2][128]
-        constexpr uint32_t TM_V = 256, TM_K = 256 + D;
-        if (n > 0 && warp == 9) {
+    // Loads, products and statistics (warps 8 to 10).
+    __device__ void keys_work() {
+        if (n == 0) return;
+        if (warp == 9) {
             bool ok = true;
             if (lane == 0) {
                 mbar_expect_tx(&sh.fix, 2 * C::TILE);
@@ -197,80 +210,63 @@ struct Cta {
                     attn::zero_rows<C::SLABS>(base + (2 + j % 4) * C::TILE, valid, lane);
                     if (lane == 0) mbar_arrive(&sh.tail[j & 1]);
                 }
-        } else if (n > 0 && warp == 8) {
-            constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
-            constexpr uint32_t id_h = idesc_bf16_f32(128, 64, false, false);
-            constexpr uint32_t id_g = idesc_bf16_f32(128, D, false, true);
-            // D (two halves of 64 columns) = tile A x rows of the slot
-            const auto product = [&](int A, int slot, uint32_t c0, uint32_t c1, uint64_t *bar) {
-                const uint32_t x = addr(A), y = addr(2 + slot);
-                if (c1 == c0 + 64) {
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        mma_bf16(tb + c0, attn::kdesc(x, ks), attn::kdesc(y, ks), id_s, ks > 0);
-                } else {
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        mma_bf16(tb + c0, attn::kdesc(x, ks), attn::kdesc(y, ks), id_h, ks > 0);
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)         // rows 64 .. 127 of each slab
-                        mma_bf16(tb + c1, attn::kdesc(x, ks), attn::kdesc(y + 8192, ks), id_h,
-                                 ks > 0);
-                }
-                mma_commit(bar);
-            };
-            const auto gather = [&](uint32_t out, uint32_t block, int slot, bool acc) {
-                const uint32_t y = addr(2 + slot);
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    mma_bf16_ts(tb + out, tb + block + 8u * ks, attn::mdesc(y, ks), id_g,
-                                acc || ks > 0);
-                mma_commit(&sh.empty[slot]);
-            };
-            // the last row tile may end inside: the loads' warp zeroes what
-            // follows, which is a neighbour's
-            const bool ragged = last * TT > seq.lq;
-            const auto landed = [&](int j) {
-                return wait(&sh.full[j % 4], j / 4) &&
-                       (!ragged || j < 2 * n - 2 || wait(&sh.tail[j & 1], 0));
-            };
+        } else if (warp == 8) {
             if (lane == 0) {
-            bool ok = wait(&sh.fix, 0) && landed(0);
-            if (ok) {
-                const Blocks b = blocks_of(0);
-                product(0, 0, b.s0, b.s1, &sh.s[0]);
-                ok = landed(1);
-                if (ok) product(1, 1, b.d0, b.d1, &sh.dp);
+                constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
+                constexpr uint32_t id_g = idesc_bf16_f32(128, D, false, true);
+                // tile A (K or V) x the rows of a slot
+                const auto product = [&](int A, int j, uint32_t out, uint64_t *bar) {
+                    const uint32_t x = addr(A), y = addr(2 + j % 4);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_bf16(tb + out, attn::kdesc(x, ks), attn::kdesc(y, ks), id_s, ks > 0);
+                    mma_commit(bar);
+                };
+                // P^T or dS^T x the rows of a slot
+                const auto gather = [&](uint32_t from, int j, uint32_t out, bool acc) {
+                    const uint32_t y = addr(2 + j % 4);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_bf16_ts(tb + out, tb + operand(from, ks), attn::mdesc(y, ks), id_g,
+                                    acc || ks > 0);
+                    mma_commit(&sh.empty[j % 4]);
+                };
+                // the last row tile may end inside: the loads' warp zeroes what
+                // follows, which is a neighbour's
+                const bool ragged = last * TT > seq.lq;
+                const auto landed = [&](int j) {
+                    return wait(&sh.full[j % 4], j / 4) &&
+                           (!ragged || j < 2 * n - 2 || wait(&sh.tail[j & 1], 0));
+                };
+                bool ok = wait(&sh.fix, 0) && landed(0);
+                if (ok) product(0, 0, TM_S, &sh.s[0]);
+                ok = ok && landed(1);
+                if (ok) product(1, 1, TM_P, &sh.dp);
                 ok = ok && wait(&sh.p, 0);
-                if (ok) {
-                    tc_fence_after();
-                    gather(TM_V, b.p, 1, false);
-                }
-            }
-            for (int i = 0; ok && i < n; ++i) {
-                const Blocks b = blocks_of(i), c = blocks_of(i + 1);
-                const bool more = i + 1 < n;
-                ok = wait(&sh.ds, i) && (!more || landed(2 * i + 2));
-                if (!ok) break;
                 tc_fence_after();
-                if (more) product(0, (2 * i + 2) % 4, c.s0, c.s1, &sh.s[0]);
-                gather(TM_K, b.ds, (2 * i) % 4, i > 0);
-                if (more) {
+                if (ok) gather(TM_S, 1, TM_V, false);
+                for (int i = 0; ok && i < n; ++i) {
+                    const bool more = i + 1 < n;
+                    ok = (!more || landed(2 * i + 2)) && wait(&sh.ds, i);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (more) product(0, 2 * i + 2, TM_S, &sh.s[0]);
+                    gather(TM_P, 2 * i, TM_K, i > 0);
+                    if (!more) break;
                     ok = landed(2 * i + 3);
                     if (!ok) break;
-                    product(1, (2 * i + 3) % 4, c.d0, c.d1, &sh.dp);
+                    product(1, 2 * i + 3, TM_P, &sh.dp);
                     ok = wait(&sh.p, i + 1);
                     if (!ok) break;
                     tc_fence_after();
-                    gather(TM_V, c.p, (2 * i + 3) % 4, true);
+                    gather(TM_S, 2 * i + 3, TM_V, true);
                 }
-            }
-            if (!ok) give_up();
-            mma_commit(&sh.fin);
-            (void)mbar_wait(&sh.fin, 0u);
+                if (!ok) give_up();
+                mma_commit(&sh.fin);
+                (void)mbar_wait(&sh.fin, 0u);
             }
             __syncwarp();
-        } else if (n > 0 && warp == 10) {
+        } else if (warp == 10) {
             // -lse log2 e and -delta of the tile's rows; a row that is none, or
             // saw no key, gets p = exp2(-inf) = 0
             for (int i = 0; i < n; ++i) {
@@ -292,92 +288,93 @@ struct Cta {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.st[i & 1]);
             }
-        } else if (warp < 8) {
+        }
+    }
+    __device__ void keys_softmax() {
+        {
             const int half = warp / 4, w = warp % 4, key = j0 + 32 * w + lane;
-            const uint32_t lanes = (uint32_t)(32 * w) << 16;
+            const uint32_t at_s = tb + TM_S + 64u * half + ((uint32_t)(32 * w) << 16);
+            const uint32_t at_p = at_s + (TM_P - TM_S);
             const float c = a.scale_log2;
             bool ok = true;
-            for (int i = 0; i < n; ++i) {
-                const Blocks b = blocks_of(i);
+            for (int i = 0; ok && i < n; ++i) {
+                // the rows' statistics into registers ahead of the waits: the
+                // products hold shared memory busy, and a read takes its time
+                const float4 *st = reinterpret_cast<const float4 *>(stats + (i & 1) * 256 + 64 * half);
+                ok = wait_warp(&sh.st[i & 1], i / 2);
+                if (!ok) break;
                 float p[64];
-                const float *st = stats + (i & 1) * 256 + 64 * half;
-                ok = ok && wait_warp(&sh.st[i & 1], i / 2) && wait_warp(&sh.s[0], i);
-                if (ok) {
+                {
+                    float4 nl[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) nl[k] = st[k];
+                    ok = wait_warp(&sh.s[0], i);
+                    if (!ok) break;
                     tc_fence_after();
                     uint32_t x[2][32];
-                    const uint32_t tS = tb + (half ? b.s1 : b.s0) + lanes;
-                    tmem_ld32(tS, x[0]);
-                    tmem_ld32(tS + 32, x[1]);
+                    tmem_ld32(at_s, x[0]);
+                    tmem_ld32(at_s + 32, x[1]);
                     tmem_ld_wait();
 #pragma unroll
                     for (int k = 0; k < 64; k += 4) {
-                        const float4 nl = *reinterpret_cast<const float4 *>(st + k);
 #pragma unroll
                         for (int z = 0; z < 4; ++z)
                             p[k + z] = __uint_as_float(x[k / 32][k % 32 + z]);
-                        fma2v(p[k], p[k + 1], c, nl.x, nl.y);
-                        fma2v(p[k + 2], p[k + 3], c, nl.z, nl.w);
+                        fma2v(p[k], p[k + 1], c, nl[k / 4].x, nl[k / 4].y);
+                        fma2v(p[k + 2], p[k + 3], c, nl[k / 4].z, nl[k / 4].w);
 #pragma unroll
                         for (int z = 0; z < 4; ++z) p[k + z] = attn::ex2(p[k + z]);
                     }
-                    const int tok0 = (first + i) * TT;
-                    if (tok0 + shift < j0 + kTile - 1) {
-                        // the rows are in the order of their tokens: those from
-                        // `from` on see this key
-                        const int from = min(max(key - shift - tok0, 0), TT) * a.G - 64 * half;
-#pragma unroll
-                        for (int k = 0; k < 64; ++k)
-                            if (k < from) p[k] = 0.f;
-                    }
                 }
-                tc_fence_before();
-                named_sync(1, kSoftmax);      // both halves of S^T are read
-                if (ok) {
-                    tc_fence_after();
+                const int t0 = (first + i) * TT;
+                if (t0 + shift < j0 + kTile - 1) {
+                    // the rows are in the order of their tokens: those from
+                    // `from` on see this key
+                    const int from = min(max(key - shift - t0, 0), TT) * a.G - 64 * half;
+#pragma unroll
+                    for (int k = 0; k < 64; ++k)
+                        if (k < from) p[k] = 0.f;
+                }
+                {
                     uint32_t y[32];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) y[k] = attn::pack2(p[2 * k], p[2 * k + 1]);
-                    attn::tmem_st32(tb + b.p + 32u * half + lanes, y);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.p);
-                    ok = wait_warp(&sh.dp, i);
+                    attn::tmem_st32(at_s, y);
                 }
-                if (ok) {
-                    tc_fence_after();
-                    uint32_t x[2][32];
-                    const uint32_t tD = tb + (half ? b.d1 : b.d0) + lanes;
-                    tmem_ld32(tD, x[0]);
-                    tmem_ld32(tD + 32, x[1]);
-                    tmem_ld_wait();
+                float4 nd[16];
 #pragma unroll
-                    for (int k = 0; k < 64; k += 4) {
-                        const float4 nd = *reinterpret_cast<const float4 *>(st + 128 + k);
-                        float d[4];
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) d[z] = __uint_as_float(x[k / 32][k % 32 + z]);
-                        attn::add2(d[0], d[1], nd.x, nd.y);
-                        attn::add2(d[2], d[3], nd.z, nd.w);
-                        mul2(p[k], p[k + 1], d[0], d[1]);
-                        mul2(p[k + 2], p[k + 3], d[2], d[3]);
-                    }
-                }
+                for (int k = 0; k < 16; ++k) nd[k] = st[32 + k];
+                tmem_st_wait();
                 tc_fence_before();
-                named_sync(1, kSoftmax);      // both halves of dP^T are read
-                if (ok) {
-                    tc_fence_after();
-                    uint32_t y[32];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p);
+                ok = wait_warp(&sh.dp, i);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t x[2][32];
+                tmem_ld32(at_p, x[0]);
+                tmem_ld32(at_p + 32, x[1]);
+                tmem_ld_wait();
+                uint32_t y[32];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) y[k] = attn::pack2(p[2 * k], p[2 * k + 1]);
-                    attn::tmem_st32(tb + b.ds + 32u * half + lanes, y);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&sh.ds);
-                        mbar_arrive(&sh.read[i & 1]);
-                    }
+                for (int k = 0; k < 64; k += 4) {
+                    float d[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) d[z] = __uint_as_float(x[k / 32][k % 32 + z]);
+                    attn::add2(d[0], d[1], nd[k / 4].x, nd[k / 4].y);
+                    attn::add2(d[2], d[3], nd[k / 4].z, nd[k / 4].w);
+                    mul2(d[0], d[1], p[k], p[k + 1]);
+                    mul2(d[2], d[3], p[k + 2], p[k + 3]);
+                    y[k / 2] = attn::pack2(d[0], d[1]);
+                    y[k / 2 + 1] = attn::pack2(d[2], d[3]);
+                }
+                attn::tmem_st32(at_p, y);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh.ds);
+                    mbar_arrive(&sh.read[i & 1]);
                 }
             }
             if (n > 0) ok = ok && wait_warp(&sh.fin, 0);
@@ -386,7 +383,7 @@ struct Cta {
             } else {
                 tc_fence_after();
                 const long long at = ((seq.k0 + key) * a.Hk + it.head) * D;
-                store_row<D>(tb + (half ? TM_K : TM_V) + lanes,
+                store_row<D>(tb + (half ? TM_K : TM_V) + ((uint32_t)(32 * w) << 16),
                              static_cast<__nv_bfloat16 *>(half ? a.dk : a.dv) + at,
                              half ? a.scale : 1.f, n > 0, key < seq.lk);
             }
@@ -396,13 +393,9 @@ struct Cta {
     // ------------------------------------------------------------- row tile
     // Tiles: 0 Q, 1 dO; 2, 3, 4 the ring of K; 5, 6 of V.  Ring barriers: K 0
     // to 2, V 3 and 4.
-    __device__ void rows() {
-        const int TT = maps.tokens, R = TT * a.G, tok0 = it.tile * TT;
-        const int shift = seq.lk - seq.lq;
-        const int seen = min(tok0 + TT, seq.lq) + shift;
-        const int n = seen > 0 ? (seen + kTile - 1) / kTile : 0;
-        constexpr uint32_t TM_P = 256, TM_Q = 384;
-        if (n > 0 && warp == 9) {
+    __device__ void rows_work() {
+        if (n == 0) return;
+        if (warp == 9) {
             bool ok = true;
             if (lane == 0) {
                 const uint32_t box = (uint32_t)R * 128u * C::SLABS;
@@ -443,52 +436,64 @@ struct Cta {
                 attn::zero_rows<C::SLABS>(base + (2 + slot) * C::TILE, valid, lane);
                 if (lane == 0) mbar_arrive(&sh.tail[0]);
             }
-        } else if (n > 0 && warp == 8) {
-            constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
-            constexpr uint32_t id_g = idesc_bf16_f32(128, D, false, true);
-            const auto product = [&](int A, int tile, uint32_t out, uint64_t *bar) {
-                const uint32_t x = addr(A), y = addr(tile);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    mma_bf16(tb + out, attn::kdesc(x, ks), attn::kdesc(y, ks), id_s, ks > 0);
-                mma_commit(bar);
-            };
-            // the keys' rows are summed over in dQ: those behind the last are a
-            // neighbour's, and the loads' warp zeroes them
-            const bool ragged = n * kTile > seq.lk;
-            const auto scores = [&](int i) {
-                if (!wait(&sh.full[i % 3], i / 3)) return false;
-                if (ragged && i == n - 1 && !wait(&sh.tail[0], 0)) return false;
-                product(0, 2 + i % 3, 128u * (i & 1), &sh.s[i & 1]);
-                return true;
-            };
-            const auto grads = [&](int i) {
-                if (!wait(&sh.full[3 + i % 2], i / 2)) return false;
-                product(1, 5 + i % 2, TM_P, &sh.dp);
-                mma_commit(&sh.empty[3 + i % 2]);
-                return true;
-            };
+        } else if (warp == 8) {
             if (lane == 0) {
-            bool ok = wait(&sh.fix, 0) && scores(0) && grads(0) && (n < 2 || scores(1));
-            for (int i = 0; ok && i < n; ++i) {
-                ok = wait(&sh.ds, i);
-                tc_fence_after();
-                ok = ok && (i + 1 >= n || grads(i + 1));
-                if (!ok) break;
-                const uint32_t y = addr(2 + i % 3);
+                constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
+                constexpr uint32_t id_g = idesc_bf16_f32(128, D, false, true);
+                const auto product = [&](int A, int tile, uint32_t out, uint64_t *bar) {
+                    const uint32_t x = addr(A), y = addr(tile);
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)          // dS: 32 columns in each half of S's
-                    mma_bf16_ts(tb + TM_Q, tb + 128u * (i & 1) + 64u * (ks / 4) + 8u * (ks % 4),
-                                attn::mdesc(y, ks), id_g, i > 0 || ks > 0);
-                mma_commit(&sh.empty[i % 3]);
-                if (i + 2 < n) ok = scores(i + 2);
-            }
-            if (!ok) give_up();
-            mma_commit(&sh.fin);
-            (void)mbar_wait(&sh.fin, 0u);
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_bf16(tb + out, attn::kdesc(x, ks), attn::kdesc(y, ks), id_s, ks > 0);
+                    mma_commit(bar);
+                };
+                // the keys' rows are summed over in dQ: those behind the last are a
+                // neighbour's, and the loads' warp zeroes them
+                const bool ragged = n * kTile > seq.lk;
+                const auto key_landed = [&](int i) {
+                    return wait(&sh.full[i % 3], i / 3) &&
+                           (!ragged || i < n - 1 || wait(&sh.tail[0], 0));
+                };
+                const auto value_landed = [&](int i) { return wait(&sh.full[3 + i % 2], i / 2); };
+                const auto scores = [&](int i) { product(0, 2 + i % 3, 128u * (i & 1), &sh.s[i & 1]); };
+                const auto grads = [&](int i) {
+                    product(1, 5 + i % 2, TM_DP, &sh.dp);
+                    mma_commit(&sh.empty[3 + i % 2]);
+                };
+                bool ok = wait(&sh.fix, 0) && key_landed(0);
+                if (ok) scores(0);
+                ok = ok && value_landed(0);
+                if (ok) grads(0);
+                ok = ok && (n < 2 || key_landed(1));
+                if (ok && n > 1) scores(1);
+                ok = ok && (n < 2 || value_landed(1));
+                for (int i = 0; ok && i < n; ++i) {
+                    ok = wait(&sh.ds, i);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (i + 1 < n) grads(i + 1);
+                    const uint32_t y = addr(2 + i % 3);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_bf16_ts(tb + TM_Q, tb + operand(128u * (i & 1), ks), attn::mdesc(y, ks),
+                                    id_g, i > 0 || ks > 0);
+                    mma_commit(&sh.empty[i % 3]);
+                    if (i + 2 < n) {
+                        ok = key_landed(i + 2);
+                        if (!ok) break;
+                        scores(i + 2);
+                        ok = value_landed(i + 2);
+                    }
+                }
+                if (!ok) give_up();
+                mma_commit(&sh.fin);
+                (void)mbar_wait(&sh.fin, 0u);
             }
             __syncwarp();
-        } else if (warp < 8) {
+        }
+    }
+    __device__ void rows_softmax() {
+        {
             const int half = warp / 4, w = warp % 4, r = 32 * w + lane;
             const int tok = tok0 + r / a.G;
             const bool row = r < R && tok < seq.lq;
@@ -527,7 +532,7 @@ struct Cta {
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t x[2][32];
-                const uint32_t tD = tb + TM_P + 64u * half + lanes;
+                const uint32_t tD = tb + TM_DP + 64u * half + lanes;
                 tmem_ld32(tD, x[0]);
                 tmem_ld32(tD + 32, x[1]);
                 tmem_ld_wait();
@@ -613,9 +618,17 @@ attn_tc_bwd_kernel(const __grid_constant__ Args ak, const __grid_constant__ Args
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    Cta<D> cta{a, maps, sh, base, sh.tmem, warp, lane, it, seq};
-    if (key_tile) cta.keys();
-    else cta.rows();
+    Cta<D> cta(a, maps, sh, base, warp, lane, it, seq, key_tile);
+    // Registers of a thread: 128 x 88 + 256 x 208 = 384 x 168.
+    if (warp >= 8) {
+        attn::fewer_registers<88>();
+        if (key_tile) cta.keys_work();
+        else cta.rows_work();
+    } else {
+        attn::more_registers<208>();
+        if (key_tile) cta.keys_softmax();
+        else cta.rows_softmax();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
