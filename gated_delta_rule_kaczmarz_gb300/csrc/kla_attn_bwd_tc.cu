@@ -19,12 +19,18 @@
 // issues the products, the loads (TMA) and, for key tiles, the rows' lse and
 // delta.  p and ds are rounded to bf16 as operands; sums are fp32.
 //
-// Order of a key tile's products (one thread issues them, so they run in this
-// order): dV runs under the dS step, dK and the next dP^T under the
-// exponentials.  P^T takes the columns of S^T, dS^T those of dP^T:
+// Order of a key tile's products: dV runs under the dS step, dK and the next
+// dP^T under the exponentials.  P^T takes the columns of S^T, dS^T those of
+// dP^T:
 //
 //     S' (next)   dK   dP'   dV'
 //     [ds done]        [exp: P']   [ds']
+//
+// A wait takes 100 to 150 cycles even where there is nothing to wait for, and
+// the queue of issued products about 300: two warps issue, one lane each, so
+// that one's waits run under the other's products.  Products that overwrite
+// what an earlier one reads are the same lane's (dV, then S^T; dK, then dP^T;
+// dQ, then S), so they run in order.
 #include "kla_attn_tc.cuh"
 
 namespace kla {
@@ -50,7 +56,8 @@ struct Cfg {
 struct Shared {
     uint64_t fix;                        // the CTA's own tiles landed
     uint64_t full[5], empty[5];          // ring slots
-    uint64_t s[2], dp, p, ds;            // products ready; operands ready
+    uint64_t s[2], dp, p, ds[2];         // products ready; operands ready
+    uint64_t turn[2];                    // of the second warp of products
     uint64_t st[2], read[2];             // row statistics ready, and read
     uint64_t tail[2], fin;
     uint32_t tmem;
@@ -210,7 +217,8 @@ struct Cta {
                     attn::zero_rows<C::SLABS>(base + (2 + j % 4) * C::TILE, valid, lane);
                     if (lane == 0) mbar_arrive(&sh.tail[j & 1]);
                 }
-        } else if (warp == 8) {
+        } else if (warp == 8 || warp == 11) {
+            // two warps, a lane each: S^T and dV, dP^T and dK
             if (lane == 0) {
                 constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
                 constexpr uint32_t id_g = idesc_bf16_f32(128, D, false, true);
@@ -238,28 +246,38 @@ struct Cta {
                     return wait(&sh.full[j % 4], j / 4) &&
                            (!ragged || j < 2 * n - 2 || wait(&sh.tail[j & 1], 0));
                 };
-                bool ok = wait(&sh.fix, 0) && landed(0);
-                if (ok) product(0, 0, TM_S, &sh.s[0]);
-                ok = ok && landed(1);
-                if (ok) product(1, 1, TM_P, &sh.dp);
-                ok = ok && wait(&sh.p, 0);
-                tc_fence_after();
-                if (ok) gather(TM_S, 1, TM_V, false);
-                for (int i = 0; ok && i < n; ++i) {
-                    const bool more = i + 1 < n;
-                    ok = (!more || landed(2 * i + 2)) && wait(&sh.ds, i);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (more) product(0, 2 * i + 2, TM_S, &sh.s[0]);
-                    gather(TM_P, 2 * i, TM_K, i > 0);
-                    if (!more) break;
-                    ok = landed(2 * i + 3);
-                    if (!ok) break;
-                    product(1, 2 * i + 3, TM_P, &sh.dp);
-                    ok = wait(&sh.p, i + 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    gather(TM_S, 2 * i + 3, TM_V, true);
+                bool ok = wait(&sh.fix, 0);
+                if (warp == 8) {
+                    ok = ok && landed(0);
+                    if (ok) product(0, 0, TM_S, &sh.s[0]);
+                    for (int i = 0; ok && i < n; ++i) {
+                        ok = wait(&sh.p, i);
+                        if (!ok) break;
+                        tc_fence_after();
+                        gather(TM_S, 2 * i + 1, TM_V, i > 0);
+                        if (i + 1 == n) break;
+                        ok = landed(2 * i + 2) && wait(&sh.ds[i & 1], i / 2);
+                        if (!ok) break;
+                        product(0, 2 * i + 2, TM_S, &sh.s[0]);
+                        mbar_arrive(&sh.turn[0]);
+                    }
+                } else {
+                    ok = ok && landed(1);
+                    if (ok) {
+                        product(1, 1, TM_P, &sh.dp);
+                        mma_commit(&sh.empty[1]);
+                    }
+                    for (int i = 0; ok && i < n; ++i) {
+                        const bool more = i + 1 < n;
+                        ok = (!more || landed(2 * i + 3)) && wait(&sh.ds[i & 1], i / 2) &&
+                             (!more || wait(&sh.turn[0], i));
+                        if (!ok) break;
+                        tc_fence_after();
+                        gather(TM_P, 2 * i, TM_K, i > 0);
+                        if (!more) break;
+                        product(1, 2 * i + 3, TM_P, &sh.dp);
+                        mma_commit(&sh.empty[(2 * i + 3) % 4]);
+                    }
                 }
                 if (!ok) give_up();
                 mma_commit(&sh.fin);
@@ -341,13 +359,13 @@ struct Cta {
                     for (int k = 0; k < 32; ++k) y[k] = attn::pack2(p[2 * k], p[2 * k + 1]);
                     attn::tmem_st32(at_s, y);
                 }
-                float4 nd[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) nd[k] = st[32 + k];
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.p);
+                float4 nd[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) nd[k] = st[32 + k];
                 ok = wait_warp(&sh.dp, i);
                 if (!ok) break;
                 tc_fence_after();
@@ -373,7 +391,7 @@ struct Cta {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&sh.ds);
+                    mbar_arrive(&sh.ds[i & 1]);
                     mbar_arrive(&sh.read[i & 1]);
                 }
             }
@@ -436,7 +454,8 @@ struct Cta {
                 attn::zero_rows<C::SLABS>(base + (2 + slot) * C::TILE, valid, lane);
                 if (lane == 0) mbar_arrive(&sh.tail[0]);
             }
-        } else if (warp == 8) {
+        } else if (warp == 8 || warp == 11) {
+            // two warps, a lane each: S and dQ, dP
             if (lane == 0) {
                 constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
                 constexpr uint32_t id_g = idesc_bf16_f32(128, D, false, true);
@@ -460,29 +479,31 @@ struct Cta {
                     product(1, 5 + i % 2, TM_DP, &sh.dp);
                     mma_commit(&sh.empty[3 + i % 2]);
                 };
-                bool ok = wait(&sh.fix, 0) && key_landed(0);
-                if (ok) scores(0);
-                ok = ok && value_landed(0);
-                if (ok) grads(0);
-                ok = ok && (n < 2 || key_landed(1));
-                if (ok && n > 1) scores(1);
-                ok = ok && (n < 2 || value_landed(1));
-                for (int i = 0; ok && i < n; ++i) {
-                    ok = wait(&sh.ds, i);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (i + 1 < n) grads(i + 1);
-                    const uint32_t y = addr(2 + i % 3);
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_bf16_ts(tb + TM_Q, tb + operand(128u * (i & 1), ks), attn::mdesc(y, ks),
-                                    id_g, i > 0 || ks > 0);
-                    mma_commit(&sh.empty[i % 3]);
-                    if (i + 2 < n) {
-                        ok = key_landed(i + 2);
+                bool ok = wait(&sh.fix, 0);
+                if (warp == 8) {
+                    for (int i = 0; ok && i < 2 && i < n; ++i) {
+                        ok = key_landed(i);
+                        if (ok) scores(i);
+                    }
+                    for (int i = 0; ok && i < n; ++i) {
+                        ok = (i + 2 >= n || key_landed(i + 2)) && wait(&sh.ds[i & 1], i / 2) &&
+                             (i + 1 >= n || wait(&sh.turn[i & 1], i / 2));
                         if (!ok) break;
-                        scores(i + 2);
-                        ok = value_landed(i + 2);
+                        tc_fence_after();
+                        const uint32_t y = addr(2 + i % 3);
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_bf16_ts(tb + TM_Q, tb + operand(128u * (i & 1), ks),
+                                        attn::mdesc(y, ks), id_g, i > 0 || ks > 0);
+                        mma_commit(&sh.empty[i % 3]);
+                        if (i + 2 < n) scores(i + 2);
+                    }
+                } else {
+                    for (int i = 0; ok && i < n; ++i) {
+                        ok = value_landed(i) && (i == 0 || wait(&sh.ds[(i - 1) & 1], (i - 1) / 2));
+                        if (!ok) break;
+                        grads(i);
+                        if (i > 0) mbar_arrive(&sh.turn[(i - 1) & 1]);
                     }
                 }
                 if (!ok) give_up();
@@ -556,7 +577,7 @@ struct Cta {
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.ds);
+                if (lane == 0) mbar_arrive(&sh.ds[i & 1]);
             }
             if (n > 0) ok = ok && wait_warp(&sh.fin, 0);
             if (!ok) {
@@ -593,19 +614,21 @@ attn_tc_bwd_kernel(const __grid_constant__ Args ak, const __grid_constant__ Args
 #pragma unroll
         for (int i = 0; i < 5; ++i) {
             mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], 1);
+            // a key tile's dO slots are read by both warps of products
+            mbar_init(&sh.empty[i], key_tile && i % 2 == 1 ? 2 : 1);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s[i], 1);
+            mbar_init(&sh.ds[i], 8);
+            mbar_init(&sh.turn[i], 1);
             mbar_init(&sh.tail[i], 1);
             mbar_init(&sh.st[i], 1);
             mbar_init(&sh.read[i], 8);
         }
         mbar_init(&sh.dp, 1);
         mbar_init(&sh.p, 8);
-        mbar_init(&sh.ds, 8);
-        mbar_init(&sh.fin, 1);
+        mbar_init(&sh.fin, 2);
         sh.abort = 0;
         fence_mbar_init();
     }
