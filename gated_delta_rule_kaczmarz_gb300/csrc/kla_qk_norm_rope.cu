@@ -49,53 +49,52 @@ struct QkArgs {
     float eps;
 };
 
-__device__ __forceinline__ void ld8(const float *p, float (&x)[8]) {
-    const float4 a = *reinterpret_cast<const float4 *>(p);
-    const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void unpack(const uint4 &v, float (&x)[8]) {
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-}
+// 8 features as loaded and as four pairs for the packed fp32 instructions: the
+// pass executes about 90 instructions for 1 KB of bf16 with them and 170
+// without, where it was bound by their issue.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// 8 features as loaded: one or two 16-byte words.
 template <typename T>
 struct Raw;
 template <>
 struct Raw<__nv_bfloat16> {
     uint4 v;
+    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
         v = *reinterpret_cast<const uint4 *>(p);
     }
-    __device__ __forceinline__ void get(float (&x)[8]) const { unpack(v, x); }
+    __device__ __forceinline__ void get(float2 *x) const {
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+    }
 };
 template <>
 struct Raw<float> {
-    float x[8];
-    __device__ __forceinline__ void load(const float *p) { ld8(p, x); }
-    __device__ __forceinline__ void get(float (&o)[8]) const {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = x[i];
+    float4 u, v;
+    __device__ __forceinline__ void zero() { u = v = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void load(const float *p) {
+        u = *reinterpret_cast<const float4 *>(p);
+        v = *reinterpret_cast<const float4 *>(p + 4);
+    }
+    __device__ __forceinline__ void get(float2 *x) const {
+        x[0] = make_float2(u.x, u.y); x[1] = make_float2(u.z, u.w);
+        x[2] = make_float2(v.x, v.y); x[3] = make_float2(v.z, v.w);
     }
 };
-__device__ __forceinline__ void st8(__nv_bfloat16 *p, const float (&x)[8]) {
+__device__ __forceinline__ void st8(__nv_bfloat16 *p, const float2 *x) {
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[i].x, x[i].y);
         u[i] = reinterpret_cast<const uint32_t &>(h);
     }
     *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ void st8(float *p, const float (&x)[8]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void st8(float *p, const float2 *x) {
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+    *reinterpret_cast<float4 *>(p + 4) = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
 }
 
 // inv_freq / 2 pi, modulo one turn, as a 64-bit fraction.
@@ -126,57 +125,69 @@ struct Lane {
     }
 };
 
-// Cosines and sines of the token into cs[pair] (the warp's own array).
+// Cosines and sines of a token: each lane computes those of two pairs and
+// takes from the warp's array those of its own features, once for all heads.
 struct Angles {
     unsigned long long step[2];
-    int axis[2];
+    long long at[2];          // of the pair's axis in the positions
+    int pos[2];               // of the token to come, read ahead
+    float2 c[4], s[4];        // of the lane's eight pairs
     __device__ void init(const QkArgs &a, int lane) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int p = lane + 32 * i;
             step[i] = p < a.pairs ? turns_per_position(a.freq[p]) : 0ull;
-            axis[i] = (p >= a.end[0]) + (p >= a.end[1]) + (p >= a.end[2]);
+            at[i] = (long long)((p >= a.end[0]) + (p >= a.end[1]) + (p >= a.end[2])) * a.tokens;
         }
     }
-    __device__ __forceinline__ void write(const QkArgs &a, int lane, int t, float2 *cs) const {
+    __device__ __forceinline__ void read(const QkArgs &a, int lane, int t) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (lane + 32 * i < a.pairs) pos[i] = a.pos[at[i] + t];
+    }
+    template <int D>
+    __device__ __forceinline__ void turn(const QkArgs &a, int lane, const Lane<D> &l, float2 *cs) {
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int p = lane + 32 * i;
             if (p < a.pairs) {
-                const long long pos = a.pos[(long long)axis[i] * a.tokens + t];
-                const int top = (int)((step[i] * (unsigned long long)pos) >> 32);
-                float s, c;
-                sincospif((float)top * 0x1p-31f, &s, &c);
-                cs[p] = make_float2(c, s);
+                const int top = (int)((step[i] * (unsigned long long)(long long)pos[i]) >> 32);
+                float sn, cn;
+                sincospif((float)top * 0x1p-31f, &sn, &cn);
+                cs[p] = make_float2(cn, sn);
             }
+        }
+        __syncwarp();
+        if (!l.rotated) return;
+        // half: pairs col0 .. col0 + 7; pairs: four from each run
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = a.pair_style == 0 ? l.col0 + 2 * i : i < 2 ? l.pair0 + 2 * i : l.pair1 + 2 * i - 4;
+            const float4 v = *reinterpret_cast<const float4 *>(cs + p);
+            c[i] = make_float2(v.x, v.z);
+            s[i] = make_float2(v.y, v.w);
         }
     }
 };
 
-// (x0, x1): a lane's two runs; dir 1 turns forward, -1 back.
-template <int D>
-__device__ __forceinline__ void rotate(float (&x0)[8], float (&x1)[8], const Lane<D> &l,
-                                       const float2 *cs, int pair_style, float dir) {
+// x: a lane's two runs of four pairs; BACK turns back.
+template <int D, bool BACK>
+__device__ __forceinline__ void rotate(float2 (&x)[8], const Lane<D> &l, const Angles &g,
+                                       int pair_style) {
     if (!l.rotated) return;
-    if (pair_style == 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 c = cs[l.col0 + i];
-            const float s = dir * c.y, u = x0[i], v = x1[i];
-            x0[i] = u * c.x - v * s;
-            x1[i] = v * c.x + u * s;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float2 c = cs[l.pair0 + i];
-            float s = dir * c.y, u = x0[2 * i], v = x0[2 * i + 1];
-            x0[2 * i] = u * c.x - v * s;
-            x0[2 * i + 1] = v * c.x + u * s;
-            c = cs[l.pair1 + i];
-            s = dir * c.y; u = x1[2 * i]; v = x1[2 * i + 1];
-            x1[2 * i] = u * c.x - v * s;
-            x1[2 * i + 1] = v * c.x + u * s;
+    for (int i = 0; i < 4; ++i) {
+        const float2 c = g.c[i], m = make_float2(-g.s[i].x, -g.s[i].y);
+        const float2 s = BACK ? m : g.s[i], n = BACK ? g.s[i] : m;      // sine, -sine
+        if (pair_style == 0) {
+            const float2 u = x[i], v = x[4 + i];
+            x[i] = __ffma2_rn(v, n, __fmul2_rn(u, c));
+            x[4 + i] = __ffma2_rn(u, s, __fmul2_rn(v, c));
+        } else {
+            const float2 u = x[2 * i], v = x[2 * i + 1];
+            x[2 * i] = __ffma2_rn(make_float2(u.y, u.x), make_float2(n.x, s.x), __fmul2_rn(u, both(c.x)));
+            x[2 * i + 1] = __ffma2_rn(make_float2(v.y, v.x), make_float2(n.y, s.y), __fmul2_rn(v, both(c.y)));
         }
     }
 }
@@ -189,14 +200,34 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 template <int D>
-__device__ __forceinline__ float inv_norm(float n2, int mode, float eps) {
+__device__ __forceinline__ float row_dot(const float2 (&x)[8], const float2 (&y)[8]) {
+    float2 a = __fmul2_rn(x[0], y[0]), b = __fmul2_rn(x[1], y[1]);
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) {
+        a = __ffma2_rn(x[i], y[i], a);
+        b = __ffma2_rn(x[i + 1], y[i + 1], b);
+    }
+    a = __fadd2_rn(a, b);
+    return row_sum<D>(a.x + a.y);
+}
+template <int D>
+__device__ __forceinline__ float inv_norm(const float2 (&x)[8], int mode, float eps) {
     if (mode == 0) return 1.f;
-    const float m = (mode == 1 ? n2 * (1.f / D) : n2) + eps;
-    return m == 0.f ? 0.f : 1.f / sqrtf(m);      // a zero row with eps = 0 stays zero
+    const float n2 = row_dot<D>(x, x), m = (mode == 1 ? n2 * (1.f / D) : n2) + eps;
+    return m == 0.f ? 0.f : rsqrtf(m);      // a zero row with eps = 0 stays zero
+}
+// The weights of a lane's features.
+template <int D>
+__device__ __forceinline__ void load_weight(float2 (&w)[8], const float *p, const Lane<D> &l) {
+    Raw<float> a, b;
+    a.load(p + l.col0);
+    b.load(p + l.col1);
+    a.get(w);
+    b.get(w + 4);
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 qk_fwd_kernel(const __grid_constant__ QkArgs a) {
     constexpr int RW = 512 / D;                       // rows of a warp's group
     constexpr int U = sizeof(T) == 2 ? 4 : 2;         // groups loaded ahead
@@ -206,23 +237,20 @@ qk_fwd_kernel(const __grid_constant__ QkArgs a) {
     const Lane<D> l(lane, a.pairs);
     Angles ang;
     ang.init(a, lane);
-    const long long items = (long long)a.tokens * a.parts;
-    for (long long it = (long long)blockIdx.x * kWarps + warp; it < items;
-         it += (long long)gridDim.x * kWarps) {
-        const int t = (int)(it / a.parts), part = (int)(it % a.parts);
-        __syncwarp();
-        ang.write(a, lane, t, cs);
-        __syncwarp();
+    const int stride = gridDim.x * kWarps, part = blockIdx.y;
+    int t = blockIdx.x * kWarps + warp;
+    if (t < a.tokens) ang.read(a, lane, t);
+    // (unsigned: the last step may pass 2^31)
+    for (; (unsigned)t < (unsigned)a.tokens; t = (int)((unsigned)t + stride)) {
+        ang.turn(a, lane, l, cs);
+        if ((unsigned)t + stride < (unsigned)a.tokens) ang.read(a, lane, t + stride);
 #pragma unroll 1
         for (int z = 0; z < 2; ++z) {
             const int H = a.heads[z];
             if (H == 0) continue;
-            float w0[8], w1[8];
+            float2 w[8];
             const bool weighted = a.w[z] != nullptr;
-            if (weighted) {
-                ld8(a.w[z] + l.col0, w0);
-                ld8(a.w[z] + l.col1, w1);
-            }
+            if (weighted) load_weight<D>(w, a.w[z], l);
             const T *x = static_cast<const T *>(a.x[z]) + (long long)t * a.xs[z];
             T *y = static_cast<T *>(a.y[z]) + (long long)t * a.ys[z];
             const int mode = a.norm[z];
@@ -240,31 +268,22 @@ qk_fwd_kernel(const __grid_constant__ QkArgs a) {
                 for (int u = 0; u < U; ++u) {
                     if (h0 + u * a.parts * RW >= H) break;      // the warp's whole group
                     const int h = h0 + u * a.parts * RW + l.row;
-                    float x0[8], x1[8];
-                    r0[u].get(x0);
-                    r1[u].get(x1);
+                    float2 v[8];
+                    r0[u].get(v);
+                    r1[u].get(v + 4);
                     if (mode != 0) {
-                        float n2 = 0.f;
+                        const float2 r = both(inv_norm<D>(v, mode, a.eps));
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) n2 += x0[i] * x0[i] + x1[i] * x1[i];
-                        const float r = inv_norm<D>(row_sum<D>(n2), mode, a.eps);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            x0[i] *= r;
-                            x1[i] *= r;
-                        }
+                        for (int i = 0; i < 8; ++i) v[i] = __fmul2_rn(v[i], r);
                     }
                     if (weighted) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            x0[i] *= w0[i];
-                            x1[i] *= w1[i];
-                        }
+                        for (int i = 0; i < 8; ++i) v[i] = __fmul2_rn(v[i], w[i]);
                     }
-                    rotate<D>(x0, x1, l, cs, a.pair_style, 1.f);
+                    rotate<D, false>(v, l, ang, a.pair_style);
                     if (h < H) {
-                        st8(y + h * D + l.col0, x0);
-                        st8(y + h * D + l.col1, x1);
+                        st8(y + h * D + l.col0, v);
+                        st8(y + h * D + l.col1, v + 4);
                     }
                 }
             }
@@ -276,7 +295,7 @@ qk_fwd_kernel(const __grid_constant__ QkArgs a) {
 // the block, and leave as one partial sum per block: no atomics, so a result
 // does not depend on the order in which blocks run.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 qk_bwd_kernel(const __grid_constant__ QkArgs a) {
     constexpr int RW = 512 / D;
     constexpr int U = sizeof(T) == 2 ? 2 : 1;
@@ -287,85 +306,69 @@ qk_bwd_kernel(const __grid_constant__ QkArgs a) {
     const Lane<D> l(lane, a.pairs);
     Angles ang;
     ang.init(a, lane);
-    float acc[2][16];
+    float2 acc[2][8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[0][i] = acc[1][i] = 0.f;
-    const long long items = (long long)a.tokens * a.parts;
-    for (long long it = (long long)blockIdx.x * kWarps + warp; it < items;
-         it += (long long)gridDim.x * kWarps) {
-        const int t = (int)(it / a.parts), part = (int)(it % a.parts);
-        __syncwarp();
-        ang.write(a, lane, t, cs);
-        __syncwarp();
+    for (int i = 0; i < 8; ++i) acc[0][i] = acc[1][i] = both(0.f);
+    const int stride = gridDim.x * kWarps, part = blockIdx.y;
+    int t = blockIdx.x * kWarps + warp;
+    if (t < a.tokens) ang.read(a, lane, t);
+    // (unsigned: the last step may pass 2^31)
+    for (; (unsigned)t < (unsigned)a.tokens; t = (int)((unsigned)t + stride)) {
+        ang.turn(a, lane, l, cs);
+        if ((unsigned)t + stride < (unsigned)a.tokens) ang.read(a, lane, t + stride);
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
             const int H = a.heads[z];
             if (H == 0) continue;
-            float w0[8], w1[8];
+            float2 w[8];
             const bool weighted = a.w[z] != nullptr;
-            if (weighted) {
-                ld8(a.w[z] + l.col0, w0);
-                ld8(a.w[z] + l.col1, w1);
-            }
+            if (weighted) load_weight<D>(w, a.w[z], l);
             const T *x = static_cast<const T *>(a.x[z]) + (long long)t * a.xs[z];
             const T *g = static_cast<const T *>(a.g[z]) + (long long)t * a.gs[z];
             T *y = static_cast<T *>(a.y[z]) + (long long)t * a.ys[z];
             const int mode = a.norm[z];
             for (int h0 = part * RW; h0 < H; h0 += U * a.parts * RW) {
-                Raw<T> rx0[U], rx1[U], rg0[U], rg1[U];
+                Raw<T> x0[U], x1[U], g0[U], g1[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int h = h0 + u * a.parts * RW + l.row;
                     if (h < H) {
-                        rx0[u].load(x + h * D + l.col0);
-                        rx1[u].load(x + h * D + l.col1);
-                        rg0[u].load(g + h * D + l.col0);
-                        rg1[u].load(g + h * D + l.col1);
+                        x0[u].load(x + h * D + l.col0);
+                        x1[u].load(x + h * D + l.col1);
+                        g0[u].load(g + h * D + l.col0);
+                        g1[u].load(g + h * D + l.col1);
+                    } else {              // no row: adds nothing to the weights' gradients
+                        x0[u].zero(); x1[u].zero(); g0[u].zero(); g1[u].zero();
                     }
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (h0 + u * a.parts * RW >= H) break;
                     const int h = h0 + u * a.parts * RW + l.row;
-                    float x0[8], x1[8], g0[8], g1[8];
-                    rx0[u].get(x0);
-                    rx1[u].get(x1);
-                    rg0[u].get(g0);
-                    rg1[u].get(g1);
-                    rotate<D>(g0, g1, l, cs, a.pair_style, -1.f);
-                    float r = 1.f;
-                    if (mode != 0) {
-                        float n2 = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) n2 += x0[i] * x0[i] + x1[i] * x1[i];
-                        r = inv_norm<D>(row_sum<D>(n2), mode, a.eps);
-                    }
+                    float2 v[8], d[8];
+                    x0[u].get(v);
+                    x1[u].get(v + 4);
+                    g0[u].get(d);
+                    g1[u].get(d + 4);
+                    rotate<D, true>(d, l, ang, a.pair_style);
+                    const float r = inv_norm<D>(v, mode, a.eps);
                     if (weighted) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            if (h < H) {
-                                acc[z][i] = fmaf(g0[i], x0[i] * r, acc[z][i]);
-                                acc[z][8 + i] = fmaf(g1[i], x1[i] * r, acc[z][8 + i]);
-                            }
-                            g0[i] *= w0[i];
-                            g1[i] *= w1[i];
+                            acc[z][i] = __ffma2_rn(d[i], __fmul2_rn(v[i], both(r)), acc[z][i]);
+                            d[i] = __fmul2_rn(d[i], w[i]);
                         }
                     }
                     if (mode != 0) {
-                        float dot = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) dot += g0[i] * x0[i] + g1[i] * x1[i];
-                        dot = row_sum<D>(dot) * r * r;
+                        float dot = row_dot<D>(d, v) * r * r;
                         if (mode == 1) dot *= 1.f / D;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            g0[i] = r * (g0[i] - x0[i] * dot);
-                            g1[i] = r * (g1[i] - x1[i] * dot);
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            d[i] = __fmul2_rn(__ffma2_rn(v[i], both(-dot), d[i]), both(r));
                     }
                     if (h < H) {
-                        st8(y + h * D + l.col0, g0);
-                        st8(y + h * D + l.col1, g1);
+                        st8(y + h * D + l.col0, d);
+                        st8(y + h * D + l.col1, d + 4);
                     }
                 }
             }
@@ -376,7 +379,7 @@ qk_bwd_kernel(const __grid_constant__ QkArgs a) {
     for (int z = 0; z < 2; ++z)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float v = acc[z][i];
+            float v = i % 2 ? acc[z][i / 2].y : acc[z][i / 2].x;
 #pragma unroll
             for (int o = 16; o >= D / 16; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
             if (l.row == 0) part_w[warp][z][i < 8 ? l.col0 + i : l.col1 + i - 8] = v;
@@ -386,7 +389,7 @@ qk_bwd_kernel(const __grid_constant__ QkArgs a) {
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v += part_w[w][i / D][i % D];
-        a.dw[(size_t)blockIdx.x * 2 * D + i] = v;
+        a.dw[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 * D + i] = v;
     }
 }
 
@@ -410,7 +413,7 @@ qk_dw_kernel(const float *part, int blocks, int d, float *dwq, float *dwk) {
 
 // Blocks that a launch may use: the partial sums of the backward pass are
 // sized by it, so it depends on the problem alone.
-constexpr int kMaxBlocks = 152 * 8;
+constexpr int kMaxBlocks = 152 * 12;
 
 // A warp takes a token's heads in `parts` parts: one when the tokens alone
 // give every SM 32 warps (the cosines are then computed once a token), else as
@@ -440,21 +443,23 @@ QkArgs make_args(const QkProblem &p) {
     return a;
 }
 
-int blocks_for(const QkArgs &a) {
-    const long long want = ((long long)a.tokens * a.parts + kWarps - 1) / kWarps;
-    return (int)(want < kMaxBlocks ? want : kMaxBlocks);
+// Blocks over the tokens, and their parts beside.
+dim3 blocks_for(const QkArgs &a) {
+    const int want = (a.tokens - 1) / kWarps + 1, most = (kMaxBlocks - 1) / a.parts + 1;
+    return dim3((unsigned)(want < most ? want : most), (unsigned)a.parts);
 }
 
 }  // namespace
 
 size_t qk_bwd_workspace_bytes(const QkProblem &p) {
     if (p.tokens == 0) return 0;
-    return (size_t)blocks_for(make_args(p)) * 2 * p.d * sizeof(float);
+    const dim3 b = blocks_for(make_args(p));
+    return (size_t)b.x * b.y * 2 * p.d * sizeof(float);
 }
 
 cudaError_t launch_qk_fwd(const QkProblem &p, cudaStream_t s) {
     const QkArgs a = make_args(p);
-    const int blocks = blocks_for(a);
+    const dim3 blocks = blocks_for(a);
     if (p.dtype == 1) {
         if (p.d == 128) qk_fwd_kernel<__nv_bfloat16, 128><<<blocks, kThreads, 0, s>>>(a);
         else qk_fwd_kernel<__nv_bfloat16, 64><<<blocks, kThreads, 0, s>>>(a);
@@ -470,7 +475,7 @@ cudaError_t launch_qk_bwd(const QkProblem &p, cudaStream_t s) {
     QkArgs a = make_args(p);
     const bool weights = p.dwq != nullptr || p.dwk != nullptr;
     a.dw = weights ? static_cast<float *>(p.ws) : nullptr;
-    const int blocks = blocks_for(a);
+    const dim3 blocks = blocks_for(a);
     if (p.dtype == 1) {
         if (p.d == 128) qk_bwd_kernel<__nv_bfloat16, 128><<<blocks, kThreads, 0, s>>>(a);
         else qk_bwd_kernel<__nv_bfloat16, 64><<<blocks, kThreads, 0, s>>>(a);
@@ -481,7 +486,7 @@ cudaError_t launch_qk_bwd(const QkProblem &p, cudaStream_t s) {
     note_launch();
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !weights) return e;
-    qk_dw_kernel<<<2 * p.d / 32, dim3(32, 32), 0, s>>>(a.dw, blocks, p.d, p.dwq, p.dwk);
+    qk_dw_kernel<<<2 * p.d / 32, dim3(32, 32), 0, s>>>(a.dw, (int)(blocks.x * blocks.y), p.d, p.dwq, p.dwk);
     note_launch();
     return cudaGetLastError();
 }
