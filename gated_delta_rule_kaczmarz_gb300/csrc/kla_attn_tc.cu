@@ -36,7 +36,7 @@ using attn::kSlab;
 using attn::kTile;
 using attn::Seq;
 
-constexpr int kThreads = 384;            // 8 softmax warps, 2 of products, loads, one idle
+constexpr int kThreads = 384;            // 8 softmax warps, 2 of products, loads, zeroing
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kGrow = 8.f;             // see above
 
@@ -62,7 +62,7 @@ struct Shared {
     uint64_t q[2], q_read[2];            // Q tiles landed, and no longer read
     uint64_t s[2], p[2], o[2];           // scores ready, probabilities ready, product done
     uint64_t work[2], work_read[2];      // items published, and read
-    uint64_t turn[2], tail, asked, fin;
+    uint64_t turn[2], last, tail, asked, fin;
     uint4 answer;
     Work item[2];
     uint32_t tmem;
@@ -103,9 +103,10 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
             mbar_init(&sh.p[t], 4);
             mbar_init(&sh.o[t], 1);
             mbar_init(&sh.work[t], 1);
-            mbar_init(&sh.work_read[t], 10);     // two lanes of products and eight softmax warps
+            mbar_init(&sh.work_read[t], 11);     // products (2), zeroing and softmax (8)
             mbar_init(&sh.turn[t], 1);
         }
+        mbar_init(&sh.last, 1);
         mbar_init(&sh.tail, 1);
         mbar_init(&sh.asked, 1);
         mbar_init(&sh.fin, 2);
@@ -166,20 +167,36 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                 const Work w = sh.item[m & 1];
                 if (!ok || !w.any) break;
                 const int nb = w.b1 - w.b0;
-                if (lane == 0 && nb > 0) {
+                bool asked = false;
+                if (lane == 0) {
                     const uint32_t box = (uint32_t)R * 128u;
+                    // The next block is asked for four key tiles before the end:
+                    // the answer and the item's rows are there when the last
+                    // load is under way.  (Earlier, a CTA would hold what
+                    // another could start.)  Q's tiles are free only after the
+                    // item before has its last scores, so the first key and
+                    // value tile go ahead of them.
+                    const int ask_at = max(0, 2 * nb - 8);
+                    for (int i = 0; ok && i <= 2 * nb; ++i) {
+                        if (i == ask_at) {
+                            mbar_expect_tx(&sh.asked, 16);
+                            attn::ask_block(&sh.answer, &sh.asked);
+                            asked = true;
+                        }
+                        if (i == 2) {
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (w.e[t] <= w.b0) continue;
-                        ok = ok && (used[t] == 0 || wait(&sh.q_read[t], used[t] - 1));
-                        if (!ok) break;
-                        ++used[t];
-                        mbar_expect_tx(&sh.q[t], box * C::SLABS);
-                        for (int c = 0; c < C::SLABS; ++c)
-                            tma_load_3d(sQ + t * C::TILE + c * kSlab, &maps.q, &sh.q[t], c * 64,
-                                        w.head * a.G, w.q0 + w.tok0 + t * TT);
-                    }
-                    for (int i = 0; ok && i < 2 * nb; ++i) {
+                            for (int t = 0; t < 2; ++t) {
+                                if (w.e[t] <= w.b0) continue;
+                                ok = ok && (used[t] == 0 || wait(&sh.q_read[t], used[t] - 1));
+                                if (!ok) break;
+                                ++used[t];
+                                mbar_expect_tx(&sh.q[t], box * C::SLABS);
+                                for (int c = 0; c < C::SLABS; ++c)
+                                    tma_load_3d(sQ + t * C::TILE + c * kSlab, &maps.q, &sh.q[t],
+                                                c * 64, w.head * a.G, w.q0 + w.tok0 + t * TT);
+                            }
+                        }
+                        if (!ok || i == 2 * nb) break;
                         const int slot = j % C::SLOTS, use = j / C::SLOTS;
                         ok = use == 0 || wait(&sh.empty[slot], use - 1);
                         if (!ok) break;
@@ -190,30 +207,14 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                             tma_load_3d(sKV + slot * C::TILE + c * kSlab, i % 2 ? &maps.v : &maps.k,
                                         &sh.full[slot], c * 64, w.head, row);
                     }
-                }
-                // the next block is asked for late, so that one CTA does not
-                // hold what another could start
-                const bool asked = ok;
-                if (lane == 0 && asked) {
-                    mbar_expect_tx(&sh.asked, 16);
-                    attn::ask_block(&sh.answer, &sh.asked);
-                }
-                ok = __all_sync(0xffffffffu, ok);
-                j = __shfl_sync(0xffffffffu, j, 0);
-                const int valid = w.lk - (w.b1 - 1) * kTile;
-                if (ok && nb > 0 && valid < kTile) {     // rows behind the sequence's last
-                    const int slot = (j - 1) % C::SLOTS;
-                    ok = wait_warp(&sh.full[slot], (j - 1) / C::SLOTS);
-                    if (ok) attn::zero_rows<C::SLABS>(sKV + slot * C::TILE, valid, lane);
-                    if (ok && lane == 0) mbar_arrive(&sh.tail);
-                }
-                if (lane == 0 && asked) {
-                    ok = mbar_wait(&sh.asked, (uint32_t)(m & 1)) && ok;
-                    block = attn::answered_block(&sh.answer);
-                    fence_async_smem();        // read before the next answer is written
+                    if (ok && nb > 0 && w.b1 * kTile > w.lk) mbar_arrive(&sh.last);
+                    if (asked) {
+                        ok = mbar_wait(&sh.asked, (uint32_t)(m & 1)) && ok;
+                        block = attn::answered_block(&sh.answer);
+                        fence_async_smem();        // read before the next answer is written
+                    }
                 }
                 ok = __all_sync(0xffffffffu, ok);
-                block = __shfl_sync(0xffffffffu, block, 0);
             }
             if (!ok && lane == 0) {    // given up: the copies in flight land before the CTA leaves
                 give_up();
@@ -222,6 +223,28 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                 for (int t = 0; t < 2; ++t)
                     if (used[t] > 0) (void)mbar_wait(&sh.q[t], (uint32_t)((used[t] - 1) & 1));
             }
+        } else if (warp == 11) {
+            // -------------- rows of a last V tile that are a neighbour's: zeroed
+            int j = 0, tails = 0;
+            bool ok = true;
+            for (int m = 0; ok; ++m) {
+                ok = wait_warp(&sh.work[m & 1], m / 2);
+                if (!ok) break;
+                const Work w = sh.item[m & 1];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.work_read[m & 1]);
+                if (!w.any) break;
+                j += 2 * (w.b1 - w.b0);
+                const int valid = w.lk - (w.b1 - 1) * kTile, slot = (j - 1) % C::SLOTS;
+                if (w.b1 == w.b0 || valid >= kTile) continue;
+                // asked for, so that the slot's barrier is in that load's phase
+                ok = wait_warp(&sh.last, tails++) &&
+                     wait_warp(&sh.full[slot], (j - 1) / C::SLOTS);
+                if (!ok) break;
+                attn::zero_rows<C::SLABS>(sKV + slot * C::TILE, valid, lane);
+                if (lane == 0) mbar_arrive(&sh.tail);
+            }
+            if (!ok) give_up();
         } else if (warp == 8 || warp == 10) {
             // ---------------------------------------------------------- products
             // A warp per row tile, one lane of which waits and issues: a wait
