@@ -118,7 +118,7 @@ FwdPlan fwd_plan(const AttnProblem &p) {
 struct BwdPlan {
     bool tc;
     Side q, k;
-    int rows, keys;
+    int tile;
     size_t table_q, table_k, delta, bytes;
 };
 BwdPlan bwd_plan(const AttnProblem &p) {
@@ -129,10 +129,10 @@ BwdPlan bwd_plan(const AttnProblem &p) {
         b.q = side(p, false, 1, attn::tile_tokens(G));
         b.k = side(p, true, 1, attn::kTile);
     } else {
-        b.rows = simt_rows(p, false);
-        b.keys = p.total_k > 0 ? simt_rows(p, true) : 16;
-        b.q = side(p, false, G, b.rows);
-        b.k = side(p, true, 1, b.keys);
+        b.tile = simt_rows(p, false);
+        if (p.total_k == 0 || simt_rows(p, true) == 16) b.tile = 16;
+        b.q = side(p, false, G, b.tile);
+        b.k = side(p, true, 1, b.tile);
     }
     size_t at = kWsHeader;
     b.table_q = at;
@@ -238,17 +238,11 @@ cudaError_t launch_attn_bwd(const AttnProblem &p, cudaStream_t s) {
     a.delta = reinterpret_cast<float *>(at(p, b.delta));
     e = launch_attn_delta(a, p.d, p.dtype, s);
     if (e != cudaSuccess) return e;
-    if (b.tc) {
-        attn::Args keys = a;
-        take(keys, b.k, tk);
-        take(a, b.q, tq);
-        return launch_attn_tc_bwd(keys, a, p.d, p.total_k, s);
-    }
-    take(a, b.k, tk);
-    e = launch_attn_simt_dkv(a, b.keys, p.d, p.dtype, s);
-    if (e != cudaSuccess) return e;
+    attn::Args keys = a;
+    take(keys, b.k, tk);
     take(a, b.q, tq);
-    return launch_attn_simt_dq(a, b.rows, p.d, p.dtype, s);
+    return b.tc ? launch_attn_tc_bwd(keys, a, p.d, p.total_k, s)
+                : launch_attn_simt_bwd(keys, a, b.tile, p.d, p.dtype, s);
 }
 
 }  // namespace kla

@@ -125,9 +125,9 @@ cudaError_t attn_allow_smem(const void *kernel, size_t bytes);
 cudaError_t launch_attn_join(const attn::Args &a, int d, int dtype, cudaStream_t s);
 cudaError_t launch_attn_delta(const attn::Args &a, int d, int dtype, cudaStream_t s);
 
-// CUDA-core kernels: any G.  rows / keys: rows of a tile, 16 or 64.
+// CUDA-core kernels: any G.  rows / tile: rows of a tile, 16 or 64.
 cudaError_t launch_attn_simt_fwd(const attn::Args &a, int rows, int d, int dtype, cudaStream_t s);
-cudaError_t launch_attn_simt_dq(const attn::Args &a, int rows, int d, int dtype, cudaStream_t s);
-cudaError_t launch_attn_simt_dkv(const attn::Args &a, int keys, int d, int dtype, cudaStream_t s);
+cudaError_t launch_attn_simt_bwd(const attn::Args &keys, const attn::Args &rows, int tile, int d,
+                                 int dtype, cudaStream_t s);
 
 }  // namespace kla

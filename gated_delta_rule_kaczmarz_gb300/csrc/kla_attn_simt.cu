@@ -252,13 +252,12 @@ constexpr size_t dq_smem() {
 }
 
 template <typename T, int D, int BM>
-__global__ void __launch_bounds__(kT) attn_simt_dq_kernel(const __grid_constant__ Args a) {
+__device__ void attn_simt_dq(const Args &a, int block, float *sm) {
     constexpr int MI = BM / 16;
-    extern __shared__ __align__(16) float sm[];
     float *Q = sm, *G = Q + BM * (D + 4), *K = G + BM * (D + 4), *V = K + 32 * (D + 4),
           *S = V + 32 * (D + 4);
     Item it;
-    if (!attn::item_of(a, blockIdx.x, true, it)) return;
+    if (!attn::item_of(a, block, true, it)) return;
     const Seq s = attn::sequence(a, it.seq);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const long long row0 = (long long)it.tile * BM, rows = (long long)s.lq * a.G;
@@ -315,13 +314,12 @@ constexpr size_t dkv_smem() {
 // the tile's keys are the 16-row side: thread (ty, tx) has keys ty + 16 i and
 // rows tx + 16 j.
 template <typename T, int D, int BN>
-__global__ void __launch_bounds__(kT) attn_simt_dkv_kernel(const __grid_constant__ Args a) {
+__device__ void attn_simt_dkv(const Args &a, int block, float *sm) {
     constexpr int MI = BN / 16;
-    extern __shared__ __align__(16) float sm[];
     float *K = sm, *V = K + BN * (D + 4), *Q = V + BN * (D + 4), *G = Q + 32 * (D + 4),
           *P = G + 32 * (D + 4), *S = P + BN * 36;
     Item it;
-    if (!attn::item_of(a, blockIdx.x, false, it)) return;
+    if (!attn::item_of(a, block, false, it)) return;
     const Seq s = attn::sequence(a, it.seq);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const int j0 = it.tile * BN;
@@ -380,6 +378,16 @@ __global__ void __launch_bounds__(kT) attn_simt_dkv_kernel(const __grid_constant
             st4(static_cast<T *>(a.dv) + at + 4 * tx + 64 * j, dv[i][j]);
         }
     }
+}
+
+// Both sides in one launch: the blocks of the key tiles first.
+template <typename T, int D, int B>
+__global__ void __launch_bounds__(kT)
+attn_simt_bwd_kernel(const __grid_constant__ Args keys, const __grid_constant__ Args rows,
+                     int key_blocks) {
+    extern __shared__ __align__(16) float sm[];
+    if ((int)blockIdx.x < key_blocks) attn_simt_dkv<T, D, B>(keys, blockIdx.x, sm);
+    else attn_simt_dq<T, D, B>(rows, blockIdx.x - key_blocks, sm);
 }
 
 // ------------------------------------------------------- shared by all paths
@@ -498,15 +506,26 @@ attn_prep_kernel(const int *cu_q, const int *cu_k, int n, int total_q, int total
     }
 }
 
-template <typename K>
-cudaError_t launch(K *kernel, const Args &a, size_t smem, cudaStream_t s) {
-    const long long blocks = (long long)a.items * a.splits * a.Hk;
+template <typename K, typename... A>
+cudaError_t launch(K *kernel, long long blocks, size_t smem, cudaStream_t s, const A &...args) {
     if (blocks == 0) return cudaSuccess;
     cudaError_t e = attn_allow_smem(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)blocks, kT, smem, s>>>(a);
+    kernel<<<(unsigned)blocks, kT, smem, s>>>(args...);
     note_launch();
     return cudaGetLastError();
+}
+
+template <typename T, int D, int B>
+cudaError_t launch_fwd(const Args &a, cudaStream_t s) {
+    return launch(attn_simt_fwd_kernel<T, D, B>, (long long)a.items * a.splits * a.Hk,
+                  fwd_smem<D, B>(), s, a);
+}
+template <typename T, int D, int B>
+cudaError_t launch_bwd(const Args &keys, const Args &rows, cudaStream_t s) {
+    const long long kb = (long long)keys.items * keys.Hk, rb = (long long)rows.items * rows.Hk;
+    constexpr size_t smem = dkv_smem<D, B>() > dq_smem<D, B>() ? dkv_smem<D, B>() : dq_smem<D, B>();
+    return launch(attn_simt_bwd_kernel<T, D, B>, kb + rb, smem, s, keys, rows, (int)kb);
 }
 
 }  // namespace
@@ -523,27 +542,14 @@ cudaError_t launch(K *kernel, const Args &a, size_t smem, cudaStream_t s) {
     } while (0)
 
 cudaError_t launch_attn_simt_fwd(const Args &a, int rows, int d, int dtype, cudaStream_t s) {
-    if (rows == 16)
-        KLA_BY_TYPE(d, dtype, return launch((attn_simt_fwd_kernel<T, D, 16>), a,
-                                            (fwd_smem<D, 16>()), s));
-    KLA_BY_TYPE(d, dtype, return launch((attn_simt_fwd_kernel<T, D, 64>), a,
-                                        (fwd_smem<D, 64>()), s));
+    if (rows == 16) KLA_BY_TYPE(d, dtype, return (launch_fwd<T, D, 16>(a, s)));
+    KLA_BY_TYPE(d, dtype, return (launch_fwd<T, D, 64>(a, s)));
 }
 
-cudaError_t launch_attn_simt_dq(const Args &a, int rows, int d, int dtype, cudaStream_t s) {
-    if (rows == 16)
-        KLA_BY_TYPE(d, dtype, return launch((attn_simt_dq_kernel<T, D, 16>), a,
-                                            (dq_smem<D, 16>()), s));
-    KLA_BY_TYPE(d, dtype, return launch((attn_simt_dq_kernel<T, D, 64>), a,
-                                        (dq_smem<D, 64>()), s));
-}
-
-cudaError_t launch_attn_simt_dkv(const Args &a, int keys, int d, int dtype, cudaStream_t s) {
-    if (keys == 16)
-        KLA_BY_TYPE(d, dtype, return launch((attn_simt_dkv_kernel<T, D, 16>), a,
-                                            (dkv_smem<D, 16>()), s));
-    KLA_BY_TYPE(d, dtype, return launch((attn_simt_dkv_kernel<T, D, 64>), a,
-                                        (dkv_smem<D, 64>()), s));
+cudaError_t launch_attn_simt_bwd(const Args &keys, const Args &rows, int tile, int d, int dtype,
+                                 cudaStream_t s) {
+    if (tile == 16) KLA_BY_TYPE(d, dtype, return (launch_bwd<T, D, 16>(keys, rows, s)));
+    KLA_BY_TYPE(d, dtype, return (launch_bwd<T, D, 64>(keys, rows, s)));
 }
 
 cudaError_t launch_attn_delta(const Args &a, int d, int dtype, cudaStream_t s) {
