@@ -62,7 +62,9 @@ struct Shared {
     uint64_t q[2], q_read[2];            // Q tiles landed, and no longer read
     uint64_t s[2], p[2], o[2];           // scores ready, probabilities ready, product done
     uint64_t work[2], work_read[2];      // items published, and read
-    uint64_t turn[2], last, tail, asked, fin;
+    uint64_t turn[2];
+    uint64_t raw, zeroed;                // a ragged V tile landed, and cleaned
+    uint64_t asked, fin;
     uint4 answer;
     Work item[2];
     uint32_t tmem;
@@ -106,8 +108,8 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
             mbar_init(&sh.work_read[t], 11);     // products (2), zeroing and softmax (8)
             mbar_init(&sh.turn[t], 1);
         }
-        mbar_init(&sh.last, 1);
-        mbar_init(&sh.tail, 1);
+        mbar_init(&sh.raw, 1);
+        mbar_init(&sh.zeroed, 1);
         mbar_init(&sh.asked, 1);
         mbar_init(&sh.fin, 2);
         sh.abort = 0;
@@ -134,7 +136,8 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
         attn::fewer_registers<88>();
         if (warp == 9) {
             // ------------------------------------------- items and their loads
-            int j = 0, used[2] = {0, 0}, block = blockIdx.x;
+            int j = 0, used[2] = {0, 0}, raws = 0, block = blockIdx.x;
+            uint32_t raw_slots = 0;     // slots whose last load went by way of sh.raw
             bool ok = true;
             for (int m = 0; ok; ++m) {
                 // publish item m (the consumers may be an item behind)
@@ -200,14 +203,23 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                         const int slot = j % C::SLOTS, use = j / C::SLOTS;
                         ok = use == 0 || wait(&sh.empty[slot], use - 1);
                         if (!ok) break;
+                        // a last V tile that holds a neighbour's rows goes to
+                        // the zeroing warp, which completes the slot; one at a time
+                        uint64_t *bar = &sh.full[slot];
+                        if (i == 2 * nb - 1 && w.b1 * kTile > w.lk) {
+                            bar = &sh.raw;
+                            ok = raws == 0 || wait(&sh.zeroed, raws - 1);
+                            if (!ok) break;
+                            ++raws;
+                        }
+                        raw_slots = (raw_slots & ~(1u << slot)) | (bar == &sh.raw ? 1u << slot : 0u);
                         ++j;
-                        mbar_expect_tx(&sh.full[slot], C::TILE);
+                        mbar_expect_tx(bar, C::TILE);
                         const int row = w.k0 + (w.b0 + i / 2) * kTile;
                         for (int c = 0; c < C::SLABS; ++c)
                             tma_load_3d(sKV + slot * C::TILE + c * kSlab, i % 2 ? &maps.v : &maps.k,
-                                        &sh.full[slot], c * 64, w.head, row);
+                                        bar, c * 64, w.head, row);
                     }
-                    if (ok && nb > 0 && w.b1 * kTile > w.lk) mbar_arrive(&sh.last);
                     if (asked) {
                         ok = mbar_wait(&sh.asked, (uint32_t)(m & 1)) && ok;
                         block = attn::answered_block(&sh.answer);
@@ -219,13 +231,15 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
             if (!ok && lane == 0) {    // given up: the copies in flight land before the CTA leaves
                 give_up();
                 for (int i = max(0, j - C::SLOTS); i < j; ++i)
-                    (void)mbar_wait(&sh.full[i % C::SLOTS], (uint32_t)((i / C::SLOTS) & 1));
+                    if (!(raw_slots >> (i % C::SLOTS) & 1u))
+                        (void)mbar_wait(&sh.full[i % C::SLOTS], (uint32_t)((i / C::SLOTS) & 1));
+                if (raws > 0) (void)mbar_wait(&sh.raw, (uint32_t)((raws - 1) & 1));
                 for (int t = 0; t < 2; ++t)
                     if (used[t] > 0) (void)mbar_wait(&sh.q[t], (uint32_t)((used[t] - 1) & 1));
             }
         } else if (warp == 11) {
             // -------------- rows of a last V tile that are a neighbour's: zeroed
-            int j = 0, tails = 0;
+            int j = 0, raws = 0;
             bool ok = true;
             for (int m = 0; ok; ++m) {
                 ok = wait_warp(&sh.work[m & 1], m / 2);
@@ -237,12 +251,13 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                 j += 2 * (w.b1 - w.b0);
                 const int valid = w.lk - (w.b1 - 1) * kTile, slot = (j - 1) % C::SLOTS;
                 if (w.b1 == w.b0 || valid >= kTile) continue;
-                // asked for, so that the slot's barrier is in that load's phase
-                ok = wait_warp(&sh.last, tails++) &&
-                     wait_warp(&sh.full[slot], (j - 1) / C::SLOTS);
+                ok = wait_warp(&sh.raw, raws++);
                 if (!ok) break;
                 attn::zero_rows<C::SLABS>(sKV + slot * C::TILE, valid, lane);
-                if (lane == 0) mbar_arrive(&sh.tail);
+                if (lane == 0) {
+                    mbar_arrive(&sh.full[slot]);
+                    mbar_arrive(&sh.zeroed);
+                }
             }
             if (!ok) give_up();
         } else if (warp == 8 || warp == 10) {
@@ -267,7 +282,7 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                              attn::kdesc(aKV + (j % C::SLOTS) * C::TILE, ks), id_s, ks > 0);
             };
             if (lane == 0) {
-                int j = 0, used = 0, step = 0, tails = 0, turns = 0;
+                int j = 0, used = 0, step = 0, turns = 0;
                 bool ok = true;
                 for (int m = 0; ok; ++m) {
                     ok = wait(&sh.work[m & 1], m / 2);
@@ -289,11 +304,9 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                     } else if (ok) {
                         mbar_arrive(&sh.empty[j % C::SLOTS]);
                     }
-                    // the last V tile may hold a neighbour's rows: they are zeroed first
-                    const bool ragged = w.b1 * kTile > w.lk;
                     for (int n = 0; ok && n < nb; ++n) {
                         const int jv = j + 2 * n + 1, jk = j + 2 * n + 2, sv = jv % C::SLOTS;
-                        ok = landed(jv) && (n + 1 < nb ? landed(jk) : !ragged || wait(&sh.tail, tails));
+                        ok = landed(jv) && (n + 1 == nb || landed(jk));
                         if (!ok) break;
                         if (n >= mine) {       // the other tile's keys
                             mbar_arrive(&sh.empty[sv]);
@@ -329,7 +342,6 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                         }
                     }
                     j += 2 * nb;
-                    tails += ragged;
                 }
                 if (!ok) give_up();
                 // every product issued has completed before the tensor memory is released

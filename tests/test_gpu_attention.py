@@ -154,6 +154,28 @@ def test_packed(case, dtype):
         aq, ak = aq + a, ak + b
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_short_sequences(d):
+    """Items of one key tile one after another, every one with a neighbour's
+    rows in its last tile: the loads run several items ahead of the products."""
+    g = torch.Generator().manual_seed(11)
+    lens = torch.randint(1, 41, (1500,), generator=g).tolist()
+    hq, hk = 8, 4
+    data = [_inputs(n, n, hq, hk, d, BF16, seed=i) for i, n in enumerate(lens)]
+    q, k, v, go = (torch.cat(x).cuda() for x in zip(*data))
+    cu = torch.tensor([0] + lens).cumsum(0).int().cuda()
+    for _ in range(3):
+        o, lse = kla.kla_attn_fwd_varlen(q, k, v, cu, check_status=True)
+        grads = kla.kla_attn_bwd_varlen(q, k, v, o, lse, go, cu, check_status=True)
+    at = 0
+    for i, n in enumerate(lens):
+        if i % 37 == 0:
+            ref = _ref(*data[i], 1 / math.sqrt(d))
+            for what, got in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
+                _check(got[at:at + n], ref[what], what)
+        at += n
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("tq", [1, 3, 150])
 def test_padded_cache_with_anything_behind_its_lengths(dtype, tq):
