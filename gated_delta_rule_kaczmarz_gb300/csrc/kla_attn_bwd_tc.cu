@@ -19,6 +19,10 @@
 // issues the products, the loads (TMA) and, for key tiles, the rows' lse and
 // delta.  p and ds are rounded to bf16 as operands; sums are fp32.
 //
+// There is a block per tile, key tiles first; a running CTA takes over blocks
+// that have not started, so that an item's loads and first scores run under the
+// end of the one before (its start and end cost about 6 us, a step 1.5 to 2).
+//
 // Order of the products.  A key tile's next scores do not wait for dS: P is in
 // registers for that step, and S^T's columns are free after dV.  So the dS step
 // runs under dV and S^T, the exponentials under dK and dP^T:
@@ -48,13 +52,27 @@ using attn::Seq;
 
 constexpr int kThreads = 384;            // 8 softmax warps, products, loads, row statistics
 
+// An item: one tile of keys or of rows, and the tiles of the other side.
+struct Work {
+    int key_tile;
+    int q0, k0, lq, lk;                  // the sequence: first rows and lengths
+    int at, head;                        // first key or token of the tile; key head
+    int first, n;                        // tiles of the other side: the first, how many
+    int valid;                           // rows of the last of them that are the sequence's own
+    int any;                             // 0: there is no more work
+};
+
 struct Shared {
-    uint64_t fix;                        // the CTA's own tiles landed
     uint64_t full[5], empty[5];          // ring slots
+    uint64_t fix, fix_read;              // the item's own tiles landed, and no longer read
     uint64_t s, dp[2];                   // scores and dP ready
     uint64_t s_read, p, ds[2];           // scores read; P and dS in place
     uint64_t st[2], read[2];             // row statistics ready, and read
-    uint64_t tail[2], fin;
+    uint64_t raw[2], zeroed;             // last tiles with a neighbour's rows landed, and cleaned
+    uint64_t fin, drained;               // an item's products complete, its sums read
+    uint64_t work[2], work_read[2], asked, done;
+    uint4 answer;
+    Work item[2];
     uint32_t tmem;
     volatile int abort;
 };
@@ -66,10 +84,10 @@ struct Cfg {
     // seven tiles, the row statistics of two, the barriers; what is left of a
     // block's 227 KB covers the alignment
     static constexpr size_t STATS = (size_t)TILE * 7, BARS = STATS + 2048;
-    static constexpr size_t USED = BARS + 256;
-    static constexpr size_t SMEM = USED + 768;
+    static constexpr size_t USED = BARS + 512;
+    static constexpr size_t SMEM = USED + 512;
     static constexpr uint32_t TM_COLS = 512;
-    static_assert(sizeof(Shared) <= 256 && SMEM <= 227 * 1024, "shared memory");
+    static_assert(sizeof(Shared) <= 512 && SMEM <= 227 * 1024, "shared memory");
 };
 
 struct Maps {
@@ -128,49 +146,38 @@ __device__ __forceinline__ void store_row(uint32_t tmem, __nv_bfloat16 *dst, flo
 template <int D>
 struct Cta {
     using C = Cfg<D>;
-    const Args &a;
+    const Args &ak, &ar;      // key tiles and row tiles
     const Maps &maps;
+    const int key_blocks;
     Shared &sh;
-    unsigned char *base;      // tiles 0, 1: the CTA's own; 2 to 4: ring X; 5, 6: ring Y
-    uint32_t tb;
-    int warp, lane;
-    bool key_tile;
-    Item it;
-    Seq seq;
-    int TT, R, shift;         // tokens and rows of a row tile; lk - lq
-    int j0, tok0;             // key tile: its first key; row tile: its first token
-    int first, last, n;       // tiles of the other side: first .. last, how many
-    int valid;                // rows of the last of them that are the sequence's own
+    unsigned char *base;      // tiles 0, 1: the item's own; 2 to 4: ring X; 5, 6: ring Y
+    const uint32_t tb;
+    const int warp, lane;
+    const int TT, R;          // tokens and rows of a row tile
     float *stats;             // key tiles: [2][-lse log2 e, -delta][128]
 
     // Tensor memory of a key tile: S^T, dP^T, dV, dK; of a row tile: S, dP twice, dQ.
     static constexpr uint32_t TM_S = 0, TM_P = 128, TM_V = 256, TM_K = 256 + D, TM_Q = 384;
 
-    __device__ Cta(const Args &a_, const Maps &maps_, Shared &sh_, unsigned char *base_, int warp_,
-                   int lane_, const Item &it_, const Seq &seq_, bool key_tile_)
-        : a(a_), maps(maps_), sh(sh_), base(base_), tb(sh_.tmem), warp(warp_), lane(lane_),
-          key_tile(key_tile_), it(it_), seq(seq_) {
-        TT = maps.tokens;
-        R = TT * a.G;
-        shift = seq.lk - seq.lq;
-        j0 = it.tile * kTile;
-        tok0 = it.tile * TT;
-        stats = reinterpret_cast<float *>(base + C::STATS);
-        if (key_tile) {
-            first = max(0, j0 - shift) / TT;
-            last = (seq.lq + TT - 1) / TT;
-            valid = min((seq.lq - (last - 1) * TT) * a.G, R);
-        } else {
-            const int seen = min(tok0 + TT, seq.lq) + shift;
-            first = 0;
-            last = seen > 0 ? (seen + kTile - 1) / kTile : 0;
-            valid = min(seq.lk - (last - 1) * kTile, kTile);
+    // Where an item begins in the barriers' phases: steps of all items, of key
+    // and of row tiles, items with steps.  Every role counts the same.
+    struct Count {
+        int g = 0, key = 0, row = 0, items = 0;
+        __device__ void add(const Work &w) {
+            g += w.n;
+            (w.key_tile ? key : row) += w.n;
+            items += w.n > 0;
         }
-        n = max(0, last - first);
-    }
+    };
+
+    __device__ Cta(const Args &ak_, const Args &ar_, const Maps &maps_, int key_blocks_,
+                   Shared &sh_, unsigned char *base_, int warp_, int lane_)
+        : ak(ak_), ar(ar_), maps(maps_), key_blocks(key_blocks_), sh(sh_), base(base_),
+          tb(sh_.tmem), warp(warp_), lane(lane_), TT(maps_.tokens), R(maps_.tokens * ar_.G),
+          stats(reinterpret_cast<float *>(base_ + C::STATS)) {}
     __device__ void give_up() {
         sh.abort = 1;
-        *a.status = kDevTimeout;
+        *ar.status = kDevTimeout;
     }
     // One lane's wait, and a warp's.
     __device__ bool wait(uint64_t *bar, int phase) {
@@ -179,73 +186,172 @@ struct Cta {
     __device__ bool wait_warp(uint64_t *bar, int phase) {
         return __all_sync(0xffffffffu, wait(bar, phase));
     }
+    // The m-th item for a reader: a lane, or a warp.
+    __device__ bool item(int m, Work &w) {
+        if (!wait(&sh.work[m & 1], m / 2)) return false;
+        w = sh.item[m & 1];
+        mbar_arrive(&sh.work_read[m & 1]);
+        return true;
+    }
+    __device__ bool item_warp(int m, Work &w) {
+        if (!wait_warp(&sh.work[m & 1], m / 2)) return false;
+        w = sh.item[m & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.work_read[m & 1]);
+        return true;
+    }
     __device__ uint32_t addr(int tile) { return smem_u32(base + tile * C::TILE); }
     // K step ks of an operand in the columns of the product it came from, 32
     // columns in each half (a warpgroup's own).
     static __device__ uint32_t operand(uint32_t col, int ks) {
         return col + 64u * (ks / 4) + 8u * (ks % 4);
     }
-
-    // Ring slots of the i-th tile of the other side: Q (key tile) or K in X, dO
-    // or V in Y.  Those of the last tile's rows that are a neighbour's are
-    // zeroed before they are summed over.
-    static __device__ int slot_x(int i) { return i % 3; }
-    static __device__ int slot_y(int i) { return 3 + i % 2; }
-    __device__ bool ragged() const { return valid < (key_tile ? R : kTile); }
-    __device__ bool landed_x(int i) {
-        return wait(&sh.full[slot_x(i)], i / 3) &&
-               (i < n - 1 || !ragged() || wait(&sh.tail[0], 0));
+    // Ring slots of step g of all items: Q (key tile) or K in X, dO or V in Y.
+    static __device__ int slot_x(int g) { return g % 3; }
+    static __device__ int slot_y(int g) { return 3 + g % 2; }
+    __device__ bool landed_x(int g) { return wait(&sh.full[slot_x(g)], g / 3); }
+    __device__ bool landed_y(int g) { return wait(&sh.full[slot_y(g)], g / 2); }
+    // The last tile of the other side holds rows that are a neighbour's: they
+    // are zeroed before they are summed over.
+    __device__ bool ragged(const Work &w) const {
+        return w.n > 0 && w.valid < (w.key_tile ? R : kTile);
     }
-    __device__ bool landed_y(int i) {
-        return wait(&sh.full[slot_y(i)], i / 2) &&
-               (i < n - 1 || !ragged() || !key_tile || wait(&sh.tail[1], 0));
+
+    // ---------------------------------------------------------- items and their loads
+    __device__ Work decode(int block) {
+        Work w{};
+        if (block < 0) return w;
+        w.key_tile = block < key_blocks;
+        const Args &a = w.key_tile ? ak : ar;
+        Item it;
+        if (!attn::item_of(a, w.key_tile ? block : block - key_blocks, !w.key_tile, it)) return w;
+        const Seq seq = attn::sequence(a, it.seq);
+        const int shift = seq.lk - seq.lq;
+        w.q0 = (int)seq.q0; w.k0 = (int)seq.k0; w.lq = seq.lq; w.lk = seq.lk;
+        w.head = it.head;
+        int last;
+        if (w.key_tile) {
+            w.at = it.tile * kTile;
+            w.first = max(0, w.at - shift) / TT;
+            last = (seq.lq + TT - 1) / TT;
+            w.valid = min((seq.lq - (last - 1) * TT) * a.G, R);
+        } else {
+            w.at = it.tile * TT;
+            const int seen = min(w.at + TT, seq.lq) + shift;
+            last = seen > 0 ? (seen + kTile - 1) / kTile : 0;
+            w.valid = min(seq.lk - (last - 1) * kTile, kTile);
+        }
+        w.n = max(0, last - w.first);
+        w.any = 1;
+        return w;
     }
     __device__ void load(int tile, const CUtensorMap *m, uint64_t *bar, int y, int z) {
         for (int c = 0; c < C::SLABS; ++c)
             tma_load_3d(base + tile * C::TILE + c * kSlab, m, bar, c * 64, y, z);
     }
     __device__ void loads() {
-        bool ok = true;
-        if (lane == 0) {
-            const uint32_t rows = (uint32_t)R * 128u * C::SLABS, keys = C::TILE;
-            const int hq = it.head * a.G, hk = it.head;
-            const int q0 = (int)seq.q0, k0 = (int)seq.k0;
-            mbar_expect_tx(&sh.fix, 2 * (key_tile ? keys : rows));
-            load(0, key_tile ? &maps.k : &maps.q, &sh.fix, key_tile ? hk : hq,
-                 key_tile ? k0 + j0 : q0 + tok0);
-            load(1, key_tile ? &maps.v : &maps.go, &sh.fix, key_tile ? hk : hq,
-                 key_tile ? k0 + j0 : q0 + tok0);
-            const CUtensorMap *mx = key_tile ? &maps.q : &maps.k, *my = key_tile ? &maps.go : &maps.v;
-            int nx = 0, ny = 0;           // tiles asked for
-            const auto next = [&](bool y, int i) {
-                const int slot = y ? slot_y(i) : slot_x(i), use = y ? i / 2 : i / 3;
-                ok = use == 0 || wait(&sh.empty[slot], use - 1);
-                if (!ok) return;
-                mbar_expect_tx(&sh.full[slot], key_tile ? rows : keys);
-                load(2 + slot, y ? my : mx, &sh.full[slot], key_tile ? hq : hk,
-                     key_tile ? q0 + (first + i) * TT : k0 + i * kTile);
-                ++(y ? ny : nx);
-            };
-            next(false, 0);
-            for (int i = 0; ok && i < n; ++i) {      // in the order of their first use
-                next(true, i);
-                if (ok && i + 1 < n) next(false, i + 1);
+        const uint32_t row_bytes = (uint32_t)R * 128u * C::SLABS, key_bytes = C::TILE;
+        Count at;
+        int block = blockIdx.x, raws = 0, raws_y = 0, fixed = 0, gx = 0, gy = 0;
+        uint32_t raw_slots = 0;              // slots whose last load went by way of sh.raw
+        bool ok = true, rows_before = false;
+        for (int m = 0; ok; ++m) {
+            Work w{};
+            if (lane == 0) {
+                w = decode(block);
+                ok = m < 2 || wait(&sh.work_read[m & 1], m / 2 - 1);
+                sh.item[m & 1] = w;
+                mbar_arrive(&sh.work[m & 1]);
             }
-            if (!ok) {     // given up: the copies in flight land before the CTA leaves
-                give_up();
-                for (int i = max(0, nx - 3); i < nx; ++i)
-                    (void)mbar_wait(&sh.full[slot_x(i)], (uint32_t)((i / 3) & 1));
-                for (int i = max(0, ny - 2); i < ny; ++i)
-                    (void)mbar_wait(&sh.full[slot_y(i)], (uint32_t)((i / 2) & 1));
-                (void)mbar_wait(&sh.fix, 0u);
+            ok = __all_sync(0xffffffffu, ok);
+            __syncwarp();
+            w = sh.item[m & 1];
+            if (!ok || !w.any) break;
+            // Rows that no copy of a row tile fills (the group does not divide
+            // 128) were zeroed at the start.  Key tiles come before row tiles;
+            // if one came after, the key rows that are in the slots by then go.
+            if (w.key_tile && rows_before && R < kTile) {
+                for (int i = 0; i < 3 && i < at.g; ++i)
+                    ok = ok && wait_warp(&sh.empty[slot_x(at.g - 1 - i)], (at.g - 1 - i) / 3);
+                for (int i = 0; i < 2 && i < at.g; ++i)
+                    ok = ok && wait_warp(&sh.empty[slot_y(at.g - 1 - i)], (at.g - 1 - i) / 2);
+                for (int i = 0; ok && i < 5; ++i)
+                    attn::zero_rows<C::SLABS>(base + (2 + i) * C::TILE, R, lane);
             }
+            rows_before = !w.key_tile;
+            if (lane == 0) {
+                const bool key = w.key_tile;
+                const int hq = w.head * ar.G, hk = w.head;
+                const CUtensorMap *mx = key ? &maps.q : &maps.k, *my = key ? &maps.go : &maps.v;
+                // a last tile with a neighbour's rows goes to the cleaning warp,
+                // which completes the slot; one item's at a time
+                const auto next = [&](bool y, int i) {
+                    const int g = at.g + i, slot = y ? slot_y(g) : slot_x(g), use = y ? g / 2 : g / 3;
+                    ok = use == 0 || wait(&sh.empty[slot], use - 1);
+                    uint64_t *bar = &sh.full[slot];
+                    const bool raw = i == w.n - 1 && ragged(w) && (key || !y);
+                    if (ok && raw) {
+                        if (!y) {
+                            ok = raws == 0 || wait(&sh.zeroed, raws - 1);
+                            raws += ok;
+                        } else {
+                            ++raws_y;
+                        }
+                        bar = &sh.raw[y];
+                    }
+                    if (!ok) return;
+                    raw_slots = (raw_slots & ~(1u << slot)) | ((raw ? 1u : 0u) << slot);
+                    mbar_expect_tx(bar, key ? row_bytes : key_bytes);
+                    load(2 + slot, y ? my : mx, bar, key ? hq : hk,
+                         key ? w.q0 + (w.first + i) * TT : w.k0 + i * kTile);
+                    ++(y ? gy : gx);
+                };
+                // In the order of their first use; the own tiles after the first
+                // of each ring, because the item before reads its own until its
+                // last scores.  The next block is asked for a few tiles before
+                // the end: earlier, a CTA would hold what another could start.
+                bool asked = false;
+                for (int i = 0; ok && i <= w.n; ++i) {
+                    if (i == max(0, w.n - 4)) {
+                        mbar_expect_tx(&sh.asked, 16);
+                        attn::ask_block(&sh.answer, &sh.asked);
+                        asked = true;
+                    }
+                    if (i == w.n) break;
+                    if (i == 0) next(false, 0);
+                    if (ok) next(true, i);
+                    if (ok && i == 0) {
+                        ok = fixed == 0 || wait(&sh.fix_read, fixed - 1);
+                        if (!ok) break;
+                        ++fixed;
+                        mbar_expect_tx(&sh.fix, 2 * (key ? key_bytes : row_bytes));
+                        load(0, key ? &maps.k : &maps.q, &sh.fix, key ? hk : hq,
+                             (key ? w.k0 : w.q0) + w.at);
+                        load(1, key ? &maps.v : &maps.go, &sh.fix, key ? hk : hq,
+                             (key ? w.k0 : w.q0) + w.at);
+                    }
+                    if (ok && i + 1 < w.n) next(false, i + 1);
+                }
+                if (asked) {
+                    ok = mbar_wait(&sh.asked, (uint32_t)(m & 1)) && ok;
+                    block = attn::answered_block(&sh.answer);
+                    fence_async_smem();        // read before the next answer is written
+                }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            at.add(w);
         }
-        if (!__all_sync(0xffffffffu, ok) || !ragged()) return;
-        for (int y = 0; y < (key_tile ? 2 : 1); ++y) {
-            const int slot = y ? slot_y(n - 1) : slot_x(n - 1), use = y ? (n - 1) / 2 : (n - 1) / 3;
-            (void)mbar_wait(&sh.full[slot], (uint32_t)(use & 1));
-            attn::zero_rows<C::SLABS>(base + (2 + slot) * C::TILE, valid, lane);
-            if (lane == 0) mbar_arrive(&sh.tail[y]);
+        if (!ok && lane == 0) {    // given up: the copies in flight land before the CTA leaves
+            give_up();
+            for (int i = max(0, gx - 3); i < gx; ++i)
+                if (!(raw_slots >> slot_x(i) & 1u))
+                    (void)mbar_wait(&sh.full[slot_x(i)], (uint32_t)((i / 3) & 1));
+            for (int i = max(0, gy - 2); i < gy; ++i)
+                if (!(raw_slots >> slot_y(i) & 1u))
+                    (void)mbar_wait(&sh.full[slot_y(i)], (uint32_t)((i / 2) & 1));
+            if (raws > 0) (void)mbar_wait(&sh.raw[0], (uint32_t)((raws - 1) & 1));
+            if (raws_y > 0) (void)mbar_wait(&sh.raw[1], (uint32_t)((raws_y - 1) & 1));
+            if (fixed > 0) (void)mbar_wait(&sh.fix, (uint32_t)((fixed - 1) & 1));
         }
     }
 
@@ -269,133 +375,184 @@ struct Cta {
             mma_bf16_ts(tb + out, tb + operand(from, ks), attn::mdesc(y, ks), id, acc || ks > 0);
         mma_commit(&sh.empty[slot]);
     }
-    __device__ void finish(bool ok) {
-        if (!ok) give_up();
-        mma_commit(&sh.fin);
-        (void)mbar_wait(&sh.fin, 0u);
+    // The sums of the item before are read, and with them all it had in tensor
+    // memory is free.
+    __device__ bool drained(const Count &at) {
+        return at.items == 0 || wait(&sh.drained, at.items - 1);
     }
     // S^T and dV of a key tile.
-    __device__ void key_products_v() {
-        bool ok = wait(&sh.fix, 0) && landed_x(0);
-        if (ok) product(0, slot_x(0), TM_S, &sh.s);
-        for (int i = 0; ok && i < n; ++i) {
-            ok = landed_y(i) && wait(&sh.p, i);
+    __device__ bool key_products_v(const Work &w, const Count &at) {
+        bool ok = wait(&sh.fix, at.items) && landed_x(at.g);
+        for (int i = 0; ok && i < w.n; ++i) {
+            const int g = at.g + i;
+            if (i == 0) {
+                product(0, slot_x(g), TM_S, &sh.s);
+                if (w.n == 1) mma_commit(&sh.fix_read);
+                ok = drained(at);
+            }
+            ok = ok && landed_y(g) && wait(&sh.p, at.key + i);
             if (!ok) break;
-            gather(TM_S, slot_y(i), TM_V, i > 0);
-            if (i + 1 == n) break;
-            ok = landed_x(i + 1);
-            if (ok) product(0, slot_x(i + 1), TM_S, &sh.s);
+            gather(TM_S, slot_y(g), TM_V, i > 0);
+            if (i + 1 == w.n) break;
+            ok = landed_x(g + 1);
+            if (!ok) break;
+            product(0, slot_x(g + 1), TM_S, &sh.s);
+            if (i + 2 == w.n) mma_commit(&sh.fix_read);
         }
-        finish(ok);
+        if (ok) mma_commit(&sh.fin);
+        return ok;
     }
     // dP^T and dK of a key tile.
-    __device__ void key_products_k() {
-        bool ok = wait(&sh.fix, 0) && landed_y(0);
+    __device__ bool key_products_k(const Work &w, const Count &at) {
+        bool ok = wait(&sh.fix, at.items) && landed_y(at.g) && drained(at);
         if (ok) {
-            product(1, slot_y(0), TM_P, &sh.dp[0]);
-            mma_commit(&sh.empty[slot_y(0)]);
+            product(1, slot_y(at.g), TM_P, &sh.dp[at.g & 1]);
+            mma_commit(&sh.empty[slot_y(at.g)]);
+            if (w.n == 1) mma_commit(&sh.fix_read);
         }
-        for (int i = 0; ok && i < n; ++i) {
-            ok = wait(&sh.ds[i & 1], i / 2);
+        for (int i = 0; ok && i < w.n; ++i) {
+            const int g = at.g + i;
+            ok = wait(&sh.ds[g & 1], g / 2);
             if (!ok) break;
-            gather(TM_P, slot_x(i), TM_K, i > 0);
-            if (i + 1 == n) break;
-            ok = landed_y(i + 1);
+            gather(TM_P, slot_x(g), TM_K, i > 0);
+            if (i + 1 == w.n) break;
+            ok = landed_y(g + 1);
             if (!ok) break;
-            product(1, slot_y(i + 1), TM_P, &sh.dp[0]);
-            mma_commit(&sh.empty[slot_y(i + 1)]);
+            product(1, slot_y(g + 1), TM_P, &sh.dp[(g + 1) & 1]);
+            mma_commit(&sh.empty[slot_y(g + 1)]);
+            if (i + 2 == w.n) mma_commit(&sh.fix_read);
         }
-        finish(ok);
+        if (ok) mma_commit(&sh.fin);
+        return ok;
     }
-    // All of a row tile.
-    __device__ void row_products() {
-        bool ok = wait(&sh.fix, 0);
-        for (int i = 0; ok && i <= n; ++i) {
-            if (i < n) {
-                ok = landed_x(i) && (i == 0 || wait(&sh.s_read, i - 1));
+    // All of a row tile.  What both warps release at a key tile is released
+    // twice here.
+    __device__ bool row_products(const Work &w, const Count &at) {
+        bool ok = wait(&sh.fix, at.items);
+        for (int i = 0; ok && i <= w.n; ++i) {
+            const int g = at.g + i;
+            if (i < w.n) {
+                ok = landed_x(g) && (i == 0 || wait(&sh.s_read, at.row + i - 1));
                 if (!ok) break;
-                product(0, slot_x(i), TM_S, &sh.s);
-                ok = landed_y(i);
+                product(0, slot_x(g), TM_S, &sh.s);
+                ok = landed_y(g) && (i > 0 || drained(at));
                 if (!ok) break;
-                product(1, slot_y(i), TM_P + 128u * (i & 1), &sh.dp[i & 1]);
-                mma_commit(&sh.empty[slot_y(i)]);
+                product(1, slot_y(g), TM_P + 128u * (g & 1), &sh.dp[g & 1]);
+                mma_commit(&sh.empty[slot_y(g)]);
+                mma_commit(&sh.empty[slot_y(g)]);
+                if (i + 1 == w.n) {
+                    mma_commit(&sh.fix_read);
+                    mma_commit(&sh.fix_read);
+                }
             }
             if (i > 0) {
-                ok = wait(&sh.ds[(i - 1) & 1], (i - 1) / 2);
-                if (ok) gather(TM_P + 128u * ((i - 1) & 1), slot_x(i - 1), TM_Q, i > 1);
+                ok = wait(&sh.ds[(g - 1) & 1], (g - 1) / 2);
+                if (ok) gather(TM_P + 128u * ((g - 1) & 1), slot_x(g - 1), TM_Q, i > 1);
             }
         }
-        finish(ok);
+        if (ok) mma_commit(&sh.fin);
+        return ok && wait(&sh.s_read, at.row + w.n - 1);
+    }
+    // One lane of warp 8 (second = false) and of warp 11.
+    __device__ void products(bool second) {
+        Count at;
+        bool ok = true;
+        for (int m = 0; ok; ++m) {
+            Work w;
+            ok = item(m, w);
+            if (!ok || !w.any) break;
+            if (w.n > 0) {
+                if (w.key_tile) {
+                    ok = second ? key_products_k(w, at) : key_products_v(w, at);
+                } else if (!second) {
+                    ok = row_products(w, at);
+                } else {
+                    // not needed; it stays with the item, so that the barriers
+                    // that it waits on next are in the phase before
+                    mbar_arrive(&sh.fin);
+                    ok = wait(&sh.fin, at.items);
+                }
+            }
+            at.add(w);
+        }
+        if (!ok) give_up();
     }
 
-    // Warps 8 to 11.
-    __device__ void work() {
-        if (n == 0) return;
-        if (warp == 9) {
-            loads();
-        } else if (key_tile && warp == 10) {
-            statistics();
-        } else if (warp == 8 || (key_tile && warp == 11)) {
-            if (lane == 0) {
-                if (!key_tile) row_products();
-                else if (warp == 8) key_products_v();
-                else key_products_k();
-            }
-            __syncwarp();
-        }
-    }
+    // ------------------------------------------------ row statistics, cleaning
     // -lse log2 e and -delta of a row; a row that is none, or saw no key, gets
     // p = exp2(-inf) = 0.
-    __device__ void row_statistics(int r, int tok, float &nl, float &nd) {
+    __device__ void row_statistics(const Work &w, int r, int tok, float &nl, float &nd) {
         nl = -INFINITY;
         nd = 0.f;
-        if (r < R && tok < seq.lq) {
-            const long long at = (seq.q0 + tok) * a.Hq + it.head * a.G + r % a.G;
-            const float l = a.lse_in[at];
+        if (r < R && tok < w.lq) {
+            const long long at = (long long)(w.q0 + tok) * ar.Hq + w.head * ar.G + r % ar.G;
+            const float l = ar.lse_in[at];
             nl = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
-            nd = -a.delta[at];
+            nd = -ar.delta[at];
         }
     }
     __device__ void statistics() {
-        for (int i = 0; i < n; ++i) {
-            float nl[4], nd[4];
+        Count at;
+        int raws[2] = {0, 0};
+        bool ok = true;
+        for (int m = 0; ok; ++m) {
+            Work w;
+            ok = item_warp(m, w);
+            if (!ok || !w.any) break;
+            for (int i = 0; ok && w.key_tile && i < w.n; ++i) {
+                const int g = at.key + i;
+                float nl[4], nd[4];
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                const int r = lane + 32 * z;
-                row_statistics(r, (first + i) * TT + r / a.G, nl[z], nd[z]);
-            }
-            if (i >= 2 && !wait_warp(&sh.read[i & 1], i / 2 - 1)) break;
-            float *dst = stats + (i & 1) * 256;
+                for (int z = 0; z < 4; ++z) {
+                    const int r = lane + 32 * z;
+                    row_statistics(w, r, (w.first + i) * TT + r / ar.G, nl[z], nd[z]);
+                }
+                ok = g < 2 || wait_warp(&sh.read[g & 1], g / 2 - 1);
+                if (!ok) break;
+                float *dst = stats + (g & 1) * 256;
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                dst[lane + 32 * z] = nl[z];
-                dst[128 + lane + 32 * z] = nd[z];
+                for (int z = 0; z < 4; ++z) {
+                    dst[lane + 32 * z] = nl[z];
+                    dst[128 + lane + 32 * z] = nd[z];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.st[g & 1]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.st[i & 1]);
+            if (ok && ragged(w)) {
+                const int g = at.g + w.n - 1;
+                for (int y = 0; ok && y < (w.key_tile ? 2 : 1); ++y) {
+                    const int slot = y ? slot_y(g) : slot_x(g);
+                    ok = wait_warp(&sh.raw[y], raws[y]++);
+                    if (!ok) break;
+                    attn::zero_rows<C::SLABS>(base + (2 + slot) * C::TILE, w.valid, lane);
+                    if (lane == 0) mbar_arrive(&sh.full[slot]);
+                }
+                if (ok && lane == 0) mbar_arrive(&sh.zeroed);
+            }
+            at.add(w);
         }
+        if (!ok) give_up();
     }
 
     // ------------------------------------------------------- softmax, warps 0 to 7
-    __device__ void key_softmax() {
-        const int half = warp / 4, w = warp % 4, key = j0 + 32 * w + lane;
-        const uint32_t lanes = tb + ((uint32_t)(32 * w) << 16);
+    __device__ bool key_softmax(const Work &w, const Count &at) {
+        const int half = warp / 4, key = w.at + 32 * (warp % 4) + lane;
+        const int shift = w.lk - w.lq;
+        const uint32_t lanes = tb + ((uint32_t)(32 * (warp % 4)) << 16);
         const uint32_t at_s = lanes + TM_S + 64u * half, at_p = lanes + TM_P + 64u * half;
-        const float c = a.scale_log2;
-        bool ok = true;
-        for (int i = 0; ok && i < n; ++i) {
+        const float c = ak.scale_log2;
+        for (int i = 0; i < w.n; ++i) {
+            const int g = at.g + i, gk = at.key + i;
             // the rows' statistics into registers ahead of the waits: the
             // products hold shared memory busy, and a read takes its time
-            const float4 *st = reinterpret_cast<const float4 *>(stats + (i & 1) * 256 + 64 * half);
-            ok = wait_warp(&sh.st[i & 1], i / 2);
-            if (!ok) break;
+            const float4 *st = reinterpret_cast<const float4 *>(stats + (gk & 1) * 256 + 64 * half);
+            if (!wait_warp(&sh.st[gk & 1], gk / 2)) return false;
             float p[64];
             {
                 float4 nl[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) nl[k] = st[k];
-                ok = wait_warp(&sh.s, i);
-                if (!ok) break;
+                if (!wait_warp(&sh.s, g)) return false;
                 tc_fence_after();
                 uint32_t x[2][32];
                 tmem_ld32(at_s, x[0]);
@@ -412,11 +569,11 @@ struct Cta {
                     for (int z = 0; z < 4; ++z) p[k + z] = attn::ex2(p[k + z]);
                 }
             }
-            const int t0 = (first + i) * TT;
-            if (t0 + shift < j0 + kTile - 1) {
+            const int t0 = (w.first + i) * TT;
+            if (t0 + shift < w.at + kTile - 1) {
                 // the rows are in the order of their tokens: those from `from`
                 // on see this key
-                const int from = min(max(key - shift - t0, 0), TT) * a.G - 64 * half;
+                const int from = min(max(key - shift - t0, 0), TT) * ak.G - 64 * half;
 #pragma unroll
                 for (int k = 0; k < 64; ++k)
                     if (k < from) p[k] = 0.f;
@@ -434,8 +591,7 @@ struct Cta {
             float4 nd[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) nd[k] = st[32 + k];
-            ok = wait_warp(&sh.dp[0], i);
-            if (!ok) break;
+            if (!wait_warp(&sh.dp[g & 1], g / 2)) return false;
             tc_fence_after();
             uint32_t x[2][32], y[32];
             tmem_ld32(at_p, x[0]);
@@ -458,36 +614,31 @@ struct Cta {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&sh.ds[i & 1]);
-                mbar_arrive(&sh.read[i & 1]);
+                mbar_arrive(&sh.ds[g & 1]);
+                mbar_arrive(&sh.read[gk & 1]);
             }
         }
-        if (n > 0) ok = ok && wait_warp(&sh.fin, 0);
-        if (!ok) {
-            give_up();
-            return;
-        }
+        if (w.n > 0 && !wait_warp(&sh.fin, at.items)) return false;
         tc_fence_after();
-        const long long at = ((seq.k0 + key) * a.Hk + it.head) * D;
+        const long long row = ((long long)(w.k0 + key) * ak.Hk + w.head) * D;
         store_row<D>(lanes + (half ? TM_K : TM_V),
-                     static_cast<__nv_bfloat16 *>(half ? a.dk : a.dv) + at, half ? a.scale : 1.f,
-                     n > 0, key < seq.lk);
+                     static_cast<__nv_bfloat16 *>(half ? ak.dk : ak.dv) + row,
+                     half ? ak.scale : 1.f, w.n > 0, key < w.lk);
+        return true;
     }
-    __device__ void row_softmax() {
-        const int half = warp / 4, w = warp % 4, r = 32 * w + lane;
-        const int tok = tok0 + r / a.G;
-        const bool row = r < R && tok < seq.lq;
-        const int limit = row ? tok + shift : -1, full = tok0 + shift;
-        const long long at = (seq.q0 + tok) * a.Hq + it.head * a.G + r % a.G;
-        const uint32_t lanes = tb + ((uint32_t)(32 * w) << 16);
+    __device__ bool row_softmax(const Work &w, const Count &at) {
+        const int half = warp / 4, r = 32 * (warp % 4) + lane;
+        const int tok = w.at + r / ar.G, shift = w.lk - w.lq;
+        const bool row = r < R && tok < w.lq;
+        const int limit = row ? tok + shift : -1, full = w.at + shift;
+        const uint32_t lanes = tb + ((uint32_t)(32 * (warp % 4)) << 16);
         const uint32_t at_s = lanes + TM_S + 64u * half;
-        const float c = a.scale_log2;
+        const float c = ar.scale_log2;
         float nl, nd;
-        row_statistics(r, tok, nl, nd);
-        bool ok = true;
-        for (int i = 0; ok && i < n; ++i) {
-            ok = wait_warp(&sh.s, i);
-            if (!ok) break;
+        row_statistics(w, r, tok, nl, nd);
+        for (int i = 0; i < w.n; ++i) {
+            const int g = at.g + i;
+            if (!wait_warp(&sh.s, g)) return false;
             tc_fence_after();
             uint32_t x[2][32];
             tmem_ld32(at_s, x[0]);
@@ -505,10 +656,9 @@ struct Cta {
                 p[k] = attn::ex2(p[k]);
                 p[k + 1] = attn::ex2(p[k + 1]);
             }
-            ok = wait_warp(&sh.dp[i & 1], i / 2);
-            if (!ok) break;
+            if (!wait_warp(&sh.dp[g & 1], g / 2)) return false;
             tc_fence_after();
-            const uint32_t at_p = lanes + TM_P + 128u * (i & 1) + 64u * half;
+            const uint32_t at_p = lanes + TM_P + 128u * (g & 1) + 64u * half;
             tmem_ld32(at_p, x[0]);
             tmem_ld32(at_p + 32, x[1]);
             tmem_ld_wait();
@@ -532,18 +682,34 @@ struct Cta {
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.ds[i & 1]);
+            if (lane == 0) mbar_arrive(&sh.ds[g & 1]);
         }
-        if (n > 0) ok = ok && wait_warp(&sh.fin, 0);
-        if (!ok) {
-            give_up();
-            return;
-        }
+        if (w.n > 0 && !wait_warp(&sh.fin, at.items)) return false;
         tc_fence_after();
         // the halves of the row's features to the two warpgroups
+        const long long out = ((long long)(w.q0 + tok) * ar.Hq + w.head * ar.G + r % ar.G) * D;
         store_row<D / 2>(lanes + TM_Q + (uint32_t)(D / 2 * half),
-                         static_cast<__nv_bfloat16 *>(a.dq) + at * D + D / 2 * half, a.scale,
-                         n > 0, row);
+                         static_cast<__nv_bfloat16 *>(ar.dq) + out + D / 2 * half, ar.scale,
+                         w.n > 0, row);
+        return true;
+    }
+    __device__ void softmax() {
+        Count at;
+        bool ok = true;
+        for (int m = 0; ok; ++m) {
+            Work w;
+            ok = item_warp(m, w);
+            if (!ok || !w.any) break;
+            ok = w.key_tile ? key_softmax(w, at) : row_softmax(w, at);
+            if (!ok) break;
+            if (w.n > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.drained);
+            }
+            at.add(w);
+        }
+        if (!ok) give_up();
     }
 };
 
@@ -555,25 +721,19 @@ attn_tc_bwd_kernel(const __grid_constant__ Args ak, const __grid_constant__ Args
     extern __shared__ __align__(1024) unsigned char raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    const bool key_tile = (int)blockIdx.x < key_blocks;
-    const Args &a = key_tile ? ak : ar;
+    if (attn::rejected(ar)) return;
     if (base + C::USED > raw + C::SMEM) {      // not where the array's alignment is kept
-        *a.status = kDevTimeout;
+        *ar.status = kDevTimeout;
         return;
     }
     Shared &sh = *reinterpret_cast<Shared *>(base + C::BARS);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    Item it;
-    if (!attn::item_of(a, key_tile ? blockIdx.x : blockIdx.x - key_blocks, !key_tile, it)) return;
-    const Seq seq = attn::sequence(a, it.seq);
 
     if (threadIdx.x == 0) {
-        mbar_init(&sh.fix, 1);
 #pragma unroll
         for (int i = 0; i < 5; ++i) {
             mbar_init(&sh.full[i], 1);
-            // a key tile's dO slots are read by both warps of products
-            mbar_init(&sh.empty[i], key_tile && i >= 3 ? 2 : 1);
+            mbar_init(&sh.empty[i], i >= 3 ? 2 : 1);     // dO is read by both product warps
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -581,32 +741,51 @@ attn_tc_bwd_kernel(const __grid_constant__ Args ak, const __grid_constant__ Args
             mbar_init(&sh.ds[i], 8);
             mbar_init(&sh.st[i], 1);
             mbar_init(&sh.read[i], 8);
-            mbar_init(&sh.tail[i], 1);
+            mbar_init(&sh.raw[i], 1);
+            mbar_init(&sh.work[i], 1);
+            mbar_init(&sh.work_read[i], 11);             // products (2), statistics, softmax (8)
         }
+        mbar_init(&sh.fix, 1);
+        mbar_init(&sh.fix_read, 2);
         mbar_init(&sh.s, 1);
         mbar_init(&sh.s_read, 8);
         mbar_init(&sh.p, 8);
-        mbar_init(&sh.fin, key_tile ? 2 : 1);
+        mbar_init(&sh.zeroed, 1);
+        mbar_init(&sh.fin, 2);
+        mbar_init(&sh.drained, 8);
+        mbar_init(&sh.asked, 1);
+        mbar_init(&sh.done, 2);
         sh.abort = 0;
         fence_mbar_init();
     }
     // rows that no copy fills (the group does not divide 128) are summed over
     // by a key tile's products
-    if (key_tile && maps.tokens * a.G < kTile && warp < 5)
-        attn::zero_rows<C::SLABS>(base + (2 + warp) * C::TILE, maps.tokens * a.G, lane);
+    if (maps.tokens * ar.G < kTile && warp < 5)
+        attn::zero_rows<C::SLABS>(base + (2 + warp) * C::TILE, maps.tokens * ar.G, lane);
     if (warp == 8) tmem_alloc(&sh.tmem, C::TM_COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    Cta<D> cta(a, maps, sh, base, warp, lane, it, seq, key_tile);
+    Cta<D> cta(ak, ar, maps, key_blocks, sh, base, warp, lane);
     // Registers of a thread: 128 x 88 + 256 x 208 = 384 x 168.
     if (warp >= 8) {
         attn::fewer_registers<88>();
-        cta.work();
+        if (warp == 9) {
+            cta.loads();
+        } else if (warp == 10) {
+            cta.statistics();
+        } else {
+            if (lane == 0) {
+                cta.products(warp == 11);
+                // every product issued has completed before the tensor memory is released
+                mma_commit(&sh.done);
+                (void)mbar_wait(&sh.done, 0u);
+            }
+            __syncwarp();
+        }
     } else {
         attn::more_registers<208>();
-        if (key_tile) cta.key_softmax();
-        else cta.row_softmax();
+        cta.softmax();
     }
     tc_fence_before();
     __syncthreads();
