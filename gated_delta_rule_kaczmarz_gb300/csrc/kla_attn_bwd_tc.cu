@@ -65,7 +65,7 @@ struct Work {
 struct Shared {
     uint64_t full[5], empty[5];          // ring slots
     uint64_t fix, fix_read;              // the item's own tiles landed, and no longer read
-    uint64_t s, dp[2];                   // scores and dP ready
+    uint64_t s[2], dp[2];                // scores and dP ready
     uint64_t s_read, p, ds[2];           // scores read; P and dS in place
     uint64_t st[2], read[2];             // row statistics ready, and read
     uint64_t raw[2], zeroed;             // last tiles with a neighbour's rows landed, and cleaned
@@ -158,6 +158,7 @@ struct Cta {
 
     // Tensor memory of a key tile: S^T, dP^T, dV, dK; of a row tile: S, dP twice, dQ.
     static constexpr uint32_t TM_S = 0, TM_P = 128, TM_V = 256, TM_K = 256 + D, TM_Q = 384;
+    static constexpr uint32_t TM_S2 = 384;      // head size 64: S^T of every second step
 
     // Where an item begins in the barriers' phases: steps of all items, of key
     // and of row tiles, items with steps.  Every role counts the same.
@@ -208,9 +209,8 @@ struct Cta {
     }
     // Ring slots of step g of all items: Q (key tile) or K in X, dO or V in Y.
     static __device__ int slot_x(int g) { return g % 3; }
-    static __device__ int slot_y(int g) { return 3 + g % 2; }
-    __device__ bool landed_x(int g) { return wait(&sh.full[slot_x(g)], g / 3); }
-    __device__ bool landed_y(int g) { return wait(&sh.full[slot_y(g)], g / 2); }
+    static __device__ int slot_y(int g) { return 3 + (g & 1); }
+    __device__ bool landed_y(int g) { return wait(&sh.full[slot_y(g)], g >> 1); }
     // The last tile of the other side holds rows that are a neighbour's: they
     // are zeroed before they are summed over.
     __device__ bool ragged(const Work &w) const {
@@ -380,78 +380,96 @@ struct Cta {
     __device__ bool drained(const Count &at) {
         return at.items == 0 || wait(&sh.drained, at.items - 1);
     }
-    // S^T and dV of a key tile.
-    __device__ bool key_products_v(const Work &w, const Count &at) {
-        bool ok = wait(&sh.fix, at.items) && landed_x(at.g);
-        for (int i = 0; ok && i < w.n; ++i) {
-            const int g = at.g + i;
-            if (i == 0) {
-                product(0, slot_x(g), TM_S, &sh.s);
-                if (w.n == 1) mma_commit(&sh.fix_read);
-                ok = drained(at);
+    // Ring X walked without divisions: a step's instructions on the issuing
+    // lanes are part of its latency.
+    struct RingX {
+        int slot, use;
+        __device__ RingX(int g) : slot(g % 3), use(g / 3) {}
+        __device__ void next() {
+            if (++slot == 3) {
+                slot = 0;
+                ++use;
             }
-            ok = ok && landed_y(g) && wait(&sh.p, at.key + i);
-            if (!ok) break;
-            gather(TM_S, slot_y(g), TM_V, i > 0);
-            if (i + 1 == w.n) break;
-            ok = landed_x(g + 1);
-            if (!ok) break;
-            product(0, slot_x(g + 1), TM_S, &sh.s);
-            if (i + 2 == w.n) mma_commit(&sh.fix_read);
         }
-        if (ok) mma_commit(&sh.fin);
-        return ok;
+    };
+    // Where a key tile has S^T of its step i (and P^T after it): at head size
+    // 64 tensor memory has room for two.
+    static __device__ uint32_t key_scores(int i) { return D == 64 && (i & 1) ? TM_S2 : TM_S; }
+    // S^T and dV of a key tile.  With one S^T the next takes its columns after
+    // dV; with two it goes ahead of the wait for P^T.
+    __device__ bool key_products_v(const Work &w, const Count &at) {
+        const int n = w.n;
+        RingX x(at.g);
+        const auto scores = [&](int i) {
+            if (!wait(&sh.full[x.slot], x.use)) return false;
+            product(0, x.slot, key_scores(i), &sh.s[(at.g + i) & 1]);
+            if (i + 1 == n) mma_commit(&sh.fix_read);
+            x.next();
+            return true;
+        };
+        if (!wait(&sh.fix, at.items) || !scores(0) || !drained(at)) return false;
+        for (int i = 0; i < n; ++i) {
+            const int g = at.g + i;
+            if (D == 64 && i + 1 < n && !scores(i + 1)) return false;
+            if (!landed_y(g) || !wait(&sh.p, at.key + i)) return false;
+            gather(key_scores(i), slot_y(g), TM_V, i > 0);
+            if (D != 64 && i + 1 < n && !scores(i + 1)) return false;
+        }
+        mma_commit(&sh.fin);
+        return true;
     }
     // dP^T and dK of a key tile.
     __device__ bool key_products_k(const Work &w, const Count &at) {
-        bool ok = wait(&sh.fix, at.items) && landed_y(at.g) && drained(at);
-        if (ok) {
-            product(1, slot_y(at.g), TM_P, &sh.dp[at.g & 1]);
-            mma_commit(&sh.empty[slot_y(at.g)]);
-            if (w.n == 1) mma_commit(&sh.fix_read);
-        }
-        for (int i = 0; ok && i < w.n; ++i) {
+        const int n = w.n;
+        RingX x(at.g);
+        if (!wait(&sh.fix, at.items) || !landed_y(at.g) || !drained(at)) return false;
+        product(1, slot_y(at.g), TM_P, &sh.dp[at.g & 1]);
+        mma_commit(&sh.empty[slot_y(at.g)]);
+        if (n == 1) mma_commit(&sh.fix_read);
+        for (int i = 0;; ++i) {
             const int g = at.g + i;
-            ok = wait(&sh.ds[g & 1], g / 2);
-            if (!ok) break;
-            gather(TM_P, slot_x(g), TM_K, i > 0);
-            if (i + 1 == w.n) break;
-            ok = landed_y(g + 1);
-            if (!ok) break;
+            if (!wait(&sh.ds[g & 1], g >> 1)) return false;
+            gather(TM_P, x.slot, TM_K, i > 0);
+            if (i + 1 == n) break;
+            x.next();
+            if (!landed_y(g + 1)) return false;
             product(1, slot_y(g + 1), TM_P, &sh.dp[(g + 1) & 1]);
             mma_commit(&sh.empty[slot_y(g + 1)]);
-            if (i + 2 == w.n) mma_commit(&sh.fix_read);
+            if (i + 2 == n) mma_commit(&sh.fix_read);
         }
-        if (ok) mma_commit(&sh.fin);
-        return ok;
+        mma_commit(&sh.fin);
+        return true;
     }
     // All of a row tile.  What both warps release at a key tile is released
     // twice here.
     __device__ bool row_products(const Work &w, const Count &at) {
-        bool ok = wait(&sh.fix, at.items);
-        for (int i = 0; ok && i <= w.n; ++i) {
+        const int n = w.n;
+        RingX x(at.g), before(at.g);
+        if (!wait(&sh.fix, at.items)) return false;
+        for (int i = 0; i <= n; ++i) {
             const int g = at.g + i;
-            if (i < w.n) {
-                ok = landed_x(g) && (i == 0 || wait(&sh.s_read, at.row + i - 1));
-                if (!ok) break;
-                product(0, slot_x(g), TM_S, &sh.s);
-                ok = landed_y(g) && (i > 0 || drained(at));
-                if (!ok) break;
+            if (i < n) {
+                if (!wait(&sh.full[x.slot], x.use)) return false;
+                if (i > 0 && !wait(&sh.s_read, at.row + i - 1)) return false;
+                product(0, x.slot, TM_S, &sh.s[g & 1]);
+                x.next();
+                if (!landed_y(g) || (i == 0 && !drained(at))) return false;
                 product(1, slot_y(g), TM_P + 128u * (g & 1), &sh.dp[g & 1]);
                 mma_commit(&sh.empty[slot_y(g)]);
                 mma_commit(&sh.empty[slot_y(g)]);
-                if (i + 1 == w.n) {
+                if (i + 1 == n) {
                     mma_commit(&sh.fix_read);
                     mma_commit(&sh.fix_read);
                 }
             }
             if (i > 0) {
-                ok = wait(&sh.ds[(g - 1) & 1], (g - 1) / 2);
-                if (ok) gather(TM_P + 128u * ((g - 1) & 1), slot_x(g - 1), TM_Q, i > 1);
+                if (!wait(&sh.ds[(g - 1) & 1], (g - 1) >> 1)) return false;
+                gather(TM_P + 128u * ((g - 1) & 1), before.slot, TM_Q, i > 1);
+                before.next();
             }
         }
-        if (ok) mma_commit(&sh.fin);
-        return ok && wait(&sh.s_read, at.row + w.n - 1);
+        mma_commit(&sh.fin);
+        return wait(&sh.s_read, at.row + n - 1);
     }
     // One lane of warp 8 (second = false) and of warp 11.
     __device__ void products(bool second) {
@@ -539,20 +557,21 @@ struct Cta {
         const int half = warp / 4, key = w.at + 32 * (warp % 4) + lane;
         const int shift = w.lk - w.lq;
         const uint32_t lanes = tb + ((uint32_t)(32 * (warp % 4)) << 16);
-        const uint32_t at_s = lanes + TM_S + 64u * half, at_p = lanes + TM_P + 64u * half;
+        const uint32_t at_p = lanes + TM_P + 64u * half;
         const float c = ak.scale_log2;
         for (int i = 0; i < w.n; ++i) {
             const int g = at.g + i, gk = at.key + i;
+            const uint32_t at_s = lanes + key_scores(i) + 64u * half;
             // the rows' statistics into registers ahead of the waits: the
             // products hold shared memory busy, and a read takes its time
             const float4 *st = reinterpret_cast<const float4 *>(stats + (gk & 1) * 256 + 64 * half);
-            if (!wait_warp(&sh.st[gk & 1], gk / 2)) return false;
+            if (!wait_warp(&sh.st[gk & 1], gk >> 1)) return false;
             float p[64];
             {
                 float4 nl[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) nl[k] = st[k];
-                if (!wait_warp(&sh.s, g)) return false;
+                if (!wait_warp(&sh.s[g & 1], g >> 1)) return false;
                 tc_fence_after();
                 uint32_t x[2][32];
                 tmem_ld32(at_s, x[0]);
@@ -591,7 +610,7 @@ struct Cta {
             float4 nd[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) nd[k] = st[32 + k];
-            if (!wait_warp(&sh.dp[g & 1], g / 2)) return false;
+            if (!wait_warp(&sh.dp[g & 1], g >> 1)) return false;
             tc_fence_after();
             uint32_t x[2][32], y[32];
             tmem_ld32(at_p, x[0]);
@@ -638,7 +657,7 @@ struct Cta {
         row_statistics(w, r, tok, nl, nd);
         for (int i = 0; i < w.n; ++i) {
             const int g = at.g + i;
-            if (!wait_warp(&sh.s, g)) return false;
+            if (!wait_warp(&sh.s[g & 1], g >> 1)) return false;
             tc_fence_after();
             uint32_t x[2][32];
             tmem_ld32(at_s, x[0]);
@@ -656,7 +675,7 @@ struct Cta {
                 p[k] = attn::ex2(p[k]);
                 p[k + 1] = attn::ex2(p[k + 1]);
             }
-            if (!wait_warp(&sh.dp[g & 1], g / 2)) return false;
+            if (!wait_warp(&sh.dp[g & 1], g >> 1)) return false;
             tc_fence_after();
             const uint32_t at_p = lanes + TM_P + 128u * (g & 1) + 64u * half;
             tmem_ld32(at_p, x[0]);
@@ -737,6 +756,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Args ak, const __grid_constant__ Args
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s[i], 1);
             mbar_init(&sh.dp[i], 1);
             mbar_init(&sh.ds[i], 8);
             mbar_init(&sh.st[i], 1);
@@ -747,7 +767,6 @@ attn_tc_bwd_kernel(const __grid_constant__ Args ak, const __grid_constant__ Args
         }
         mbar_init(&sh.fix, 1);
         mbar_init(&sh.fix_read, 2);
-        mbar_init(&sh.s, 1);
         mbar_init(&sh.s_read, 8);
         mbar_init(&sh.p, 8);
         mbar_init(&sh.zeroed, 1);
