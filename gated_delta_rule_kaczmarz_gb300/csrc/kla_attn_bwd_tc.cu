@@ -497,17 +497,16 @@ struct Cta {
     }
 
     // ------------------------------------------------ row statistics, cleaning
-    // -lse log2 e and -delta of a row; a row that is none, or saw no key, gets
-    // p = exp2(-inf) = 0.
-    __device__ void row_statistics(const Work &w, int r, int tok, float &nl, float &nd) {
-        nl = -INFINITY;
-        nd = 0.f;
-        if (r < R && tok < w.lq) {
-            const long long at = (long long)(w.q0 + tok) * ar.Hq + w.head * ar.G + r % ar.G;
-            const float l = ar.lse_in[at];
-            nl = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
-            nd = -ar.delta[at];
-        }
+    // lse and delta of a row as they are, and what the exponentials and dS take:
+    // -lse log2 e and -delta; a row that is none, or saw no key, gets p =
+    // exp2(-inf) = 0.
+    __device__ float2 read_statistics(const Work &w, int r, int tok) {
+        if (r >= R || tok >= w.lq) return make_float2(-INFINITY, 0.f);
+        const long long at = (long long)(w.q0 + tok) * ar.Hq + w.head * ar.G + r % ar.G;
+        return make_float2(ar.lse_in[at], ar.delta[at]);
+    }
+    static __device__ float2 row_statistics(float2 x) {
+        return make_float2(x.x == -INFINITY ? -INFINITY : -x.x * 1.4426950408889634f, -x.y);
     }
     __device__ void statistics() {
         Count at;
@@ -517,24 +516,41 @@ struct Cta {
             Work w;
             ok = item_warp(m, w);
             if (!ok || !w.any) break;
-            for (int i = 0; ok && w.key_tile && i < w.n; ++i) {
-                const int g = at.key + i;
-                float nl[4], nd[4];
+            if (w.key_tile && w.n > 0) {
+                // read two tiles ahead: a read takes about as long as a step
+                float2 x[2][4];
+                int tok[4];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const int r = lane + 32 * z;
-                    row_statistics(w, r, (w.first + i) * TT + r / ar.G, nl[z], nd[z]);
-                }
-                ok = g < 2 || wait_warp(&sh.read[g & 1], g / 2 - 1);
-                if (!ok) break;
-                float *dst = stats + (g & 1) * 256;
+                for (int z = 0; z < 4; ++z) tok[z] = (lane + 32 * z) / ar.G;
+                const auto fetch = [&](int i, float2 (&x)[4]) {
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    dst[lane + 32 * z] = nl[z];
-                    dst[128 + lane + 32 * z] = nd[z];
+                    for (int z = 0; z < 4; ++z)
+                        x[z] = read_statistics(w, lane + 32 * z, (w.first + i) * TT + tok[z]);
+                };
+                const auto store = [&](int i, const float2 (&x)[4]) {
+                    const int g = at.key + i;
+                    if (g >= 2 && !wait_warp(&sh.read[g & 1], (g >> 1) - 1)) return false;
+                    float *dst = stats + (g & 1) * 256;
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const float2 v = row_statistics(x[z]);
+                        dst[lane + 32 * z] = v.x;
+                        dst[128 + lane + 32 * z] = v.y;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.st[g & 1]);
+                    return true;
+                };
+                fetch(0, x[0]);
+                if (w.n > 1) fetch(1, x[1]);
+                for (int i = 0; ok && i < w.n; i += 2) {
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        if (!ok || i + z >= w.n) break;
+                        ok = store(i + z, x[z]);
+                        if (i + z + 2 < w.n) fetch(i + z + 2, x[z]);
+                    }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.st[g & 1]);
             }
             if (ok && ragged(w)) {
                 const int g = at.g + w.n - 1;
@@ -653,8 +669,8 @@ struct Cta {
         const uint32_t lanes = tb + ((uint32_t)(32 * (warp % 4)) << 16);
         const uint32_t at_s = lanes + TM_S + 64u * half;
         const float c = ar.scale_log2;
-        float nl, nd;
-        row_statistics(w, r, tok, nl, nd);
+        const float2 stat = row_statistics(read_statistics(w, r, tok));
+        const float nl = stat.x, nd = stat.y;
         for (int i = 0; i < w.n; ++i) {
             const int g = at.g + i;
             if (!wait_warp(&sh.s[g & 1], g >> 1)) return false;
