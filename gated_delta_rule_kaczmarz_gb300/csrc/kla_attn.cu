@@ -179,7 +179,7 @@ void take(attn::Args &a, const Side &x, int2 *table) {
 
 // The setting stays with the device's context, so each kernel asks once per
 // device (a few kernels: a short list of what was asked for).
-cudaError_t attn_allow_smem(const void *kernel, size_t bytes) {
+cudaError_t allow_dynamic_smem(const void *kernel, size_t bytes) {
     struct Asked {
         const void *kernel;
         int device;

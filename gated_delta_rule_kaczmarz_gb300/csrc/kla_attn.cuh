@@ -120,8 +120,6 @@ struct AttnTable {
 cudaError_t launch_attn_prep(const int *cu_q, const int *cu_k, int n, int total_q, int total_k,
                              const AttnTable &t0, const AttnTable &t1, unsigned *status,
                              cudaStream_t s);
-// Lets a kernel use this much dynamic shared memory on the current device.
-cudaError_t attn_allow_smem(const void *kernel, size_t bytes);
 cudaError_t launch_attn_join(const attn::Args &a, int d, int dtype, cudaStream_t s);
 cudaError_t launch_attn_delta(const attn::Args &a, int d, int dtype, cudaStream_t s);
 

@@ -835,7 +835,7 @@ template <int D>
 cudaError_t launch_bwd(const Args &keys, const Args &rows, const Maps &maps, cudaStream_t s) {
     const long long kb = (long long)keys.items * keys.Hk, rb = (long long)rows.items * rows.Hk;
     if (kb + rb == 0) return cudaSuccess;
-    cudaError_t e = attn_allow_smem(reinterpret_cast<const void *>(attn_tc_bwd_kernel<D>), Cfg<D>::SMEM);
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(attn_tc_bwd_kernel<D>), Cfg<D>::SMEM);
     if (e != cudaSuccess) return e;
     attn_tc_bwd_kernel<D><<<(unsigned)(kb + rb), kThreads, Cfg<D>::SMEM, s>>>(keys, rows, maps,
                                                                               (int)kb);

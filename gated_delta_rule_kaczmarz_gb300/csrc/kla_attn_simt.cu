@@ -509,7 +509,7 @@ attn_prep_kernel(const int *cu_q, const int *cu_k, int n, int total_q, int total
 template <typename K, typename... A>
 cudaError_t launch(K *kernel, long long blocks, size_t smem, cudaStream_t s, const A &...args) {
     if (blocks == 0) return cudaSuccess;
-    cudaError_t e = attn_allow_smem(reinterpret_cast<const void *>(kernel), smem);
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)blocks, kT, smem, s>>>(args...);
     note_launch();

@@ -527,7 +527,7 @@ template <int D>
 cudaError_t launch_fwd(const Args &a, const Maps &maps, cudaStream_t s) {
     const long long blocks = (long long)a.items * a.splits * a.Hk;
     if (blocks == 0) return cudaSuccess;
-    cudaError_t e = attn_allow_smem(reinterpret_cast<const void *>(attn_tc_fwd_kernel<D>), Cfg<D>::SMEM);
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(attn_tc_fwd_kernel<D>), Cfg<D>::SMEM);
     if (e != cudaSuccess) return e;
     attn_tc_fwd_kernel<D><<<(unsigned)blocks, kThreads, Cfg<D>::SMEM, s>>>(a, maps);
     note_launch();

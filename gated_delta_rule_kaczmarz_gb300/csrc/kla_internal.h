@@ -80,6 +80,10 @@ cudaError_t launch_ccq_step(const void *q, const void *k, const float *lambda, f
                             float *ms, float *ns, void *q_clean, int BH, int d, int dtype,
                             cudaStream_t s);
 
+// Lets a kernel use this much dynamic shared memory on the current device; the
+// same amount in every call for a kernel (kla_attn.cu).
+cudaError_t allow_dynamic_smem(const void *kernel, size_t bytes);
+
 // Query and key conditioning (kla_qk_norm_rope.cu).  Strides are elements
 // between token rows; the heads of a row are d apart.
 struct QkProblem {

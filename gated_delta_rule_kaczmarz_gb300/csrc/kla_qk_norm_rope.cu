@@ -27,6 +27,7 @@
 #include <cuda_bf16.h>
 
 #include "kla_internal.h"
+#include "kla_tc.cuh"
 
 namespace kla {
 namespace {
@@ -226,155 +227,113 @@ __device__ __forceinline__ void load_weight(float2 (&w)[8], const float *p, cons
     b.get(w + 4);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 4)
-qk_fwd_kernel(const __grid_constant__ QkArgs a) {
-    constexpr int RW = 512 / D;                       // rows of a warp's group
-    constexpr int U = sizeof(T) == 2 ? 4 : 2;         // groups loaded ahead
-    __shared__ __align__(16) float2 cs_all[kWarps][64];
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    float2 *cs = cs_all[warp];
-    const Lane<D> l(lane, a.pairs);
-    Angles ang;
-    ang.init(a, lane);
-    const int stride = gridDim.x * kWarps, part = blockIdx.y;
-    int t = blockIdx.x * kWarps + warp;
-    if (t < a.tokens) ang.read(a, lane, t);
-    // (unsigned: the last step may pass 2^31)
-    for (; (unsigned)t < (unsigned)a.tokens; t = (int)((unsigned)t + stride)) {
-        ang.turn(a, lane, l, cs);
-        if ((unsigned)t + stride < (unsigned)a.tokens) ang.read(a, lane, t + stride);
-#pragma unroll 1
-        for (int z = 0; z < 2; ++z) {
-            const int H = a.heads[z];
-            if (H == 0) continue;
-            float2 w[8];
-            const bool weighted = a.w[z] != nullptr;
-            if (weighted) load_weight<D>(w, a.w[z], l);
-            const T *x = static_cast<const T *>(a.x[z]) + (long long)t * a.xs[z];
-            T *y = static_cast<T *>(a.y[z]) + (long long)t * a.ys[z];
-            const int mode = a.norm[z];
-            for (int h0 = part * RW; h0 < H; h0 += U * a.parts * RW) {
-                Raw<T> r0[U], r1[U];
+// The heads of one tensor (z: q, k) of a token: groups of 512 / D rows, `parts`
+// apart, U of them loaded ahead.  x and y may be the same rows.
+template <typename T, int D, int U>
+__device__ __forceinline__ void forward_rows(const QkArgs &a, int z, const T *x, T *y, int part,
+                                             int parts, const Lane<D> &l, const Angles &ang) {
+    constexpr int RW = 512 / D;
+    const int H = a.heads[z], mode = a.norm[z];
+    float2 w[8];
+    const bool weighted = a.w[z] != nullptr;
+    if (weighted) load_weight<D>(w, a.w[z], l);
+    for (int h0 = part * RW; h0 < H; h0 += U * parts * RW) {
+        Raw<T> r0[U], r1[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int h = h0 + u * a.parts * RW + l.row;
-                    if (h < H) {
-                        r0[u].load(x + h * D + l.col0);
-                        r1[u].load(x + h * D + l.col1);
-                    }
-                }
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + u * parts * RW + l.row;
+            if (h < H) {
+                r0[u].load(x + h * D + l.col0);
+                r1[u].load(x + h * D + l.col1);
+            }
+        }
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (h0 + u * a.parts * RW >= H) break;      // the warp's whole group
-                    const int h = h0 + u * a.parts * RW + l.row;
-                    float2 v[8];
-                    r0[u].get(v);
-                    r1[u].get(v + 4);
-                    if (mode != 0) {
-                        const float2 r = both(inv_norm<D>(v, mode, a.eps));
+        for (int u = 0; u < U; ++u) {
+            if (h0 + u * parts * RW >= H) break;            // the warp's whole group
+            const int h = h0 + u * parts * RW + l.row;
+            float2 v[8];
+            r0[u].get(v);
+            r1[u].get(v + 4);
+            if (mode != 0) {
+                const float2 r = both(inv_norm<D>(v, mode, a.eps));
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = __fmul2_rn(v[i], r);
-                    }
-                    if (weighted) {
+                for (int i = 0; i < 8; ++i) v[i] = __fmul2_rn(v[i], r);
+            }
+            if (weighted) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = __fmul2_rn(v[i], w[i]);
-                    }
-                    rotate<D, false>(v, l, ang, a.pair_style);
-                    if (h < H) {
-                        st8(y + h * D + l.col0, v);
-                        st8(y + h * D + l.col1, v + 4);
-                    }
-                }
+                for (int i = 0; i < 8; ++i) v[i] = __fmul2_rn(v[i], w[i]);
+            }
+            rotate<D, false>(v, l, ang, a.pair_style);
+            if (h < H) {
+                st8(y + h * D + l.col0, v);
+                st8(y + h * D + l.col1, v + 4);
             }
         }
     }
 }
-
-// The weight gradients are summed in registers over a warp's rows, then over
-// the block, and leave as one partial sum per block: no atomics, so a result
-// does not depend on the order in which blocks run.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 3)
-qk_bwd_kernel(const __grid_constant__ QkArgs a) {
+// Their gradients: x and g into y, the weight's into acc.
+template <typename T, int D, int U>
+__device__ __forceinline__ void backward_rows(const QkArgs &a, int z, const T *x, const T *g, T *y,
+                                              int part, int parts, const Lane<D> &l,
+                                              const Angles &ang, float2 (&acc)[8]) {
     constexpr int RW = 512 / D;
-    constexpr int U = sizeof(T) == 2 ? 2 : 1;
-    __shared__ __align__(16) float2 cs_all[kWarps][64];
-    __shared__ float part_w[kWarps][2][D];
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    float2 *cs = cs_all[warp];
-    const Lane<D> l(lane, a.pairs);
-    Angles ang;
-    ang.init(a, lane);
-    float2 acc[2][8];
+    const int H = a.heads[z], mode = a.norm[z];
+    float2 w[8];
+    const bool weighted = a.w[z] != nullptr;
+    if (weighted) load_weight<D>(w, a.w[z], l);
+    for (int h0 = part * RW; h0 < H; h0 += U * parts * RW) {
+        Raw<T> x0[U], x1[U], g0[U], g1[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[0][i] = acc[1][i] = both(0.f);
-    const int stride = gridDim.x * kWarps, part = blockIdx.y;
-    int t = blockIdx.x * kWarps + warp;
-    if (t < a.tokens) ang.read(a, lane, t);
-    // (unsigned: the last step may pass 2^31)
-    for (; (unsigned)t < (unsigned)a.tokens; t = (int)((unsigned)t + stride)) {
-        ang.turn(a, lane, l, cs);
-        if ((unsigned)t + stride < (unsigned)a.tokens) ang.read(a, lane, t + stride);
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + u * parts * RW + l.row;
+            if (h < H) {
+                x0[u].load(x + h * D + l.col0);
+                x1[u].load(x + h * D + l.col1);
+                g0[u].load(g + h * D + l.col0);
+                g1[u].load(g + h * D + l.col1);
+            } else {                  // no row: adds nothing to the weights' gradients
+                x0[u].zero(); x1[u].zero(); g0[u].zero(); g1[u].zero();
+            }
+        }
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            const int H = a.heads[z];
-            if (H == 0) continue;
-            float2 w[8];
-            const bool weighted = a.w[z] != nullptr;
-            if (weighted) load_weight<D>(w, a.w[z], l);
-            const T *x = static_cast<const T *>(a.x[z]) + (long long)t * a.xs[z];
-            const T *g = static_cast<const T *>(a.g[z]) + (long long)t * a.gs[z];
-            T *y = static_cast<T *>(a.y[z]) + (long long)t * a.ys[z];
-            const int mode = a.norm[z];
-            for (int h0 = part * RW; h0 < H; h0 += U * a.parts * RW) {
-                Raw<T> x0[U], x1[U], g0[U], g1[U];
+        for (int u = 0; u < U; ++u) {
+            if (h0 + u * parts * RW >= H) break;
+            const int h = h0 + u * parts * RW + l.row;
+            float2 v[8], d[8];
+            x0[u].get(v);
+            x1[u].get(v + 4);
+            g0[u].get(d);
+            g1[u].get(d + 4);
+            rotate<D, true>(d, l, ang, a.pair_style);
+            const float r = inv_norm<D>(v, mode, a.eps);
+            if (weighted) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int h = h0 + u * a.parts * RW + l.row;
-                    if (h < H) {
-                        x0[u].load(x + h * D + l.col0);
-                        x1[u].load(x + h * D + l.col1);
-                        g0[u].load(g + h * D + l.col0);
-                        g1[u].load(g + h * D + l.col1);
-                    } else {              // no row: adds nothing to the weights' gradients
-                        x0[u].zero(); x1[u].zero(); g0[u].zero(); g1[u].zero();
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    acc[i] = __ffma2_rn(d[i], __fmul2_rn(v[i], both(r)), acc[i]);
+                    d[i] = __fmul2_rn(d[i], w[i]);
                 }
+            }
+            if (mode != 0) {
+                float dot = row_dot<D>(d, v) * r * r;
+                if (mode == 1) dot *= 1.f / D;
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (h0 + u * a.parts * RW >= H) break;
-                    const int h = h0 + u * a.parts * RW + l.row;
-                    float2 v[8], d[8];
-                    x0[u].get(v);
-                    x1[u].get(v + 4);
-                    g0[u].get(d);
-                    g1[u].get(d + 4);
-                    rotate<D, true>(d, l, ang, a.pair_style);
-                    const float r = inv_norm<D>(v, mode, a.eps);
-                    if (weighted) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            acc[z][i] = __ffma2_rn(d[i], __fmul2_rn(v[i], both(r)), acc[z][i]);
-                            d[i] = __fmul2_rn(d[i], w[i]);
-                        }
-                    }
-                    if (mode != 0) {
-                        float dot = row_dot<D>(d, v) * r * r;
-                        if (mode == 1) dot *= 1.f / D;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            d[i] = __fmul2_rn(__ffma2_rn(v[i], both(-dot), d[i]), both(r));
-                    }
-                    if (h < H) {
-                        st8(y + h * D + l.col0, d);
-                        st8(y + h * D + l.col1, d + 4);
-                    }
-                }
+                for (int i = 0; i < 8; ++i)
+                    d[i] = __fmul2_rn(__ffma2_rn(v[i], both(-dot), d[i]), both(r));
+            }
+            if (h < H) {
+                st8(y + h * D + l.col0, d);
+                st8(y + h * D + l.col1, d + 4);
             }
         }
     }
-    if (a.dw == nullptr) return;
+}
+// A block's sums of the weights' gradients, warp by warp in part_w, to its
+// place among the partial sums.  No atomics: a result does not depend on the
+// order in which blocks run.
+template <int D>
+__device__ __forceinline__ void leave_partial_sums(const QkArgs &a, const float2 (&acc)[2][8],
+                                                   const Lane<D> &l, float *part_w, int warp,
+                                                   int warps, int block) {
 #pragma unroll
     for (int z = 0; z < 2; ++z)
 #pragma unroll
@@ -382,14 +341,171 @@ qk_bwd_kernel(const __grid_constant__ QkArgs a) {
             float v = i % 2 ? acc[z][i / 2].y : acc[z][i / 2].x;
 #pragma unroll
             for (int o = 16; o >= D / 16; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (l.row == 0) part_w[warp][z][i < 8 ? l.col0 + i : l.col1 + i - 8] = v;
+            if (l.row == 0) part_w[(warp * 2 + z) * D + (i < 8 ? l.col0 + i : l.col1 + i - 8)] = v;
         }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
         float v = 0.f;
+        for (int w = 0; w < warps; ++w) v += part_w[w * 2 * D + i];
+        a.dw[(size_t)block * 2 * D + i] = v;
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 4)
+qk_fwd_kernel(const __grid_constant__ QkArgs a) {
+    constexpr int U = sizeof(T) == 2 ? 4 : 2;
+    __shared__ __align__(16) float2 cs_all[kWarps][64];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const Lane<D> l(lane, a.pairs);
+    Angles ang;
+    ang.init(a, lane);
+    const int stride = gridDim.x * kWarps;
+    int t = blockIdx.x * kWarps + warp;
+    if (t < a.tokens) ang.read(a, lane, t);
+    // (unsigned: the last step may pass 2^31)
+    for (; (unsigned)t < (unsigned)a.tokens; t = (int)((unsigned)t + stride)) {
+        ang.turn(a, lane, l, cs_all[warp]);
+        if ((unsigned)t + stride < (unsigned)a.tokens) ang.read(a, lane, t + stride);
+#pragma unroll 1
+        for (int z = 0; z < 2; ++z)
+            forward_rows<T, D, U>(a, z, static_cast<const T *>(a.x[z]) + (long long)t * a.xs[z],
+                                  static_cast<T *>(a.y[z]) + (long long)t * a.ys[z], blockIdx.y,
+                                  a.parts, l, ang);
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 3)
+qk_bwd_kernel(const __grid_constant__ QkArgs a) {
+    constexpr int U = sizeof(T) == 2 ? 2 : 1;
+    __shared__ __align__(16) float2 cs_all[kWarps][64];
+    __shared__ float part_w[kWarps * 2 * D];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const Lane<D> l(lane, a.pairs);
+    Angles ang;
+    ang.init(a, lane);
+    float2 acc[2][8];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += part_w[w][i / D][i % D];
-        a.dw[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 * D + i] = v;
+    for (int i = 0; i < 8; ++i) acc[0][i] = acc[1][i] = both(0.f);
+    const int stride = gridDim.x * kWarps;
+    int t = blockIdx.x * kWarps + warp;
+    if (t < a.tokens) ang.read(a, lane, t);
+    for (; (unsigned)t < (unsigned)a.tokens; t = (int)((unsigned)t + stride)) {
+        ang.turn(a, lane, l, cs_all[warp]);
+        if ((unsigned)t + stride < (unsigned)a.tokens) ang.read(a, lane, t + stride);
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+            backward_rows<T, D, U>(a, z, static_cast<const T *>(a.x[z]) + (long long)t * a.xs[z],
+                                   static_cast<const T *>(a.g[z]) + (long long)t * a.gs[z],
+                                   static_cast<T *>(a.y[z]) + (long long)t * a.ys[z], blockIdx.y,
+                                   a.parts, l, ang, acc[z]);
+    }
+    if (a.dw != nullptr)
+        leave_partial_sums<D>(a, acc, l, part_w, warp, kWarps, blockIdx.y * gridDim.x + blockIdx.x);
+}
+
+// ------------------------------------------------------------ many tokens
+// A warp walks whole tokens; their rows come by bulk copies into a ring of
+// stages of its own in shared memory, are worked on in place and leave by bulk
+// copies, so that HBM is busy while a warp computes.  The kernels above keep a
+// token's rows in registers: a warp's loads then wait for its arithmetic.
+struct Pipe {
+    int warps, stages;               // of a block
+    uint32_t bytes[2];               // a token's rows of q and of k
+    uint32_t stage;                  // bytes of a stage: x, and for the backward g
+};
+constexpr int kPipeMost = 16;        // warps of a block, forward; backward 12 (registers)
+constexpr size_t kPipeSmem = 200 * 1024;
+
+template <typename T, int D, bool BACK>
+__global__ void __launch_bounds__(BACK ? 384 : kPipeMost * 32, 1)
+qk_pipe_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ Pipe p) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ uint64_t full[kPipeMost][4];
+    __shared__ __align__(16) float2 cs_all[kPipeMost][64];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, S = p.stages;
+    unsigned char *ring = smem + (size_t)warp * S * p.stage;
+    if (lane == 0) {
+        for (int i = 0; i < S; ++i) tc::mbar_init(&full[warp][i], 1);
+        tc::fence_mbar_init();
+    }
+    __syncwarp();
+    const Lane<D> l(lane, a.pairs);
+    Angles ang;
+    ang.init(a, lane);
+    float2 acc[2][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[0][i] = acc[1][i] = both(0.f);
+    const unsigned first = blockIdx.x * p.warps + warp, stride = gridDim.x * p.warps;
+    const unsigned tokens = a.tokens;
+    const int n = first < tokens ? (int)((tokens - 1 - first) / stride) + 1 : 0;   // of this warp
+
+    const auto load = [&](int i, int s) {       // one lane: the warp's i-th token
+        const long long t = first + (long long)i * stride;
+        unsigned char *dst = ring + (size_t)s * p.stage;
+        tc::mbar_expect_tx(&full[warp][s], p.stage);
+#pragma unroll
+        for (int g = 0; g < (BACK ? 2 : 1); ++g)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                if (p.bytes[z] == 0) continue;
+                const T *src = g ? static_cast<const T *>(a.g[z]) + t * a.gs[z]
+                                 : static_cast<const T *>(a.x[z]) + t * a.xs[z];
+                tc::bulk_load(dst, src, p.bytes[z], &full[warp][s]);
+                dst += p.bytes[z];
+            }
+    };
+    if (lane == 0)
+        for (int i = 0; i < S - 1 && i < n; ++i) load(i, i);
+    if (n > 0) ang.read(a, lane, (int)first);
+    int s = 0, use = 0, i = 0;
+    for (; i < n; ++i) {
+        const long long t = first + (long long)i * stride;
+        ang.turn(a, lane, l, cs_all[warp]);
+        if (i + 1 < n) ang.read(a, lane, (int)(t + stride));
+        // the warp's own copy: it comes, and the bound is never reached
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[warp][s], use & 1))) break;
+        unsigned char *row = ring + (size_t)s * p.stage;
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            T *x = reinterpret_cast<T *>(row + (z ? p.bytes[0] : 0));
+            if (BACK)
+                backward_rows<T, D, 1>(a, z, x,
+                                       reinterpret_cast<T *>(reinterpret_cast<unsigned char *>(x) +
+                                                             p.bytes[0] + p.bytes[1]),
+                                       x, 0, 1, l, ang, acc[z]);
+            else
+                forward_rows<T, D, 2>(a, z, x, x, 0, 1, l, ang);
+        }
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+                if (p.bytes[z])
+                    tc::bulk_store(static_cast<T *>(a.y[z]) + t * a.ys[z],
+                                   row + (z ? p.bytes[0] : 0), p.bytes[z]);
+            tc::bulk_commit_group();
+            // the stage of the token before is free once its rows have left
+            if (i + S - 1 < n) {
+                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                load(i + S - 1, s == 0 ? S - 1 : s - 1);
+            }
+        }
+        if (++s == S) {
+            s = 0;
+            ++use;
+        }
+    }
+    if (lane == 0) {
+        for (int j = i; j < n && j < i + S - 1; ++j)       // a copy that had not come
+            (void)tc::mbar_wait(&full[warp][j % S], (j / S) & 1);
+        tc::bulk_wait_group0();
+    }
+    if (BACK && a.dw != nullptr) {
+        __syncthreads();       // the rings are done with: the warps' sums take their place
+        leave_partial_sums<D>(a, acc, l, reinterpret_cast<float *>(smem), warp, p.warps, blockIdx.x);
     }
 }
 
@@ -449,8 +565,67 @@ dim3 blocks_for(const QkArgs &a) {
     return dim3((unsigned)(want < most ? want : most), (unsigned)a.parts);
 }
 
+// The pipelined kernel's shape, or warps = 0 where it does not pay: it wants 12
+// warps of three stages in a block's shared memory (backward: 8 of two), and 4
+// tokens for each.  32768 tokens of 16 + 4 heads of 128 in bf16 take 69 us with
+// it and 77 without (backward 114 and 132), of head size 64 46 and 57; with
+// rows of 16 + 16 heads, where it has 8 warps, 106 and 97 (backward, 6 warps,
+// 196 and 172).  Both are bound by the warps' own latency, at about half of the
+// issue slots; a copy alone would take 51 us.
+Pipe pipe_for(const QkProblem &p, bool back) {
+    Pipe r{};
+    const uint32_t row = (uint32_t)p.d * (p.dtype == 1 ? 2 : 4);
+    r.bytes[0] = p.Hq * row;
+    r.bytes[1] = p.Hk * row;
+    r.stage = (r.bytes[0] + r.bytes[1]) * (back ? 2 : 1);
+    const int most = back ? 12 : kPipeMost;
+    for (r.stages = 3; r.stages >= (back ? 2 : 3); --r.stages) {
+        const size_t fit = kPipeSmem / ((size_t)r.stages * r.stage);
+        r.warps = fit < (size_t)most ? (int)fit : most;
+        if (r.warps >= (r.stages == 3 ? 12 : 8)) {
+            if (p.tokens < 4 * 152 * r.warps) break;
+            return r;
+        }
+    }
+    r.warps = 0;
+    return r;
+}
+
+template <typename T, int D, bool BACK>
+cudaError_t launch_pipe(const QkArgs &a, const Pipe &p, cudaStream_t s) {
+    const void *kernel = reinterpret_cast<const void *>(qk_pipe_kernel<T, D, BACK>);
+    cudaError_t e = allow_dynamic_smem(kernel, kPipeSmem);
+    if (e != cudaSuccess) return e;
+    size_t smem = (size_t)p.warps * p.stages * p.stage;
+    const size_t sums = (size_t)p.warps * 2 * D * sizeof(float);
+    if (BACK && smem < sums) smem = sums;
+    qk_pipe_kernel<T, D, BACK><<<152, p.warps * 32, smem, s>>>(a, p);
+    note_launch();
+    return cudaGetLastError();
+}
+template <typename T, int D, bool BACK>
+cudaError_t launch_rows(const QkArgs &a, cudaStream_t s) {
+    if (BACK) qk_bwd_kernel<T, D><<<blocks_for(a), kThreads, 0, s>>>(a);
+    else qk_fwd_kernel<T, D><<<blocks_for(a), kThreads, 0, s>>>(a);
+    note_launch();
+    return cudaGetLastError();
+}
+template <bool BACK>
+cudaError_t launch_qk(const QkProblem &p, const QkArgs &a, const Pipe &pipe, cudaStream_t s) {
+    const bool on = pipe.warps > 0;
+    if (p.dtype == 1) {
+        using T = __nv_bfloat16;
+        if (p.d == 128) return on ? launch_pipe<T, 128, BACK>(a, pipe, s) : launch_rows<T, 128, BACK>(a, s);
+        return on ? launch_pipe<T, 64, BACK>(a, pipe, s) : launch_rows<T, 64, BACK>(a, s);
+    }
+    if (p.d == 128) return on ? launch_pipe<float, 128, BACK>(a, pipe, s) : launch_rows<float, 128, BACK>(a, s);
+    return on ? launch_pipe<float, 64, BACK>(a, pipe, s) : launch_rows<float, 64, BACK>(a, s);
+}
+
 }  // namespace
 
+// Partial sums of the weights' gradients.  The pipelined kernel's 152 blocks
+// need no more than the others' over as many tokens.
 size_t qk_bwd_workspace_bytes(const QkProblem &p) {
     if (p.tokens == 0) return 0;
     const dim3 b = blocks_for(make_args(p));
@@ -458,35 +633,19 @@ size_t qk_bwd_workspace_bytes(const QkProblem &p) {
 }
 
 cudaError_t launch_qk_fwd(const QkProblem &p, cudaStream_t s) {
-    const QkArgs a = make_args(p);
-    const dim3 blocks = blocks_for(a);
-    if (p.dtype == 1) {
-        if (p.d == 128) qk_fwd_kernel<__nv_bfloat16, 128><<<blocks, kThreads, 0, s>>>(a);
-        else qk_fwd_kernel<__nv_bfloat16, 64><<<blocks, kThreads, 0, s>>>(a);
-    } else {
-        if (p.d == 128) qk_fwd_kernel<float, 128><<<blocks, kThreads, 0, s>>>(a);
-        else qk_fwd_kernel<float, 64><<<blocks, kThreads, 0, s>>>(a);
-    }
-    note_launch();
-    return cudaGetLastError();
+    return launch_qk<false>(p, make_args(p), pipe_for(p, false), s);
 }
 
 cudaError_t launch_qk_bwd(const QkProblem &p, cudaStream_t s) {
     QkArgs a = make_args(p);
     const bool weights = p.dwq != nullptr || p.dwk != nullptr;
     a.dw = weights ? static_cast<float *>(p.ws) : nullptr;
-    const dim3 blocks = blocks_for(a);
-    if (p.dtype == 1) {
-        if (p.d == 128) qk_bwd_kernel<__nv_bfloat16, 128><<<blocks, kThreads, 0, s>>>(a);
-        else qk_bwd_kernel<__nv_bfloat16, 64><<<blocks, kThreads, 0, s>>>(a);
-    } else {
-        if (p.d == 128) qk_bwd_kernel<float, 128><<<blocks, kThreads, 0, s>>>(a);
-        else qk_bwd_kernel<float, 64><<<blocks, kThreads, 0, s>>>(a);
-    }
-    note_launch();
-    cudaError_t e = cudaGetLastError();
+    const Pipe pipe = pipe_for(p, true);
+    cudaError_t e = launch_qk<true>(p, a, pipe, s);
     if (e != cudaSuccess || !weights) return e;
-    qk_dw_kernel<<<2 * p.d / 32, dim3(32, 32), 0, s>>>(a.dw, (int)(blocks.x * blocks.y), p.d, p.dwq, p.dwk);
+    const dim3 b = blocks_for(a);
+    qk_dw_kernel<<<2 * p.d / 32, dim3(32, 32), 0, s>>>(a.dw, pipe.warps ? 152 : (int)(b.x * b.y), p.d,
+                                                       p.dwq, p.dwk);
     note_launch();
     return cudaGetLastError();
 }

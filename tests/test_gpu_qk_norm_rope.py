@@ -89,6 +89,11 @@ CASES = [
     (65, 17, 33, 64, 0, 1, "half", "rms", "l2", True),
     (5001, 2, 1, 128, 128, 1, "half", "none", "none", False),
     (5001, 3, 7, 64, 16, 1, "half", "rms", "rms", True),
+    # enough tokens for the pipelined kernel: a warp's ring turns over
+    (9001, 2, 1, 128, 128, 1, "half", "rms", "rms", True),
+    (9730, 5, 3, 64, 32, 3, "pairs", "l2", "none", True),
+    (7297, 3, 0, 128, 64, 2, "half", "rms", "none", True),
+    (9728, 1, 16, 64, 0, 1, "half", "none", "rms", False),
 ]
 
 
@@ -177,6 +182,28 @@ def test_views_of_a_projection_in_place_and_into_a_cache(dtype):
                              q_out=q, k_out=k)
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
     assert bool((x[..., (hq + hk) * d:] == 7).all())     # the values stayed
+
+
+def test_many_tokens_of_a_projection_in_place():
+    """The pipelined kernel on strided rows: the rows of the values between
+    them stay, in place equals out of place, gradients equal those of dense
+    rows."""
+    T, hq, hk, d = 10000, 4, 2, 128
+    dt = torch.bfloat16
+    inp = _cuda(_inputs(T, hq, hk, d, dt, 128, 1, seed=12))
+    x = torch.full((T, (hq + 2 * hk) * d), 7.0, dtype=dt, device="cuda")
+    q, k = x[:, :hq * d].unflatten(-1, (hq, d)), x[:, hq * d:(hq + hk) * d].unflatten(-1, (hk, d))
+    q.copy_(inp["q"])
+    k.copy_(inp["k"])
+    args = (inp["pos"], inp["freq"])
+    want = kla.kla_qk_norm_rope_fwd(inp["q"], inp["k"], *args, inp["wq"], inp["wk"])
+    grads = kla.kla_qk_norm_rope_bwd(inp["q"], inp["k"], *args, inp["gq"], inp["gk"], inp["wq"],
+                                     inp["wk"])
+    again = kla.kla_qk_norm_rope_bwd(q, k, *args, inp["gq"], inp["gk"], inp["wq"], inp["wk"])
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+    kla.kla_qk_norm_rope_fwd(q, k, *args, inp["wq"], inp["wk"], q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    assert bool((x[:, (hq + hk) * d:] == 7).all())
 
 
 def test_zero_rows_with_eps_zero_and_no_tokens():
