@@ -66,7 +66,7 @@ struct Shared {
     uint64_t full[5], empty[5];          // ring slots
     uint64_t fix, fix_read;              // the item's own tiles landed, and no longer read
     uint64_t s[2], dp[2];                // scores and dP ready
-    uint64_t s_read, p, ds[2];           // scores read; P and dS in place
+    uint64_t s_read, p[2], ds[2];        // scores read; P and dS in place
     uint64_t st[2], read[2];             // row statistics ready, and read
     uint64_t raw[2], zeroed;             // last tiles with a neighbour's rows landed, and cleaned
     uint64_t fin, drained;               // an item's products complete, its sums read
@@ -411,7 +411,10 @@ struct Cta {
         for (int i = 0; i < n; ++i) {
             const int g = at.g + i;
             if (D == 64 && i + 1 < n && !scores(i + 1)) return false;
-            if (!landed_y(g) || !wait(&sh.p, at.key + i)) return false;
+            // one barrier for odd and one for even steps: with two S^T the next
+            // step's P can be in place before this wait is looked at
+            const int gk = at.key + i;
+            if (!landed_y(g) || !wait(&sh.p[gk & 1], gk >> 1)) return false;
             gather(key_scores(i), slot_y(g), TM_V, i > 0);
             if (D != 64 && i + 1 < n && !scores(i + 1)) return false;
         }
@@ -622,7 +625,7 @@ struct Cta {
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p);
+            if (lane == 0) mbar_arrive(&sh.p[gk & 1]);
             float4 nd[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) nd[k] = st[32 + k];
@@ -774,6 +777,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Args ak, const __grid_constant__ Args
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s[i], 1);
             mbar_init(&sh.dp[i], 1);
+            mbar_init(&sh.p[i], 8);
             mbar_init(&sh.ds[i], 8);
             mbar_init(&sh.st[i], 1);
             mbar_init(&sh.read[i], 8);
@@ -784,7 +788,6 @@ attn_tc_bwd_kernel(const __grid_constant__ Args ak, const __grid_constant__ Args
         mbar_init(&sh.fix, 1);
         mbar_init(&sh.fix_read, 2);
         mbar_init(&sh.s_read, 8);
-        mbar_init(&sh.p, 8);
         mbar_init(&sh.zeroed, 1);
         mbar_init(&sh.fin, 2);
         mbar_init(&sh.drained, 8);
