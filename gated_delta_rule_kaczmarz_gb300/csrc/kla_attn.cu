@@ -119,7 +119,7 @@ struct BwdPlan {
     bool tc;
     Side q, k;
     int tile;
-    size_t table_q, table_k, delta, bytes;
+    size_t table_q, table_k, delta, delta_few, bytes;
 };
 BwdPlan bwd_plan(const AttnProblem &p) {
     BwdPlan b{};
@@ -140,7 +140,9 @@ BwdPlan bwd_plan(const AttnProblem &p) {
     b.table_k = at;
     if (p.cu_q) at = up256(at + b.k.items * sizeof(int2));
     b.delta = at;
-    b.bytes = up256(at + (size_t)p.total_q * p.Hq * sizeof(float));
+    const size_t rows = up256((size_t)p.total_q * p.Hq * sizeof(float));
+    b.delta_few = p.dtype == 1 ? at + rows : at;
+    b.bytes = b.delta_few + rows;
     return b;
 }
 
@@ -236,6 +238,7 @@ cudaError_t launch_attn_bwd(const AttnProblem &p, cudaStream_t s) {
                             {tk, p.cu_k, b.k.mult, b.k.per, (int)b.k.items, false}, s);
     if (e != cudaSuccess) return e;
     a.delta = reinterpret_cast<float *>(at(p, b.delta));
+    a.delta_few = reinterpret_cast<float *>(at(p, b.delta_few));
     e = launch_attn_delta(a, p.d, p.dtype, s);
     if (e != cudaSuccess) return e;
     attn::Args keys = a;

@@ -3,6 +3,7 @@
 //
 //   p = exp2(c s - lse log2 e),  ds = p (dp - delta),  dp = go v^T,
 //   dv = p^T go,  dk = scale ds^T q,  dq = scale ds k,  delta = sum go o
+// (what delta is of rows with few keys: delta_of)
 //
 // One launch has two kinds of CTAs, each on 128 x 128 tiles of (packed rows,
 // keys) with scores, probabilities and sums in tensor memory:
@@ -506,7 +507,7 @@ struct Cta {
     __device__ float2 read_statistics(const Work &w, int r, int tok) {
         if (r >= R || tok >= w.lq) return make_float2(-INFINITY, 0.f);
         const long long at = (long long)(w.q0 + tok) * ar.Hq + w.head * ar.G + r % ar.G;
-        return make_float2(ar.lse_in[at], ar.delta[at]);
+        return make_float2(ar.lse_in[at], attn::delta_of(ar, at, tok + w.lk - w.lq + 1));
     }
     static __device__ float2 row_statistics(float2 x) {
         return make_float2(x.x == -INFINITY ? -INFINITY : -x.x * 1.4426950408889634f, -x.y);

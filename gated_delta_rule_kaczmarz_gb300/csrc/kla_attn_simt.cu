@@ -276,7 +276,7 @@ __device__ void attn_simt_dq(const Args &a, int block, float *sm) {
         limit[i] = on ? (int)(r / a.G) + s.lk - s.lq : -1;
         const long long at = (s.q0 + r / a.G) * a.Hq + it.head * a.G + (int)(r % a.G);
         lse2[i] = on ? a.lse_in[at] / kLn2 : 0.f;
-        delta[i] = on ? a.delta[at] : 0.f;
+        delta[i] = on ? attn::delta_of(a, at, limit[i] + 1) : 0.f;
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) acc[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -352,7 +352,7 @@ __device__ void attn_simt_dkv(const Args &a, int block, float *sm) {
             const int limit = on_r ? (int)(r / a.G) + s.lk - s.lq : -1;
             const long long at = (s.q0 + r / a.G) * a.Hq + it.head * a.G + (int)(r % a.G);
             const float lse2 = on_r ? a.lse_in[at] / kLn2 : 0.f;
-            const float delta = on_r ? a.delta[at] : 0.f;
+            const float delta = on_r ? attn::delta_of(a, at, limit + 1) : 0.f;
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 const int key = j0 + ty + 16 * i;
@@ -391,27 +391,115 @@ attn_simt_bwd_kernel(const __grid_constant__ Args keys, const __grid_constant__ 
 }
 
 // ------------------------------------------------------- shared by all paths
-// Row sums of go o: a warp per (token, head).
-template <typename T, int D>
-__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ Args a) {
-    attn::clear_status(a);
-    if (attn::rejected(a)) return;
-    const long long n = (long long)a.total_q * a.Hq;
-    const long long i = (long long)blockIdx.x * 16 + threadIdx.x / 16;
-    const int lane = threadIdx.x % 16;
-    float sum = 0.f;
-    if (i < n) {
-        const T *o = static_cast<const T *>(a.o) + i * D;
-        const T *g = static_cast<const T *>(a.go) + i / a.Hq * a.go_stride + i % a.Hq * D;
+// 16 bytes of a row, and what two such parts add to a dot product.
+template <typename T>
+__device__ __forceinline__ uint4 ld16(const T *p) { return *reinterpret_cast<const uint4 *>(p); }
+template <typename T>
+__device__ __forceinline__ float dot16(const uint4 &a, const uint4 &b, float sum) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-            const float4 x = ld4(o + 4 * lane + 64 * j), y = ld4(g + 4 * lane + 64 * j);
-            sum += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            sum = fmaf(__uint_as_float(x[i]), __uint_as_float(y[i]), sum);
+        } else {
+            sum = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), sum);
+            sum = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), sum);
         }
     }
+    return sum;
+}
+
+constexpr int kDeltaRows = 2;
+template <typename T, int D>
+struct DeltaShape {
+    static constexpr int V = 16 / (int)sizeof(T), L = D / V, ROWS = 256 / L * kDeltaRows;
+};
+// The sum over the L lanes of a row.
+template <int L>
+__device__ __forceinline__ float sum_lanes(float x) {
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (i < n && lane == 0) a.delta[i] = sum;
+    for (int m = L / 2; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    return x;
+}
+
+// delta = sum go o of every row: 16 bytes of it a lane, kDeltaRows rows a
+// thread; bound by the bytes of o and go.
+template <typename T, int D>
+__device__ __forceinline__ void delta_rows(const Args &a, int block_index) {
+    using S = DeltaShape<T, D>;
+    const long long n = (long long)a.total_q * a.Hq;
+    const long long block = (long long)block_index * S::ROWS;
+    const int block_tok = n <= 0xffffffffll ? (int)((unsigned)block / (unsigned)a.Hq)
+                                            : (int)(block / a.Hq);
+    const int block_head = (int)(block - (long long)block_tok * a.Hq);
+    const int lane = threadIdx.x % S::L;
+    uint4 o[kDeltaRows], g[kDeltaRows];
+    long long row[kDeltaRows];            // behind the last one: that one
+#pragma unroll
+    for (int r = 0; r < kDeltaRows; ++r) {
+        row[r] = min(block + threadIdx.x / S::L + 256 / S::L * r, n - 1);
+        const int x = block_head + (int)(row[r] - block);
+        const long long at = (block_tok + x / a.Hq) * a.go_stride + (long long)(x % a.Hq) * D;
+        o[r] = ld16(static_cast<const T *>(a.o) + row[r] * D + lane * S::V);
+        g[r] = ld16(static_cast<const T *>(a.go) + at + lane * S::V);
+    }
+#pragma unroll
+    for (int r = 0; r < kDeltaRows; ++r) {
+        const float sum = sum_lanes<S::L>(dot16<T>(o[r], g[r], 0.f));
+        if (lane == 0) a.delta[row[r]] = sum;
+    }
+}
+
+// The same of the rows with few keys, as sum p dp.
+template <typename T, int D>
+__device__ __forceinline__ void few_rows(const Args &a, int block, int blocks) {
+    using S = DeltaShape<T, D>;
+    constexpr int GROUPS = 256 / S::L;
+    const long long n = (long long)a.n_seq * attn::kFewKeys * a.Hq;
+    const int lane = threadIdx.x % S::L;
+    for (long long x0 = (long long)block * GROUPS; x0 < n; x0 += (long long)blocks * GROUPS) {
+        const long long x = min(x0 + threadIdx.x / S::L, n - 1), y = x / a.Hq;
+        const int head = (int)(x % a.Hq);
+        const Seq q = attn::sequence(a, (int)(y / attn::kFewKeys));
+        const int shift = q.lk - q.lq, i = (int)(y % attn::kFewKeys) + max(0, -shift);
+        int keys = i + shift + 1;
+        if (i >= q.lq || keys > attn::kFewKeys) keys = 0;
+        const int most = __reduce_max_sync(0xffffffffu, keys);
+        const long long row = (q.q0 + i) * a.Hq + head;
+        const long long own = (long long)head * D + lane * S::V;
+        const long long shared = (long long)(head / a.G) * D + lane * S::V;
+        uint4 qx = make_uint4(0, 0, 0, 0), gx = qx;
+        float l = 0.f, sum = 0.f;
+        if (keys > 0) {
+            qx = ld16(static_cast<const T *>(a.q) + (q.q0 + i) * a.q_stride + own);
+            gx = ld16(static_cast<const T *>(a.go) + (q.q0 + i) * a.go_stride + own);
+            l = a.lse_in[row] * 1.4426950408889634f;
+        }
+        for (int j = 0; j < most; ++j) {
+            float score = 0.f, dp = 0.f;
+            if (j < keys) {
+                const T *k = static_cast<const T *>(a.k) + (q.k0 + j) * a.k_stride + shared;
+                const T *v = static_cast<const T *>(a.v) + (q.k0 + j) * a.v_stride + shared;
+                score = dot16<T>(qx, ld16(k), 0.f);
+                dp = dot16<T>(gx, ld16(v), 0.f);
+            }
+            score = sum_lanes<S::L>(score);
+            dp = sum_lanes<S::L>(dp);
+            if (j < keys) sum = fmaf(exp2f(fmaf(score, a.scale_log2, -l)), dp, sum);
+        }
+        if (keys > 0 && lane == 0) a.delta_few[row] = sum;
+    }
+}
+
+// The first blocks take the rows with few keys: their keys one after another
+// take about as long as all other rows.
+template <typename T, int D>
+__global__ void __launch_bounds__(256, 6) attn_delta_kernel(const __grid_constant__ Args a,
+                                                         int few_blocks) {
+    attn::clear_status(a);
+    if (attn::rejected(a)) return;
+    if ((int)blockIdx.x < few_blocks) few_rows<T, D>(a, blockIdx.x, few_blocks);
+    else delta_rows<T, D>(a, blockIdx.x - few_blocks);
 }
 
 // o = sum_s exp(lse_s - lse) o_s, lse = log sum_s exp(lse_s): 16 lanes a row.
@@ -553,8 +641,14 @@ cudaError_t launch_attn_simt_bwd(const Args &keys, const Args &rows, int tile, i
 }
 
 cudaError_t launch_attn_delta(const Args &a, int d, int dtype, cudaStream_t s) {
-    const long long blocks = ((long long)a.total_q * a.Hq + 15) / 16;
-    KLA_BY_TYPE(d, dtype, (attn_delta_kernel<T, D><<<(unsigned)blocks, 256, 0, s>>>(a)));
+    // 16-byte parts of a row; groups of lanes of a block, see DeltaShape
+    const int parts = d * (dtype == 1 ? 2 : 4) / 16, groups = 256 / parts;
+    const long long rows = (long long)a.total_q * a.Hq;
+    const long long blocks = (rows + groups * kDeltaRows - 1) / (groups * kDeltaRows);
+    long long few = 0;
+    if (a.delta_few != a.delta && (a.cu_q || a.Tk - a.Tq < attn::kFewKeys))
+        few = min(((long long)a.n_seq * attn::kFewKeys * a.Hq + groups - 1) / groups, 4096ll);
+    KLA_BY_TYPE(d, dtype, (attn_delta_kernel<T, D><<<(unsigned)(few + blocks), 256, 0, s>>>(a, (int)few)));
     note_launch();
     return cudaGetLastError();
 }

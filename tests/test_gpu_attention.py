@@ -193,6 +193,32 @@ def test_many_calls_end_and_give_the_same_bits(d):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("hq, hk, d", [(8, 4, 64), (2, 2, 128), (160, 1, 64)])
+def test_rows_with_one_key_have_no_score_gradient(hq, hk, d):
+    """p is 1, so dS = p (dp - p dp) is zero but for fp32: both dp are off by
+    d u sum |dO V|, both p by 2 e, and nothing that was rounded to bf16 is in it."""
+    lens = [1, 130, 1, 0, 1, 1, 40, 1]
+    data = [_inputs(n, n, hq, hk, d, BF16, seed=50 + i) for i, n in enumerate(lens)]
+    q, k, v, go = (torch.cat(x).cuda() for x in zip(*data))
+    cu = torch.tensor([0] + lens).cumsum(0).int().cuda()
+    o, lse = kla.kla_attn_fwd_varlen(q, k, v, cu, check_status=True)
+    dq, dk, _ = kla.kla_attn_bwd_varlen(q, k, v, o, lse, go, cu, check_status=True)
+    scale, at = 1 / math.sqrt(d), 0
+    for i, n in enumerate(lens):
+        qq, kk, vv, gg = (x.double() for x in data[i])
+        if n:
+            qq, gg = (x[0].reshape(hk, hq // hk, d) for x in (qq, gg))     # the first row
+            kk, vv = kk[0][:, None], vv[0][:, None]
+            e = (d + 8) * U * (qq.abs() * kk.abs()).sum(-1, keepdim=True) * scale + 1e-6
+            dots = (gg.abs() * vv.abs()).sum(-1, keepdim=True)
+            ds = scale * (2 * d * U + 4 * e) * dots * (1 + 2.0 ** -6)
+            got = dq[at].cpu().double().reshape(hk, hq // hk, d)
+            assert (got.abs() <= ds * kk.abs()).all(), i
+            if n == 1:
+                assert (dk[at].cpu().double().abs() <= (ds * qq.abs()).sum(1)).all(), i
+        at += n
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("tq", [1, 3, 150])
 def test_padded_cache_with_anything_behind_its_lengths(dtype, tq):
