@@ -47,14 +47,32 @@ int simt_rows(const AttnProblem &p, bool keys) {
     return each <= 16 || side(p, keys, mult, 64).items * p.Hk < sm_count() ? 16 : 64;
 }
 
-// Parts of the key axis: enough that every SM has a block, each at least 4
-// tiles of 64 keys, so that the join's traffic stays small beside the keys'.
-int key_splits(const AttnProblem &p, long long blocks, int wanted, int tile) {
-    if (blocks >= wanted) return 1;
-    const long long tiles = ceil_div(p.total_k, (long long)p.n_seq * tile);
-    long long n = ceil_div(wanted, blocks < 1 ? 1 : blocks);
-    if (n > tiles / 4) n = tiles / 4;
-    return n < 1 ? 1 : (int)n;
+// The number of parts of `tiles` key tiles that makes a launch shortest, each
+// part of at least `least` tiles: waves of blocks, `slots` at a time, times the
+// tiles that each walks and `extra` tiles' time for its start and end; a join
+// takes `extra` tiles' time too.  Only where there are under two waves.
+int cheapest_splits(long long blocks, long long tiles, int slots, int extra, int least) {
+    if (blocks < 1 || blocks >= 2 * slots) return 1;
+    int best = 1;
+    long long cost = 0;
+    for (int n = 1; n <= 64 && n * least < tiles + least; ++n) {
+        const long long c = ceil_div(blocks * n, slots) * (ceil_div(tiles, n) + extra) +
+                            (n > 1 ? extra : 0);
+        if (n == 1 || c < cost) {
+            cost = c;
+            best = n;
+        }
+    }
+    return best;
+}
+
+// Parts of the key axis on the CUDA cores: as on the tensor cores below, with
+// two blocks per SM, tiles of 64 keys, and a tile's time for a block's start and
+// end and for the join.  In fp32, one part and the
+// chosen: B 1, T 256, 2 heads of 64 18 and 16 us; one token over 32768 keys of 8
+// heads of 64 1544 and 96 us; of B 16 over 4096 keys of 4 heads of 128 367 and 181.
+int simt_splits(const AttnProblem &p, long long blocks) {
+    return cheapest_splits(blocks, ceil_div(p.total_k, (long long)p.n_seq * 64), 2 * sm_count(), 1, 1);
 }
 
 // The tensor cores take bf16 with groups that fit into a tile's 128 rows.
@@ -68,19 +86,8 @@ bool on_tensor_cores(const AttnProblem &p) {
 // CTA's start and end).  Only where the unsplit launch has under two waves of
 // CTAs that all walk about the same tiles, that is few query rows.
 int tc_splits(const AttnProblem &p, long long blocks) {
-    const int sms = sm_count();
     const long long tiles = ceil_div(p.total_k, (long long)p.n_seq * attn::kTile);
-    if (blocks < 1 || blocks >= 2 * sms) return 1;
-    int best = 1;
-    long long least = 0;
-    for (int n = 1; n <= 64 && n <= (tiles + 1) / 2; ++n) {
-        const long long cost = ceil_div(blocks * n, sms) * (ceil_div(tiles, n) + 4) + (n > 1 ? 4 : 0);
-        if (n == 1 || cost < least) {
-            least = cost;
-            best = n;
-        }
-    }
-    return best;
+    return cheapest_splits(blocks, tiles, sm_count(), 4, 2);
 }
 
 struct FwdPlan {
@@ -99,7 +106,7 @@ FwdPlan fwd_plan(const AttnProblem &p) {
     } else {
         f.rows = simt_rows(p, false);
         f.q = side(p, false, G, f.rows);
-        f.splits = key_splits(p, f.q.items * p.Hk, 2 * sm_count(), 64);
+        f.splits = simt_splits(p, f.q.items * p.Hk);
     }
     size_t at = kWsHeader;
     f.table = at;
@@ -207,7 +214,9 @@ size_t attn_bwd_workspace_bytes(const AttnProblem &p) { return bwd_plan(p).bytes
 bool attn_too_large(const AttnProblem &p) {
     const int G = p.Hq / p.Hk;
     const long long q = side(p, false, G, 16).items, k = side(p, true, 1, 16).items;
-    const long long rows = ((long long)p.total_q * p.Hq + 15) / 16;
+    // rows are counted in 32 bits, up to a tile past the last (as many of the
+    // smallest size are 275 GB)
+    const long long rows = (long long)p.total_q * p.Hq + attn::kTile;
     return q * p.Hk > INT32_MAX || k * p.Hk > INT32_MAX || rows > INT32_MAX;
 }
 

@@ -14,10 +14,16 @@
 // 256 threads as 16 x 16; thread (ty, tx) holds the scores of rows ty + 16 i
 // and keys tx + 16 j, and of the outputs rows ty + 16 i, features 4 tx + 64 j.
 // Rows in shared memory are 4 floats longer than d, so that the 16-byte reads
-// of 8 neighbouring keys fall into different banks.
+// of 8 neighbouring keys fall into different banks.  A tile's rows are read
+// from memory into registers a step ahead.  Bound by the reads of shared memory
+// (a 16-byte read for 2 to 3 multiply-adds of a thread); few blocks: by the
+// steps' latency, 4 to 5 us each.  fp32, forward and backward: B 1, T 256, 2
+// heads of 64 16 and 39 us; B 4, T 2048, 8 heads of 64 0.53 and 1.73 ms (16 and
+// 25 TFLOP/s); single tokens of B 16, 16 + 4 heads of 128 over 4096 keys 181 us.
 #include <cuda_bf16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "kla_attn.cuh"
 
@@ -44,37 +50,55 @@ __device__ __forceinline__ void st4(__nv_bfloat16 *p, float4 x) {
                                                reinterpret_cast<const uint32_t &>(b));
 }
 
-// ROWS query-side rows (packed) of a tile into dst[ROWS][D + 4]; rows past the
-// sequence's last are zero.
+// ROWS rows of a tile on their way to shared memory, a part of them in each
+// thread's registers: asked for a step ahead, so that the wait for memory runs
+// under the products of the step before.
 template <typename T, int D, int ROWS>
-__device__ __forceinline__ void load_rows(float *dst, const T *src, long long stride,
-                                          const Args &a, const Seq &q, int head, long long row0) {
-    for (int i = threadIdx.x; i < ROWS * D / 4; i += kT) {
-        const int r = i / (D / 4), c = i % (D / 4) * 4;
-        const long long row = row0 + r;
-        const int tok = (int)(row / a.G), g = (int)(row % a.G);
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (tok < q.lq) x = ld4(src + (q.q0 + tok) * stride + (long long)(head * a.G + g) * D + c);
-        *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) = x;
+struct Ahead {
+    using Raw = std::conditional_t<sizeof(T) == 4, float4, uint2>;      // 4 features
+    static constexpr int N = ROWS * D / 4 / kT;
+    static_assert(N * kT * 4 == ROWS * D, "whole parts");
+    Raw x[N];
+
+    __device__ __forceinline__ void take(int z, const T *p, bool on) {
+        x[z] = Raw{};
+        if (on) x[z] = *reinterpret_cast<const Raw *>(p);
     }
-}
-// ROWS keys or values from j0 into dst[ROWS][D + 4]; zero past the last.
-template <typename T, int D, int ROWS>
-__device__ __forceinline__ void load_keys(float *dst, const T *src, long long stride, const Seq &q,
-                                          int head, int j0) {
-    for (int i = threadIdx.x; i < ROWS * D / 4; i += kT) {
-        const int r = i / (D / 4), c = i % (D / 4) * 4;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j0 + r < q.lk) x = ld4(src + (q.k0 + j0 + r) * stride + (long long)head * D + c);
-        *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) = x;
+    // Query-side rows (packed); zero past the sequence's last.
+    __device__ __forceinline__ void rows(const T *src, long long stride, const Args &a,
+                                         const Seq &q, int head, int row0) {
+#pragma unroll
+        for (int z = 0; z < N; ++z) {
+            const int i = threadIdx.x + z * kT, row = row0 + i / (D / 4), c = i % (D / 4) * 4;
+            const int tok = (int)((unsigned)row / (unsigned)a.G), g = row - tok * a.G;
+            take(z, src + (q.q0 + tok) * stride + (long long)(head * a.G + g) * D + c, tok < q.lq);
+        }
     }
-}
+    // Keys or values from j0; zero past the last.
+    __device__ __forceinline__ void keys(const T *src, long long stride, const Seq &q, int head,
+                                         int j0) {
+#pragma unroll
+        for (int z = 0; z < N; ++z) {
+            const int i = threadIdx.x + z * kT, r = i / (D / 4), c = i % (D / 4) * 4;
+            take(z, src + (q.k0 + j0 + r) * stride + (long long)head * D + c, j0 + r < q.lk);
+        }
+    }
+    // Into dst[ROWS][D + 4].
+    __device__ __forceinline__ void put(float *dst) const {
+#pragma unroll
+        for (int z = 0; z < N; ++z) {
+            const int i = threadIdx.x + z * kT;
+            *reinterpret_cast<float4 *>(dst + i / (D / 4) * (D + 4) + i % (D / 4) * 4) =
+                ld4(reinterpret_cast<const T *>(&x[z]));
+        }
+    }
+};
 
 // acc[i][j] += sum_c A[ty + 16 i][c] B[tx + 16 j][c] over the D features.
 template <int D, int MI, int NJ>
 __device__ __forceinline__ void dots(const float *A, const float *B, float (&acc)[MI][NJ]) {
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-#pragma unroll 4
+#pragma unroll 8
     for (int c = 0; c < D; c += 4) {
         float4 x[MI], y[NJ];
 #pragma unroll
@@ -94,7 +118,7 @@ __device__ __forceinline__ void dots(const float *A, const float *B, float (&acc
 template <int D, int MI, int N, int LD>
 __device__ __forceinline__ void mix(const float *W, const float *X, float4 (&acc)[MI][D / 64]) {
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-#pragma unroll 2
+#pragma unroll 4
     for (int n = 0; n < N; n += 4) {
         float4 w[MI];
 #pragma unroll
@@ -132,19 +156,23 @@ __global__ void __launch_bounds__(kT) attn_simt_fwd_kernel(const __grid_constant
     if (!attn::item_of(a, blockIdx.x, true, it)) return;
     const Seq s = attn::sequence(a, it.seq);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    const long long row0 = (long long)it.tile * BM, rows = (long long)s.lq * a.G;
-    load_rows<T, D, BM>(Q, static_cast<const T *>(a.q), a.q_stride, a, s, it.head, row0);
-    const long long last = row0 + BM < rows ? row0 + BM - 1 : rows - 1;
-    const int seen = (int)(last / a.G) + 1 + s.lk - s.lq;      // keys of the last row
+    const int row0 = it.tile * BM, rows = s.lq * a.G;
+    const int seen = (min(row0 + BM, rows) - 1) / a.G + 1 + s.lk - s.lq;      // keys of the last row
     int begin, end;
     attn::split_range(seen > 0 ? (seen + 63) / 64 : 0, a.splits, it.split, begin, end);
+    const T *key = static_cast<const T *>(a.k), *value = static_cast<const T *>(a.v);
+    Ahead<T, D, BM> q;
+    Ahead<T, D, 64> kv;
+    q.rows(static_cast<const T *>(a.q), a.q_stride, a, s, it.head, row0);
+    if (begin < end) kv.keys(key, a.k_stride, s, it.head, begin * 64);
+    q.put(Q);
     int limit[MI];                                             // last key of each row
     float m[MI], l[MI];
     float4 acc[MI][D / 64];
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-        const long long r = row0 + ty + 16 * i;
-        limit[i] = r < rows ? (int)(r / a.G) + s.lk - s.lq : -1;
+        const int r = row0 + ty + 16 * i;
+        limit[i] = r < rows ? r / a.G + s.lk - s.lq : -1;
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
@@ -152,8 +180,9 @@ __global__ void __launch_bounds__(kT) attn_simt_fwd_kernel(const __grid_constant
     }
     for (int kb = begin; kb < end; ++kb) {
         __syncthreads();
-        load_keys<T, D, 64>(KV, static_cast<const T *>(a.k), a.k_stride, s, it.head, kb * 64);
+        kv.put(KV);
         __syncthreads();
+        kv.keys(value, a.v_stride, s, it.head, kb * 64);
         float x[MI][4];
 #pragma unroll
         for (int i = 0; i < MI; ++i)
@@ -161,7 +190,8 @@ __global__ void __launch_bounds__(kT) attn_simt_fwd_kernel(const __grid_constant
             for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
         dots<D, MI, 4>(Q, KV, x);
         __syncthreads();
-        load_keys<T, D, 64>(KV, static_cast<const T *>(a.v), a.v_stride, s, it.head, kb * 64);
+        kv.put(KV);
+        if (kb + 1 < end) kv.keys(key, a.k_stride, s, it.head, kb * 64 + 64);
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             float mx = m[i];
@@ -197,10 +227,10 @@ __global__ void __launch_bounds__(kT) attn_simt_fwd_kernel(const __grid_constant
     }
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-        const long long r = row0 + ty + 16 * i;
+        const int r = row0 + ty + 16 * i;
         if (r >= rows) continue;
         const long long tok = s.q0 + r / a.G;
-        const int head = it.head * a.G + (int)(r % a.G);
+        const int head = it.head * a.G + r % a.G;
         const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
         const float lse = l[i] == 0.f ? -INFINITY : m[i] * kLn2 + logf(l[i]);
         long long at = (tok * a.Hq + head) * D;
@@ -260,21 +290,29 @@ __device__ void attn_simt_dq(const Args &a, int block, float *sm) {
     if (!attn::item_of(a, block, true, it)) return;
     const Seq s = attn::sequence(a, it.seq);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    const long long row0 = (long long)it.tile * BM, rows = (long long)s.lq * a.G;
-    load_rows<T, D, BM>(Q, static_cast<const T *>(a.q), a.q_stride, a, s, it.head, row0);
-    load_rows<T, D, BM>(G, static_cast<const T *>(a.go), a.go_stride, a, s, it.head, row0);
-    const long long last = row0 + BM < rows ? row0 + BM - 1 : rows - 1;
-    const int seen = (int)(last / a.G) + 1 + s.lk - s.lq;
+    const int row0 = it.tile * BM, rows = s.lq * a.G;
+    const int seen = (min(row0 + BM, rows) - 1) / a.G + 1 + s.lk - s.lq;
     const int tiles = seen > 0 ? (seen + 31) / 32 : 0;
+    const T *key = static_cast<const T *>(a.k), *value = static_cast<const T *>(a.v);
+    Ahead<T, D, BM> own;
+    Ahead<T, D, 32> k, v;
+    if (tiles > 0) {
+        k.keys(key, a.k_stride, s, it.head, 0);
+        v.keys(value, a.v_stride, s, it.head, 0);
+    }
+    own.rows(static_cast<const T *>(a.q), a.q_stride, a, s, it.head, row0);
+    own.put(Q);
+    own.rows(static_cast<const T *>(a.go), a.go_stride, a, s, it.head, row0);
+    own.put(G);
     int limit[MI];
     float lse2[MI], delta[MI];
     float4 acc[MI][D / 64];
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-        const long long r = row0 + ty + 16 * i;
+        const int r = row0 + ty + 16 * i;
         const bool on = r < rows;
-        limit[i] = on ? (int)(r / a.G) + s.lk - s.lq : -1;
-        const long long at = (s.q0 + r / a.G) * a.Hq + it.head * a.G + (int)(r % a.G);
+        limit[i] = on ? r / a.G + s.lk - s.lq : -1;
+        const long long at = (s.q0 + r / a.G) * a.Hq + it.head * a.G + r % a.G;
         lse2[i] = on ? a.lse_in[at] / kLn2 : 0.f;
         delta[i] = on ? attn::delta_of(a, at, limit[i] + 1) : 0.f;
 #pragma unroll
@@ -282,9 +320,13 @@ __device__ void attn_simt_dq(const Args &a, int block, float *sm) {
     }
     for (int kb = 0; kb < tiles; ++kb) {
         __syncthreads();
-        load_keys<T, D, 32>(K, static_cast<const T *>(a.k), a.k_stride, s, it.head, kb * 32);
-        load_keys<T, D, 32>(V, static_cast<const T *>(a.v), a.v_stride, s, it.head, kb * 32);
+        k.put(K);
+        v.put(V);
         __syncthreads();
+        if (kb + 1 < tiles) {
+            k.keys(key, a.k_stride, s, it.head, kb * 32 + 32);
+            v.keys(value, a.v_stride, s, it.head, kb * 32 + 32);
+        }
         float p[MI][2], ds[MI][2];
         grads_tile<D, MI, 2>(Q, K, G, V, limit, lse2, delta, kb * 32, a, p, ds);
 #pragma unroll
@@ -296,9 +338,9 @@ __device__ void attn_simt_dq(const Args &a, int block, float *sm) {
     }
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-        const long long r = row0 + ty + 16 * i;
+        const int r = row0 + ty + 16 * i;
         if (r >= rows) continue;
-        const long long at = ((s.q0 + r / a.G) * a.Hq + it.head * a.G + (int)(r % a.G)) * D;
+        const long long at = ((s.q0 + r / a.G) * a.Hq + it.head * a.G + r % a.G) * D;
 #pragma unroll
         for (int j = 0; j < D / 64; ++j)
             st4(static_cast<T *>(a.dq) + at + 4 * tx + 64 * j, acc[i][j]);
@@ -323,21 +365,45 @@ __device__ void attn_simt_dkv(const Args &a, int block, float *sm) {
     const Seq s = attn::sequence(a, it.seq);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const int j0 = it.tile * BN;
-    load_keys<T, D, BN>(K, static_cast<const T *>(a.k), a.k_stride, s, it.head, j0);
-    load_keys<T, D, BN>(V, static_cast<const T *>(a.v), a.v_stride, s, it.head, j0);
+    const T *query = static_cast<const T *>(a.q), *grad = static_cast<const T *>(a.go);
+    const int rows = s.lq * a.G;
+    const int first = max(0, j0 + s.lq - s.lk) * a.G / 32 * 32;   // rows of the first query that sees key j0
+    Ahead<T, D, BN> own;
+    Ahead<T, D, 32> q, g;
+    float lse2[2], delta[2];
+    int limit[2];
+    const auto fetch = [&](int row0) {
+        if (row0 >= rows) return;
+        q.rows(query, a.q_stride, a, s, it.head, row0);
+        g.rows(grad, a.go_stride, a, s, it.head, row0);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = row0 + tx + 16 * j, tok = r / a.G;
+            const bool on = r < rows;
+            limit[j] = on ? tok + s.lk - s.lq : -1;
+            const long long at = (s.q0 + tok) * a.Hq + it.head * a.G + r % a.G;
+            lse2[j] = on ? a.lse_in[at] / kLn2 : 0.f;
+            delta[j] = on ? attn::delta_of(a, at, limit[j] + 1) : 0.f;
+        }
+    };
+    fetch(first);
+    own.keys(static_cast<const T *>(a.k), a.k_stride, s, it.head, j0);
+    own.put(K);
+    own.keys(static_cast<const T *>(a.v), a.v_stride, s, it.head, j0);
+    own.put(V);
     float4 dk[MI][D / 64], dv[MI][D / 64];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) dk[i][j] = dv[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const long long rows = (long long)s.lq * a.G;
-    const int first = j0 + s.lq - s.lk;          // the first query that sees key j0
-    for (long long row0 = (long long)(first > 0 ? first : 0) * a.G / 32 * 32; row0 < rows;
-         row0 += 32) {
+    for (int row0 = first; row0 < rows; row0 += 32) {
         __syncthreads();
-        load_rows<T, D, 32>(Q, static_cast<const T *>(a.q), a.q_stride, a, s, it.head, row0);
-        load_rows<T, D, 32>(G, static_cast<const T *>(a.go), a.go_stride, a, s, it.head, row0);
+        q.put(Q);
+        g.put(G);
         __syncthreads();
+        const float l[2] = {lse2[0], lse2[1]}, dl[2] = {delta[0], delta[1]};
+        const int last[2] = {limit[0], limit[1]};
+        fetch(row0 + 32);
         float p[MI][2], ds[MI][2];
 #pragma unroll
         for (int i = 0; i < MI; ++i)
@@ -347,20 +413,14 @@ __device__ void attn_simt_dkv(const Args &a, int block, float *sm) {
         dots<D, MI, 2>(V, G, ds);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const long long r = row0 + tx + 16 * j;
-            const bool on_r = r < rows;
-            const int limit = on_r ? (int)(r / a.G) + s.lk - s.lq : -1;
-            const long long at = (s.q0 + r / a.G) * a.Hq + it.head * a.G + (int)(r % a.G);
-            const float lse2 = on_r ? a.lse_in[at] / kLn2 : 0.f;
-            const float delta = on_r ? attn::delta_of(a, at, limit + 1) : 0.f;
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 const int key = j0 + ty + 16 * i;
-                const bool on = key <= limit && key < s.lk;
-                const float pv = on ? exp2f(p[i][j] * a.scale_log2 - lse2) : 0.f;
+                const bool on = key <= last[j] && key < s.lk;
+                const float pv = on ? exp2f(p[i][j] * a.scale_log2 - l[j]) : 0.f;
                 P[(ty + 16 * i) * 36 + tx + 16 * j] = pv;
                 S[(ty + 16 * i) * 36 + tx + 16 * j] =
-                    on ? pv * (ds[i][j] - delta) * a.scale : 0.f;
+                    on ? pv * (ds[i][j] - dl[j]) * a.scale : 0.f;
             }
         }
         __syncthreads();
@@ -382,7 +442,7 @@ __device__ void attn_simt_dkv(const Args &a, int block, float *sm) {
 
 // Both sides in one launch: the blocks of the key tiles first.
 template <typename T, int D, int B>
-__global__ void __launch_bounds__(kT)
+__global__ void __launch_bounds__(kT, D == 64 ? 2 : 1)
 attn_simt_bwd_kernel(const __grid_constant__ Args keys, const __grid_constant__ Args rows,
                      int key_blocks) {
     extern __shared__ __align__(16) float sm[];
