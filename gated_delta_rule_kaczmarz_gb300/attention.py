@@ -14,6 +14,7 @@ import functools
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .binding import KlaError, load
 
@@ -77,17 +78,22 @@ def _dense(t, name, dtype, device, shape):
     return t.data_ptr()
 
 
-def _call(device, stream, fn, *args):
+def _given(stream, t):
+    """A caller's stream (a torch stream or a handle) made current, so that
+    what a call allocates belongs to the stream that uses it."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = (torch.cuda.ExternalStream(int(stream), device=t.device) if stream
+                  else torch.cuda.default_stream(t.device))
+    return torch.cuda.stream(stream)
+
+
+def _call(device, fn, *args):
     """Runs a library call with the tensors' device current and its stream
     last in the arguments; raises on a non-OK status."""
     if torch.cuda.current_device() != device:
         with torch.cuda.device(device):
-            return _call(device, stream, fn, *args)
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device)
-    elif hasattr(stream, "cuda_stream"):
-        stream = stream.cuda_stream
-    status = fn(*args, stream)
+            return _call(device, fn, *args)
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     if status:
         lib = load()
         raise KlaError(status, lib.kla_last_error_message().decode() or
@@ -181,6 +187,10 @@ def kla_qk_norm_rope_fwd(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, 
     norm_k: "rms", "l2" or "none"; style "half" (features i, i + rot/2) or
     "pairs" (2i, 2i + 1).  q_out, k_out may be q and k (in place).  Returns
     (q_out, k_out)."""
+    if stream is not None:
+        with _given(stream, q):
+            return kla_qk_norm_rope_fwd(q, k, positions, inv_freq, wq, wk, eps, norm_q, norm_k,
+                                        sections, style, q_out, k_out)
     dev, dt, ins, end = _conditioning(q, k, positions, inv_freq, wq, wk, sections, norm_q,
                                       norm_k, style)
     q_out, qo = _out_rows(q_out, "q_out", q)
@@ -189,7 +199,7 @@ def kla_qk_norm_rope_fwd(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, 
         k_out = None
     else:
         k_out, ko = _out_rows(k_out, "k_out", k)
-    _call(dev, stream, load().kla_qk_norm_rope_fwd, *ins, q_out.data_ptr(), qo, _at(k_out), ko,
+    _call(dev, load().kla_qk_norm_rope_fwd, *ins, q_out.data_ptr(), qo, _at(k_out), ko,
           *end, eps, dt)
     return q_out, k_out
 
@@ -204,6 +214,10 @@ def kla_qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, wq=None, wk=
     """Backward of kla_qk_norm_rope_fwd on the same inputs: dq_out, dk_out are
     the gradients of its outputs.  Returns (dq, dk, dwq, dwk), None for what is
     not there (k, a weight)."""
+    if stream is not None:
+        with _given(stream, q):
+            return kla_qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, wq, wk, eps,
+                                        norm_q, norm_k, sections, style, dq, dk, workspace)
     dev, dt, ins, end = _conditioning(q, k, positions, inv_freq, wq, wk, sections, norm_q,
                                       norm_k, style)
     gqs = _rows(dq_out, "dq_out", q.dtype, dev, q.shape)
@@ -224,7 +238,7 @@ def kla_qk_norm_rope_bwd(q, k, positions, inv_freq, dq_out, dk_out, wq=None, wk=
                                     workspace)
     else:
         workspace = None
-    _call(dev, stream, lib.kla_qk_norm_rope_bwd, *ins, dq_out.data_ptr(), gqs, _at(dk_out), gks,
+    _call(dev, lib.kla_qk_norm_rope_bwd, *ins, dq_out.data_ptr(), gqs, _at(dk_out), gks,
           dq.data_ptr(), dqs, _at(dk), dks, _at(dwq), _at(dwk), *end, eps, dt, _at(workspace),
           wsb)
     return dq, dk, dwq, dwk
@@ -248,6 +262,7 @@ class _QkNormRope(torch.autograd.Function):
         return out if k is not None else out[0]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *grads):
         q, k, positions, inv_freq, wq, wk = ctx.saved_tensors
         gk = None if k is None else _dense_rows(grads[1], k)
@@ -314,6 +329,9 @@ def kla_attn_fwd(q, k, v, scale=None, k_lens=None, o=None, lse=None, return_lse=
     k_lens: int32 [B], the keys of each sequence of a padded cache, or None
     (all Tk); scale: 1/sqrt(d) unless given.  Returns (o, lse), o dense, lse
     [B,Tq,Hq] fp32 (None with return_lse=False)."""
+    if stream is not None:
+        with _given(stream, q):
+            return kla_attn_fwd(q, k, v, scale, k_lens, o, lse, return_lse, workspace)
     dev, dt, rows, (hq, hk, d) = _qkv(q, k, v, 4)
     B, Tq, Tk = q.shape[0], q.shape[1], k.shape[1]
     lens = _dense(k_lens, "k_lens", torch.int32, dev, (B,))
@@ -323,7 +341,7 @@ def kla_attn_fwd(q, k, v, scale=None, k_lens=None, o=None, lse=None, return_lse=
         lse, stats = _out(lse, "lse", (B, Tq, hq), torch.float32, q)
     lib, sizes = load(), (B, Tq, Tk, hq, hk, d, dt)
     workspace, wsb = _workspace(dev, lib.kla_attn_fwd_workspace_size, sizes, q, workspace)
-    _call(dev, stream, lib.kla_attn_fwd, *rows, lens, _scale(scale, d), at, stats, *sizes,
+    _call(dev, lib.kla_attn_fwd, *rows, lens, _scale(scale, d), at, stats, *sizes,
           _at(workspace), wsb)
     return o, lse
 
@@ -341,6 +359,10 @@ def kla_attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, o=
     """kla_attn_fwd over packed sequences: q [total_q,Hq,d], k, v [total_k,Hk,d],
     cu_seqlens_q, cu_seqlens_k: int32 [N+1] on the device (cu_seqlens_k None:
     the same table).  Returns (o, lse)."""
+    if stream is not None:
+        with _given(stream, q):
+            return kla_attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, o, lse,
+                                       return_lse, workspace, check_status=check_status)
     dev, dt, rows, (hq, hk, d) = _qkv(q, k, v, 3)
     cu_q, cu_k, N = _tables(q, dev, cu_seqlens_q, cu_seqlens_k)
     o, at = _out(o, "o", q.shape, q.dtype, q)
@@ -349,15 +371,14 @@ def kla_attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, o=
         lse, stats = _out(lse, "lse", q.shape[:-1], torch.float32, q)
     lib, sizes = load(), (N, q.shape[0], k.shape[0], hq, hk, d, dt)
     workspace, wsb = _workspace(dev, lib.kla_attn_fwd_varlen_workspace_size, sizes, q, workspace)
-    _call(dev, stream, lib.kla_attn_fwd_varlen, *rows, cu_q, cu_k, _scale(scale, d), at, stats,
+    _call(dev, lib.kla_attn_fwd_varlen, *rows, cu_q, cu_k, _scale(scale, d), at, stats,
           *sizes, _at(workspace), wsb)
     if check_status:
-        _call(dev, None, _status, workspace, wsb, stream)
+        _call(dev, _status, workspace, wsb)
     return o, lse
 
 
-def _status(workspace, wsb, stream, current):
-    stream = current if stream is None else getattr(stream, "cuda_stream", stream)
+def _status(workspace, wsb, stream):
     return load().kla_workspace_status(_at(workspace), wsb, stream)
 
 
@@ -377,11 +398,14 @@ def kla_attn_bwd(q, k, v, o, lse, d_o, scale=None, dq=None, dk=None, dv=None, wo
                  stream=None):
     """Backward of kla_attn_fwd (without k_lens): the gradients of sum <d_o, o>
     from the forward's inputs and its o and lse.  Returns (dq, dk, dv), dense."""
+    if stream is not None:
+        with _given(stream, q):
+            return kla_attn_bwd(q, k, v, o, lse, d_o, scale, dq, dk, dv, workspace)
     dev, dt, rows, (hq, hk, d) = _qkv(q, k, v, 4)
     ins, at, grads = _grads(q, k, v, o, lse, d_o, dev, dq, dk, dv)
     lib, sizes = load(), (q.shape[0], q.shape[1], k.shape[1], hq, hk, d, dt)
     workspace, wsb = _workspace(dev, lib.kla_attn_bwd_workspace_size, sizes, q, workspace)
-    _call(dev, stream, lib.kla_attn_bwd, *rows, *ins, _scale(scale, d), *at, *sizes,
+    _call(dev, lib.kla_attn_bwd, *rows, *ins, _scale(scale, d), *at, *sizes,
           _at(workspace), wsb)
     return grads
 
@@ -390,15 +414,19 @@ def kla_attn_bwd_varlen(q, k, v, o, lse, d_o, cu_seqlens_q, cu_seqlens_k=None, s
                         dq=None, dk=None, dv=None, workspace=None, stream=None,
                         check_status=False):
     """Backward of kla_attn_fwd_varlen; otherwise as kla_attn_bwd."""
+    if stream is not None:
+        with _given(stream, q):
+            return kla_attn_bwd_varlen(q, k, v, o, lse, d_o, cu_seqlens_q, cu_seqlens_k, scale,
+                                       dq, dk, dv, workspace, check_status=check_status)
     dev, dt, rows, (hq, hk, d) = _qkv(q, k, v, 3)
     cu_q, cu_k, N = _tables(q, dev, cu_seqlens_q, cu_seqlens_k)
     ins, at, grads = _grads(q, k, v, o, lse, d_o, dev, dq, dk, dv)
     lib, sizes = load(), (N, q.shape[0], k.shape[0], hq, hk, d, dt)
     workspace, wsb = _workspace(dev, lib.kla_attn_bwd_varlen_workspace_size, sizes, q, workspace)
-    _call(dev, stream, lib.kla_attn_bwd_varlen, *rows, *ins, cu_q, cu_k, _scale(scale, d), *at,
+    _call(dev, lib.kla_attn_bwd_varlen, *rows, *ins, cu_q, cu_k, _scale(scale, d), *at,
           *sizes, _at(workspace), wsb)
     if check_status:
-        _call(dev, None, _status, workspace, wsb, stream)
+        _call(dev, _status, workspace, wsb)
     return grads
 
 
@@ -416,6 +444,7 @@ class _KlaAttn(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_o):
         q, k, v, o, lse, cu_q, cu_k = ctx.saved_tensors
         d_o = _dense_rows(d_o, o)

@@ -683,7 +683,7 @@ kla_status check_attn(const kla::AttnProblem &p) {
         return fail(KLA_ERR_UNSUPPORTED, "supported head sizes: 64 and 128 (got %d)", p.d);
     if (p.Hq > 1024) return fail(KLA_ERR_UNSUPPORTED, "at most 1024 heads (Hq=%d)", p.Hq);
     if (p.n_seq > 0 && p.total_q > 0 && kla::attn_too_large(p))
-        return fail(KLA_ERR_UNSUPPORTED, "problem too large (tiles must fit in int32)");
+        return fail(KLA_ERR_UNSUPPORTED, "problem too large (query rows times heads and tiles must fit in int32)");
     return KLA_OK;
 }
 kla_status fixed_attn(kla::AttnProblem &p, int B, int Tq, int Tk) {
@@ -705,7 +705,7 @@ kla_status packed_attn(kla::AttnProblem &p, int N, int total_q, int total_k, con
     return check_attn(p);
 }
 kla_status check_scale(float scale) {
-    if (!(scale > 0.f) || scale > 3e38f)
+    if (!(scale > 0.f) || scale > 2e38f)      // times log2 e, still finite
         return fail(KLA_ERR_INVALID_ARG, "scale must be positive and finite");
     return KLA_OK;
 }

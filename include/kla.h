@@ -435,7 +435,7 @@ KLA_API int kla_qk_norm_rope_bwd(const void *q, long long q_stride, const void *
  *              keys (clamped to 0..Tk; the rest of a padded cache is not
  *              read into a result), its queries are the last Tq of them
  *   lse      : [B, Tq, Hq] fp32, written unless NULL (kla_attn_bwd wants it)
- *   scale    : positive and finite
+ *   scale    : positive, at most 2e38
  *   workspace: kla_attn_fwd_workspace_size(...) bytes, 256-byte aligned; it
  *              starts with the device status word (kla_workspace_status), the
  *              rest is scratch.  The size depends on the SM count of the

@@ -357,6 +357,55 @@ def test_another_stream_and_a_captured_graph():
     assert all(torch.equal(a, b) for a, b in zip((*got, *grads, *packed), (*want, *ref, *again)))
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_memory_of_a_call_on_a_given_stream_belongs_to_it(handle):
+    """What the call allocates must not be a block that the current stream still
+    reads: here one of the output's size, freed while its reader waits."""
+    q, k, v, _ = (x[None].cuda() for x in _inputs(2048, 2048, 4, 4, 128, BF16, seed=6))
+    want, _ = kla.kla_attn_fwd(q, k, v)
+    side = torch.cuda.Stream()
+    ones = torch.ones_like(want)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                 # about 10 ms
+    twos = ones + 1
+    del ones
+    got, _ = kla.kla_attn_fwd(q, k, v, stream=side.cuda_stream if handle else side)
+    torch.cuda.synchronize()
+    assert bool((twos == 2).all()) and torch.equal(got, want)
+
+
+def test_calls_at_once_on_two_streams():
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    data = [tuple(x[None].cuda() for x in _inputs(n, n, 4, 2, 64, BF16, seed=n)) for n in (900, 333)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for side, (q, k, v, go), g in zip(sides, data, got):
+            with torch.cuda.stream(side):
+                o, lse = kla.kla_attn_fwd(q, k, v)
+                g.append((o, lse, *kla.kla_attn_bwd(q, k, v, o, lse, go)))
+    torch.cuda.synchronize()
+    for (q, k, v, go), g in zip(data, got):
+        o, lse = kla.kla_attn_fwd(q, k, v)
+        want = (o, lse, *kla.kla_attn_bwd(q, k, v, o, lse, go))
+        assert all(torch.equal(x, y) for run in g for x, y in zip(run, want))
+
+
+@pytest.mark.parametrize("case", [(2, 5, 300, 128, 1, 64), (1, 3, 150, 100, 1, 128),
+                                  (1, 140, 140, 130, 2, 64)])
+def test_groups_that_fill_a_tile(case):
+    test_batches(case, BF16)
+
+
+def test_a_second_derivative_is_refused():
+    q, k, v, _ = (x.cuda().requires_grad_() for x in _inputs(20, 20, 2, 1, 64, FP32, seed=9))
+    cu = torch.tensor([0, 20]).int().cuda()
+    dq, = torch.autograd.grad(kla.kla_attn(q, k, v, cu_seqlens_q=cu).square().sum(), q,
+                              create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(dq.sum(), k)
+
+
 def test_prompt_then_single_tokens_equal_the_whole_prompt():
     """The cache as it is used: a prompt, then tokens one at a time over the
     growing cache, against the whole sequence at once."""
