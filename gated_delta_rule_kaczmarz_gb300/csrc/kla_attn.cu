@@ -55,7 +55,7 @@ int cheapest_splits(long long blocks, long long tiles, int slots, int extra, int
     if (blocks < 1 || blocks >= 2 * slots) return 1;
     int best = 1;
     long long cost = 0;
-    for (int n = 1; n <= 64 && n * least < tiles + least; ++n) {
+    for (int n = 1; n <= attn::kMaxSplits && n * least < tiles + least; ++n) {
         const long long c = ceil_div(blocks * n, slots) * (ceil_div(tiles, n) + extra) +
                             (n > 1 ? extra : 0);
         if (n == 1 || c < cost) {

@@ -71,6 +71,8 @@ __device__ __forceinline__ Seq sequence(const Args &a, int s) {
 // change it by less than 0.1e-3.  fp32: delta_few is delta.  (Rows without keys
 // have a delta, 0, but no entry in delta_few.)
 constexpr int kFewKeys = 8;
+// Parts of a split key axis, at most (a multiple of the 16 lanes that join a row).
+constexpr int kMaxSplits = 64;
 __device__ __forceinline__ float delta_of(const Args &a, long long row, int keys) {
     return (keys >= 1 && keys <= kFewKeys ? a.delta_few : a.delta)[row];
 }
