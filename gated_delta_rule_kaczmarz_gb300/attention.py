@@ -55,6 +55,8 @@ def _rows(t, name, dtype, device, shape):
     st = t.stride()
     if (size[-1] > 1 and st[-1] != 1) or (size[-2] > 1 and st[-2] != size[-1]):
         raise ValueError(f"{name}: the heads of a token row must be dense (strides {st})")
+    if len(size) == 3:
+        return st[0] if size[0] > 1 else size[-2] * size[-1]
     row, step = None, None               # the leading dimensions walk one row at a time
     for n, x in zip(reversed(size[:-2]), reversed(st[:-2])):
         if n == 1:
@@ -166,14 +168,20 @@ def _conditioning(q, k, positions, inv_freq, wq, wk, sections, norm_q, norm_k, s
     return dev, dt, ins, end
 
 
+def _new(shape, dtype, like):
+    """A dense tensor on like's device."""
+    if like.is_contiguous() and like.dtype == dtype and like.shape == shape:
+        return torch.empty_like(like)            # the quicker call
+    return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def _out_rows(t, name, like):
     """An output of like's shape, made dense where there is none; with its row
     stride."""
+    shape = like.shape
     if t is None:
-        shape = like.shape
-        return (torch.empty(shape, dtype=like.dtype, device=like.device),
-                shape[-2] * shape[-1])
-    return t, _rows(t, name, like.dtype, like.get_device(), like.shape)
+        return _new(shape, like.dtype, like), shape[-2] * shape[-1]
+    return t, _rows(t, name, like.dtype, like.get_device(), shape)
 
 
 def kla_qk_norm_rope_fwd(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, norm_q="rms",
@@ -313,7 +321,7 @@ def _qkv(q, k, v, dims):
 def _out(t, name, shape, dtype, like):
     """A dense output, made where there is none; and its address."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=like.device)
+        t = _new(shape, dtype, like)
         return t, t.data_ptr()
     return t, _dense(t, name, dtype, like.get_device(), shape)
 
@@ -389,8 +397,8 @@ def _grads(q, k, v, o, lse, d_o, dev, dq, dk, dv):
     ins = (_dense(o, "o", q.dtype, dev, q.shape),
            _dense(lse, "lse", torch.float32, dev, q.shape[:-1]), d_o.data_ptr(), gs)
     dq, a = _out(dq, "dq", q.shape, q.dtype, q)
-    dk, b = _out(dk, "dk", k.shape, q.dtype, q)
-    dv, c = _out(dv, "dv", v.shape, q.dtype, q)
+    dk, b = _out(dk, "dk", k.shape, q.dtype, k)
+    dv, c = _out(dv, "dv", v.shape, q.dtype, v)
     return ins, (a, b, c), (dq, dk, dv)
 
 
