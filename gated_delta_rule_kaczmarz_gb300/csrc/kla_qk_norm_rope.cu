@@ -527,9 +527,12 @@ qk_dw_kernel(const float *part, int blocks, int d, float *dwq, float *dwk) {
     }
 }
 
-// Blocks that a launch may use: the partial sums of the backward pass are
-// sized by it, so it depends on the problem alone.
-constexpr int kMaxBlocks = 152 * 12;
+// Blocks of a launch: as many as are resident at once, so that none starts late
+// and a warp's start is paid once.  30011 tokens of 16 + 16 heads of 128 in bf16
+// take 93 us (backward 160), with three (four) times as many blocks 95 (170).
+// The partial sums of the backward pass are sized by it, so it depends on the
+// problem alone.
+constexpr int kBlocksFwd = 152 * 4, kBlocksBwd = 152 * 3;
 
 // A warp takes a token's heads in `parts` parts: one when the tokens alone
 // give every SM 32 warps (the cosines are then computed once a token), else as
@@ -560,17 +563,19 @@ QkArgs make_args(const QkProblem &p) {
 }
 
 // Blocks over the tokens, and their parts beside.
-dim3 blocks_for(const QkArgs &a) {
-    const int want = (a.tokens - 1) / kWarps + 1, most = (kMaxBlocks - 1) / a.parts + 1;
+dim3 blocks_for(const QkArgs &a, bool back) {
+    const int want = (a.tokens - 1) / kWarps + 1;
+    const int most = ((back ? kBlocksBwd : kBlocksFwd) - 1) / a.parts + 1;
     return dim3((unsigned)(want < most ? want : most), (unsigned)a.parts);
 }
 
 // The pipelined kernel's shape, or warps = 0 where it does not pay: it wants 12
 // warps of three stages in a block's shared memory (backward: 8 of two), and 4
 // tokens for each.  32768 tokens of 16 + 4 heads of 128 in bf16 take 69 us with
-// it and 77 without (backward 114 and 132), of head size 64 46 and 57; with
-// rows of 16 + 16 heads, where it has 8 warps, 106 and 97 (backward, 6 warps,
-// 196 and 172).  Both are bound by the warps' own latency, at about half of the
+// it and 74 without (backward 114 and 123), of head size 64 46 and 55 (66 and
+// 80); 65536 of 12 + 12 heads of 128, the backward's 8 warps, 260 and 284; with
+// rows of 16 + 16 heads, where it has 8 warps, 106 and 93 (backward, 6 warps,
+// 196 and 160).  Both are bound by the warps' own latency, at about half of the
 // issue slots; a copy alone would take 51 us.
 Pipe pipe_for(const QkProblem &p, bool back) {
     Pipe r{};
@@ -605,8 +610,8 @@ cudaError_t launch_pipe(const QkArgs &a, const Pipe &p, cudaStream_t s) {
 }
 template <typename T, int D, bool BACK>
 cudaError_t launch_rows(const QkArgs &a, cudaStream_t s) {
-    if (BACK) qk_bwd_kernel<T, D><<<blocks_for(a), kThreads, 0, s>>>(a);
-    else qk_fwd_kernel<T, D><<<blocks_for(a), kThreads, 0, s>>>(a);
+    if (BACK) qk_bwd_kernel<T, D><<<blocks_for(a, BACK), kThreads, 0, s>>>(a);
+    else qk_fwd_kernel<T, D><<<blocks_for(a, BACK), kThreads, 0, s>>>(a);
     note_launch();
     return cudaGetLastError();
 }
@@ -628,7 +633,7 @@ cudaError_t launch_qk(const QkProblem &p, const QkArgs &a, const Pipe &pipe, cud
 // need no more than the others' over as many tokens.
 size_t qk_bwd_workspace_bytes(const QkProblem &p) {
     if (p.tokens == 0) return 0;
-    const dim3 b = blocks_for(make_args(p));
+    const dim3 b = blocks_for(make_args(p), true);
     return (size_t)b.x * b.y * 2 * p.d * sizeof(float);
 }
 
@@ -643,7 +648,7 @@ cudaError_t launch_qk_bwd(const QkProblem &p, cudaStream_t s) {
     const Pipe pipe = pipe_for(p, true);
     cudaError_t e = launch_qk<true>(p, a, pipe, s);
     if (e != cudaSuccess || !weights) return e;
-    const dim3 b = blocks_for(a);
+    const dim3 b = blocks_for(a, true);
     qk_dw_kernel<<<2 * p.d / 32, dim3(32, 32), 0, s>>>(a.dw, pipe.warps ? 152 : (int)(b.x * b.y), p.d,
                                                        p.dwq, p.dwk);
     note_launch();
