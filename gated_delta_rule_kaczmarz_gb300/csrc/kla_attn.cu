@@ -1,5 +1,6 @@
 // Causal attention, host side: which kernels a call runs, its workspace and
 // its launches.  The kernels and their reasons are in kla_attn_simt.cu.
+#include <atomic>
 #include <mutex>
 
 #include "kla_attn_tc.cuh"
@@ -10,13 +11,16 @@ namespace {
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
+// Of the current device; a device's count is asked for once.
 int sm_count() {
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+    if (cudaGetDevice(&dev) == cudaSuccess && dev < 64 && (n = known[dev].load()) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
         cudaGetLastError();     // no device: sizes are still wanted
         return 152;
     }
+    if (dev < 64) known[dev].store(n);
     return n;
 }
 

@@ -500,8 +500,10 @@ struct Cta {
                 } else {
                     // not needed; it stays with the item, so that the barriers
                     // that it waits on next are in the phase before
-                    mbar_arrive(&sh.fin);
-                    ok = wait(&sh.fin, at.items);
+                    // (and not ahead: its arrival would count for the item before)
+                    ok = at.items == 0 || wait(&sh.fin, at.items - 1);
+                    if (ok) mbar_arrive(&sh.fin);
+                    ok = ok && wait(&sh.fin, at.items);
                 }
             }
             at.add(w);
