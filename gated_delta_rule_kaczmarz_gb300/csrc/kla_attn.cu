@@ -1,5 +1,6 @@
 // Causal attention, host side: which kernels a call runs, its workspace and
-// its launches.  The kernels and their reasons are in kla_attn_simt.cu.
+// its launches.  The kernels and their reasons are in kla_attn_tc.cu and
+// kla_attn_bwd_tc.cu (tensor cores) and kla_attn_simt.cu (CUDA cores).
 #include <atomic>
 #include <mutex>
 
