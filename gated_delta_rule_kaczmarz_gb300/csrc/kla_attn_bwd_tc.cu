@@ -46,8 +46,8 @@
 //
 // Bound: the chain of a step, through its products and the softmax, at half of
 // the tensor cores' cycles (ncu: 51%).  16 + 4 heads in bf16, with the row sums:
-// B 4, T 2048, d 128 227 us; B 1, T 32768 11.1 ms, 0.99 PFLOP/s of the five
-// products it needs (1.38 of the seven it does); d 64, B 4, T 2048 180 us.
+// B 4, T 2048, d 128 224 us; B 1, T 32768 11.1 ms, 0.99 PFLOP/s of the five
+// products it needs (1.38 of the seven it does); d 64, B 4, T 2048 177 us.
 #include "kla_attn_tc.cuh"
 
 namespace kla {
@@ -138,16 +138,11 @@ __device__ __forceinline__ void store_row(uint32_t tmem, __nv_bfloat16 *dst, flo
             for (int k = 0; k < 16; ++k) y[k] = 0;
         }
         if (on) {
-            uint4 *p = reinterpret_cast<uint4 *>(dst + 16 * j);
+            uint32_t u[8];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t u[4];
-#pragma unroll
-                for (int z = 0; z < 4; ++z)
-                    u[z] = attn::pack2(__uint_as_float(y[8 * k + 2 * z]) * f,
-                                       __uint_as_float(y[8 * k + 2 * z + 1]) * f);
-                p[k] = make_uint4(u[0], u[1], u[2], u[3]);
-            }
+            for (int z = 0; z < 8; ++z)
+                u[z] = attn::pack2(__uint_as_float(y[2 * z]) * f, __uint_as_float(y[2 * z + 1]) * f);
+            attn::store16(dst + 16 * j, u);
         }
         __syncwarp();
     }

@@ -25,7 +25,7 @@
 // Bound: the tensor cores over a prompt (4 d flops a pair and head), HBM for
 // single tokens over a cache (the key tiles pass once for all heads of a
 // group).  16 + 4 heads of 128 in bf16: B 1, T 32768 2.73 ms, 1.61 PFLOP/s; B 4,
-// T 2048 70 us, 0.98 (three to four items a CTA, and each costs about 3 us at
+// T 2048 67 us, 1.02 (three to four items a CTA, and each costs about 3 us at
 // its ends); single tokens of B 16 over 32768 keys 169 us, 6.4 TB/s.  Head size
 // 64, B 1, T 8192 186 us, 0.74 PFLOP/s: its P V has 64 columns, which take the
 // tensor cores as long as 128, and the softmax does not shrink with the head.
@@ -506,14 +506,16 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                         for (int i = 0; i < 4; ++i)
                             dst[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
                     } else if (row) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(
-                            static_cast<__nv_bfloat16 *>(a.out) + at * D + 16 * j);
+                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + at * D + 16 * j;
+                        uint32_t u[8];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            dst[i] = make_uint4(attn::pack2(f[8 * i], f[8 * i + 1]),
-                                                attn::pack2(f[8 * i + 2], f[8 * i + 3]),
-                                                attn::pack2(f[8 * i + 4], f[8 * i + 5]),
-                                                attn::pack2(f[8 * i + 6], f[8 * i + 7]));
+                        for (int i = 0; i < 8; ++i) u[i] = attn::pack2(f[2 * i], f[2 * i + 1]);
+                        if constexpr (D == 128) {       // 70 -> 67 us; head size 64 slower
+                            attn::store16(dst, u);
+                        } else {
+                            reinterpret_cast<uint4 *>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+                            reinterpret_cast<uint4 *>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+                        }
                     }
                     __syncwarp();
                 }

@@ -91,6 +91,20 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
                  : "memory");
 }
 
+// 16 bf16 values of a row: a thread stores a row of its own, so each store is a
+// sector of its own, and half of one without the 32-byte form.  It is not taken
+// where the tensor is only 16-byte aligned.
+__device__ __forceinline__ void store16(__nv_bfloat16 *p, const uint32_t (&u)[8]) {
+    if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]),
+                     "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+    }
+}
+
 // Asks for a block of this launch that has not started: the answer lands in
 // *answer (16 bytes of shared memory, 16-byte aligned) and completes 16 bytes
 // on *bar.  Not asked again once the answer was that there is none.

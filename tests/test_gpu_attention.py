@@ -272,6 +272,27 @@ def test_parts_of_a_projection_are_read_where_they_lie(dtype):
     assert all(torch.equal(a, b) for a, b in zip((*got, *grads), (*want, *ref)))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_outputs_that_are_only_16_byte_aligned(d):
+    q, k, v, go = (x[None].cuda() for x in _inputs(200, 200, 4, 2, d, BF16, seed=12))
+    want = kla.kla_attn_fwd(q, k, v)
+    grads = kla.kla_attn_bwd(q, k, v, *want, go)
+
+    def odd(t):
+        return torch.full((t.numel() + 16,), 7.0, dtype=BF16, device="cuda")
+
+    def inside(t, like):
+        return t[8:8 + like.numel()].view(like.shape)          # 16 bytes behind a 512-byte block's start
+
+    hold = [odd(x) for x in (want[0], *grads)]
+    o, dq, dk, dv = (inside(t, x) for t, x in zip(hold, (want[0], *grads)))
+    kla.kla_attn_fwd(q, k, v, o=o)
+    kla.kla_attn_bwd(q, k, v, *want, go, dq=dq, dk=dk, dv=dv)
+    for t, x, y in zip(hold, (want[0], *grads), (o, dq, dk, dv)):
+        assert torch.equal(x, y)
+        assert bool((t[:8] == 7).all()) and bool((t[-8:] == 7).all())
+
+
 def test_offsets_past_32_bits():
     """Key rows 2^15 elements apart, 70000 of them in two sequences."""
     B, Tk, hk, d = 2, 35000, 2, 64
