@@ -465,5 +465,7 @@ class _KlaAttn(torch.autograd.Function):
 
 def kla_attn(q, k, v, scale=None, cu_seqlens_q=None, cu_seqlens_k=None):
     """Differentiable causal attention: o, with gradients for q, k and v.  A
-    batch [B,T,H,d], or packed sequences [total,H,d] with their tables."""
+    batch [B,T,H,d], or packed sequences [total,H,d] with their tables.  Forward
+    and backward may be captured into a CUDA graph; as for every torch operation,
+    no eager graph of the same leaves may be alive then."""
     return _KlaAttn.apply(q, k, v, scale, cu_seqlens_q, cu_seqlens_k)

@@ -427,6 +427,27 @@ def test_a_second_derivative_is_refused():
         torch.autograd.grad(dq.sum(), k)
 
 
+def test_a_captured_training_step_follows_its_inputs():
+    q, k, v, go = (x[None].cuda() for x in _inputs(150, 150, 4, 2, 64, BF16, seed=14))
+    w = torch.ones(64, device="cuda")
+    pos, freq = torch.arange(150).int().cuda()[None], torch.rand(32).cuda()
+    leaves = [x.requires_grad_() for x in (q, k, v, w)]
+
+    def step():
+        o = kla.kla_attn(*kla.kla_qk_norm_rope(q, k, pos, freq, w, w), v)
+        return (o.detach(), *torch.autograd.grad(o, leaves, go))
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    with torch.no_grad():
+        q.mul_(0.5)
+        go.neg_()
+    graph.replay()
+    assert all(torch.equal(x, y) for x, y in zip(got, step()))
+
+
 def test_prompt_then_single_tokens_equal_the_whole_prompt():
     """The cache as it is used: a prompt, then tokens one at a time over the
     growing cache, against the whole sequence at once."""
