@@ -510,12 +510,7 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                         uint32_t u[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) u[i] = attn::pack2(f[2 * i], f[2 * i + 1]);
-                        if constexpr (D == 128) {       // 70 -> 67 us; head size 64 slower
-                            attn::store16(dst, u);
-                        } else {
-                            reinterpret_cast<uint4 *>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-                            reinterpret_cast<uint4 *>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
-                        }
+                        attn::store16(dst, u);
                     }
                     __syncwarp();
                 }
