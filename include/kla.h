@@ -441,7 +441,8 @@ KLA_API int kla_qk_norm_rope_bwd(const void *q, long long q_stride, const void *
  *              rest is scratch.  The size depends on the SM count of the
  *              current device.  One workspace must not be shared by calls that
  *              may run concurrently.
- * Hq a multiple of Hk, at most 1024; d in {64, 128}.  B, Tq or Tk may be 0.
+ * Hq a multiple of Hk, at most 1024; d in {64, 128}.  B, Tq or Tk may be 0;
+ * all query rows times Hq stay 128 below 2^31.
  * Scores, statistics and sums are fp32.  Keys and values of rows that are not
  * the sequence's own (behind its length, of its neighbours) may hold anything;
  * its own must be finite for the queries before them to stay finite.
@@ -481,6 +482,8 @@ KLA_API int kla_attn_fwd_varlen(const void *q, long long q_stride, const void *k
  *     P = exp(S - lse),  dS = P (d_o v^T - rowsum(d_o o)) scale
  *     dq = dS k,  dk = dS^T q,  dv = P^T d_o  (summed over a group's heads)
  *
+ * (bf16 rows that see at most 8 keys take rowsum(P d_o v^T), which is the same
+ * before o was rounded.)
  * dq [B, Tq, Hq, d], dk, dv [B, Tk, Hk, d] (dtype, dense) are written whole;
  * keys that no query sees get 0.  No atomics: a result does not depend on the
  * order of blocks.  workspace as for the forward, of its own size.

@@ -80,6 +80,18 @@ def test_backward_refuses(over, status):
 
 
 @no_gpu_only
+@pytest.mark.parametrize("call", [_fwd, _packed, _bwd])
+def test_what_32_bits_do_not_hold_is_refused(call):
+    """Rows are counted in 32 bits, a tile past the last; log2 e times the scale
+    is finite."""
+    most = dict(B=1, Tq=(1 << 31) // 64 - 2, Tk=64, Hq=64, Hk=64, qs=64 * 64, ks=64 * 64, vs=64 * 64,
+                gs=64 * 64)
+    assert call(**most) == UNSUPPORTED                       # its rows + 128 = 2^31
+    assert call(**{**most, "Tq": most["Tq"] - 1}, wsb=64) == WORKSPACE      # not too large
+    assert call(scale=2e38, wsb=64) == WORKSPACE and call(scale=3e38) == INVALID
+
+
+@no_gpu_only
 def test_nothing_to_do_and_the_injected_fault(monkeypatch):
     assert _fwd(B=0) == binding.KLA_OK
     assert _fwd(Tq=0, q=None, o=None) == binding.KLA_OK
