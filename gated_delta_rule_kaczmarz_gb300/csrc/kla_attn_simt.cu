@@ -15,11 +15,20 @@
 // and keys tx + 16 j, and of the outputs rows ty + 16 i, features 4 tx + 64 j.
 // Rows in shared memory are 4 floats longer than d, so that the 16-byte reads
 // of 8 neighbouring keys fall into different banks.  A tile's rows are read
-// from memory into registers a step ahead.  Bound by the reads of shared memory
-// (a 16-byte read for 2 to 3 multiply-adds of a thread); few blocks: by the
-// steps' latency, 4 to 5 us each.  fp32, forward and backward: B 1, T 256, 2
-// heads of 64 16 and 37 us; B 4, T 2048, 8 heads of 64 0.53 and 1.73 ms (16 and
-// 25 TFLOP/s); single tokens of B 16, 16 + 4 heads of 128 over 4096 keys 181 us.
+// from memory into registers a step ahead.  Bound by the issue of the products
+// and by the reads of shared memory between them (a 16-byte read for 4 packed
+// multiply-adds); few blocks: by the steps' latency, 4 to 5 us each.  fp32,
+// forward and backward: B 1, T 256, 2 heads of 64 16 and 37 us; B 4, T 2048, 8
+// heads of 64 0.49 and 1.66 ms (35 and 26 TFLOP/s); B 2, T 2048, 8 + 4 heads of
+// 128 0.49 and 1.69 ms; single tokens of B 16, 16 + 4 heads of 128 over 4096
+// keys 178 us.
+//
+// Blocks an SM, as measured (B 4, T 2048, 8 heads of 64 or B 2, 8 + 4 heads of
+// 128): forward, tiles of 64 rows, d 64: one, 494 us (two 453, but 100 against
+// 76 where there are fewer blocks than places), d 128: two, 491 (one 559);
+// backward, d 64: two, 1660 (one 2115), d 128: one, 1690 (two 2100).  Tiles of
+// 16 rows: three at d 64 (one: 64 single tokens over 700 keys 244 us against 213), two
+// at d 128 (backward, T 82 over 694 keys: 295 us against 315).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -94,10 +103,16 @@ struct Ahead {
     }
 };
 
-// acc[i][j] += sum_c A[ty + 16 i][c] B[tx + 16 j][c] over the D features.
+// acc[i][j] += sum_c A[ty + 16 i][c] B[tx + 16 j][c] over the D features, two
+// products an instruction: even and odd features are summed apart.
 template <int D, int MI, int NJ>
 __device__ __forceinline__ void dots(const float *A, const float *B, float (&acc)[MI][NJ]) {
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    float2 s[MI][NJ];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) s[i][j] = make_float2(acc[i][j], 0.f);
 #pragma unroll 8
     for (int c = 0; c < D; c += 4) {
         float4 x[MI], y[NJ];
@@ -108,10 +123,15 @@ __device__ __forceinline__ void dots(const float *A, const float *B, float (&acc
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                acc[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y,
-                                 fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, acc[i][j]))));
+            for (int j = 0; j < NJ; ++j) {
+                s[i][j] = __ffma2_rn(make_float2(x[i].x, x[i].y), make_float2(y[j].x, y[j].y), s[i][j]);
+                s[i][j] = __ffma2_rn(make_float2(x[i].z, x[i].w), make_float2(y[j].z, y[j].w), s[i][j]);
+            }
     }
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = s[i][j].x + s[i][j].y;
 }
 // acc[i][:] += sum_n W[ty + 16 i][n] X[n][:], features 4 tx + 64 j; W has LD
 // floats a row, N terms.
@@ -131,10 +151,11 @@ __device__ __forceinline__ void mix(const float *W, const float *X, float4 (&acc
 #pragma unroll
                 for (int i = 0; i < MI; ++i) {
                     const float f = m == 0 ? w[i].x : m == 1 ? w[i].y : m == 2 ? w[i].z : w[i].w;
-                    acc[i][j].x = fmaf(f, x.x, acc[i][j].x);
-                    acc[i][j].y = fmaf(f, x.y, acc[i][j].y);
-                    acc[i][j].z = fmaf(f, x.z, acc[i][j].z);
-                    acc[i][j].w = fmaf(f, x.w, acc[i][j].w);
+                    const float2 lo = __ffma2_rn(make_float2(f, f), make_float2(x.x, x.y),
+                                                 make_float2(acc[i][j].x, acc[i][j].y));
+                    const float2 hi = __ffma2_rn(make_float2(f, f), make_float2(x.z, x.w),
+                                                 make_float2(acc[i][j].z, acc[i][j].w));
+                    acc[i][j] = make_float4(lo.x, lo.y, hi.x, hi.y);
                 }
             }
         }
@@ -147,7 +168,8 @@ constexpr size_t fwd_smem() {
 }
 
 template <typename T, int D, int BM>
-__global__ void __launch_bounds__(kT) attn_simt_fwd_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kT, D == 128 ? 2 : BM == 16 ? 3 : 1)
+attn_simt_fwd_kernel(const __grid_constant__ Args a) {
     constexpr int MI = BM / 16;
     extern __shared__ __align__(16) float sm[];
     float *Q = sm, *KV = Q + BM * (D + 4), *P = KV + 64 * (D + 4);
@@ -442,7 +464,7 @@ __device__ void attn_simt_dkv(const Args &a, int block, float *sm) {
 
 // Both sides in one launch: the blocks of the key tiles first.
 template <typename T, int D, int B>
-__global__ void __launch_bounds__(kT, D == 64 ? 2 : 1)
+__global__ void __launch_bounds__(kT, D == 64 || B == 16 ? 2 : 1)
 attn_simt_bwd_kernel(const __grid_constant__ Args keys, const __grid_constant__ Args rows,
                      int key_blocks) {
     extern __shared__ __align__(16) float sm[];
