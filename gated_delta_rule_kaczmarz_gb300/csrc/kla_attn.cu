@@ -2,6 +2,7 @@
 // its launches.  The kernels and their reasons are in kla_attn_tc.cu and
 // kla_attn_bwd_tc.cu (tensor cores) and kla_attn_simt.cu (CUDA cores).
 #include <atomic>
+#include <cstdlib>
 #include <mutex>
 
 #include "kla_attn_tc.cuh"
@@ -168,6 +169,9 @@ attn::Args make_args(const AttnProblem &p) {
     a.n_seq = p.n_seq; a.Tq = p.Tq; a.Tk = p.Tk; a.Hq = p.Hq; a.Hk = p.Hk; a.G = p.Hq / p.Hk;
     a.splits = 1; a.total_q = p.total_q; a.scale = p.scale;
     a.scale_log2 = p.scale * 1.4426950408889634f;
+    // Test hook: with KLA_TEST_LOST_WAIT set, every tensor-core CTA takes a wait
+    // under way of its first item for one that ran out.
+    a.lost_wait = std::getenv("KLA_TEST_LOST_WAIT") != nullptr;
     return a;
 }
 

@@ -35,6 +35,7 @@ struct Args {
     float *o_part, *lse_part;             // splits > 1: [splits][total_q][Hq][d], [..][Hq]
     int total_q;
     float scale, scale_log2;
+    bool lost_wait;                       // test hook: a wait of every CTA runs out (tensor cores)
 };
 
 struct Seq {
@@ -77,7 +78,9 @@ __device__ __forceinline__ float delta_of(const Args &a, long long row, int keys
     return (keys >= 1 && keys <= kFewKeys ? a.delta_few : a.delta)[row];
 }
 
-// Packed sequences whose tables the check refused: nothing is done.
+// Packed sequences whose tables the check refused: nothing is done.  In the
+// tensor-core kernels other CTAs of the launch write the word where a wait runs
+// out, so there one thread reads it for all of its CTA.
 __device__ __forceinline__ bool rejected(const Args &a) { return a.cu_q && *a.status != kDevOk; }
 
 // Fixed lengths have no check before them: the first block of a call's first

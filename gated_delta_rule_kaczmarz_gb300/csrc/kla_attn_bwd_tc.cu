@@ -85,6 +85,7 @@ struct Shared {
     Work item[2];
     uint32_t tmem;
     volatile int abort;
+    bool rejected;                       // the status word as the CTA's first thread read it
 };
 
 template <int D>
@@ -265,8 +266,11 @@ struct Cta {
             if (lane == 0) {
                 w = decode(block);
                 ok = m < 2 || wait(&sh.work_read[m & 1], m / 2 - 1);
-                sh.item[m & 1] = w;
-                mbar_arrive(&sh.work[m & 1]);
+                if (m == 1 && ar.lost_wait) ok = mbar_try_wait(&sh.work_read[1], 0);   // not published yet
+                if (ok) {
+                    sh.item[m & 1] = w;
+                    mbar_arrive(&sh.work[m & 1]);
+                }
             }
             ok = __all_sync(0xffffffffu, ok);
             __syncwarp();
@@ -766,7 +770,6 @@ attn_tc_bwd_kernel(const __grid_constant__ Args ak, const __grid_constant__ Args
     extern __shared__ __align__(1024) unsigned char raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    if (attn::rejected(ar)) return;
     if (base + C::USED > raw + C::SMEM) {      // not where the array's alignment is kept
         *ar.status = kDevTimeout;
         return;
@@ -801,6 +804,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Args ak, const __grid_constant__ Args
         mbar_init(&sh.asked, 1);
         mbar_init(&sh.done, 2);
         sh.abort = 0;
+        sh.rejected = attn::rejected(ar);
         fence_mbar_init();
     }
     // rows that no copy fills (the group does not divide 128) are summed over
@@ -811,6 +815,13 @@ attn_tc_bwd_kernel(const __grid_constant__ Args ak, const __grid_constant__ Args
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (sh.rejected) {
+        if (warp == 8) {
+            tmem_relinquish();
+            tmem_dealloc(sh.tmem, C::TM_COLS);
+        }
+        return;
+    }
     Cta<D> cta(ak, ar, maps, key_blocks, sh, base, warp, lane);
     // Registers of a thread: 128 x 88 + 256 x 208 = 384 x 168.
     if (warp >= 8) {

@@ -76,6 +76,7 @@ struct Shared {
     Work item[2];
     uint32_t tmem;
     volatile int abort;
+    bool rejected;                       // the status word as the CTA's first thread read it
 };
 
 // Maps of a launch and its row tiling.
@@ -95,7 +96,6 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
     unsigned char *sQ = base, *sKV = base + 2 * C::TILE;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     attn::clear_status(a);
-    if (attn::rejected(a)) return;
     const int TT = maps.tokens, R = TT * a.G;
 
     if (threadIdx.x == 0) {
@@ -120,6 +120,7 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
         mbar_init(&sh.asked, 1);
         mbar_init(&sh.fin, 2);
         sh.abort = 0;
+        sh.rejected = attn::rejected(a);
         fence_mbar_init();
     }
     if (warp == 8) tmem_alloc(&sh.tmem, C::TM_COLS);
@@ -127,6 +128,13 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = sh.tmem;
+    if (sh.rejected) {
+        if (warp == 8) {
+            tmem_relinquish();
+            tmem_dealloc(tb, C::TM_COLS);
+        }
+        return;
+    }
     const auto give_up = [&] {
         sh.abort = 1;
         *a.status = kDevTimeout;
@@ -169,8 +177,11 @@ attn_tc_fwd_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps 
                         w.any = 1;
                     }
                     ok = m < 2 || wait(&sh.work_read[m & 1], m / 2 - 1);
-                    sh.item[m & 1] = w;
-                    mbar_arrive(&sh.work[m & 1]);
+                    if (m == 1 && a.lost_wait) ok = mbar_try_wait(&sh.work_read[1], 0);   // not published yet
+                    if (ok) {
+                        sh.item[m & 1] = w;
+                        mbar_arrive(&sh.work[m & 1]);
+                    }
                 }
                 ok = __all_sync(0xffffffffu, ok);
                 __syncwarp();

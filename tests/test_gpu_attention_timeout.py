@@ -1,0 +1,69 @@
+"""A wait of the tensor-core attention kernels that runs out, without a hang or
+a fault: with KLA_TEST_LOST_WAIT set every CTA gives up while its first item is
+under way.  The call reports KLA_ERR_TIMEOUT, the CTAs that start after others
+wrote the status word leave whole, and the next call on the same workspace is
+exact."""
+import time
+
+import pytest
+import torch
+
+import gated_delta_rule_kaczmarz_gb300 as kla
+from gated_delta_rule_kaczmarz_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+
+def _normal(*shape, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(*shape, generator=g).bfloat16().cuda()
+
+
+CASES = [
+    # lengths (None: a batch), B, Tq, Tk, Hq, Hk, d
+    (None, 1, 1000, 1000, 8, 2, 128),
+    (None, 8, 2048, 2048, 8, 4, 64),            # more blocks than SMs
+    (None, 2, 3, 5000, 8, 2, 128),              # a split key axis
+    ([900, 1, 0, 2100, 77] * 9, 0, 0, 0, 12, 4, 64),
+    ([900, 1, 0, 2100, 77] * 9, 0, 0, 0, 6, 2, 128),      # three heads: a tile of 126 rows
+]
+
+
+def _sides(case):
+    lens, B, Tq, Tk, hq, hk, d = case
+    if lens is None:
+        q, go = _normal(B, Tq, hq, d, seed=1), _normal(B, Tq, hq, d, seed=2)
+        k, v = _normal(B, Tk, hk, d, seed=3), _normal(B, Tk, hk, d, seed=4)
+        sizes = B, Tq, Tk, hq, hk, d
+        return (q, k, v, go), (), sizes, (kla.kla_attn_fwd, kla.kla_attn_fwd_workspace_size,
+                                          kla.kla_attn_bwd, kla.kla_attn_bwd_workspace_size)
+    n = sum(lens)
+    q, go = _normal(n, hq, d, seed=1), _normal(n, hq, d, seed=2)
+    k, v = _normal(n, hk, d, seed=3), _normal(n, hk, d, seed=4)
+    cu = torch.tensor([0] + lens).cumsum(0).int().cuda()
+    return (q, k, v, go), (cu,), (len(lens), n, n, hq, hk, d), \
+        (kla.kla_attn_fwd_varlen, kla.kla_attn_fwd_varlen_workspace_size,
+         kla.kla_attn_bwd_varlen, kla.kla_attn_bwd_varlen_workspace_size)
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_exact(monkeypatch, case):
+    (q, k, v, go), cu, sizes, (fwd, fwd_size, bwd, bwd_size) = _sides(case)
+    ws = torch.empty(max(fwd_size(*sizes), bwd_size(*sizes)), dtype=torch.uint8, device="cuda")
+    want = fwd(q, k, v, *cu, workspace=ws)
+    grads = bwd(q, k, v, *want, go, *cu, workspace=ws)
+    torch.cuda.synchronize()
+    for call, ref in ((lambda: fwd(q, k, v, *cu, workspace=ws), want),
+                      (lambda: bwd(q, k, v, *want, go, *cu, workspace=ws), grads)):
+        monkeypatch.setenv("KLA_TEST_LOST_WAIT", "1")
+        t0 = time.perf_counter()
+        call()
+        with pytest.raises(kla.KlaError) as err:
+            kla.kla_workspace_status(ws)
+        assert err.value.status == binding.KLA_ERR_TIMEOUT
+        # no role sat out its own bound of about one second
+        assert time.perf_counter() - t0 < 0.5
+        monkeypatch.delenv("KLA_TEST_LOST_WAIT")
+        got = call()
+        assert kla.kla_workspace_status(ws) == binding.KLA_OK
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
