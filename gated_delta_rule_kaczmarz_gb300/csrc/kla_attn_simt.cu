@@ -592,10 +592,11 @@ __global__ void __launch_bounds__(256, 6) attn_delta_kernel(const __grid_constan
 // few rows of many parts do not wait for one read after another; the groups'
 // sums meet in shared memory in a fixed order.  Bound by the latency of those
 // reads: 16 tokens of 16 heads of 128 in 7 parts take 4.3 us, one in 38 parts 4.3
-// (with one group a row 7.7 and 10.3).
+// (with one group a row 7.7 and 10.3).  Nothing is joined where the tables were
+// refused or a wait ran out: parts are missing then.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ Args a, int per) {
-    if (attn::rejected(a)) return;
+    if (*a.status != kDevOk) return;
     constexpr int MOST = attn::kMaxSplits / 16;
     __shared__ __align__(16) float part[16][D];
     const long long n = (long long)a.total_q * a.Hq;

@@ -67,3 +67,19 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_exact(monkeypatch
         got = call()
         assert kla.kla_workspace_status(ws) == binding.KLA_OK
         assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_parts_of_a_call_that_timed_out_are_not_joined(monkeypatch, d):
+    """A split key axis: the parts that were not written are no result."""
+    q, k, v = _normal(2, 3, 8, d, seed=1), _normal(2, 5000, 2, d, seed=2), _normal(2, 5000, 2, d, seed=3)
+    size = kla.kla_attn_fwd_workspace_size(2, 3, 5000, 8, 2, d)
+    assert size > 256 + 2 * 2 * 3 * 8 * d * 4               # two parts and more
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")        # parts of NaN
+    o, lse = torch.full_like(q, 3.0), torch.full((2, 3, 8), 3.0, device="cuda")
+    monkeypatch.setenv("KLA_TEST_LOST_WAIT", "1")
+    kla.kla_attn_fwd(q, k, v, o=o, lse=lse, workspace=ws)
+    with pytest.raises(kla.KlaError) as err:
+        kla.kla_workspace_status(ws)
+    assert err.value.status == binding.KLA_ERR_TIMEOUT
+    assert bool((o == 3).all()) and bool((lse == 3).all())
