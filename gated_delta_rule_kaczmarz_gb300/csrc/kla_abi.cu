@@ -630,6 +630,19 @@ int kla_qk_norm_rope_bwd(const void *q, long long q_stride, const void *k, long 
 }  // extern "C"
 
 namespace {
+// A call that runs no kernel still records its status in a workspace that holds
+// a status word, so that kla_workspace_status reads this call's.  (A host without
+// a GPU has no word to write, and no status to read.)
+cudaError_t reset_status(void *workspace, size_t workspace_bytes, cudaStream_t s) {
+    if (workspace == nullptr || workspace_bytes < kla::kWsHeader ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return cudaSuccess;
+    const cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(unsigned), s);
+    if (e != cudaErrorNoDevice && e != cudaErrorInsufficientDriver) return e;
+    cudaGetLastError();
+    return cudaSuccess;
+}
+
 // Checks and runs a forward or backward attention request whose sizes and
 // pointers are in p.
 kla_status run_attn(kla::AttnProblem &p, bool backward, void *workspace, size_t workspace_bytes,
@@ -654,7 +667,8 @@ kla_status run_attn(kla::AttnProblem &p, bool backward, void *workspace, size_t 
     if (p.total_q == 0) {      // no queries: the keys' gradients are zero
         if (inject_launch_fault()) return fail(KLA_ERR_CUDA, "injected launch fault (KLA_FAULT_INJECT)");
         const size_t n = (size_t)p.total_k * p.Hk * p.d * (p.dtype == KLA_DTYPE_BF16 ? 2 : 4);
-        cudaError_t e = cudaSuccess;
+        cudaError_t e = reset_status(workspace, workspace_bytes, s);
+        if (e != cudaSuccess) return cuda_fail(e, "status init");
         if (backward && n) e = cudaMemsetAsync(p.dk, 0, n, s);
         if (backward && n && e == cudaSuccess) e = cudaMemsetAsync(p.dv, 0, n, s);
         return e == cudaSuccess ? ok() : cuda_fail(e, "gradient reset");
