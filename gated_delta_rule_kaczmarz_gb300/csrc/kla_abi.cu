@@ -643,6 +643,13 @@ cudaError_t reset_status(void *workspace, size_t workspace_bytes, cudaStream_t s
     return cudaSuccess;
 }
 
+// The workspace of a request that passed its checks: without queries the status
+// word, where there are tables to check.
+size_t attn_bytes(const kla::AttnProblem &p, bool backward) {
+    if (p.total_q == 0) return p.cu_q && p.n_seq > 0 ? kla::kWsHeader : 0;
+    return backward ? kla::attn_bwd_workspace_bytes(p) : kla::attn_fwd_workspace_bytes(p);
+}
+
 // Checks and runs a forward or backward attention request whose sizes and
 // pointers are in p.
 kla_status run_attn(kla::AttnProblem &p, bool backward, void *workspace, size_t workspace_bytes,
@@ -664,7 +671,7 @@ kla_status run_attn(kla::AttnProblem &p, bool backward, void *workspace, size_t 
         return fail(KLA_ERR_INVALID_ARG, "o and the gradients must be 16-byte aligned, lse and "
                     "the length tables 4-byte");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (p.total_q == 0) {      // no queries: the keys' gradients are zero
+    if (p.total_q == 0 && (!p.cu_q || p.n_seq == 0)) {   // no queries: the keys' gradients are zero
         if (inject_launch_fault()) return fail(KLA_ERR_CUDA, "injected launch fault (KLA_FAULT_INJECT)");
         const size_t n = (size_t)p.total_k * p.Hk * p.d * (p.dtype == KLA_DTYPE_BF16 ? 2 : 4);
         cudaError_t e = reset_status(workspace, workspace_bytes, s);
@@ -673,7 +680,7 @@ kla_status run_attn(kla::AttnProblem &p, bool backward, void *workspace, size_t 
         if (backward && n && e == cudaSuccess) e = cudaMemsetAsync(p.dv, 0, n, s);
         return e == cudaSuccess ? ok() : cuda_fail(e, "gradient reset");
     }
-    const size_t need = backward ? kla::attn_bwd_workspace_bytes(p) : kla::attn_fwd_workspace_bytes(p);
+    const size_t need = attn_bytes(p, backward);
     if (workspace == nullptr || workspace_bytes < need)
         return fail(KLA_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need,
                     workspace ? workspace_bytes : (size_t)0);
@@ -681,7 +688,9 @@ kla_status run_attn(kla::AttnProblem &p, bool backward, void *workspace, size_t 
         return fail(KLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     if (inject_launch_fault()) return fail(KLA_ERR_CUDA, "injected launch fault (KLA_FAULT_INJECT)");
     p.ws = workspace;
-    cudaError_t e = backward ? kla::launch_attn_bwd(p, s) : kla::launch_attn_fwd(p, s);
+    cudaError_t e = p.total_q == 0 ? kla::launch_attn_no_queries(p, s)
+                    : backward     ? kla::launch_attn_bwd(p, s)
+                                   : kla::launch_attn_fwd(p, s);
     if (e != cudaSuccess) return cuda_fail(e, backward ? "attention backward launch" : "attention launch");
     return ok();
 }
@@ -730,8 +739,8 @@ extern "C" {
 size_t kla_attn_fwd_workspace_size(int B, int Tq, int Tk, int Hq, int Hk, int d, int dtype) {
     kla::AttnProblem p{};
     p.Hq = Hq; p.Hk = Hk; p.d = d; p.dtype = dtype;
-    if (fixed_attn(p, B, Tq, Tk) != KLA_OK || p.total_q == 0) return 0;
-    return kla::attn_fwd_workspace_bytes(p);
+    if (fixed_attn(p, B, Tq, Tk) != KLA_OK) return 0;
+    return attn_bytes(p, false);
 }
 
 size_t kla_attn_fwd_varlen_workspace_size(int N, int total_q, int total_k, int Hq, int Hk, int d,
@@ -739,15 +748,15 @@ size_t kla_attn_fwd_varlen_workspace_size(int N, int total_q, int total_k, int H
     kla::AttnProblem p{};
     p.Hq = Hq; p.Hk = Hk; p.d = d; p.dtype = dtype;
     static const int some = 0;      // packed: the tables' contents are not read here
-    if (packed_attn(p, N, total_q, total_k, &some, &some) != KLA_OK || total_q == 0) return 0;
-    return kla::attn_fwd_workspace_bytes(p);
+    if (packed_attn(p, N, total_q, total_k, &some, &some) != KLA_OK) return 0;
+    return attn_bytes(p, false);
 }
 
 size_t kla_attn_bwd_workspace_size(int B, int Tq, int Tk, int Hq, int Hk, int d, int dtype) {
     kla::AttnProblem p{};
     p.Hq = Hq; p.Hk = Hk; p.d = d; p.dtype = dtype;
-    if (fixed_attn(p, B, Tq, Tk) != KLA_OK || p.total_q == 0) return 0;
-    return kla::attn_bwd_workspace_bytes(p);
+    if (fixed_attn(p, B, Tq, Tk) != KLA_OK) return 0;
+    return attn_bytes(p, true);
 }
 
 size_t kla_attn_bwd_varlen_workspace_size(int N, int total_q, int total_k, int Hq, int Hk, int d,
@@ -755,8 +764,8 @@ size_t kla_attn_bwd_varlen_workspace_size(int N, int total_q, int total_k, int H
     kla::AttnProblem p{};
     p.Hq = Hq; p.Hk = Hk; p.d = d; p.dtype = dtype;
     static const int some = 0;
-    if (packed_attn(p, N, total_q, total_k, &some, &some) != KLA_OK || total_q == 0) return 0;
-    return kla::attn_bwd_workspace_bytes(p);
+    if (packed_attn(p, N, total_q, total_k, &some, &some) != KLA_OK) return 0;
+    return attn_bytes(p, true);
 }
 
 int kla_attn_fwd(const void *q, long long q_stride, const void *k, long long k_stride,

@@ -229,6 +229,13 @@ bool attn_too_large(const AttnProblem &p) {
     return q * p.Hk > INT32_MAX || k * p.Hk > INT32_MAX || rows > INT32_MAX;
 }
 
+cudaError_t launch_attn_no_queries(const AttnProblem &p, cudaStream_t s) {
+    const cudaError_t e = prepare(p, {}, {}, s);
+    const long long bytes = (long long)p.total_k * p.Hk * p.d * (p.dtype == 1 ? 2 : 4);
+    if (e != cudaSuccess || !p.dk || bytes == 0) return e;
+    return launch_attn_zero(p.dk, p.dv, bytes, static_cast<unsigned *>(p.ws), s);
+}
+
 cudaError_t launch_attn_fwd(const AttnProblem &p, cudaStream_t s) {
     const FwdPlan f = fwd_plan(p);
     attn::Args a = make_args(p);

@@ -139,6 +139,9 @@ struct AttnTable {
 cudaError_t launch_attn_prep(const int *cu_q, const int *cu_k, int n, int total_q, int total_k,
                              const AttnTable &t0, const AttnTable &t1, unsigned *status,
                              cudaStream_t s);
+// Zeroes dk and dv (bytes each, a multiple of 16) where *status is OK.
+cudaError_t launch_attn_zero(void *dk, void *dv, long long bytes, const unsigned *status,
+                             cudaStream_t s);
 cudaError_t launch_attn_join(const attn::Args &a, int d, int dtype, cudaStream_t s);
 cudaError_t launch_attn_delta(const attn::Args &a, int d, int dtype, cudaStream_t s);
 

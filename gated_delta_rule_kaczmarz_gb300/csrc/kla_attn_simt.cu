@@ -722,6 +722,17 @@ attn_prep_kernel(const int *cu_q, const int *cu_k, int n, int total_q, int total
     }
 }
 
+// Key gradients of packed sequences without queries, if their tables passed.
+__global__ void __launch_bounds__(256)
+attn_zero_kernel(uint4 *dk, uint4 *dv, long long n, const unsigned *status) {
+    if (*status != kDevOk) return;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
+        dk[i] = zero;
+        dv[i] = zero;
+    }
+}
+
 template <typename K, typename... A>
 cudaError_t launch(K *kernel, long long blocks, size_t smem, cudaStream_t s, const A &...args) {
     if (blocks == 0) return cudaSuccess;
@@ -786,6 +797,15 @@ cudaError_t launch_attn_join(const Args &a, int d, int dtype, cudaStream_t s) {
     while (per < a.splits && per < 16) per *= 2;
     const long long blocks = ((long long)a.total_q * a.Hq * per + 15) / 16;
     KLA_BY_TYPE(d, dtype, (attn_join_kernel<T, D><<<(unsigned)blocks, 256, 0, s>>>(a, per)));
+    note_launch();
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_zero(void *dk, void *dv, long long bytes, const unsigned *status,
+                             cudaStream_t s) {
+    const long long n = bytes / 16, blocks = (n + 255) / 256;
+    attn_zero_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(
+        static_cast<uint4 *>(dk), static_cast<uint4 *>(dv), n, status);
     note_launch();
     return cudaGetLastError();
 }

@@ -128,6 +128,8 @@ size_t attn_bwd_workspace_bytes(const AttnProblem &p);
 bool attn_too_large(const AttnProblem &p);   // more blocks than a launch may have
 cudaError_t launch_attn_fwd(const AttnProblem &p, cudaStream_t s);
 cudaError_t launch_attn_bwd(const AttnProblem &p, cudaStream_t s);
+// Packed, total_q 0: the check of the tables, and zeros in dk and dv if given.
+cudaError_t launch_attn_no_queries(const AttnProblem &p, cudaStream_t s);
 
 // Backward of the chunkwise forward (kla_chunk_bwd.cu), fixed length or varlen.
 struct BwdProblem {

@@ -463,7 +463,8 @@ KLA_API int kla_attn_fwd(const void *q, long long q_stride, const void *k, long 
  * (device int32 [N + 1]; the two may be the same array).  Both tables must
  * start with 0, not decrease and end with the totals; the device checks this,
  * and a violation skips all work and is reported by kla_workspace_status() as
- * KLA_ERR_INVALID_ARG.  Sequences may be empty on either side.
+ * KLA_ERR_INVALID_ARG (in calls without queries too, whose workspace is the
+ * status word's 256 bytes).  Sequences may be empty on either side.
  */
 KLA_API size_t kla_attn_fwd_varlen_workspace_size(int N, int total_q, int total_k, int Hq, int Hk,
                                                   int d, int dtype);

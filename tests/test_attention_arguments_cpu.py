@@ -1,0 +1,11 @@
+"""What the attention calls take besides their sizes."""
+import gated_delta_rule_kaczmarz_gb300 as kla
+
+
+def test_packed_calls_without_queries_want_a_status_word():
+    """Their tables are checked on the device, and reported there."""
+    for size in (kla.kla_attn_fwd_varlen_workspace_size, kla.kla_attn_bwd_varlen_workspace_size):
+        assert size(2, 0, 40, 4, 2, 64) == size(2, 0, 0, 4, 2, 128) == 256
+        assert size(0, 0, 0, 4, 2, 64) == 0
+    for size in (kla.kla_attn_fwd_workspace_size, kla.kla_attn_bwd_workspace_size):
+        assert size(2, 0, 40, 4, 2, 64) == size(0, 5, 5, 4, 2, 64) == 0

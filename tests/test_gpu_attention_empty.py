@@ -1,4 +1,5 @@
-"""Attention calls without queries: the status word is the call's own."""
+"""Attention calls without queries: the status word is the call's own, and the
+tables of packed sequences are checked as in any other."""
 import pytest
 import torch
 
@@ -57,3 +58,36 @@ def test_no_sequences_leave_their_own_status():
     q, k, _ = _sides(0)
     ws = _refused()
     kla.kla_attn_fwd_varlen(q, k, k, _table(0), workspace=ws, check_status=True)
+
+
+@pytest.mark.parametrize("own", [False, True])
+@pytest.mark.parametrize("keys,cu_q,cu_k", [
+    (40, (0, 0, 0), (0, 50, 40)), (40, (0, 0, 0), (1, 20, 40)), (40, (0, 0, 0), (0, 20, 39)),
+    (40, (1, 0, 0), (0, 20, 40)), (40, (0, 3, 0), (0, 20, 40)), (0, (0, 0, 0), (0, 1, 0))])
+def test_bad_tables_without_queries_are_reported_and_nothing_is_written(keys, cu_q, cu_k, own):
+    q, k, lse = _sides(keys)
+    cu_q, cu_k = _table(*cu_q), _table(*cu_k)
+    ws = torch.zeros(1 << 12, dtype=torch.uint8, device="cuda") if own else None
+    with pytest.raises(kla.KlaError) as err:
+        kla.kla_attn_fwd_varlen(q, k, k, cu_q, cu_k, workspace=ws, check_status=True)
+    assert err.value.status == binding.KLA_ERR_INVALID_ARG
+    dk, dv = torch.full_like(k, 3.0), torch.full_like(k, 3.0)
+    with pytest.raises(kla.KlaError) as err:
+        kla.kla_attn_bwd_varlen(q, k, k, q, lse, q, cu_q, cu_k, dk=dk, dv=dv, workspace=ws,
+                                check_status=True)
+    assert err.value.status == binding.KLA_ERR_INVALID_ARG
+    assert bool((dk == 3).all()) and bool((dv == 3).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+@pytest.mark.parametrize("keys", [1, 4097])
+def test_key_gradients_of_many_keys_without_queries_are_zero(keys, dtype):
+    """Written whole and nothing behind them."""
+    q = torch.empty(0, 4, 128, dtype=dtype, device="cuda")
+    k = torch.randn(keys, 2, 128, device="cuda").to(dtype)
+    hold = [torch.full((k.numel() + 64,), 3.0, dtype=dtype, device="cuda") for _ in range(2)]
+    dk, dv = (t[:k.numel()].view(k.shape) for t in hold)
+    kla.kla_attn_bwd_varlen(q, k, k, q, torch.empty(0, 4, device="cuda"), q, _table(0, 0),
+                            _table(0, keys), dk=dk, dv=dv, check_status=True)
+    for t in hold:
+        assert bool((t[:k.numel()] == 0).all()) and bool((t[k.numel():] == 3).all())
