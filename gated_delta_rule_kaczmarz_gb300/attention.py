@@ -331,15 +331,17 @@ def _scale(scale, d):
 
 
 def kla_attn_fwd(q, k, v, scale=None, k_lens=None, o=None, lse=None, return_lse=True,
-                 workspace=None, stream=None):
+                 workspace=None, stream=None, check_status=False):
     """Causal attention with grouped heads.  q: [B,Tq,Hq,d], k, v: [B,Tk,Hk,d];
     query i sees the keys j <= i + Tk - Tq (one token over a cache: Tq = 1);
     k_lens: int32 [B], the keys of each sequence of a padded cache, or None
-    (all Tk); scale: 1/sqrt(d) unless given.  Returns (o, lse), o dense, lse
-    [B,Tq,Hq] fp32 (None with return_lse=False)."""
+    (all Tk); scale: 1/sqrt(d) unless given; check_status waits for the call and
+    raises what the device reports.  Returns (o, lse), o dense, lse [B,Tq,Hq]
+    fp32 (None with return_lse=False)."""
     if stream is not None:
         with _given(stream, q):
-            return kla_attn_fwd(q, k, v, scale, k_lens, o, lse, return_lse, workspace)
+            return kla_attn_fwd(q, k, v, scale, k_lens, o, lse, return_lse, workspace,
+                                check_status=check_status)
     dev, dt, rows, (hq, hk, d) = _qkv(q, k, v, 4)
     B, Tq, Tk = q.shape[0], q.shape[1], k.shape[1]
     lens = _dense(k_lens, "k_lens", torch.int32, dev, (B,))
@@ -351,6 +353,8 @@ def kla_attn_fwd(q, k, v, scale=None, k_lens=None, o=None, lse=None, return_lse=
     workspace, wsb = _workspace(dev, lib.kla_attn_fwd_workspace_size, sizes, q, workspace)
     _call(dev, lib.kla_attn_fwd, *rows, lens, _scale(scale, d), at, stats, *sizes,
           _at(workspace), wsb)
+    if check_status:
+        _call(dev, _status, workspace, wsb)
     return o, lse
 
 
@@ -403,18 +407,21 @@ def _grads(q, k, v, o, lse, d_o, dev, dq, dk, dv):
 
 
 def kla_attn_bwd(q, k, v, o, lse, d_o, scale=None, dq=None, dk=None, dv=None, workspace=None,
-                 stream=None):
+                 stream=None, check_status=False):
     """Backward of kla_attn_fwd (without k_lens): the gradients of sum <d_o, o>
     from the forward's inputs and its o and lse.  Returns (dq, dk, dv), dense."""
     if stream is not None:
         with _given(stream, q):
-            return kla_attn_bwd(q, k, v, o, lse, d_o, scale, dq, dk, dv, workspace)
+            return kla_attn_bwd(q, k, v, o, lse, d_o, scale, dq, dk, dv, workspace,
+                                check_status=check_status)
     dev, dt, rows, (hq, hk, d) = _qkv(q, k, v, 4)
     ins, at, grads = _grads(q, k, v, o, lse, d_o, dev, dq, dk, dv)
     lib, sizes = load(), (q.shape[0], q.shape[1], k.shape[1], hq, hk, d, dt)
     workspace, wsb = _workspace(dev, lib.kla_attn_bwd_workspace_size, sizes, q, workspace)
     _call(dev, lib.kla_attn_bwd, *rows, *ins, _scale(scale, d), *at, *sizes,
           _at(workspace), wsb)
+    if check_status:
+        _call(dev, _status, workspace, wsb)
     return grads
 
 
@@ -442,13 +449,13 @@ class _KlaAttn(torch.autograd.Function):
     """Causal attention under autograd: kla_attn_fwd[_varlen] and its backward."""
 
     @staticmethod
-    def forward(ctx, q, k, v, scale, cu_q, cu_k):
+    def forward(ctx, q, k, v, scale, cu_q, cu_k, check):
         if cu_q is None:
-            o, lse = kla_attn_fwd(q, k, v, scale)
+            o, lse = kla_attn_fwd(q, k, v, scale, check_status=check)
         else:
-            o, lse = kla_attn_fwd_varlen(q, k, v, cu_q, cu_k, scale)
+            o, lse = kla_attn_fwd_varlen(q, k, v, cu_q, cu_k, scale, check_status=check)
         ctx.save_for_backward(q, k, v, o, lse, cu_q, cu_k)
-        ctx.scale = scale
+        ctx.scale, ctx.check = scale, check
         return o
 
     @staticmethod
@@ -457,15 +464,19 @@ class _KlaAttn(torch.autograd.Function):
         q, k, v, o, lse, cu_q, cu_k = ctx.saved_tensors
         d_o = _dense_rows(d_o, o)
         if cu_q is None:
-            grads = kla_attn_bwd(q, k, v, o, lse, d_o, ctx.scale)
+            grads = kla_attn_bwd(q, k, v, o, lse, d_o, ctx.scale, check_status=ctx.check)
         else:
-            grads = kla_attn_bwd_varlen(q, k, v, o, lse, d_o, cu_q, cu_k, ctx.scale)
-        return *grads, None, None, None
+            grads = kla_attn_bwd_varlen(q, k, v, o, lse, d_o, cu_q, cu_k, ctx.scale,
+                                        check_status=ctx.check)
+        return *grads, None, None, None, None
 
 
-def kla_attn(q, k, v, scale=None, cu_seqlens_q=None, cu_seqlens_k=None):
+def kla_attn(q, k, v, scale=None, cu_seqlens_q=None, cu_seqlens_k=None, check_status=False):
     """Differentiable causal attention: o, with gradients for q, k and v.  A
-    batch [B,T,H,d], or packed sequences [total,H,d] with their tables.  Forward
-    and backward may be captured into a CUDA graph; as for every torch operation,
-    no eager graph of the same leaves may be alive then."""
-    return _KlaAttn.apply(q, k, v, scale, cu_seqlens_q, cu_seqlens_k)
+    batch [B,T,H,d], or packed sequences [total,H,d] with their tables.
+    check_status waits for the forward and the backward and raises what the device
+    reports; without it tables that the device refuses leave o and the gradients
+    unwritten and unreported.  Forward and backward may be captured into a CUDA
+    graph (without check_status); as for every torch operation, no eager graph of
+    the same leaves may be alive then."""
+    return _KlaAttn.apply(q, k, v, scale, cu_seqlens_q, cu_seqlens_k, check_status)

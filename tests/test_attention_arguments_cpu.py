@@ -1,4 +1,8 @@
 """What the attention calls take besides their sizes."""
+import inspect
+
+import pytest
+
 import gated_delta_rule_kaczmarz_gb300 as kla
 
 
@@ -9,3 +13,9 @@ def test_packed_calls_without_queries_want_a_status_word():
         assert size(0, 0, 0, 4, 2, 64) == 0
     for size in (kla.kla_attn_fwd_workspace_size, kla.kla_attn_bwd_workspace_size):
         assert size(2, 0, 40, 4, 2, 64) == size(0, 5, 5, 4, 2, 64) == 0
+
+
+@pytest.mark.parametrize("name", ["kla_attn", "kla_attn_fwd", "kla_attn_bwd",
+                                  "kla_attn_fwd_varlen", "kla_attn_bwd_varlen"])
+def test_every_call_can_check_its_status(name):
+    assert inspect.signature(getattr(kla, name)).parameters["check_status"].default is False

@@ -83,3 +83,34 @@ def test_parts_of_a_call_that_timed_out_are_not_joined(monkeypatch, d):
         kla.kla_workspace_status(ws)
     assert err.value.status == binding.KLA_ERR_TIMEOUT
     assert bool((o == 3).all()) and bool((lse == 3).all())
+
+
+def test_a_fixed_length_call_raises_what_timed_out(monkeypatch):
+    q, k, go = _normal(1, 300, 4, 64, seed=1), _normal(1, 300, 2, 64, seed=2), _normal(1, 300, 4, 64, seed=3)
+    o, lse = kla.kla_attn_fwd(q, k, k, check_status=True)
+    kla.kla_attn_bwd(q, k, k, o, lse, go, check_status=True)
+    leaves = [x.clone().requires_grad_() for x in (q, k, k)]
+    y = kla.kla_attn(*leaves, check_status=True)
+    monkeypatch.setenv("KLA_TEST_LOST_WAIT", "1")
+    for call in (lambda: kla.kla_attn_fwd(q, k, k, check_status=True),
+                 lambda: kla.kla_attn_fwd(q, k, k, check_status=True, stream=torch.cuda.Stream()),
+                 lambda: kla.kla_attn_bwd(q, k, k, o, lse, go, check_status=True),
+                 lambda: kla.kla_attn(*leaves, check_status=True),
+                 lambda: torch.autograd.grad(y, leaves, go)):
+        with pytest.raises(kla.KlaError) as err:
+            call()
+        assert err.value.status == binding.KLA_ERR_TIMEOUT
+
+
+def test_a_refused_table_is_raised_under_autograd():
+    x = _normal(20, 2, 64, seed=1).requires_grad_()
+    bad, good = torch.tensor([0, 12, 11]).int().cuda(), torch.tensor([0, 5, 20]).int().cuda()
+    with pytest.raises(kla.KlaError) as err:
+        kla.kla_attn(x, x, x, cu_seqlens_q=bad, check_status=True)
+    assert err.value.status == binding.KLA_ERR_INVALID_ARG
+    cu = good.clone()
+    y = kla.kla_attn(x, x, x, cu_seqlens_q=cu, check_status=True)
+    cu.data.copy_(bad)                      # refused in the backward pass
+    with pytest.raises(kla.KlaError) as err:
+        torch.autograd.grad(y.float().sum(), x)
+    assert err.value.status == binding.KLA_ERR_INVALID_ARG
