@@ -86,6 +86,8 @@ def _given(stream, t):
     if not hasattr(stream, "cuda_stream"):
         stream = (torch.cuda.ExternalStream(int(stream), device=t.device) if stream
                   else torch.cuda.default_stream(t.device))
+    elif stream.device != t.device:
+        raise ValueError(f"stream must be one of {t.device}, got one of {stream.device}")
     return torch.cuda.stream(stream)
 
 

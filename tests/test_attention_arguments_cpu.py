@@ -1,9 +1,12 @@
 """What the attention calls take besides their sizes."""
 import inspect
+import types
 
 import pytest
+import torch
 
 import gated_delta_rule_kaczmarz_gb300 as kla
+from gated_delta_rule_kaczmarz_gb300 import attention
 
 
 def test_packed_calls_without_queries_want_a_status_word():
@@ -19,3 +22,10 @@ def test_packed_calls_without_queries_want_a_status_word():
                                   "kla_attn_fwd_varlen", "kla_attn_bwd_varlen"])
 def test_every_call_can_check_its_status(name):
     assert inspect.signature(getattr(kla, name)).parameters["check_status"].default is False
+
+
+def test_a_stream_of_another_device_is_refused():
+    """It would be replaced by the current stream of the tensors' device."""
+    stream = types.SimpleNamespace(cuda_stream=1, device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="stream"):
+        attention._given(stream, types.SimpleNamespace(device=torch.device("cuda", 0)))
