@@ -481,4 +481,6 @@ def kla_attn(q, k, v, scale=None, cu_seqlens_q=None, cu_seqlens_k=None, check_st
     unwritten and unreported.  Forward and backward may be captured into a CUDA
     graph (without check_status); as for every torch operation, no eager graph of
     the same leaves may be alive then."""
+    if cu_seqlens_q is None and cu_seqlens_k is not None:
+        raise ValueError("cu_seqlens_k needs cu_seqlens_q")
     return _KlaAttn.apply(q, k, v, scale, cu_seqlens_q, cu_seqlens_k, check_status)

@@ -29,3 +29,11 @@ def test_a_stream_of_another_device_is_refused():
     stream = types.SimpleNamespace(cuda_stream=1, device=torch.device("cuda", 1))
     with pytest.raises(ValueError, match="stream"):
         attention._given(stream, types.SimpleNamespace(device=torch.device("cuda", 0)))
+
+
+@pytest.mark.parametrize("dims", [3, 4])
+def test_a_table_of_the_keys_alone_is_refused(dims):
+    """A batch would be taken without it."""
+    x = torch.zeros(*([1] * (dims - 3)), 4, 2, 64)
+    with pytest.raises(ValueError, match="cu_seqlens_q"):
+        kla.kla_attn(x, x, x, cu_seqlens_k=torch.tensor([0, 4]).int())
