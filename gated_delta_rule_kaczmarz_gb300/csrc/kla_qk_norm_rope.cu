@@ -19,11 +19,15 @@
 // shared by its heads through shared memory.
 //
 // Angles: inv_freq / 2 pi is formed as the sum of two fp32 numbers (products
-// by fma, 48 bits) and kept as a 64-bit fixed-point fraction of a turn;
-// multiplied by the integer position modulo 2^64 it loses nothing at any
-// position, and its upper 32 bits go to sincospif.  The error is below
-// 2^-47 turns per position, that is 1e-8 radians at position 10^6, where an
-// fp32 product would be off by 0.03.  No fp64 instruction is used.
+// by fma, 48 bits) and kept as a 64-bit fixed-point fraction of a turn; the
+// integer position multiplies it modulo 2^64, and the upper 32 bits of that are
+// rounded to fp32 and go to sincospif.  The fraction is off by less than 2^-49
+// inv_freq turns per position (of the second number the rounding of its sum
+// 2^-49.9, of its product 2^-51.2, of its constant 2^-52) and 2^-61: 1.2e-8
+// radians at one radian and position 10^6, 2.4e-5 at the ends of int32.  The
+// rounding adds 1e-7 radians at any position.  An fp32 product would be off by
+// 0.03 at position 10^6.  (With 1 / 2 pi to 192 bits nothing but that rounding
+// would be left, but each launch starts 0.5 us later.)  No fp64 instruction.
 #include <cuda_bf16.h>
 
 #include "kla_internal.h"
@@ -98,7 +102,8 @@ __device__ __forceinline__ void st8(float *p, const float2 *x) {
     *reinterpret_cast<float4 *>(p + 4) = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
 }
 
-// inv_freq / 2 pi, modulo one turn, as a 64-bit fraction.
+// inv_freq / 2 pi, modulo one turn, as a 64-bit fraction; up to 2^26 radians (e
+// stays below 2).
 __device__ __forceinline__ unsigned long long turns_per_position(float f) {
     constexpr float kHi = 0x1.45f306p-3f, kLo = 0x1.b9391p-28f;   // 1 / 2 pi
     float p = f * kHi;

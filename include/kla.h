@@ -374,9 +374,11 @@ KLA_API int kla_ccq_query_step(const void *q, const void *k, const float *lambda
  *                   NULL: q alone.
  *   wq, wk        : [d] fp32 or NULL (no weight), 16-byte aligned
  *   positions     : [n_axes][tokens] int32, any values
- *   inv_freq      : [rot / 2] fp32, in radians per position.  The angle is
- *                   the exact product, reduced in integer arithmetic, so far
- *                   positions lose nothing.
+ *   inv_freq      : [rot / 2] fp32, in radians per position, of at most 2^26.
+ *                   The product is reduced in integer arithmetic: the angle is
+ *                   off by 1e-7 radians (its rounding) and less than 2^-49
+ *                   inv_freq turns a position, which is 1.2e-8 radians at one
+ *                   radian and position 10^6, 2.4e-5 at the ends of int32.
  *   sections      : host array of n_axes (1 to 4) counts of frequency pairs:
  *                   the first sections[0] pairs take axis 0 and so on (time,
  *                   height, width); they sum to rot / 2.
