@@ -30,6 +30,8 @@
 // would be left, but each launch starts 0.5 us later.)  No fp64 instruction.
 #include <cuda_bf16.h>
 
+#include <cstdlib>
+
 #include "kla_internal.h"
 #include "kla_tc.cuh"
 
@@ -419,9 +421,21 @@ struct Pipe {
     int warps, stages;               // of a block
     uint32_t bytes[2];               // a token's rows of q and of k
     uint32_t stage;                  // bytes of a stage: x, and for the backward g
+    bool lost_wait;                  // test hook: as if every warp's first wait had run out
 };
 constexpr int kPipeMost = 16;        // warps of a block, forward; backward 12 (registers)
 constexpr size_t kPipeSmem = 200 * 1024;
+
+// A copy did not come within the bound: there is no status word, so the rows that
+// are left to the warp become NaN (as do the weights' gradients).
+template <typename T, int D>
+__device__ __noinline__ void lost_rows(const QkArgs &a, int lane, long long t, unsigned stride) {
+    const float2 nan = both(__int_as_float(0x7fffffff)), row[4] = {nan, nan, nan, nan};
+    for (; t < a.tokens; t += stride)
+        for (int z = 0; z < 2; ++z)
+            for (int c = lane * 8; c < a.heads[z] * D; c += 256)
+                st8(static_cast<T *>(a.y[z]) + t * a.ys[z] + c, row);
+}
 
 template <typename T, int D, bool BACK>
 __global__ void __launch_bounds__(BACK ? 384 : kPipeMost * 32, 1)
@@ -465,11 +479,12 @@ qk_pipe_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ Pipe p)
         for (int i = 0; i < S - 1 && i < n; ++i) load(i, i);
     if (n > 0) ang.read(a, lane, (int)first);
     int s = 0, use = 0, i = 0;
-    for (; i < n; ++i) {
+    const int walk = p.lost_wait ? 0 : n;
+    for (; i < walk; ++i) {
         const long long t = first + (long long)i * stride;
         ang.turn(a, lane, l, cs_all[warp]);
         if (i + 1 < n) ang.read(a, lane, (int)(t + stride));
-        // the warp's own copy: it comes, and the bound is never reached
+        // the warp's own copy: it comes, and the bound is not met
         if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[warp][s], use & 1))) break;
         unsigned char *row = ring + (size_t)s * p.stage;
 #pragma unroll
@@ -507,6 +522,11 @@ qk_pipe_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ Pipe p)
         for (int j = i; j < n && j < i + S - 1; ++j)       // a copy that had not come
             (void)tc::mbar_wait(&full[warp][j % S], (j / S) & 1);
         tc::bulk_wait_group0();
+    }
+    if (i < n) {
+        lost_rows<T, D>(a, lane, first + (long long)i * stride, stride);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[0][j] = acc[1][j] = both(__int_as_float(0x7fffffff));
     }
     if (BACK && a.dw != nullptr) {
         __syncthreads();       // the rings are done with: the warps' sums take their place
@@ -609,7 +629,9 @@ cudaError_t launch_pipe(const QkArgs &a, const Pipe &p, cudaStream_t s) {
     size_t smem = (size_t)p.warps * p.stages * p.stage;
     const size_t sums = (size_t)p.warps * 2 * D * sizeof(float);
     if (BACK && smem < sums) smem = sums;
-    qk_pipe_kernel<T, D, BACK><<<152, p.warps * 32, smem, s>>>(a, p);
+    Pipe q = p;
+    q.lost_wait = std::getenv("KLA_TEST_LOST_WAIT") != nullptr;
+    qk_pipe_kernel<T, D, BACK><<<152, p.warps * 32, smem, s>>>(a, q);
     note_launch();
     return cudaGetLastError();
 }

@@ -388,7 +388,8 @@ KLA_API int kla_ccq_query_step(const void *q, const void *k, const float *lambda
  * d in {64, 128}; rot a multiple of 16 in 0..d (0: norm only, positions,
  * inv_freq and sections unused); at most 1024 heads; strides a multiple of 16
  * bytes and at least heads * d.  tokens == 0 is valid.  Arithmetic is fp32,
- * rounded once.  One launch, no workspace.
+ * rounded once.  One launch, no workspace and so no status word: rows whose
+ * copy a bounded wait gave up are NaN, here and in the backward pass.
  */
 KLA_API int kla_qk_norm_rope_fwd(const void *q, long long q_stride, const void *k,
                                  long long k_stride, const float *wq, const float *wk,
