@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(256, 6) attn_delta_kernel(const __grid_constan
 // refused or a wait ran out: parts are missing then.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ Args a, int per) {
-    if (*a.status != kDevOk) return;
+    const unsigned status = *a.status;        // looked at last: its read runs under the others
     constexpr int MOST = attn::kMaxSplits / 16;
     __shared__ __align__(16) float part[16][D];
     const long long n = (long long)a.total_q * a.Hq;
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
                 acc[j].x += v.x; acc[j].y += v.y; acc[j].z += v.z; acc[j].w += v.w;
             }
     }
-    if (row >= n) return;
+    if (row >= n || status != kDevOk) return;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
