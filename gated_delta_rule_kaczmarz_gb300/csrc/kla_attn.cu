@@ -73,10 +73,15 @@ int cheapest_splits(long long blocks, long long tiles, int slots, int extra, int
 }
 
 // Parts of the key axis on the CUDA cores: as on the tensor cores below, with
-// two blocks per SM, tiles of 64 keys, and a tile's time for a block's start and
+// two places an SM, tiles of 64 keys, and a tile's time for a block's start and
 // end and for the join.  In fp32, one part and the
 // chosen: B 1, T 256, 2 heads of 64 18 and 16 us; one token over 32768 keys of 8
 // heads of 64 1544 and 96 us; of B 16 over 4096 keys of 4 heads of 128 367 and 181.
+// Two places whatever the kernel: the blocks that an SM holds (1, 2 or 3, by head
+// size and rows) moved 46 of 68 sizes with heads of 64, to between 0.77 (B 2,
+// T 2048, one head: 131 and 101 us) and 1.17 of their time (40 tokens over 700 keys
+// of 8 heads: 83 and 96; B 4, T 2048, 2 heads: 141 and 164), because the model takes
+// all blocks for equally long.
 int simt_splits(const AttnProblem &p, long long blocks) {
     return cheapest_splits(blocks, ceil_div(p.total_k, (long long)p.n_seq * 64), 2 * sm_count(), 1, 1);
 }

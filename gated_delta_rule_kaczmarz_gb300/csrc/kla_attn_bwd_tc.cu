@@ -44,6 +44,9 @@
 // the wait for P^T.  A barrier that another role may pass twice before a waiter
 // looks comes in pairs, for odd and even steps.
 //
+// The barriers' phases are modelled in tests/test_attention_roles_cpu.py, by hand: a
+// change of the order of waits and arrivals here is made there too.
+//
 // Bound: the chain of a step, through its products and the softmax, at half of
 // the tensor cores' cycles (ncu: 51%).  16 + 4 heads in bf16, with the row sums:
 // B 4, T 2048, d 128 224 us; B 1, T 32768 11.1 ms, 0.99 PFLOP/s of the five

@@ -25,7 +25,8 @@
 //
 // Blocks an SM, as measured (B 4, T 2048, 8 heads of 64 or B 2, 8 + 4 heads of
 // 128): forward, tiles of 64 rows, d 64: one, 494 us (two 453, but 100 against
-// 76 where there are fewer blocks than places), d 128: two, 491 (one 559);
+// 76 where there are fewer blocks than places), d 128: two, 491 (one 559; two cost
+// fp32 172 bytes of spilled registers a thread and bf16 60, and pay all the same);
 // backward, d 64: two, 1660 (one 2115), d 128: one, 1690 (two 2100).  Tiles of
 // 16 rows: three at d 64 (one: 64 single tokens over 700 keys 244 us against 213), two
 // at d 128 (backward, T 82 over 694 keys: 295 us against 315).

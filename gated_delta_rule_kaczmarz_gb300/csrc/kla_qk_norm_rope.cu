@@ -596,7 +596,7 @@ dim3 blocks_for(const QkArgs &a, bool back) {
 
 // The pipelined kernel's shape, or warps = 0 where it does not pay: it wants 12
 // warps of three stages in a block's shared memory (backward: 8 of two), and 4
-// tokens for each.  32768 tokens of 16 + 4 heads of 128 in bf16 take 69 us with
+// tokens for each.  32768 tokens of 16 + 4 heads of 128 in bf16 take 70 us with
 // it and 74 without (backward 114 and 123), of head size 64 46 and 55 (66 and
 // 80); 65536 of 12 + 12 heads of 128, the backward's 8 warps, 260 and 284; with
 // rows of 16 + 16 heads, where it has 8 warps, 106 and 93 (backward, 6 warps,

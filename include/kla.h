@@ -446,9 +446,13 @@ KLA_API int kla_qk_norm_rope_bwd(const void *q, long long q_stride, const void *
  *              may run concurrently.
  * Hq a multiple of Hk, at most 1024; d in {64, 128}.  B, Tq or Tk may be 0;
  * all query rows times Hq stay 128 below 2^31.
- * Scores, statistics and sums are fp32.  Keys and values of rows that are not
- * the sequence's own (behind its length, of its neighbours) may hold anything;
- * its own must be finite for the queries before them to stay finite.
+ * Scores, statistics and sums are fp32, and scale <q, k> has to be finite there.
+ * On the tensor cores (bf16, up to 128 query heads to a key head) the factors of
+ * the second products are rounded to bf16 as their operands: exp(S - m) here, P and
+ * dS in the backward pass; elsewhere nothing is rounded before the result.  Keys
+ * and values of rows that are not the sequence's own (behind its length, of its
+ * neighbours) may hold anything; its own must be finite for the queries before
+ * them to stay finite.
  * Few rows over many keys (a decode batch) run split over the key axis, and
  * a second kernel joins the parts.
  */
