@@ -84,9 +84,9 @@ __device__ __forceinline__ float delta_of(const Args &a, long long row, int keys
 __device__ __forceinline__ bool rejected(const Args &a) { return a.cu_q && *a.status != kDevOk; }
 
 // Fixed lengths have no check before them: the first block of a call's first
-// kernel clears the status word (blocks start in the order of their numbers, so
-// it is none of those that a running CTA takes over).  What else writes it is a wait that ran out,
-// a second and more after that block started.
+// kernel clears the status word (blocks start in the order of their numbers, so it
+// is none of those that a running CTA takes over).  What else writes it is a wait
+// that ran out, a second and more after that block started.
 __device__ __forceinline__ void clear_status(const Args &a) {
     if (!a.cu_q && blockIdx.x == 0 && threadIdx.x == 0) *a.status = kDevOk;
 }

@@ -28,10 +28,11 @@
 // Bound: the tensor cores over a prompt (4 d flops a pair and head), HBM for
 // single tokens over a cache (the key tiles pass once for all heads of a
 // group).  16 + 4 heads of 128 in bf16: B 1, T 32768 2.73 ms, 1.61 PFLOP/s, by itself
-// (2.89 ms, 1.52, at the clock of a busy GPU); B 4, T 2048 66 us, 1.04 (three to four items a CTA, and each costs about 3 us at
-// its ends); single tokens of B 16 over 32768 keys 169 us, 6.4 TB/s.  Head size
-// 64, B 1, T 8192 186 us, 0.74 PFLOP/s: its P V has 64 columns, which take the
-// tensor cores as long as 128, and the softmax does not shrink with the head.
+// (2.89 ms, 1.52, at the clock of a busy GPU); B 4, T 2048 66 us, 1.04 (three to
+// four items a CTA, and each costs about 3 us at its ends); single tokens of B 16
+// over 32768 keys 169 us, 6.4 TB/s.  Head size 64, B 1, T 8192 186 us, 0.74
+// PFLOP/s: its P V has 64 columns, which take the tensor cores as long as 128, and
+// the softmax does not shrink with the head.
 // The exponentials are not the bound: a part of them as polynomials on the
 // multiply-add units made every size slower (T 32768: an eighth 5%).
 #include "kla_attn_tc.cuh"
