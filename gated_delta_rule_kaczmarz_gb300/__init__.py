@@ -2,7 +2,8 @@
 
 The compute path is the CUDA library ``libkla_gb300.so`` (C ABI in
 ``include/kla.h``); ``binding`` is its thin ctypes binding, ``attention`` that
-of query and key conditioning and of causal attention.  ``workloads`` draws seeded synthetic inputs.
+of query and key conditioning and of causal attention, ``cache`` that of the paged
+4-bit key/value cache.  ``workloads`` draws seeded synthetic inputs.
 """
 from .attention import (  # noqa: F401
     kla_attn,
@@ -44,4 +45,18 @@ from .binding import (  # noqa: F401
     kla_version,
     kla_workspace_status,
     load,
+)
+from .cache import (  # noqa: F401
+    kla_kv4_append,
+    kla_kv4_attn,
+    kla_kv4_attn_workspace_size,
+    kla_kv4_page_bytes,
+    kla_kv4_pool,
+    kla_kv4_read,
+    kla_pages_compact,
+    kla_pages_copy,
+    kla_pages_fork,
+    kla_pages_free,
+    kla_pages_grow,
+    kla_pages_workspace_size,
 )

@@ -25,6 +25,7 @@ KLA_ERR_UNSUPPORTED = 2
 KLA_ERR_CUDA = 3
 KLA_ERR_TIMEOUT = 4
 KLA_ERR_WORKSPACE = 5
+KLA_ERR_PAGES = 6
 KLA_DTYPE_F32 = 0
 KLA_DTYPE_BF16 = 1
 KLA_BETA_KACZMARZ = 0
@@ -133,6 +134,27 @@ def load(build_if_stale: bool = True) -> ctypes.CDLL:
         lib.kla_attn_fwd_varlen.argtypes = [*rows, ip, ip, F, vp, fp, *end]
         lib.kla_attn_bwd.argtypes = [*rows, vp, fp, vp, L, F, vp, vp, vp, *end]
         lib.kla_attn_bwd_varlen.argtypes = [*rows, vp, fp, vp, L, ip, ip, F, vp, vp, vp, *end]
+        lib.kla_kv4_page_bytes.restype = Z
+        lib.kla_kv4_page_bytes.argtypes = [I, I, I]
+        book = [I, I, I, I, I, I, I, I, vp, Z, vp]
+        for name in ("kla_kv4_append", "kla_kv4_read"):
+            fn = getattr(lib, name)
+            fn.restype = I
+            fn.argtypes = [vp, L, vp, L, vp, ip, ip, ip, F, F, *book]
+        lib.kla_kv4_attn_workspace_size.restype = Z
+        lib.kla_kv4_attn_workspace_size.argtypes = [I, I, I, I, I, I, I, I]
+        lib.kla_kv4_attn.restype = I
+        lib.kla_kv4_attn.argtypes = [vp, L, vp, ip, ip, F, F, F, vp, fp, I, *book]
+        lib.kla_pages_workspace_size.restype = Z
+        lib.kla_pages_workspace_size.argtypes = [I, I, I, I]
+        lib.kla_pages_fork.restype = I
+        lib.kla_pages_fork.argtypes = [ip, ip, ip, ip, ip, I, I, I, I, I, vp, Z, vp]
+        lib.kla_pages_grow.restype = I
+        lib.kla_pages_grow.argtypes = [vp, I, L, ip, ip, ip, ip, I, I, I, I, vp, Z, vp]
+        lib.kla_pages_compact.restype = I
+        lib.kla_pages_compact.argtypes = [vp, I, L, ip, ip, ip, ip, ip, I, I, I, I, vp, Z, vp]
+        lib.kla_pages_copy.restype = I
+        lib.kla_pages_copy.argtypes = [vp, I, L, ip, ip, I, I, vp, Z, vp]
         lib.kla_workspace_status.restype = I
         lib.kla_workspace_status.argtypes = [vp, Z, vp]
         _lib = lib

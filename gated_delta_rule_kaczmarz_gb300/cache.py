@@ -1,0 +1,279 @@
+"""Binding of the paged key/value cache in 4 bits: rows appended and read back,
+attention over it, and the pages' operators (fork, free, growth, compaction,
+copies).
+
+The same rules as in ``attention``: argument marshalling only, a non-OK status
+raises ``KlaError``, and a call runs on the device of its tensors.  A cache is a
+pool of pages, uint8 [n_pages, Hk, page / 16, 18 d] (``kla_kv4_pool``), and its
+book: table int32 [B, columns] of page numbers, lens int32 [B], refs int32
+[n_pages] with the number of sequences that hold each page.  A step of a decode
+loop: ``kla_pages_grow`` makes room, ``kla_kv4_append`` writes the new rows,
+``kla_kv4_attn`` attends over them.
+"""
+from __future__ import annotations
+
+import torch
+
+from .attention import (_at, _call, _dense, _given, _out, _refuse, _rows, _scale, _status,
+                        _type_code, _workspace)
+from .binding import load
+
+_INT = torch.int32
+
+
+def kla_kv4_page_bytes(page, Hk, d) -> int:
+    return int(load().kla_kv4_page_bytes(page, Hk, d))
+
+
+def kla_kv4_attn_workspace_size(B, Tq, Hq, Hk, d, page, columns, dtype=1) -> int:
+    return int(load().kla_kv4_attn_workspace_size(B, Tq, Hq, Hk, d, page, columns, dtype))
+
+
+def kla_pages_workspace_size(S, columns, n_pages, n=0) -> int:
+    return int(load().kla_pages_workspace_size(S, columns, n_pages, n))
+
+
+def kla_kv4_pool(n_pages, page, Hk, d, layers=None, device="cuda"):
+    """An empty pool: uint8 [n_pages, Hk, page / 16, 18 d], with `layers` one of
+    them for each layer ([layers, ...]: pool[i] for a layer's calls, the whole for
+    kla_pages_*)."""
+    if not kla_kv4_page_bytes(page, Hk, d):
+        raise ValueError("page must be a multiple of 16 and d 64 or 128 "
+                         f"(got page={page} Hk={Hk} d={d})")
+    shape = (n_pages, Hk, page // 16, 18 * d)
+    return torch.zeros(shape if layers is None else (layers, *shape), dtype=torch.uint8,
+                       device=device)
+
+
+def _book(table, lens, dev):
+    if table.dim() != 2:
+        raise ValueError(f"table must have shape [B, columns], got {tuple(table.shape)}")
+    return (_dense(table, "table", _INT, dev, table.shape),
+            _dense(lens, "lens", _INT, dev, table.shape[:1]))
+
+
+def _pool(pool, dev, Hk=None, d=None):
+    """The address of a layer's pool, and (Hk, d, page, n_pages)."""
+    if pool.dim() != 4:
+        raise ValueError("pool must have shape [n_pages, Hk, page / 16, 18 d], got "
+                         f"{tuple(pool.shape)}")
+    n_pages, heads, blocks, size = pool.shape
+    d = size // 18 if d is None else d
+    if heads != (heads if Hk is None else Hk) or size != 18 * d:
+        _refuse(pool, "pool", torch.uint8, dev, (n_pages, Hk, blocks, 18 * d))
+    return _dense(pool, "pool", torch.uint8, dev, pool.shape), (heads, d, 16 * blocks, n_pages)
+
+
+def _lists(cu_seqlens, table, dev):
+    return _dense(cu_seqlens, "cu_seqlens", _INT, dev, (table.shape[0] + 1,))
+
+
+def _word(workspace, check, like):
+    """The status word of calls that need no workspace: (workspace, its size)."""
+    if workspace is None:
+        if not check:
+            return None, 0
+        return torch.empty(256, dtype=torch.uint8, device=like.device), 256
+    if workspace.get_device() != like.get_device():
+        raise ValueError(f"workspace must be on {like.device}, got {workspace.device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _rows_call(fn, k, v, pool, table, lens, cu_seqlens, units, workspace, check):
+    dt, dev = _type_code(k), pool.get_device()
+    packed = cu_seqlens is not None
+    if k.dim() != (3 if packed else 4):
+        raise ValueError(f"k must have shape {'[total, Hk, d]' if packed else '[B, T, Hk, d]'}, "
+                         f"got {tuple(k.shape)}")
+    hk, d = k.shape[-2], k.shape[-1]
+    at, (hk, d, page, n_pages) = _pool(pool, dev, hk, d)
+    book = _book(table, lens, dev)
+    B, columns = table.shape
+    shape = k.shape if packed else (B, k.shape[1], hk, d)
+    ks, vs = _rows(k, "k", k.dtype, dev, shape), _rows(v, "v", k.dtype, dev, shape)
+    cu = _lists(cu_seqlens, table, dev) if packed else None
+    workspace, wsb = _word(workspace, check, pool)
+    _call(dev, fn, k.data_ptr(), ks, v.data_ptr(), vs, at, *book, cu, *units, B, shape[-3], hk, d,
+          page, n_pages, columns, dt, _at(workspace), wsb)
+    if check:
+        _call(dev, _status, workspace, wsb)
+
+
+def kla_kv4_append(k, v, pool, table, lens, cu_seqlens=None, k_unit=1.0, v_unit=1.0,
+                   workspace=None, stream=None, check_status=False):
+    """Writes rows of keys and values to the places of each sequence's last
+    positions (lens counts them already).  k, v: [B,T,Hk,d], or packed [total,Hk,d]
+    with cu_seqlens int32 [B+1]; views of a fused projection's output among them.
+    Rows before position 0 are left out.  k_unit, v_unit: powers of two, the same
+    in every call on a cache.  check_status waits for the call and raises what the
+    device reports."""
+    if stream is not None:
+        with _given(stream, pool):
+            return kla_kv4_append(k, v, pool, table, lens, cu_seqlens, k_unit, v_unit, workspace,
+                                  check_status=check_status)
+    _rows_call(load().kla_kv4_append, k, v, pool, table, lens, cu_seqlens, (k_unit, v_unit),
+               workspace, check_status)
+
+
+def kla_kv4_read(pool, table, lens, T=None, total=None, cu_seqlens=None, dtype=torch.bfloat16,
+                 k_unit=1.0, v_unit=1.0, k_out=None, v_out=None, workspace=None, stream=None,
+                 check_status=False):
+    """The inverse of kla_kv4_append: the last T positions of each sequence,
+    [B,T,Hk,d], or packed rows [total,Hk,d] with cu_seqlens; rows before position 0
+    are zeros.  k_out, v_out: written where given, views among them.  Returns
+    (k, v)."""
+    if stream is not None:
+        with _given(stream, pool):
+            return kla_kv4_read(pool, table, lens, T, total, cu_seqlens, dtype, k_unit, v_unit,
+                                k_out, v_out, workspace, check_status=check_status)
+    if (T is None) == (cu_seqlens is None) or (total is None) != (cu_seqlens is None):
+        raise ValueError("T must be given, or total and cu_seqlens")
+    _, (hk, d, _, _) = _pool(pool, pool.get_device())
+    shape = (table.shape[0], T, hk, d) if cu_seqlens is None else (total, hk, d)
+    out = [torch.empty(shape, dtype=dtype, device=pool.device) if x is None else x
+           for x in (k_out, v_out)]
+    for x, name in zip(out, ("k_out", "v_out")):
+        if x.shape != shape:
+            _refuse(x, name, dtype, pool.get_device(), shape)
+    _rows_call(load().kla_kv4_read, *out, pool, table, lens, cu_seqlens, (k_unit, v_unit),
+               workspace, check_status)
+    return tuple(out)
+
+
+def kla_kv4_attn(q, pool, table, lens, scale=None, k_unit=1.0, v_unit=1.0, o=None, lse=None,
+                 return_lse=True, workspace=None, stream=None, check_status=False):
+    """Causal attention with grouped heads over a paged 4-bit cache.  q:
+    [B,Tq,Hq,d], the last Tq positions of each sequence; query i sees the positions
+    j <= i + lens - Tq; scale: 1/sqrt(d) unless given.  Returns (o, lse), o dense,
+    lse [B,Tq,Hq] fp32 (None with return_lse=False)."""
+    if stream is not None:
+        with _given(stream, q):
+            return kla_kv4_attn(q, pool, table, lens, scale, k_unit, v_unit, o, lse, return_lse,
+                                workspace, check_status=check_status)
+    if q.dim() != 4:
+        raise ValueError(f"q must have shape [B, Tq, Hq, d], got {tuple(q.shape)}")
+    dt, dev = _type_code(q), q.get_device()
+    B, Tq, hq, d = q.shape
+    qs = _rows(q, "q", q.dtype, dev, q.shape)
+    at, (hk, d, page, n_pages) = _pool(pool, dev, d=d)
+    if table.shape[0] != B:
+        raise ValueError(f"table must have {B} rows, got {tuple(table.shape)}")
+    book, columns = _book(table, lens, dev), table.shape[1]
+    o, out = _out(o, "o", q.shape, q.dtype, q)
+    stats = None
+    if return_lse or lse is not None:
+        lse, stats = _out(lse, "lse", (B, Tq, hq), torch.float32, q)
+    lib, sizes = load(), (B, Tq, hq, hk, d, page)
+    workspace, wsb = _workspace(dev, lib.kla_kv4_attn_workspace_size, (*sizes, columns, dt), q,
+                                workspace)
+    _call(dev, lib.kla_kv4_attn, q.data_ptr(), qs, at, *book, _scale(scale, d), k_unit, v_unit,
+          out, stats, *sizes, n_pages, columns, dt, _at(workspace), wsb)
+    if check_status:
+        _call(dev, _status, workspace, wsb)
+    return o, lse
+
+
+# ---------------------------------------------------------------------- pages
+def _layers(pool, n_pages):
+    """The address of all layers' pages, their number and a page's bytes."""
+    if pool.dim() < 2 or (n_pages is not None and pool.shape[1] != n_pages):
+        raise ValueError(f"pool must have shape [layers, {n_pages or 'n_pages'}, ...], got "
+                         f"{tuple(pool.shape)}")
+    if not pool.is_contiguous():
+        raise ValueError("pool must be contiguous")
+    return pool.data_ptr(), pool.shape[0], pool[:1, :1].numel() * pool.element_size()
+
+
+def _pages_call(fn, dev, like, args, sizes, workspace, check):
+    """args up to the sizes (S, columns, n_pages, n) of the workspace's, then it."""
+    workspace, wsb = _workspace(dev, load().kla_pages_workspace_size, sizes, like, workspace)
+    _call(dev, fn, *args, _at(workspace), wsb)
+    if check:
+        _call(dev, _status, workspace, wsb)
+
+
+def _held(table, lens, refs):
+    dev = table.get_device()
+    n_pages = refs.numel()
+    return dev, n_pages, (*_book(table, lens, dev), _dense(refs, "refs", _INT, dev, (n_pages,)))
+
+
+def kla_pages_fork(table, lens, refs, src, dst, page, workspace=None, stream=None,
+                   check_status=False):
+    """Sequence dst[f] becomes what src[f] was before the call, for all f at once:
+    its length and its pages, shared (src[f] = -1: empty).  src, dst: int32 [n] on
+    the device, dst without repetition.  Changes table, lens and refs."""
+    if stream is not None:
+        with _given(stream, table):
+            return kla_pages_fork(table, lens, refs, src, dst, page, workspace,
+                                  check_status=check_status)
+    dev, n_pages, book = _held(table, lens, refs)
+    n = dst.numel()
+    to = _dense(dst, "dst", _INT, dev, (n,))
+    of = _dense(src, "src", _INT, dev, (n,))
+    S, columns = table.shape
+    _pages_call(load().kla_pages_fork, dev, table, (*book, of, to, S, columns, page, n_pages, n),
+                (S, columns, n_pages, n), workspace, check_status)
+
+
+def kla_pages_free(table, lens, refs, seqs, page, workspace=None, stream=None,
+                   check_status=False):
+    """The sequences seqs (int32 [n]) become empty; pages that nobody holds any
+    more are free."""
+    kla_pages_fork(table, lens, refs, None, seqs, page, workspace, stream, check_status)
+
+
+def kla_pages_grow(pool, table, lens, refs, n_new, page, workspace=None, stream=None,
+                   check_status=False):
+    """Room for n_new[s] (int32 [S]) more positions of every sequence; lens counts
+    them.  A shared last page that is partly filled is copied first, in all layers of
+    the pool ([layers, n_pages, ...], any type).  check_status raises
+    KLA_ERR_PAGES where there are not enough free pages; nothing has changed then."""
+    if stream is not None:
+        with _given(stream, table):
+            return kla_pages_grow(pool, table, lens, refs, n_new, page, workspace,
+                                  check_status=check_status)
+    dev, n_pages, book = _held(table, lens, refs)
+    S, columns = table.shape
+    more = _dense(n_new, "n_new", _INT, dev, (S,))
+    if pool.get_device() != dev:
+        _refuse(pool, "pool", pool.dtype, dev, pool.shape)
+    _pages_call(load().kla_pages_grow, dev, table,
+                (*_layers(pool, n_pages), *book, more, S, columns, page, n_pages),
+                (S, columns, n_pages, 0), workspace, check_status)
+
+
+def kla_pages_compact(pool, table, lens, refs, page, page_map=None, n_used=None, workspace=None,
+                      stream=None, check_status=False):
+    """Pages in use move below n_used, the number of them, in all layers of the
+    pool.  Returns (page_map, n_used): int32 [n_pages], where each page is now (-1:
+    free), and int32 [1], on the device."""
+    if stream is not None:
+        with _given(stream, table):
+            return kla_pages_compact(pool, table, lens, refs, page, page_map, n_used, workspace,
+                                     check_status=check_status)
+    dev, n_pages, book = _held(table, lens, refs)
+    S, columns = table.shape
+    page_map, where = _out(page_map, "page_map", (n_pages,), _INT, refs)
+    n_used, count = _out(n_used, "n_used", (1,), _INT, refs)
+    if pool.get_device() != dev:
+        _refuse(pool, "pool", pool.dtype, dev, pool.shape)
+    _pages_call(load().kla_pages_compact, dev, table,
+                (*_layers(pool, n_pages), *book, where, count, S, columns, page, n_pages),
+                (S, columns, n_pages, 0), workspace, check_status)
+    return page_map, n_used
+
+
+def kla_pages_copy(pool, src, dst, workspace=None, stream=None, check_status=False):
+    """The contents of pages src[i] to dst[i] in all layers of the pool ([layers,
+    n_pages, ...], any type; KLA's states [B,H,dk,dv] as S[None]).  No target may be
+    there twice or be the source of another."""
+    if stream is not None:
+        with _given(stream, pool):
+            return kla_pages_copy(pool, src, dst, workspace, check_status=check_status)
+    dev, n = pool.get_device(), dst.numel()
+    at, layers, size = _layers(pool, None)
+    n_pages = pool.shape[1]
+    of, to = _dense(src, "src", _INT, dev, (n,)), _dense(dst, "dst", _INT, dev, (n,))
+    _pages_call(load().kla_pages_copy, dev, pool, (at, layers, size, of, to, n_pages, n),
+                (0, 0, n_pages, n), workspace, check_status)

@@ -2,6 +2,7 @@
 // path selection and launches.  No device memory is allocated here.
 
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -286,6 +287,7 @@ const char *kla_status_str(int status) {
         case KLA_ERR_CUDA: return "CUDA error";
         case KLA_ERR_TIMEOUT: return "device wait timed out";
         case KLA_ERR_WORKSPACE: return "workspace missing or too small";
+        case KLA_ERR_PAGES: return "not enough free pages";
         default: return "unknown status";
     }
 }
@@ -830,6 +832,280 @@ int kla_attn_bwd_varlen(const void *q, long long q_stride, const void *k, long l
     return run_attn(p, true, workspace, workspace_bytes, stream);
 }
 
+}  // extern "C"
+
+namespace {
+// Sizes of a cache's book.  Tables and pages are numbered in 32 bits.
+kla_status check_pages(int S, int columns, int page, int n_pages) {
+    if (S < 0 || columns < 0 || n_pages < 0 || page <= 0)
+        return fail(KLA_ERR_INVALID_ARG, "sizes must not be negative, a page not empty (S=%d "
+                    "columns=%d n_pages=%d page=%d)", S, columns, n_pages, page);
+    if ((long long)S * columns > INT32_MAX || (long long)columns * page > INT32_MAX)
+        return fail(KLA_ERR_UNSUPPORTED, "table too large (sequences times columns and columns times "
+                    "page must fit in int32)");
+    return KLA_OK;
+}
+kla_status check_kv4(const void *pool, const int *table, const int *lens, int B, int Hk, int d, int page,
+                     int n_pages, int columns, int dtype, float k_unit, float v_unit) {
+    kla_status st = check_pages(B, columns, page, n_pages);
+    if (st != KLA_OK) return st;
+    if (Hk <= 0) return fail(KLA_ERR_INVALID_ARG, "Hk must be positive (Hk=%d)", Hk);
+    if (dtype != KLA_DTYPE_F32 && dtype != KLA_DTYPE_BF16)
+        return fail(KLA_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+    if (d != 64 && d != 128)
+        return fail(KLA_ERR_UNSUPPORTED, "supported head sizes: 64 and 128 (got %d)", d);
+    if (page % 16 != 0)
+        return fail(KLA_ERR_UNSUPPORTED, "a page must hold a multiple of 16 tokens (got %d)", page);
+    if (Hk > 1024) return fail(KLA_ERR_UNSUPPORTED, "at most 1024 heads (Hk=%d)", Hk);
+    if ((long long)n_pages * Hk * (page / 16) > UINT32_MAX)
+        return fail(KLA_ERR_UNSUPPORTED, "pool too large (blocks of 16 tokens must fit in 32 bits)");
+    const float units[] = {k_unit, v_unit};
+    for (float u : units) {
+        int e;
+        if (!(u > 0.f) || !std::isfinite(u) || std::frexp(u, &e) != 0.5f || e < -31 || e > 33)
+            return fail(KLA_ERR_INVALID_ARG, "k_unit and v_unit must be powers of two from 2^-32 to 2^32");
+    }
+    if (B == 0) return KLA_OK;
+    if (!lens || ((!table || !pool) && n_pages > 0 && columns > 0))
+        return fail(KLA_ERR_INVALID_ARG, "pool, table and lens must be non-null");
+    if (!aligned16(pool) || !aligned4(table) || !aligned4(lens))
+        return fail(KLA_ERR_INVALID_ARG, "the pool must be 16-byte aligned, tables and lengths 4-byte");
+    return KLA_OK;
+}
+
+kla_status check_workspace(const void *workspace, size_t have, size_t need) {
+    if (workspace == nullptr || have < need)
+        return fail(KLA_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need,
+                    workspace ? have : (size_t)0);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(KLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    return KLA_OK;
+}
+
+// Rows into the pages or out of them.
+kla_status run_rows(kla::Kv4Rows &p, bool read, void *workspace, size_t workspace_bytes, void *stream) {
+    if (p.T < 0) return fail(KLA_ERR_INVALID_ARG, "negative size (T=%d)", p.T);
+    kla_status st = check_kv4(p.pool, p.table, p.lens, p.B, p.Hk, p.d, p.page, p.n_pages, p.columns,
+                              p.dtype, p.k_unit, p.v_unit);
+    if (st != KLA_OK) return st;
+    if (!aligned4(p.cu)) return fail(KLA_ERR_INVALID_ARG, "cu_seqlens must be 4-byte aligned");
+    if (p.cu && p.B == 0 && p.T > 0)
+        return fail(KLA_ERR_INVALID_ARG, "rows without sequences (N == 0, total=%d)", p.T);
+    p.total = p.T;
+    if (!p.cu && (long long)p.B * p.T > INT32_MAX)
+        return fail(KLA_ERR_UNSUPPORTED, "problem too large (B*T must fit in int32)");
+    if (kla::kv4_rows_too_large(p))
+        return fail(KLA_ERR_UNSUPPORTED, "problem too large (rows times heads must fit a launch)");
+    const bool any = p.B > 0 && p.T > 0;
+    const Rows rows[] = {{read ? p.k_out : p.k, p.k_stride, any ? p.Hk : 0, "k"},
+                         {read ? p.v_out : p.v, p.v_stride, any ? p.Hk : 0, "v"}};
+    for (const Rows &r : rows)
+        if ((st = check_rows(r, p.d, p.dtype)) != KLA_OK) return st;
+    if (workspace != nullptr && (st = check_workspace(workspace, workspace_bytes, kla::kWsHeader)) != KLA_OK)
+        return st;
+    if (inject_launch_fault()) return fail(KLA_ERR_CUDA, "injected launch fault (KLA_FAULT_INJECT)");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = reset_status(workspace, workspace_bytes, s);
+    if (e != cudaSuccess) return cuda_fail(e, "status init");
+    if (p.B == 0 || (!any && !p.cu)) return ok();
+    p.status = static_cast<unsigned *>(workspace);
+    p.k_inv = 1.f / p.k_unit;
+    p.v_inv = 1.f / p.v_unit;
+    e = kla::launch_kv4_rows(p, read, s);
+    return e == cudaSuccess ? ok() : cuda_fail(e, read ? "cache read launch" : "cache append launch");
+}
+
+kla_status kv4_attn_sizes(kla::Kv4Attn &p, int B, int Tq, int Hq, int Hk, int d, int page, int n_pages,
+                          int columns, int dtype) {
+    if (B < 0 || Tq < 0) return fail(KLA_ERR_INVALID_ARG, "negative size (B=%d Tq=%d)", B, Tq);
+    if (Hq <= 0 || Hk <= 0 || Hq % Hk != 0)
+        return fail(KLA_ERR_INVALID_ARG, "Hq must be a positive multiple of Hk (Hq=%d Hk=%d)", Hq, Hk);
+    if (Hq > 1024) return fail(KLA_ERR_UNSUPPORTED, "at most 1024 heads (Hq=%d)", Hq);
+    p.B = B; p.Tq = Tq; p.Hq = Hq; p.Hk = Hk; p.d = d; p.page = page; p.n_pages = n_pages;
+    p.columns = columns; p.dtype = dtype;
+    const kla_status st = check_kv4(nullptr, nullptr, nullptr, 0, Hk, d, page, n_pages, columns, dtype, 1.f, 1.f);
+    if (st != KLA_OK) return st;
+    if ((long long)B * columns > INT32_MAX)
+        return fail(KLA_ERR_UNSUPPORTED, "table too large (sequences times columns must fit in int32)");
+    if (kla::kv4_attn_too_large(p))
+        return fail(KLA_ERR_UNSUPPORTED, "problem too large (query rows times heads and tiles must fit in int32)");
+    return KLA_OK;
+}
+
+kla_status pages_call(kla::Pages &p, int n, void *workspace, size_t workspace_bytes) {
+    const kla_status st = check_workspace(workspace, workspace_bytes,
+                                          kla::pages_workspace_bytes(p.S, p.columns, p.n_pages, n));
+    if (st != KLA_OK) return st;
+    p.n = n;
+    p.ws = workspace;
+    if (inject_launch_fault()) return fail(KLA_ERR_CUDA, "injected launch fault (KLA_FAULT_INJECT)");
+    return KLA_OK;
+}
+kla_status check_book(const kla::Pages &p) {
+    const kla_status st = check_pages(p.S, p.columns, p.page, p.n_pages);
+    if (st != KLA_OK) return st;
+    if ((p.S > 0 && (!p.lens || (p.columns > 0 && !p.table))) || (p.n_pages > 0 && !p.refs))
+        return fail(KLA_ERR_INVALID_ARG, "table, lens and refs must be non-null");
+    if (!aligned4(p.table) || !aligned4(p.lens) || !aligned4(p.refs))
+        return fail(KLA_ERR_INVALID_ARG, "table, lens and refs must be 4-byte aligned");
+    return KLA_OK;
+}
+kla_status check_pool(const kla::Pages &p) {
+    if (p.layers < 0 || p.page_bytes < 0)
+        return fail(KLA_ERR_INVALID_ARG, "negative size (layers=%d page_bytes=%lld)", p.layers, p.page_bytes);
+    if (p.page_bytes % 16 != 0)
+        return fail(KLA_ERR_UNSUPPORTED, "a page must be a multiple of 16 bytes (got %lld)", p.page_bytes);
+    if (p.page_bytes > ((long long)1 << 40))
+        return fail(KLA_ERR_UNSUPPORTED, "a page of at most 2^40 bytes (got %lld)", p.page_bytes);
+    if (p.layers > 0 && p.n_pages > 0 && p.page_bytes > 0 && !p.pool)
+        return fail(KLA_ERR_INVALID_ARG, "the pool must be non-null");
+    if (!aligned16(p.pool)) return fail(KLA_ERR_INVALID_ARG, "the pool must be 16-byte aligned");
+    return KLA_OK;
+}
+}  // namespace
+
+extern "C" {
+
+size_t kla_kv4_page_bytes(int page, int Hk, int d) {
+    if (page <= 0 || page % 16 != 0 || Hk <= 0 || (d != 64 && d != 128)) return 0;
+    return (size_t)(page / 16) * Hk * 18 * d;
+}
+
+int kla_kv4_append(const void *k, long long k_stride, const void *v, long long v_stride, void *pool,
+                   const int *table, const int *lens, const int *cu_seqlens, float k_unit,
+                   float v_unit, int B, int T, int Hk, int d, int page, int n_pages, int columns,
+                   int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    kla::Kv4Rows p{};
+    p.k = k; p.v = v; p.k_stride = k_stride; p.v_stride = v_stride; p.cu = cu_seqlens;
+    p.pool = pool; p.table = table; p.lens = lens; p.B = B; p.T = T; p.Hk = Hk; p.d = d;
+    p.page = page; p.n_pages = n_pages; p.columns = columns; p.dtype = dtype;
+    p.k_unit = k_unit; p.v_unit = v_unit;
+    return run_rows(p, false, workspace, workspace_bytes, stream);
+}
+
+int kla_kv4_read(void *k, long long k_stride, void *v, long long v_stride, const void *pool,
+                 const int *table, const int *lens, const int *cu_seqlens, float k_unit,
+                 float v_unit, int B, int T, int Hk, int d, int page, int n_pages, int columns,
+                 int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    kla::Kv4Rows p{};
+    p.k_out = k; p.v_out = v; p.k_stride = k_stride; p.v_stride = v_stride; p.cu = cu_seqlens;
+    p.pool = const_cast<void *>(pool); p.table = table; p.lens = lens; p.B = B; p.T = T; p.Hk = Hk;
+    p.d = d; p.page = page; p.n_pages = n_pages; p.columns = columns; p.dtype = dtype;
+    p.k_unit = k_unit; p.v_unit = v_unit;
+    return run_rows(p, true, workspace, workspace_bytes, stream);
+}
+
+size_t kla_kv4_attn_workspace_size(int B, int Tq, int Hq, int Hk, int d, int page, int columns, int dtype) {
+    kla::Kv4Attn p{};
+    if (kv4_attn_sizes(p, B, Tq, Hq, Hk, d, page, 0, columns, dtype) != KLA_OK) return 0;
+    return (long long)B * Tq == 0 ? 0 : kla::kv4_attn_workspace_bytes(p);
+}
+
+int kla_kv4_attn(const void *q, long long q_stride, const void *pool, const int *table,
+                 const int *lens, float scale, float k_unit, float v_unit, void *o, float *lse,
+                 int B, int Tq, int Hq, int Hk, int d, int page, int n_pages, int columns,
+                 int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    kla::Kv4Attn p{};
+    kla_status st = kv4_attn_sizes(p, B, Tq, Hq, Hk, d, page, n_pages, columns, dtype);
+    if (st != KLA_OK) return st;
+    if ((st = check_kv4(pool, table, lens, B, Hk, d, page, n_pages, columns, dtype, k_unit, v_unit)) != KLA_OK)
+        return st;
+    if (!(scale > 0.f) || !(scale <= 2e38f) || !(scale * k_unit <= 2e38f) || !(scale * k_unit >= 1e-37f))
+        return fail(KLA_ERR_INVALID_ARG, "scale and scale * k_unit must be positive, normal and at most 2e38");
+    p.q = q; p.q_stride = q_stride; p.pool = pool; p.table = table; p.lens = lens; p.o = o;
+    p.lse = lse; p.scale = scale; p.k_unit = k_unit; p.v_unit = v_unit;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool any = B > 0 && Tq > 0;
+    const Rows rows = {q, q_stride, any ? Hq : 0, "q"};
+    if ((st = check_rows(rows, d, dtype)) != KLA_OK) return st;
+    if (any && !o) return fail(KLA_ERR_INVALID_ARG, "o must be non-null");
+    if (!aligned16(o) || !aligned4(lse))
+        return fail(KLA_ERR_INVALID_ARG, "o must be 16-byte aligned, lse 4-byte");
+    if (any && (st = check_workspace(workspace, workspace_bytes, kla::kv4_attn_workspace_bytes(p))) != KLA_OK)
+        return st;
+    if (inject_launch_fault()) return fail(KLA_ERR_CUDA, "injected launch fault (KLA_FAULT_INJECT)");
+    if (!any) {
+        const cudaError_t e = reset_status(workspace, workspace_bytes, s);
+        return e == cudaSuccess ? ok() : cuda_fail(e, "status init");
+    }
+    p.ws = workspace;
+    const cudaError_t e = kla::launch_kv4_attn(p, s);
+    return e == cudaSuccess ? ok() : cuda_fail(e, "cache attention launch");
+}
+
+size_t kla_pages_workspace_size(int S, int columns, int n_pages, int n) {
+    if (n < 0 || check_pages(S, columns, 1, n_pages) != KLA_OK) return 0;
+    return kla::pages_workspace_bytes(S, columns, n_pages, n);
+}
+
+int kla_pages_fork(int *table, int *lens, int *refs, const int *src, const int *dst, int S,
+                   int columns, int page, int n_pages, int n, void *workspace,
+                   size_t workspace_bytes, void *stream) {
+    kla::Pages p{};
+    p.table = table; p.lens = lens; p.refs = refs; p.S = S; p.columns = columns; p.page = page;
+    p.n_pages = n_pages; p.src = src; p.dst = dst;
+    kla_status st = check_book(p);
+    if (st != KLA_OK) return st;
+    if (n < 0) return fail(KLA_ERR_INVALID_ARG, "negative size (n=%d)", n);
+    if (n > 0 && !dst) return fail(KLA_ERR_INVALID_ARG, "dst must be non-null");
+    if (!aligned4(src) || !aligned4(dst))
+        return fail(KLA_ERR_INVALID_ARG, "src and dst must be 4-byte aligned");
+    if ((long long)n * (columns + 1LL) > INT32_MAX)
+        return fail(KLA_ERR_UNSUPPORTED, "problem too large (rows times columns must fit in int32)");
+    if ((st = pages_call(p, n, workspace, workspace_bytes)) != KLA_OK) return st;
+    const cudaError_t e = kla::launch_pages_fork(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "fork launch");
+}
+
+int kla_pages_grow(void *pool, int layers, long long page_bytes, int *table, int *lens, int *refs,
+                   const int *n_new, int S, int columns, int page, int n_pages, void *workspace,
+                   size_t workspace_bytes, void *stream) {
+    kla::Pages p{};
+    p.table = table; p.lens = lens; p.refs = refs; p.S = S; p.columns = columns; p.page = page;
+    p.n_pages = n_pages; p.more = n_new; p.pool = pool; p.layers = layers; p.page_bytes = page_bytes;
+    kla_status st = check_book(p);
+    if (st != KLA_OK || (st = check_pool(p)) != KLA_OK) return st;
+    if (S > 0 && !n_new) return fail(KLA_ERR_INVALID_ARG, "n_new must be non-null");
+    if (!aligned4(n_new)) return fail(KLA_ERR_INVALID_ARG, "n_new must be 4-byte aligned");
+    if ((st = pages_call(p, 0, workspace, workspace_bytes)) != KLA_OK) return st;
+    const cudaError_t e = kla::launch_pages_grow(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "growth launch");
+}
+
+int kla_pages_compact(void *pool, int layers, long long page_bytes, int *table, const int *lens,
+                      int *refs, int *page_map, int *n_used, int S, int columns, int page,
+                      int n_pages, void *workspace, size_t workspace_bytes, void *stream) {
+    kla::Pages p{};
+    p.table = table; p.lens = const_cast<int *>(lens); p.refs = refs; p.S = S; p.columns = columns;
+    p.page = page; p.n_pages = n_pages; p.page_map = page_map; p.n_used = n_used; p.pool = pool;
+    p.layers = layers; p.page_bytes = page_bytes;
+    kla_status st = check_book(p);
+    if (st != KLA_OK || (st = check_pool(p)) != KLA_OK) return st;
+    if ((n_pages > 0 && !page_map) || !n_used)
+        return fail(KLA_ERR_INVALID_ARG, "page_map and n_used must be non-null");
+    if (!aligned4(page_map) || !aligned4(n_used))
+        return fail(KLA_ERR_INVALID_ARG, "page_map and n_used must be 4-byte aligned");
+    if ((st = pages_call(p, 0, workspace, workspace_bytes)) != KLA_OK) return st;
+    const cudaError_t e = kla::launch_pages_compact(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "compaction launch");
+}
+
+int kla_pages_copy(void *pool, int layers, long long page_bytes, const int *src, const int *dst,
+                   int n_pages, int n, void *workspace, size_t workspace_bytes, void *stream) {
+    kla::Pages p{};
+    p.page = 1; p.n_pages = n_pages; p.src = src; p.dst = dst; p.pool = pool; p.layers = layers;
+    p.page_bytes = page_bytes;
+    kla_status st = check_pages(0, 0, 1, n_pages);
+    if (st != KLA_OK || (st = check_pool(p)) != KLA_OK) return st;
+    if (n < 0) return fail(KLA_ERR_INVALID_ARG, "negative size (n=%d)", n);
+    if (n > 0 && (!src || !dst)) return fail(KLA_ERR_INVALID_ARG, "src and dst must be non-null");
+    if (!aligned4(src) || !aligned4(dst))
+        return fail(KLA_ERR_INVALID_ARG, "src and dst must be 4-byte aligned");
+    if ((st = pages_call(p, n, workspace, workspace_bytes)) != KLA_OK) return st;
+    const cudaError_t e = kla::launch_pages_copy(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "page copy launch");
+}
+
 int kla_workspace_status(const void *workspace, size_t workspace_bytes, void *stream) {
     if (workspace == nullptr || workspace_bytes < kla::kWsHeader) return ok();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -841,6 +1117,9 @@ int kla_workspace_status(const void *workspace, size_t workspace_bytes, void *st
     if (word == kla::kDevOk) return ok();
     if (word == kla::kDevBadSeqlens)
         return fail(KLA_ERR_INVALID_ARG, "cu_seqlens rejected on the device");
+    if (word == kla::kDevBadTable)
+        return fail(KLA_ERR_INVALID_ARG, "a page table, length or sequence number rejected on the device");
+    if (word == kla::kDevNoPages) return fail(KLA_ERR_PAGES, "not enough free pages");
     if (word == kla::kDevTimeout) return fail(KLA_ERR_TIMEOUT, "a device-side wait timed out");
     return fail(KLA_ERR_CUDA, "unknown device status %u", word);
 }

@@ -17,6 +17,8 @@ enum DevStatus : unsigned {
     kDevOk = 0,
     kDevBadSeqlens = 1,
     kDevTimeout = 2,
+    kDevBadTable = 3,     // pages, lengths or sequence numbers out of range
+    kDevNoPages = 4,
 };
 
 // One prefill request after host validation.  Token row r of head h of a
@@ -130,6 +132,59 @@ cudaError_t launch_attn_fwd(const AttnProblem &p, cudaStream_t s);
 cudaError_t launch_attn_bwd(const AttnProblem &p, cudaStream_t s);
 // Packed, total_q 0: the check of the tables, and zeros in dk and dv if given.
 cudaError_t launch_attn_no_queries(const AttnProblem &p, cudaStream_t s);
+
+// Pages of a cache and the rows in 4 bits that they hold (layout: kla_kv4.cuh).
+// Sequence b's positions 0 .. lens[b] - 1 lie in the pages table[b][0 ..
+// ceil(lens[b] / page) - 1] of the pool.
+struct Kv4Rows {
+    const void *k, *v;              // append: rows of Hk heads of d
+    void *k_out, *v_out;            // read
+    long long k_stride, v_stride;   // elements between token rows
+    const int *cu;                  // device [B + 1]: packed rows, or nullptr: T of each sequence
+    int total;                      // packed: rows
+    bool from_start;                // rows are positions 0 .. min(T, len) - 1, else the last T
+    void *pool;
+    const int *table, *lens;
+    int B, T, Hk, d, page, n_pages, columns, dtype;
+    float k_unit, v_unit, k_inv, v_inv;
+    unsigned *status;               // or nullptr
+};
+bool kv4_rows_too_large(const Kv4Rows &p);
+cudaError_t launch_kv4_rows(const Kv4Rows &p, bool read, cudaStream_t s);
+
+struct Kv4Attn {
+    const void *q;
+    long long q_stride;
+    const void *pool;
+    const int *table, *lens;
+    void *o;
+    float *lse;                     // or nullptr
+    int B, Tq, Hq, Hk, d, page, n_pages, columns, dtype;
+    float scale, k_unit, v_unit;
+    void *ws;                       // kv4_attn_workspace_bytes(p), the status word first
+};
+size_t kv4_attn_workspace_bytes(const Kv4Attn &p);
+bool kv4_attn_too_large(const Kv4Attn &p);
+cudaError_t launch_kv4_attn(const Kv4Attn &p, cudaStream_t s);
+
+// The pages' own operators (kla_pages.cu).
+struct Pages {
+    int *table, *lens, *refs;
+    int S, columns, page, n_pages;
+    const int *src, *dst;           // fork: n entries; copy: pages
+    int n;
+    const int *more;                // grow: [S]
+    int *page_map, *n_used;         // compact
+    void *pool;                     // [layers][n_pages][page_bytes]
+    int layers;
+    long long page_bytes;
+    void *ws;                       // the status word first
+};
+size_t pages_workspace_bytes(int S, int columns, int n_pages, int n);
+cudaError_t launch_pages_fork(const Pages &p, cudaStream_t s);
+cudaError_t launch_pages_grow(const Pages &p, cudaStream_t s);
+cudaError_t launch_pages_compact(const Pages &p, cudaStream_t s);
+cudaError_t launch_pages_copy(const Pages &p, cudaStream_t s);
 
 // Backward of the chunkwise forward (kla_chunk_bwd.cu), fixed length or varlen.
 struct BwdProblem {

@@ -1,0 +1,882 @@
+// Causal attention of few query rows over the 4-bit paged cache.
+//
+//   s = scale <q, k>,  p = exp2(s log2 e - base),  o = sum p v / sum p
+//
+// Work.  Keys go in tiles of 32 (two blocks of the cache).  A work item is a
+// sequence, key head and group of R query rows (the heads of a key head and the
+// call's tokens, packed); all items' tiles in a row are cut into equal parts, one
+// for each warp of one CTA an SM, so lengths may differ as they like.  A warp
+// keeps its own running base, sums and outputs and brings its tiles by bulk copies
+// through a ring of its own: warps wait for nobody.  What the warps of a CTA hold
+// of the same item is joined in shared memory; items that more than one CTA had
+// are joined by a second kernel.
+//
+// Products.  S^T = K Q^T and O^T = V^T P^T as m16n8k16: 16 keys (16 features)
+// against 8 query rows, so 4 rows of a decode batch fill half of an operand where
+// 16 rows a tile would leave it to a quarter.  A thread's 16 bytes of shared memory
+// are its part of the operand for all products of a block, whichever features the
+// hardware numbers so: Q is laid out and O written back in the same order.  Codes become fp16 by
+// the hardware's conversion and one multiplication by the scale, exactly.  q is
+// split into one (bf16) or two (fp32) fp16 terms after a power of two per row, p is
+// rounded to fp16 once (bf16) or split in two (fp32); sums are fp32.
+//
+// Bound by HBM for long caches.
+#include <cuda_bf16.h>
+
+#include <atomic>
+#include <cstdlib>
+
+#include "kla_attn.cuh"
+#include "kla_kv4.cuh"
+#include "kla_tc.cuh"
+
+namespace kla {
+namespace {
+
+using kv4::kBlock;
+using kv4::Layout;
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+constexpr int kTile = 32;       // keys
+// p = 2^(s - m + kTop) with a base m that follows the maximum only when that is
+// kLag above it: p stays below 2^15 (fp16), and what is 2^-29 of the maximum is
+// still a normal number there.
+constexpr float kTop = 7.f, kLag = 8.f;
+
+// NT: tiles of 8 query rows.  One tile leaves room for 16 warps an SM.
+template <int D, int NT, bool F32>
+struct Config {
+    static constexpr int kWarps = NT == 1 && !F32 ? 16 : 8;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kStage = kTile / kBlock * Layout<D>::kBytes;
+    static constexpr int kStages = D == 64 ? 6 : (kWarps == 16 ? 3 : 6);
+    static constexpr int kRing = kStages * kStage;                       // of a warp
+    static constexpr int kPart = kRows * (D + 2);                        // floats of a partial result
+    static_assert(kRing >= kPart * 4, "a warp's partial result lies in its ring");
+    static constexpr int kSmem = kWarps * kRing;
+};
+
+struct Args {
+    const void *q;
+    long long q_stride;
+    const unsigned char *pool;
+    const int *table, *lens;
+    void *o;
+    float *lse;
+    int B, Tq, Hq, Hk, G, blocks, n_pages, columns;     // blocks: of 16 tokens in a page
+    int rows, groups, items;     // query rows of a key head, their groups, items of a sequence
+    float scale_log2, v_unit;
+    unsigned *status;
+    unsigned *cta_status;        // [CTAs]
+    unsigned *before;            // [B + 1] tiles of a head's sequences before b
+    float *part;                 // [CTAs][2][warps][kPart]
+    int ctas;
+    bool lost_wait;              // test hook
+};
+
+// ------------------------------------------------------------------ the split
+// Tile u of all: items in order, their tiles in order.
+struct Split {
+    unsigned long long total;
+    int ctas;
+    __device__ unsigned long long cta(int c) const { return total * (unsigned)c / (unsigned)ctas; }
+    template <int WARPS>
+    __device__ unsigned long long warp(int c, int w) const {
+        const unsigned long long a = cta(c), n = cta(c + 1) - a;
+        return a + n * (unsigned)w / WARPS;
+    }
+};
+template <int WARPS>
+__device__ __forceinline__ Split split_of(const Args &a, unsigned tiles) {
+    Split s;
+    s.total = (unsigned long long)tiles * (unsigned)a.items;
+    const unsigned long long most = (s.total + WARPS - 1) / WARPS;      // a tile for each warp at least
+    s.ctas = most < (unsigned)a.ctas ? (most > 0 ? (int)most : 1) : a.ctas;
+    return s;
+}
+
+__device__ __forceinline__ int length(const Args &a, int b) {
+    const int n = a.lens[b], most = a.columns * a.blocks * kBlock;
+    return n < 0 ? 0 : (n < most ? n : most);
+}
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+// ------------------------------------------------------------------ products
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+                 "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ float exp2_of(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return reinterpret_cast<const uint32_t &>(h);
+}
+__device__ __forceinline__ float2 unpack_half(uint32_t h) {
+    return __half22float2(reinterpret_cast<const __half2 &>(h));
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(const unsigned char *p, uint32_t (&w)[N]) {
+    if (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x; w[1] = v.y; w[N - 2] = v.z; w[N - 1] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x; w[1] = v.y;
+    }
+}
+
+__device__ __forceinline__ void st(float *p, float x) { *p = x; }
+__device__ __forceinline__ void st(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void load4(const float *p, float (&x)[4]) {
+    const float4 v = *reinterpret_cast<const float4 *>(p);
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4]) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
+    x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+
+// Output row of row n of a group: its offset in [B, Tq, Hq], or -1 behind the last.
+__device__ __forceinline__ long long out_row(const Args &a, int seq, int head, int n) {
+    if (n >= a.rows) return -1;
+    const int token = n / a.G, g = n - token * a.G;
+    return ((long long)seq * a.Tq + token) * a.Hq + head * a.G + g;
+}
+
+// What a warp holds of an item.  Thread (r, c) = (lane / 4, lane % 4) has query
+// rows 8 nt + 2c, + 1 and of their outputs the features r D / 8 + 2 mt, + 1.
+template <int D, int NT, bool F32>
+struct State {
+    static constexpr int kSteps = D / 16;
+    uint32_t q[F32 ? 2 : 1][NT][kSteps][2];
+    float o[NT][kSteps][4];
+    float m[NT][2], l[NT][2], mul[NT][2];
+    int limit[NT][2];            // keys below it are seen
+    int full;                    // keys below it are seen by all rows
+
+    template <typename T>
+    __device__ __forceinline__ void begin(const Args &a, int seq, int head, int group, int len) {
+        const int lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
+        const int first = len - a.Tq + 1;
+        full = first + group * 8 * NT / a.G;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int n = group * 8 * NT + nt * 8 + r;
+            const long long row = n / a.G;
+            const T *src = static_cast<const T *>(a.q) + ((long long)seq * a.Tq + row) * a.q_stride +
+                           (long long)(head * a.G + n % a.G) * D + c * (D / 4);
+            float x[D / 4], top = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                float y[4] = {};
+                if (n < a.rows) load4(src + 4 * j, y);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    x[4 * j + z] = y[z];
+                    top = fmaxf(top, fabsf(y[z]));
+                }
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // the row times a power of two that takes its largest to 2^14 and above
+            int e = 268 - (int)(__float_as_uint(top) >> 23);
+            e = e < 253 ? e : 253;
+            const float up = __uint_as_float((unsigned)e << 23);
+            const float down = __uint_as_float((unsigned)(254 - e) << 23) * a.scale_log2;
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const float u = x[4 * j + 2 * z] * up, v = x[4 * j + 2 * z + 1] * up;
+                    q[0][nt][j][z] = pack_half(u, v);
+                    if (F32) {
+                        const float2 h = unpack_half(q[0][nt][j][z]);
+                        q[F32 ? 1 : 0][nt][j][z] = pack_half(u - h.x, v - h.y);
+                    }
+                }
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                mul[nt][z] = __shfl_sync(0xffffffffu, down, (2 * c + z) * 4);
+                limit[nt][z] = first + (group * 8 * NT + nt * 8 + 2 * c + z) / a.G;
+                m[nt][z] = -INFINITY;
+                l[nt][z] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) o[nt][j][z] = 0.f;
+        }
+    }
+
+    // Scores of a block: s[nt][0..1] key r, s[nt][2..3] key r + 8.
+    __device__ __forceinline__ void scores(const unsigned char *block, float (&s)[NT][4]) {
+        const int lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
+        uint32_t wa[D / 32], wb[D / 32];
+        load_words(block + r * (D / 2) + c * (D / 8), wa);
+        load_words(block + (r + 8) * (D / 2) + c * (D / 8), wb);
+        const unsigned char *ks = block + Layout<D>::kKs;
+        uint32_t sa, sb;
+        if (D == 128) {
+            sa = kv4::scales_to_half2(*reinterpret_cast<const unsigned short *>(ks + r * 8 + 2 * c));
+            sb = kv4::scales_to_half2(*reinterpret_cast<const unsigned short *>(ks + (r + 8) * 8 + 2 * c));
+        } else {
+            sa = kv4::scales_to_half2(ks[r * 4 + c] * 0x101u);
+            sb = kv4::scales_to_half2(ks[(r + 8) * 4 + c] * 0x101u);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) s[nt][z] = 0.f;
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+            const uint32_t fa = __byte_perm(sa, 0, x < 2 ? 0x1010 : 0x3232);
+            const uint32_t fb = __byte_perm(sb, 0, x < 2 ? 0x1010 : 0x3232);
+            uint32_t ha[4], hb[4];
+            kv4::codes_to_half2(wa[x], ha);
+            kv4::codes_to_half2(wb[x], hb);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const uint32_t k[4] = {kv4::mul_half2(ha[2 * y], fa), kv4::mul_half2(hb[2 * y], fb),
+                                       kv4::mul_half2(ha[2 * y + 1], fa), kv4::mul_half2(hb[2 * y + 1], fb)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma(s[nt], k, q[0][nt][2 * x + y]);
+                    if (F32) mma(s[nt], k, q[F32 ? 1 : 0][nt][2 * x + y]);
+                }
+            }
+        }
+    }
+
+    // o += p v over a block; p as operands, values of keys from `left` on are zeros.
+    __device__ __forceinline__ void mix(const unsigned char *block, const uint32_t (&p)[F32 ? 2 : 1][NT][2],
+                                        int left) {
+        const int lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
+        uint32_t w0[D / 32], w1[D / 32];
+        load_words(block + Layout<D>::kV + c * D + r * (D / 8), w0);
+        load_words(block + Layout<D>::kV + (c + 4) * D + r * (D / 8), w1);
+        const unsigned char *vs = block + Layout<D>::kVs + r * (D / 8) / 16 * kBlock + 2 * c;
+        uint32_t f0 = kv4::scales_to_half2(*reinterpret_cast<const unsigned short *>(vs));
+        uint32_t f1 = kv4::scales_to_half2(*reinterpret_cast<const unsigned short *>(vs + 8));
+        if (left < kBlock) {         // what lies behind the last key may be anything
+            f0 = 2 * c + 1 < left ? f0 : (2 * c < left ? f0 & 0xffffu : 0u);
+            f1 = 2 * c + 9 < left ? f1 : (2 * c + 8 < left ? f1 & 0xffffu : 0u);
+        }
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+            uint32_t h0[4], h1[4];
+            kv4::codes_to_half2(w0[x], h0);
+            kv4::codes_to_half2(w1[x], h1);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const uint32_t v[4] = {kv4::mul_half2(h0[2 * y], f0), kv4::mul_half2(h0[2 * y + 1], f0),
+                                       kv4::mul_half2(h1[2 * y], f1), kv4::mul_half2(h1[2 * y + 1], f1)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma(o[nt][2 * x + y], v, p[0][nt]);
+                    if (F32) mma(o[nt][2 * x + y], v, p[F32 ? 1 : 0][nt]);
+                }
+            }
+        }
+    }
+
+    // A tile of keys key0 .. key0 + 31, those below len.
+    __device__ __forceinline__ void tile(const unsigned char *stage, int key0, int len) {
+        const int r = threadIdx.x % 32 / 4;
+        float s[2][NT][4];
+        const bool both = key0 + kBlock < len;
+        scores(stage, s[0]);
+        if (both) {
+            scores(stage + Layout<D>::kBytes, s[1]);
+        } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) s[1][nt][z] = 0.f;
+        }
+        const bool edge = key0 + kTile > full;
+        float top[NT][2];
+        bool above = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                float t = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float &x = s[i][nt][2 * j + z];
+                        x *= mul[nt][z];
+                        if (edge && key0 + i * kBlock + 8 * j + r >= limit[nt][z]) x = -INFINITY;
+                        t = fmaxf(t, x);
+                    }
+                top[nt][z] = t;
+                above = above || t > m[nt][z] + kLag;
+            }
+        if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    float t = top[nt][z];
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                    t = fmaxf(t, m[nt][z]);
+                    const float f = m[nt][z] == t ? 1.f : exp2_of(m[nt][z] - t);
+                    m[nt][z] = t;
+                    l[nt][z] *= f;
+#pragma unroll
+                    for (int j = 0; j < kSteps; ++j) {
+                        o[nt][j][z] *= f;
+                        o[nt][j][2 + z] *= f;
+                    }
+                }
+        }
+        uint32_t p[2][F32 ? 2 : 1][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float base[2];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) base[z] = m[nt][z] == -INFINITY ? 0.f : m[nt][z] - kTop;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float u = exp2_of(s[i][nt][2 * j] - base[0]), v = exp2_of(s[i][nt][2 * j + 1] - base[1]);
+                    l[nt][0] += u;
+                    l[nt][1] += v;
+                    const uint32_t h = pack_half(u, v);
+                    p[i][0][nt][j] = transposed(h);
+                    if (F32) {
+                        const float2 g = unpack_half(h);
+                        p[i][F32 ? 1 : 0][nt][j] = transposed(pack_half(u - g.x, v - g.y));
+                    }
+                }
+        }
+        mix(stage, p[0], len - key0);
+        if (both) mix(stage + Layout<D>::kBytes, p[1], len - key0 - kBlock);
+    }
+
+    __device__ __forceinline__ void finish() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                float &x = l[nt][z];
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                x += __shfl_xor_sync(0xffffffffu, x, 8);
+                x += __shfl_xor_sync(0xffffffffu, x, 16);
+            }
+    }
+    // Outputs of an item that this warp had alone.
+    template <typename T>
+    __device__ __forceinline__ void write(const Args &a, int seq, int head, int group) const {
+        const int lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                const long long row = out_row(a, seq, head, group * 8 * NT + nt * 8 + 2 * c + z);
+                if (row < 0) continue;
+                const float sum = l[nt][z], f = sum == 0.f ? 0.f : a.v_unit / sum;
+                T *to = static_cast<T *>(a.o) + row * D + r * (D / 8);
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j) {
+                    st(to + 2 * j, o[nt][j][z] * f);
+                    st(to + 2 * j + 1, o[nt][j][2 + z] * f);
+                }
+                if (r == 0 && a.lse)
+                    a.lse[row] = sum == 0.f ? -INFINITY : (m[nt][z] - kTop + log2f(sum)) * kLn2;
+            }
+    }
+    // A partial result: outputs [rows][D], then bases, then sums.
+    __device__ __forceinline__ void put(float *part) const {
+        const int lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                const int n = nt * 8 + 2 * c + z;
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j)
+                    *reinterpret_cast<float2 *>(part + n * D + r * (D / 8) + 2 * j) =
+                        make_float2(o[nt][j][z], o[nt][j][2 + z]);
+                if (r == 0) {
+                    part[8 * NT * D + n] = m[nt][z] - kTop;
+                    part[8 * NT * D + 8 * NT + n] = l[nt][z];
+                }
+            }
+    }
+};
+
+// ------------------------------------------------------------------ the kernel
+// A place among all tiles.
+struct Place {
+    int seq, len, item, tile;
+};
+__device__ __forceinline__ void next_item(const Args &a, Place &p) {
+    p.tile = 0;
+    if (++p.item < a.items) return;
+    p.item = 0;
+    do {
+        ++p.seq;
+        p.len = p.seq < a.B ? length(a, p.seq) : 1;
+    } while (p.len == 0);
+}
+
+// A warp's last part of an item, for the join in shared memory.
+struct Last {
+    int seq, item;       // item < 0: none
+    bool first, end;     // has the item's first tile, its last
+};
+
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(Config<D, NT, F32>::kThreads, 1)
+kv4_attn_kernel(const __grid_constant__ Args a) {
+    using C = Config<D, NT, F32>;
+    using T = std::conditional_t<F32, float, __nv_bfloat16>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ uint64_t bars[C::kWarps][C::kStages];
+    __shared__ unsigned sums[C::kThreads], warp_sums[C::kWarps];
+    __shared__ Last lasts[C::kWarps];
+    __shared__ unsigned trouble;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, cta = blockIdx.x;
+    unsigned char *ring = smem + warp * C::kRing;
+    if (lane == 0) {
+        for (int i = 0; i < C::kStages; ++i) tc::mbar_init(&bars[warp][i], 1);
+        tc::fence_mbar_init();
+        lasts[warp].item = -1;
+    }
+    if (tid == 0) trouble = kDevOk;
+
+    // tiles before each thread's share of the sequences
+    const int share = (a.B + C::kThreads - 1) / C::kThreads, b0 = tid * share;
+    unsigned mine = 0;
+    for (int b = b0; b < b0 + share && b < a.B; ++b) mine += tiles_of(length(a, b));
+    unsigned sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += x;
+    }
+    if (lane == 31) warp_sums[warp] = sum;
+    __syncthreads();
+    unsigned tiles = 0;
+    for (int w = 0; w < C::kWarps; ++w) {
+        if (w == warp) sum += tiles;
+        tiles += warp_sums[w];
+    }
+    sums[tid] = sum - mine;
+    if (cta == 0) {              // for the join
+        unsigned x = sum - mine;
+        for (int b = b0; b < b0 + share && b < a.B; ++b) {
+            a.before[b] = x;
+            x += tiles_of(length(a, b));
+        }
+        if (tid == 0) a.before[a.B] = tiles;
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const Split split = split_of<C::kWarps>(a, tiles);
+    unsigned long long u = 0, end = 0;
+    if (cta < split.ctas) {
+        u = split.warp<C::kWarps>(cta, warp);
+        end = split.warp<C::kWarps>(cta, warp + 1);
+    }
+    bool ok = true, bad = false;
+    if (u < end) {
+        // where the warp's tiles begin
+        Place at;
+        {
+            const unsigned x = (unsigned)(u / (unsigned)a.items);
+            int lo = 0, hi = C::kThreads - 1;
+            while (lo < hi) {                        // the last share that begins at x or before
+                const int mid = (lo + hi + 1) / 2;
+                if (sums[mid] <= x) lo = mid; else hi = mid - 1;
+            }
+            unsigned y = sums[lo];
+            at.seq = lo * share;
+            at.len = length(a, at.seq);
+            while (y + tiles_of(at.len) <= x) {
+                y += tiles_of(at.len);
+                at.len = length(a, ++at.seq);
+            }
+            const unsigned long long rest = u - (unsigned long long)y * (unsigned)a.items;
+            at.item = (int)(rest / (unsigned)tiles_of(at.len));
+            at.tile = (int)(rest % (unsigned)tiles_of(at.len));
+        }
+        const int n = (int)(end - u);
+        // copies: the lanes look up the blocks of 16 tiles at a time
+        Place ahead = at;
+        int issued = 0, looked = -1;
+        unsigned block = 0;
+        auto issue = [&](int slot) {
+            if (looked < 0 || ahead.tile >= looked + 16) {
+                looked = ahead.tile;
+                const int nb = 2 * looked + lane;
+                block = 0;
+                if (nb * kBlock < ahead.len) {
+                    const int column = nb / a.blocks;
+                    int page = a.table[(long long)ahead.seq * a.columns + column];
+                    if (page < 0 || page >= a.n_pages) {
+                        bad = true;
+                        page = 0;
+                    }
+                    block = ((unsigned)page * a.Hk + ahead.item / a.groups) * a.blocks + (nb - column * a.blocks);
+                }
+            }
+            const int i = 2 * (ahead.tile - looked);
+            const unsigned from = __shfl_sync(0xffffffffu, block, i + (lane & 1));
+            const bool two = ahead.tile * kTile + kBlock < ahead.len;
+            if (lane == 0) tc::mbar_expect_tx(&bars[warp][slot], (two ? 2 : 1) * Layout<D>::kBytes);
+            __syncwarp();
+            if (lane < (two ? 2 : 1))
+                tc::bulk_load(ring + slot * C::kStage + lane * Layout<D>::kBytes,
+                              a.pool + (unsigned long long)from * Layout<D>::kBytes, Layout<D>::kBytes,
+                              &bars[warp][slot]);
+            ++issued;
+            if (++ahead.tile == tiles_of(ahead.len)) {
+                looked = -1;
+                if (issued < n) next_item(a, ahead);
+            }
+        };
+        for (int i = 0; i < C::kStages && issued < n; ++i) issue(i);
+
+        State<D, NT, F32> st;
+        int slot = 0, parity = 0;
+        for (int done = 0; done < n;) {
+            const int head = at.item / a.groups, group = at.item - head * a.groups;
+            const int stop = min(tiles_of(at.len), at.tile + n - done), begin = at.tile;
+            st.template begin<T>(a, at.seq, head, group, at.len);
+            for (; at.tile < stop; ++at.tile, ++done) {
+                ok = tc::mbar_wait(&bars[warp][slot], parity) && !a.lost_wait;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                st.tile(ring + slot * C::kStage, at.tile * kTile, at.len);
+                __syncwarp();
+                if (issued < n) issue(slot);
+                if (++slot == C::kStages) {
+                    slot = 0;
+                    parity ^= 1;
+                }
+            }
+            if (!ok) break;
+            const bool first = begin == 0, whole = stop == tiles_of(at.len);
+            st.finish();
+            if (first && whole) {
+                st.template write<T>(a, at.seq, head, group);
+            } else if (done < n) {                   // closes an item that others began
+                st.put(a.part + ((size_t)(2 * cta + 1) * C::kWarps + warp) * C::kPart);
+            } else {
+                st.put(reinterpret_cast<float *>(ring));
+                if (lane == 0) lasts[warp] = {at.seq, at.item, first, whole};
+            }
+            if (done < n) next_item(a, at);
+        }
+        if (!ok) {
+            // what was asked for arrives by itself; the ring must outlive it
+            for (int i = 0; i < C::kStages; ++i) {
+                const int left = issued < C::kStages ? issued : C::kStages;
+                if (i < left) {
+                    // the last issue of slot i: the phase that completes last
+                    const int turns = (issued - 1 - i) / C::kStages;
+                    tc::mbar_wait(&bars[warp][i], turns & 1);
+                }
+            }
+            if (lane == 0) atomicMax(&trouble, (unsigned)kDevTimeout);
+        }
+        if (bad) atomicMax(&trouble, (unsigned)kDevBadTable);
+    }
+    __syncthreads();
+
+    // items that several of the CTA's warps had at their ends, in order
+    for (int w = 0; w < C::kWarps;) {
+        const Last x = lasts[w];
+        int to = w + 1, last = w;
+        if (x.item < 0) {
+            ++w;
+            continue;
+        }
+        for (; to < C::kWarps; ++to) {
+            if (lasts[to].item < 0) continue;        // no tiles (or an item of its own, whole)
+            if (lasts[to].item != x.item || lasts[to].seq != x.seq) break;
+            last = to;
+        }
+        const bool whole = x.first && lasts[last].end;
+        const int head = x.item / a.groups, group = x.item - head * a.groups;
+        float *out = a.part + ((size_t)(2 * cta) * C::kWarps + w) * C::kPart;
+        for (int i = tid; i < C::kRows * D; i += C::kThreads) {
+            const int n = i / D, f = i - n * D;
+            if (group * C::kRows + n >= a.rows) break;
+            float base = -INFINITY, l = 0.f, v = 0.f;
+            for (int y = w; y <= last; ++y)
+                if (lasts[y].item >= 0)
+                    base = fmaxf(base, reinterpret_cast<const float *>(smem + y * C::kRing)[C::kRows * D + n]);
+            for (int y = w; y <= last; ++y) {
+                if (lasts[y].item < 0) continue;
+                const float *part = reinterpret_cast<const float *>(smem + y * C::kRing);
+                const float b = part[C::kRows * D + n], s = b == base ? 1.f : exp2_of(b - base);
+                l = fmaf(s, part[C::kRows * D + C::kRows + n], l);
+                v = fmaf(s, part[i], v);
+            }
+            if (whole) {
+                const long long row = out_row(a, x.seq, head, group * C::kRows + n);
+                st(static_cast<T *>(a.o) + row * D + f, v * (l == 0.f ? 0.f : a.v_unit / l));
+                if (f == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (base + log2f(l)) * kLn2;
+            } else {
+                out[i] = v;
+                if (f == 0) {
+                    out[C::kRows * D + n] = base;
+                    out[C::kRows * D + C::kRows + n] = l;
+                }
+            }
+        }
+        w = to;
+    }
+    if (tid == 0) a.cta_status[cta] = trouble;
+}
+
+// Joins the parts of items that several CTAs had, and writes the rows of empty
+// caches; PER warps to a row.  The first block writes the status word.
+template <int D, int NT, bool F32, int PER>
+__global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ Args a) {
+    using C = Config<D, NT, F32>;
+    using T = std::conditional_t<F32, float, __nv_bfloat16>;
+    constexpr int V = D / 32;
+    __shared__ float shared_v[PER == 1 ? 1 : 8][D], shared_l[8];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = warp % PER;
+    if (blockIdx.x == 0 && warp == 0) {
+        unsigned x = kDevOk;
+        for (int c = lane; c < a.ctas; c += 32) x = max(x, a.cta_status[c]);
+        x = __reduce_max_sync(0xffffffffu, x);
+        if (lane == 0) *a.status = x;
+    }
+    const long long rows = (long long)a.B * a.Hk * a.rows;
+    const long long i = (long long)blockIdx.x * (8 / PER) + warp / PER;
+    bool there = i < rows;
+    const int seq = there ? (int)(i / ((long long)a.Hk * a.rows)) : 0;
+    const int rest = there ? (int)(i - (long long)seq * a.Hk * a.rows) : 0;
+    const int head = rest / a.rows, r = rest - head * a.rows, group = r / C::kRows, n = r - group * C::kRows;
+    const unsigned before = a.before[seq], nt = a.before[seq + 1] - before;
+    const Split split = split_of<C::kWarps>(a, a.before[a.B]);
+    const unsigned long long x = (unsigned long long)before * (unsigned)a.items +
+                                 (unsigned long long)(head * a.groups + group) * nt, y = x + nt;
+    int c0 = 0, c1 = -1;
+    if (there && nt > 0) {
+        c0 = (int)(x * (unsigned)split.ctas / split.total);
+        while (c0 + 1 < split.ctas && split.cta(c0 + 1) <= x) ++c0;
+        while (split.cta(c0) > x) --c0;
+        c1 = c0;
+        while (c1 + 1 < split.ctas && split.cta(c1 + 1) < y) ++c1;
+    }
+    // each lane looks for the parts of a CTA: what its warps joined, and what a warp closed
+    float base = -INFINITY, l = 0.f, v[V] = {};
+    int parts = 0;
+    for (int c = c0; c <= c1; c += 32) {
+        int slot[2] = {-1, -1};
+        if (c + lane <= c1) {
+            for (int w = 0; w < C::kWarps; ++w) {
+                const unsigned long long s = split.warp<C::kWarps>(c + lane, w),
+                                         e = split.warp<C::kWarps>(c + lane, w + 1);
+                if (s >= e || s >= y || e <= x) continue;
+                if (e <= y) {
+                    if (slot[0] < 0) slot[0] = (2 * (c + lane)) * C::kWarps + w;
+                } else {
+                    slot[1] = (2 * (c + lane) + 1) * C::kWarps + w;
+                }
+            }
+        }
+        const unsigned has[2] = {__ballot_sync(0xffffffffu, slot[0] >= 0), __ballot_sync(0xffffffffu, slot[1] >= 0)};
+        parts += __popc(has[0]) + __popc(has[1]);
+        if (c0 == c1 && parts == 1) break;           // one writer: it wrote the result
+        float m[2], sum[2], top = base;
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const float *part = a.part + (size_t)max(slot[z], 0) * C::kPart + C::kRows * D;
+            m[z] = slot[z] >= 0 ? part[n] : -INFINITY;
+            sum[z] = slot[z] >= 0 ? part[C::kRows + n] : 0.f;
+            top = fmaxf(top, m[z]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float f = base == top ? 1.f : exp2_of(base - top);
+        l *= f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] *= f;
+        base = top;
+        float wt[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) wt[z] = slot[z] < 0 ? 0.f : (m[z] == top ? 1.f : exp2_of(m[z] - top));
+        for (int k = sub; k < 32; k += PER) {
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                if (!(has[z] >> k & 1)) continue;
+                const float g = __shfl_sync(0xffffffffu, wt[z], k), gs = __shfl_sync(0xffffffffu, sum[z], k);
+                const float *part = a.part + (size_t)__shfl_sync(0xffffffffu, slot[z], k) * C::kPart + n * D;
+                l = fmaf(g, gs, l);
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[j] = fmaf(g, part[lane + 32 * j], v[j]);
+            }
+        }
+    }
+    there = there && parts != 1;
+    if (PER > 1) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) shared_v[PER == 1 ? 0 : warp][lane + 32 * j] = v[j];
+        if (lane == 0) shared_l[warp] = l;
+        __syncthreads();
+        if (sub != 0) return;
+        for (int z = 1; z < PER; ++z) {              // the warps of a row share its base
+            l += shared_l[warp + z];
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] += shared_v[PER == 1 ? 0 : warp + z][lane + 32 * j];
+        }
+    }
+    if (!there) return;
+    const long long row = out_row(a, seq, head, r);
+    const float f = l == 0.f ? 0.f : a.v_unit / l;
+#pragma unroll
+    for (int j = 0; j < V; ++j) st(static_cast<T *>(a.o) + row * D + lane + 32 * j, v[j] * f);
+    if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (base + log2f(l)) * kLn2;
+}
+
+// Without any key: zeros, from a launch that has no table to read.
+__global__ void kv4_no_keys_kernel(uint4 *o, long long n, float *lse, long long rows, unsigned *status) {
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i == 0) *status = kDevOk;
+    if (i < n) o[i] = make_uint4(0, 0, 0, 0);
+    if (lse && i < rows) lse[i] = -INFINITY;
+}
+
+// ------------------------------------------------------------------ host
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev < 64 && (n = known[dev].load()) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+        cudaGetLastError();     // no device: sizes are still wanted
+        return 152;
+    }
+    if (dev < 64) known[dev].store(n);
+    return n;
+}
+
+struct Plan {
+    int nt, ctas;
+    size_t cta_status, before, part, bytes;
+};
+template <int D, int NT, bool F32>
+void sizes(Plan &p) {
+    using C = Config<D, NT, F32>;
+    p.nt = NT;
+    p.bytes = up256(p.part + (size_t)p.ctas * 2 * C::kWarps * C::kPart * sizeof(float));
+}
+Plan plan_of(const Kv4Attn &p) {
+    Plan x{};
+    x.ctas = sm_count();
+    x.cta_status = kWsHeader;
+    x.before = up256(x.cta_status + x.ctas * sizeof(unsigned));
+    x.part = up256(x.before + ((size_t)p.B + 1) * sizeof(unsigned));
+    const bool two = (long long)p.Hq / p.Hk * p.Tq > 8;
+    if (p.d == 64) {
+        if (p.dtype == 1) two ? sizes<64, 2, false>(x) : sizes<64, 1, false>(x);
+        else two ? sizes<64, 2, true>(x) : sizes<64, 1, true>(x);
+    } else {
+        if (p.dtype == 1) two ? sizes<128, 2, false>(x) : sizes<128, 1, false>(x);
+        else two ? sizes<128, 2, true>(x) : sizes<128, 1, true>(x);
+    }
+    return x;
+}
+
+template <int D, int NT, bool F32>
+cudaError_t launch(const Args &a, cudaStream_t s) {
+    using C = Config<D, NT, F32>;
+    cudaError_t e = allow_dynamic_smem((const void *)kv4_attn_kernel<D, NT, F32>, C::kSmem);
+    if (e != cudaSuccess) return e;
+    kv4_attn_kernel<D, NT, F32><<<a.ctas, C::kThreads, C::kSmem, s>>>(a);
+    note_launch();
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // a warp for each row where there are enough of them, else 8
+    const long long rows = (long long)a.B * a.Hk * a.rows;
+    const bool many = rows >= 1024;
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(many ? (rows + 7) / 8 : rows));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    e = many ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, F32, 1>, a)
+             : cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, F32, 8>, a);
+    note_launch();
+    return e;
+}
+
+}  // namespace
+
+size_t kv4_attn_workspace_bytes(const Kv4Attn &p) { return plan_of(p).bytes; }
+
+bool kv4_attn_too_large(const Kv4Attn &p) {
+    const long long tiles = (long long)p.B * ((long long)p.columns * p.page / kTile + 1);
+    const long long rows = (long long)p.B * p.Tq * p.Hq;
+    const long long blocks = (long long)p.n_pages * p.Hk * (p.page / kBlock);
+    return tiles > INT32_MAX || rows > INT32_MAX || blocks > UINT32_MAX ||
+           (long long)p.columns * p.page > INT32_MAX;
+}
+
+cudaError_t launch_kv4_attn(const Kv4Attn &p, cudaStream_t s) {
+    const Plan x = plan_of(p);
+    unsigned char *ws = static_cast<unsigned char *>(p.ws);
+    Args a{};
+    a.q = p.q; a.q_stride = p.q_stride; a.pool = static_cast<const unsigned char *>(p.pool);
+    a.table = p.table; a.lens = p.lens; a.o = p.o; a.lse = p.lse;
+    a.B = p.B; a.Tq = p.Tq; a.Hq = p.Hq; a.Hk = p.Hk; a.G = p.Hq / p.Hk;
+    a.blocks = p.page / kBlock; a.n_pages = p.n_pages; a.columns = p.columns;
+    a.rows = a.G * p.Tq;
+    a.groups = (a.rows + 8 * x.nt - 1) / (8 * x.nt);
+    a.items = p.Hk * a.groups;
+    a.scale_log2 = p.scale * p.k_unit * kLog2e;
+    a.v_unit = p.v_unit;
+    a.status = static_cast<unsigned *>(p.ws);
+    a.cta_status = reinterpret_cast<unsigned *>(ws + x.cta_status);
+    a.before = reinterpret_cast<unsigned *>(ws + x.before);
+    a.part = reinterpret_cast<float *>(ws + x.part);
+    a.ctas = x.ctas;
+    // test hook: every warp takes its first wait for one that ran out
+    a.lost_wait = std::getenv("KLA_TEST_LOST_WAIT") != nullptr;
+    if (p.n_pages == 0 || p.columns == 0) {
+        const long long rows = (long long)p.B * p.Tq * p.Hq, n = rows * p.d * (p.dtype == 1 ? 2 : 4) / 16;
+        kv4_no_keys_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(static_cast<uint4 *>(p.o), n, p.lse, rows, a.status);
+        note_launch();
+        return cudaGetLastError();
+    }
+    const bool f32 = p.dtype == 0;
+#define KLA_KV4(D, NT) (f32 ? launch<D, NT, true>(a, s) : launch<D, NT, false>(a, s))
+    if (p.d == 64) return x.nt == 2 ? KLA_KV4(64, 2) : KLA_KV4(64, 1);
+    return x.nt == 2 ? KLA_KV4(128, 2) : KLA_KV4(128, 1);
+#undef KLA_KV4
+}
+
+}  // namespace kla

@@ -70,7 +70,8 @@ typedef enum {
     KLA_ERR_UNSUPPORTED = 2,   /* valid request outside the supported set */
     KLA_ERR_CUDA = 3,          /* a CUDA runtime call failed (launch, attribute, ...) */
     KLA_ERR_TIMEOUT = 4,       /* a bounded device-side wait gave up */
-    KLA_ERR_WORKSPACE = 5      /* workspace missing or smaller than required */
+    KLA_ERR_WORKSPACE = 5,     /* workspace missing or smaller than required */
+    KLA_ERR_PAGES = 6          /* a cache's pool has not enough free pages */
 } kla_status;
 
 typedef enum {
@@ -512,6 +513,122 @@ KLA_API int kla_attn_bwd_varlen(const void *q, long long q_stride, const void *k
                                 const int *cu_seqlens_k, float scale, void *dq, void *dk,
                                 void *dv, int N, int total_q, int total_k, int Hq, int Hk, int d,
                                 int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * A key/value cache in pages of 4-bit rows: the cache of kla_attn in 0.28 of its
+ * bytes, for as many sequences as its pages hold.
+ *
+ * Values.  A value is code * scale * unit: a code of 4 bits (e2m1: a sign and
+ * one of 0, 0.5, 1, 1.5, 2, 3, 4, 6), a scale (e4m3) for 16 neighbouring features
+ * of a token's head, and a unit for all keys and one for all values: powers of two
+ * from 2^-32 to 2^32, part of the cache as its sizes are.  Of x:
+ *
+ *     scale = e4m3(min(max |x / unit| / 6, 448)),  code = e2m1(x / unit / scale)
+ *
+ * both to nearest, ties to even, codes saturated; a scale of 0 has codes of 0,
+ * and 16 features of which one is not finite read as NaN.
+ * Pages.  A page holds `page` tokens (a multiple of 16) of Hk heads:
+ * [Hk][page / 16][18 d] bytes, kla_kv4_page_bytes(...) in all.  The 18 d bytes
+ * are 16 tokens of a head: keys' codes [16][d / 2] (byte i: feature 2i in the low
+ * four bits, 2i + 1 in the high), values' codes [8][d] (of a pair of tokens, byte
+ * i: feature i, the even token in the low four bits), keys' scales [16][d / 16],
+ * values' scales [d / 16][16].  A pool is n_pages of them, 16-byte aligned; a model
+ * of several layers has a pool for each, one behind the other, and one book for all.
+ * The book.  table [B, columns] int32: sequence b's position t lies in page
+ * table[b][t / page]; lens [B] int32: its positions, clamped to 0..columns * page.
+ * Entries behind ceil(lens[b] / page) are not read.  All on the device.  An entry
+ * outside 0..n_pages-1 is not followed and reported as KLA_ERR_INVALID_ARG; what
+ * the call writes for its sequence is unspecified (append: nothing to that page).
+ *
+ * kla_kv4_append writes rows of k and v to the places of each sequence's last
+ * positions: lens counts them already.  cu_seqlens NULL: k, v [B, T, Hk, d],
+ * row i of sequence b goes to position lens[b] - T + i, and rows before position 0
+ * are left out.  cu_seqlens (device int32 [B + 1]): packed rows [T, Hk, d], T the
+ * total, sequence b's rows cu_seqlens[b] .. cu_seqlens[b+1]-1 likewise.  The table
+ * must start with 0, not decrease and end with T; one that does not is reported,
+ * and which rows are then written is unspecified.  Rows lie k_stride, v_stride
+ * elements apart as in kla_attn_fwd.  The places must not be shared by sequences
+ * (kla_pages_grow sees to it); other positions keep their values.
+ * kla_kv4_read is its inverse, rows before position 0 are zeros.  Read rows are
+ * exact in both types.
+ * d in {64, 128}, Hk at most 1024.  The workspace may be NULL; 256 bytes or more
+ * (256-byte aligned) take the status word.
+ */
+KLA_API size_t kla_kv4_page_bytes(int page, int Hk, int d);
+KLA_API int kla_kv4_append(const void *k, long long k_stride, const void *v, long long v_stride,
+                           void *pool, const int *table, const int *lens, const int *cu_seqlens,
+                           float k_unit, float v_unit, int B, int T, int Hk, int d, int page,
+                           int n_pages, int columns, int dtype, void *workspace,
+                           size_t workspace_bytes, void *stream);
+KLA_API int kla_kv4_read(void *k, long long k_stride, void *v, long long v_stride,
+                         const void *pool, const int *table, const int *lens,
+                         const int *cu_seqlens, float k_unit, float v_unit, int B, int T, int Hk,
+                         int d, int page, int n_pages, int columns, int dtype, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * Causal attention over such a cache: kla_attn_fwd with k_lens = lens, q [B, Tq,
+ * Hq, d] (rows q_stride elements apart), o and lse (or NULL) as there, keys and
+ * values as kla_kv4_read gives them.  A query that sees no key has o = 0 and
+ * lse = -infinity.  What lies behind a sequence's last position may be anything.
+ * scale * k_unit from 1e-37 to 2e38.  Scores, statistics and sums are fp32;
+ * exp(S - m) is rounded once as an operand of the second product (bf16: to fp16,
+ * fp32: to 22 bits), q of fp32 to 22 bits; keys and values are exact.
+ * workspace: kla_kv4_attn_workspace_size(...) bytes, 256-byte aligned, the status
+ * word first.  The size depends on the SM count of the current device.
+ */
+KLA_API size_t kla_kv4_attn_workspace_size(int B, int Tq, int Hq, int Hk, int d, int page,
+                                           int columns, int dtype);
+KLA_API int kla_kv4_attn(const void *q, long long q_stride, const void *pool, const int *table,
+                         const int *lens, float scale, float k_unit, float v_unit, void *o,
+                         float *lse, int B, int Tq, int Hq, int Hk, int d, int page, int n_pages,
+                         int columns, int dtype, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/*
+ * The pages' operators, for caches of any kind of row: S sequences in a book as
+ * above (`page` any positive number) and refs [n_pages], the number of sequences
+ * that hold each page.  A page with refs 0 is free.  Pages lie in `layers` pools
+ * of n_pages * page_bytes bytes one behind the other (page_bytes a multiple of 16).
+ * kla_pages_fork: for all f at once, sequence dst[f] becomes what src[f] was before
+ *   the call: its length and its pages, shared; the rest of its table row becomes -1.
+ *   src[f] = -1, or src NULL: it becomes empty.  refs follow, so pages that nobody
+ *   holds any more are free.  A dst that is there twice or a number out of range
+ *   refuses the call: nothing changes.
+ * kla_pages_grow: room for n_new[s] more positions of every sequence, and lens[s]
+ *   += n_new[s].  New pages are the lowest free ones, in the order of sequences and
+ *   positions.  A partly filled last page that other sequences hold too is replaced
+ *   by a copy of its own (of all layers, by every one of them that grows), the first
+ *   page that the sequence takes.  Pages that lose their last holder here are free
+ *   from the next call on.  Without enough free pages nothing changes
+ *   and KLA_ERR_PAGES is reported; a negative n_new or a row that is too short for
+ *   it refuses the call: nothing changes.
+ * kla_pages_compact: pages in use from number n_used on (n_used pages are in use)
+ *   move to the free ones below it, in order, with their contents; table and refs
+ *   follow.  page_map [n_pages]: where each page is now, -1 for a free one.  n_used:
+ *   one int.  Pages may be held by others than the book's sequences (by their refs):
+ *   page_map says where they went.
+ * kla_pages_copy: the contents of pages src[i] to dst[i], i < n.  A target that is
+ *   there twice, or is a source of another, or a number out of range refuses the
+ *   call.  KLA's states are such pages too: [B, H, dk, dv] is a layer of B pages.
+ * Lists and results are on the device; workspace: kla_pages_workspace_size(S,
+ * columns, n_pages, n) bytes (n: 0 where the call takes none; copy: S = columns =
+ * 0), 256-byte aligned, the status word first, the rest scratch.
+ */
+KLA_API size_t kla_pages_workspace_size(int S, int columns, int n_pages, int n);
+KLA_API int kla_pages_fork(int *table, int *lens, int *refs, const int *src, const int *dst,
+                           int S, int columns, int page, int n_pages, int n, void *workspace,
+                           size_t workspace_bytes, void *stream);
+KLA_API int kla_pages_grow(void *pool, int layers, long long page_bytes, int *table, int *lens,
+                           int *refs, const int *n_new, int S, int columns, int page, int n_pages,
+                           void *workspace, size_t workspace_bytes, void *stream);
+KLA_API int kla_pages_compact(void *pool, int layers, long long page_bytes, int *table,
+                              const int *lens, int *refs, int *page_map, int *n_used, int S,
+                              int columns, int page, int n_pages, void *workspace,
+                              size_t workspace_bytes, void *stream);
+KLA_API int kla_pages_copy(void *pool, int layers, long long page_bytes, const int *src,
+                           const int *dst, int n_pages, int n, void *workspace,
+                           size_t workspace_bytes, void *stream);
 
 /*
  * Synchronises `stream` and returns the status that the last prefill call

@@ -1,0 +1,228 @@
+"""The paged 4-bit cache: what the host refuses, before any device work, the
+workspaces, and the split of attention's tiles over CTAs and warps."""
+import random
+
+import pytest
+import torch
+
+import gated_delta_rule_kaczmarz_gb300 as kla
+from gated_delta_rule_kaczmarz_gb300 import binding
+
+no_gpu_only = pytest.mark.skipif(torch.cuda.is_available(),
+                                 reason="uses fake device pointers; host validation only")
+FAKE = 0x10000
+INVALID, UNSUPPORTED = binding.KLA_ERR_INVALID_ARG, binding.KLA_ERR_UNSUPPORTED
+WORKSPACE = binding.KLA_ERR_WORKSPACE
+KV = dict(pool=FAKE, table=FAKE, lens=FAKE, k_unit=1.0, v_unit=0.5, B=2, Hk=2, d=64, page=32,
+          n_pages=9, columns=4, dtype=1, ws=FAKE, wsb=1 << 40)
+
+
+def _rows(name, **over):
+    a = {**KV, "k": FAKE, "ks": 128, "v": FAKE, "vs": 128, "cu": None, "T": 3, **over}
+    return getattr(binding.load(), name)(
+        a["k"], a["ks"], a["v"], a["vs"], a["pool"], a["table"], a["lens"], a["cu"], a["k_unit"],
+        a["v_unit"], a["B"], a["T"], a["Hk"], a["d"], a["page"], a["n_pages"], a["columns"],
+        a["dtype"], a["ws"], a["wsb"], None)
+
+
+def _attn(**over):
+    a = {**KV, "q": FAKE, "qs": 256, "scale": 0.1, "o": FAKE, "lse": FAKE, "Tq": 1, "Hq": 4, **over}
+    return binding.load().kla_kv4_attn(
+        a["q"], a["qs"], a["pool"], a["table"], a["lens"], a["scale"], a["k_unit"], a["v_unit"],
+        a["o"], a["lse"], a["B"], a["Tq"], a["Hq"], a["Hk"], a["d"], a["page"], a["n_pages"],
+        a["columns"], a["dtype"], a["ws"], a["wsb"], None)
+
+
+SHARED = [
+    (dict(pool=None), INVALID), (dict(table=None), INVALID), (dict(lens=None), INVALID),
+    (dict(pool=FAKE + 8), INVALID), (dict(table=FAKE + 2), INVALID), (dict(lens=FAKE + 1), INVALID),
+    (dict(k_unit=0.3), INVALID), (dict(v_unit=0.0), INVALID), (dict(k_unit=-1.0), INVALID),
+    (dict(v_unit=float("nan")), INVALID), (dict(k_unit=2.0 ** 33), INVALID),
+    (dict(v_unit=2.0 ** -33), INVALID), (dict(B=-1), INVALID), (dict(Hk=0), INVALID),
+    (dict(page=0), INVALID), (dict(n_pages=-1), INVALID), (dict(columns=-1), INVALID),
+    (dict(dtype=2), INVALID), (dict(d=96), UNSUPPORTED), (dict(page=24), UNSUPPORTED),
+    (dict(columns=1 << 30), UNSUPPORTED), (dict(n_pages=2 ** 31 - 1), UNSUPPORTED),
+    (dict(ws=FAKE + 16), INVALID), (dict(wsb=64), WORKSPACE),
+]
+
+
+@no_gpu_only
+@pytest.mark.parametrize("name", ["kla_kv4_append", "kla_kv4_read"])
+@pytest.mark.parametrize("over,status", SHARED + [
+    (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(k=FAKE + 8), INVALID),
+    (dict(ks=120), INVALID), (dict(vs=132), INVALID), (dict(T=-1), INVALID),
+    (dict(cu=FAKE + 2), INVALID), (dict(cu=FAKE, B=0, lens=None), INVALID),
+    (dict(Hk=2048, ks=1 << 20, vs=1 << 20), UNSUPPORTED),
+    (dict(B=1 << 16, T=1 << 16), UNSUPPORTED)])
+def test_rows_refuse(name, over, status):
+    assert _rows(name, **over) == status
+    assert binding.load().kla_last_error_message().decode() != ""
+
+
+@no_gpu_only
+@pytest.mark.parametrize("over,status", SHARED + [
+    (dict(q=None), INVALID), (dict(o=None), INVALID), (dict(q=FAKE + 8), INVALID),
+    (dict(o=FAKE + 8), INVALID), (dict(lse=FAKE + 2), INVALID), (dict(qs=250), INVALID),
+    (dict(Hq=3), INVALID), (dict(Hq=0), INVALID), (dict(Tq=-1), INVALID),
+    (dict(Hq=2048), UNSUPPORTED), (dict(scale=0.0), INVALID), (dict(scale=float("inf")), INVALID),
+    (dict(scale=float("nan")), INVALID), (dict(scale=1e-36, k_unit=2.0 ** -20), INVALID),
+    (dict(ws=None), WORKSPACE), (dict(B=1 << 20, Tq=1 << 10, columns=1), UNSUPPORTED)])
+def test_attention_refuses(over, status):
+    assert _attn(**over) == status
+    assert binding.load().kla_last_error_message().decode() != ""
+
+
+def _pages(name, **over):
+    a = dict(pool=FAKE, layers=2, bytes=64, table=FAKE, lens=FAKE, refs=FAKE, src=FAKE, dst=FAKE,
+             more=FAKE, where=FAKE, used=FAKE, S=3, columns=4, page=16, n_pages=10, n=2, ws=FAKE,
+             wsb=1 << 40)
+    a.update(over)
+    pool, book = [a["pool"], a["layers"], a["bytes"]], [a["table"], a["lens"], a["refs"]]
+    sizes, end = [a["S"], a["columns"], a["page"], a["n_pages"]], [a["ws"], a["wsb"], None]
+    args = {"fork": [*book, a["src"], a["dst"], *sizes, a["n"]],
+            "grow": [*pool, *book, a["more"], *sizes],
+            "compact": [*pool, *book, a["where"], a["used"], *sizes],
+            "copy": [*pool, a["src"], a["dst"], a["n_pages"], a["n"]]}
+    return getattr(binding.load(), "kla_pages_" + name)(*args[name], *end)
+
+
+BOOK = [(dict(table=None), INVALID), (dict(lens=None), INVALID), (dict(refs=None), INVALID),
+        (dict(table=FAKE + 2), INVALID), (dict(S=-1), INVALID), (dict(page=0), INVALID),
+        (dict(columns=1 << 30), UNSUPPORTED)]
+POOL = [(dict(pool=None), INVALID), (dict(pool=FAKE + 4), INVALID), (dict(layers=-1), INVALID),
+        (dict(bytes=-16), INVALID), (dict(bytes=40), UNSUPPORTED), (dict(bytes=1 << 41), UNSUPPORTED)]
+ENDS = [(dict(ws=None), WORKSPACE), (dict(wsb=256), WORKSPACE), (dict(ws=FAKE + 16), INVALID),
+        (dict(n_pages=-1), INVALID)]
+
+
+@no_gpu_only
+@pytest.mark.parametrize("name,over,status", [
+    *[("fork", *x) for x in BOOK + ENDS], *[("grow", *x) for x in BOOK + POOL + ENDS],
+    *[("compact", *x) for x in BOOK + POOL + ENDS], *[("copy", *x) for x in POOL + ENDS],
+    ("fork", dict(dst=None), INVALID), ("fork", dict(n=-1), INVALID),
+    ("fork", dict(n=1 << 30), UNSUPPORTED), ("fork", dict(src=FAKE + 1), INVALID),
+    ("grow", dict(more=None), INVALID), ("compact", dict(where=None), INVALID),
+    ("compact", dict(used=None), INVALID), ("copy", dict(src=None), INVALID),
+    ("copy", dict(n=-1), INVALID)])
+def test_pages_refuse(name, over, status):
+    assert _pages(name, **over) == status
+    assert binding.load().kla_last_error_message().decode() != ""
+
+
+@no_gpu_only
+def test_injected_launch_fault(monkeypatch):
+    monkeypatch.setenv("KLA_FAULT_INJECT", "launch")
+    calls = [lambda: _rows("kla_kv4_append"), lambda: _rows("kla_kv4_read"), _attn]
+    calls += [lambda n=n: _pages(n) for n in ("fork", "grow", "compact", "copy")]
+    for call in calls:
+        assert call() == binding.KLA_ERR_CUDA
+        assert "injected" in binding.load().kla_last_error_message().decode()
+
+
+def test_sizes():
+    assert kla.kla_kv4_page_bytes(64, 4, 128) == 64 * 4 * 144
+    for page, hk, d in ((24, 1, 64), (0, 1, 64), (16, 0, 64), (16, 1, 80)):
+        assert kla.kla_kv4_page_bytes(page, hk, d) == 0
+        with pytest.raises(ValueError):
+            kla.kla_kv4_pool(3, page, hk, d, device="cpu")
+    assert kla.kla_kv4_pool(3, 32, 2, 64, device="cpu").shape == (3, 2, 2, 18 * 64)
+    assert kla.kla_kv4_pool(3, 32, 2, 64, layers=5, device="cpu").shape == (5, 3, 2, 2, 18 * 64)
+    assert kla.kla_kv4_attn_workspace_size(2, 1, 4, 2, 64, 32, 4) > 256
+    assert kla.kla_kv4_attn_workspace_size(2, 0, 4, 2, 64, 32, 4) == 0
+    assert kla.kla_kv4_attn_workspace_size(2, 1, 3, 2, 64, 32, 4) == 0
+    assert kla.kla_pages_workspace_size(3, 4, 100, 2) >= 256 + 4 * 100 * 4
+    assert binding.load().kla_status_str(binding.KLA_ERR_PAGES) == b"not enough free pages"
+
+
+def test_the_binding_refuses():
+    pool, table = kla.kla_kv4_pool(3, 16, 2, 64, device="cpu"), torch.zeros(2, 4).int()
+    lens, q = torch.zeros(2).int(), torch.zeros(2, 1, 4, 64)
+    with pytest.raises(ValueError):
+        kla.kla_kv4_attn(q, pool, table, lens)                       # not on a GPU
+    with pytest.raises(ValueError, match="4|dim|shape"):
+        kla.kla_kv4_attn(q[0], pool, table, lens)
+    with pytest.raises(ValueError, match="total"):
+        kla.kla_kv4_read(pool, table, lens)
+    with pytest.raises(ValueError, match="total"):
+        kla.kla_kv4_read(pool, table, lens, T=1, cu_seqlens=lens)
+    with pytest.raises(ValueError, match="shape"):
+        kla.kla_kv4_append(q[0], q[0], pool, table, lens)
+    with pytest.raises(TypeError):
+        kla.kla_kv4_append(q.half(), q.half(), pool, table, lens)
+
+
+def _split(tiles, items, ctas, warps):
+    """The kernel's split: tile ranges of every CTA's warps."""
+    total = sum(tiles) * items
+    ctas = max(1, min(ctas, -(-total // warps)))
+
+    def cta(c):
+        return total * c // ctas
+
+    return [[cta(c) + (cta(c + 1) - cta(c)) * w // warps for w in range(warps + 1)]
+            for c in range(ctas)]
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_parts_that_are_left_are_the_parts_that_are_joined(seed):
+    """What warps and CTAs write of an item is what the join looks for, and covers it once."""
+    r = random.Random(seed)
+    warps, ctas = r.choice([8, 16]), r.choice([3, 20, 152])
+    tiles = [r.choice([0, 1, 2, r.randint(0, 40), r.randint(0, 900)]) for _ in range(r.randint(1, 30))]
+    items = r.randint(1, 6)
+    ranges = _split(tiles, items, ctas, warps)
+    starts, at = [], 0
+    for n in tiles:
+        for _ in range(items):
+            if n:
+                starts.append((at, at + n))
+            at += n
+    written = {x: [] for x in starts}            # item: (slot, first tile, end)
+    for c, edges in enumerate(ranges):
+        last = [None] * warps
+        for w in range(warps):
+            s, e = edges[w], edges[w + 1]
+            for x, y in starts:
+                if s >= e or s >= y or e <= x:
+                    continue
+                a, b = max(s, x), min(e, y)
+                if (a, b) == (x, y):
+                    written[x, y].append(("whole", a, b))
+                elif e > y:
+                    written[x, y].append(((2 * c + 1) * warps + w, a, b))
+                else:
+                    last[w] = (x, y, a, b)
+        w = 0
+        while w < warps:
+            if last[w] is None:
+                w += 1
+                continue
+            x, y, a, b = last[w]
+            to = w + 1
+            while to < warps and (last[to] is None or last[to][:2] == (x, y)):
+                if last[to] is not None:
+                    b = last[to][3]
+                to += 1
+            written[x, y].append(("whole" if (a, b) == (x, y) else 2 * c * warps + w, a, b))
+            w = to
+    for (x, y), parts in written.items():
+        assert sorted((a, b) for _, a, b in parts)[0][0] == x
+        assert sum(b - a for _, a, b in parts) == y - x
+        found = []
+        c0 = max(c for c in range(len(ranges)) if ranges[c][0] <= x)
+        c1 = max(c for c in range(len(ranges)) if ranges[c][0] < y)
+        for c in range(c0, c1 + 1):
+            slot = [None, None]
+            for w in range(warps):
+                s, e = ranges[c][w], ranges[c][w + 1]
+                if s >= e or s >= y or e <= x:
+                    continue
+                if e <= y:
+                    slot[0] = 2 * c * warps + w if slot[0] is None else slot[0]
+                else:
+                    slot[1] = (2 * c + 1) * warps + w
+            found += [z for z in slot if z is not None]
+        if len(found) == 1:
+            assert [p[0] for p in parts] == ["whole"]
+        else:
+            assert sorted(found) == sorted(p[0] for p in parts)
