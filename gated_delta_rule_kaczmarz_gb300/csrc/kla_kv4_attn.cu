@@ -37,24 +37,36 @@ using kv4::kBlock;
 using kv4::Layout;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
-constexpr int kTile = 32;       // keys
 // p = 2^(s - m + kTop) with a base m that follows the maximum only when that is
 // kLag above it: p stays below 2^15 (fp16), and what is 2^-29 of the maximum is
 // still a normal number there.
 constexpr float kTop = 7.f, kLag = 8.f;
 
-// NT: tiles of 8 query rows.  One tile leaves room for 16 warps an SM.
+// NT: tiles of 8 query rows.
+#ifndef W1
+#define W1 12
+#define T1 64
+#define W2 8
+#define T2 64
+#endif
 template <int D, int NT, bool F32>
 struct Config {
-    static constexpr int kWarps = NT == 1 && !F32 ? 16 : 8;
+    static constexpr int kWarps = F32 ? 8 : (NT == 1 ? W1 : W2);
+    static constexpr int kTile = F32 ? 64 : (NT == 1 ? T1 : T2);         // keys
+    static constexpr int kBlocks = kTile / kBlock;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kRows = 8 * NT;
-    static constexpr int kStage = kTile / kBlock * Layout<D>::kBytes;
-    static constexpr int kStages = D == 64 ? 6 : (kWarps == 16 ? 3 : 6);
+    static constexpr int kStage = kBlocks * Layout<D>::kBytes;
+    static constexpr int kStages = 221184 / kWarps / kStage > 6 ? 6 : 221184 / kWarps / kStage;
     static constexpr int kRing = kStages * kStage;                       // of a warp
     static constexpr int kPart = kRows * (D + 2);                        // floats of a partial result
-    static_assert(kRing >= kPart * 4, "a warp's partial result lies in its ring");
+    static_assert(kStages >= 2 && kRing >= kPart * 4, "a warp's partial result lies in its ring");
     static constexpr int kSmem = kWarps * kRing;
+};
+
+// An item that began in CTA `from` and ends in this one: joined by the second kernel.
+struct Owner {
+    int seq, item, from;         // seq < 0: none
 };
 
 struct Args {
@@ -69,8 +81,9 @@ struct Args {
     float scale_log2, v_unit;
     unsigned *status;
     unsigned *cta_status;        // [CTAs]
-    unsigned *before;            // [B + 1] tiles of a head's sequences before b
-    float *part;                 // [CTAs][2][warps][kPart]
+    Owner *owners;               // [CTAs]
+    float *part;                 // [CTAs][2 + warps][kPart]: of the CTA's first item, its last,
+                                 // and what each warp closed
     int ctas;
     bool lost_wait;              // test hook
 };
@@ -80,19 +93,29 @@ struct Args {
 struct Split {
     unsigned long long total;
     int ctas;
-    __device__ unsigned long long cta(int c) const { return total * (unsigned)c / (unsigned)ctas; }
+    unsigned long long each;         // floor(total c / ctas) = each c + floor(rest c / ctas)
+    unsigned rest;
+    __device__ unsigned long long cta(int c) const {
+        return each * (unsigned)c + rest * (unsigned)c / (unsigned)ctas;
+    }
     template <int WARPS>
     __device__ unsigned long long warp(int c, int w) const {
         const unsigned long long a = cta(c), n = cta(c + 1) - a;
         return a + n * (unsigned)w / WARPS;
     }
 };
+// Quotients of 64 bits take a hundred instructions; most are of 32.
+__device__ __forceinline__ unsigned long long divide(unsigned long long a, unsigned b) {
+    return a >> 32 ? a / b : (unsigned)a / b;
+}
 template <int WARPS>
 __device__ __forceinline__ Split split_of(const Args &a, unsigned tiles) {
     Split s;
     s.total = (unsigned long long)tiles * (unsigned)a.items;
     const unsigned long long most = (s.total + WARPS - 1) / WARPS;      // a tile for each warp at least
     s.ctas = most < (unsigned)a.ctas ? (most > 0 ? (int)most : 1) : a.ctas;
+    s.each = divide(s.total, s.ctas);
+    s.rest = (unsigned)(s.total - s.each * (unsigned)s.ctas);
     return s;
 }
 
@@ -100,11 +123,12 @@ __device__ __forceinline__ int length(const Args &a, int b) {
     const int n = a.lens[b], most = a.columns * a.blocks * kBlock;
     return n < 0 ? 0 : (n < most ? n : most);
 }
-__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+template <int TILE>
+__device__ __forceinline__ int tiles_of(int len) { return (len + TILE - 1) / TILE; }
 
 // ------------------------------------------------------------------ products
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
                  "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
@@ -161,7 +185,7 @@ __device__ __forceinline__ long long out_row(const Args &a, int seq, int head, i
 // rows 8 nt + 2c, + 1 and of their outputs the features r D / 8 + 2 mt, + 1.
 template <int D, int NT, bool F32>
 struct State {
-    static constexpr int kSteps = D / 16;
+    static constexpr int kSteps = D / 16, kTile = Config<D, NT, F32>::kTile;
     uint32_t q[F32 ? 2 : 1][NT][kSteps][2];
     float o[NT][kSteps][4];
     float m[NT][2], l[NT][2], mul[NT][2];
@@ -196,7 +220,8 @@ struct State {
             int e = 268 - (int)(__float_as_uint(top) >> 23);
             e = e < 253 ? e : 253;
             const float up = __uint_as_float((unsigned)e << 23);
-            const float down = __uint_as_float((unsigned)(254 - e) << 23) * a.scale_log2;
+            // (never 0: hidden scores are -infinity times it)
+            const float down = fmaxf(__uint_as_float((unsigned)(254 - e) << 23) * a.scale_log2, 1.2e-38f);
 #pragma unroll
             for (int j = 0; j < kSteps; ++j)
 #pragma unroll
@@ -261,9 +286,10 @@ struct State {
         }
     }
 
-    // o += p v over a block; p as operands, values of keys from `left` on are zeros.
+    // o += p v over a block; p as operands.  LEFT: values of keys from `left` on are zeros.
+    template <bool LEFT>
     __device__ __forceinline__ void mix(const unsigned char *block, const uint32_t (&p)[F32 ? 2 : 1][NT][2],
-                                        int left) {
+                                        int left, float (&apart)[F32 ? NT : 1][F32 ? kSteps : 1][4]) {
         const int lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
         uint32_t w0[D / 32], w1[D / 32];
         load_words(block + Layout<D>::kV + c * D + r * (D / 8), w0);
@@ -271,7 +297,7 @@ struct State {
         const unsigned char *vs = block + Layout<D>::kVs + r * (D / 8) / 16 * kBlock + 2 * c;
         uint32_t f0 = kv4::scales_to_half2(*reinterpret_cast<const unsigned short *>(vs));
         uint32_t f1 = kv4::scales_to_half2(*reinterpret_cast<const unsigned short *>(vs + 8));
-        if (left < kBlock) {         // what lies behind the last key may be anything
+        if (LEFT && left < kBlock) { // what lies behind the last key may be anything
             f0 = 2 * c + 1 < left ? f0 : (2 * c < left ? f0 & 0xffffu : 0u);
             f1 = 2 * c + 9 < left ? f1 : (2 * c + 8 < left ? f1 & 0xffffu : 0u);
         }
@@ -286,28 +312,35 @@ struct State {
                                        kv4::mul_half2(h1[2 * y], f1), kv4::mul_half2(h1[2 * y + 1], f1)};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma(o[nt][2 * x + y], v, p[0][nt]);
-                    if (F32) mma(o[nt][2 * x + y], v, p[F32 ? 1 : 0][nt]);
+                    if (F32) {
+                        mma(apart[F32 ? nt : 0][F32 ? 2 * x + y : 0], v, p[0][nt]);
+                        mma(apart[F32 ? nt : 0][F32 ? 2 * x + y : 0], v, p[F32 ? 1 : 0][nt]);
+                    } else {
+                        mma(o[nt][2 * x + y], v, p[0][nt]);
+                    }
                 }
             }
         }
     }
 
-    // A tile of keys key0 .. key0 + 31, those below len.
+    // A tile of keys from key0 on, those below len.  EDGE: some of them may not be there, or
+    // not be seen by all rows.
+    template <bool EDGE>
     __device__ __forceinline__ void tile(const unsigned char *stage, int key0, int len) {
         const int r = threadIdx.x % 32 / 4;
-        float s[2][NT][4];
-        const bool both = key0 + kBlock < len;
-        scores(stage, s[0]);
-        if (both) {
-            scores(stage + Layout<D>::kBytes, s[1]);
-        } else {
+        constexpr int N = kTile / kBlock;
+        float s[N][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < N; ++i) {
+            if (!EDGE || key0 + i * kBlock < len) {
+                scores(stage + i * Layout<D>::kBytes, s[i]);
+            } else {
 #pragma unroll
-                for (int z = 0; z < 4; ++z) s[1][nt][z] = 0.f;
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) s[i][nt][z] = -INFINITY;
+            }
         }
-        const bool edge = key0 + kTile > full;
         float top[NT][2];
         bool above = false;
 #pragma unroll
@@ -316,16 +349,15 @@ struct State {
             for (int z = 0; z < 2; ++z) {
                 float t = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < N; ++i)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         float &x = s[i][nt][2 * j + z];
-                        x *= mul[nt][z];
-                        if (edge && key0 + i * kBlock + 8 * j + r >= limit[nt][z]) x = -INFINITY;
+                        if (EDGE && key0 + i * kBlock + 8 * j + r >= limit[nt][z]) x = -INFINITY;
                         t = fmaxf(t, x);
                     }
-                top[nt][z] = t;
-                above = above || t > m[nt][z] + kLag;
+                top[nt][z] = t * mul[nt][z];             // mul is positive
+                above = above || top[nt][z] > m[nt][z] + kLag;
             }
         if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
@@ -347,17 +379,18 @@ struct State {
                     }
                 }
         }
-        uint32_t p[2][F32 ? 2 : 1][NT][2];
+        uint32_t p[N][F32 ? 2 : 1][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float base[2];
 #pragma unroll
-            for (int z = 0; z < 2; ++z) base[z] = m[nt][z] == -INFINITY ? 0.f : m[nt][z] - kTop;
+            for (int z = 0; z < 2; ++z) base[z] = m[nt][z] == -INFINITY ? 0.f : kTop - m[nt][z];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < N; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float u = exp2_of(s[i][nt][2 * j] - base[0]), v = exp2_of(s[i][nt][2 * j + 1] - base[1]);
+                    const float u = exp2_of(fmaf(s[i][nt][2 * j], mul[nt][0], base[0])),
+                                v = exp2_of(fmaf(s[i][nt][2 * j + 1], mul[nt][1], base[1]));
                     l[nt][0] += u;
                     l[nt][1] += v;
                     const uint32_t h = pack_half(u, v);
@@ -368,8 +401,22 @@ struct State {
                     }
                 }
         }
-        mix(stage, p[0], len - key0);
-        if (both) mix(stage + Layout<D>::kBytes, p[1], len - key0 - kBlock);
+        // fp32: the tensor cores' sums are cut, not rounded, so a tile's are added to the others
+        // by an addition that rounds (16 contexts of 32768 keys: 3.7e-6 of o, all of one sign,
+        // and @ so)
+        float apart[F32 ? NT : 1][F32 ? kSteps : 1][4] = {};
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (!EDGE || key0 + i * kBlock < len)
+                mix<EDGE>(stage + i * Layout<D>::kBytes, p[i], len - key0 - i * kBlock, apart);
+        if (F32) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) o[nt][j][z] += apart[F32 ? nt : 0][F32 ? j : 0][z];
+        }
     }
 
     __device__ __forceinline__ void finish() {
@@ -439,11 +486,63 @@ __device__ __forceinline__ void next_item(const Args &a, Place &p) {
     } while (p.len == 0);
 }
 
-// A warp's last part of an item, for the join in shared memory.
-struct Last {
-    int seq, item;       // item < 0: none
+// A part of an item that a warp did not have alone: where in shared memory or
+// the workspace it lies, for the CTA's own join.
+struct Part {
+    int seq, item;       // seq < 0: none
     bool first, end;     // has the item's first tile, its last
 };
+
+// Parts of a row joined: lane m < count brings a part's base and sum; returns its
+// weight, and the row's base and sum.
+__device__ __forceinline__ float join_weights(bool there, float m, float sum, float &base, float &l) {
+    base = there ? m : -INFINITY;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) base = fmaxf(base, __shfl_xor_sync(0xffffffffu, base, o));
+    const float w = !there ? 0.f : (m == base ? 1.f : exp2_of(m - base));
+    l = there ? w * sum : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    return w;
+}
+
+template <int N>
+__device__ __forceinline__ void load_row(const float *p, float (&v)[N]) {
+    if (N == 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(p);
+        v[0] = x.x; v[1] = x.y; v[N - 2] = x.z; v[N - 1] = x.w;
+    } else {
+        const float2 x = *reinterpret_cast<const float2 *>(p);
+        v[0] = x.x; v[1] = x.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_row(float *p, const float (&v)[N]) {
+    if (N == 4) *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[N - 2], v[N - 1]);
+    else *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+}
+template <int N>
+__device__ __forceinline__ void store_row(__nv_bfloat16 *p, const float (&v)[N]) {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = reinterpret_cast<const uint32_t &>(b);
+    }
+    if (N == 4) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[N / 2 - 1]);
+    else *reinterpret_cast<uint32_t *>(p) = w[0];
+}
+
+// A row's result: lane's N features of it.
+template <typename T, int D, int N>
+__device__ __forceinline__ void write_row(const Args &a, long long row, float (&v)[N], float base, float l) {
+    const int lane = threadIdx.x % 32;
+    const float f = l == 0.f ? 0.f : a.v_unit / l;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] *= f;
+    store_row(static_cast<T *>(a.o) + row * D + N * lane, v);
+    if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (base + log2f(l)) * kLn2;
+}
 
 template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(Config<D, NT, F32>::kThreads, 1)
@@ -453,21 +552,22 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t bars[C::kWarps][C::kStages];
     __shared__ unsigned sums[C::kThreads], warp_sums[C::kWarps];
-    __shared__ Last lasts[C::kWarps];
+    __shared__ Part parts[2 * C::kWarps];       // of each warp: what it closed, what it had last
     __shared__ unsigned trouble;
+    __shared__ int from;                        // the CTA in which this one's first item begins
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, cta = blockIdx.x;
     unsigned char *ring = smem + warp * C::kRing;
     if (lane == 0) {
         for (int i = 0; i < C::kStages; ++i) tc::mbar_init(&bars[warp][i], 1);
         tc::fence_mbar_init();
-        lasts[warp].item = -1;
+        parts[2 * warp].seq = parts[2 * warp + 1].seq = -1;
     }
     if (tid == 0) trouble = kDevOk;
 
     // tiles before each thread's share of the sequences
     const int share = (a.B + C::kThreads - 1) / C::kThreads, b0 = tid * share;
     unsigned mine = 0;
-    for (int b = b0; b < b0 + share && b < a.B; ++b) mine += tiles_of(length(a, b));
+    for (int b = b0; b < b0 + share && b < a.B; ++b) mine += tiles_of<C::kTile>(length(a, b));
     unsigned sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -482,14 +582,6 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
         tiles += warp_sums[w];
     }
     sums[tid] = sum - mine;
-    if (cta == 0) {              // for the join
-        unsigned x = sum - mine;
-        for (int b = b0; b < b0 + share && b < a.B; ++b) {
-            a.before[b] = x;
-            x += tiles_of(length(a, b));
-        }
-        if (tid == 0) a.before[a.B] = tiles;
-    }
     __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -500,11 +592,12 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
         end = split.warp<C::kWarps>(cta, warp + 1);
     }
     bool ok = true, bad = false;
+    float *const mine_at = a.part + (size_t)cta * (2 + C::kWarps) * C::kPart;
     if (u < end) {
         // where the warp's tiles begin
         Place at;
         {
-            const unsigned x = (unsigned)(u / (unsigned)a.items);
+            const unsigned x = (unsigned)divide(u, a.items);
             int lo = 0, hi = C::kThreads - 1;
             while (lo < hi) {                        // the last share that begins at x or before
                 const int mid = (lo + hi + 1) / 2;
@@ -513,23 +606,30 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
             unsigned y = sums[lo];
             at.seq = lo * share;
             at.len = length(a, at.seq);
-            while (y + tiles_of(at.len) <= x) {
-                y += tiles_of(at.len);
+            while (y + tiles_of<C::kTile>(at.len) <= x) {
+                y += tiles_of<C::kTile>(at.len);
                 at.len = length(a, ++at.seq);
             }
             const unsigned long long rest = u - (unsigned long long)y * (unsigned)a.items;
-            at.item = (int)(rest / (unsigned)tiles_of(at.len));
-            at.tile = (int)(rest % (unsigned)tiles_of(at.len));
+            at.item = (int)divide(rest, tiles_of<C::kTile>(at.len));
+            at.tile = (int)(rest - (unsigned long long)at.item * (unsigned)tiles_of<C::kTile>(at.len));
         }
         const int n = (int)(end - u);
+        if (lane == 0 && u == split.cta(cta)) {      // the CTA's first tile
+            const unsigned long long x = u - at.tile;
+            int c = min((int)((float)x / (float)split.total * split.ctas), cta);
+            while (c > 0 && split.cta(c) > x) --c;
+            while (split.cta(c + 1) <= x) ++c;
+            from = c;
+        }
         // copies: the lanes look up the blocks of 16 tiles at a time
         Place ahead = at;
         int issued = 0, looked = -1;
         unsigned block = 0;
         auto issue = [&](int slot) {
-            if (looked < 0 || ahead.tile >= looked + 16) {
+            if (looked < 0 || ahead.tile >= looked + 32 / C::kBlocks) {
                 looked = ahead.tile;
-                const int nb = 2 * looked + lane;
+                const int nb = C::kBlocks * looked + lane;
                 block = 0;
                 if (nb * kBlock < ahead.len) {
                     const int column = nb / a.blocks;
@@ -541,17 +641,16 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
                     block = ((unsigned)page * a.Hk + ahead.item / a.groups) * a.blocks + (nb - column * a.blocks);
                 }
             }
-            const int i = 2 * (ahead.tile - looked);
-            const unsigned from = __shfl_sync(0xffffffffu, block, i + (lane & 1));
-            const bool two = ahead.tile * kTile + kBlock < ahead.len;
-            if (lane == 0) tc::mbar_expect_tx(&bars[warp][slot], (two ? 2 : 1) * Layout<D>::kBytes);
+            const unsigned from = __shfl_sync(0xffffffffu, block, C::kBlocks * (ahead.tile - looked) + lane % C::kBlocks);
+            const int there = min(C::kBlocks, (ahead.len - ahead.tile * C::kTile + kBlock - 1) / kBlock);
+            if (lane == 0) tc::mbar_expect_tx(&bars[warp][slot], there * Layout<D>::kBytes);
             __syncwarp();
-            if (lane < (two ? 2 : 1))
+            if (lane < there)
                 tc::bulk_load(ring + slot * C::kStage + lane * Layout<D>::kBytes,
                               a.pool + (unsigned long long)from * Layout<D>::kBytes, Layout<D>::kBytes,
                               &bars[warp][slot]);
             ++issued;
-            if (++ahead.tile == tiles_of(ahead.len)) {
+            if (++ahead.tile == tiles_of<C::kTile>(ahead.len)) {
                 looked = -1;
                 if (issued < n) next_item(a, ahead);
             }
@@ -562,13 +661,14 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
         int slot = 0, parity = 0;
         for (int done = 0; done < n;) {
             const int head = at.item / a.groups, group = at.item - head * a.groups;
-            const int stop = min(tiles_of(at.len), at.tile + n - done), begin = at.tile;
+            const int stop = min(tiles_of<C::kTile>(at.len), at.tile + n - done), begin = at.tile;
             st.template begin<T>(a, at.seq, head, group, at.len);
             for (; at.tile < stop; ++at.tile, ++done) {
                 ok = tc::mbar_wait(&bars[warp][slot], parity) && !a.lost_wait;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                st.tile(ring + slot * C::kStage, at.tile * kTile, at.len);
+                if ((at.tile + 1) * C::kTile <= st.full) st.template tile<false>(ring + slot * C::kStage, at.tile * C::kTile, at.len);
+                else st.template tile<true>(ring + slot * C::kStage, at.tile * C::kTile, at.len);
                 __syncwarp();
                 if (issued < n) issue(slot);
                 if (++slot == C::kStages) {
@@ -577,15 +677,16 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
                 }
             }
             if (!ok) break;
-            const bool first = begin == 0, whole = stop == tiles_of(at.len);
+            const bool first = begin == 0, whole = stop == tiles_of<C::kTile>(at.len);
             st.finish();
             if (first && whole) {
                 st.template write<T>(a, at.seq, head, group);
             } else if (done < n) {                   // closes an item that others began
-                st.put(a.part + ((size_t)(2 * cta + 1) * C::kWarps + warp) * C::kPart);
+                st.put(mine_at + (2 + warp) * C::kPart);
+                if (lane == 0) parts[2 * warp] = {at.seq, at.item, false, true};
             } else {
                 st.put(reinterpret_cast<float *>(ring));
-                if (lane == 0) lasts[warp] = {at.seq, at.item, first, whole};
+                if (lane == 0) parts[2 * warp + 1] = {at.seq, at.item, first, whole};
             }
             if (done < n) next_item(a, at);
         }
@@ -605,156 +706,151 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
     }
     __syncthreads();
 
-    // items that several of the CTA's warps had at their ends, in order
-    for (int w = 0; w < C::kWarps;) {
-        const Last x = lasts[w];
-        int to = w + 1, last = w;
-        if (x.item < 0) {
-            ++w;
-            continue;
-        }
-        for (; to < C::kWarps; ++to) {
-            if (lasts[to].item < 0) continue;        // no tiles (or an item of its own, whole)
-            if (lasts[to].item != x.item || lasts[to].seq != x.seq) break;
-            last = to;
-        }
-        const bool whole = x.first && lasts[last].end;
-        const int head = x.item / a.groups, group = x.item - head * a.groups;
-        float *out = a.part + ((size_t)(2 * cta) * C::kWarps + w) * C::kPart;
-        for (int i = tid; i < C::kRows * D; i += C::kThreads) {
-            const int n = i / D, f = i - n * D;
-            if (group * C::kRows + n >= a.rows) break;
-            float base = -INFINITY, l = 0.f, v = 0.f;
-            for (int y = w; y <= last; ++y)
-                if (lasts[y].item >= 0)
-                    base = fmaxf(base, reinterpret_cast<const float *>(smem + y * C::kRing)[C::kRows * D + n]);
-            for (int y = w; y <= last; ++y) {
-                if (lasts[y].item < 0) continue;
-                const float *part = reinterpret_cast<const float *>(smem + y * C::kRing);
-                const float b = part[C::kRows * D + n], s = b == base ? 1.f : exp2_of(b - base);
-                l = fmaf(s, part[C::kRows * D + C::kRows + n], l);
-                v = fmaf(s, part[i], v);
-            }
-            if (whole) {
-                const long long row = out_row(a, x.seq, head, group * C::kRows + n);
-                st(static_cast<T *>(a.o) + row * D + f, v * (l == 0.f ? 0.f : a.v_unit / l));
-                if (f == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (base + log2f(l)) * kLn2;
-            } else {
-                out[i] = v;
-                if (f == 0) {
-                    out[C::kRows * D + n] = base;
-                    out[C::kRows * D + C::kRows + n] = l;
+    // Items that several of the CTA's warps had: a warp for each row.  Lane i
+    // looks at part i; parts of an item follow each other.
+    {
+        constexpr int N = D / 32;
+        Part x{-1, 0, false, false};
+        if (lane < 2 * C::kWarps) x = parts[lane];
+        const unsigned all = __ballot_sync(0xffffffffu, x.seq >= 0);
+        const unsigned lower = all & ((1u << lane) - 1);
+        const int prev = lower ? 31 - __clz(lower) : lane;
+        const int pseq = __shfl_sync(0xffffffffu, x.seq, prev), pitem = __shfl_sync(0xffffffffu, x.item, prev);
+        unsigned leaders = __ballot_sync(0xffffffffu, x.seq >= 0 && (!lower || pseq != x.seq || pitem != x.item));
+        int turn = warp;
+        Owner own{-1, 0, 0};
+        while (leaders) {
+            const int a0 = __ffs(leaders) - 1;
+            leaders &= leaders - 1;
+            const int a1 = leaders ? __ffs(leaders) - 1 : 32;      // the next item's
+            const unsigned members = all & (a1 == 32 ? 0xffffffffu : (1u << a1) - 1) & ~((1u << a0) - 1);
+            const int seq = __shfl_sync(0xffffffffu, x.seq, a0), item = __shfl_sync(0xffffffffu, x.item, a0);
+            const bool first = __shfl_sync(0xffffffffu, (int)x.first, a0);
+            const bool whole = __shfl_sync(0xffffffffu, (int)x.end, 31 - __clz(members));
+            const int head = item / a.groups, group = item - head * a.groups;
+            const int rows = min(C::kRows, a.rows - group * C::kRows);
+            float *out = mine_at + (first ? 1 : 0) * C::kPart;
+            const float *part = lane & 1 ? reinterpret_cast<const float *>(smem + lane / 2 * C::kRing)
+                                         : mine_at + (2 + lane / 2) * C::kPart;
+            const bool here = members >> lane & 1;
+            for (; turn < rows; turn += C::kWarps) {
+                const float m = here ? part[C::kRows * D + turn] : 0.f,
+                            t = here ? part[C::kRows * D + C::kRows + turn] : 0.f;
+                float base, l, v[N] = {};
+                const float w = join_weights(here, m, t, base, l);
+                for (unsigned left = members; left; left &= left - 1) {
+                    const int k = __ffs(left) - 1;
+                    const float *p = k & 1 ? reinterpret_cast<const float *>(smem + k / 2 * C::kRing)
+                                           : mine_at + (2 + k / 2) * C::kPart;
+                    const float f = __shfl_sync(0xffffffffu, w, k);
+                    float y[N];
+                    load_row(p + turn * D + N * lane, y);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) v[i] = fmaf(f, y[i], v[i]);
+                }
+                if (first && whole) {
+                    write_row<T, D>(a, out_row(a, seq, head, group * C::kRows + turn), v, base, l);
+                } else {
+                    store_row(out + turn * D + N * lane, v);
+                    if (lane == 0) {
+                        out[C::kRows * D + turn] = base;
+                        out[C::kRows * D + C::kRows + turn] = l;
+                    }
                 }
             }
+            turn -= rows;
+            while (turn < 0) turn += C::kWarps;
+            if (!first && whole) own = {seq, item, from};        // (the CTA's first item, if any)
         }
-        w = to;
+        if (tid == 0) a.owners[cta] = own;
     }
     if (tid == 0) a.cta_status[cta] = trouble;
+
+    // rows of empty caches
+    for (int b = cta; b < a.B; b += gridDim.x) {
+        if (length(a, b) > 0) continue;
+        const long long row0 = (long long)b * a.Tq * a.Hq;
+        const long long n = (long long)a.Tq * a.Hq;
+        for (long long i = tid; i < n * (D / 4); i += C::kThreads) {
+            const float zero[4] = {};
+            store_row(static_cast<T *>(a.o) + row0 * D + 4 * i, zero);
+        }
+        if (a.lse)
+            for (long long i = tid; i < n; i += C::kThreads) a.lse[row0 + i] = -INFINITY;
+    }
 }
 
-// Joins the parts of items that several CTAs had, and writes the rows of empty
-// caches; PER warps to a row.  The first block writes the status word.
-template <int D, int NT, bool F32, int PER>
-__global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ Args a) {
+// Joins the parts of the item that began in an earlier CTA and ends in CTA
+// blockIdx.x; PER warps to a row.  The first block writes the status word.
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(512) kv4_join_kernel(const __grid_constant__ Args a) {
     using C = Config<D, NT, F32>;
     using T = std::conditional_t<F32, float, __nv_bfloat16>;
-    constexpr int V = D / 32;
-    __shared__ float shared_v[PER == 1 ? 1 : 8][D], shared_l[8];
+    constexpr int N = D / 32, kPer = 16 / C::kRows;
+    __shared__ __align__(16) float shared_v[16][D];
+    __shared__ float shared_m[16], shared_l[16];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, n = warp % C::kRows, sub = warp / C::kRows;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = warp % PER;
+    const Owner own = a.owners[blockIdx.x];
     if (blockIdx.x == 0 && warp == 0) {
         unsigned x = kDevOk;
         for (int c = lane; c < a.ctas; c += 32) x = max(x, a.cta_status[c]);
         x = __reduce_max_sync(0xffffffffu, x);
         if (lane == 0) *a.status = x;
     }
-    const long long rows = (long long)a.B * a.Hk * a.rows;
-    const long long i = (long long)blockIdx.x * (8 / PER) + warp / PER;
-    bool there = i < rows;
-    const int seq = there ? (int)(i / ((long long)a.Hk * a.rows)) : 0;
-    const int rest = there ? (int)(i - (long long)seq * a.Hk * a.rows) : 0;
-    const int head = rest / a.rows, r = rest - head * a.rows, group = r / C::kRows, n = r - group * C::kRows;
-    const unsigned before = a.before[seq], nt = a.before[seq + 1] - before;
-    const Split split = split_of<C::kWarps>(a, a.before[a.B]);
-    const unsigned long long x = (unsigned long long)before * (unsigned)a.items +
-                                 (unsigned long long)(head * a.groups + group) * nt, y = x + nt;
-    int c0 = 0, c1 = -1;
-    if (there && nt > 0) {
-        c0 = (int)(x * (unsigned)split.ctas / split.total);
-        while (c0 + 1 < split.ctas && split.cta(c0 + 1) <= x) ++c0;
-        while (split.cta(c0) > x) --c0;
-        c1 = c0;
-        while (c1 + 1 < split.ctas && split.cta(c1 + 1) < y) ++c1;
-    }
-    // each lane looks for the parts of a CTA: what its warps joined, and what a warp closed
-    float base = -INFINITY, l = 0.f, v[V] = {};
-    int parts = 0;
-    for (int c = c0; c <= c1; c += 32) {
-        int slot[2] = {-1, -1};
-        if (c + lane <= c1) {
-            for (int w = 0; w < C::kWarps; ++w) {
-                const unsigned long long s = split.warp<C::kWarps>(c + lane, w),
-                                         e = split.warp<C::kWarps>(c + lane, w + 1);
-                if (s >= e || s >= y || e <= x) continue;
-                if (e <= y) {
-                    if (slot[0] < 0) slot[0] = (2 * (c + lane)) * C::kWarps + w;
-                } else {
-                    slot[1] = (2 * (c + lane) + 1) * C::kWarps + w;
-                }
-            }
-        }
-        const unsigned has[2] = {__ballot_sync(0xffffffffu, slot[0] >= 0), __ballot_sync(0xffffffffu, slot[1] >= 0)};
-        parts += __popc(has[0]) + __popc(has[1]);
-        if (c0 == c1 && parts == 1) break;           // one writer: it wrote the result
-        float m[2], sum[2], top = base;
+    if (own.seq < 0) return;
+    const int head = own.item / a.groups, group = own.item - head * a.groups;
+    const bool there = group * C::kRows + n < a.rows;
+    // parts: of its first CTA the last item's, of the others the first item's
+    const int count = (int)blockIdx.x - own.from + 1;
+    float base = -INFINITY, l = 0.f, v[N] = {};
+    for (int k0 = 32 * sub; k0 < count && there; k0 += 32 * kPer) {
+        const int k = k0 + lane, c = own.from + k;
+        const float *part = a.part + ((size_t)min(c, (int)blockIdx.x) * (2 + C::kWarps) + (k == 0)) * C::kPart;
+        const bool here = k < count;
+        const float m = part[C::kRows * D + n], sum = part[C::kRows * D + C::kRows + n];
+        float top, t;
+        const float w = join_weights(here, m, sum, top, t);
+        const float both = fmaxf(base, top);
+        const float f0 = base == both ? 1.f : exp2_of(base - both), f1 = top == both ? 1.f : exp2_of(top - both);
+        base = both;
+        l = l * f0 + t * f1;
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            const float *part = a.part + (size_t)max(slot[z], 0) * C::kPart + C::kRows * D;
-            m[z] = slot[z] >= 0 ? part[n] : -INFINITY;
-            sum[z] = slot[z] >= 0 ? part[C::kRows + n] : 0.f;
-            top = fmaxf(top, m[z]);
-        }
+        for (int i = 0; i < N; ++i) v[i] *= f0;
+        const int most = min(32, count - k0);
+#pragma unroll 4
+        for (int j = 0; j < most; ++j) {
+            const float f = __shfl_sync(0xffffffffu, w, j) * f1;
+            const float *p = a.part + ((size_t)(own.from + k0 + j) * (2 + C::kWarps) + (k0 + j == 0)) * C::kPart;
+            float y[N];
+            load_row(p + n * D + N * lane, y);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float f = base == top ? 1.f : exp2_of(base - top);
-        l *= f;
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[k] *= f;
-        base = top;
-        float wt[2];
-#pragma unroll
-        for (int z = 0; z < 2; ++z) wt[z] = slot[z] < 0 ? 0.f : (m[z] == top ? 1.f : exp2_of(m[z] - top));
-        for (int k = sub; k < 32; k += PER) {
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                if (!(has[z] >> k & 1)) continue;
-                const float g = __shfl_sync(0xffffffffu, wt[z], k), gs = __shfl_sync(0xffffffffu, sum[z], k);
-                const float *part = a.part + (size_t)__shfl_sync(0xffffffffu, slot[z], k) * C::kPart + n * D;
-                l = fmaf(g, gs, l);
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[j] = fmaf(g, part[lane + 32 * j], v[j]);
-            }
+            for (int i = 0; i < N; ++i) v[i] = fmaf(f, y[i], v[i]);
         }
     }
-    there = there && parts != 1;
-    if (PER > 1) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) shared_v[PER == 1 ? 0 : warp][lane + 32 * j] = v[j];
-        if (lane == 0) shared_l[warp] = l;
+    if (kPer > 1 && count > 32) {                    // (the same for all of the block)
+        store_row(&shared_v[warp][N * lane], v);
+        if (lane == 0) {
+            shared_m[warp] = base;
+            shared_l[warp] = l;
+        }
         __syncthreads();
         if (sub != 0) return;
-        for (int z = 1; z < PER; ++z) {              // the warps of a row share its base
-            l += shared_l[warp + z];
+        for (int z = 1; z < kPer; ++z) {
+            const int y = warp + z * C::kRows;
+            const float m = shared_m[y], both = fmaxf(base, m);
+            const float f0 = base == both ? 1.f : exp2_of(base - both), f1 = m == both ? 1.f : exp2_of(m - both);
+            base = both;
+            l = l * f0 + shared_l[y] * f1;
+            float t[N];
+            load_row(&shared_v[y][N * lane], t);
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[j] += shared_v[PER == 1 ? 0 : warp + z][lane + 32 * j];
+            for (int i = 0; i < N; ++i) v[i] = v[i] * f0 + t[i] * f1;
         }
+    } else if (sub != 0) {
+        return;
     }
-    if (!there) return;
-    const long long row = out_row(a, seq, head, r);
-    const float f = l == 0.f ? 0.f : a.v_unit / l;
-#pragma unroll
-    for (int j = 0; j < V; ++j) st(static_cast<T *>(a.o) + row * D + lane + 32 * j, v[j] * f);
-    if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (base + log2f(l)) * kLn2;
+    if (there) write_row<T, D>(a, out_row(a, own.seq, head, group * C::kRows + n), v, base, l);
 }
 
 // Without any key: zeros, from a launch that has no table to read.
@@ -782,27 +878,27 @@ int sm_count() {
 
 struct Plan {
     int nt, ctas;
-    size_t cta_status, before, part, bytes;
+    size_t cta_status, owners, part, bytes;
 };
 template <int D, int NT, bool F32>
 void sizes(Plan &p) {
     using C = Config<D, NT, F32>;
     p.nt = NT;
-    p.bytes = up256(p.part + (size_t)p.ctas * 2 * C::kWarps * C::kPart * sizeof(float));
+    p.bytes = up256(p.part + (size_t)p.ctas * (2 + C::kWarps) * C::kPart * sizeof(float));
 }
 Plan plan_of(const Kv4Attn &p) {
     Plan x{};
     x.ctas = sm_count();
     x.cta_status = kWsHeader;
-    x.before = up256(x.cta_status + x.ctas * sizeof(unsigned));
-    x.part = up256(x.before + ((size_t)p.B + 1) * sizeof(unsigned));
+    x.owners = up256(x.cta_status + x.ctas * sizeof(unsigned));
+    x.part = up256(x.owners + x.ctas * sizeof(Owner));
     const bool two = (long long)p.Hq / p.Hk * p.Tq > 8;
     if (p.d == 64) {
-        if (p.dtype == 1) two ? sizes<64, 2, false>(x) : sizes<64, 1, false>(x);
-        else two ? sizes<64, 2, true>(x) : sizes<64, 1, true>(x);
+        if (p.dtype == 0) sizes<64, 1, true>(x);
+        else two ? sizes<64, 2, false>(x) : sizes<64, 1, false>(x);
     } else {
-        if (p.dtype == 1) two ? sizes<128, 2, false>(x) : sizes<128, 1, false>(x);
-        else two ? sizes<128, 2, true>(x) : sizes<128, 1, true>(x);
+        if (p.dtype == 0) sizes<128, 1, true>(x);
+        else two ? sizes<128, 2, false>(x) : sizes<128, 1, false>(x);
     }
     return x;
 }
@@ -816,20 +912,16 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
     note_launch();
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // a warp for each row where there are enough of them, else 8
-    const long long rows = (long long)a.B * a.Hk * a.rows;
-    const bool many = rows >= 1024;
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(many ? (rows + 7) / 8 : rows));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)a.ctas);
+    cfg.blockDim = dim3(512);
     cfg.stream = s;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    e = many ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, F32, 1>, a)
-             : cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, F32, 8>, a);
+    e = cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, F32>, a);
     note_launch();
     return e;
 }
@@ -839,7 +931,7 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
 size_t kv4_attn_workspace_bytes(const Kv4Attn &p) { return plan_of(p).bytes; }
 
 bool kv4_attn_too_large(const Kv4Attn &p) {
-    const long long tiles = (long long)p.B * ((long long)p.columns * p.page / kTile + 1);
+    const long long tiles = (long long)p.B * ((long long)p.columns * p.page / 32 + 1);
     const long long rows = (long long)p.B * p.Tq * p.Hq;
     const long long blocks = (long long)p.n_pages * p.Hk * (p.page / kBlock);
     return tiles > INT32_MAX || rows > INT32_MAX || blocks > UINT32_MAX ||
@@ -861,7 +953,7 @@ cudaError_t launch_kv4_attn(const Kv4Attn &p, cudaStream_t s) {
     a.v_unit = p.v_unit;
     a.status = static_cast<unsigned *>(p.ws);
     a.cta_status = reinterpret_cast<unsigned *>(ws + x.cta_status);
-    a.before = reinterpret_cast<unsigned *>(ws + x.before);
+    a.owners = reinterpret_cast<Owner *>(ws + x.owners);
     a.part = reinterpret_cast<float *>(ws + x.part);
     a.ctas = x.ctas;
     // test hook: every warp takes its first wait for one that ran out
@@ -872,11 +964,9 @@ cudaError_t launch_kv4_attn(const Kv4Attn &p, cudaStream_t s) {
         note_launch();
         return cudaGetLastError();
     }
-    const bool f32 = p.dtype == 0;
-#define KLA_KV4(D, NT) (f32 ? launch<D, NT, true>(a, s) : launch<D, NT, false>(a, s))
-    if (p.d == 64) return x.nt == 2 ? KLA_KV4(64, 2) : KLA_KV4(64, 1);
-    return x.nt == 2 ? KLA_KV4(128, 2) : KLA_KV4(128, 1);
-#undef KLA_KV4
+    if (p.dtype == 0) return p.d == 64 ? launch<64, 1, true>(a, s) : launch<128, 1, true>(a, s);
+    if (p.d == 64) return x.nt == 2 ? launch<64, 2, false>(a, s) : launch<64, 1, false>(a, s);
+    return x.nt == 2 ? launch<128, 2, false>(a, s) : launch<128, 1, false>(a, s);
 }
 
 }  // namespace kla

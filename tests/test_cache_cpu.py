@@ -163,11 +163,12 @@ def _split(tiles, items, ctas, warps):
             for c in range(ctas)]
 
 
-@pytest.mark.parametrize("seed", range(16))
+@pytest.mark.parametrize("seed", range(24))
 def test_parts_that_are_left_are_the_parts_that_are_joined(seed):
-    """What warps and CTAs write of an item is what the join looks for, and covers it once."""
+    """The model of attention's split: every tile of an item is in one part, and the CTA that
+    has an item's end finds all of them."""
     r = random.Random(seed)
-    warps, ctas = r.choice([8, 16]), r.choice([3, 20, 152])
+    warps, ctas = r.choice([8, 12, 16]), r.choice([3, 20, 152])
     tiles = [r.choice([0, 1, 2, r.randint(0, 40), r.randint(0, 900)]) for _ in range(r.randint(1, 30))]
     items = r.randint(1, 6)
     ranges = _split(tiles, items, ctas, warps)
@@ -177,52 +178,46 @@ def test_parts_that_are_left_are_the_parts_that_are_joined(seed):
             if n:
                 starts.append((at, at + n))
             at += n
-    written = {x: [] for x in starts}            # item: (slot, first tile, end)
+    done, slots, owners = {}, {}, []
     for c, edges in enumerate(ranges):
-        last = [None] * warps
+        parts = []                                   # in the order of 2 w, 2 w + 1
         for w in range(warps):
             s, e = edges[w], edges[w + 1]
-            for x, y in starts:
-                if s >= e or s >= y or e <= x:
-                    continue
-                a, b = max(s, x), min(e, y)
-                if (a, b) == (x, y):
-                    written[x, y].append(("whole", a, b))
-                elif e > y:
-                    written[x, y].append(((2 * c + 1) * warps + w, a, b))
-                else:
-                    last[w] = (x, y, a, b)
-        w = 0
-        while w < warps:
-            if last[w] is None:
-                w += 1
+            if s == e:
                 continue
-            x, y, a, b = last[w]
-            to = w + 1
-            while to < warps and (last[to] is None or last[to][:2] == (x, y)):
-                if last[to] is not None:
-                    b = last[to][3]
-                to += 1
-            written[x, y].append(("whole" if (a, b) == (x, y) else 2 * c * warps + w, a, b))
-            w = to
-    for (x, y), parts in written.items():
-        assert sorted((a, b) for _, a, b in parts)[0][0] == x
-        assert sum(b - a for _, a, b in parts) == y - x
-        found = []
-        c0 = max(c for c in range(len(ranges)) if ranges[c][0] <= x)
-        c1 = max(c for c in range(len(ranges)) if ranges[c][0] < y)
-        for c in range(c0, c1 + 1):
-            slot = [None, None]
-            for w in range(warps):
-                s, e = ranges[c][w], ranges[c][w + 1]
-                if s >= e or s >= y or e <= x:
+            for x, y in starts:
+                a, b = max(s, x), min(e, y)
+                if a >= b:
                     continue
-                if e <= y:
-                    slot[0] = 2 * c * warps + w if slot[0] is None else slot[0]
+                if (a, b) == (x, y):
+                    assert done.setdefault((x, y), "warp") == "warp"
                 else:
-                    slot[1] = (2 * c + 1) * warps + w
-            found += [z for z in slot if z is not None]
-        if len(found) == 1:
-            assert [p[0] for p in parts] == ["whole"]
-        else:
-            assert sorted(found) == sorted(p[0] for p in parts)
+                    parts.append((2 * w + (b == e), (x, y), a, b))
+        assert [p[0] for p in parts] == sorted({p[0] for p in parts})
+        groups = []
+        for p in parts:
+            if groups and groups[-1][0] == p[1]:
+                assert groups[-1][2] == p[2]
+                groups[-1][2] = p[3]
+            else:
+                groups.append([p[1], p[2], p[3]])
+        for (x, y), a, b in groups:
+            if (a, b) == (x, y):
+                assert (x, y) not in done
+                done[x, y] = "cta"
+                continue
+            slot = (c, int(a == x))
+            assert slot not in slots
+            slots[slot] = ((x, y), a, b)
+            if a != x and b == y:
+                first = next(z for z in range(len(ranges)) if ranges[z][0] <= x < ranges[z][-1])
+                owners.append(((x, y), first, c))
+    for item, first, last in owners:
+        assert item not in done
+        done[item] = "join"
+        found = [slots.pop((c, int(c == first))) for c in range(first, last + 1)]
+        assert all(f[0] == item for f in found)
+        assert [f[1] for f in found[1:]] == [f[2] for f in found[:-1]]
+        assert (found[0][1], found[-1][2]) == item
+    assert not slots and set(done) == set(starts)
+    assert len({c for _, _, c in owners}) == len(owners)
