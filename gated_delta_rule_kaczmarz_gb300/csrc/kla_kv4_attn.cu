@@ -43,25 +43,25 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr float kTop = 7.f, kLag = 8.f;
 
 // NT: tiles of 8 query rows.
-#ifndef W1
-#define W1 12
-#define T1 64
-#define W2 8
-#define T2 64
-#endif
 template <int D, int NT, bool F32>
 struct Config {
-    static constexpr int kWarps = F32 ? 8 : (NT == 1 ? W1 : W2);
-    static constexpr int kTile = F32 ? 64 : (NT == 1 ? T1 : T2);         // keys
+    static constexpr int kWarps = F32 || NT > 1 ? 8 : 12;        // as many as registers allow
+    static constexpr int kTile = 64;                             // keys of a stage
+    static constexpr int kKeys = 32;                             // of a step of the softmax
     static constexpr int kBlocks = kTile / kBlock;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kRows = 8 * NT;
     static constexpr int kStage = kBlocks * Layout<D>::kBytes;
-    static constexpr int kStages = 221184 / kWarps / kStage > 6 ? 6 : 221184 / kWarps / kStage;
-    static constexpr int kRing = kStages * kStage;                       // of a warp
-    static constexpr int kPart = kRows * (D + 2);                        // floats of a partial result
-    static_assert(kStages >= 2 && kRing >= kPart * 4, "a warp's partial result lies in its ring");
+    static constexpr int kFit = 221184 / kWarps / kStage, kStages = kFit < 6 ? kFit : 6;
+    static constexpr int kRing = kStages * kStage;               // of a warp
     static constexpr int kSmem = kWarps * kRing;
+    static_assert(kStages >= 2 && kStage >= (kRows * (D + 2) + 3) * 4, "a part lies in a stage");
+};
+
+// n / d: (t + ((n - t) >> shift1)) >> shift2 with t the high half of multiplier n.
+struct Divisor {
+    unsigned multiplier;
+    int shift1, shift2;
 };
 
 // An item that began in CTA `from` and ends in this one: joined by the second kernel.
@@ -76,47 +76,44 @@ struct Args {
     const int *table, *lens;
     void *o;
     float *lse;
-    int B, Tq, Hq, Hk, G, blocks, n_pages, columns;     // blocks: of 16 tokens in a page
+    int B, Tq, Hq, Hk, G, d, blocks, n_pages, columns;     // blocks: of 16 tokens in a page
     int rows, groups, items;     // query rows of a key head, their groups, items of a sequence
+    Divisor by_G, by_groups, by_items, by_blocks;
     float scale_log2, v_unit;
+    int part_rows;               // rows of a part: of a group, as far as there are
+    int part_size;               // floats of a part, in whole 16 bytes
     unsigned *status;
     unsigned *cta_status;        // [CTAs]
     Owner *owners;               // [CTAs]
-    float *part;                 // [CTAs][2 + warps][kPart]: of the CTA's first item, its last,
+    float *part;                 // [CTAs][2 + warps][part_size]: of the CTA's first and last item,
                                  // and what each warp closed
     int ctas;
     bool lost_wait;              // test hook
 };
 
 // ------------------------------------------------------------------ the split
-// Tile u of all: items in order, their tiles in order.
+// Tile u of all (fewer than 2^31): items in order, their tiles in order.
 struct Split {
-    unsigned long long total;
+    unsigned total;
     int ctas;
-    unsigned long long each;         // floor(total c / ctas) = each c + floor(rest c / ctas)
-    unsigned rest;
-    __device__ unsigned long long cta(int c) const {
-        return each * (unsigned)c + rest * (unsigned)c / (unsigned)ctas;
-    }
-    template <int WARPS>
-    __device__ unsigned long long warp(int c, int w) const {
-        const unsigned long long a = cta(c), n = cta(c + 1) - a;
-        return a + n * (unsigned)w / WARPS;
-    }
+    unsigned each, rest;         // floor(total c / ctas) = each c + floor(rest c / ctas)
+    __device__ unsigned cta(int c) const { return each * (unsigned)c + rest * (unsigned)c / (unsigned)ctas; }
 };
-// Quotients of 64 bits take a hundred instructions; most are of 32.
-__device__ __forceinline__ unsigned long long divide(unsigned long long a, unsigned b) {
-    return a >> 32 ? a / b : (unsigned)a / b;
-}
 template <int WARPS>
 __device__ __forceinline__ Split split_of(const Args &a, unsigned tiles) {
     Split s;
-    s.total = (unsigned long long)tiles * (unsigned)a.items;
-    const unsigned long long most = (s.total + WARPS - 1) / WARPS;      // a tile for each warp at least
+    s.total = tiles * (unsigned)a.items;
+    const unsigned most = (s.total + WARPS - 1) / WARPS;        // a tile for each warp at least
     s.ctas = most < (unsigned)a.ctas ? (most > 0 ? (int)most : 1) : a.ctas;
-    s.each = divide(s.total, s.ctas);
-    s.rest = (unsigned)(s.total - s.each * (unsigned)s.ctas);
+    s.each = s.total / (unsigned)s.ctas;
+    s.rest = s.total - s.each * (unsigned)s.ctas;
     return s;
+}
+// Quotients by numbers that a launch keeps (Granlund and Montgomery, Division by
+// invariant integers using multiplication, 1994).
+__device__ __forceinline__ int divided(int n, const Divisor &d) {
+    const unsigned t = __umulhi(d.multiplier, (unsigned)n);
+    return (int)((t + (((unsigned)n - t) >> d.shift1)) >> d.shift2);
 }
 
 __device__ __forceinline__ int length(const Args &a, int b) {
@@ -177,15 +174,23 @@ __device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4]) {
 // Output row of row n of a group: its offset in [B, Tq, Hq], or -1 behind the last.
 __device__ __forceinline__ long long out_row(const Args &a, int seq, int head, int n) {
     if (n >= a.rows) return -1;
-    const int token = n / a.G, g = n - token * a.G;
+    const int token = divided(n, a.by_G), g = n - token * a.G;
     return ((long long)seq * a.Tq + token) * a.Hq + head * a.G + g;
+}
+
+// Row n of a key head's query rows.
+template <typename T>
+__device__ __forceinline__ const T *query(const Args &a, int seq, int head, int n) {
+    const int token = divided(n, a.by_G);
+    return static_cast<const T *>(a.q) + ((long long)seq * a.Tq + token) * a.q_stride +
+           (long long)(head * a.G + n - token * a.G) * a.d;
 }
 
 // What a warp holds of an item.  Thread (r, c) = (lane / 4, lane % 4) has query
 // rows 8 nt + 2c, + 1 and of their outputs the features r D / 8 + 2 mt, + 1.
 template <int D, int NT, bool F32>
 struct State {
-    static constexpr int kSteps = D / 16, kTile = Config<D, NT, F32>::kTile;
+    static constexpr int kSteps = D / 16, kKeys = Config<D, NT, F32>::kKeys;
     uint32_t q[F32 ? 2 : 1][NT][kSteps][2];
     float o[NT][kSteps][4];
     float m[NT][2], l[NT][2], mul[NT][2];
@@ -196,18 +201,16 @@ struct State {
     __device__ __forceinline__ void begin(const Args &a, int seq, int head, int group, int len) {
         const int lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
         const int first = len - a.Tq + 1;
-        full = first + group * 8 * NT / a.G;
+        full = first + divided(group * 8 * NT, a.by_G);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int n = group * 8 * NT + nt * 8 + r;
-            const long long row = n / a.G;
-            const T *src = static_cast<const T *>(a.q) + ((long long)seq * a.Tq + row) * a.q_stride +
-                           (long long)(head * a.G + n % a.G) * D + c * (D / 4);
+            const T *rows = query<T>(a, seq, head, n) + c * (D / 4);
             float x[D / 4], top = 0.f;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
                 float y[4] = {};
-                if (n < a.rows) load4(src + 4 * j, y);
+                if (n < a.rows) load4(rows + 4 * j, y);
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
                     x[4 * j + z] = y[z];
@@ -236,7 +239,7 @@ struct State {
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
                 mul[nt][z] = __shfl_sync(0xffffffffu, down, (2 * c + z) * 4);
-                limit[nt][z] = first + (group * 8 * NT + nt * 8 + 2 * c + z) / a.G;
+                limit[nt][z] = first + divided(group * 8 * NT + nt * 8 + 2 * c + z, a.by_G);
                 m[nt][z] = -INFINITY;
                 l[nt][z] = 0.f;
             }
@@ -286,8 +289,8 @@ struct State {
         }
     }
 
-    // o += p v over a block; p as operands.  LEFT: values of keys from `left` on are zeros.
-    template <bool LEFT>
+    // o += p v over a block; p as operands.  EDGE: values of keys from `left` on are zeros.
+    template <bool EDGE>
     __device__ __forceinline__ void mix(const unsigned char *block, const uint32_t (&p)[F32 ? 2 : 1][NT][2],
                                         int left, float (&apart)[F32 ? NT : 1][F32 ? kSteps : 1][4]) {
         const int lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
@@ -297,7 +300,7 @@ struct State {
         const unsigned char *vs = block + Layout<D>::kVs + r * (D / 8) / 16 * kBlock + 2 * c;
         uint32_t f0 = kv4::scales_to_half2(*reinterpret_cast<const unsigned short *>(vs));
         uint32_t f1 = kv4::scales_to_half2(*reinterpret_cast<const unsigned short *>(vs + 8));
-        if (LEFT && left < kBlock) { // what lies behind the last key may be anything
+        if (EDGE && left < kBlock) { // what lies behind the last key may be anything
             f0 = 2 * c + 1 < left ? f0 : (2 * c < left ? f0 & 0xffffu : 0u);
             f1 = 2 * c + 9 < left ? f1 : (2 * c + 8 < left ? f1 & 0xffffu : 0u);
         }
@@ -323,23 +326,24 @@ struct State {
         }
     }
 
-    // A tile of keys from key0 on, those below len.  EDGE: some of them may not be there, or
+    // kKeys keys from key0 on, those below len.  EDGE: some of them may not be there, or
     // not be seen by all rows.
     template <bool EDGE>
-    __device__ __forceinline__ void tile(const unsigned char *stage, int key0, int len) {
+    __device__ __forceinline__ void keys(const unsigned char *stage, int key0, int len) {
         const int r = threadIdx.x % 32 / 4;
-        constexpr int N = kTile / kBlock;
+        constexpr int N = kKeys / kBlock;
         float s[N][NT][4];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (!EDGE || key0 + i * kBlock < len) {
-                scores(stage + i * Layout<D>::kBytes, s[i]);
-            } else {
+        for (int i = 0; i < N; ++i)
+            if (!EDGE || key0 + i * kBlock < len) scores(stage + i * Layout<D>::kBytes, s[i]);
+        if (EDGE) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) s[i][nt][z] = -INFINITY;
-            }
+                for (int i = 0; i < N; ++i)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        if (key0 + i * kBlock + z / 2 * 8 + r >= limit[nt][z % 2]) s[i][nt][z] = -INFINITY;
         }
         float top[NT][2];
         bool above = false;
@@ -352,9 +356,7 @@ struct State {
                 for (int i = 0; i < N; ++i)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float &x = s[i][nt][2 * j + z];
-                        if (EDGE && key0 + i * kBlock + 8 * j + r >= limit[nt][z]) x = -INFINITY;
-                        t = fmaxf(t, x);
+                        t = fmaxf(t, s[i][nt][2 * j + z]);
                     }
                 top[nt][z] = t * mul[nt][z];             // mul is positive
                 above = above || top[nt][z] > m[nt][z] + kLag;
@@ -451,21 +453,22 @@ struct State {
                     a.lse[row] = sum == 0.f ? -INFINITY : (m[nt][z] - kTop + log2f(sum)) * kLn2;
             }
     }
-    // A partial result: outputs [rows][D], then bases, then sums.
-    __device__ __forceinline__ void put(float *part) const {
+    // A part: outputs [part_rows][D], then bases, then sums.
+    __device__ __forceinline__ void put(const Args &a, float *part) const {
         const int lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
                 const int n = nt * 8 + 2 * c + z;
+                if (n >= a.part_rows) continue;
 #pragma unroll
                 for (int j = 0; j < kSteps; ++j)
                     *reinterpret_cast<float2 *>(part + n * D + r * (D / 8) + 2 * j) =
                         make_float2(o[nt][j][z], o[nt][j][2 + z]);
                 if (r == 0) {
-                    part[8 * NT * D + n] = m[nt][z] - kTop;
-                    part[8 * NT * D + 8 * NT + n] = l[nt][z];
+                    part[a.part_rows * D + n] = m[nt][z] - kTop;
+                    part[a.part_rows * D + a.part_rows + n] = l[nt][z];
                 }
             }
     }
@@ -476,13 +479,15 @@ struct State {
 struct Place {
     int seq, len, item, tile;
 };
-__device__ __forceinline__ void next_item(const Args &a, Place &p) {
+// lens: the lengths in shared memory where they fit there, else nullptr.
+__device__ __forceinline__ int length(const Args &a, const int *lens, int b) { return lens ? lens[b] : length(a, b); }
+__device__ __forceinline__ void next_item(const Args &a, const int *lens, Place &p) {
     p.tile = 0;
     if (++p.item < a.items) return;
     p.item = 0;
     do {
         ++p.seq;
-        p.len = p.seq < a.B ? length(a, p.seq) : 1;
+        p.len = p.seq < a.B ? length(a, lens, p.seq) : 1;
     } while (p.len == 0);
 }
 
@@ -491,6 +496,7 @@ __device__ __forceinline__ void next_item(const Args &a, Place &p) {
 struct Part {
     int seq, item;       // seq < 0: none
     bool first, end;     // has the item's first tile, its last
+    int at;              // in shared memory
 };
 
 // Parts of a row joined: lane m < count brings a part's base and sum; returns its
@@ -552,6 +558,7 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t bars[C::kWarps][C::kStages];
     __shared__ unsigned sums[C::kThreads], warp_sums[C::kWarps];
+    __shared__ int all_lens[C::kThreads];
     __shared__ Part parts[2 * C::kWarps];       // of each warp: what it closed, what it had last
     __shared__ unsigned trouble;
     __shared__ int from;                        // the CTA in which this one's first item begins
@@ -567,7 +574,12 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
     // tiles before each thread's share of the sequences
     const int share = (a.B + C::kThreads - 1) / C::kThreads, b0 = tid * share;
     unsigned mine = 0;
-    for (int b = b0; b < b0 + share && b < a.B; ++b) mine += tiles_of<C::kTile>(length(a, b));
+    for (int b = b0; b < b0 + share && b < a.B; ++b) {
+        const int n = length(a, b);
+        all_lens[tid] = n;
+        mine += tiles_of<C::kTile>(n);
+    }
+    const int *const lens = share == 1 ? all_lens : nullptr;
     unsigned sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -586,18 +598,20 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const Split split = split_of<C::kWarps>(a, tiles);
-    unsigned long long u = 0, end = 0;
+    const unsigned cta0 = split.cta(cta);
+    unsigned u = 0, end = 0;
     if (cta < split.ctas) {
-        u = split.warp<C::kWarps>(cta, warp);
-        end = split.warp<C::kWarps>(cta, warp + 1);
+        const unsigned size = split.cta(cta + 1) - cta0;
+        u = cta0 + size / C::kWarps * warp + size % C::kWarps * warp / C::kWarps;
+        end = cta0 + size / C::kWarps * (warp + 1) + size % C::kWarps * (warp + 1) / C::kWarps;
     }
     bool ok = true, bad = false;
-    float *const mine_at = a.part + (size_t)cta * (2 + C::kWarps) * C::kPart;
+    float *const mine_at = a.part + (size_t)cta * (2 + C::kWarps) * a.part_size;
     if (u < end) {
         // where the warp's tiles begin
         Place at;
         {
-            const unsigned x = (unsigned)divide(u, a.items);
+            const unsigned x = (unsigned)divided((int)u, a.by_items);
             int lo = 0, hi = C::kThreads - 1;
             while (lo < hi) {                        // the last share that begins at x or before
                 const int mid = (lo + hi + 1) / 2;
@@ -605,104 +619,157 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
             }
             unsigned y = sums[lo];
             at.seq = lo * share;
-            at.len = length(a, at.seq);
+            at.len = length(a, lens, at.seq);
             while (y + tiles_of<C::kTile>(at.len) <= x) {
                 y += tiles_of<C::kTile>(at.len);
-                at.len = length(a, ++at.seq);
+                at.len = length(a, lens, ++at.seq);
             }
-            const unsigned long long rest = u - (unsigned long long)y * (unsigned)a.items;
-            at.item = (int)divide(rest, tiles_of<C::kTile>(at.len));
-            at.tile = (int)(rest - (unsigned long long)at.item * (unsigned)tiles_of<C::kTile>(at.len));
+            const unsigned rest = u - y * (unsigned)a.items, of = (unsigned)tiles_of<C::kTile>(at.len);
+            at.item = (int)(rest / of);
+            at.tile = (int)(rest - (unsigned)at.item * of);
         }
         const int n = (int)(end - u);
-        if (lane == 0 && u == split.cta(cta)) {      // the CTA's first tile
-            const unsigned long long x = u - at.tile;
-            int c = min((int)((float)x / (float)split.total * split.ctas), cta);
-            while (c > 0 && split.cta(c) > x) --c;
-            while (split.cta(c + 1) <= x) ++c;
-            from = c;
-        }
-        // copies: the lanes look up the blocks of 16 tiles at a time
-        Place ahead = at;
-        int issued = 0, looked = -1;
-        unsigned block = 0;
+        const int first_tile = at.tile;
+
+        // Copies.  The lanes look up the blocks of kAhead tiles at once, and those of the
+        // next before they are needed: with the ring's copies under way, a read from
+        // memory waits as long as they do.
+        constexpr int kAhead = 32 / C::kBlocks;
+        auto look_up = [&](const Place &p) {
+            const int nb = C::kBlocks * p.tile + lane, column = divided(nb, a.by_blocks);
+            int page = 0;
+            if (nb * kBlock < p.len) page = a.table[(long long)p.seq * a.columns + column];
+            return page;
+        };
+        Place ahead = at, after = at;                // of the tile to be asked for, of the lookup
+        int pages_after = look_up(at), issued = 0, looked = -kAhead;
+        unsigned block = 0;                          // this lane's, of the tiles from `looked` on
+        bool fresh = true;                           // the tile begins an item
+        auto advance = [&]() {                       // the lookup behind `after`
+            if (after.tile + kAhead < tiles_of<C::kTile>(after.len)) after.tile += kAhead;
+            else next_item(a, lens, after);
+            if (after.seq < a.B) pages_after = look_up(after);
+        };
         auto issue = [&](int slot) {
-            if (looked < 0 || ahead.tile >= looked + 32 / C::kBlocks) {
+            if (fresh || ahead.tile >= looked + kAhead) {
+                const bool known = pages_after >= 0 && pages_after < a.n_pages;
+                bad = bad || !known;
                 looked = ahead.tile;
                 const int nb = C::kBlocks * looked + lane;
-                block = 0;
-                if (nb * kBlock < ahead.len) {
-                    const int column = nb / a.blocks;
-                    int page = a.table[(long long)ahead.seq * a.columns + column];
-                    if (page < 0 || page >= a.n_pages) {
-                        bad = true;
-                        page = 0;
-                    }
-                    block = ((unsigned)page * a.Hk + ahead.item / a.groups) * a.blocks + (nb - column * a.blocks);
-                }
+                block = ((unsigned)(known ? pages_after : 0) * a.Hk + divided(ahead.item, a.by_groups)) * a.blocks +
+                        nb - divided(nb, a.by_blocks) * a.blocks;
+                advance();
             }
-            const unsigned from = __shfl_sync(0xffffffffu, block, C::kBlocks * (ahead.tile - looked) + lane % C::kBlocks);
+            const unsigned src = __shfl_sync(0xffffffffu, block, C::kBlocks * (ahead.tile - looked) + lane % C::kBlocks);
             const int there = min(C::kBlocks, (ahead.len - ahead.tile * C::kTile + kBlock - 1) / kBlock);
             if (lane == 0) tc::mbar_expect_tx(&bars[warp][slot], there * Layout<D>::kBytes);
             __syncwarp();
             if (lane < there)
                 tc::bulk_load(ring + slot * C::kStage + lane * Layout<D>::kBytes,
-                              a.pool + (unsigned long long)from * Layout<D>::kBytes, Layout<D>::kBytes,
+                              a.pool + (unsigned long long)src * Layout<D>::kBytes, Layout<D>::kBytes,
                               &bars[warp][slot]);
-            ++issued;
-            if (++ahead.tile == tiles_of<C::kTile>(ahead.len)) {
-                looked = -1;
-                if (issued < n) next_item(a, ahead);
-            }
-        };
-        for (int i = 0; i < C::kStages && issued < n; ++i) issue(i);
-
-        State<D, NT, F32> st;
-        int slot = 0, parity = 0;
-        for (int done = 0; done < n;) {
-            const int head = at.item / a.groups, group = at.item - head * a.groups;
-            const int stop = min(tiles_of<C::kTile>(at.len), at.tile + n - done), begin = at.tile;
-            st.template begin<T>(a, at.seq, head, group, at.len);
-            for (; at.tile < stop; ++at.tile, ++done) {
-                ok = tc::mbar_wait(&bars[warp][slot], parity) && !a.lost_wait;
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if ((at.tile + 1) * C::kTile <= st.full) st.template tile<false>(ring + slot * C::kStage, at.tile * C::kTile, at.len);
-                else st.template tile<true>(ring + slot * C::kStage, at.tile * C::kTile, at.len);
-                __syncwarp();
-                if (issued < n) issue(slot);
-                if (++slot == C::kStages) {
-                    slot = 0;
-                    parity ^= 1;
+            if (fresh) {                             // its query rows into L2
+                const int head = divided(ahead.item, a.by_groups), row = (ahead.item - head * a.groups) * C::kRows + lane;
+                if (lane < C::kRows && row < a.rows) {
+                    const T *q = query<T>(a, ahead.seq, head, row);
+#pragma unroll
+                    for (int i = 0; i < D * (int)sizeof(T); i += 128)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(q) + i));
                 }
             }
-            if (!ok) break;
-            const bool first = begin == 0, whole = stop == tiles_of<C::kTile>(at.len);
-            st.finish();
-            if (first && whole) {
-                st.template write<T>(a, at.seq, head, group);
-            } else if (done < n) {                   // closes an item that others began
-                st.put(mine_at + (2 + warp) * C::kPart);
-                if (lane == 0) parts[2 * warp] = {at.seq, at.item, false, true};
-            } else {
-                st.put(reinterpret_cast<float *>(ring));
-                if (lane == 0) parts[2 * warp + 1] = {at.seq, at.item, first, whole};
+            ++issued;
+            fresh = ++ahead.tile == tiles_of<C::kTile>(ahead.len);
+            if (fresh && issued < n) next_item(a, lens, ahead);
+        };
+
+        State<D, NT, F32> st;
+        int to = 0, slot = 0, parity = 0, begin = first_tile;
+        bool start = true, closed = false, back = false;
+        for (int step = 0; step < n + C::kStages - 1; ++step) {
+            if (step < n) {
+                issue(to);
+                if (++to == C::kStages) to = 0;
             }
-            if (done < n) next_item(a, at);
+            const int done = step - (C::kStages - 1);
+            if (done < 0) continue;
+            const int free_slot = slot + 1 == C::kStages ? 0 : slot + 1;
+            if (done + 1 == n && closed) {
+                // the part that the warp closed comes back, into a stage that is free: its
+                // way to memory and back runs under the last tile
+                if (lane == 0) {
+                    tc::mbar_expect_tx(&bars[warp][free_slot], a.part_size * 4);
+                    tc::bulk_load(ring + free_slot * C::kStage, mine_at + (2 + warp) * a.part_size, a.part_size * 4,
+                                  &bars[warp][free_slot]);
+                    parts[2 * warp].at = warp * C::kRing + free_slot * C::kStage;
+                }
+                back = true;
+                __syncwarp();
+            }
+            ok = tc::mbar_wait(&bars[warp][slot], parity) && !a.lost_wait;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const unsigned char *stage = ring + slot * C::kStage;
+            const int head = divided(at.item, a.by_groups), group = at.item - head * a.groups;
+            if (start) st.template begin<T>(a, at.seq, head, group, at.len);
+            start = false;
+#pragma unroll 1
+            for (int i = 0; i < C::kTile; i += C::kKeys) {
+                const int key0 = at.tile * C::kTile + i;
+                const unsigned char *keys = stage + i / kBlock * Layout<D>::kBytes;
+                if (key0 + C::kKeys <= st.full) st.template keys<false>(keys, key0, at.len);
+                else if (key0 < at.len) st.template keys<true>(keys, key0, at.len);
+            }
+            __syncwarp();
+            if (++slot == C::kStages) {
+                slot = 0;
+                parity ^= 1;
+            }
+            const bool whole = ++at.tile == tiles_of<C::kTile>(at.len), last = done + 1 == n;
+            if (!whole && !last) continue;
+            // the end of the warp's part of an item
+            st.finish();
+            if (begin == 0 && whole) {
+                st.template write<T>(a, at.seq, head, group);
+            } else {
+                // (the last tile's stage is free)
+                const int last_slot = slot == 0 ? C::kStages - 1 : slot - 1;
+                st.put(a, last ? reinterpret_cast<float *>(ring + last_slot * C::kStage)
+                               : mine_at + (2 + warp) * a.part_size);
+                if (lane == 0)
+                    parts[2 * warp + last] = {at.seq, at.item, begin == 0, whole,
+                                              warp * C::kRing + last_slot * C::kStage};
+                if (!last) {
+                    closed = true;
+                    tc::fence_proxy_async_global();
+                    __syncwarp();
+                }
+            }
+            if (last) break;
+            next_item(a, lens, at);
+            begin = 0;
+            start = true;
+        }
+        // the stage that the closed part came back to: behind the last tile's
+        const int free_slot = !back ? -1 : ok ? slot : (slot + 1 == C::kStages ? 0 : slot + 1);
+        if (back) {
+            const int turns = n > free_slot ? (n - 1 - free_slot) / C::kStages + 1 : 0;
+            ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[warp][free_slot], turns & 1)) && ok;
         }
         if (!ok) {
             // what was asked for arrives by itself; the ring must outlive it
-            for (int i = 0; i < C::kStages; ++i) {
-                const int left = issued < C::kStages ? issued : C::kStages;
-                if (i < left) {
-                    // the last issue of slot i: the phase that completes last
-                    const int turns = (issued - 1 - i) / C::kStages;
-                    tc::mbar_wait(&bars[warp][i], turns & 1);
-                }
-            }
+            for (int i = 0; i < C::kStages && i < issued; ++i)
+                if (i != free_slot)
+                    tc::mbar_wait(&bars[warp][i], (issued - 1 - i) / C::kStages & 1);    // its last phase
             if (lane == 0) atomicMax(&trouble, (unsigned)kDevTimeout);
         }
         if (bad) atomicMax(&trouble, (unsigned)kDevBadTable);
+        if (lane == 0 && u == cta0) {                // the CTA's first tile
+            const unsigned x = u - first_tile;
+            int c = min((int)((float)x / (float)split.total * split.ctas), cta);
+            while (c > 0 && split.cta(c) > x) --c;
+            while (split.cta(c + 1) <= x) ++c;
+            from = c;
+        }
     }
     __syncthreads();
 
@@ -710,7 +777,7 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
     // looks at part i; parts of an item follow each other.
     {
         constexpr int N = D / 32;
-        Part x{-1, 0, false, false};
+        Part x{-1, 0, false, false, 0};
         if (lane < 2 * C::kWarps) x = parts[lane];
         const unsigned all = __ballot_sync(0xffffffffu, x.seq >= 0);
         const unsigned lower = all & ((1u << lane) - 1);
@@ -727,34 +794,44 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
             const int seq = __shfl_sync(0xffffffffu, x.seq, a0), item = __shfl_sync(0xffffffffu, x.item, a0);
             const bool first = __shfl_sync(0xffffffffu, (int)x.first, a0);
             const bool whole = __shfl_sync(0xffffffffu, (int)x.end, 31 - __clz(members));
-            const int head = item / a.groups, group = item - head * a.groups;
+            const int head = divided(item, a.by_groups), group = item - head * a.groups;
             const int rows = min(C::kRows, a.rows - group * C::kRows);
-            float *out = mine_at + (first ? 1 : 0) * C::kPart;
-            const float *part = lane & 1 ? reinterpret_cast<const float *>(smem + lane / 2 * C::kRing)
-                                         : mine_at + (2 + lane / 2) * C::kPart;
+            const int pr = a.part_rows;
+            float *out = mine_at + (first ? 1 : 0) * a.part_size;
+            const float *part = reinterpret_cast<const float *>(smem + x.at);
             const bool here = members >> lane & 1;
             for (; turn < rows; turn += C::kWarps) {
-                const float m = here ? part[C::kRows * D + turn] : 0.f,
-                            t = here ? part[C::kRows * D + C::kRows + turn] : 0.f;
-                float base, l, v[N] = {};
-                const float w = join_weights(here, m, t, base, l);
-                for (unsigned left = members; left; left &= left - 1) {
-                    const int k = __ffs(left) - 1;
-                    const float *p = k & 1 ? reinterpret_cast<const float *>(smem + k / 2 * C::kRing)
-                                           : mine_at + (2 + k / 2) * C::kPart;
-                    const float f = __shfl_sync(0xffffffffu, w, k);
-                    float y[N];
-                    load_row(p + turn * D + N * lane, y);
+                const float m = here ? part[pr * D + turn] : 0.f, t = here ? part[pr * D + pr + turn] : 0.f;
+                float base, l, v[N] = {}, w = 0.f;
+                bool weighed = false;
+                for (unsigned left = members; left;) {           // four parts at once
+                    int k[4];
+                    float y[4][N];
 #pragma unroll
-                    for (int i = 0; i < N; ++i) v[i] = fmaf(f, y[i], v[i]);
+                    for (int j = 0; j < 4; ++j) {
+                        k[j] = left ? __ffs(left) - 1 : -1;
+                        left &= left - 1;
+                        const int from_k = __shfl_sync(0xffffffffu, x.at, max(k[j], 0));
+                        if (k[j] >= 0)
+                            load_row(reinterpret_cast<const float *>(smem + from_k) + turn * D + N * lane, y[j]);
+                    }
+                    if (!weighed) w = join_weights(here, m, t, base, l);
+                    weighed = true;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (k[j] < 0) continue;
+                        const float f = __shfl_sync(0xffffffffu, w, k[j]);
+#pragma unroll
+                        for (int i = 0; i < N; ++i) v[i] = fmaf(f, y[j][i], v[i]);
+                    }
                 }
                 if (first && whole) {
                     write_row<T, D>(a, out_row(a, seq, head, group * C::kRows + turn), v, base, l);
                 } else {
                     store_row(out + turn * D + N * lane, v);
                     if (lane == 0) {
-                        out[C::kRows * D + turn] = base;
-                        out[C::kRows * D + C::kRows + turn] = l;
+                        out[pr * D + turn] = base;
+                        out[pr * D + pr + turn] = l;
                     }
                 }
             }
@@ -768,7 +845,7 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
 
     // rows of empty caches
     for (int b = cta; b < a.B; b += gridDim.x) {
-        if (length(a, b) > 0) continue;
+        if (length(a, lens, b) > 0) continue;
         const long long row0 = (long long)b * a.Tq * a.Hq;
         const long long n = (long long)a.Tq * a.Hq;
         for (long long i = tid; i < n * (D / 4); i += C::kThreads) {
@@ -799,16 +876,16 @@ __global__ void __launch_bounds__(512) kv4_join_kernel(const __grid_constant__ A
         if (lane == 0) *a.status = x;
     }
     if (own.seq < 0) return;
-    const int head = own.item / a.groups, group = own.item - head * a.groups;
+    const int head = divided(own.item, a.by_groups), group = own.item - head * a.groups;
     const bool there = group * C::kRows + n < a.rows;
     // parts: of its first CTA the last item's, of the others the first item's
     const int count = (int)blockIdx.x - own.from + 1;
     float base = -INFINITY, l = 0.f, v[N] = {};
     for (int k0 = 32 * sub; k0 < count && there; k0 += 32 * kPer) {
         const int k = k0 + lane, c = own.from + k;
-        const float *part = a.part + ((size_t)min(c, (int)blockIdx.x) * (2 + C::kWarps) + (k == 0)) * C::kPart;
+        const float *part = a.part + ((size_t)min(c, (int)blockIdx.x) * (2 + C::kWarps) + (k == 0)) * a.part_size;
         const bool here = k < count;
-        const float m = part[C::kRows * D + n], sum = part[C::kRows * D + C::kRows + n];
+        const float m = part[a.part_rows * D + n], sum = part[a.part_rows * (D + 1) + n];
         float top, t;
         const float w = join_weights(here, m, sum, top, t);
         const float both = fmaxf(base, top);
@@ -821,7 +898,7 @@ __global__ void __launch_bounds__(512) kv4_join_kernel(const __grid_constant__ A
 #pragma unroll 4
         for (int j = 0; j < most; ++j) {
             const float f = __shfl_sync(0xffffffffu, w, j) * f1;
-            const float *p = a.part + ((size_t)(own.from + k0 + j) * (2 + C::kWarps) + (k0 + j == 0)) * C::kPart;
+            const float *p = a.part + ((size_t)(own.from + k0 + j) * (2 + C::kWarps) + (k0 + j == 0)) * a.part_size;
             float y[N];
             load_row(p + n * D + N * lane, y);
 #pragma unroll
@@ -876,23 +953,37 @@ int sm_count() {
     return n;
 }
 
+Divisor divisor(int d) {
+    int l = 0;
+    while ((1LL << l) < d) ++l;
+    return {(unsigned)(((1ULL << 32) * ((1ULL << l) - d)) / d + 1), l < 1 ? l : 1, l < 1 ? 0 : l - 1};
+}
+
 struct Plan {
-    int nt, ctas;
+    int ctas, rows, groups, part_rows, part_size;
     size_t cta_status, owners, part, bytes;
+    cudaError_t (*run)(const Args &, cudaStream_t);
 };
+template <int D, int NT, bool F32>
+cudaError_t launch(const Args &a, cudaStream_t s);
+
 template <int D, int NT, bool F32>
 void sizes(Plan &p) {
     using C = Config<D, NT, F32>;
-    p.nt = NT;
-    p.bytes = up256(p.part + (size_t)p.ctas * (2 + C::kWarps) * C::kPart * sizeof(float));
+    p.run = launch<D, NT, F32>;
+    p.groups = (p.rows + C::kRows - 1) / C::kRows;
+    p.part_rows = p.rows < C::kRows ? p.rows : C::kRows;
+    p.part_size = (p.part_rows * (D + 2) + 3) & ~3;
+    p.bytes = up256(p.part + (size_t)p.ctas * (2 + C::kWarps) * p.part_size * sizeof(float));
 }
 Plan plan_of(const Kv4Attn &p) {
     Plan x{};
     x.ctas = sm_count();
+    x.rows = p.Hq / p.Hk * p.Tq;
     x.cta_status = kWsHeader;
     x.owners = up256(x.cta_status + x.ctas * sizeof(unsigned));
     x.part = up256(x.owners + x.ctas * sizeof(Owner));
-    const bool two = (long long)p.Hq / p.Hk * p.Tq > 8;
+    const bool two = x.rows > 8;
     if (p.d == 64) {
         if (p.dtype == 0) sizes<64, 1, true>(x);
         else two ? sizes<64, 2, false>(x) : sizes<64, 1, false>(x);
@@ -931,11 +1022,10 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
 size_t kv4_attn_workspace_bytes(const Kv4Attn &p) { return plan_of(p).bytes; }
 
 bool kv4_attn_too_large(const Kv4Attn &p) {
-    const long long tiles = (long long)p.B * ((long long)p.columns * p.page / 32 + 1);
     const long long rows = (long long)p.B * p.Tq * p.Hq;
-    const long long blocks = (long long)p.n_pages * p.Hk * (p.page / kBlock);
-    return tiles > INT32_MAX || rows > INT32_MAX || blocks > UINT32_MAX ||
-           (long long)p.columns * p.page > INT32_MAX;
+    const long long tiles = (long long)p.B * ((long long)p.columns * p.page / 64 + 1);
+    const long long items = (long long)p.Hk * ((p.Hq / p.Hk * (long long)p.Tq + 7) / 8);
+    return rows > INT32_MAX || items > INT32_MAX || (items > 0 && tiles > INT32_MAX / items);
 }
 
 cudaError_t launch_kv4_attn(const Kv4Attn &p, cudaStream_t s) {
@@ -944,11 +1034,14 @@ cudaError_t launch_kv4_attn(const Kv4Attn &p, cudaStream_t s) {
     Args a{};
     a.q = p.q; a.q_stride = p.q_stride; a.pool = static_cast<const unsigned char *>(p.pool);
     a.table = p.table; a.lens = p.lens; a.o = p.o; a.lse = p.lse;
-    a.B = p.B; a.Tq = p.Tq; a.Hq = p.Hq; a.Hk = p.Hk; a.G = p.Hq / p.Hk;
+    a.B = p.B; a.Tq = p.Tq; a.Hq = p.Hq; a.Hk = p.Hk; a.G = p.Hq / p.Hk; a.d = p.d;
     a.blocks = p.page / kBlock; a.n_pages = p.n_pages; a.columns = p.columns;
-    a.rows = a.G * p.Tq;
-    a.groups = (a.rows + 8 * x.nt - 1) / (8 * x.nt);
-    a.items = p.Hk * a.groups;
+    a.rows = x.rows;
+    a.groups = x.groups;
+    a.items = p.Hk * x.groups;
+    a.by_G = divisor(a.G); a.by_groups = divisor(a.groups); a.by_items = divisor(a.items);
+    a.by_blocks = divisor(a.blocks);
+    a.part_rows = x.part_rows; a.part_size = x.part_size;
     a.scale_log2 = p.scale * p.k_unit * kLog2e;
     a.v_unit = p.v_unit;
     a.status = static_cast<unsigned *>(p.ws);
@@ -964,9 +1057,7 @@ cudaError_t launch_kv4_attn(const Kv4Attn &p, cudaStream_t s) {
         note_launch();
         return cudaGetLastError();
     }
-    if (p.dtype == 0) return p.d == 64 ? launch<64, 1, true>(a, s) : launch<128, 1, true>(a, s);
-    if (p.d == 64) return x.nt == 2 ? launch<64, 2, false>(a, s) : launch<64, 1, false>(a, s);
-    return x.nt == 2 ? launch<128, 2, false>(a, s) : launch<128, 1, false>(a, s);
+    return x.run(a, s);
 }
 
 }  // namespace kla
