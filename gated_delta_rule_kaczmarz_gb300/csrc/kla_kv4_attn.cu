@@ -930,6 +930,18 @@ __global__ void __launch_bounds__(512) kv4_join_kernel(const __grid_constant__ A
     if (there) write_row<T, D>(a, out_row(a, own.seq, head, group * C::kRows + n), v, base, l);
 }
 
+// The unpacked path's check of the table, after the attention that writes the status word.
+__global__ void kv4_check_kernel(const int *table, const int *lens, int columns, int page, int n_pages,
+                                 unsigned *status) {
+    const int b = blockIdx.x;
+    const long long most = (long long)columns * page;
+    const int len = lens[b], held = (int)((len < 0 ? 0 : len < most ? len : most) + page - 1) / page;
+    for (int c = threadIdx.x; c < held; c += blockDim.x) {
+        const int x = table[(long long)b * columns + c];
+        if (x < 0 || x >= n_pages) atomicMax(status, (unsigned)kDevBadTable);
+    }
+}
+
 // Without any key: zeros, from a launch that has no table to read.
 __global__ void kv4_no_keys_kernel(uint4 *o, long long n, float *lse, long long rows, unsigned *status) {
     const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
@@ -957,6 +969,35 @@ Divisor divisor(int d) {
     int l = 0;
     while ((1LL << l) < d) ++l;
     return {(unsigned)(((1ULL << 32) * ((1ULL << l) - d)) / d + 1), l < 1 ? l : 1, l < 1 ? 0 : l - 1};
+}
+
+// Many query rows: the cache's rows are unpacked into the workspace once and go
+// through the attention of dense rows, whose tcgen05 products take 128 rows (bf16;
+// in fp32 that runs on the CUDA cores, 4 to 8 times as long as here).  Both, in us,
+// with 16 + 4 heads of 128 over 32768 keys, by tokens: 24 42 and 45, 32 51 and 46, 64
+// 83 and 55, 512 559 and 163; 16 + 2 of 64 over 4 caches of 16384: 8 26 and 32, 16 37 and
+// 35, 64 107 and 59; 8 + 8 of 64 over 1024 keys: 128 14 and 17, 512 22 and 22.
+constexpr int kUnpackRows = 128;
+bool unpacked(const Kv4Attn &p, AttnProblem &x, Kv4Rows &r) {
+    if (p.dtype != 1 || (long long)p.Hq / p.Hk * p.Tq < kUnpackRows) return false;
+    const long long keys = (long long)p.B * p.columns * p.page;
+    if (keys > INT32_MAX) return false;
+    x.q = p.q; x.q_stride = p.q_stride; x.out = p.o; x.lse = p.lse; x.k_lens = p.lens;
+    x.k_stride = x.v_stride = (long long)p.Hk * p.d;
+    x.n_seq = p.B; x.Tq = p.Tq; x.Tk = p.columns * p.page; x.total_q = p.B * p.Tq; x.total_k = (int)keys;
+    x.Hq = p.Hq; x.Hk = p.Hk; x.d = p.d; x.dtype = p.dtype; x.scale = p.scale;
+    r.k_stride = x.k_stride; r.v_stride = x.v_stride; r.from_start = true;
+    r.pool = const_cast<void *>(p.pool); r.table = p.table; r.lens = p.lens; r.B = p.B; r.T = x.Tk;
+    r.Hk = p.Hk; r.d = p.d; r.page = p.page; r.n_pages = p.n_pages; r.columns = p.columns;
+    r.dtype = p.dtype; r.k_unit = p.k_unit; r.v_unit = p.v_unit;
+    return !attn_too_large(x) && !kv4_rows_too_large(r);
+}
+// Keys' and values' places behind the attention's workspace.
+size_t unpacked_bytes(const AttnProblem &x, size_t &k, size_t &v) {
+    const size_t rows = up256((size_t)x.total_k * x.Hk * x.d * (x.dtype == 1 ? 2 : 4));
+    k = up256(attn_fwd_workspace_bytes(x));
+    v = k + rows;
+    return v + rows;
 }
 
 struct Plan {
@@ -1019,7 +1060,12 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
 
 }  // namespace
 
-size_t kv4_attn_workspace_bytes(const Kv4Attn &p) { return plan_of(p).bytes; }
+size_t kv4_attn_workspace_bytes(const Kv4Attn &p) {
+    AttnProblem x{};
+    Kv4Rows r{};
+    size_t k, v;
+    return p.columns > 0 && unpacked(p, x, r) ? unpacked_bytes(x, k, v) : plan_of(p).bytes;
+}
 
 bool kv4_attn_too_large(const Kv4Attn &p) {
     const long long rows = (long long)p.B * p.Tq * p.Hq;
@@ -1029,8 +1075,30 @@ bool kv4_attn_too_large(const Kv4Attn &p) {
 }
 
 cudaError_t launch_kv4_attn(const Kv4Attn &p, cudaStream_t s) {
-    const Plan x = plan_of(p);
     unsigned char *ws = static_cast<unsigned char *>(p.ws);
+    if (p.n_pages == 0 || p.columns == 0) {
+        const long long rows = (long long)p.B * p.Tq * p.Hq, n = rows * p.d * (p.dtype == 1 ? 2 : 4) / 16;
+        kv4_no_keys_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(static_cast<uint4 *>(p.o), n, p.lse, rows,
+                                                                      static_cast<unsigned *>(p.ws));
+        note_launch();
+        return cudaGetLastError();
+    }
+    AttnProblem dense{};
+    Kv4Rows rows{};
+    if (unpacked(p, dense, rows)) {
+        size_t k, v;
+        unpacked_bytes(dense, k, v);
+        dense.ws = p.ws;
+        dense.k = rows.k_out = ws + k;
+        dense.v = rows.v_out = ws + v;
+        cudaError_t e = launch_kv4_rows(rows, true, s);
+        if (e != cudaSuccess || (e = launch_attn_fwd(dense, s)) != cudaSuccess) return e;
+        kv4_check_kernel<<<p.B, 256, 0, s>>>(p.table, p.lens, p.columns, p.page, p.n_pages,
+                                             static_cast<unsigned *>(p.ws));
+        note_launch();
+        return cudaGetLastError();
+    }
+    const Plan x = plan_of(p);
     Args a{};
     a.q = p.q; a.q_stride = p.q_stride; a.pool = static_cast<const unsigned char *>(p.pool);
     a.table = p.table; a.lens = p.lens; a.o = p.o; a.lse = p.lse;
@@ -1051,12 +1119,6 @@ cudaError_t launch_kv4_attn(const Kv4Attn &p, cudaStream_t s) {
     a.ctas = x.ctas;
     // test hook: every warp takes its first wait for one that ran out
     a.lost_wait = std::getenv("KLA_TEST_LOST_WAIT") != nullptr;
-    if (p.n_pages == 0 || p.columns == 0) {
-        const long long rows = (long long)p.B * p.Tq * p.Hq, n = rows * p.d * (p.dtype == 1 ? 2 : 4) / 16;
-        kv4_no_keys_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(static_cast<uint4 *>(p.o), n, p.lse, rows, a.status);
-        note_launch();
-        return cudaGetLastError();
-    }
     return x.run(a, s);
 }
 

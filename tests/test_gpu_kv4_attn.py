@@ -53,6 +53,11 @@ SIZES = [
     ([90, 200], 7, 12, 2, 128, 64),               # 42 rows
     ([75], 75, 4, 2, 64, 16),                     # a whole prompt
     ([0, 0], 2, 4, 2, 128, 16),
+    # many rows to a key head: 128 and more go another way in bf16
+    ([130, 0, 300, 5], 40, 8, 2, 128, 16),
+    ([63, 64], 64, 4, 2, 64, 48),
+    ([200], 127, 3, 3, 64, 32),
+    ([70, 90], 4, 128, 2, 64, 16),
 ]
 
 
@@ -159,7 +164,15 @@ def test_shared_pages():
 
 
 def test_bad_entries_are_reported():
-    q, (pool, table, lens), refs, how = _case([60, 40], 1, 4, 2, 128, 16, BF16)
+    _bad_entries(1)
+
+
+def test_bad_entries_are_reported_for_many_rows():
+    _bad_entries(64)
+
+
+def _bad_entries(Tq):
+    q, (pool, table, lens), refs, how = _case([60, 40], Tq, 4, 2, 128, 16, BF16)
     for bad in (-1, pool.shape[0], 1 << 30):
         t = table.clone()
         t[1, 1] = bad
