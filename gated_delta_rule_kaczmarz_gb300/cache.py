@@ -181,7 +181,8 @@ def _layers(pool, n_pages):
                          f"{tuple(pool.shape)}")
     if not pool.is_contiguous():
         raise ValueError("pool must be contiguous")
-    return pool.data_ptr(), pool.shape[0], pool[:1, :1].numel() * pool.element_size()
+    layers, n = pool.shape[:2]
+    return pool.data_ptr(), layers, pool.numel() // max(1, layers * n) * pool.element_size()
 
 
 def _pages_call(fn, dev, like, args, sizes, workspace, check):

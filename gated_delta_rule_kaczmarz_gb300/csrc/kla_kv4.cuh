@@ -59,5 +59,22 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
     return d;
 }
 
+// Quotients of numbers below 2^31 by one that a launch keeps (Granlund and
+// Montgomery, Division by invariant integers using multiplication, 1994):
+// n / d = (t + ((n - t) >> shift1)) >> shift2, t the high half of multiplier n.
+struct Divisor {
+    unsigned multiplier;
+    int shift1, shift2;
+};
+inline Divisor divisor(int d) {
+    int l = 0;
+    while ((1LL << l) < d) ++l;
+    return {(unsigned)(((1ULL << 32) * ((1ULL << l) - d)) / d + 1), l < 1 ? l : 1, l < 1 ? 0 : l - 1};
+}
+__device__ __forceinline__ int divided(int n, const Divisor &d) {
+    const unsigned t = __umulhi(d.multiplier, (unsigned)n);
+    return (int)((t + (((unsigned)n - t) >> d.shift1)) >> d.shift2);
+}
+
 }  // namespace kv4
 }  // namespace kla

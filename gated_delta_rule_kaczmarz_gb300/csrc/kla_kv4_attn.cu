@@ -34,6 +34,9 @@ namespace kla {
 namespace {
 
 using kv4::kBlock;
+using kv4::divided;
+using kv4::Divisor;
+using kv4::divisor;
 using kv4::Layout;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
@@ -56,12 +59,6 @@ struct Config {
     static constexpr int kRing = kStages * kStage;               // of a warp
     static constexpr int kSmem = kWarps * kRing;
     static_assert(kStages >= 2 && kStage >= (kRows * (D + 2) + 3) * 4, "a part lies in a stage");
-};
-
-// n / d: (t + ((n - t) >> shift1)) >> shift2 with t the high half of multiplier n.
-struct Divisor {
-    unsigned multiplier;
-    int shift1, shift2;
 };
 
 // An item that began in CTA `from` and ends in this one: joined by the second kernel.
@@ -109,13 +106,6 @@ __device__ __forceinline__ Split split_of(const Args &a, unsigned tiles) {
     s.rest = s.total - s.each * (unsigned)s.ctas;
     return s;
 }
-// Quotients by numbers that a launch keeps (Granlund and Montgomery, Division by
-// invariant integers using multiplication, 1994).
-__device__ __forceinline__ int divided(int n, const Divisor &d) {
-    const unsigned t = __umulhi(d.multiplier, (unsigned)n);
-    return (int)((t + (((unsigned)n - t) >> d.shift1)) >> d.shift2);
-}
-
 __device__ __forceinline__ int length(const Args &a, int b) {
     const int n = a.lens[b], most = a.columns * a.blocks * kBlock;
     return n < 0 ? 0 : (n < most ? n : most);
@@ -963,12 +953,6 @@ int sm_count() {
     }
     if (dev < 64) known[dev].store(n);
     return n;
-}
-
-Divisor divisor(int d) {
-    int l = 0;
-    while ((1LL << l) < d) ++l;
-    return {(unsigned)(((1ULL << 32) * ((1ULL << l) - d)) / d + 1), l < 1 ? l : 1, l < 1 ? 0 : l - 1};
 }
 
 // Many query rows: the cache's rows are unpacked into the workspace once and go

@@ -5,8 +5,14 @@
 //
 // A thread takes 16 features of one head of a pair of tokens (an even position
 // and the next): the pair's values share bytes, so no byte has two writers, and
-// of a pair with one new token the other's codes are kept.  Bound by HBM for
-// prompts and by latency for single tokens.
+// of a pair with one new token the other's codes are kept.  Bound by HBM, the append
+// by the issue of its conversions too (0.68 of the slots): 306282 packed rows of 4 heads
+// of 128 in bf16 133 and 122 us, 0.89 and 0.97 of measured HBM bandwidth.  A thread
+// that goes on to 2, 4 or 8 pairs goes through the three reads before the first
+// (sequence, length, page) once, but keeps fewer under way: the read 172, 183, 176
+// where one pair took 164.  Rows are read and, where they lie so, written 32 bytes a
+// thread at once (the read 164 -> 122).  Single tokens are bound by latency: 256 of 4
+// heads of 128 2.5 us each way.
 #include <cuda_bf16.h>
 
 #include "kla_kv4.cuh"
@@ -26,29 +32,31 @@ struct Span {
 
 struct Work {
     Kv4Rows p;
-    long long slots;     // pairs of positions, all sequences'
+    int slots;           // pairs of positions, all sequences'
     int per_seq;         // pairs of a sequence, not packed
+    kv4::Divisor by_each, by_seq, by_page;
 };
 
-// Sequence and pair of a slot; false: a table that does not hold.
-__device__ __forceinline__ bool span_of(const Work &w, long long slot, int &seq, int &pair, Span &s) {
+// Sequence and pair of a slot; false: a table that does not hold.  n rows lie in
+// n / 2 + 1 pairs at most, wherever they begin.
+__device__ __forceinline__ bool span_of(const Work &w, int slot, int &seq, int &pair, Span &s) {
     const Kv4Rows &p = w.p;
     if (p.cu) {
         // sequence n's slots begin at cu[n] / 2 + n
         int lo = 0, hi = p.B - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
-            if ((long long)(p.cu[mid] >> 1) + mid <= slot) lo = mid; else hi = mid - 1;
+            if ((p.cu[mid] >> 1) + mid <= slot) lo = mid; else hi = mid - 1;
         }
         seq = lo;
         const int a = p.cu[lo], e = p.cu[lo + 1];
-        pair = (int)(slot - (a >> 1) - lo);
+        pair = slot - (a >> 1) - lo;
         s.row0 = a;
         s.rows = e - a;
-        if (a < 0 || e < a || e > p.total) return false;
+        if (a < 0 || e < a || e > p.total || pair < 0) return false;
     } else {
-        seq = (int)(slot / w.per_seq);
-        pair = (int)(slot - (long long)seq * w.per_seq);
+        seq = kv4::divided(slot, w.by_seq);
+        pair = slot - seq * w.per_seq;
         s.row0 = (long long)seq * p.T;
         s.rows = p.T;
     }
@@ -66,82 +74,107 @@ __device__ __forceinline__ bool span_of(const Work &w, long long slot, int &seq,
 
 // The block of a position, or nullptr where the table names no page of the pool.
 template <int D>
-__device__ __forceinline__ unsigned char *block_of(const Kv4Rows &p, int seq, int pos, int head) {
-    const int column = pos / p.page, in = pos - column * p.page;
+__device__ __forceinline__ unsigned char *block_of(const Work &w, int seq, int pos, int head) {
+    const Kv4Rows &p = w.p;
+    const int column = kv4::divided(pos, w.by_page), in = pos - column * p.page;
     const int page = p.table[(long long)seq * p.columns + column];
     if (page < 0 || page >= p.n_pages) return nullptr;
     const long long block = ((long long)page * p.Hk + head) * (p.page / kv4::kBlock) + in / kv4::kBlock;
     return static_cast<unsigned char *>(p.pool) + block * Layout<D>::kBytes;
 }
 
-__device__ __forceinline__ void load16(const float *p, float (&x)[16]) {
+// 16 features as they lie in memory, and as fp32.
+template <typename T>
+struct Raw {
+    uint4 x[sizeof(T)];
+    __device__ __forceinline__ void load(const T *p, bool on) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = reinterpret_cast<const float4 *>(p)[i];
-        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+        for (int i = 0; i < (int)sizeof(T); ++i)
+            x[i] = on ? __ldcs(reinterpret_cast<const uint4 *>(p) + i) : make_uint4(0, 0, 0, 0);
     }
-}
-__device__ __forceinline__ void load16(const __nv_bfloat16 *p, float (&x)[16]) {
+    __device__ __forceinline__ void get(float (&y)[16]) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < (int)sizeof(T); ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-            x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            for (int j = 0; j < 4; ++j) {
+                if (sizeof(T) == 4) {
+                    y[4 * i + j] = __uint_as_float(w[j]);
+                } else {
+                    y[(8 * i + 2 * j) % 16] = __uint_as_float(w[j] << 16);
+                    y[(8 * i + 2 * j + 1) % 16] = __uint_as_float(w[j] & 0xffff0000u);
+                }
+            }
         }
+    }
+};
+// 32 bytes in one store where they lie on such a boundary (rows may begin on any of
+// 16), else in two.
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
+    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
 }
 __device__ __forceinline__ void store16(float *p, const float (&x)[16]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        reinterpret_cast<float4 *>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    for (int i = 0; i < 2; ++i) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(x[8 * i + j]);
+        store32(p + 8 * i, w);
+    }
 }
 __device__ __forceinline__ void store16(__nv_bfloat16 *p, const float (&x)[16]) {
+    uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(x[8 * i + 2 * j], x[8 * i + 2 * j + 1]);
-            w[j] = reinterpret_cast<const uint32_t &>(b);
-        }
-        reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int j = 0; j < 8; ++j) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+        w[j] = reinterpret_cast<const uint32_t &>(b);
     }
+    store32(p, w);
 }
 
-// x in units of its scale; returns the scale's code.  The scale's border cases
-// are decided by amax / 6 correctly rounded (a midpoint of e4m3 times 6 has at
-// most 8 bits, so no other quotient rounds to it).  x / scale is x times the
-// reciprocal, corrected once by the exact remainder, which leaves less than 2^-45
-// before the rounding; a quotient that is no border of e2m1 is at least 8/15 of a
-// step of fp32 from one (a border times a scale has 8 bits, so x is a step or more
-// from it, and a scale's significand is at most 15/8), so ties are ties.
-__device__ __forceinline__ unsigned scaled(float (&x)[16], float inv_unit) {
+// a / b, given r = 1 / b within 2^-22: the product, corrected once by its exact
+// remainder, which leaves less than 2^-44 before the rounding.
+__device__ __forceinline__ float quotient(float a, float b, float r) {
+    const float q = a * r;
+    return fmaf(fmaf(-q, b, a), r, q);
+}
+// x / unit in units of its scale; returns the scale's code (0, and what is not
+// finite: the codes have no meaning).  Such quotients decide border cases as exact
+// ones do: a midpoint of e4m3 times 6, and a border of e2m1 times a scale, have at
+// most 8 bits, so an fp32 that is not just that is a step or more away, and its
+// quotient by 6 at least 2/3, by a scale (significand at most 15/8) 8/15 of a step.
+__device__ __forceinline__ unsigned scaled(float (&x)[16], float unit, float inv_unit) {
     float top = 0.f;
-    bool fine = true;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        x[i] *= inv_unit;
-        top = fmaxf(top, fabsf(x[i]));
-        fine = fine && fabsf(x[i]) < INFINITY;
-    }
+    for (int i = 0; i < 16; ++i)            // a NaN stays
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(x[i])));
+    const bool fine = top < INFINITY;
+    top *= inv_unit;
     uint32_t code;
     asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\tcvt.u32.u16 %0, t;\n\t}"
-        : "=r"(code) : "f"(0.f), "f"(__fdiv_rn(top, 6.f)));
-    if (!fine) code = 0x7f;                                  // the block reads as NaN
+        : "=r"(code) : "f"(0.f), "f"(quotient(fminf(top, 8.f * 448.f), 6.f, 1.f / 6.f)));
+    if (!fine) return 0x7f;                 // the 16 read as NaN
     const uint32_t h = kv4::scales_to_half2(code);
-    const float s = __half2float(__ushort_as_half((unsigned short)h));
-    const bool none = !fine || s == 0.f;
-    const float r = none ? 0.f : __frcp_rn(s);
+    const float s = __half2float(__ushort_as_half((unsigned short)h)) * unit;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    if (top > 8.f * 448.f) {                // far beyond the largest code: the quotients stay finite
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float a = none ? 0.f : x[i], y = a * r;
-        x[i] = fmaf(fmaf(-y, s, a), r, y);
+        for (int i = 0; i < 16; ++i) x[i] = fminf(fmaxf(x[i], -8.f * s), 8.f * s);
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = quotient(x[i], s, r);
     return code;
 }
+// Whether a scale's codes are to be written as zeros.
+__device__ __forceinline__ bool no_codes(unsigned scale) { return scale == 0 || scale == 0x7f; }
 // Codes of four bytes: lo[i] in the low four bits of byte i, hi[i] in the high.
 __device__ __forceinline__ uint32_t codes(const float (&lo)[4], const float (&hi)[4]) {
     uint32_t w;
@@ -166,9 +199,8 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_constant__ Work w) {
     const Kv4Rows &p = w.p;
     check_table(p);
-    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const int each = p.Hk * (D / 16), unit = (int)(i % each), head = unit / (D / 16), f = unit % (D / 16);
-    const long long slot = i / each;
+    const int i = blockIdx.x * kThreads + threadIdx.x, each = p.Hk * (D / 16);
+    const int slot = kv4::divided(i, w.by_each), unit = i - slot * each, head = unit / (D / 16), f = unit % (D / 16);
     if (slot >= w.slots) return;
     int seq, pair;
     Span s;
@@ -177,60 +209,59 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_const
         return;
     }
     // the pair that holds the sequence's first new position, and those behind it
-    const int first = s.pos0 < 0 ? 0 : s.pos0, pos = (first & ~1) + 2 * pair;
-    const int end = s.pos0 + s.rows;
-    if (pos >= end) return;
-    const bool even = pos >= first, odd = pos + 1 < end;
-    if (!even && !odd) return;                      // no new rows behind an odd length
-    unsigned char *block = block_of<D>(p, seq, pos, head);
+    const int first = s.pos0 < 0 ? 0 : s.pos0, pos = (first & ~1) + 2 * pair, end = s.pos0 + s.rows;
+    const bool even = pos >= first && pos < end, odd = pos + 1 < end;
+    if (!even && !odd) return;
+    unsigned char *block = block_of<D>(w, seq, pos, head);
     if (!block) {
         if (p.status) *p.status = kDevBadTable;
         return;
     }
+    const long long at = head * D + f * 16;
     const int t = pos % kv4::kBlock;
     const long long row = s.row0 + (pos - s.pos0);
+    Raw<T> k[2], v[2];                           // all that is read is asked for at once
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+        k[z].load(static_cast<const T *>(p.k) + (row + z) * p.k_stride + at, z ? odd : even);
+        v[z].load(static_cast<const T *>(p.v) + (row + z) * p.v_stride + at, z ? odd : even);
+    }
     float x[2][16];
     unsigned code[2];
-    // keys
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
         if (!(z ? odd : even)) continue;
-        load16(static_cast<const T *>(p.k) + (row + z) * p.k_stride + head * D + f * 16, x[z]);
-    }
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-        if (!(z ? odd : even)) continue;
-        code[z] = scaled(x[z], p.k_inv);
+        k[z].get(x[0]);
+        const unsigned scale = scaled(x[0], p.k_unit, p.k_inv);
         uint32_t c[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            c[j] = codes({x[z][8 * j], x[z][8 * j + 2], x[z][8 * j + 4], x[z][8 * j + 6]},
-                         {x[z][8 * j + 1], x[z][8 * j + 3], x[z][8 * j + 5], x[z][8 * j + 7]});
+            c[j] = codes({x[0][8 * j], x[0][8 * j + 2], x[0][8 * j + 4], x[0][8 * j + 6]},
+                         {x[0][8 * j + 1], x[0][8 * j + 3], x[0][8 * j + 5], x[0][8 * j + 7]});
+        if (no_codes(scale)) c[0] = c[1] = 0;
         *reinterpret_cast<uint2 *>(block + (t + z) * (D / 2) + 8 * f) = make_uint2(c[0], c[1]);
-        block[Layout<D>::kKs + (t + z) * (D / 16) + f] = (unsigned char)code[z];
+        block[Layout<D>::kKs + (t + z) * (D / 16) + f] = (unsigned char)scale;
     }
-    // values
+    // values: of a token that is not there zeros
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
-        if (z ? odd : even) {
-            load16(static_cast<const T *>(p.v) + (row + z) * p.v_stride + head * D + f * 16, x[z]);
-            code[z] = scaled(x[z], p.v_inv);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) x[z][j] = 0.f;
-        }
+        v[z].get(x[z]);
+        code[z] = scaled(x[z], p.v_unit, p.v_inv);
     }
     uint32_t c[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         c[j] = codes({x[0][4 * j], x[0][4 * j + 1], x[0][4 * j + 2], x[0][4 * j + 3]},
                      {x[1][4 * j], x[1][4 * j + 1], x[1][4 * j + 2], x[1][4 * j + 3]});
+    const uint32_t mask = (no_codes(code[0]) ? 0u : 0x0f0f0f0fu) | (no_codes(code[1]) ? 0u : 0xf0f0f0f0u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] &= mask;
     uint4 *to = reinterpret_cast<uint4 *>(block + Layout<D>::kV + (t / 2) * D + 16 * f);
     unsigned char *vs = block + Layout<D>::kVs + f * kv4::kBlock + t;
     if (even && odd) {
         *to = make_uint4(c[0], c[1], c[2], c[3]);
         *reinterpret_cast<unsigned short *>(vs) = (unsigned short)(code[0] | code[1] << 8);
-    } else {                            // the other token's codes stay
+    } else {                        // the other token's codes stay
         const uint32_t keep = even ? 0xf0f0f0f0u : 0x0f0f0f0fu;
         const uint4 old = *to;
         *to = make_uint4((old.x & keep) | (c[0] & ~keep), (old.y & keep) | (c[1] & ~keep),
@@ -249,9 +280,8 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constant__ Work w) {
     const Kv4Rows &p = w.p;
     check_table(p);
-    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const int each = p.Hk * (D / 16), unit = (int)(i % each), head = unit / (D / 16), f = unit % (D / 16);
-    const long long slot = i / each;
+    const int i = blockIdx.x * kThreads + threadIdx.x, each = p.Hk * (D / 16);
+    const int slot = kv4::divided(i, w.by_each), unit = i - slot * each, head = unit / (D / 16), f = unit % (D / 16);
     if (slot >= w.slots) return;
     int seq, pair;
     Span s;
@@ -265,10 +295,11 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
     const long long row = s.row0 + (pos - s.pos0);
     const unsigned char *block = nullptr;
     if (pos >= 0) {
-        block = block_of<D>(p, seq, pos, head);
+        block = block_of<D>(w, seq, pos, head);
         if (!block && p.status) *p.status = kDevBadTable;
     }
     const int t = pos & (kv4::kBlock - 1);
+    const long long at = head * D + f * 16;
     uint2 kc[2] = {};
     uint4 vc = {};
     uint32_t ks[2] = {}, vs = 0;
@@ -297,8 +328,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
                 x[z][8 * j + 2 * y + 1] = two.y * unit_of;
             }
         }
-        if (want[z])
-            store16(static_cast<T *>(p.k_out) + (row + z) * p.k_stride + head * D + f * 16, x[z]);
+        if (want[z]) store16(static_cast<T *>(p.k_out) + (row + z) * p.k_stride + at, x[z]);
     }
     const float2 units = to_float2(kv4::scales_to_half2(vs));
     const uint32_t c[4] = {vc.x, vc.y, vc.z, vc.w};
@@ -315,33 +345,32 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
     }
 #pragma unroll
     for (int z = 0; z < 2; ++z)
-        if (want[z])
-            store16(static_cast<T *>(p.v_out) + (row + z) * p.v_stride + head * D + f * 16, x[z]);
+        if (want[z]) store16(static_cast<T *>(p.v_out) + (row + z) * p.v_stride + at, x[z]);
 }
 
 template <typename T, int D>
 cudaError_t launch(const Work &w, bool read, cudaStream_t s) {
-    const long long n = w.slots * w.p.Hk * (D / 16), blocks = (n + kThreads - 1) / kThreads;
+    const long long n = (long long)w.slots * w.p.Hk * (D / 16), blocks = (n + kThreads - 1) / kThreads;
     if (read) kv4_read_kernel<T, D><<<(unsigned)blocks, kThreads, 0, s>>>(w);
     else kv4_append_kernel<T, D><<<(unsigned)blocks, kThreads, 0, s>>>(w);
     note_launch();
     return cudaGetLastError();
 }
 
-Work work_of(const Kv4Rows &p) {
-    Work w{p, 0, p.T / 2 + 1};
-    w.slots = p.cu ? (long long)p.total / 2 + p.B : (long long)p.B * w.per_seq;
-    return w;
+long long slots_of(const Kv4Rows &p) {
+    return p.cu ? (long long)p.total / 2 + p.B : (long long)p.B * (p.T / 2 + 1);
 }
 
 }  // namespace
 
 bool kv4_rows_too_large(const Kv4Rows &p) {
-    return work_of(p).slots * p.Hk * (p.d / 16) / kThreads >= INT32_MAX;
+    return slots_of(p) * p.Hk * (p.d / 16) + kThreads > INT32_MAX;
 }
 
 cudaError_t launch_kv4_rows(const Kv4Rows &p, bool read, cudaStream_t s) {
-    const Work w = work_of(p);
+    const int per_seq = p.T / 2 + 1;
+    const Work w{p, (int)slots_of(p), per_seq, kv4::divisor(p.Hk * (p.d / 16)), kv4::divisor(per_seq),
+                 kv4::divisor(p.page)};
     if (p.dtype == 1)
         return p.d == 64 ? launch<__nv_bfloat16, 64>(w, read, s) : launch<__nv_bfloat16, 128>(w, read, s);
     return p.d == 64 ? launch<float, 64>(w, read, s) : launch<float, 128>(w, read, s);

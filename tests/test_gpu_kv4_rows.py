@@ -129,6 +129,41 @@ def test_borders(dtype):
         assert torch.equal(got[0].cpu().double().nan_to_num(nan=1e9), want.nan_to_num(nan=1e9))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("unit", [2.0 ** -32, 2.0 ** 32])
+def test_units_at_their_ends(unit, dtype):
+    """Values that the unit takes out of fp32's range, and into its smallest numbers."""
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(2, 24, 1, 64, generator=g) * torch.exp2(
+        torch.randint(-140, 126, (2, 24, 1, 4), generator=g).float()).repeat_interleave(16, -1))
+    k, v = k.to(dtype), v.to(dtype)
+    k[3, 0, 5] = torch.finfo(dtype).max
+    k[4, 0, 5] = -torch.finfo(dtype).max
+    table = torch.tensor([[1, 0]]).int().cuda()
+    pool, lens = _cache.garbage(2, 1, 1, 18 * 64).cuda(), torch.tensor([24]).int().cuda()
+    kla.kla_kv4_append(k[None].cuda(), v[None].cuda(), pool, table, lens, k_unit=unit, v_unit=unit)
+    want = _cache.garbage(2, 1, 1, 18 * 64)
+    _put(want, table.cpu(), [24], [24], k, v, 16, (unit, unit))
+    assert torch.equal(pool.cpu(), want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_rows_on_boundaries_of_16_bytes(dtype):
+    n, hk, d, step = 21, 2, 64, 16 // torch.finfo(dtype).bits * 8
+    table, lens = _cache.book([n], 16, 2, 2, 1).cuda(), torch.tensor([n]).int().cuda()
+    pool = _cache.garbage(2, hk, 1, 18 * d).cuda()
+    k, v = _rows(n, hk, d, dtype, 2)
+    flat = torch.zeros(2, n * (hk * d + step) + step, dtype=dtype, device="cuda")
+    kk, vv = (x[step:].view(n, hk * d + step)[:, : hk * d].unflatten(1, (hk, d))[None] for x in flat)
+    kk.copy_(k[None])
+    vv.copy_(v[None])
+    kla.kla_kv4_append(kk, vv, pool, table, lens)
+    flat.zero_()
+    kla.kla_kv4_read(pool, table, lens, T=n, dtype=dtype, k_out=kk, v_out=vv)
+    assert torch.equal(kk[0].cpu().double(), _cache.rounded(k, 1.0))
+    assert torch.equal(vv[0].cpu().double(), _cache.rounded(v, 1.0))
+
+
 def test_steps_are_a_chunk():
     """Tokens appended one by one are the bytes of the chunk."""
     lens, hk, d, page = [37, 5], 2, 128, 16
