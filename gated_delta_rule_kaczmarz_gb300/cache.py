@@ -12,13 +12,36 @@ loop: ``kla_pages_grow`` makes room, ``kla_kv4_append`` writes the new rows,
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from .attention import (_at, _call, _dense, _given, _out, _refuse, _rows, _scale, _status,
-                        _type_code, _workspace)
+                        _type_code)
 from .binding import load
 
 _INT = torch.int32
+
+
+@functools.lru_cache(maxsize=1024)
+def _size(device, name, args):
+    """A workspace's size, asked for once: it goes by the device and the sizes alone."""
+    with torch.cuda.device(device):
+        return getattr(load(), name)(*args)
+
+
+def _workspace(device, name, args, like, workspace):
+    """The workspace that the library asks for, on like's device: it and its size in bytes."""
+    need = _size(device, name, args)
+    if workspace is None:
+        # kept by the caller's variable until the call is enqueued
+        return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None, need
+    have = workspace.numel() * workspace.element_size()
+    if workspace.get_device() != device:
+        raise ValueError(f"workspace must be on cuda:{device}, got {workspace.device}")
+    if have < need:
+        raise ValueError(f"workspace needs {need} bytes")
+    return workspace, have
 
 
 def kla_kv4_page_bytes(page, Hk, d) -> int:
@@ -46,26 +69,25 @@ def kla_kv4_pool(n_pages, page, Hk, d, layers=None, device="cuda"):
 
 
 def _book(table, lens, dev):
-    if table.dim() != 2:
-        raise ValueError(f"table must have shape [B, columns], got {tuple(table.shape)}")
-    return (_dense(table, "table", _INT, dev, table.shape),
-            _dense(lens, "lens", _INT, dev, table.shape[:1]))
+    size = table.shape
+    if dev < 0:
+        raise ValueError("table must be a CUDA tensor")
+    if len(size) != 2:
+        raise ValueError(f"table must have shape [B, columns], got {tuple(size)}")
+    return _dense(table, "table", _INT, dev, size), _dense(lens, "lens", _INT, dev, size[:1])
 
 
 def _pool(pool, dev, Hk=None, d=None):
     """The address of a layer's pool, and (Hk, d, page, n_pages)."""
-    if pool.dim() != 4:
+    shape = pool.shape
+    if len(shape) != 4:
         raise ValueError("pool must have shape [n_pages, Hk, page / 16, 18 d], got "
-                         f"{tuple(pool.shape)}")
-    n_pages, heads, blocks, size = pool.shape
+                         f"{tuple(shape)}")
+    n_pages, heads, blocks, size = shape
     d = size // 18 if d is None else d
     if heads != (heads if Hk is None else Hk) or size != 18 * d:
         _refuse(pool, "pool", torch.uint8, dev, (n_pages, Hk, blocks, 18 * d))
-    return _dense(pool, "pool", torch.uint8, dev, pool.shape), (heads, d, 16 * blocks, n_pages)
-
-
-def _lists(cu_seqlens, table, dev):
-    return _dense(cu_seqlens, "cu_seqlens", _INT, dev, (table.shape[0] + 1,))
+    return _dense(pool, "pool", torch.uint8, dev, shape), (heads, d, 16 * blocks, n_pages)
 
 
 def _word(workspace, check, like):
@@ -80,20 +102,21 @@ def _word(workspace, check, like):
 
 
 def _rows_call(fn, k, v, pool, table, lens, cu_seqlens, units, workspace, check):
-    dt, dev = _type_code(k), pool.get_device()
+    dt, dev, kind, shape = _type_code(k), pool.get_device(), k.dtype, k.shape
     packed = cu_seqlens is not None
-    if k.dim() != (3 if packed else 4):
+    if len(shape) != (3 if packed else 4):
         raise ValueError(f"k must have shape {'[total, Hk, d]' if packed else '[B, T, Hk, d]'}, "
-                         f"got {tuple(k.shape)}")
-    hk, d = k.shape[-2], k.shape[-1]
+                         f"got {tuple(shape)}")
+    T, hk, d = shape[-3:]
     at, (hk, d, page, n_pages) = _pool(pool, dev, hk, d)
-    book = _book(table, lens, dev)
+    rows, lengths = _book(table, lens, dev)
     B, columns = table.shape
-    shape = k.shape if packed else (B, k.shape[1], hk, d)
-    ks, vs = _rows(k, "k", k.dtype, dev, shape), _rows(v, "v", k.dtype, dev, shape)
-    cu = _lists(cu_seqlens, table, dev) if packed else None
+    if not packed:
+        shape = (B, T, hk, d)
+    ks, vs = _rows(k, "k", kind, dev, shape), _rows(v, "v", kind, dev, shape)
+    cu = _dense(cu_seqlens, "cu_seqlens", _INT, dev, (B + 1,)) if packed else None
     workspace, wsb = _word(workspace, check, pool)
-    _call(dev, fn, k.data_ptr(), ks, v.data_ptr(), vs, at, *book, cu, *units, B, shape[-3], hk, d,
+    _call(dev, fn, k.data_ptr(), ks, v.data_ptr(), vs, at, rows, lengths, cu, *units, B, T, hk, d,
           page, n_pages, columns, dt, _at(workspace), wsb)
     if check:
         _call(dev, _status, workspace, wsb)
@@ -150,24 +173,25 @@ def kla_kv4_attn(q, pool, table, lens, scale=None, k_unit=1.0, v_unit=1.0, o=Non
         with _given(stream, q):
             return kla_kv4_attn(q, pool, table, lens, scale, k_unit, v_unit, o, lse, return_lse,
                                 workspace, check_status=check_status)
-    if q.dim() != 4:
-        raise ValueError(f"q must have shape [B, Tq, Hq, d], got {tuple(q.shape)}")
-    dt, dev = _type_code(q), q.get_device()
-    B, Tq, hq, d = q.shape
-    qs = _rows(q, "q", q.dtype, dev, q.shape)
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError(f"q must have shape [B, Tq, Hq, d], got {tuple(shape)}")
+    dt, dev, kind = _type_code(q), q.get_device(), q.dtype
+    B, Tq, hq, d = shape
+    qs = _rows(q, "q", kind, dev, shape)
     at, (hk, d, page, n_pages) = _pool(pool, dev, d=d)
+    rows, lengths = _book(table, lens, dev)
     if table.shape[0] != B:
         raise ValueError(f"table must have {B} rows, got {tuple(table.shape)}")
-    book, columns = _book(table, lens, dev), table.shape[1]
-    o, out = _out(o, "o", q.shape, q.dtype, q)
+    columns = table.shape[1]
+    o, out = _out(o, "o", shape, kind, q)
     stats = None
     if return_lse or lse is not None:
-        lse, stats = _out(lse, "lse", (B, Tq, hq), torch.float32, q)
-    lib, sizes = load(), (B, Tq, hq, hk, d, page)
-    workspace, wsb = _workspace(dev, lib.kla_kv4_attn_workspace_size, (*sizes, columns, dt), q,
-                                workspace)
-    _call(dev, lib.kla_kv4_attn, q.data_ptr(), qs, at, *book, _scale(scale, d), k_unit, v_unit,
-          out, stats, *sizes, n_pages, columns, dt, _at(workspace), wsb)
+        lse, stats = _out(lse, "lse", shape[:3], torch.float32, q)
+    workspace, wsb = _workspace(dev, "kla_kv4_attn_workspace_size",
+                                (B, Tq, hq, hk, d, page, columns, dt), q, workspace)
+    _call(dev, load().kla_kv4_attn, q.data_ptr(), qs, at, rows, lengths, _scale(scale, d), k_unit,
+          v_unit, out, stats, B, Tq, hq, hk, d, page, n_pages, columns, dt, _at(workspace), wsb)
     if check_status:
         _call(dev, _status, workspace, wsb)
     return o, lse
@@ -187,7 +211,7 @@ def _layers(pool, n_pages):
 
 def _pages_call(fn, dev, like, args, sizes, workspace, check):
     """args up to the sizes (S, columns, n_pages, n) of the workspace's, then it."""
-    workspace, wsb = _workspace(dev, load().kla_pages_workspace_size, sizes, like, workspace)
+    workspace, wsb = _workspace(dev, "kla_pages_workspace_size", sizes, like, workspace)
     _call(dev, fn, *args, _at(workspace), wsb)
     if check:
         _call(dev, _status, workspace, wsb)
@@ -273,6 +297,8 @@ def kla_pages_copy(pool, src, dst, workspace=None, stream=None, check_status=Fal
         with _given(stream, pool):
             return kla_pages_copy(pool, src, dst, workspace, check_status=check_status)
     dev, n = pool.get_device(), dst.numel()
+    if dev < 0:
+        raise ValueError("pool must be a CUDA tensor")
     at, layers, size = _layers(pool, None)
     n_pages = pool.shape[1]
     of, to = _dense(src, "src", _INT, dev, (n,)), _dense(dst, "dst", _INT, dev, (n,))

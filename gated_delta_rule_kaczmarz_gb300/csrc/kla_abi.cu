@@ -1050,6 +1050,7 @@ int kla_pages_fork(int *table, int *lens, int *refs, const int *src, const int *
     if (n > 0 && !dst) return fail(KLA_ERR_INVALID_ARG, "dst must be non-null");
     if (!aligned4(src) || !aligned4(dst))
         return fail(KLA_ERR_INVALID_ARG, "src and dst must be 4-byte aligned");
+    if (kla::pages_too_many(S)) return fail(KLA_ERR_UNSUPPORTED, "at most 2^18 sequences (S=%d)", S);
     if ((long long)n * (columns + 1LL) > INT32_MAX)
         return fail(KLA_ERR_UNSUPPORTED, "problem too large (rows times columns must fit in int32)");
     if ((st = pages_call(p, n, workspace, workspace_bytes)) != KLA_OK) return st;

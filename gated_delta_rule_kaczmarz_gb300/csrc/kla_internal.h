@@ -181,6 +181,7 @@ struct Pages {
     void *ws;                       // the status word first
 };
 size_t pages_workspace_bytes(int S, int columns, int n_pages, int n);
+bool pages_too_many(int S);       // sequences of a fork
 cudaError_t launch_pages_fork(const Pages &p, cudaStream_t s);
 cudaError_t launch_pages_grow(const Pages &p, cudaStream_t s);
 cudaError_t launch_pages_compact(const Pages &p, cudaStream_t s);

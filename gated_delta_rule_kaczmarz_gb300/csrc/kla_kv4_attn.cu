@@ -831,7 +831,7 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
         }
         if (tid == 0) a.owners[cta] = own;
     }
-    if (tid == 0) a.cta_status[cta] = trouble;
+    if (tid == 0) *(a.ctas == 1 ? a.status : a.cta_status + cta) = trouble;
 
     // rows of empty caches
     for (int b = cta; b < a.B; b += gridDim.x) {
@@ -986,6 +986,7 @@ size_t unpacked_bytes(const AttnProblem &x, size_t &k, size_t &v) {
 
 struct Plan {
     int ctas, rows, groups, part_rows, part_size;
+    long long tiles;             // at most, of all sequences and key heads
     size_t cta_status, owners, part, bytes;
     cudaError_t (*run)(const Args &, cudaStream_t);
 };
@@ -999,12 +1000,16 @@ void sizes(Plan &p) {
     p.groups = (p.rows + C::kRows - 1) / C::kRows;
     p.part_rows = p.rows < C::kRows ? p.rows : C::kRows;
     p.part_size = (p.part_rows * (D + 2) + 3) & ~3;
+    // no more CTAs than there can be tiles for their warps
+    const long long wanted = (p.tiles * p.groups + C::kWarps - 1) / C::kWarps;
+    if (wanted < p.ctas) p.ctas = wanted > 0 ? (int)wanted : 1;
     p.bytes = up256(p.part + (size_t)p.ctas * (2 + C::kWarps) * p.part_size * sizeof(float));
 }
 Plan plan_of(const Kv4Attn &p) {
     Plan x{};
     x.ctas = sm_count();
     x.rows = p.Hq / p.Hk * p.Tq;
+    x.tiles = (long long)p.B * p.Hk * (((long long)p.columns * p.page + 63) / 64);
     x.cta_status = kWsHeader;
     x.owners = up256(x.cta_status + x.ctas * sizeof(unsigned));
     x.part = up256(x.owners + x.ctas * sizeof(Owner));
@@ -1027,7 +1032,7 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
     kv4_attn_kernel<D, NT, F32><<<a.ctas, C::kThreads, C::kSmem, s>>>(a);
     note_launch();
     e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.ctas == 1) return e;      // one CTA joins what there is
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;

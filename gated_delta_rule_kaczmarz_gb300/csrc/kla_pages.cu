@@ -15,14 +15,13 @@ namespace kla {
 namespace {
 
 constexpr int kCtas = 8, kThreads = 1024, kAll = kCtas * kThreads;
+constexpr int kMostSequences = 1 << 18;
 
 // The workspace: status word, what the phases share, then arrays.
 struct Shared {
     unsigned status;
-    unsigned trouble;            // set by any thread; cleared in the first phase
-    unsigned late;               // what is found once changes have begun: reported alone
     int copies;                  // pages that the copy kernel moves
-    int sums[3][kCtas];
+    int sums[4][kCtas];
 };
 static_assert(sizeof(Shared) <= kWsHeader, "fits the header");
 
@@ -30,21 +29,17 @@ struct Book {
     Pages p;
     Shared *sh;
     int *from, *to;              // [n] pages that move
-    int *a, *b;                  // [n] scratch
+    int *a, *b, *c;              // [n] scratch
     int *rows;                   // [n][columns + 1]
 };
 
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ unsigned cta_of_cluster() { return blockIdx.x; }      // one cluster a launch
+__device__ __forceinline__ int cta_of_cluster() { return blockIdx.x; }           // one cluster a launch
 __device__ __forceinline__ int thread_of_all() { return blockIdx.x * kThreads + threadIdx.x; }
-// Before a phase that looks whether to go on; and after it.
-__device__ __forceinline__ void report(const Book &k, unsigned what) { atomicMax(&k.sh->trouble, what); }
-__device__ __forceinline__ void report_late(const Book &k) { atomicMax(&k.sh->late, (unsigned)kDevBadTable); }
-__device__ __forceinline__ unsigned look(const unsigned *p) { return *(const volatile unsigned *)p; }
 
-// Entries are written by other CTAs of the cluster: not through the read-only path.
+// What other CTAs of the cluster wrote: not through the read-only path.
 __device__ __forceinline__ int at(const int *p) { return *(const volatile int *)p; }
 
 __device__ __forceinline__ int length_of(const Book &k, int s) {
@@ -55,26 +50,37 @@ __device__ __forceinline__ int length_of(const Book &k, int s) {
 __device__ __forceinline__ int pages_of(const Book &k, int len) { return (int)(((long long)len + k.p.page - 1) / k.p.page); }
 __device__ __forceinline__ bool is_page(const Book &k, int p) { return p >= 0 && p < k.p.n_pages; }
 
-// Sum over the CTA, and of the threads before this one.
-__device__ __forceinline__ int cta_scan(int x, int &before, int *warps) {
+// Sums of N numbers over the CTA, and of the threads before this one.
+template <int N>
+__device__ __forceinline__ void cta_scan(const int (&x)[N], int (&before)[N], int (&all)[N], int (*warps)[32]) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    int s = x;
+    int s[N];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
-    }
-    __syncthreads();
-    if (lane == 31) warps[warp] = s;
-    __syncthreads();
-    int w = warps[lane], t = w;
+    for (int i = 0; i < N; ++i) s[i] = x[i];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, t, o);
-        if (lane >= o) t += y;
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int y = __shfl_up_sync(0xffffffffu, s[i], o);
+            if (lane >= o) s[i] += y;
+        }
+    __syncthreads();
+    if (lane == 31)
+#pragma unroll
+        for (int i = 0; i < N; ++i) warps[i][warp] = s[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int w = warps[i][lane];
+        int t = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, t, o);
+            if (lane >= o) t += y;
+        }
+        before[i] = s[i] - x[i] + __shfl_sync(0xffffffffu, t - w, warp);
+        all[i] = __shfl_sync(0xffffffffu, t, 31);
     }
-    before = s - x + __shfl_sync(0xffffffffu, t - w, warp);
-    return __shfl_sync(0xffffffffu, t, 31);
 }
 
 // The share of n things that a CTA takes, in multiples of 4.
@@ -85,47 +91,40 @@ __device__ __forceinline__ void share_of(int n, int &a, int &e) {
     e = x + each < n ? (int)(x + each) : n;
 }
 
-// The sum of a share's counts, and of those before it.
+// The sum of the shares' counts, and of those before this CTA's.
 __device__ __forceinline__ int total_of(const int *sums, int &before) {
     int t = 0;
     before = 0;
+#pragma unroll
     for (int c = 0; c < kCtas; ++c) {
         const int x = at(sums + c);
-        if (c < (int)cta_of_cluster()) before += x;
+        if (c < cta_of_cluster()) before += x;
         t += x;
     }
     return t;
 }
 
-__device__ __forceinline__ void start(const Book &k) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");     // the copies' launch
-    if (thread_of_all() == 0) {
-        k.sh->trouble = k.sh->late = kDevOk;
-        k.sh->copies = 0;
-    }
-}
-__device__ __forceinline__ void finish(const Book &k) {
-    cluster_barrier();
-    if (thread_of_all() == 0) k.sh->status = max(look(&k.sh->trouble), look(&k.sh->late));
+__device__ __forceinline__ void launch_copies() {       // the second kernel's launch
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ fork, free
 // Sequence dst[f] becomes what src[f] was (src NULL or -1: empty), all at once.
 __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const __grid_constant__ Book k) {
     const Pages &p = k.p;
-    const int tid = thread_of_all(), lane = tid % 32, warp = tid / 32;
-    start(k);
-    for (int f = tid; f < p.n; f += kAll)
-        if (p.dst[f] >= 0 && p.dst[f] < p.S) k.a[p.dst[f]] = -1;
-    cluster_barrier();
-    for (int f = tid; f < p.n; f += kAll) {
+    __shared__ unsigned seen[kMostSequences / 32];       // a bit for each target
+    const int tid = threadIdx.x, lane = tid % 32, warp = thread_of_all() / 32;
+    // every CTA looks the whole list over
+    for (int i = tid; i < (p.S + 31) / 32; i += kThreads) seen[i] = 0;
+    __syncthreads();
+    bool bad = false;
+    for (int f = tid; f < p.n; f += kThreads) {
         const int d = p.dst[f], s = p.src ? p.src[f] : -1;
-        if (d < 0 || d >= p.S || s < -1 || s >= p.S || atomicCAS(&k.a[d], -1, f) != -1)
-            report(k, kDevBadTable);
+        bad = bad || d < 0 || d >= p.S || s < -1 || s >= p.S ||
+              (atomicOr(&seen[d / 32], 1u << d % 32) >> d % 32 & 1);
     }
-    cluster_barrier();
-    if (look(&k.sh->trouble) != kDevOk) {        // nothing is changed
-        finish(k);
+    if (__syncthreads_or(bad)) {                         // nothing is changed
+        if (thread_of_all() == 0) k.sh->status = kDevBadTable;
         return;
     }
     // what the rows will be, and the counts: the tables are still as they were
@@ -138,17 +137,19 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const __grid_const
             if (c < held) {
                 x = p.table[(long long)s * p.columns + c];
                 if (is_page(k, x)) atomicAdd(&p.refs[x], 1);
-                else report_late(k);
+                else bad = true;
             }
             row[c] = x;
             if (c < had) {
                 const int y = p.table[(long long)d * p.columns + c];
                 if (is_page(k, y)) atomicAdd(&p.refs[y], -1);
-                else report_late(k);
+                else bad = true;
             }
         }
         if (lane == 0) row[p.columns] = len;
     }
+    bad = __syncthreads_or(bad);
+    if (tid == 0) k.sh->sums[0][cta_of_cluster()] = bad;
     cluster_barrier();
     for (int f = warp; f < p.n; f += kAll / 32) {
         const int d = p.dst[f];
@@ -156,7 +157,8 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const __grid_const
         for (int c = lane; c < p.columns; c += 32) p.table[(long long)d * p.columns + c] = at(row + c);
         if (lane == 0) p.lens[d] = at(row + p.columns);
     }
-    finish(k);
+    int before;
+    if (thread_of_all() == 0) k.sh->status = total_of(k.sh->sums[0], before) ? kDevBadTable : kDevOk;
 }
 
 // ------------------------------------------------------------------ growth
@@ -183,80 +185,74 @@ __device__ __forceinline__ Need need_of(const Book &k, int s) {
 
 __global__ void __launch_bounds__(kThreads) pages_grow_kernel(const __grid_constant__ Book k) {
     const Pages &p = k.p;
-    __shared__ int warps[32];
+    __shared__ int warps[4][32];
     const int tid = threadIdx.x, cta = cta_of_cluster();
-    start(k);
+    launch_copies();
     // pages needed and copies, of this CTA's sequences; free pages of its share
-    int s0, s1, r0, r1, before;
+    int s0, s1, r0, r1;
     share_of(p.S, s0, s1);
     share_of(p.n_pages, r0, r1);
-    int need = 0, copies = 0, spare = 0;
-    bool bad = false;
+    int count[4] = {};           // needed, copies, free, bad
     for (int s = s0 + tid; s < s1; s += kThreads) {
         const Need x = need_of(k, s);
-        need += x.pages;
-        copies += x.copy;
-        bad = bad || x.bad;
+        count[0] += x.pages;
+        count[1] += x.copy;
+        count[3] += x.bad;
     }
-    for (int r = r0 + tid; r < r1; r += kThreads) spare += p.refs[r] == 0;
-    need = cta_scan(need, before, warps);
-    copies = cta_scan(copies, before, warps);
-    spare = cta_scan(spare, before, warps);
-    if (tid == 0) {
-        k.sh->sums[0][cta] = need;
-        k.sh->sums[1][cta] = copies;
-        k.sh->sums[2][cta] = spare;
+    for (int r = r0 + tid; r < r1; r += kThreads) count[2] += p.refs[r] == 0;
+    {
+        int before[4], all[4];
+        cta_scan(count, before, all, warps);
+        if (tid < 4) k.sh->sums[tid][cta] = tid == 0 ? all[0] : tid == 1 ? all[1] : tid == 2 ? all[2] : all[3];
     }
-    cluster_barrier();           // (trouble is cleared)
-    if (bad) report(k, kDevBadTable);
-    int need0, copies0, spare0;
-    need = total_of(k.sh->sums[0], need0);
-    copies = total_of(k.sh->sums[1], copies0);
-    spare = total_of(k.sh->sums[2], spare0);
-    if (need > spare && tid == 0) report(k, kDevNoPages);
+    cluster_barrier();
+    int need0, copies0, spare0, none;
+    const int need = total_of(k.sh->sums[0], need0), copies = total_of(k.sh->sums[1], copies0);
+    const int spare = total_of(k.sh->sums[2], spare0), bad = total_of(k.sh->sums[3], none);
+    if (thread_of_all() == 0) {
+        k.sh->status = bad ? kDevBadTable : need > spare ? kDevNoPages : kDevOk;
+        k.sh->copies = bad || need > spare ? 0 : copies;
+    }
+    if (bad || need > spare) return;                     // nothing is changed
     // the free pages, in order, as far as they are needed
     for (int r = r0; r < r1 && spare0 < need; r += 4 * kThreads) {
-        int free[4], n = 0;
+        int free[4], n[1] = {};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int x = r + 4 * tid + i;
             free[i] = x < r1 && p.refs[x] == 0;
-            n += free[i];
+            n[0] += free[i];
         }
-        int rank;
-        const int all = cta_scan(n, rank, warps);
-        rank += spare0;
+        int rank[1], all[1];
+        cta_scan(n, rank, all, warps);
+        rank[0] += spare0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (free[i] && rank < need) k.a[rank] = r + 4 * tid + i;
-            rank += free[i];
+            if (free[i] && rank[0] < need) k.a[rank[0]] = r + 4 * tid + i;
+            rank[0] += free[i];
         }
-        spare0 += all;
+        spare0 += all[0];
     }
-    // where each sequence's begin in that order
+    // where each sequence's begin in that order, and its copy's number
     for (int s = s0; s < s1; s += kThreads) {
         Need x{0, 0, false, false};
         if (s + tid < s1) x = need_of(k, s + tid);
-        int rank, crank;
-        const int all = cta_scan(x.pages, rank, warps), call = cta_scan(x.copy, crank, warps);
+        const int n[2] = {x.pages, x.copy};
+        int rank[2], all[2];
+        cta_scan(n, rank, all, warps);
         if (s + tid < s1) {
-            k.b[s + tid] = need0 + rank;
-            k.to[s + tid] = x.copy ? copies0 + crank : -1;       // its number among the copies, for now
+            k.b[s + tid] = need0 + rank[0];
+            k.c[s + tid] = x.copy ? copies0 + rank[1] : -1;
         }
-        need0 += all;
-        copies0 += call;
+        need0 += all[0];
+        copies0 += all[1];
     }
     cluster_barrier();
-    if (look(&k.sh->trouble) != kDevOk) {        // nothing is changed
-        finish(k);
-        return;
-    }
-    // what a sequence copies: read before any count changes
     const int warp = thread_of_all() / 32, lane = tid % 32;
     for (int s = warp; s < p.S; s += kAll / 32) {
         const int n = p.more[s];
         if (n == 0) continue;
-        const int len = length_of(k, s), number = at(k.to + s);
+        const int len = length_of(k, s), number = at(k.c + s);
         const int first = pages_of(k, len) - (number >= 0), pages = pages_of(k, len + n) - first;
         const int rank = at(k.b + s);
         int *row = p.table + (long long)s * p.columns;
@@ -268,74 +264,75 @@ __global__ void __launch_bounds__(kThreads) pages_grow_kernel(const __grid_const
             row[first + i] = page;
             p.refs[page] = 1;
             if (i == 0 && number >= 0) {
-                k.rows[number] = page;
+                k.to[number] = page;
                 k.from[number] = old;
                 atomicAdd(&p.refs[old], -1);
             }
         }
+        __syncwarp();
         if (lane == 0) p.lens[s] = len + n;
     }
-    cluster_barrier();
-    for (int i = thread_of_all(); i < copies; i += kAll) k.to[i] = at(k.rows + i);
-    if (thread_of_all() == 0) k.sh->copies = copies;
-    finish(k);
 }
 
 // ------------------------------------------------------------------ compaction
 __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_constant__ Book k) {
     const Pages &p = k.p;
-    __shared__ int warps[32];
+    __shared__ int warps[1][32];
     const int tid = threadIdx.x, cta = cta_of_cluster();
-    start(k);
+    launch_copies();
+    if (thread_of_all() == 0) k.sh->status = kDevOk;     // (reports come behind the barriers)
     int r0, r1, before;
     share_of(p.n_pages, r0, r1);
-    int used = 0;
-    for (int r = r0 + tid; r < r1; r += kThreads) used += p.refs[r] > 0;
-    used = cta_scan(used, before, warps);
-    if (tid == 0) k.sh->sums[0][cta] = used;
+    int used[1] = {}, rank[1], all[1];
+    for (int r = r0 + tid; r < r1; r += kThreads) used[0] += p.refs[r] > 0;
+    cta_scan(used, rank, all, warps);
+    if (tid == 0) k.sh->sums[0][cta] = all[0];
     cluster_barrier();
     const int n_used = total_of(k.sh->sums[0], before);
     // holes below n_used in order (a), used pages from there on in reverse order (b)
-    int holes = 0;
+    int holes[1] = {};
     for (int r = r0; r < r1; r += 4 * kThreads) {
-        int on[4], n = 0;
+        int on[4], n[1] = {};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int x = r + 4 * tid + i;
             on[i] = x < r1 && p.refs[x] > 0;
-            n += on[i];
+            n[0] += on[i];
         }
-        int rank;
-        const int all = cta_scan(n, rank, warps);
-        rank += before;
+        cta_scan(n, rank, all, warps);
+        rank[0] += before;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int x = r + 4 * tid + i;
             if (x >= r1) break;
             if (on[i] && x >= n_used) {
-                k.b[n_used - 1 - rank] = x;
+                k.b[n_used - 1 - rank[0]] = x;
             } else {
                 if (!on[i] && x < n_used) {
-                    k.a[x - rank] = x;
-                    ++holes;
+                    k.a[x - rank[0]] = x;
+                    ++holes[0];
                 }
                 p.page_map[x] = on[i] ? x : -1;
             }
-            rank += on[i];
+            rank[0] += on[i];
         }
-        before += all;
+        before += all[0];
     }
-    holes = cta_scan(holes, before, warps);
-    if (tid == 0) k.sh->sums[1][cta] = holes;
+    cta_scan(holes, rank, all, warps);
+    if (tid == 0) k.sh->sums[1][cta] = all[0];
     cluster_barrier();
-    holes = total_of(k.sh->sums[1], before);
-    for (int i = thread_of_all(); i < holes; i += kAll) {
-        const int from = at(k.b + holes - 1 - i), to = at(k.a + i);
+    const int moved = total_of(k.sh->sums[1], before);
+    for (int i = thread_of_all(); i < moved; i += kAll) {
+        const int from = at(k.b + moved - 1 - i), to = at(k.a + i);
         p.page_map[from] = to;
         p.refs[to] = p.refs[from];
         p.refs[from] = 0;
         k.from[i] = from;
         k.to[i] = to;
+    }
+    if (thread_of_all() == 0) {
+        k.sh->copies = moved;
+        *p.n_used = n_used;
     }
     cluster_barrier();
     const int warp = thread_of_all() / 32, lane = tid % 32;
@@ -345,15 +342,10 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_co
         for (int c = lane; c < held; c += 32) {
             const int x = row[c];
             const int y = is_page(k, x) ? at(p.page_map + x) : -1;
-            if (y < 0) report_late(k);                           // no page, or a free one: left
+            if (y < 0) atomicMax(&k.sh->status, (unsigned)kDevBadTable);     // no page, or a free one: left
             else if (y != x) row[c] = y;
         }
     }
-    if (thread_of_all() == 0) {
-        k.sh->copies = holes;
-        *p.n_used = n_used;
-    }
-    finish(k);
 }
 
 // ------------------------------------------------------------------ copies
@@ -362,30 +354,33 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_co
 __global__ void __launch_bounds__(kThreads) pages_check_kernel(const __grid_constant__ Book k) {
     const Pages &p = k.p;
     const int tid = thread_of_all();
-    start(k);
+    launch_copies();
     for (int i = tid; i < p.n; i += kAll) {
         if (is_page(k, p.src[i])) k.a[p.src[i]] = -1;
         if (is_page(k, p.dst[i])) k.a[p.dst[i]] = -1;
     }
     cluster_barrier();
-    for (int i = tid; i < p.n; i += kAll)
-        if (!is_page(k, p.src[i]) || !is_page(k, p.dst[i]) || atomicCAS(&k.a[p.dst[i]], -1, i) != -1)
-            report(k, kDevBadTable);
+    bool bad = false;
+    for (int i = tid; i < p.n; i += kAll) {
+        bad = bad || !is_page(k, p.src[i]) || !is_page(k, p.dst[i]) || atomicCAS(&k.a[p.dst[i]], -1, i) != -1;
+        k.from[i] = p.src[i];
+        k.to[i] = p.dst[i];
+    }
     cluster_barrier();
     for (int i = tid; i < p.n; i += kAll)
         if (is_page(k, p.src[i])) {
             const int other = at(k.a + p.src[i]);
-            if (other != -1 && other != i) report(k, kDevBadTable);
+            bad = bad || (other != -1 && other != i);
         }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) k.sh->sums[0][cta_of_cluster()] = bad;
     cluster_barrier();
-    if (look(&k.sh->trouble) == kDevOk) {
-        for (int i = tid; i < p.n; i += kAll) {
-            k.from[i] = p.src[i];
-            k.to[i] = p.dst[i];
-        }
-        if (tid == 0) k.sh->copies = p.n;
+    if (tid == 0) {
+        int before;
+        bad = total_of(k.sh->sums[0], before) != 0;
+        k.sh->status = bad ? kDevBadTable : kDevOk;
+        k.sh->copies = bad ? 0 : p.n;
     }
-    finish(k);
 }
 
 constexpr int kCopyThreads = 256, kEach = 4;
@@ -427,13 +422,14 @@ size_t most(int S, int n_pages, int n) {
 }
 
 Book book_of(const Pages &p) {
-    Book k{p, static_cast<Shared *>(p.ws), nullptr, nullptr, nullptr, nullptr, nullptr};
+    Book k{p, static_cast<Shared *>(p.ws), nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
     const size_t n = most(p.S, p.n_pages, p.n);
     k.from = reinterpret_cast<int *>(static_cast<unsigned char *>(p.ws) + kWsHeader);
     k.to = k.from + n;
     k.a = k.to + n;
     k.b = k.a + n;
-    k.rows = k.b + n;
+    k.c = k.b + n;
+    k.rows = k.c + n;
     return k;
 }
 
@@ -476,10 +472,12 @@ cudaError_t copy(const Book &k, long long copies, cudaStream_t s) {
 
 }  // namespace
 
+bool pages_too_many(int S) { return S > kMostSequences; }
+
 size_t pages_workspace_bytes(int S, int columns, int n_pages, int n) {
     const size_t x = most(S, n_pages, n);
     const size_t rows = (size_t)n * ((size_t)columns + 1);
-    return (kWsHeader + (4 * x + (rows > x ? rows : x)) * sizeof(int) + 255) & ~(size_t)255;
+    return (kWsHeader + (5 * x + rows) * sizeof(int) + 255) & ~(size_t)255;
 }
 
 cudaError_t launch_pages_fork(const Pages &p, cudaStream_t s) {

@@ -594,7 +594,7 @@ KLA_API int kla_kv4_attn(const void *q, long long q_stride, const void *pool, co
  *   the call: its length and its pages, shared; the rest of its table row becomes -1.
  *   src[f] = -1, or src NULL: it becomes empty.  refs follow, so pages that nobody
  *   holds any more are free.  A dst that is there twice or a number out of range
- *   refuses the call: nothing changes.
+ *   refuses the call: nothing changes.  At most 2^18 sequences.
  * kla_pages_grow: room for n_new[s] more positions of every sequence, and lens[s]
  *   += n_new[s].  New pages are the lowest free ones, in the order of sequences and
  *   positions.  A partly filled last page that other sequences hold too is replaced

@@ -147,6 +147,16 @@ def test_the_binding_refuses():
         kla.kla_kv4_read(pool, table, lens, T=1, cu_seqlens=lens)
     with pytest.raises(ValueError, match="shape"):
         kla.kla_kv4_append(q[0], q[0], pool, table, lens)
+    refs, some = torch.zeros(3).int(), torch.zeros(1).int()
+    for call in (lambda: kla.kla_pages_fork(table, lens, refs, some, some, 16),
+                 lambda: kla.kla_pages_free(table, lens, refs, some, 16),
+                 lambda: kla.kla_pages_grow(pool[None], table, lens, refs, lens, 16),
+                 lambda: kla.kla_pages_compact(pool[None], table, lens, refs, 16),
+                 lambda: kla.kla_pages_copy(pool[None], some, some),
+                 lambda: kla.kla_kv4_append(q[:, :, :2], q[:, :, :2], pool, table, lens),
+                 lambda: kla.kla_kv4_read(pool, table, lens, T=1)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
     with pytest.raises(TypeError):
         kla.kla_kv4_append(q.half(), q.half(), pool, table, lens)
 
