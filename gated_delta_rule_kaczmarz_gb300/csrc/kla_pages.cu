@@ -4,24 +4,25 @@
 // a count of holders for each page; a page without holders is free.  Nothing else is kept, so
 // any order of calls, captured ones too, finds the state that the last one left.
 //
-// Each operator is one cluster of 8 CTAs that reads and changes the book (its
-// phases part at cluster barriers, what they hand over goes through the
-// workspace), and where pages move a second kernel that copies those that the
-// first listed.  The first is bound by latency: a barrier and a round trip to L2 for
-// each phase.  The second is bound by HBM.
+// Each operator is one CTA, or one cluster of 8, that reads and changes the book
+// (its phases part at barriers, what they hand over goes through the workspace), and
+// where pages move a second kernel that copies those that the first listed.  The
+// first is bound by latency, a barrier and a round trip to L2 for each phase: 4 to 9
+// us.  The second is bound by HBM: 2048 pages of 36 KB in 4 layers 89 us, 0.99 of
+// measured bandwidth.
 #include "kla_internal.h"
 
 namespace kla {
 namespace {
 
-constexpr int kCtas = 8, kThreads = 1024, kAll = kCtas * kThreads;
+constexpr int kCtas = 8, kThreads = 1024;
 constexpr int kMostSequences = 1 << 18;
 
 // The workspace: status word, what the phases share, then arrays.
 struct Shared {
     unsigned status;
     int copies;                  // pages that the copy kernel moves
-    int sums[4][kCtas];
+    alignas(16) int sums[4][kCtas];
 };
 static_assert(sizeof(Shared) <= kWsHeader, "fits the header");
 
@@ -33,14 +34,18 @@ struct Book {
     int *rows;                   // [n][columns + 1]
 };
 
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+// All threads of the launch, which is one cluster or one CTA.
+__device__ __forceinline__ void all_barrier() {
+    if (gridDim.x == 1) __syncthreads();
+    else asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ int cta_of_cluster() { return blockIdx.x; }           // one cluster a launch
+__device__ __forceinline__ int cta_of_all() { return blockIdx.x; }
 __device__ __forceinline__ int thread_of_all() { return blockIdx.x * kThreads + threadIdx.x; }
+__device__ __forceinline__ int threads_of_all() { return gridDim.x * kThreads; }
 
-// What other CTAs of the cluster wrote: not through the read-only path.
-__device__ __forceinline__ int at(const int *p) { return *(const volatile int *)p; }
+// What other CTAs of the cluster wrote: from L2.  (Volatile reads would wait for one
+// another: the sums below took 8000 cycles so.)
+__device__ __forceinline__ int at(const int *p) { return __ldcg(p); }
 
 __device__ __forceinline__ int length_of(const Book &k, int s) {
     const long long most = (long long)k.p.columns * k.p.page;
@@ -85,21 +90,23 @@ __device__ __forceinline__ void cta_scan(const int (&x)[N], int (&before)[N], in
 
 // The share of n things that a CTA takes, in multiples of 4.
 __device__ __forceinline__ void share_of(int n, int &a, int &e) {
-    const int each = ((n + kCtas - 1) / kCtas + 3) & ~3;
-    const long long x = (long long)each * cta_of_cluster();
+    const int each = ((n + (int)gridDim.x - 1) / (int)gridDim.x + 3) & ~3;
+    const long long x = (long long)each * cta_of_all();
     a = x < n ? (int)x : n;
     e = x + each < n ? (int)(x + each) : n;
 }
 
 // The sum of the shares' counts, and of those before this CTA's.
 __device__ __forceinline__ int total_of(const int *sums, int &before) {
+    static_assert(kCtas == 8, "two reads");
+    const int4 u = __ldcg(reinterpret_cast<const int4 *>(sums)), v = __ldcg(reinterpret_cast<const int4 *>(sums) + 1);
+    const int x[kCtas] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
     int t = 0;
     before = 0;
 #pragma unroll
     for (int c = 0; c < kCtas; ++c) {
-        const int x = at(sums + c);
-        if (c < cta_of_cluster()) before += x;
-        t += x;
+        if (c < cta_of_all()) before += x[c];
+        if (c < (int)gridDim.x) t += x[c];
     }
     return t;
 }
@@ -128,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const __grid_const
         return;
     }
     // what the rows will be, and the counts: the tables are still as they were
-    for (int f = warp; f < p.n; f += kAll / 32) {
+    for (int f = warp; f < p.n; f += threads_of_all() / 32) {
         const int s = p.src ? p.src[f] : -1, d = p.dst[f], len = s < 0 ? 0 : length_of(k, s);
         const int held = pages_of(k, len), had = pages_of(k, length_of(k, d));
         int *row = k.rows + (long long)f * (p.columns + 1);
@@ -149,9 +156,9 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const __grid_const
         if (lane == 0) row[p.columns] = len;
     }
     bad = __syncthreads_or(bad);
-    if (tid == 0) k.sh->sums[0][cta_of_cluster()] = bad;
-    cluster_barrier();
-    for (int f = warp; f < p.n; f += kAll / 32) {
+    if (tid == 0) k.sh->sums[0][cta_of_all()] = bad;
+    all_barrier();
+    for (int f = warp; f < p.n; f += threads_of_all() / 32) {
         const int d = p.dst[f];
         const int *row = k.rows + (long long)f * (p.columns + 1);
         for (int c = lane; c < p.columns; c += 32) p.table[(long long)d * p.columns + c] = at(row + c);
@@ -186,7 +193,7 @@ __device__ __forceinline__ Need need_of(const Book &k, int s) {
 __global__ void __launch_bounds__(kThreads) pages_grow_kernel(const __grid_constant__ Book k) {
     const Pages &p = k.p;
     __shared__ int warps[4][32];
-    const int tid = threadIdx.x, cta = cta_of_cluster();
+    const int tid = threadIdx.x, cta = cta_of_all();
     launch_copies();
     // pages needed and copies, of this CTA's sequences; free pages of its share
     int s0, s1, r0, r1;
@@ -205,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) pages_grow_kernel(const __grid_const
         cta_scan(count, before, all, warps);
         if (tid < 4) k.sh->sums[tid][cta] = tid == 0 ? all[0] : tid == 1 ? all[1] : tid == 2 ? all[2] : all[3];
     }
-    cluster_barrier();
+    all_barrier();
     int need0, copies0, spare0, none;
     const int need = total_of(k.sh->sums[0], need0), copies = total_of(k.sh->sums[1], copies0);
     const int spare = total_of(k.sh->sums[2], spare0), bad = total_of(k.sh->sums[3], none);
@@ -247,9 +254,9 @@ __global__ void __launch_bounds__(kThreads) pages_grow_kernel(const __grid_const
         need0 += all[0];
         copies0 += all[1];
     }
-    cluster_barrier();
+    all_barrier();
     const int warp = thread_of_all() / 32, lane = tid % 32;
-    for (int s = warp; s < p.S; s += kAll / 32) {
+    for (int s = warp; s < p.S; s += threads_of_all() / 32) {
         const int n = p.more[s];
         if (n == 0) continue;
         const int len = length_of(k, s), number = at(k.c + s);
@@ -278,7 +285,7 @@ __global__ void __launch_bounds__(kThreads) pages_grow_kernel(const __grid_const
 __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_constant__ Book k) {
     const Pages &p = k.p;
     __shared__ int warps[1][32];
-    const int tid = threadIdx.x, cta = cta_of_cluster();
+    const int tid = threadIdx.x, cta = cta_of_all();
     launch_copies();
     if (thread_of_all() == 0) k.sh->status = kDevOk;     // (reports come behind the barriers)
     int r0, r1, before;
@@ -287,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_co
     for (int r = r0 + tid; r < r1; r += kThreads) used[0] += p.refs[r] > 0;
     cta_scan(used, rank, all, warps);
     if (tid == 0) k.sh->sums[0][cta] = all[0];
-    cluster_barrier();
+    all_barrier();
     const int n_used = total_of(k.sh->sums[0], before);
     // holes below n_used in order (a), used pages from there on in reverse order (b)
     int holes[1] = {};
@@ -320,9 +327,9 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_co
     }
     cta_scan(holes, rank, all, warps);
     if (tid == 0) k.sh->sums[1][cta] = all[0];
-    cluster_barrier();
+    all_barrier();
     const int moved = total_of(k.sh->sums[1], before);
-    for (int i = thread_of_all(); i < moved; i += kAll) {
+    for (int i = thread_of_all(); i < moved; i += threads_of_all()) {
         const int from = at(k.b + moved - 1 - i), to = at(k.a + i);
         p.page_map[from] = to;
         p.refs[to] = p.refs[from];
@@ -334,9 +341,9 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_co
         k.sh->copies = moved;
         *p.n_used = n_used;
     }
-    cluster_barrier();
+    all_barrier();
     const int warp = thread_of_all() / 32, lane = tid % 32;
-    for (int s = warp; s < p.S; s += kAll / 32) {
+    for (int s = warp; s < p.S; s += threads_of_all() / 32) {
         const int held = pages_of(k, length_of(k, s));
         int *row = p.table + (long long)s * p.columns;
         for (int c = lane; c < held; c += 32) {
@@ -355,26 +362,26 @@ __global__ void __launch_bounds__(kThreads) pages_check_kernel(const __grid_cons
     const Pages &p = k.p;
     const int tid = thread_of_all();
     launch_copies();
-    for (int i = tid; i < p.n; i += kAll) {
+    for (int i = tid; i < p.n; i += threads_of_all()) {
         if (is_page(k, p.src[i])) k.a[p.src[i]] = -1;
         if (is_page(k, p.dst[i])) k.a[p.dst[i]] = -1;
     }
-    cluster_barrier();
+    all_barrier();
     bool bad = false;
-    for (int i = tid; i < p.n; i += kAll) {
+    for (int i = tid; i < p.n; i += threads_of_all()) {
         bad = bad || !is_page(k, p.src[i]) || !is_page(k, p.dst[i]) || atomicCAS(&k.a[p.dst[i]], -1, i) != -1;
         k.from[i] = p.src[i];
         k.to[i] = p.dst[i];
     }
-    cluster_barrier();
-    for (int i = tid; i < p.n; i += kAll)
+    all_barrier();
+    for (int i = tid; i < p.n; i += threads_of_all())
         if (is_page(k, p.src[i])) {
             const int other = at(k.a + p.src[i]);
             bad = bad || (other != -1 && other != i);
         }
     bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) k.sh->sums[0][cta_of_cluster()] = bad;
-    cluster_barrier();
+    if (threadIdx.x == 0) k.sh->sums[0][cta_of_all()] = bad;
+    all_barrier();
     if (tid == 0) {
         int before;
         bad = total_of(k.sh->sums[0], before) != 0;
@@ -433,7 +440,20 @@ Book book_of(const Pages &p) {
     return k;
 }
 
-cudaError_t run(void (*kernel)(const Book), const Book &k, cudaStream_t s) {
+// One CTA up to `most` entries, whose barriers are cheaper (1.0 to 2.6 us a call),
+// else the cluster, which has more hands.  Both in us: a fork of 32 rows of 64 pages 5.8
+// and 6.3, of 64 8.6 and 6.2; growth among 16384 pages 7.4 and 8.1, 32768 7.9 and 8.0,
+// 131072 13.4 and 9.5 (a sequence that grows counts as 128 of them: of 256 that do among
+// 3200 pages 18.5 and 11.5); compaction of 2048 pages with a table of 32 x 64 7.1 and 8.6, 4096
+// with 64 x 64 8.7 and 8.7, 8192 with 128 x 64 12.3 and 8.9.
+constexpr long long kForkEntries = 2048, kGrowEntries = 32768, kCompactEntries = 8192, kCopyEntries = 4096;
+
+cudaError_t run(void (*kernel)(const Book), const Book &k, long long entries, long long most, cudaStream_t s) {
+    if (entries <= most) {
+        kernel<<<1, kThreads, 0, s>>>(k);
+        note_launch();
+        return cudaGetLastError();
+    }
     cudaLaunchAttribute cluster{};
     cluster.id = cudaLaunchAttributeClusterDimension;
     cluster.val.clusterDim.x = kCtas;
@@ -481,21 +501,21 @@ size_t pages_workspace_bytes(int S, int columns, int n_pages, int n) {
 }
 
 cudaError_t launch_pages_fork(const Pages &p, cudaStream_t s) {
-    return run(pages_fork_kernel, book_of(p), s);
+    return run(pages_fork_kernel, book_of(p), (long long)p.n * p.columns + p.S / 32, kForkEntries, s);
 }
 cudaError_t launch_pages_grow(const Pages &p, cudaStream_t s) {
     const Book k = book_of(p);
-    const cudaError_t e = run(pages_grow_kernel, k, s);
+    const cudaError_t e = run(pages_grow_kernel, k, p.n_pages + 128LL * p.S, kGrowEntries, s);
     return e != cudaSuccess ? e : copy(k, p.S, s);
 }
 cudaError_t launch_pages_compact(const Pages &p, cudaStream_t s) {
     const Book k = book_of(p);
-    const cudaError_t e = run(pages_compact_kernel, k, s);
+    const cudaError_t e = run(pages_compact_kernel, k, p.n_pages + (long long)p.S * p.columns, kCompactEntries, s);
     return e != cudaSuccess ? e : copy(k, p.n_pages / 2, s);
 }
 cudaError_t launch_pages_copy(const Pages &p, cudaStream_t s) {
     const Book k = book_of(p);
-    const cudaError_t e = run(pages_check_kernel, k, s);
+    const cudaError_t e = run(pages_check_kernel, k, p.n, kCopyEntries, s);
     return e != cudaSuccess ? e : copy(k, p.n, s);
 }
 
