@@ -962,10 +962,12 @@ int sm_count() {
 // 83 and 55, 512 559 and 163; 16 + 2 of 64 over 4 caches of 16384: 8 26 and 32, 16 37 and
 // 35, 64 107 and 59; 8 + 8 of 64 over 1024 keys: 128 14 and 17, 512 22 and 22.
 constexpr int kUnpackRows = 128;
+// Not where the unpacked rows, of the table's whole width, would take more than this.
+constexpr long long kUnpackBytes = 8LL << 30;
 bool unpacked(const Kv4Attn &p, AttnProblem &x, Kv4Rows &r) {
     if (p.dtype != 1 || (long long)p.Hq / p.Hk * p.Tq < kUnpackRows) return false;
     const long long keys = (long long)p.B * p.columns * p.page;
-    if (keys > INT32_MAX) return false;
+    if (keys > INT32_MAX || keys * p.Hk * p.d * 4 > kUnpackBytes) return false;
     x.q = p.q; x.q_stride = p.q_stride; x.out = p.o; x.lse = p.lse; x.k_lens = p.lens;
     x.k_stride = x.v_stride = (long long)p.Hk * p.d;
     x.n_seq = p.B; x.Tq = p.Tq; x.Tk = p.columns * p.page; x.total_q = p.B * p.Tq; x.total_k = (int)keys;
