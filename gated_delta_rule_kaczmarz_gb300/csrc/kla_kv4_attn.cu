@@ -28,6 +28,7 @@
 
 #include "kla_attn.cuh"
 #include "kla_kv4.cuh"
+#include "kla_launch.cuh"
 #include "kla_tc.cuh"
 
 namespace kla {
@@ -560,6 +561,8 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
         parts[2 * warp].seq = parts[2 * warp + 1].seq = -1;
     }
     if (tid == 0) trouble = kDevOk;
+    after_previous();
+    let_next_start();
 
     // tiles before each thread's share of the sequences
     const int share = (a.B + C::kThreads - 1) / C::kThreads, b0 = tid * share;
@@ -585,7 +588,6 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
     }
     sums[tid] = sum - mine;
     __syncthreads();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const Split split = split_of<C::kWarps>(a, tiles);
     const unsigned cta0 = split.cta(cta);
@@ -857,7 +859,8 @@ __global__ void __launch_bounds__(512) kv4_join_kernel(const __grid_constant__ A
     __shared__ __align__(16) float shared_v[16][D];
     __shared__ float shared_m[16], shared_l[16];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, n = warp % C::kRows, sub = warp / C::kRows;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
+    let_next_start();
     const Owner own = a.owners[blockIdx.x];
     if (blockIdx.x == 0 && warp == 0) {
         unsigned x = kDevOk;
@@ -1031,20 +1034,10 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
     using C = Config<D, NT, F32>;
     cudaError_t e = allow_dynamic_smem((const void *)kv4_attn_kernel<D, NT, F32>, C::kSmem);
     if (e != cudaSuccess) return e;
-    kv4_attn_kernel<D, NT, F32><<<a.ctas, C::kThreads, C::kSmem, s>>>(a);
+    e = launch_next(kv4_attn_kernel<D, NT, F32>, a.ctas, C::kThreads, C::kSmem, 1, a, s);
     note_launch();
-    e = cudaGetLastError();
     if (e != cudaSuccess || a.ctas == 1) return e;      // one CTA joins what there is
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)a.ctas);
-    cfg.blockDim = dim3(512);
-    cfg.stream = s;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, F32>, a);
+    e = launch_next(kv4_join_kernel<D, NT, F32>, a.ctas, 512, 0, 1, a, s);
     note_launch();
     return e;
 }

@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 
 #include "kla_kv4.cuh"
+#include "kla_launch.cuh"
 
 namespace kla {
 namespace {
@@ -198,6 +199,8 @@ __device__ __forceinline__ void check_table(const Kv4Rows &p) {
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_constant__ Work w) {
     const Kv4Rows &p = w.p;
+    after_previous();
+    let_next_start();
     check_table(p);
     const int i = blockIdx.x * kThreads + threadIdx.x, each = p.Hk * (D / 16);
     const int slot = kv4::divided(i, w.by_each), unit = i - slot * each, head = unit / (D / 16), f = unit % (D / 16);
@@ -279,6 +282,8 @@ __device__ __forceinline__ float2 to_float2(uint32_t h) {
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constant__ Work w) {
     const Kv4Rows &p = w.p;
+    after_previous();
+    let_next_start();
     check_table(p);
     const int i = blockIdx.x * kThreads + threadIdx.x, each = p.Hk * (D / 16);
     const int slot = kv4::divided(i, w.by_each), unit = i - slot * each, head = unit / (D / 16), f = unit % (D / 16);
@@ -351,10 +356,10 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
 template <typename T, int D>
 cudaError_t launch(const Work &w, bool read, cudaStream_t s) {
     const long long n = (long long)w.slots * w.p.Hk * (D / 16), blocks = (n + kThreads - 1) / kThreads;
-    if (read) kv4_read_kernel<T, D><<<(unsigned)blocks, kThreads, 0, s>>>(w);
-    else kv4_append_kernel<T, D><<<(unsigned)blocks, kThreads, 0, s>>>(w);
+    const cudaError_t e = launch_next(read ? kv4_read_kernel<T, D> : kv4_append_kernel<T, D>, (unsigned)blocks, kThreads,
+                                      0, 1, w, s);
     note_launch();
-    return cudaGetLastError();
+    return e;
 }
 
 long long slots_of(const Kv4Rows &p) {

@@ -11,6 +11,7 @@
 // us.  The second is bound by HBM: 2048 pages of 36 KB in 4 layers 89 us, 0.99 of
 // measured bandwidth.
 #include "kla_internal.h"
+#include "kla_launch.cuh"
 
 namespace kla {
 namespace {
@@ -111,16 +112,14 @@ __device__ __forceinline__ int total_of(const int *sums, int &before) {
     return t;
 }
 
-__device__ __forceinline__ void launch_copies() {       // the second kernel's launch
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // ------------------------------------------------------------------ fork, free
 // Sequence dst[f] becomes what src[f] was (src NULL or -1: empty), all at once.
 __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const __grid_constant__ Book k) {
     const Pages &p = k.p;
     __shared__ unsigned seen[kMostSequences / 32];       // a bit for each target
     const int tid = threadIdx.x, lane = tid % 32, warp = thread_of_all() / 32;
+    after_previous();
+    let_next_start();
     // every CTA looks the whole list over
     for (int i = tid; i < (p.S + 31) / 32; i += kThreads) seen[i] = 0;
     __syncthreads();
@@ -194,7 +193,8 @@ __global__ void __launch_bounds__(kThreads) pages_grow_kernel(const __grid_const
     const Pages &p = k.p;
     __shared__ int warps[4][32];
     const int tid = threadIdx.x, cta = cta_of_all();
-    launch_copies();
+    after_previous();
+    let_next_start();
     // pages needed and copies, of this CTA's sequences; free pages of its share
     int s0, s1, r0, r1;
     share_of(p.S, s0, s1);
@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_co
     const Pages &p = k.p;
     __shared__ int warps[1][32];
     const int tid = threadIdx.x, cta = cta_of_all();
-    launch_copies();
+    after_previous();
+    let_next_start();
     if (thread_of_all() == 0) k.sh->status = kDevOk;     // (reports come behind the barriers)
     int r0, r1, before;
     share_of(p.n_pages, r0, r1);
@@ -361,7 +362,8 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_co
 __global__ void __launch_bounds__(kThreads) pages_check_kernel(const __grid_constant__ Book k) {
     const Pages &p = k.p;
     const int tid = thread_of_all();
-    launch_copies();
+    after_previous();
+    let_next_start();
     for (int i = tid; i < p.n; i += threads_of_all()) {
         if (is_page(k, p.src[i])) k.a[p.src[i]] = -1;
         if (is_page(k, p.dst[i])) k.a[p.dst[i]] = -1;
@@ -394,7 +396,8 @@ constexpr int kCopyThreads = 256, kEach = 4;
 constexpr long long kPiece = (long long)kCopyThreads * kEach * 16;      // bytes
 
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ Book k) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
+    let_next_start();
     const Pages &p = k.p;
     const int copies = k.sh->copies;
     const unsigned pieces = (unsigned)((p.page_bytes + kPiece - 1) / kPiece);
@@ -449,22 +452,8 @@ Book book_of(const Pages &p) {
 constexpr long long kForkEntries = 2048, kGrowEntries = 32768, kCompactEntries = 8192, kCopyEntries = 4096;
 
 cudaError_t run(void (*kernel)(const Book), const Book &k, long long entries, long long most, cudaStream_t s) {
-    if (entries <= most) {
-        kernel<<<1, kThreads, 0, s>>>(k);
-        note_launch();
-        return cudaGetLastError();
-    }
-    cudaLaunchAttribute cluster{};
-    cluster.id = cudaLaunchAttributeClusterDimension;
-    cluster.val.clusterDim.x = kCtas;
-    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(kCtas);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
-    cfg.attrs = &cluster;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, k);
+    const bool one = entries <= most;
+    const cudaError_t e = launch_next(kernel, one ? 1 : kCtas, kThreads, 0, one ? 1 : kCtas, k, s);
     note_launch();
     return e;
 }
@@ -475,17 +464,9 @@ cudaError_t copy(const Book &k, long long copies, cudaStream_t s) {
     if (p.layers == 0 || p.page_bytes == 0 || copies == 0) return cudaSuccess;
     const long long pieces = (p.page_bytes + kPiece - 1) / kPiece;
     const long long most = copies * p.layers;
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
     const long long blocks = most > 152 * 8 / pieces ? 152 * 8 : most * pieces;
-    cfg.gridDim = dim3((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8));
-    cfg.blockDim = dim3(kCopyThreads);
-    cfg.stream = s;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, pages_copy_kernel, k);
+    const cudaError_t e = launch_next(pages_copy_kernel, (unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), kCopyThreads,
+                                      0, 1, k, s);
     note_launch();
     return e;
 }
