@@ -94,7 +94,7 @@ def _given(stream, t):
 def _call(device, fn, *args):
     """Runs a library call with the tensors' device current and its stream
     last in the arguments; raises on a non-OK status."""
-    if torch.cuda.current_device() != device:
+    if torch._C._cuda_getDevice() != device:
         with torch.cuda.device(device):
             return _call(device, fn, *args)
     status = fn(*args, torch._C._cuda_getCurrentRawStream(device))

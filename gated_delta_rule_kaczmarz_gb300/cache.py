@@ -151,16 +151,20 @@ def kla_kv4_read(pool, table, lens, T=None, total=None, cu_seqlens=None, dtype=t
                                 k_out, v_out, workspace, check_status=check_status)
     if (T is None) == (cu_seqlens is None) or (total is None) != (cu_seqlens is None):
         raise ValueError("T must be given, or total and cu_seqlens")
-    _, (hk, d, _, _) = _pool(pool, pool.get_device())
+    if pool.dim() != 4:
+        _pool(pool, pool.get_device())
+    hk, d = pool.shape[1], pool.shape[3] // 18
     shape = (table.shape[0], T, hk, d) if cu_seqlens is None else (total, hk, d)
-    out = [torch.empty(shape, dtype=dtype, device=pool.device) if x is None else x
-           for x in (k_out, v_out)]
-    for x, name in zip(out, ("k_out", "v_out")):
-        if x.shape != shape:
-            _refuse(x, name, dtype, pool.get_device(), shape)
-    _rows_call(load().kla_kv4_read, *out, pool, table, lens, cu_seqlens, (k_unit, v_unit),
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=pool.device)
+    elif k_out.shape != shape:
+        _refuse(k_out, "k_out", dtype, pool.get_device(), shape)
+    if v_out is None:
+        v_out = torch.empty_like(k_out) if k_out.is_contiguous() else \
+            torch.empty(shape, dtype=dtype, device=pool.device)
+    _rows_call(load().kla_kv4_read, k_out, v_out, pool, table, lens, cu_seqlens, (k_unit, v_unit),
                workspace, check_status)
-    return tuple(out)
+    return k_out, v_out
 
 
 def kla_kv4_attn(q, pool, table, lens, scale=None, k_unit=1.0, v_unit=1.0, o=None, lse=None,
@@ -209,18 +213,19 @@ def _layers(pool, n_pages):
     return pool.data_ptr(), layers, pool.numel() // max(1, layers * n) * pool.element_size()
 
 
-def _pages_call(fn, dev, like, args, sizes, workspace, check):
-    """args up to the sizes (S, columns, n_pages, n) of the workspace's, then it."""
+def _held(table, lens, refs):
+    """The device, the pages' number, the sizes of the table and the book's addresses."""
+    dev, n_pages, size = table.get_device(), refs.numel(), table.shape
+    rows, lengths = _book(table, lens, dev)
+    return dev, n_pages, size, (rows, lengths, _dense(refs, "refs", _INT, dev, (n_pages,)))
+
+
+def _run(fn, dev, like, args, sizes, workspace, check):
+    """A pages' call: its arguments, then the workspace for sizes (S, columns, n_pages, n)."""
     workspace, wsb = _workspace(dev, "kla_pages_workspace_size", sizes, like, workspace)
     _call(dev, fn, *args, _at(workspace), wsb)
     if check:
         _call(dev, _status, workspace, wsb)
-
-
-def _held(table, lens, refs):
-    dev = table.get_device()
-    n_pages = refs.numel()
-    return dev, n_pages, (*_book(table, lens, dev), _dense(refs, "refs", _INT, dev, (n_pages,)))
 
 
 def kla_pages_fork(table, lens, refs, src, dst, page, workspace=None, stream=None,
@@ -232,12 +237,11 @@ def kla_pages_fork(table, lens, refs, src, dst, page, workspace=None, stream=Non
         with _given(stream, table):
             return kla_pages_fork(table, lens, refs, src, dst, page, workspace,
                                   check_status=check_status)
-    dev, n_pages, book = _held(table, lens, refs)
+    dev, n_pages, (S, columns), book = _held(table, lens, refs)
     n = dst.numel()
     to = _dense(dst, "dst", _INT, dev, (n,))
     of = _dense(src, "src", _INT, dev, (n,))
-    S, columns = table.shape
-    _pages_call(load().kla_pages_fork, dev, table, (*book, of, to, S, columns, page, n_pages, n),
+    _run(load().kla_pages_fork, dev, table, (*book, of, to, S, columns, page, n_pages, n),
                 (S, columns, n_pages, n), workspace, check_status)
 
 
@@ -258,12 +262,11 @@ def kla_pages_grow(pool, table, lens, refs, n_new, page, workspace=None, stream=
         with _given(stream, table):
             return kla_pages_grow(pool, table, lens, refs, n_new, page, workspace,
                                   check_status=check_status)
-    dev, n_pages, book = _held(table, lens, refs)
-    S, columns = table.shape
+    dev, n_pages, (S, columns), book = _held(table, lens, refs)
     more = _dense(n_new, "n_new", _INT, dev, (S,))
     if pool.get_device() != dev:
         _refuse(pool, "pool", pool.dtype, dev, pool.shape)
-    _pages_call(load().kla_pages_grow, dev, table,
+    _run(load().kla_pages_grow, dev, table,
                 (*_layers(pool, n_pages), *book, more, S, columns, page, n_pages),
                 (S, columns, n_pages, 0), workspace, check_status)
 
@@ -277,13 +280,12 @@ def kla_pages_compact(pool, table, lens, refs, page, page_map=None, n_used=None,
         with _given(stream, table):
             return kla_pages_compact(pool, table, lens, refs, page, page_map, n_used, workspace,
                                      check_status=check_status)
-    dev, n_pages, book = _held(table, lens, refs)
-    S, columns = table.shape
+    dev, n_pages, (S, columns), book = _held(table, lens, refs)
     page_map, where = _out(page_map, "page_map", (n_pages,), _INT, refs)
     n_used, count = _out(n_used, "n_used", (1,), _INT, refs)
     if pool.get_device() != dev:
         _refuse(pool, "pool", pool.dtype, dev, pool.shape)
-    _pages_call(load().kla_pages_compact, dev, table,
+    _run(load().kla_pages_compact, dev, table,
                 (*_layers(pool, n_pages), *book, where, count, S, columns, page, n_pages),
                 (S, columns, n_pages, 0), workspace, check_status)
     return page_map, n_used
@@ -302,5 +304,5 @@ def kla_pages_copy(pool, src, dst, workspace=None, stream=None, check_status=Fal
     at, layers, size = _layers(pool, None)
     n_pages = pool.shape[1]
     of, to = _dense(src, "src", _INT, dev, (n,)), _dense(dst, "dst", _INT, dev, (n,))
-    _pages_call(load().kla_pages_copy, dev, pool, (at, layers, size, of, to, n_pages, n),
+    _run(load().kla_pages_copy, dev, pool, (at, layers, size, of, to, n_pages, n),
                 (0, 0, n_pages, n), workspace, check_status)
