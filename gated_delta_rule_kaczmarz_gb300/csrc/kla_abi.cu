@@ -840,9 +840,9 @@ kla_status check_pages(int S, int columns, int page, int n_pages) {
     if (S < 0 || columns < 0 || n_pages < 0 || page <= 0)
         return fail(KLA_ERR_INVALID_ARG, "sizes must not be negative, a page not empty (S=%d "
                     "columns=%d n_pages=%d page=%d)", S, columns, n_pages, page);
-    if ((long long)S * columns > INT32_MAX || (long long)columns * page > INT32_MAX)
-        return fail(KLA_ERR_UNSUPPORTED, "table too large (sequences times columns and columns times "
-                    "page must fit in int32)");
+    if ((long long)S * columns > INT32_MAX || (long long)columns * page > INT32_MAX - (1 << 16))
+        return fail(KLA_ERR_UNSUPPORTED, "table too large (sequences times columns, and columns times "
+                    "page and 2^16 more, must fit in int32)");
     return KLA_OK;
 }
 kla_status check_kv4(const void *pool, const int *table, const int *lens, int B, int Hk, int d, int page,

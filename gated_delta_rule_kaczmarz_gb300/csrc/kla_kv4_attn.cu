@@ -2,25 +2,32 @@
 //
 //   s = scale <q, k>,  p = exp2(s log2 e - base),  o = sum p v / sum p
 //
-// Work.  Keys go in tiles of 32 (two blocks of the cache).  A work item is a
-// sequence, key head and group of R query rows (the heads of a key head and the
-// call's tokens, packed); all items' tiles in a row are cut into equal parts, one
-// for each warp of one CTA an SM, so lengths may differ as they like.  A warp
+// Work.  Keys go in tiles of 64 (four blocks of the cache).  A work item is a
+// sequence, key head and group of 8 or 16 query rows (the heads of a key head and
+// the call's tokens, packed); all items' tiles in a row are cut into equal parts,
+// one for each warp of one CTA an SM, so lengths may differ as they like.  A warp
 // keeps its own running base, sums and outputs and brings its tiles by bulk copies
-// through a ring of its own: warps wait for nobody.  What the warps of a CTA hold
-// of the same item is joined in shared memory; items that more than one CTA had
-// are joined by a second kernel.
+// through a ring of its own: warps wait for nobody.  What the warps of a CTA hold of
+// the same item is joined in shared memory, a warp for each row; items that reach
+// over a CTA's edge, at most one for each CTA, are left to a second kernel.
 //
 // Products.  S^T = K Q^T and O^T = V^T P^T as m16n8k16: 16 keys (16 features)
-// against 8 query rows, so 4 rows of a decode batch fill half of an operand where
-// 16 rows a tile would leave it to a quarter.  A thread's 16 bytes of shared memory
-// are its part of the operand for all products of a block, whichever features the
-// hardware numbers so: Q is laid out and O written back in the same order.  Codes become fp16 by
-// the hardware's conversion and one multiplication by the scale, exactly.  q is
-// split into one (bf16) or two (fp32) fp16 terms after a power of two per row, p is
-// rounded to fp16 once (bf16) or split in two (fp32); sums are fp32.
+// against 8 query rows, so that 4 rows of a decode batch fill half of an operand
+// where 16 rows a tile would leave it to a quarter.  16 bytes of shared memory are a
+// thread's part of the operand for all products of a block, whichever features the
+// hardware takes them for: Q is laid out, and O written back, in the same order.
+// Codes become fp16 by the hardware's conversion and one multiplication by the
+// scale, exactly.  q is one (bf16) or two (fp32) fp16 terms after a power of two for
+// each row, p is rounded to fp16 once (bf16) or split in two (fp32); sums are fp32.
 //
-// Bound by HBM for long caches.
+// Measured (16 + 4 heads of 128, bf16, one token): 16 contexts of 16384 to 32768
+// 50.5 us, 256 of up to 4096 66.0, 0.70 of measured HBM bandwidth each.  The tiles
+// themselves run at 6.8 TB/s; 5.5 us pass before the first (length, table, keys: three
+// reads that wait for each other), 4.5 behind the last and 3 in the second kernel.
+// Streaming alone, without the products, took 3 us less.  221 KB of ring in flight an
+// SM are needed: 147 KB took 56 us, 110 KB 61 (an earlier form).  12 warps of 64 keys and
+// two stages; 16 warps of 32 keys 53.0, 11 of 64 53.0.  tcgen05 takes e2m1 with its
+// scales along the contracted axis: that is so of the keys, not of the values.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -49,7 +56,7 @@ constexpr float kTop = 7.f, kLag = 8.f;
 // NT: tiles of 8 query rows.
 template <int D, int NT, bool F32>
 struct Config {
-    static constexpr int kWarps = F32 || NT > 1 ? 8 : 12;        // as many as registers allow
+    static constexpr int kWarps = F32 || NT > 1 ? 8 : 12;        // as the registers allow
     static constexpr int kTile = 64;                             // keys of a stage
     static constexpr int kKeys = 32;                             // of a step of the softmax
     static constexpr int kBlocks = kTile / kBlock;
@@ -396,7 +403,7 @@ struct State {
         }
         // fp32: the tensor cores' sums are cut, not rounded, so a tile's are added to the others
         // by an addition that rounds (16 contexts of 32768 keys: 3.7e-6 of o, all of one sign,
-        // and @ so)
+        // and 5.3e-7 so)
         float apart[F32 ? NT : 1][F32 ? kSteps : 1][4] = {};
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -910,14 +917,12 @@ __global__ void __launch_bounds__(512) kv4_join_kernel(const __grid_constant__ A
 }
 
 // The unpacked path's check of the table, after the attention that writes the status word.
-__global__ void kv4_check_kernel(const int *table, const int *lens, int columns, int page, int n_pages,
-                                 unsigned *status) {
-    const int b = blockIdx.x;
-    const long long most = (long long)columns * page;
-    const int len = lens[b], held = (int)((len < 0 ? 0 : len < most ? len : most) + page - 1) / page;
+__global__ void kv4_check_kernel(const __grid_constant__ Args a) {
+    after_previous();
+    const int b = blockIdx.x, page = a.blocks * kBlock, held = (int)(((long long)length(a, b) + page - 1) / page);
     for (int c = threadIdx.x; c < held; c += blockDim.x) {
-        const int x = table[(long long)b * columns + c];
-        if (x < 0 || x >= n_pages) atomicMax(status, (unsigned)kDevBadTable);
+        const int x = a.table[(long long)b * a.columns + c];
+        if (x < 0 || x >= a.n_pages) atomicMax(a.status, (unsigned)kDevBadTable);
     }
 }
 
@@ -1063,10 +1068,12 @@ cudaError_t launch_kv4_attn(const Kv4Attn &p, cudaStream_t s) {
         dense.v = rows.v_out = ws + v;
         cudaError_t e = launch_kv4_rows(rows, true, s);
         if (e != cudaSuccess || (e = launch_attn_fwd(dense, s)) != cudaSuccess) return e;
-        kv4_check_kernel<<<p.B, 256, 0, s>>>(p.table, p.lens, p.columns, p.page, p.n_pages,
-                                             static_cast<unsigned *>(p.ws));
+        Args a{};
+        a.table = p.table; a.lens = p.lens; a.columns = p.columns; a.blocks = p.page / kBlock;
+        a.n_pages = p.n_pages; a.status = static_cast<unsigned *>(p.ws);
+        e = launch_next(kv4_check_kernel, p.B, 256, 0, 1, a, s);
         note_launch();
-        return cudaGetLastError();
+        return e;
     }
     const Plan x = plan_of(p);
     Args a{};

@@ -1,6 +1,6 @@
 // Rows of keys and values into the 4-bit cache and out of it.
 //
-//   scale = e4m3(min(max |x| / 6, 448)) over 16 features of x / unit
+//   scale = e4m3(min(max |x| * (1/6), 448)) over 16 features of x / unit, 1/6 in fp32
 //   code  = e2m1(x / unit / scale), nearest, ties to even, saturated at 6
 //
 // A thread takes 16 features of one head of a pair of tokens (an even position
@@ -147,10 +147,10 @@ __device__ __forceinline__ float quotient(float a, float b, float r) {
     return fmaf(fmaf(-q, b, a), r, q);
 }
 // x / unit in units of its scale; returns the scale's code (0, and what is not
-// finite: the codes have no meaning).  Such quotients decide border cases as exact
-// ones do: a midpoint of e4m3 times 6, and a border of e2m1 times a scale, have at
-// most 8 bits, so an fp32 that is not just that is a step or more away, and its
-// quotient by 6 at least 2/3, by a scale (significand at most 15/8) 8/15 of a step.
+// finite: the codes have no meaning).  Such quotients decide a code's border cases as
+// exact ones do: a border of e2m1 times a scale has at most 8 bits, so an x that is not
+// just that is a step of fp32 or more away, and its quotient by the scale, whose
+// significand is at most 15/8, at least 8/15 of a step.
 __device__ __forceinline__ unsigned scaled(float (&x)[16], float unit, float inv_unit) {
     float top = 0.f;
 #pragma unroll
@@ -160,7 +160,7 @@ __device__ __forceinline__ unsigned scaled(float (&x)[16], float unit, float inv
     top *= inv_unit;
     uint32_t code;
     asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\tcvt.u32.u16 %0, t;\n\t}"
-        : "=r"(code) : "f"(0.f), "f"(quotient(fminf(top, 8.f * 448.f), 6.f, 1.f / 6.f)));
+        : "=r"(code) : "f"(0.f), "f"(top * (1.f / 6.f)));
     if (!fine) return 0x7f;                 // the 16 read as NaN
     const uint32_t h = kv4::scales_to_half2(code);
     const float s = __half2float(__ushort_as_half((unsigned short)h)) * unit;

@@ -523,9 +523,10 @@ KLA_API int kla_attn_bwd_varlen(const void *q, long long q_stride, const void *k
  * of a token's head, and a unit for all keys and one for all values: powers of two
  * from 2^-32 to 2^32, part of the cache as its sizes are.  Of x:
  *
- *     scale = e4m3(min(max |x / unit| / 6, 448)),  code = e2m1(x / unit / scale)
+ *     scale = e4m3(min(max |x / unit| * (1/6), 448)),  code = e2m1(x / unit / scale)
  *
- * both to nearest, ties to even, codes saturated; a scale of 0 has codes of 0,
+ * both to nearest, ties to even, codes saturated, the product with the fp32 nearest
+ * to 1/6 rounded to fp32; a scale of 0 has codes of 0,
  * and 16 features of which one is not finite read as NaN.
  * Pages.  A page holds `page` tokens (a multiple of 16) of Hk heads:
  * [Hk][page / 16][18 d] bytes, kla_kv4_page_bytes(...) in all.  The 18 d bytes

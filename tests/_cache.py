@@ -31,7 +31,9 @@ def quantise(x, unit):
     with np.errstate(invalid="ignore"):
         top = np.abs(y).max(-1)
     fine = np.isfinite(y).all(-1)
-    s = np.where(fine, _nearest(np.where(fine, top, 0.0) / 6, SCALES), 127)
+    with np.errstate(over="ignore"):          # a product of two fp32 is exact in 64 bits
+        sixth = (np.where(fine, top, 0.0) * np.float64(np.float32(1 / 6))).astype(np.float32)
+    s = np.where(fine, _nearest(np.minimum(sixth.astype(np.float64), 448.0), SCALES), 127)
     value = np.where(fine, SCALES[np.minimum(s, 126)], 0.0)[..., None]
     a = np.divide(np.abs(y), value, out=np.zeros_like(y), where=(value > 0) & fine[..., None])
     code = _nearest(a, LEVELS) + 8 * (np.signbit(y) & (value > 0) & fine[..., None])
