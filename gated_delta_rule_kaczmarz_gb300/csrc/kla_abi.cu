@@ -866,7 +866,7 @@ kla_status check_kv4(const void *pool, const int *table, const int *lens, int B,
             return fail(KLA_ERR_INVALID_ARG, "k_unit and v_unit must be powers of two from 2^-32 to 2^32");
     }
     if (B == 0) return KLA_OK;
-    if (!lens || ((!table || !pool) && n_pages > 0 && columns > 0))
+    if (!lens || (!table && columns > 0) || (!pool && n_pages > 0 && columns > 0))
         return fail(KLA_ERR_INVALID_ARG, "pool, table and lens must be non-null");
     if (!aligned16(pool) || !aligned4(table) || !aligned4(lens))
         return fail(KLA_ERR_INVALID_ARG, "the pool must be 16-byte aligned, tables and lengths 4-byte");

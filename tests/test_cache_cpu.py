@@ -35,6 +35,7 @@ def _attn(**over):
 
 SHARED = [
     (dict(pool=None), INVALID), (dict(table=None), INVALID), (dict(lens=None), INVALID),
+    (dict(table=None, n_pages=0), INVALID),
     (dict(pool=FAKE + 8), INVALID), (dict(table=FAKE + 2), INVALID), (dict(lens=FAKE + 1), INVALID),
     (dict(k_unit=0.3), INVALID), (dict(v_unit=0.0), INVALID), (dict(k_unit=-1.0), INVALID),
     (dict(v_unit=float("nan")), INVALID), (dict(k_unit=2.0 ** 33), INVALID),
@@ -42,6 +43,7 @@ SHARED = [
     (dict(page=0), INVALID), (dict(n_pages=-1), INVALID), (dict(columns=-1), INVALID),
     (dict(dtype=2), INVALID), (dict(d=96), UNSUPPORTED), (dict(page=24), UNSUPPORTED),
     (dict(columns=1 << 30), UNSUPPORTED), (dict(n_pages=2 ** 31 - 1), UNSUPPORTED),
+    (dict(columns=(1 << 26) - 1), UNSUPPORTED),
     (dict(ws=FAKE + 16), INVALID), (dict(wsb=64), WORKSPACE),
 ]
 

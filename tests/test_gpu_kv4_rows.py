@@ -200,6 +200,14 @@ def test_what_the_device_refuses():
             kla.kla_kv4_append(k[0], k[0], pool, table, lens, check_status=True,
                                cu_seqlens=torch.tensor(cu).int().cuda())
         assert e.value.status == binding.KLA_ERR_INVALID_ARG
+    # a pool without pages: no row has a place, and rows are read as zeros
+    none = pool[:0]
+    with pytest.raises(kla.KlaError):
+        kla.kla_kv4_append(k, k, none, table[:1], lens[:1], check_status=True)
+    with pytest.raises(kla.KlaError):
+        kla.kla_kv4_read(none, table[:1], lens[:1], T=4, check_status=True)
+    assert not any(x.any() for x in kla.kla_kv4_read(none, table[:1], lens[:1], T=4))
+    assert not any(x.any() for x in kla.kla_kv4_read(none, table[:1, :0], lens[:1], T=4, check_status=True))
     # lengths that no row of the table holds are clamped
     kla.kla_kv4_append(k, k, pool, table[:1], torch.tensor([1 << 30]).int().cuda(), check_status=True)
     kla.kla_kv4_append(k, k, pool, table[:1], torch.tensor([-5]).int().cuda(), check_status=True)
