@@ -835,14 +835,19 @@ int kla_attn_bwd_varlen(const void *q, long long q_stride, const void *k, long l
 }  // extern "C"
 
 namespace {
-// Sizes of a cache's book.  Tables and pages are numbered in 32 bits.
+// Sizes of a cache's book.  Tables and pages are numbered in 32 bits, and a thread's
+// number goes past their end by less than kPast.
+constexpr int kPast = 1 << 16;
 kla_status check_pages(int S, int columns, int page, int n_pages) {
     if (S < 0 || columns < 0 || n_pages < 0 || page <= 0)
         return fail(KLA_ERR_INVALID_ARG, "sizes must not be negative, a page not empty (S=%d "
                     "columns=%d n_pages=%d page=%d)", S, columns, n_pages, page);
-    if ((long long)S * columns > INT32_MAX || (long long)columns * page > INT32_MAX - (1 << 16))
+    if ((long long)S * columns > INT32_MAX || (long long)columns * page > INT32_MAX - kPast)
         return fail(KLA_ERR_UNSUPPORTED, "table too large (sequences times columns, and columns times "
                     "page and 2^16 more, must fit in int32)");
+    if (S > INT32_MAX - kPast || n_pages > INT32_MAX - kPast)
+        return fail(KLA_ERR_UNSUPPORTED, "too many sequences or pages (with 2^16 more they must fit in "
+                    "int32; S=%d n_pages=%d)", S, n_pages);
     return KLA_OK;
 }
 kla_status check_kv4(const void *pool, const int *table, const int *lens, int B, int Hk, int d, int page,
@@ -933,6 +938,8 @@ kla_status kv4_attn_sizes(kla::Kv4Attn &p, int B, int Tq, int Hq, int Hk, int d,
 }
 
 kla_status pages_call(kla::Pages &p, int n, void *workspace, size_t workspace_bytes) {
+    if (n > INT32_MAX - kPast)
+        return fail(KLA_ERR_UNSUPPORTED, "too many entries (with 2^16 more they must fit in int32; n=%d)", n);
     const kla_status st = check_workspace(workspace, workspace_bytes,
                                           kla::pages_workspace_bytes(p.S, p.columns, p.n_pages, n));
     if (st != KLA_OK) return st;
@@ -1034,7 +1041,7 @@ int kla_kv4_attn(const void *q, long long q_stride, const void *pool, const int 
 }
 
 size_t kla_pages_workspace_size(int S, int columns, int n_pages, int n) {
-    if (n < 0 || check_pages(S, columns, 1, n_pages) != KLA_OK) return 0;
+    if (n < 0 || n > INT32_MAX - kPast || check_pages(S, columns, 1, n_pages) != KLA_OK) return 0;
     return kla::pages_workspace_bytes(S, columns, n_pages, n);
 }
 

@@ -105,7 +105,13 @@ ENDS = [(dict(ws=None), WORKSPACE), (dict(wsb=256), WORKSPACE), (dict(ws=FAKE + 
     ("fork", dict(n=1 << 30), UNSUPPORTED), ("fork", dict(src=FAKE + 1), INVALID),
     ("grow", dict(more=None), INVALID), ("compact", dict(where=None), INVALID),
     ("compact", dict(used=None), INVALID), ("copy", dict(src=None), INVALID),
-    ("copy", dict(n=-1), INVALID)])
+    ("copy", dict(n=-1), INVALID),
+    # numbers that a thread's next one would pass in 32 bits
+    *[(name, dict(n_pages=2 ** 31 - 2 ** 16), UNSUPPORTED) for name in ("fork", "grow", "compact", "copy")],
+    ("grow", dict(S=2 ** 31 - 2 ** 16, columns=1), UNSUPPORTED),
+    ("compact", dict(S=2 ** 31 - 2 ** 16, columns=1), UNSUPPORTED),
+    ("copy", dict(n=2 ** 31 - 2 ** 16), UNSUPPORTED),
+    ("fork", dict(n=2 ** 31 - 2 ** 16, columns=0), UNSUPPORTED)])
 def test_pages_refuse(name, over, status):
     assert _pages(name, **over) == status
     assert binding.load().kla_last_error_message().decode() != ""
@@ -132,6 +138,8 @@ def test_sizes():
     assert kla.kla_kv4_attn_workspace_size(2, 1, 4, 2, 64, 32, 4) > 256
     assert kla.kla_kv4_attn_workspace_size(2, 0, 4, 2, 64, 32, 4) == 0
     assert kla.kla_kv4_attn_workspace_size(2, 1, 3, 2, 64, 32, 4) == 0
+    for sizes in ((2 ** 31 - 2 ** 16, 1, 1, 0), (1, 1, 2 ** 31 - 2 ** 16, 0), (0, 0, 1, 2 ** 31 - 2 ** 16)):
+        assert kla.kla_pages_workspace_size(*sizes) == 0
     assert kla.kla_pages_workspace_size(3, 4, 100, 2) >= 256 + 4 * 100 * 4
     assert binding.load().kla_status_str(binding.KLA_ERR_PAGES) == b"not enough free pages"
 
