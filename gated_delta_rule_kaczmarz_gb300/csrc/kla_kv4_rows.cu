@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_const
         if (p.status) *p.status = kDevBadSeqlens;
         return;
     }
+    if (pair > s.rows / 2) return;               // (a table that does not hold may ask for any)
     // the pair that holds the sequence's first new position, and those behind it
     const int first = s.pos0 < 0 ? 0 : s.pos0, pos = (first & ~1) + 2 * pair, end = s.pos0 + s.rows;
     const bool even = pos >= first && pos < end, odd = pos + 1 < end;
@@ -294,6 +295,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
         if (p.status) *p.status = kDevBadSeqlens;
         return;
     }
+    if (pair > s.rows / 2) return;
     const int pos = (s.pos0 & ~1) + 2 * pair, end = s.pos0 + s.rows;
     if (pos >= end) return;
     const bool want[2] = {pos >= s.pos0, pos + 1 < end};
@@ -356,8 +358,8 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
 template <typename T, int D>
 cudaError_t launch(const Work &w, bool read, cudaStream_t s) {
     const long long n = (long long)w.slots * w.p.Hk * (D / 16), blocks = (n + kThreads - 1) / kThreads;
-    const cudaError_t e = launch_next(read ? kv4_read_kernel<T, D> : kv4_append_kernel<T, D>, (unsigned)blocks, kThreads,
-                                      0, 1, w, s);
+    const cudaError_t e = launch_next(read ? kv4_read_kernel<T, D> : kv4_append_kernel<T, D>, (unsigned)blocks,
+                                      kThreads, 0, 1, w, s);
     note_launch();
     return e;
 }

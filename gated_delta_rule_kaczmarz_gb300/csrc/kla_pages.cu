@@ -53,7 +53,9 @@ __device__ __forceinline__ int length_of(const Book &k, int s) {
     const int n = k.p.lens[s];
     return n < 0 ? 0 : (n < most ? n : (int)most);
 }
-__device__ __forceinline__ int pages_of(const Book &k, int len) { return (int)(((long long)len + k.p.page - 1) / k.p.page); }
+__device__ __forceinline__ int pages_of(const Book &k, int len) {
+    return (int)(((long long)len + k.p.page - 1) / k.p.page);
+}
 __device__ __forceinline__ bool is_page(const Book &k, int p) { return p >= 0 && p < k.p.n_pages; }
 
 // Sums of N numbers over the CTA, and of the threads before this one.
