@@ -237,7 +237,9 @@ struct State {
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
                 mul[nt][z] = __shfl_sync(0xffffffffu, down, (2 * c + z) * 4);
-                limit[nt][z] = first + divided(group * 8 * NT + nt * 8 + 2 * c + z, a.by_G);
+                // (rows behind the last would see keys that are not there: what their scores
+                // are then must not move the base)
+                limit[nt][z] = min(first + divided(group * 8 * NT + nt * 8 + 2 * c + z, a.by_G), len);
                 m[nt][z] = -INFINITY;
                 l[nt][z] = 0.f;
             }
@@ -649,7 +651,8 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
                 }
                 block = ((unsigned)page * a.Hk + divided(ahead.item, a.by_groups)) * a.blocks + nb - column * a.blocks;
             }
-            const unsigned src = __shfl_sync(0xffffffffu, block, C::kBlocks * (ahead.tile - looked) + lane % C::kBlocks);
+            const int from_lane = C::kBlocks * (ahead.tile - looked) + lane % C::kBlocks;
+            const unsigned src = __shfl_sync(0xffffffffu, block, from_lane);
             const int there = min(C::kBlocks, (ahead.len - ahead.tile * C::kTile + kBlock - 1) / kBlock);
             if (lane == 0) tc::mbar_expect_tx(&bars[warp][slot], there * Layout<D>::kBytes);
             __syncwarp();
@@ -658,7 +661,8 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
                               a.pool + (unsigned long long)src * Layout<D>::kBytes, Layout<D>::kBytes,
                               &bars[warp][slot]);
             if (fresh) {                             // its query rows into L2
-                const int head = divided(ahead.item, a.by_groups), row = (ahead.item - head * a.groups) * C::kRows + lane;
+                const int head = divided(ahead.item, a.by_groups);
+                const int row = (ahead.item - head * a.groups) * C::kRows + lane;
                 if (lane < C::kRows && row < a.rows) {
                     const T *q = query<T>(a, ahead.seq, head, row);
 #pragma unroll
@@ -926,10 +930,17 @@ __global__ void kv4_check_kernel(const __grid_constant__ Args a) {
     }
 }
 
-// Without any key: zeros, from a launch that has no table to read.
-__global__ void kv4_no_keys_kernel(uint4 *o, long long n, float *lse, long long rows, unsigned *status) {
+// Without any key: zeros, from a launch that has no table to read.  lens: of a table
+// with columns, whose entries name no page then.
+__global__ void kv4_no_keys_kernel(uint4 *o, long long n, float *lse, long long rows, unsigned *status,
+                                   const int *lens, int B) {
     const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i == 0) *status = kDevOk;
+    if (blockIdx.x == 0) {
+        bool some = false;
+        for (int b = threadIdx.x; lens && b < B; b += blockDim.x) some = some || lens[b] > 0;
+        some = __syncthreads_or(some);
+        if (i == 0) *status = some ? kDevBadTable : kDevOk;
+    }
     if (i < n) o[i] = make_uint4(0, 0, 0, 0);
     if (lse && i < rows) lse[i] = -INFINITY;
 }
@@ -1054,7 +1065,8 @@ cudaError_t launch_kv4_attn(const Kv4Attn &p, cudaStream_t s) {
     if (p.n_pages == 0 || p.columns == 0) {
         const long long rows = (long long)p.B * p.Tq * p.Hq, n = rows * p.d * (p.dtype == 1 ? 2 : 4) / 16;
         kv4_no_keys_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(static_cast<uint4 *>(p.o), n, p.lse, rows,
-                                                                      static_cast<unsigned *>(p.ws));
+                                                                      static_cast<unsigned *>(p.ws),
+                                                                      p.columns > 0 ? p.lens : nullptr, p.B);
         note_launch();
         return cudaGetLastError();
     }

@@ -571,7 +571,9 @@ KLA_API int kla_kv4_read(void *k, long long k_stride, void *v, long long v_strid
  * Causal attention over such a cache: kla_attn_fwd with k_lens = lens, q [B, Tq,
  * Hq, d] (rows q_stride elements apart), o and lse (or NULL) as there, keys and
  * values as kla_kv4_read gives them.  A query that sees no key has o = 0 and
- * lse = -infinity.  What lies behind a sequence's last position may be anything.
+ * lse = -infinity.  What lies behind a sequence's last position may be anything; its
+ * own rows must be finite for the queries before them to stay finite, as there.
+ * o must not overlap q.
  * scale * k_unit from 1e-37 to 2e38.  Scores, statistics and sums are fp32;
  * exp(S - m) is rounded once as an operand of the second product (bf16: to fp16,
  * fp32: to 22 bits), q of fp32 to 22 bits; keys and values are exact.
@@ -591,6 +593,7 @@ KLA_API int kla_kv4_attn(const void *q, long long q_stride, const void *pool, co
  * above (`page` any positive number) and refs [n_pages], the number of sequences
  * that hold each page.  A page with refs 0 is free.  Pages lie in `layers` pools
  * of n_pages * page_bytes bytes one behind the other (page_bytes a multiple of 16).
+ * S, n_pages and n are at most 2^31 - 2^16 - 1.
  * kla_pages_fork: for all f at once, sequence dst[f] becomes what src[f] was before
  *   the call: its length and its pages, shared; the rest of its table row becomes -1.
  *   src[f] = -1, or src NULL: it becomes empty.  refs follow, so pages that nobody

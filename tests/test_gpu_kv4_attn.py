@@ -196,7 +196,35 @@ def test_no_pages():
                         (_cache.garbage(4, 2, 1, 18 * 64).cuda(), torch.zeros(2, 0).int().cuda())):
         o, lse = kla.kla_kv4_attn(q, pool, table, lens, check_status=True)
         assert not o.any() and bool((lse == -math.inf).all())
+        some = torch.tensor([0, 1]).int().cuda()
+        o, lse = kla.kla_kv4_attn(q, pool, table, some)
+        assert not o.any() and bool((lse == -math.inf).all())
+        if table.shape[1]:                        # an entry that names no page
+            with pytest.raises(kla.KlaError):
+                kla.kla_kv4_attn(q, pool, table, some, check_status=True)
+        else:                                     # the length is clamped
+            kla.kla_kv4_attn(q, pool, table, some, check_status=True)
     none = kla.kla_kv4_attn(q[:0], pool, table[:0], lens[:0], check_status=True)
     assert none[0].shape == (0, 3, 4, 64)
     none = kla.kla_kv4_attn(q[:, :0], pool, table, lens, check_status=True)
     assert none[0].shape == (2, 0, 4, 64)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("hq,Tq", [(2, 1), (6, 3), (40, 7), (40, 13)])
+def test_what_lies_behind_a_sequence_changes_no_bit(hq, Tq, dtype):
+    """Groups of fewer rows than a tile has, lengths that end inside a block, and other
+    bytes behind them."""
+    lens, d, page = [5, 70, 131, 300], 64, 32
+    q, (pool, table, length), _, how = _case(lens, Tq, hq, 2, d, page, dtype)
+    ref = kla.kla_kv4_attn(q.cuda(), pool, table, length, **how)
+    for seed in range(3):
+        other = _cache.Pages(_cache.garbage(*pool.shape, seed=20 + seed), d)
+        old = _cache.Pages(pool.cpu(), d)
+        for b, n in enumerate(lens):
+            for t in range(n):
+                for h in range(2):
+                    p = int(table[b, t // page])
+                    other.put(p, h, t % page, *old.get(p, h, t % page))
+        got = kla.kla_kv4_attn(q.cuda(), torch.from_numpy(other.b).cuda(), table, length, **how)
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
