@@ -58,5 +58,6 @@ from .cache import (  # noqa: F401
     kla_pages_fork,
     kla_pages_free,
     kla_pages_grow,
+    kla_pages_trim,
     kla_pages_workspace_size,
 )

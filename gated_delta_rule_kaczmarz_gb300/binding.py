@@ -151,6 +151,8 @@ def load(build_if_stale: bool = True) -> ctypes.CDLL:
         lib.kla_pages_fork.argtypes = [ip, ip, ip, ip, ip, I, I, I, I, I, vp, Z, vp]
         lib.kla_pages_grow.restype = I
         lib.kla_pages_grow.argtypes = [vp, I, L, ip, ip, ip, ip, I, I, I, I, vp, Z, vp]
+        lib.kla_pages_trim.restype = I
+        lib.kla_pages_trim.argtypes = [ip, ip, ip, ip, I, I, I, I, vp, Z, vp]
         lib.kla_pages_compact.restype = I
         lib.kla_pages_compact.argtypes = [vp, I, L, ip, ip, ip, ip, ip, I, I, I, I, vp, Z, vp]
         lib.kla_pages_copy.restype = I

@@ -1,6 +1,6 @@
 """Binding of the paged key/value cache in 4 bits: rows appended and read back,
-attention over it, and the pages' operators (fork, free, growth, compaction,
-copies).
+attention over it, and the pages' operators (fork, free, growth, trimming,
+compaction, copies).
 
 The same rules as in ``attention``: argument marshalling only, a non-OK status
 raises ``KlaError``, and a call runs on the device of its tensors.  A cache is a
@@ -8,7 +8,8 @@ pool of pages, uint8 [n_pages, Hk, page / 16, 18 d] (``kla_kv4_pool``), and its
 book: table int32 [B, columns] of page numbers, lens int32 [B], refs int32
 [n_pages] with the number of sequences that hold each page.  A step of a decode
 loop: ``kla_pages_grow`` makes room, ``kla_kv4_append`` writes the new rows,
-``kla_kv4_attn`` attends over them.
+``kla_kv4_attn`` attends over them, and ``kla_pages_trim`` takes back the positions of
+drafted tokens that are not taken.
 """
 from __future__ import annotations
 
@@ -269,6 +270,20 @@ def kla_pages_grow(pool, table, lens, refs, n_new, page, workspace=None, stream=
     _run(load().kla_pages_grow, dev, table,
                 (*_layers(pool, n_pages), *book, more, S, columns, page, n_pages),
                 (S, columns, n_pages, 0), workspace, check_status)
+
+
+def kla_pages_trim(table, lens, refs, n_cut, page, workspace=None, stream=None,
+                   check_status=False):
+    """The last n_cut[s] (int32 [S]) positions of every sequence are given up, drafted
+    tokens that were not taken; pages that nobody holds any more are free."""
+    if stream is not None:
+        with _given(stream, table):
+            return kla_pages_trim(table, lens, refs, n_cut, page, workspace,
+                                  check_status=check_status)
+    dev, n_pages, (S, columns), book = _held(table, lens, refs)
+    cut = _dense(n_cut, "n_cut", _INT, dev, (S,))
+    _run(load().kla_pages_trim, dev, table, (*book, cut, S, columns, page, n_pages),
+         (S, columns, n_pages, 0), workspace, check_status)
 
 
 def kla_pages_compact(pool, table, lens, refs, page, page_map=None, n_used=None, workspace=None,

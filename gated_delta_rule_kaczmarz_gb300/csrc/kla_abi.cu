@@ -1080,6 +1080,20 @@ int kla_pages_grow(void *pool, int layers, long long page_bytes, int *table, int
     return e == cudaSuccess ? ok() : cuda_fail(e, "growth launch");
 }
 
+int kla_pages_trim(int *table, int *lens, int *refs, const int *n_cut, int S, int columns, int page,
+                   int n_pages, void *workspace, size_t workspace_bytes, void *stream) {
+    kla::Pages p{};
+    p.table = table; p.lens = lens; p.refs = refs; p.S = S; p.columns = columns; p.page = page;
+    p.n_pages = n_pages; p.more = n_cut;
+    kla_status st = check_book(p);
+    if (st != KLA_OK) return st;
+    if (S > 0 && !n_cut) return fail(KLA_ERR_INVALID_ARG, "n_cut must be non-null");
+    if (!aligned4(n_cut)) return fail(KLA_ERR_INVALID_ARG, "n_cut must be 4-byte aligned");
+    if ((st = pages_call(p, 0, workspace, workspace_bytes)) != KLA_OK) return st;
+    const cudaError_t e = kla::launch_pages_trim(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "trim launch");
+}
+
 int kla_pages_compact(void *pool, int layers, long long page_bytes, int *table, const int *lens,
                       int *refs, int *page_map, int *n_used, int S, int columns, int page,
                       int n_pages, void *workspace, size_t workspace_bytes, void *stream) {

@@ -173,7 +173,7 @@ struct Pages {
     int S, columns, page, n_pages;
     const int *src, *dst;           // fork: n entries; copy: pages
     int n;
-    const int *more;                // grow: [S]
+    const int *more;                // grow, trim: [S]
     int *page_map, *n_used;         // compact
     void *pool;                     // [layers][n_pages][page_bytes]
     int layers;
@@ -184,6 +184,7 @@ size_t pages_workspace_bytes(int S, int columns, int n_pages, int n);
 bool pages_too_many(int S);       // sequences of a fork
 cudaError_t launch_pages_fork(const Pages &p, cudaStream_t s);
 cudaError_t launch_pages_grow(const Pages &p, cudaStream_t s);
+cudaError_t launch_pages_trim(const Pages &p, cudaStream_t s);
 cudaError_t launch_pages_compact(const Pages &p, cudaStream_t s);
 cudaError_t launch_pages_copy(const Pages &p, cudaStream_t s);
 

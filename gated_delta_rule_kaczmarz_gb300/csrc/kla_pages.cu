@@ -283,6 +283,46 @@ __global__ void __launch_bounds__(kThreads) pages_grow_kernel(const __grid_const
     }
 }
 
+// ------------------------------------------------------------------ trimming
+// The last more[s] positions of a sequence are given up, with the pages behind those
+// that are left: a warp to a sequence.
+__global__ void __launch_bounds__(kThreads) pages_trim_kernel(const __grid_constant__ Book k) {
+    const Pages &p = k.p;
+    const int tid = threadIdx.x, lane = tid % 32;
+    after_previous();
+    let_next_start();
+    bool bad = false;                                    // every CTA looks all of them over
+    for (int s = tid; s < p.S; s += kThreads) {
+        const int n = p.more[s];
+        bad = bad || n < 0 || n > length_of(k, s);
+    }
+    bad = __syncthreads_or(bad);
+    all_barrier();                                       // (before a length changes)
+    if (bad) {
+        if (thread_of_all() == 0) k.sh->status = kDevBadTable;
+        return;
+    }
+    for (int s = thread_of_all() / 32; s < p.S; s += threads_of_all() / 32) {
+        const int n = p.more[s];
+        if (n == 0) continue;
+        const int len = length_of(k, s), held = pages_of(k, len);
+        int *row = p.table + (long long)s * p.columns;
+        for (int c = pages_of(k, len - n) + lane; c < held; c += 32) {
+            const int x = row[c];
+            if (is_page(k, x)) atomicAdd(&p.refs[x], -1);
+            else bad = true;
+            row[c] = -1;
+        }
+        __syncwarp();
+        if (lane == 0) p.lens[s] = len - n;
+    }
+    bad = __syncthreads_or(bad);
+    if (tid == 0) k.sh->sums[0][cta_of_all()] = bad;
+    all_barrier();
+    int before;
+    if (thread_of_all() == 0) k.sh->status = total_of(k.sh->sums[0], before) ? kDevBadTable : kDevOk;
+}
+
 // ------------------------------------------------------------------ compaction
 __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_constant__ Book k) {
     const Pages &p = k.p;
@@ -450,8 +490,10 @@ Book book_of(const Pages &p) {
 // and 6.3, of 64 8.6 and 6.2; growth among 16384 pages 7.4 and 8.1, 32768 7.9 and 8.0,
 // 131072 13.4 and 9.5 (a sequence that grows counts as 128 of them: of 256 that do among
 // 3200 pages 18.5 and 11.5); compaction of 2048 pages with a table of 32 x 64 7.1 and 8.6, 4096
-// with 64 x 64 8.7 and 8.7, 8192 with 128 x 64 12.3 and 8.9.
-constexpr long long kForkEntries = 2048, kGrowEntries = 32768, kCompactEntries = 8192, kCopyEntries = 4096;
+// with 64 x 64 8.7 and 8.7, 8192 with 128 x 64 12.3 and 8.9; trimming 64 sequences 2.1 and 2.5,
+// 256 5.9 and 3.1.
+constexpr long long kForkEntries = 2048, kGrowEntries = 32768, kCompactEntries = 8192, kCopyEntries = 4096,
+                    kTrimEntries = 64;
 
 cudaError_t run(void (*kernel)(const Book), const Book &k, long long entries, long long most, cudaStream_t s) {
     const bool one = entries <= most;
@@ -490,6 +532,9 @@ cudaError_t launch_pages_grow(const Pages &p, cudaStream_t s) {
     const Book k = book_of(p);
     const cudaError_t e = run(pages_grow_kernel, k, p.n_pages + 128LL * p.S, kGrowEntries, s);
     return e != cudaSuccess ? e : copy(k, p.S, s);
+}
+cudaError_t launch_pages_trim(const Pages &p, cudaStream_t s) {
+    return run(pages_trim_kernel, book_of(p), p.S, kTrimEntries, s);
 }
 cudaError_t launch_pages_compact(const Pages &p, cudaStream_t s) {
     const Book k = book_of(p);

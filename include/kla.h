@@ -607,6 +607,10 @@ KLA_API int kla_kv4_attn(const void *q, long long q_stride, const void *pool, co
  *   from the next call on.  Without enough free pages nothing changes
  *   and KLA_ERR_PAGES is reported; a negative n_new or a row that is too short for
  *   it refuses the call: nothing changes.
+ * kla_pages_trim: the last n_cut[s] positions of every sequence are given up (drafted
+ *   tokens that were not taken): lens[s] -= n_cut[s], and the pages behind those that
+ *   are left lose this holder; their entries become -1.  A number outside 0..lens[s]
+ *   refuses the call: nothing changes.
  * kla_pages_compact: pages in use from number n_used on (n_used pages are in use)
  *   move to the free ones below it, in order, with their contents; table and refs
  *   follow.  page_map [n_pages]: where each page is now, -1 for a free one.  n_used:
@@ -626,6 +630,9 @@ KLA_API int kla_pages_fork(int *table, int *lens, int *refs, const int *src, con
 KLA_API int kla_pages_grow(void *pool, int layers, long long page_bytes, int *table, int *lens,
                            int *refs, const int *n_new, int S, int columns, int page, int n_pages,
                            void *workspace, size_t workspace_bytes, void *stream);
+KLA_API int kla_pages_trim(int *table, int *lens, int *refs, const int *n_cut, int S, int columns,
+                           int page, int n_pages, void *workspace, size_t workspace_bytes,
+                           void *stream);
 KLA_API int kla_pages_compact(void *pool, int layers, long long page_bytes, int *table,
                               const int *lens, int *refs, int *page_map, int *n_used, int S,
                               int columns, int page, int n_pages, void *workspace,

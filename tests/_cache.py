@@ -195,6 +195,12 @@ def grow(table, lens, refs, more, page):
     return table, lens, after, copies
 
 
+def trim(table, lens, cut, page):
+    table = [[-1 if -(-(n - x) // page) <= c < -(-n // page) else p for c, p in enumerate(row)]
+             for row, n, x in zip(table, lens, cut)]
+    return table, [n - x for n, x in zip(lens, cut)]
+
+
 def compact(table, lens, refs, page):
     """(table, refs, page_map, moves)."""
     n_used = sum(n > 0 for n in refs)

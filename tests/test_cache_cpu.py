@@ -83,6 +83,7 @@ def _pages(name, **over):
     sizes, end = [a["S"], a["columns"], a["page"], a["n_pages"]], [a["ws"], a["wsb"], None]
     args = {"fork": [*book, a["src"], a["dst"], *sizes, a["n"]],
             "grow": [*pool, *book, a["more"], *sizes],
+            "trim": [*book, a["more"], *sizes],
             "compact": [*pool, *book, a["where"], a["used"], *sizes],
             "copy": [*pool, a["src"], a["dst"], a["n_pages"], a["n"]]}
     return getattr(binding.load(), "kla_pages_" + name)(*args[name], *end)
@@ -100,16 +101,20 @@ ENDS = [(dict(ws=None), WORKSPACE), (dict(wsb=256), WORKSPACE), (dict(ws=FAKE + 
 @no_gpu_only
 @pytest.mark.parametrize("name,over,status", [
     *[("fork", *x) for x in BOOK + ENDS], *[("grow", *x) for x in BOOK + POOL + ENDS],
+    *[("trim", *x) for x in BOOK + ENDS],
     *[("compact", *x) for x in BOOK + POOL + ENDS], *[("copy", *x) for x in POOL + ENDS],
     ("fork", dict(dst=None), INVALID), ("fork", dict(n=-1), INVALID),
     ("fork", dict(n=1 << 30), UNSUPPORTED), ("fork", dict(src=FAKE + 1), INVALID),
-    ("grow", dict(more=None), INVALID), ("compact", dict(where=None), INVALID),
+    ("grow", dict(more=None), INVALID), ("trim", dict(more=None), INVALID),
+    ("trim", dict(more=FAKE + 2), INVALID), ("compact", dict(where=None), INVALID),
     ("compact", dict(used=None), INVALID), ("copy", dict(src=None), INVALID),
     ("copy", dict(n=-1), INVALID),
     # numbers that a thread's next one would pass in 32 bits
-    *[(name, dict(n_pages=2 ** 31 - 2 ** 16), UNSUPPORTED) for name in ("fork", "grow", "compact", "copy")],
+    *[(name, dict(n_pages=2 ** 31 - 2 ** 16), UNSUPPORTED) for name in ("fork", "grow", "trim", "compact",
+                                                                         "copy")],
     ("grow", dict(S=2 ** 31 - 2 ** 16, columns=1), UNSUPPORTED),
     ("compact", dict(S=2 ** 31 - 2 ** 16, columns=1), UNSUPPORTED),
+    ("trim", dict(S=2 ** 31 - 2 ** 16, columns=1), UNSUPPORTED),
     ("copy", dict(n=2 ** 31 - 2 ** 16), UNSUPPORTED),
     ("fork", dict(n=2 ** 31 - 2 ** 16, columns=0), UNSUPPORTED)])
 def test_pages_refuse(name, over, status):
@@ -121,7 +126,7 @@ def test_pages_refuse(name, over, status):
 def test_injected_launch_fault(monkeypatch):
     monkeypatch.setenv("KLA_FAULT_INJECT", "launch")
     calls = [lambda: _rows("kla_kv4_append"), lambda: _rows("kla_kv4_read"), _attn]
-    calls += [lambda n=n: _pages(n) for n in ("fork", "grow", "compact", "copy")]
+    calls += [lambda n=n: _pages(n) for n in ("fork", "grow", "trim", "compact", "copy")]
     for call in calls:
         assert call() == binding.KLA_ERR_CUDA
         assert "injected" in binding.load().kla_last_error_message().decode()
@@ -161,6 +166,7 @@ def test_the_binding_refuses():
     for call in (lambda: kla.kla_pages_fork(table, lens, refs, some, some, 16),
                  lambda: kla.kla_pages_free(table, lens, refs, some, 16),
                  lambda: kla.kla_pages_grow(pool[None], table, lens, refs, lens, 16),
+                 lambda: kla.kla_pages_trim(table, lens, refs, lens, 16),
                  lambda: kla.kla_pages_compact(pool[None], table, lens, refs, 16),
                  lambda: kla.kla_pages_copy(pool[None], some, some),
                  lambda: kla.kla_kv4_append(q[:, :, :2], q[:, :, :2], pool, table, lens),

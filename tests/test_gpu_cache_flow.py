@@ -107,6 +107,40 @@ def test_prompts_then_steps_then_beams():
     assert not refs.any() and not lens.any() and bool((table == -1).all())
 
 
+def test_drafted_tokens():
+    """Rows of drafted tokens go in, attention goes over all of them, and those that were not
+    taken are given up: across pages' ends, with a prefix that another sequence holds too."""
+    S, page, hq, hk, d, draft = 4, 16, 4, 2, 64, 5
+    c = Cache(S, 12, page, 30, hk, d)
+    table, lens, refs = c.book
+    c.grow([30, 0, 16, 7])
+    k, v = _normal(53, hk, d, seed=1), _normal(53, hk, d, seed=2)
+    cu = _ints([0, 30, 30, 46, 53])
+    kla.kla_kv4_append(k, v, c.pool[0], table, lens, cu_seqlens=cu, **c.units, check_status=True)
+    for s, (a, b) in enumerate(((0, 30), (30, 30), (30, 46), (46, 53))):
+        c.keep(s, k[a:b], v[a:b])
+    kla.kla_pages_fork(*c.book, _ints([0]), _ints([1]), page, check_status=True)
+    c.rows[1] = list(c.rows[0])
+    for step, taken in enumerate(([1, 5, 2, 3], [0, 1, 4, 0], [5, 5, 0, 2], [2, 0, 3, 1])):
+        c.grow([draft] * S)
+        k, v, q = (_normal(S, draft, h, d, seed=10 * step + i) for i, h in ((3, hk), (4, hk), (5, hq)))
+        kla.kla_kv4_append(k, v, c.pool[0], table, lens, **c.units, check_status=True)
+        before = [list(r) for r in c.rows]
+        for s in range(S):
+            c.keep(s, k[s], v[s])
+        o, lse = kla.kla_kv4_attn(q, c.pool[0], table, lens, scale=0.2, **c.units, check_status=True)
+        c.check(q, o, lse, 0.2)
+        kla.kla_pages_trim(*c.book, _ints([draft - n for n in taken]), page, check_status=True)
+        c.rows = before
+        for s, n in enumerate(taken):
+            c.keep(s, k[s, :n], v[s, :n])
+        assert lens.tolist() == [len(r[0]) for r in c.rows]
+        assert refs.tolist() == _cache.counted(table.tolist(), lens.tolist(), page, refs.numel())
+        q = _normal(S, 1, hq, d, seed=10 * step + 6)
+        o, lse = kla.kla_kv4_attn(q, c.pool[0], table, lens, scale=0.2, **c.units, check_status=True)
+        c.check(q, o, lse, 0.2)
+
+
 def test_beside_the_dense_attention():
     """A cache's rows read back and given to kla_attn_fwd: the same within both tolerances."""
     B, n, hq, hk, d, page = 3, 400, 8, 2, 128, 64

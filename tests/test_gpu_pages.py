@@ -93,6 +93,19 @@ def test_grow(S, columns, page, n_pages, layers, size):
 
 
 @pytest.mark.parametrize("S,columns,page,n_pages", SIZES)
+def test_trim(S, columns, page, n_pages):
+    r = random.Random(S)
+    table, lens, refs = _random_book(S, columns, page, n_pages, S + 4, share=0.5)
+    dev = _ints(table).view(S, columns), _ints(lens), _ints(refs)
+    for _ in range(3):
+        cut = [r.choice([0, min(1, n), n, n // 2, r.randint(0, n)]) for n in lens]
+        kla.kla_pages_trim(*dev, _ints(cut), page, check_status=True)
+        table, lens = _cache.trim(table, lens, cut, page)
+        refs = _cache.counted(table, lens, page, n_pages)
+        _same(dev, (table, lens, refs))
+
+
+@pytest.mark.parametrize("S,columns,page,n_pages", SIZES)
 def test_compact(S, columns, page, n_pages):
     table, lens, refs = _random_book(S, columns, page, n_pages, S + 3)
     # a page that no sequence of the book holds
@@ -157,6 +170,8 @@ def test_what_the_device_refuses():
     for more in ([0, -1, 0], [13, 0, 0], [0, 0, 33], [0, 1 << 30, 0], [0, 2147483647, 0]):
         refused(lambda: kla.kla_pages_grow(pool, table, lens, refs, _ints(more), 16,
                                            check_status=True))
+    for cut in ([21, 0, 0], [0, -1, 0], [1, 0, 1], [-2147483648, 0, 0], [0, 2147483647, 0]):
+        refused(lambda: kla.kla_pages_trim(table, lens, refs, _ints(cut), 16, check_status=True))
     refused(lambda: kla.kla_pages_grow(pool, table, lens, refs, _ints([0, 20, 20]), 16,
                                        check_status=True), binding.KLA_ERR_PAGES)
     for src, dst in (([0, 1], [3, 3]), ([0], [5]), ([-1], [3]), ([0, 3], [3, 4]), ([1, 0], [0, 1])):
@@ -174,6 +189,9 @@ def test_bad_entries_are_left_and_reported():
     with pytest.raises(kla.KlaError):
         kla.kla_pages_fork(table, lens, refs, _ints([0]), _ints([1]), 16, check_status=True)
     assert table[1].tolist() == [9, 1] and refs.tolist() == [1, 2, 0]
+    with pytest.raises(kla.KlaError):
+        kla.kla_pages_trim(table, lens, refs, _ints([20, 0, 0]), 16, check_status=True)
+    assert table[0].tolist() == [-1, -1] and lens[0].item() == 0 and refs.tolist() == [1, 1, 0]
 
 
 def test_nothing_to_do():
@@ -185,6 +203,7 @@ def test_nothing_to_do():
     where, n = kla.kla_pages_compact(pool, table, empty, empty, 16, check_status=True)
     assert where.numel() == 0 and n.tolist() == [0]
     kla.kla_pages_copy(pool, empty, empty, check_status=True)
+    kla.kla_pages_trim(table, empty, empty, empty, 16, check_status=True)
     # no layers: the book alone
     table, lens, refs = _ints([[1, -1]]), _ints([3]), _ints([0, 1])
     kla.kla_pages_grow(torch.zeros(0, 2, 16, device="cuda"), table, lens, refs, _ints([20]), 16,
