@@ -19,7 +19,7 @@ import torch
 
 from .attention import (_at, _call, _dense, _given, _out, _refuse, _rows, _scale, _status,
                         _type_code)
-from .binding import load
+from .binding import KlaError, load
 
 _INT = torch.int32
 
@@ -31,18 +31,38 @@ def _size(device, name, args):
         return getattr(load(), name)(*args)
 
 
-def _workspace(device, name, args, like, workspace):
-    """The workspace that the library asks for, on like's device: it and its size in bytes."""
-    need = _size(device, name, args)
-    if workspace is None:
-        # kept by the caller's variable until the call is enqueued
-        return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None, need
-    have = workspace.numel() * workspace.element_size()
-    if workspace.get_device() != device:
-        raise ValueError(f"workspace must be on cuda:{device}, got {workspace.device}")
-    if have < need:
-        raise ValueError(f"workspace needs {need} bytes")
-    return workspace, have
+def _run(fn, dev, args, name, sizes, workspace, check):
+    """Runs a library call with its workspace, of the size that name(*sizes) says, and the
+    stream last in the arguments."""
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _run(fn, dev, args, name, sizes, workspace, check)
+    need, stream = _size(dev, name, sizes), torch._C._cuda_getCurrentRawStream(dev)
+    if workspace is not None:
+        have = workspace.numel() * workspace.element_size()
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace must be on cuda:{dev}, got {workspace.device}")
+        if have < need:
+            raise ValueError(f"workspace needs {need} bytes")
+        return _checked(fn, args, workspace.data_ptr(), have, stream, check)
+    # torch's allocator without a tensor around it (0.7 us a call, not 5): given back
+    # once the call is enqueued, for what comes behind it in the stream
+    at = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream) if need else None
+    try:
+        _checked(fn, args, at, need, stream, check)
+    finally:
+        if at is not None:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(at)
+
+
+def _checked(fn, args, at, size, stream, check):
+    status = fn(*args, at, size, stream)
+    if check and not status:
+        status = load().kla_workspace_status(at, size, stream)
+    if status:
+        lib = load()
+        raise KlaError(status, lib.kla_last_error_message().decode() or
+                       lib.kla_status_str(status).decode())
 
 
 def kla_kv4_page_bytes(page, Hk, d) -> int:
@@ -70,12 +90,19 @@ def kla_kv4_pool(n_pages, page, Hk, d, layers=None, device="cuda"):
 
 
 def _book(table, lens, dev):
+    """The addresses of table and lens, looked over in one go: a small call takes about as
+    long as its checks do."""
     size = table.shape
-    if dev < 0:
-        raise ValueError("table must be a CUDA tensor")
-    if len(size) != 2:
-        raise ValueError(f"table must have shape [B, columns], got {tuple(size)}")
-    return _dense(table, "table", _INT, dev, size), _dense(lens, "lens", _INT, dev, size[:1])
+    if (dev < 0 or len(size) != 2 or table.dtype is not _INT or lens.dtype is not _INT
+            or lens.get_device() != dev or lens.shape != (size[0],)
+            or not table.is_contiguous() or not lens.is_contiguous()):
+        if dev < 0:
+            raise ValueError("table must be a CUDA tensor")
+        if len(size) != 2:
+            raise ValueError(f"table must have shape [B, columns], got {tuple(size)}")
+        _dense(table, "table", _INT, dev, size)
+        _dense(lens, "lens", _INT, dev, size[:1])
+    return table.data_ptr(), lens.data_ptr()
 
 
 def _pool(pool, dev, Hk=None, d=None):
@@ -193,12 +220,11 @@ def kla_kv4_attn(q, pool, table, lens, scale=None, k_unit=1.0, v_unit=1.0, o=Non
     stats = None
     if return_lse or lse is not None:
         lse, stats = _out(lse, "lse", shape[:3], torch.float32, q)
-    workspace, wsb = _workspace(dev, "kla_kv4_attn_workspace_size",
-                                (B, Tq, hq, hk, d, page, columns, dt), q, workspace)
-    _call(dev, load().kla_kv4_attn, q.data_ptr(), qs, at, rows, lengths, _scale(scale, d), k_unit,
-          v_unit, out, stats, B, Tq, hq, hk, d, page, n_pages, columns, dt, _at(workspace), wsb)
-    if check_status:
-        _call(dev, _status, workspace, wsb)
+    _run(load().kla_kv4_attn, dev,
+         (q.data_ptr(), qs, at, rows, lengths, _scale(scale, d), k_unit, v_unit, out, stats, B, Tq,
+          hq, hk, d, page, n_pages, columns, dt),
+         "kla_kv4_attn_workspace_size", (B, Tq, hq, hk, d, page, columns, dt), workspace,
+         check_status)
     return o, lse
 
 
@@ -216,17 +242,12 @@ def _layers(pool, n_pages):
 
 def _held(table, lens, refs):
     """The device, the pages' number, the sizes of the table and the book's addresses."""
-    dev, n_pages, size = table.get_device(), refs.numel(), table.shape
-    rows, lengths = _book(table, lens, dev)
-    return dev, n_pages, size, (rows, lengths, _dense(refs, "refs", _INT, dev, (n_pages,)))
+    dev, n_pages = table.get_device(), refs.numel()
+    return dev, n_pages, table.shape, (*_book(table, lens, dev),
+                                       _dense(refs, "refs", _INT, dev, (n_pages,)))
 
 
-def _run(fn, dev, like, args, sizes, workspace, check):
-    """A pages' call: its arguments, then the workspace for sizes (S, columns, n_pages, n)."""
-    workspace, wsb = _workspace(dev, "kla_pages_workspace_size", sizes, like, workspace)
-    _call(dev, fn, *args, _at(workspace), wsb)
-    if check:
-        _call(dev, _status, workspace, wsb)
+_PAGES = "kla_pages_workspace_size"      # of (S, columns, n_pages, n)
 
 
 def kla_pages_fork(table, lens, refs, src, dst, page, workspace=None, stream=None,
@@ -242,8 +263,8 @@ def kla_pages_fork(table, lens, refs, src, dst, page, workspace=None, stream=Non
     n = dst.numel()
     to = _dense(dst, "dst", _INT, dev, (n,))
     of = _dense(src, "src", _INT, dev, (n,))
-    _run(load().kla_pages_fork, dev, table, (*book, of, to, S, columns, page, n_pages, n),
-                (S, columns, n_pages, n), workspace, check_status)
+    _run(load().kla_pages_fork, dev, (*book, of, to, S, columns, page, n_pages, n), _PAGES,
+         (S, columns, n_pages, n), workspace, check_status)
 
 
 def kla_pages_free(table, lens, refs, seqs, page, workspace=None, stream=None,
@@ -267,9 +288,9 @@ def kla_pages_grow(pool, table, lens, refs, n_new, page, workspace=None, stream=
     more = _dense(n_new, "n_new", _INT, dev, (S,))
     if pool.get_device() != dev:
         _refuse(pool, "pool", pool.dtype, dev, pool.shape)
-    _run(load().kla_pages_grow, dev, table,
-                (*_layers(pool, n_pages), *book, more, S, columns, page, n_pages),
-                (S, columns, n_pages, 0), workspace, check_status)
+    _run(load().kla_pages_grow, dev,
+         (*_layers(pool, n_pages), *book, more, S, columns, page, n_pages), _PAGES,
+         (S, columns, n_pages, 0), workspace, check_status)
 
 
 def kla_pages_trim(table, lens, refs, n_cut, page, workspace=None, stream=None,
@@ -282,7 +303,7 @@ def kla_pages_trim(table, lens, refs, n_cut, page, workspace=None, stream=None,
                                   check_status=check_status)
     dev, n_pages, (S, columns), book = _held(table, lens, refs)
     cut = _dense(n_cut, "n_cut", _INT, dev, (S,))
-    _run(load().kla_pages_trim, dev, table, (*book, cut, S, columns, page, n_pages),
+    _run(load().kla_pages_trim, dev, (*book, cut, S, columns, page, n_pages), _PAGES,
          (S, columns, n_pages, 0), workspace, check_status)
 
 
@@ -300,9 +321,9 @@ def kla_pages_compact(pool, table, lens, refs, page, page_map=None, n_used=None,
     n_used, count = _out(n_used, "n_used", (1,), _INT, refs)
     if pool.get_device() != dev:
         _refuse(pool, "pool", pool.dtype, dev, pool.shape)
-    _run(load().kla_pages_compact, dev, table,
-                (*_layers(pool, n_pages), *book, where, count, S, columns, page, n_pages),
-                (S, columns, n_pages, 0), workspace, check_status)
+    _run(load().kla_pages_compact, dev,
+         (*_layers(pool, n_pages), *book, where, count, S, columns, page, n_pages), _PAGES,
+         (S, columns, n_pages, 0), workspace, check_status)
     return page_map, n_used
 
 
@@ -319,5 +340,5 @@ def kla_pages_copy(pool, src, dst, workspace=None, stream=None, check_status=Fal
     at, layers, size = _layers(pool, None)
     n_pages = pool.shape[1]
     of, to = _dense(src, "src", _INT, dev, (n,)), _dense(dst, "dst", _INT, dev, (n,))
-    _run(load().kla_pages_copy, dev, pool, (at, layers, size, of, to, n_pages, n),
-                (0, 0, n_pages, n), workspace, check_status)
+    _run(load().kla_pages_copy, dev, (at, layers, size, of, to, n_pages, n), _PAGES,
+         (0, 0, n_pages, n), workspace, check_status)
