@@ -14,11 +14,12 @@ drafted tokens that are not taken.
 from __future__ import annotations
 
 import functools
+import math
+from operator import index
 
 import torch
 
-from .attention import (_at, _call, _dense, _given, _out, _refuse, _rows, _scale, _status,
-                        _type_code)
+from .attention import _at, _call, _dense, _given, _refuse, _rows, _scale, _status, _type_code
 from .binding import KlaError, load
 
 _INT = torch.int32
@@ -29,6 +30,28 @@ def _size(device, name, args):
     """A workspace's size, asked for once: it goes by the device and the sizes alone."""
     with torch.cuda.device(device):
         return getattr(load(), name)(*args)
+
+
+#: What compiled graphs take their buffers with, on the current device: 1.5 us of a small call
+#: where torch.empty takes 4.
+_empty = getattr(torch._C._dynamo.guards, "_empty_strided_cuda", None)
+
+
+@functools.lru_cache(maxsize=1024)
+def _steps(size):
+    """The strides of a dense tensor."""
+    return tuple(math.prod(size[i + 1:]) for i in range(len(size)))
+
+
+def _out(t, name, size, dtype, dev):
+    """A dense output, made where there is none, and its address; size: a tuple."""
+    if t is None:
+        if _empty is not None and torch._C._cuda_getDevice() == dev:
+            t = _empty(size, _steps(size), dtype)
+        else:
+            t = torch.empty(size, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _dense(t, name, dtype, dev, size)
 
 
 def _run(fn, dev, args, name, sizes, workspace, check):
@@ -181,15 +204,19 @@ def kla_kv4_read(pool, table, lens, T=None, total=None, cu_seqlens=None, dtype=t
         raise ValueError("T must be given, or total and cu_seqlens")
     if pool.dim() != 4:
         _pool(pool, pool.get_device())
-    hk, d = pool.shape[1], pool.shape[3] // 18
-    shape = (table.shape[0], T, hk, d) if cu_seqlens is None else (total, hk, d)
+    hk, d, dev = pool.shape[1], pool.shape[3] // 18, pool.get_device()
+    if dev < 0:
+        raise ValueError("pool must be a CUDA tensor")
+    n = index(T if cu_seqlens is None else total)
+    if n < 0:
+        raise ValueError(f"{'T' if cu_seqlens is None else 'total'} must not be negative, got {n}")
+    shape = (table.shape[0], n, hk, d) if cu_seqlens is None else (n, hk, d)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=pool.device)
+        k_out = _out(None, "k_out", shape, dtype, dev)[0]
     elif k_out.shape != shape:
-        _refuse(k_out, "k_out", dtype, pool.get_device(), shape)
+        _refuse(k_out, "k_out", dtype, dev, shape)
     if v_out is None:
-        v_out = torch.empty_like(k_out) if k_out.is_contiguous() else \
-            torch.empty(shape, dtype=dtype, device=pool.device)
+        v_out = _out(None, "v_out", shape, k_out.dtype, dev)[0]
     _rows_call(load().kla_kv4_read, k_out, v_out, pool, table, lens, cu_seqlens, (k_unit, v_unit),
                workspace, check_status)
     return k_out, v_out
@@ -216,10 +243,10 @@ def kla_kv4_attn(q, pool, table, lens, scale=None, k_unit=1.0, v_unit=1.0, o=Non
     if table.shape[0] != B:
         raise ValueError(f"table must have {B} rows, got {tuple(table.shape)}")
     columns = table.shape[1]
-    o, out = _out(o, "o", shape, kind, q)
+    o, out = _out(o, "o", (B, Tq, hq, d), kind, dev)
     stats = None
     if return_lse or lse is not None:
-        lse, stats = _out(lse, "lse", shape[:3], torch.float32, q)
+        lse, stats = _out(lse, "lse", (B, Tq, hq), torch.float32, dev)
     _run(load().kla_kv4_attn, dev,
          (q.data_ptr(), qs, at, rows, lengths, _scale(scale, d), k_unit, v_unit, out, stats, B, Tq,
           hq, hk, d, page, n_pages, columns, dt),
@@ -317,8 +344,8 @@ def kla_pages_compact(pool, table, lens, refs, page, page_map=None, n_used=None,
             return kla_pages_compact(pool, table, lens, refs, page, page_map, n_used, workspace,
                                      check_status=check_status)
     dev, n_pages, (S, columns), book = _held(table, lens, refs)
-    page_map, where = _out(page_map, "page_map", (n_pages,), _INT, refs)
-    n_used, count = _out(n_used, "n_used", (1,), _INT, refs)
+    page_map, where = _out(page_map, "page_map", (n_pages,), _INT, dev)
+    n_used, count = _out(n_used, "n_used", (1,), _INT, dev)
     if pool.get_device() != dev:
         _refuse(pool, "pool", pool.dtype, dev, pool.shape)
     _run(load().kla_pages_compact, dev,

@@ -2,6 +2,7 @@
 definition in 64 bits."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -200,6 +201,13 @@ def test_what_the_device_refuses():
             kla.kla_kv4_append(k[0], k[0], pool, table, lens, check_status=True,
                                cu_seqlens=torch.tensor(cu).int().cuda())
         assert e.value.status == binding.KLA_ERR_INVALID_ARG
+    # sizes of another kind of whole number, and sizes that are none
+    for n in (np.int64(2), torch.tensor(2)):
+        assert kla.kla_kv4_read(pool, table, lens, T=n)[0].shape[1] == 2
+    with pytest.raises(TypeError):
+        kla.kla_kv4_read(pool, table, lens, T=2.0)
+    with pytest.raises(ValueError, match="negative"):
+        kla.kla_kv4_read(pool, table, lens, T=-1)
     # a pool without pages: no row has a place, and rows are read as zeros
     none = pool[:0]
     with pytest.raises(kla.KlaError):
