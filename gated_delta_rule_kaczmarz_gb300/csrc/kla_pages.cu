@@ -7,7 +7,7 @@
 // Each operator is one CTA, or one cluster of 8, that reads and changes the book
 // (its phases part at barriers, what they hand over goes through the workspace), and
 // where pages move a second kernel that copies those that the first listed.  The
-// first is bound by latency, a barrier and a round trip to L2 for each phase: 4 to 9
+// first is bound by latency, a barrier and a round trip to L2 for each phase: 3 to 9
 // us.  The second is bound by HBM: 2048 pages of 36 KB in 4 layers 89 us, 0.99 of
 // measured bandwidth.
 #include "kla_internal.h"
@@ -99,9 +99,13 @@ __device__ __forceinline__ void share_of(int n, int &a, int &e) {
     e = x + each < n ? (int)(x + each) : n;
 }
 
-// The sum of the shares' counts, and of those before this CTA's.
-__device__ __forceinline__ int total_of(const int *sums, int &before) {
+// The sum of the shares' counts, of which this CTA's is `own`, and of those before it.
+__device__ __forceinline__ int total_of(const int *sums, int own, int &before) {
     static_assert(kCtas == 8, "two reads");
+    if (gridDim.x == 1) {
+        before = 0;
+        return own;
+    }
     const int4 u = __ldcg(reinterpret_cast<const int4 *>(sums)), v = __ldcg(reinterpret_cast<const int4 *>(sums) + 1);
     const int x[kCtas] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
     int t = 0;
@@ -113,6 +117,10 @@ __device__ __forceinline__ int total_of(const int *sums, int &before) {
     }
     return t;
 }
+
+// Entries of a row are taken by a warp kRow at a time: what is read of them is asked
+// for at once, before anything is written.
+constexpr int kEntries = 4, kRow = 32 * kEntries;
 
 // ------------------------------------------------------------------ fork, free
 // Sequence dst[f] becomes what src[f] was (src NULL or -1: empty), all at once.
@@ -136,191 +144,256 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const __grid_const
         return;
     }
     // what the rows will be, and the counts: the tables are still as they were
-    for (int f = warp; f < p.n; f += threads_of_all() / 32) {
+    const int pieces = p.columns / kRow + 1;             // (a row of no columns has a length)
+    const unsigned work = (unsigned)p.n * (unsigned)pieces;
+    for (unsigned x = warp; x < work; x += threads_of_all() / 32) {
+        const int f = (int)(x / pieces), c0 = (int)(x % pieces) * kRow + lane;
         const int s = p.src ? p.src[f] : -1, d = p.dst[f], len = s < 0 ? 0 : length_of(k, s);
         const int held = pages_of(k, len), had = pages_of(k, length_of(k, d));
         int *row = k.rows + (long long)f * (p.columns + 1);
-        for (int c = lane; c < p.columns; c += 32) {
-            int x = -1;
-            if (c < held) {
-                x = p.table[(long long)s * p.columns + c];
-                if (is_page(k, x)) atomicAdd(&p.refs[x], 1);
-                else bad = true;
-            }
-            row[c] = x;
-            if (c < had) {
-                const int y = p.table[(long long)d * p.columns + c];
-                if (is_page(k, y)) atomicAdd(&p.refs[y], -1);
-                else bad = true;
-            }
+        int now[kEntries], old[kEntries];
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+            const int c = c0 + 32 * i;
+            now[i] = c < held ? p.table[(long long)s * p.columns + c] : -1;
+            old[i] = c < had ? p.table[(long long)d * p.columns + c] : -1;
         }
-        if (lane == 0) row[p.columns] = len;
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+            const int c = c0 + 32 * i;
+            if (c < held) {
+                if (is_page(k, now[i])) atomicAdd(&p.refs[now[i]], 1);
+                else bad = true;
+            }
+            if (c < had) {
+                if (is_page(k, old[i])) atomicAdd(&p.refs[old[i]], -1);
+                else bad = true;
+            }
+            if (c < p.columns) row[c] = now[i];
+        }
+        if (c0 == 0) row[p.columns] = len;
     }
     bad = __syncthreads_or(bad);
     if (tid == 0) k.sh->sums[0][cta_of_all()] = bad;
     all_barrier();
-    for (int f = warp; f < p.n; f += threads_of_all() / 32) {
-        const int d = p.dst[f];
+    for (unsigned x = warp; x < work; x += threads_of_all() / 32) {
+        const int f = (int)(x / pieces), c0 = (int)(x % pieces) * kRow + lane, d = p.dst[f];
         const int *row = k.rows + (long long)f * (p.columns + 1);
-        for (int c = lane; c < p.columns; c += 32) p.table[(long long)d * p.columns + c] = at(row + c);
-        if (lane == 0) p.lens[d] = at(row + p.columns);
+        int now[kEntries];
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) now[i] = c0 + 32 * i < p.columns ? at(row + c0 + 32 * i) : 0;
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i)
+            if (c0 + 32 * i < p.columns) p.table[(long long)d * p.columns + c0 + 32 * i] = now[i];
+        if (c0 == 0) p.lens[d] = at(row + p.columns);
     }
     int before;
-    if (thread_of_all() == 0) k.sh->status = total_of(k.sh->sums[0], before) ? kDevBadTable : kDevOk;
+    if (thread_of_all() == 0) k.sh->status = total_of(k.sh->sums[0], bad, before) ? kDevBadTable : kDevOk;
 }
 
 // ------------------------------------------------------------------ growth
-// What a sequence needs: pages [first, first + need) of its row, the first of
-// them a copy of the one that is there where `copy`.
+// What a sequence needs: pages [first, first + pages) of its row, the first of
+// them a copy of `last`, the one that is there, where `copy`.
 struct Need {
-    int first, pages;
+    int len, more, first, pages, last;
     bool copy, bad;
 };
 __device__ __forceinline__ Need need_of(const Book &k, int s) {
     const Pages &p = k.p;
-    const int len = length_of(k, s), n = p.more[s];
-    Need x{pages_of(k, len), 0, false, n < 0 || (long long)len + n > (long long)p.columns * p.page};
-    if (n <= 0 || x.bad) return x;
-    if (len % p.page != 0) {
-        const int last = p.table[(long long)s * p.columns + len / p.page];
-        x.bad = !is_page(k, last);
-        x.copy = !x.bad && p.refs[last] > 1;
+    Need x{length_of(k, s), p.more[s], 0, 0, 0, false, false};
+    x.bad = x.more < 0 || (long long)x.len + x.more > (long long)p.columns * p.page;
+    if (x.more <= 0 || x.bad) return x;
+    if (x.len % p.page != 0) {
+        x.last = p.table[(long long)s * p.columns + x.len / p.page];
+        x.bad = !is_page(k, x.last);
+        x.copy = !x.bad && p.refs[x.last] > 1;
     }
-    x.first -= x.copy;
-    x.pages = pages_of(k, len + n) - x.first;
+    x.first = pages_of(k, x.len) - x.copy;
+    x.pages = pages_of(k, x.len + x.more) - x.first;
     return x;
 }
+// The share of a .. e - 1 that a thread takes, and how many at most: few of them lie
+// in as many warps as they can.
+__device__ __forceinline__ int share_of_thread(int a, int e, int &x, int &y) {
+    const int gap = kThreads / max(e - a, 1), each = (e - a + kThreads - 1) / kThreads;
+    if (gap > 1) {
+        const int tid = threadIdx.x;
+        x = min(a + tid / gap, e);
+        y = tid % gap == 0 ? min(x + 1, e) : x;
+    } else {
+        x = min(a + (int)threadIdx.x * each, e);
+        y = min(x + each, e);
+    }
+    return each;
+}
 
+// A thread has sequences that follow each other, a warp pages, so one scan tells them
+// the places of all; what a thread found of its first sequence it keeps.
 __global__ void __launch_bounds__(kThreads) pages_grow_kernel(const __grid_constant__ Book k) {
     const Pages &p = k.p;
     __shared__ int warps[4][32];
-    const int tid = threadIdx.x, cta = cta_of_all();
+    const int tid = threadIdx.x, lane = tid % 32, cta = cta_of_all();
     after_previous();
     let_next_start();
-    // pages needed and copies, of this CTA's sequences; free pages of its share
     int s0, s1, r0, r1;
     share_of(p.S, s0, s1);
+    const int turns = share_of_thread(s0, s1, s0, s1);
     share_of(p.n_pages, r0, r1);
-    int count[4] = {};           // needed, copies, free, bad
-    for (int s = s0 + tid; s < s1; s += kThreads) {
+    const int per_warp = ((r1 - r0 + kThreads - 1) / kThreads) * 32;
+    r0 = min(r0 + tid / 32 * per_warp, r1);
+    r1 = min(r0 + per_warp, r1);
+    // pages needed and copies, free pages
+    int count[4] = {}, before[4], all[4];                // needed, copies, free, bad
+#pragma unroll 4
+    for (int r = r0 + lane; r < r1; r += 32) count[2] += p.refs[r] == 0;
+    Need own{};
+    for (int s = s0; s < s1; ++s) {
         const Need x = need_of(k, s);
+        if (s == s0) own = x;
         count[0] += x.pages;
         count[1] += x.copy;
         count[3] += x.bad;
     }
-    for (int r = r0 + tid; r < r1; r += kThreads) count[2] += p.refs[r] == 0;
-    {
-        int before[4], all[4];
-        cta_scan(count, before, all, warps);
-        if (tid < 4) k.sh->sums[tid][cta] = tid == 0 ? all[0] : tid == 1 ? all[1] : tid == 2 ? all[2] : all[3];
-    }
+    cta_scan(count, before, all, warps);
+    if (tid < 4) k.sh->sums[tid][cta] = tid == 0 ? all[0] : tid == 1 ? all[1] : tid == 2 ? all[2] : all[3];
     all_barrier();
-    int need0, copies0, spare0, none;
-    const int need = total_of(k.sh->sums[0], need0), copies = total_of(k.sh->sums[1], copies0);
-    const int spare = total_of(k.sh->sums[2], spare0), bad = total_of(k.sh->sums[3], none);
+    int rank, number, place, none;
+    const int need = total_of(k.sh->sums[0], all[0], rank), copies = total_of(k.sh->sums[1], all[1], number);
+    const int spare = total_of(k.sh->sums[2], all[2], place), bad = total_of(k.sh->sums[3], all[3], none);
     if (thread_of_all() == 0) {
         k.sh->status = bad ? kDevBadTable : need > spare ? kDevNoPages : kDevOk;
         k.sh->copies = bad || need > spare ? 0 : copies;
     }
     if (bad || need > spare) return;                     // nothing is changed
     // the free pages, in order, as far as they are needed
-    for (int r = r0; r < r1 && spare0 < need; r += 4 * kThreads) {
-        int free[4], n[1] = {};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int x = r + 4 * tid + i;
-            free[i] = x < r1 && p.refs[x] == 0;
-            n[0] += free[i];
-        }
-        int rank[1], all[1];
-        cta_scan(n, rank, all, warps);
-        rank[0] += spare0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (free[i] && rank[0] < need) k.a[rank[0]] = r + 4 * tid + i;
-            rank[0] += free[i];
-        }
-        spare0 += all[0];
+    place += __shfl_sync(0xffffffffu, before[2], 0);
+    for (int r = r0; r < r1 && place < need; r += 32) {
+        const bool free = r + lane < r1 && p.refs[r + lane] == 0;
+        const unsigned frees = __ballot_sync(0xffffffffu, free);
+        const int rank_of = place + __popc(frees & ((1u << lane) - 1));
+        if (free && rank_of < need) k.a[rank_of] = r + lane;
+        place += __popc(frees);
     }
     // where each sequence's begin in that order, and its copy's number
-    for (int s = s0; s < s1; s += kThreads) {
-        Need x{0, 0, false, false};
-        if (s + tid < s1) x = need_of(k, s + tid);
-        const int n[2] = {x.pages, x.copy};
-        int rank[2], all[2];
-        cta_scan(n, rank, all, warps);
-        if (s + tid < s1) {
-            k.b[s + tid] = need0 + rank[0];
-            k.c[s + tid] = x.copy ? copies0 + rank[1] : -1;
+    rank += before[0];
+    number += before[1];
+    int own_rank = rank, own_number = own.copy ? number : -1;
+    for (int s = s0; s < s1; ++s) {
+        const Need x = s == s0 ? own : need_of(k, s);
+        if (s > s0) {
+            k.b[s] = rank;
+            k.c[s] = x.copy ? number : -1;
         }
-        need0 += all[0];
-        copies0 += all[1];
+        rank += x.pages;
+        number += x.copy;
     }
-    all_barrier();
-    const int warp = thread_of_all() / 32, lane = tid % 32;
-    for (int s = warp; s < p.S; s += threads_of_all() / 32) {
-        const int n = p.more[s];
-        if (n == 0) continue;
-        const int len = length_of(k, s), number = at(k.c + s);
-        const int first = pages_of(k, len) - (number >= 0), pages = pages_of(k, len + n) - first;
-        const int rank = at(k.b + s);
-        int *row = p.table + (long long)s * p.columns;
-        int old = 0;
-        if (number >= 0) old = row[first];
-        __syncwarp();
-        for (int i = lane; i < pages; i += 32) {
-            const int page = at(k.a + rank + i);
-            row[first + i] = page;
-            p.refs[page] = 1;
-            if (i == 0 && number >= 0) {
-                k.to[number] = page;
-                k.from[number] = old;
-                atomicAdd(&p.refs[old], -1);
+    all_barrier();                                       // (counts change from here on)
+    for (int i = 0; i < turns; ++i) {
+        const int s = s0 + i;
+        if (i > 0) {
+            own.pages = own.more = 0;
+            if (s < s1) {
+                own.more = p.more[s];
+                own.len = length_of(k, s);
+                own_rank = k.b[s];
+                own_number = k.c[s];
+                own.first = pages_of(k, own.len) - (own_number >= 0);
+                own.pages = own.more > 0 ? pages_of(k, own.len + own.more) - own.first : 0;
+                if (own_number >= 0) own.last = p.table[(long long)s * p.columns + own.first];
             }
         }
-        __syncwarp();
-        if (lane == 0) p.lens[s] = len + n;
+        if (own.pages > 0) {
+            const int page = at(k.a + own_rank);
+            p.table[(long long)s * p.columns + own.first] = page;
+            p.refs[page] = 1;
+            if (own_number >= 0) {
+                k.to[own_number] = page;
+                k.from[own_number] = own.last;
+                atomicAdd(&p.refs[own.last], -1);
+            }
+        }
+        if (own.more > 0) p.lens[s] = own.len + own.more;
+        // more pages than one: by the warp
+        for (unsigned left = __ballot_sync(0xffffffffu, own.pages > 1); left; left &= left - 1) {
+            const int of = __ffs(left) - 1;
+            const int seq = __shfl_sync(0xffffffffu, s, of), pages = __shfl_sync(0xffffffffu, own.pages, of);
+            const int first = __shfl_sync(0xffffffffu, own.first, of);
+            const int at0 = __shfl_sync(0xffffffffu, own_rank, of);
+            for (int x = 1 + lane; x < pages; x += kRow) {
+                int page[kEntries];
+#pragma unroll
+                for (int y = 0; y < kEntries; ++y) page[y] = x + 32 * y < pages ? at(k.a + at0 + x + 32 * y) : -1;
+#pragma unroll
+                for (int y = 0; y < kEntries; ++y)
+                    if (page[y] >= 0) {
+                        p.table[(long long)seq * p.columns + first + x + 32 * y] = page[y];
+                        p.refs[page[y]] = 1;
+                    }
+            }
+        }
     }
 }
 
 // ------------------------------------------------------------------ trimming
 // The last more[s] positions of a sequence are given up, with the pages behind those
-// that are left: a warp to a sequence.
+// that are left: one page of a sequence by its thread, more by the warp.
 __global__ void __launch_bounds__(kThreads) pages_trim_kernel(const __grid_constant__ Book k) {
     const Pages &p = k.p;
     const int tid = threadIdx.x, lane = tid % 32;
     after_previous();
     let_next_start();
-    bool bad = false;                                    // every CTA looks all of them over
-    for (int s = tid; s < p.S; s += kThreads) {
-        const int n = p.more[s];
-        bad = bad || n < 0 || n > length_of(k, s);
-    }
-    bad = __syncthreads_or(bad);
-    all_barrier();                                       // (before a length changes)
-    if (bad) {
-        if (thread_of_all() == 0) k.sh->status = kDevBadTable;
-        return;
-    }
-    for (int s = thread_of_all() / 32; s < p.S; s += threads_of_all() / 32) {
-        const int n = p.more[s];
-        if (n == 0) continue;
-        const int len = length_of(k, s), held = pages_of(k, len);
-        int *row = p.table + (long long)s * p.columns;
-        for (int c = pages_of(k, len - n) + lane; c < held; c += 32) {
-            const int x = row[c];
-            if (is_page(k, x)) atomicAdd(&p.refs[x], -1);
-            else bad = true;
-            row[c] = -1;
-        }
-        __syncwarp();
-        if (lane == 0) p.lens[s] = len - n;
-    }
+    int s0, s1, none;
+    share_of(p.S, s0, s1);
+    const int turns = share_of_thread(s0, s1, s0, s1);
+    bool bad = false;
+    for (int s = s0; s < s1; ++s) bad = bad || p.more[s] < 0 || p.more[s] > length_of(k, s);
     bad = __syncthreads_or(bad);
     if (tid == 0) k.sh->sums[0][cta_of_all()] = bad;
     all_barrier();
-    int before;
-    if (thread_of_all() == 0) k.sh->status = total_of(k.sh->sums[0], before) ? kDevBadTable : kDevOk;
+    if (total_of(k.sh->sums[0], bad, none)) {                 // nothing is changed
+        if (thread_of_all() == 0) k.sh->status = kDevBadTable;
+        return;
+    }
+    bad = false;
+    for (int i = 0; i < turns; ++i) {
+        const int s = s0 + i, n = s < s1 ? p.more[s] : 0;
+        int first = 0, held = 0;
+        if (n > 0) {
+            const int len = length_of(k, s);
+            first = pages_of(k, len - n);
+            held = pages_of(k, len);
+            p.lens[s] = len - n;
+        }
+        auto drop = [&](int page) {
+            if (is_page(k, page)) atomicAdd(&p.refs[page], -1);
+            else bad = true;
+        };
+        if (held > first) {
+            int &entry = p.table[(long long)s * p.columns + first];
+            drop(entry);
+            entry = -1;
+        }
+        for (unsigned left = __ballot_sync(0xffffffffu, held > first + 1); left; left &= left - 1) {
+            const int of = __ffs(left) - 1;
+            const int seq = __shfl_sync(0xffffffffu, s, of), end = __shfl_sync(0xffffffffu, held, of);
+            int *row = p.table + (long long)seq * p.columns;
+            for (int c = __shfl_sync(0xffffffffu, first, of) + 1 + lane; c < end; c += kRow) {
+                int page[kEntries];
+#pragma unroll
+                for (int y = 0; y < kEntries; ++y) page[y] = c + 32 * y < end ? row[c + 32 * y] : 0;
+#pragma unroll
+                for (int y = 0; y < kEntries; ++y)
+                    if (c + 32 * y < end) {
+                        drop(page[y]);
+                        row[c + 32 * y] = -1;
+                    }
+            }
+        }
+    }
+    bad = __syncthreads_or(bad);
+    if (tid == 0) k.sh->sums[1][cta_of_all()] = bad;
+    all_barrier();
+    if (thread_of_all() == 0) k.sh->status = total_of(k.sh->sums[1], bad, none) ? kDevBadTable : kDevOk;
 }
 
 // ------------------------------------------------------------------ compaction
@@ -338,7 +411,7 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_co
     cta_scan(used, rank, all, warps);
     if (tid == 0) k.sh->sums[0][cta] = all[0];
     all_barrier();
-    const int n_used = total_of(k.sh->sums[0], before);
+    const int n_used = total_of(k.sh->sums[0], all[0], before);
     // holes below n_used in order (a), used pages from there on in reverse order (b)
     int holes[1] = {};
     for (int r = r0; r < r1; r += 4 * kThreads) {
@@ -371,7 +444,7 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_co
     cta_scan(holes, rank, all, warps);
     if (tid == 0) k.sh->sums[1][cta] = all[0];
     all_barrier();
-    const int moved = total_of(k.sh->sums[1], before);
+    const int moved = total_of(k.sh->sums[1], all[0], before);
     for (int i = thread_of_all(); i < moved; i += threads_of_all()) {
         const int from = at(k.b + moved - 1 - i), to = at(k.a + i);
         p.page_map[from] = to;
@@ -385,15 +458,22 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_co
         *p.n_used = n_used;
     }
     all_barrier();
-    const int warp = thread_of_all() / 32, lane = tid % 32;
-    for (int s = warp; s < p.S; s += threads_of_all() / 32) {
+    const int lane = tid % 32, pieces = (p.columns + kRow - 1) / kRow;
+    const unsigned long long work = (unsigned long long)p.S * (unsigned)pieces;
+    for (unsigned long long w = thread_of_all() / 32; w < work; w += threads_of_all() / 32) {
+        const int s = (int)(w / (unsigned)pieces), c0 = (int)(w % (unsigned)pieces) * kRow + lane;
         const int held = pages_of(k, length_of(k, s));
         int *row = p.table + (long long)s * p.columns;
-        for (int c = lane; c < held; c += 32) {
-            const int x = row[c];
-            const int y = is_page(k, x) ? at(p.page_map + x) : -1;
-            if (y < 0) atomicMax(&k.sh->status, (unsigned)kDevBadTable);     // no page, or a free one: left
-            else if (y != x) row[c] = y;
+        int from[kEntries], to[kEntries];
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) from[i] = c0 + 32 * i < held ? row[c0 + 32 * i] : -1;
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) to[i] = is_page(k, from[i]) ? at(p.page_map + from[i]) : -1;
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+            if (c0 + 32 * i >= held) continue;
+            if (to[i] < 0) atomicMax(&k.sh->status, (unsigned)kDevBadTable);  // no page, or a free one: left
+            else if (to[i] != from[i]) row[c0 + 32 * i] = to[i];
         }
     }
 }
@@ -428,7 +508,7 @@ __global__ void __launch_bounds__(kThreads) pages_check_kernel(const __grid_cons
     all_barrier();
     if (tid == 0) {
         int before;
-        bad = total_of(k.sh->sums[0], before) != 0;
+        bad = total_of(k.sh->sums[0], bad, before) != 0;
         k.sh->status = bad ? kDevBadTable : kDevOk;
         k.sh->copies = bad ? 0 : p.n;
     }
@@ -485,18 +565,19 @@ Book book_of(const Pages &p) {
     return k;
 }
 
-// One CTA up to `most` entries, whose barriers are cheaper (1.0 to 2.6 us a call),
-// else the cluster, which has more hands.  Both in us: a fork of 32 rows of 64 pages 5.8
-// and 6.3, of 64 8.6 and 6.2; growth among 16384 pages 7.4 and 8.1, 32768 7.9 and 8.0,
-// 131072 13.4 and 9.5 (a sequence that grows counts as 128 of them: of 256 that do among
-// 3200 pages 18.5 and 11.5); compaction of 2048 pages with a table of 32 x 64 7.1 and 8.6, 4096
-// with 64 x 64 8.7 and 8.7, 8192 with 128 x 64 12.3 and 8.9; trimming 64 sequences 2.1 and 2.5,
-// 256 5.9 and 3.1.
-constexpr long long kForkEntries = 2048, kGrowEntries = 32768, kCompactEntries = 8192, kCopyEntries = 4096,
-                    kTrimEntries = 64;
+// One CTA up to `most` units of work, whose barriers are cheaper, else the cluster,
+// which has more hands.  Both in us.  Forks, by rows times pieces of kRow entries: 32 rows
+// of 64 entries 4.6 and 5.4, 40 5.9 and 5.3, 8 of 500 4.9 and 5.8.  Growth, by pages and
+// 128 for a sequence: 128 sequences among 16384 pages 5.7 and 6.8, 1024 among 131072 11.0
+// and 8.3; 256 that take 32 pages each among 16384, with the trimming behind it, 20.5 and 17.7.
+// Trimming, by sequences: 256 that lose a page or none 2.7 and 4.3, 25 pages
+// each 6.3 and 4.3.  Compaction, by pages and entries: 2048 pages with 32 x 64 6.4
+// and 8.8, 4096 with 64 x 64 8.2 and 9.1, 8192 with 64 x 64 9.9 and 9.2.
+constexpr long long kForkPieces = 32, kGrowEntries = 32768, kCompactEntries = 8192, kCopyEntries = 4096,
+                    kTrimEntries = 256;
 
-cudaError_t run(void (*kernel)(const Book), const Book &k, long long entries, long long most, cudaStream_t s) {
-    const bool one = entries <= most;
+cudaError_t run(void (*kernel)(const Book), const Book &k, long long work, long long most, cudaStream_t s) {
+    const bool one = work <= most;
     const cudaError_t e = launch_next(kernel, one ? 1 : kCtas, kThreads, 0, one ? 1 : kCtas, k, s);
     note_launch();
     return e;
@@ -526,7 +607,7 @@ size_t pages_workspace_bytes(int S, int columns, int n_pages, int n) {
 }
 
 cudaError_t launch_pages_fork(const Pages &p, cudaStream_t s) {
-    return run(pages_fork_kernel, book_of(p), (long long)p.n * p.columns + p.S / 32, kForkEntries, s);
+    return run(pages_fork_kernel, book_of(p), (long long)p.n * (p.columns / kRow + 1), kForkPieces, s);
 }
 cudaError_t launch_pages_grow(const Pages &p, cudaStream_t s) {
     const Book k = book_of(p);

@@ -41,7 +41,7 @@ def _same(dev, want):
 
 
 SIZES = [(1, 1, 1, 1), (3, 4, 16, 9), (40, 7, 5, 300), (300, 20, 64, 5000), (9, 2, 16, 20001),
-         (2000, 3, 16, 9000)]
+         (2000, 3, 16, 9000), (5, 700, 16, 4000), (50, 257, 16, 12000)]
 
 
 @pytest.mark.parametrize("S,columns,page,n_pages", SIZES)
