@@ -146,6 +146,22 @@ __device__ __forceinline__ float2 unpack_half(uint32_t h) {
     return __half22float2(reinterpret_cast<const __half2 &>(h));
 }
 
+// A bulk copy of what is read once (`once`), which need not push anything out of L2, or of
+// what other groups of rows read too.
+__device__ __forceinline__ uint64_t policy_of(bool once) {
+    uint64_t first, normal;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
+    asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
+    return once ? first : normal;
+}
+__device__ __forceinline__ void load_block(void *dst, const void *src, uint32_t bytes, uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+        ::"r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(tc::smem_u32(bar)),
+        "l"(policy)
+        : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void load_words(const unsigned char *p, uint32_t (&w)[N]) {
     if (N == 4) {
@@ -635,6 +651,7 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
         // Copies.  The lanes look up the blocks of kAhead tiles at once.  (A lookup ahead of
         // its use, too, does not pay: 256 contexts 67.4 us, 65.9 without.)
         constexpr int kAhead = 32 / C::kBlocks;
+        const uint64_t policy = policy_of(a.groups == 1);
         Place ahead = at;                            // of the tile to be asked for
         int issued = 0, looked = -kAhead;
         unsigned block = 0;                          // this lane's, of the tiles from `looked` on
@@ -657,9 +674,9 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
             if (lane == 0) tc::mbar_expect_tx(&bars[warp][slot], there * Layout<D>::kBytes);
             __syncwarp();
             if (lane < there)
-                tc::bulk_load(ring + slot * C::kStage + lane * Layout<D>::kBytes,
-                              a.pool + (unsigned long long)src * Layout<D>::kBytes, Layout<D>::kBytes,
-                              &bars[warp][slot]);
+                load_block(ring + slot * C::kStage + lane * Layout<D>::kBytes,
+                           a.pool + (unsigned long long)src * Layout<D>::kBytes, Layout<D>::kBytes,
+                           &bars[warp][slot], policy);
             if (fresh) {                             // its query rows into L2
                 const int head = divided(ahead.item, a.by_groups);
                 const int row = (ahead.item - head * a.groups) * C::kRows + lane;
