@@ -710,13 +710,13 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
                 back = true;
                 __syncwarp();
             }
+            const int head = divided(at.item, a.by_groups), group = at.item - head * a.groups;
+            if (start) st.template begin<T>(a, at.seq, head, group, at.len);
+            start = false;
             ok = tc::mbar_wait(&bars[warp][slot], parity) && !a.lost_wait;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const unsigned char *stage = ring + slot * C::kStage;
-            const int head = divided(at.item, a.by_groups), group = at.item - head * a.groups;
-            if (start) st.template begin<T>(a, at.seq, head, group, at.len);
-            start = false;
 #pragma unroll 1
             for (int i = 0; i < C::kTile; i += C::kKeys) {
                 const int key0 = at.tile * C::kTile + i;
@@ -808,28 +808,18 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
             const bool here = members >> lane & 1;
             for (; turn < rows; turn += C::kWarps) {
                 const float m = here ? part[pr * D + turn] : 0.f, t = here ? part[pr * D + pr + turn] : 0.f;
-                float base, l, v[N] = {}, w = 0.f;
-                bool weighed = false;
-                for (unsigned left = members; left;) {           // four parts at once
-                    int k[4];
-                    float y[4][N];
+                float base, l, v[N] = {};
+                const float w = join_weights(here, m, t, base, l);
+                // (few instructions: they are fetched anew here, and four parts at once took
+                // longer)
+#pragma unroll 1
+                for (unsigned left = members; left; left &= left - 1) {
+                    const int k = __ffs(left) - 1, from_k = __shfl_sync(0xffffffffu, x.at, k);
+                    const float f = __shfl_sync(0xffffffffu, w, k);
+                    float y[N];
+                    load_row(reinterpret_cast<const float *>(smem + from_k) + turn * D + N * lane, y);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        k[j] = left ? __ffs(left) - 1 : -1;
-                        left &= left - 1;
-                        const int from_k = __shfl_sync(0xffffffffu, x.at, max(k[j], 0));
-                        if (k[j] >= 0)
-                            load_row(reinterpret_cast<const float *>(smem + from_k) + turn * D + N * lane, y[j]);
-                    }
-                    if (!weighed) w = join_weights(here, m, t, base, l);
-                    weighed = true;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (k[j] < 0) continue;
-                        const float f = __shfl_sync(0xffffffffu, w, k[j]);
-#pragma unroll
-                        for (int i = 0; i < N; ++i) v[i] = fmaf(f, y[j][i], v[i]);
-                    }
+                    for (int i = 0; i < N; ++i) v[i] = fmaf(f, y[i], v[i]);
                 }
                 if (first && whole) {
                     write_row<T, D>(a, out_row(a, seq, head, group * C::kRows + turn), v, base, l);
