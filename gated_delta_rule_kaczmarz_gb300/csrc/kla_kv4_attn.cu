@@ -515,17 +515,11 @@ struct Part {
     int at;              // in shared memory
 };
 
-// Parts of a row joined: lane m < count brings a part's base and sum; returns its
-// weight, and the row's base and sum.
-__device__ __forceinline__ float join_weights(bool there, float m, float sum, float &base, float &l) {
-    base = there ? m : -INFINITY;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) base = fmaxf(base, __shfl_xor_sync(0xffffffffu, base, o));
-    const float w = !there ? 0.f : (m == base ? 1.f : exp2_of(m - base));
-    l = there ? w * sum : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    return w;
+// Parts of a row: a lane brings a part's base, -infinity where it has none; returns its
+// weight, and the row's base.
+__device__ __forceinline__ float join_weight(float m, float &base) {
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(base) : "f"(m));
+    return m == base ? 1.f : exp2_of(m - base);
 }
 
 template <int N>
@@ -779,63 +773,79 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
     }
     __syncthreads();
 
-    // Items that several of the CTA's warps had: a warp for each row.  Lane i
-    // looks at part i; parts of an item follow each other.
+    // Items that several of the CTA's warps had.  Lane i has part i; parts of an item
+    // follow each other, and the lane of its first has the item.  Rows of all items in a
+    // row are the warps' in turn.  (Few instructions: they are fetched anew here.)
     {
         constexpr int N = D / 32;
         Part x{-1, 0, false, false, 0};
         if (lane < 2 * C::kWarps) x = parts[lane];
-        const unsigned all = __ballot_sync(0xffffffffu, x.seq >= 0);
-        const unsigned lower = all & ((1u << lane) - 1);
+        const unsigned all = __ballot_sync(0xffffffffu, x.seq >= 0), lower = all & ((1u << lane) - 1);
         const int prev = lower ? 31 - __clz(lower) : lane;
         const int pseq = __shfl_sync(0xffffffffu, x.seq, prev), pitem = __shfl_sync(0xffffffffu, x.item, prev);
-        unsigned leaders = __ballot_sync(0xffffffffu, x.seq >= 0 && (!lower || pseq != x.seq || pitem != x.item));
-        int turn = warp;
-        Owner own{-1, 0, 0};
-        while (leaders) {
-            const int a0 = __ffs(leaders) - 1;
-            leaders &= leaders - 1;
-            const int a1 = leaders ? __ffs(leaders) - 1 : 32;      // the next item's
-            const unsigned members = all & (a1 == 32 ? 0xffffffffu : (1u << a1) - 1) & ~((1u << a0) - 1);
-            const int seq = __shfl_sync(0xffffffffu, x.seq, a0), item = __shfl_sync(0xffffffffu, x.item, a0);
-            const bool first = __shfl_sync(0xffffffffu, (int)x.first, a0);
-            const bool whole = __shfl_sync(0xffffffffu, (int)x.end, 31 - __clz(members));
-            const int head = divided(item, a.by_groups), group = item - head * a.groups;
-            const int rows = min(C::kRows, a.rows - group * C::kRows);
-            const int pr = a.part_rows;
-            float *out = mine_at + (first ? 1 : 0) * a.part_size;
-            const float *part = reinterpret_cast<const float *>(smem + x.at);
-            const bool here = members >> lane & 1;
-            for (; turn < rows; turn += C::kWarps) {
-                const float m = here ? part[pr * D + turn] : 0.f, t = here ? part[pr * D + pr + turn] : 0.f;
-                float base, l, v[N] = {};
-                const float w = join_weights(here, m, t, base, l);
-                // (few instructions: they are fetched anew here, and four parts at once took
-                // longer)
-#pragma unroll 1
-                for (unsigned left = members; left; left &= left - 1) {
-                    const int k = __ffs(left) - 1, from_k = __shfl_sync(0xffffffffu, x.at, k);
-                    const float f = __shfl_sync(0xffffffffu, w, k);
-                    float y[N];
-                    load_row(reinterpret_cast<const float *>(smem + from_k) + turn * D + N * lane, y);
+        const bool leads = x.seq >= 0 && (!lower || pseq != x.seq || pitem != x.item);
+        const unsigned leaders = __ballot_sync(0xffffffffu, leads), above = leaders & ~((2u << lane) - 1);
+        const unsigned parts_of = all & (above ? (1u << (__ffs(above) - 1)) - 1 : 0xffffffffu) & ~((1u << lane) - 1);
+        const bool whole = __shfl_sync(0xffffffffu, (int)x.end, parts_of ? 31 - __clz(parts_of) : 0);
+        const int x_head = divided(x.item, a.by_groups), x_row = (x.item - x_head * a.groups) * C::kRows;
+        const int rows = leads ? min(C::kRows, a.rows - x_row) : 0;
+        int behind = rows;                           // rows of the items up to this one
 #pragma unroll
-                    for (int i = 0; i < N; ++i) v[i] = fmaf(f, y[i], v[i]);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, behind, o);
+            if (lane >= o) behind += y;
+        }
+        // an item that began in an earlier CTA: this CTA's first, if any
+        const unsigned owned = __ballot_sync(0xffffffffu, leads && !x.first && whole);
+        if (warp == 0 && (owned ? lane == __ffs(owned) - 1 : lane == 0))
+            a.owners[cta] = owned ? Owner{x.seq, x.item, from} : Owner{-1, 0, 0};
+        const int total = __shfl_sync(0xffffffffu, behind, 31), pr = a.part_rows;
+#pragma unroll 1
+        for (int p = warp; p < total; p += C::kWarps) {
+            const int of = __ffs(__ballot_sync(0xffffffffu, p < behind)) - 1;
+            const int turn = p - __shfl_sync(0xffffffffu, behind - rows, of);
+            const unsigned members = __shfl_sync(0xffffffffu, parts_of, of);
+            const bool here = members >> lane & 1;
+            const float *part = reinterpret_cast<const float *>(smem + x.at) + pr * D + turn;
+            const float m = here ? part[0] : -INFINITY, t = here ? part[pr] : 0.f;
+            int k = of;
+            float y[N], v[N] = {}, base, l = 0.f;
+            auto load = [&](float (&to)[N]) {
+                const int at = __shfl_sync(0xffffffffu, x.at, k);
+                load_row(reinterpret_cast<const float *>(smem + at) + turn * D + N * lane, to);
+            };
+            load(y);
+            const float w = join_weight(m, base), wt = w * t;
+            for (unsigned left = members;;) {
+                const int now = k;
+                left &= left - 1;
+                k = left ? __ffs(left) - 1 : now;    // (behind the last, that again)
+                float z[N];
+                load(z);
+                const float f = __shfl_sync(0xffffffffu, w, now);
+                l += __shfl_sync(0xffffffffu, wt, now);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    v[i] = fmaf(f, y[i], v[i]);
+                    y[i] = z[i];
                 }
-                if (first && whole) {
-                    write_row<T, D>(a, out_row(a, seq, head, group * C::kRows + turn), v, base, l);
-                } else {
-                    store_row(out + turn * D + N * lane, v);
-                    if (lane == 0) {
-                        out[pr * D + turn] = base;
-                        out[pr * D + pr + turn] = l;
-                    }
+                if (!left) break;
+            }
+            const bool first = __shfl_sync(0xffffffffu, (int)x.first, of);
+            const bool end = __shfl_sync(0xffffffffu, (int)whole, of);
+            const int seq = __shfl_sync(0xffffffffu, x.seq, of), head = __shfl_sync(0xffffffffu, x_head, of);
+            const int row = __shfl_sync(0xffffffffu, x_row, of) + turn;
+            if (first && end) {
+                write_row<T, D>(a, out_row(a, seq, head, row), v, base, l);
+            } else {
+                float *out = mine_at + (first ? 1 : 0) * a.part_size;
+                store_row(out + turn * D + N * lane, v);
+                if (lane == 0) {
+                    out[pr * D + turn] = base;
+                    out[pr * D + pr + turn] = l;
                 }
             }
-            turn -= rows;
-            while (turn < 0) turn += C::kWarps;
-            if (!first && whole) own = {seq, item, from};        // (the CTA's first item, if any)
         }
-        if (tid == 0) a.owners[cta] = own;
     }
     if (tid == 0) *(a.ctas == 1 ? a.status : a.cta_status + cta) = trouble;
 
@@ -882,25 +892,41 @@ __global__ void __launch_bounds__(512) kv4_join_kernel(const __grid_constant__ A
         const int k = k0 + lane, c = own.from + k;
         const float *part = a.part + ((size_t)min(c, (int)blockIdx.x) * (2 + C::kWarps) + (k == 0)) * a.part_size;
         const bool here = k < count;
-        const float m = part[a.part_rows * D + n], sum = part[a.part_rows * (D + 1) + n];
-        float top, t;
-        const float w = join_weights(here, m, sum, top, t);
+        const float m = here ? part[a.part_rows * D + n] : -INFINITY;
+        const float sum = here ? part[a.part_rows * (D + 1) + n] : 0.f;
+        const int most = min(32, count - k0);
+        float y[4][N] = {};                          // four parts are asked for ahead
+        auto ask = [&](int j0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j0 + j < most) {
+                    const size_t c_of = own.from + k0 + j0 + j;
+                    const float *p = a.part + (c_of * (2 + C::kWarps) + (k0 + j0 + j == 0)) * a.part_size;
+                    load_row(p + n * D + N * lane, y[j]);
+                }
+        };
+        ask(0);
+        float top;
+        const float w = join_weight(m, top);
+        float t = w * sum;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
         const float both = fmaxf(base, top);
         const float f0 = base == both ? 1.f : exp2_of(base - both), f1 = top == both ? 1.f : exp2_of(top - both);
         base = both;
-        l = l * f0 + t * f1;
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] *= f0;
-        const int most = min(32, count - k0);
-#pragma unroll 4
-        for (int j = 0; j < most; ++j) {
-            const float f = __shfl_sync(0xffffffffu, w, j) * f1;
-            const float *p = a.part + ((size_t)(own.from + k0 + j) * (2 + C::kWarps) + (k0 + j == 0)) * a.part_size;
-            float y[N];
-            load_row(p + n * D + N * lane, y);
+#pragma unroll 1
+        for (int j0 = 0; j0 < most; j0 += 4) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = fmaf(f, y[i], v[i]);
+            for (int j = 0; j < 4; ++j) {
+                const float f = __shfl_sync(0xffffffffu, w, (j0 + j) & 31) * f1;
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = j0 + j < most ? fmaf(f, y[j][i], v[i]) : v[i];
+            }
+            ask(j0 + 4);
         }
+        l = l * f0 + t * f1;
     }
     if (kPer > 1 && count > 32) {                    // (the same for all of the block)
         store_row(&shared_v[warp][N * lane], v);
