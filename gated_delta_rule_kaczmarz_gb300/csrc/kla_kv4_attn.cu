@@ -173,8 +173,10 @@ __device__ __forceinline__ void load_words(const unsigned char *p, uint32_t (&w)
     }
 }
 
-__device__ __forceinline__ void st(float *p, float x) { *p = x; }
-__device__ __forceinline__ void st(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void store2(float *p, float x, float y) { *reinterpret_cast<float2 *>(p) = make_float2(x, y); }
+__device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
+}
 __device__ __forceinline__ void load4(const float *p, float (&x)[4]) {
     const float4 v = *reinterpret_cast<const float4 *>(p);
     x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
@@ -461,10 +463,7 @@ struct State {
                 const float sum = l[nt][z], f = sum == 0.f ? 0.f : a.v_unit / sum;
                 T *to = static_cast<T *>(a.o) + row * D + r * (D / 8);
 #pragma unroll
-                for (int j = 0; j < kSteps; ++j) {
-                    st(to + 2 * j, o[nt][j][z] * f);
-                    st(to + 2 * j + 1, o[nt][j][2 + z] * f);
-                }
+                for (int j = 0; j < kSteps; ++j) store2(to + 2 * j, o[nt][j][z] * f, o[nt][j][2 + z] * f);
                 if (r == 0 && a.lse)
                     a.lse[row] = sum == 0.f ? -INFINITY : (m[nt][z] - kTop + log2f(sum)) * kLn2;
             }
@@ -623,11 +622,11 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
         Place at;
         {
             const unsigned x = (unsigned)divided((int)u, a.by_items);
-            int lo = 0, hi = C::kThreads - 1;
-            while (lo < hi) {                        // the last share that begins at x or before
-                const int mid = (lo + hi + 1) / 2;
-                if (sums[mid] <= x) lo = mid; else hi = mid - 1;
-            }
+            // the last share that begins at x or before: sums do not fall
+            constexpr int kStep = C::kThreads / 32;
+            static_assert(kStep <= 32, "a lane for each of a step's sums");
+            int lo = (31 - __clz(__ballot_sync(0xffffffffu, sums[lane * kStep] <= x))) * kStep;
+            lo += 31 - __clz(__ballot_sync(0xffffffffu, lane < kStep && sums[lo + lane % kStep] <= x));
             unsigned y = sums[lo];
             at.seq = lo * share;
             at.len = length(a, lens, at.seq);
