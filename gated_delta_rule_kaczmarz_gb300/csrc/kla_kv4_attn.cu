@@ -52,6 +52,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 // kLag above it: p stays below 2^15 (fp16), and what is 2^-29 of the maximum is
 // still a normal number there.
 constexpr float kTop = 7.f, kLag = 8.f;
+constexpr unsigned kMany = 2;
 
 // NT: tiles of 8 query rows.
 template <int D, int NT, bool F32>
@@ -177,15 +178,29 @@ __device__ __forceinline__ void store2(float *p, float x, float y) { *reinterpre
 __device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) {
     *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
 }
-__device__ __forceinline__ void load4(const float *p, float (&x)[4]) {
-    const float4 v = *reinterpret_cast<const float4 *>(p);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4]) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
-    x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
-}
+// A fourth of a query row.
+template <typename T, int D>
+struct Query {
+    uint4 w[D / 16 * sizeof(T) / 4];
+    __device__ __forceinline__ void load(const T *p, bool there) {
+#pragma unroll
+        for (int i = 0; i < D / 16 * (int)sizeof(T) / 4; ++i)
+            w[i] = there ? reinterpret_cast<const uint4 *>(p)[i] : make_uint4(0, 0, 0, 0);
+    }
+    // four features from 4 j on
+    __device__ __forceinline__ void get(int j, float (&x)[4]) const {
+        if (sizeof(T) == 4) {
+            const uint4 v = w[j];
+            x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
+            x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+        } else {
+            const uint4 v = w[j / 2];
+            const uint32_t lo = j % 2 ? v.z : v.x, hi = j % 2 ? v.w : v.y;
+            x[0] = __uint_as_float(lo << 16); x[1] = __uint_as_float(lo & 0xffff0000u);
+            x[2] = __uint_as_float(hi << 16); x[3] = __uint_as_float(hi & 0xffff0000u);
+        }
+    }
+};
 
 // Output row of row n of a group: its offset in [B, Tq, Hq], or -1 behind the last.
 __device__ __forceinline__ long long out_row(const Args &a, int seq, int head, int n) {
@@ -213,20 +228,28 @@ struct State {
     int limit[NT][2];            // keys below it are seen
     int full;                    // keys below it are seen by all rows
 
+    // This thread's part of the query rows, as it lies in memory.
     template <typename T>
-    __device__ __forceinline__ void begin(const Args &a, int seq, int head, int group, int len) {
+    __device__ __forceinline__ void fetch(const Args &a, int seq, int head, int group, Query<T, D> (&x)[NT]) const {
         const int lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int n = group * 8 * NT + nt * 8 + r;
+            x[nt].load(query<T>(a, seq, head, n) + c * (D / 4), n < a.rows);
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void begin(const Args &a, int group, int len, const Query<T, D> (&given)[NT]) {
+        const int lane = threadIdx.x % 32, c = lane % 4;
         const int first = len - a.Tq + 1;
         full = first + divided(group * 8 * NT, a.by_G);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int n = group * 8 * NT + nt * 8 + r;
-            const T *rows = query<T>(a, seq, head, n) + c * (D / 4);
             float x[D / 4], top = 0.f;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
-                float y[4] = {};
-                if (n < a.rows) load4(rows + 4 * j, y);
+                float y[4];
+                given[nt].get(j, y);
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
                     x[4 * j + z] = y[z];
@@ -566,7 +589,7 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
     using T = std::conditional_t<F32, float, __nv_bfloat16>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t bars[C::kWarps][C::kStages];
-    __shared__ unsigned sums[C::kThreads], warp_sums[C::kWarps];
+    __shared__ unsigned sums[C::kThreads], warp_sums[C::kWarps], warp_some[C::kWarps];
     __shared__ int all_lens[C::kThreads];
     __shared__ Part parts[2 * C::kWarps];       // of each warp: what it closed, what it had last
     __shared__ unsigned trouble;
@@ -597,14 +620,26 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
         const unsigned x = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += x;
     }
-    if (lane == 31) warp_sums[warp] = sum;
-    __syncthreads();
-    unsigned tiles = 0;
-    for (int w = 0; w < C::kWarps; ++w) {
-        if (w == warp) sum += tiles;
-        tiles += warp_sums[w];
+    const unsigned some = __ballot_sync(0xffffffffu, mine > 0);
+    if (lane == 31) {
+        warp_sums[warp] = sum;
+        warp_some[warp] = __popc(some);
     }
-    sums[tid] = sum - mine;
+    __syncthreads();
+    unsigned tiles = 0, held = 0, before = __popc(some & ((1u << lane) - 1));
+    for (int w = 0; w < C::kWarps; ++w) {
+        if (w == warp) {
+            sum += tiles;
+            before += held;
+        }
+        tiles += warp_sums[w];
+        held += warp_some[w];
+    }
+    // An item counts as a tile more than it has, for its begin and end, where warps have
+    // so many tiles that one does not matter.
+    const int extra = share == 1 && tiles * (unsigned)a.items >= kMany * (unsigned)(C::kWarps * a.ctas) ? 1 : 0;
+    sums[tid] = sum - mine + (extra ? before : 0u);
+    if (extra) tiles += held;
     __syncthreads();
 
     const Split split = split_of<C::kWarps>(a, tiles);
@@ -630,15 +665,31 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
             unsigned y = sums[lo];
             at.seq = lo * share;
             at.len = length(a, lens, at.seq);
-            while (y + tiles_of<C::kTile>(at.len) <= x) {
-                y += tiles_of<C::kTile>(at.len);
+            while (y + tiles_of<C::kTile>(at.len) + extra <= x) {
+                y += tiles_of<C::kTile>(at.len) + extra;
                 at.len = length(a, lens, ++at.seq);
             }
-            const unsigned rest = u - y * (unsigned)a.items, of = (unsigned)tiles_of<C::kTile>(at.len);
+            const unsigned rest = u - y * (unsigned)a.items, of = (unsigned)(tiles_of<C::kTile>(at.len) + extra);
             at.item = (int)(rest / of);
             at.tile = (int)(rest - (unsigned)at.item * of);
         }
-        const int n = (int)(end - u);
+        // its tiles, without those that count and are none
+        int n = (int)(end - u);
+        const bool leads_cta = u == cta0;
+        if (extra) {
+            int left = n;
+            n = 0;
+            if (at.tile == tiles_of<C::kTile>(at.len)) {
+                ++u;
+                if (--left > 0) next_item(a, lens, at);
+            }
+            for (Place p = at; left > 0;) {
+                const int some = min(left, tiles_of<C::kTile>(p.len) - p.tile);
+                n += some;
+                left -= some + 1;
+                if (left > 0) next_item(a, lens, p);
+            }
+        }
         const int first_tile = at.tile;
 
         // Copies.  The lanes look up the blocks of kAhead tiles at once.  (A lookup ahead of
@@ -670,7 +721,7 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
                 load_block(ring + slot * C::kStage + lane * Layout<D>::kBytes,
                            a.pool + (unsigned long long)src * Layout<D>::kBytes, Layout<D>::kBytes,
                            &bars[warp][slot], policy);
-            if (fresh) {                             // its query rows into L2
+            if (fresh && issued > 0) {               // its query rows into L2
                 const int head = divided(ahead.item, a.by_groups);
                 const int row = (ahead.item - head * a.groups) * C::kRows + lane;
                 if (lane < C::kRows && row < a.rows) {
@@ -685,10 +736,15 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
             if (fresh && issued < n) next_item(a, lens, ahead);
         };
 
+        // the first item's queries, before the copies: behind them they would take 4000 cycles
         State<D, NT, F32> st;
+        Query<T, D> given[NT];
+        st.template fetch<T>(a, at.seq, divided(at.item, a.by_groups),
+                             at.item - divided(at.item, a.by_groups) * a.groups, given);
         for (; issued < C::kStages && issued < n;) issue(issued);
         int slot = 0, parity = 0, begin = first_tile;
-        bool start = true, closed = false, back = false;
+        st.template begin<T>(a, at.item - divided(at.item, a.by_groups) * a.groups, at.len, given);
+        bool start = false, closed = false, back = false;
         for (int done = 0; done < n; ++done) {
             const int free_slot = slot + 1 == C::kStages ? 0 : slot + 1;
             if (done + 1 == n && closed) {
@@ -704,7 +760,11 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
                 __syncwarp();
             }
             const int head = divided(at.item, a.by_groups), group = at.item - head * a.groups;
-            if (start) st.template begin<T>(a, at.seq, head, group, at.len);
+            if (start) {
+                Query<T, D> given[NT];
+                st.template fetch<T>(a, at.seq, head, group, given);
+                st.template begin<T>(a, group, at.len, given);
+            }
             start = false;
             ok = tc::mbar_wait(&bars[warp][slot], parity) && !a.lost_wait;
             ok = __all_sync(0xffffffffu, ok);
@@ -762,7 +822,7 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
             if (lane == 0) atomicMax(&trouble, (unsigned)kDevTimeout);
         }
         if (bad) atomicMax(&trouble, (unsigned)kDevBadTable);
-        if (lane == 0 && u == cta0) {                // the CTA's first tile
+        if (lane == 0 && leads_cta) {                // the CTA's first tile
             const unsigned x = u - first_tile;
             int c = min((int)((float)x / (float)split.total * split.ctas), cta);
             while (c > 0 && split.cta(c) > x) --c;
@@ -1087,7 +1147,7 @@ size_t kv4_attn_workspace_bytes(const Kv4Attn &p) {
 
 bool kv4_attn_too_large(const Kv4Attn &p) {
     const long long rows = (long long)p.B * p.Tq * p.Hq;
-    const long long tiles = (long long)p.B * ((long long)p.columns * p.page / 64 + 1);
+    const long long tiles = (long long)p.B * ((long long)p.columns * p.page / 64 + 2);
     const long long items = (long long)p.Hk * ((p.Hq / p.Hk * (long long)p.Tq + 7) / 8);
     return rows > INT32_MAX || items > INT32_MAX || (items > 0 && tiles > INT32_MAX / items);
 }

@@ -189,6 +189,76 @@ def _split(tiles, items, ctas, warps):
             for c in range(ctas)]
 
 
+def _walk(tiles, items, u, end, extra):
+    """A warp's way from place u to place end as the kernel goes it: the tiles (counted without
+    the extra ones) that it takes, and where its first item's first tile is."""
+    y = seq = 0
+    x = u // items
+    while y + (tiles[seq] + extra if tiles[seq] else 0) <= x:
+        y += tiles[seq] + extra if tiles[seq] else 0
+        seq += 1
+    item, tile = divmod(u - y * items, tiles[seq] + extra)
+
+    def following(seq, item):
+        if item + 1 < items:
+            return seq, item + 1
+        seq += 1
+        while not tiles[seq]:
+            seq += 1
+        return seq, 0
+
+    left, n, at = end - u, end - u, (seq, item)
+    if extra:
+        n = 0
+        skip = tiles[seq] + extra - tile
+        if skip <= extra:
+            u, left = u + skip, left - skip
+            if left > 0:
+                at, tile = following(*at), 0
+        p, t, rest = at, tile, left
+        while rest > 0:
+            some = min(rest, tiles[p[0]] - t)
+            n, rest = n + some, rest - some - extra
+            if rest > 0:
+                p, t = following(*p), 0
+    got, start = [], u - tile
+    for _ in range(n):
+        if tile == tiles[at[0]]:
+            at, tile = following(*at), 0
+        got.append((*at, tile))
+        tile += 1
+    return got, start
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_warps_take_every_tile_once(seed):
+    """With extra tiles for each item and without, and a CTA's first item begins where the
+    warp that has the CTA's first place says."""
+    r = random.Random(seed)
+    warps, ctas, extra = r.choice([8, 12]), r.choice([1, 3, 20]), seed % 4
+    tiles = [r.choice([0, 1, 1, 2, r.randint(0, 9), r.randint(0, 40)]) for _ in range(r.randint(1, 30))]
+    items = r.randint(1, 6)
+    counted = [n + extra if n else 0 for n in tiles]
+    begins, at = {}, 0
+    for s, n in enumerate(tiles):
+        for i in range(items):
+            begins[s, i] = at
+            at += counted[s]
+    want = [(s, i, t) for s, n in enumerate(tiles) for i in range(items) for t in range(n)]
+    got, ranges = [], _split(counted, items, ctas, warps)
+    for edges in ranges:
+        cta = []
+        for w in range(warps):
+            if edges[w] < edges[w + 1]:
+                some, start = _walk(tiles, items, edges[w], edges[w + 1], extra)
+                if edges[w] == edges[0] and some:
+                    assert start == begins[some[0][:2]]
+                cta += some
+        assert cta or not any(tiles)      # an item from an earlier CTA has a part in each between
+        got += cta
+    assert got == want
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_parts_that_are_left_are_the_parts_that_are_joined(seed):
     """The model of attention's split: every tile of an item is in one part, and the CTA that
