@@ -19,7 +19,7 @@ from operator import index
 
 import torch
 
-from .attention import _at, _call, _dense, _given, _refuse, _rows, _scale, _status, _type_code
+from .attention import _dense, _given, _refuse, _rows, _scale, _type_code
 from .binding import KlaError, load
 
 _INT = torch.int32
@@ -55,33 +55,33 @@ def _out(t, name, size, dtype, dev):
 
 
 def _run(fn, dev, args, name, sizes, workspace, check):
-    """Runs a library call with its workspace, of the size that name(*sizes) says, and the
-    stream last in the arguments."""
+    """Runs a library call with its workspace, of the size that name(*sizes) says (name None:
+    none), and the stream last in the arguments."""
     if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _run(fn, dev, args, name, sizes, workspace, check)
-    need, stream = _size(dev, name, sizes), torch._C._cuda_getCurrentRawStream(dev)
+    need, own = 0 if name is None else _size(dev, name, sizes), None
+    stream = torch._C._cuda_getCurrentRawStream(dev)
     if workspace is not None:
-        have = workspace.numel() * workspace.element_size()
+        at, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         if workspace.get_device() != dev:
             raise ValueError(f"workspace must be on cuda:{dev}, got {workspace.device}")
         if have < need:
             raise ValueError(f"workspace needs {need} bytes")
-        return _checked(fn, args, workspace.data_ptr(), have, stream, check)
-    # torch's allocator without a tensor around it (0.7 us a call, not 5): given back
-    # once the call is enqueued, for what comes behind it in the stream
-    at = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream) if need else None
+        need = have
+    elif need:
+        # torch's allocator without a tensor around it (0.7 us a call, not 5): given back
+        # once the call is enqueued, for what comes behind it in the stream
+        at = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream)
+    else:
+        at = None
     try:
-        _checked(fn, args, at, need, stream, check)
+        status = fn(*args, at, need, stream)
+        if check and not status:
+            status = load().kla_workspace_status(at, need, stream)
     finally:
-        if at is not None:
-            torch._C._cuda_cudaCachingAllocator_raw_delete(at)
-
-
-def _checked(fn, args, at, size, stream, check):
-    status = fn(*args, at, size, stream)
-    if check and not status:
-        status = load().kla_workspace_status(at, size, stream)
+        if own is not None:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(own)
     if status:
         lib = load()
         raise KlaError(status, lib.kla_last_error_message().decode() or
@@ -112,65 +112,62 @@ def kla_kv4_pool(n_pages, page, Hk, d, layers=None, device="cuda"):
                        device=device)
 
 
+# A small call takes about as long as its checks do, so these look over in one go what is
+# nearly always right; what is not is looked at again, to say what is wrong.
 def _book(table, lens, dev):
-    """The addresses of table and lens, looked over in one go: a small call takes about as
-    long as its checks do."""
+    """The addresses of table and lens."""
     size = table.shape
-    if (dev < 0 or len(size) != 2 or table.dtype is not _INT or lens.dtype is not _INT
-            or lens.get_device() != dev or lens.shape != (size[0],)
-            or not table.is_contiguous() or not lens.is_contiguous()):
-        if dev < 0:
-            raise ValueError("table must be a CUDA tensor")
-        if len(size) != 2:
-            raise ValueError(f"table must have shape [B, columns], got {tuple(size)}")
-        _dense(table, "table", _INT, dev, size)
-        _dense(lens, "lens", _INT, dev, size[:1])
-    return table.data_ptr(), lens.data_ptr()
+    if (len(size) == 2 and dev >= 0 and table.get_device() == dev and lens.get_device() == dev
+            and table.dtype is _INT and lens.dtype is _INT and lens.shape == (size[0],)
+            and table.is_contiguous() and lens.is_contiguous()):
+        return table.data_ptr(), lens.data_ptr()
+    if dev < 0:
+        raise ValueError("table must be a CUDA tensor")
+    if len(size) != 2:
+        raise ValueError(f"table must have shape [B, columns], got {tuple(size)}")
+    return _dense(table, "table", _INT, dev, size), _dense(lens, "lens", _INT, dev, size[:1])
 
 
 def _pool(pool, dev, Hk=None, d=None):
-    """The address of a layer's pool, and (Hk, d, page, n_pages)."""
+    """The address of a layer's pool, Hk, d, a page's tokens and the pages."""
     shape = pool.shape
     if len(shape) != 4:
         raise ValueError("pool must have shape [n_pages, Hk, page / 16, 18 d], got "
                          f"{tuple(shape)}")
     n_pages, heads, blocks, size = shape
     d = size // 18 if d is None else d
-    if heads != (heads if Hk is None else Hk) or size != 18 * d:
-        _refuse(pool, "pool", torch.uint8, dev, (n_pages, Hk, blocks, 18 * d))
-    return _dense(pool, "pool", torch.uint8, dev, shape), (heads, d, 16 * blocks, n_pages)
+    if (size != 18 * d or pool.dtype is not torch.uint8 or pool.get_device() != dev or dev < 0
+            or (Hk is not None and heads != Hk)):
+        _refuse(pool, "pool", torch.uint8, dev, (n_pages, heads if Hk is None else Hk, blocks, 18 * d))
+    if not pool.is_contiguous():
+        raise ValueError("pool must be contiguous")
+    return pool.data_ptr(), heads, d, 16 * blocks, n_pages
 
 
-def _word(workspace, check, like):
-    """The status word of calls that need no workspace: (workspace, its size)."""
-    if workspace is None:
-        if not check:
-            return None, 0
-        return torch.empty(256, dtype=torch.uint8, device=like.device), 256
-    if workspace.get_device() != like.get_device():
-        raise ValueError(f"workspace must be on {like.device}, got {workspace.device}")
-    return workspace, workspace.numel() * workspace.element_size()
-
-
-def _rows_call(fn, k, v, pool, table, lens, cu_seqlens, units, workspace, check):
-    dt, dev, kind, shape = _type_code(k), pool.get_device(), k.dtype, k.shape
+def _rows_call(fn, k, v, pool, table, lens, cu_seqlens, k_unit, v_unit, workspace, check):
+    kind, dev, shape, cu = k.dtype, pool.get_device(), k.shape, None
     packed = cu_seqlens is not None
     if len(shape) != (3 if packed else 4):
         raise ValueError(f"k must have shape {'[total, Hk, d]' if packed else '[B, T, Hk, d]'}, "
                          f"got {tuple(shape)}")
     T, hk, d = shape[-3:]
-    at, (hk, d, page, n_pages) = _pool(pool, dev, hk, d)
+    dt = _type_code(k)
+    at, hk, d, page, n_pages = _pool(pool, dev, hk, d)
     rows, lengths = _book(table, lens, dev)
     B, columns = table.shape
-    if not packed:
+    if packed:
+        cu = _dense(cu_seqlens, "cu_seqlens", _INT, dev, (B + 1,))
+    elif shape[0] != B:
         shape = (B, T, hk, d)
-    ks, vs = _rows(k, "k", kind, dev, shape), _rows(v, "v", kind, dev, shape)
-    cu = _dense(cu_seqlens, "cu_seqlens", _INT, dev, (B + 1,)) if packed else None
-    workspace, wsb = _word(workspace, check, pool)
-    _call(dev, fn, k.data_ptr(), ks, v.data_ptr(), vs, at, rows, lengths, cu, *units, B, T, hk, d,
-          page, n_pages, columns, dt, _at(workspace), wsb)
-    if check:
-        _call(dev, _status, workspace, wsb)
+    if (v.dtype is kind and k.get_device() == dev and v.get_device() == dev and k.shape == shape
+            and v.shape == shape and k.is_contiguous() and v.is_contiguous()):
+        ks = vs = hk * d
+    else:
+        ks, vs = _rows(k, "k", kind, dev, shape), _rows(v, "v", kind, dev, shape)
+    if check and workspace is None:
+        workspace = torch.empty(256, dtype=torch.uint8, device=pool.device)
+    _run(fn, dev, (k.data_ptr(), ks, v.data_ptr(), vs, at, rows, lengths, cu, k_unit, v_unit, B, T,
+                   hk, d, page, n_pages, columns, dt), None, None, workspace, check)
 
 
 def kla_kv4_append(k, v, pool, table, lens, cu_seqlens=None, k_unit=1.0, v_unit=1.0,
@@ -185,7 +182,7 @@ def kla_kv4_append(k, v, pool, table, lens, cu_seqlens=None, k_unit=1.0, v_unit=
         with _given(stream, pool):
             return kla_kv4_append(k, v, pool, table, lens, cu_seqlens, k_unit, v_unit, workspace,
                                   check_status=check_status)
-    _rows_call(load().kla_kv4_append, k, v, pool, table, lens, cu_seqlens, (k_unit, v_unit),
+    _rows_call(load().kla_kv4_append, k, v, pool, table, lens, cu_seqlens, k_unit, v_unit,
                workspace, check_status)
 
 
@@ -217,7 +214,7 @@ def kla_kv4_read(pool, table, lens, T=None, total=None, cu_seqlens=None, dtype=t
         _refuse(k_out, "k_out", dtype, dev, shape)
     if v_out is None:
         v_out = _out(None, "v_out", shape, k_out.dtype, dev)[0]
-    _rows_call(load().kla_kv4_read, k_out, v_out, pool, table, lens, cu_seqlens, (k_unit, v_unit),
+    _rows_call(load().kla_kv4_read, k_out, v_out, pool, table, lens, cu_seqlens, k_unit, v_unit,
                workspace, check_status)
     return k_out, v_out
 
@@ -237,8 +234,8 @@ def kla_kv4_attn(q, pool, table, lens, scale=None, k_unit=1.0, v_unit=1.0, o=Non
         raise ValueError(f"q must have shape [B, Tq, Hq, d], got {tuple(shape)}")
     dt, dev, kind = _type_code(q), q.get_device(), q.dtype
     B, Tq, hq, d = shape
-    qs = _rows(q, "q", kind, dev, shape)
-    at, (hk, d, page, n_pages) = _pool(pool, dev, d=d)
+    qs = hq * d if q.is_contiguous() and dev >= 0 else _rows(q, "q", kind, dev, shape)
+    at, hk, d, page, n_pages = _pool(pool, dev, None, d)
     rows, lengths = _book(table, lens, dev)
     if table.shape[0] != B:
         raise ValueError(f"table must have {B} rows, got {tuple(table.shape)}")

@@ -721,14 +721,15 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
                 load_block(ring + slot * C::kStage + lane * Layout<D>::kBytes,
                            a.pool + (unsigned long long)src * Layout<D>::kBytes, Layout<D>::kBytes,
                            &bars[warp][slot], policy);
-            if (fresh && issued > 0) {               // its query rows into L2
+            if (fresh && issued > 0) {               // its query rows into L1
                 const int head = divided(ahead.item, a.by_groups);
-                const int row = (ahead.item - head * a.groups) * C::kRows + lane;
-                if (lane < C::kRows && row < a.rows) {
+                const int row = (ahead.item - head * a.groups) * C::kRows + lane % C::kRows;
+                if (row < a.rows) {
                     const T *q = query<T>(a, ahead.seq, head, row);
-#pragma unroll
-                    for (int i = 0; i < D * (int)sizeof(T); i += 128)
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(q) + i));
+                    const int i = lane / C::kRows * 128;
+                    unsigned x;
+                    if (i < D * (int)sizeof(T))
+                        asm volatile("ld.global.ca.b32 %0, [%1];" : "=r"(x) : "l"(reinterpret_cast<const char *>(q) + i));
                 }
             }
             ++issued;

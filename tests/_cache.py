@@ -213,3 +213,53 @@ def compact(table, lens, refs, page):
     table = [[where[x] if c < -(-n // page) else x for c, x in enumerate(row)]
              for row, n in zip(table, lens)]
     return table, after, where, moves
+
+
+# ------------------------------------------------------------------ arguments
+def arguments(put):
+    """Right arguments of every call on a cache, their tensors where `put` takes them."""
+    hk, d, page = 2, 64, 16
+    pool = put(garbage(5, hk, 1, 18 * d, seed=1))
+    table, lens = put(torch.arange(4).int().view(2, 2)), put(torch.tensor([20, 7]).int())
+    refs, one, none = put(torch.ones(5).int()), put(torch.ones(2).int()), put(torch.tensor([0, -1]).int())
+    order, q = put(torch.arange(2).int()), put(torch.zeros(2, 1, hk, d))
+    k, v, layer = put(torch.zeros(2, 1, hk, d)), put(torch.zeros(2, 1, hk, d)), pool[None]
+    book = dict(table=table, lens=lens, refs=refs)
+    return dict(kept=(pool, table, lens, refs), calls=dict(
+        kla_kv4_append=dict(k=k, v=v, pool=pool, table=table, lens=lens),
+        kla_kv4_read=dict(pool=pool, table=table, lens=lens, T=1, k_out=k, v_out=v, dtype=torch.float32),
+        kla_kv4_attn=dict(q=q, pool=pool, table=table, lens=lens),
+        kla_pages_fork=dict(**book, src=none, dst=order, page=page),
+        kla_pages_grow=dict(pool=layer, **book, n_new=one, page=page),
+        kla_pages_trim=dict(**book, n_cut=one, page=page),
+        kla_pages_compact=dict(pool=layer, **book, page=page),
+        kla_pages_copy=dict(pool=layer, src=one, dst=order)))
+
+
+def wrong_arguments(base, host):
+    """(call, its right arguments, the one to replace, by what): on the host, of another type,
+    shape or order."""
+    for name, args in base["calls"].items():
+        for key, t in args.items():
+            if not hasattr(t, "get_device"):
+                continue
+            wrong = [host(t)]
+            layers = key == "pool" and name.startswith("kla_pages")
+            if not layers:
+                wrong.append(t.double())
+            if t.dim() == 1:
+                wrong.append(t.repeat(2)[::2])
+                if key in ("lens", "n_new", "n_cut", "src"):
+                    wrong.append(t.repeat(2))
+            if key == "table":
+                wrong += [t.repeat(1, 2)[:, ::2], t[0]]
+                if not name.startswith("kla_pages"):
+                    wrong.append(t[:1])
+            if key == "pool" and not layers:
+                wrong += [t[..., : 17 * 64], t[:, :1].expand(-1, 2, -1, -1), t[0]]
+            if layers:
+                wrong += [t[:, ::2], t[0, 0, 0, 0]]
+            if key in ("q", "k", "v", "k_out", "v_out"):
+                wrong += [t[..., :32], t[0], t.transpose(0, 2), t.expand(2, 1, 2, 64)[..., ::2]]
+            for bad in wrong:
+                yield name, args, key, bad

@@ -5,8 +5,9 @@ import random
 import pytest
 import torch
 
+import _cache
 import gated_delta_rule_kaczmarz_gb300 as kla
-from gated_delta_rule_kaczmarz_gb300 import binding
+from gated_delta_rule_kaczmarz_gb300 import binding, cache
 
 no_gpu_only = pytest.mark.skipif(torch.cuda.is_available(),
                                  reason="uses fake device pointers; host validation only")
@@ -317,3 +318,55 @@ def test_parts_that_are_left_are_the_parts_that_are_joined(seed):
         assert (found[0][1], found[-1][2]) == item
     assert not slots and set(done) == set(starts)
     assert len({c for _, _, c in owners}) == len(owners)
+
+
+class Elsewhere:
+    """A tensor that says it is on a device."""
+
+    def __init__(self, t, device=0):
+        self.t, self.at = t, device
+
+    def get_device(self):
+        return self.at
+
+    @property
+    def is_cuda(self):
+        return self.at >= 0
+
+    @property
+    def device(self):
+        return torch.device("cuda", self.at) if self.at >= 0 else torch.device("cpu")
+
+    def __getattr__(self, name):
+        x = getattr(self.t, name)
+        if name in ("double", "repeat", "expand", "transpose"):
+            return lambda *a: Elsewhere(x(*a), self.at)
+        return x
+
+    def __getitem__(self, key):
+        return Elsewhere(self.t[key], self.at)
+
+
+def test_the_binding_refuses_wrong_tensors(monkeypatch):
+    """Right arguments reach the library with their sizes; wrong ones are refused before it."""
+    reached = []
+
+    class Library:
+        def __getattr__(self, name):
+            if name.endswith("_size"):
+                return lambda *a: 0
+            return lambda *a: reached.append(name) or 0
+
+    monkeypatch.setattr(cache, "load", Library)
+    monkeypatch.setattr(cache, "_size", lambda *a: 0)
+    monkeypatch.setattr(cache, "_empty", lambda size, steps, dtype: Elsewhere(torch.empty(size, dtype=dtype)))
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0)
+    base = _cache.arguments(Elsewhere)
+    for name, args in base["calls"].items():
+        getattr(kla, name)(**args)
+    assert reached == list(base["calls"])
+    for name, args, key, bad in _cache.wrong_arguments(base, lambda t: Elsewhere(t.t, -1)):
+        with pytest.raises((ValueError, TypeError)):
+            getattr(kla, name)(**{**args, key: bad})
+            raise AssertionError((name, key, bad.shape, bad.dtype, bad.at))

@@ -219,3 +219,13 @@ def test_what_the_device_refuses():
     # lengths that no row of the table holds are clamped
     kla.kla_kv4_append(k, k, pool, table[:1], torch.tensor([1 << 30]).int().cuda(), check_status=True)
     kla.kla_kv4_append(k, k, pool, table[:1], torch.tensor([-5]).int().cuda(), check_status=True)
+
+
+def test_tensors_that_lie_elsewhere():
+    """Each argument on the host, of another type, shape or order, in turn, is refused."""
+    base = _cache.arguments(lambda t: t.cuda())
+    before = [x.clone() for x in base["kept"]]
+    for name, args, key, bad in _cache.wrong_arguments(base, lambda t: t.cpu()):
+        with pytest.raises((ValueError, TypeError)):
+            getattr(kla, name)(**{**args, key: bad})
+    assert all(torch.equal(x, y) for x, y in zip(base["kept"], before))
