@@ -21,11 +21,13 @@
 // each row, p is rounded to fp16 once (bf16) or split in two (fp32); sums are fp32.
 //
 // Measured (16 + 4 heads of 128, bf16, one token): 16 contexts of 16384 to 32768
-// 50.5 us, 256 of up to 4096 66.0, 0.70 of measured HBM bandwidth each.  The tiles
-// themselves run at 6.8 TB/s; 5.5 us pass before the first (length, table, keys: three
-// reads that wait for each other), 4.5 behind the last and 3 in the second kernel.
-// Streaming alone, without the products, took 3 us less.  221 KB of ring in flight an
-// SM are needed: 147 KB took 56 us, 110 KB 61 (an earlier form).  12 warps of 64 keys and
+// 45.5 us, 256 of up to 4096 58.0, 0.78 and 0.79 of measured HBM bandwidth.  The tiles
+// themselves run at 6.8 TB/s; the first are asked for 1.8 us after the start (length,
+// table: reads that wait for each other, and the place between them), a CTA's last warp is
+// done 2 to 3 us behind the others (a tile is a warp's), the CTA's join takes 1.2 to 2 and
+// the second kernel 2.5.  What runs once is bound by fetching its instructions, so it is short.
+// 221 KB of ring in flight an SM are needed: 147 KB took 56 us, 110 KB 61, where this took
+// 50.5 (an earlier form, as are the next figures).  12 warps of 64 keys and
 // two stages; 16 warps of 32 keys 53.0, 11 of 64 53.0.  tcgen05 takes e2m1 with its
 // scales along the contracted axis: that is so of the keys, not of the values.
 #include <cuda_bf16.h>
@@ -52,6 +54,10 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 // kLag above it: p stays below 2^15 (fp16), and what is 2^-29 of the maximum is
 // still a normal number there.
 constexpr float kTop = 7.f, kLag = 8.f;
+// From so many tiles to a warp on an item counts as a tile more in the split.  Both, in us:
+// 16 contexts (14 tiles a warp) 46.9 and 47.1, 256 contexts (19) 61.7 and 60.0, drafted tokens
+// (4) 24.7 and 23.5; a tile a warp 6.4 and 6.7.  Two tiles more: 47.1, 60.2 and 23.2, three
+// 47.8, 61.8 and 23.1.
 constexpr unsigned kMany = 2;
 
 // NT: tiles of 8 query rows.
@@ -174,7 +180,9 @@ __device__ __forceinline__ void load_words(const unsigned char *p, uint32_t (&w)
     }
 }
 
-__device__ __forceinline__ void store2(float *p, float x, float y) { *reinterpret_cast<float2 *>(p) = make_float2(x, y); }
+__device__ __forceinline__ void store2(float *p, float x, float y) {
+    *reinterpret_cast<float2 *>(p) = make_float2(x, y);
+}
 __device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) {
     *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
 }
@@ -728,8 +736,8 @@ kv4_attn_kernel(const __grid_constant__ Args a) {
                     const T *q = query<T>(a, ahead.seq, head, row);
                     const int i = lane / C::kRows * 128;
                     unsigned x;
-                    if (i < D * (int)sizeof(T))
-                        asm volatile("ld.global.ca.b32 %0, [%1];" : "=r"(x) : "l"(reinterpret_cast<const char *>(q) + i));
+                    const char *at_q = reinterpret_cast<const char *>(q) + i;
+                    if (i < D * (int)sizeof(T)) asm volatile("ld.global.ca.b32 %0, [%1];" : "=r"(x) : "l"(at_q));
                 }
             }
             ++issued;
