@@ -954,24 +954,22 @@ __global__ void __launch_bounds__(512) kv4_join_kernel(const __grid_constant__ A
     const int head = divided(own.item, a.by_groups), group = own.item - head * a.groups;
     const bool there = group * C::kRows + n < a.rows;
     // parts: of its first CTA the last item's, of the others the first item's
-    const int count = (int)blockIdx.x - own.from + 1;
+    const int count = (int)blockIdx.x - own.from + 1, stride = (2 + C::kWarps) * a.part_size;
+    const float *const parts = a.part + (size_t)own.from * stride + n * D + N * lane;      // (fewer than 2^31)
+    const int sums = a.part_rows * D + n - (n * D + N * lane);
     float base = -INFINITY, l = 0.f, v[N] = {};
     for (int k0 = 32 * sub; k0 < count && there; k0 += 32 * kPer) {
-        const int k = k0 + lane, c = own.from + k;
-        const float *part = a.part + ((size_t)min(c, (int)blockIdx.x) * (2 + C::kWarps) + (k == 0)) * a.part_size;
+        const int k = k0 + lane;
         const bool here = k < count;
-        const float m = here ? part[a.part_rows * D + n] : -INFINITY;
-        const float sum = here ? part[a.part_rows * (D + 1) + n] : 0.f;
+        const float *part = parts + (here ? k : 0) * stride + (k == 0 ? a.part_size : 0) + sums;
+        const float m = here ? part[0] : -INFINITY, sum = here ? part[a.part_rows] : 0.f;
         const int most = min(32, count - k0);
         float y[4][N] = {};                          // four parts are asked for ahead
         auto ask = [&](int j0) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (j0 + j < most) {
-                    const size_t c_of = own.from + k0 + j0 + j;
-                    const float *p = a.part + (c_of * (2 + C::kWarps) + (k0 + j0 + j == 0)) * a.part_size;
-                    load_row(p + n * D + N * lane, y[j]);
-                }
+                if (j0 + j < most)
+                    load_row(parts + (k0 + j0 + j) * stride + (k0 + j0 + j == 0 ? a.part_size : 0), y[j]);
         };
         ask(0);
         float top;
