@@ -1061,17 +1061,21 @@ int sm_count() {
 
 // Many query rows: the cache's rows are unpacked into the workspace once and go
 // through the attention of dense rows, whose tcgen05 products take 128 rows (bf16;
-// in fp32 that runs on the CUDA cores, 4 to 8 times as long as here).  Both, in us,
-// with 16 + 4 heads of 128 over 32768 keys, by tokens: 24 42 and 45, 32 51 and 46, 64
-// 83 and 55, 512 559 and 163; 16 + 2 of 64 over 4 caches of 16384: 8 26 and 32, 16 37 and
-// 35, 64 107 and 59; 8 + 8 of 64 over 1024 keys: 128 14 and 17, 512 22 and 22.
+// in fp32 that runs on the CUDA cores, 4 to 8 times as long as here), where there is
+// enough to do for that way's launches.  Both, in us, with 16 + 4 heads of 128 over 32768 keys,
+// by tokens: 24 38 and 38, 32 46 and 40, 64 78 and 48, 512 529 and 157; over 4096 keys: 32 18 and 19,
+// 64 21 and 25, 128 29 and 29, 256 47 and 32; over 8 caches of 4096: 24 39 and 40, 32 47 and 42; 16 + 2 of
+// 64 over 4 caches of 16384: 12 28 and 28, 16 33 and 30, 64 100 and 54; 8 + 8 of 64 over 1024 keys: 64
+// 10 and 15, 256 15 and 18, 512 19 and 20.  They are the same at 8 to 13 million pairs of a row and a key.
 constexpr int kUnpackRows = 128;
+constexpr long long kUnpackPairs = 12LL << 20;
 // Not where the unpacked rows, of the table's whole width, would take more than this.
 constexpr long long kUnpackBytes = 8LL << 30;
 bool unpacked(const Kv4Attn &p, AttnProblem &x, Kv4Rows &r) {
     if (p.dtype != 1 || (long long)p.Hq / p.Hk * p.Tq < kUnpackRows) return false;
     const long long keys = (long long)p.B * p.columns * p.page;
     if (keys > INT32_MAX || keys * p.Hk * p.d * 4 > kUnpackBytes) return false;
+    if (keys * ((long long)p.Tq * p.Hq) < kUnpackPairs) return false;       // (of the tables' whole width)
     x.q = p.q; x.q_stride = p.q_stride; x.out = p.o; x.lse = p.lse; x.k_lens = p.lens;
     x.k_stride = x.v_stride = (long long)p.Hk * p.d;
     x.n_seq = p.B; x.Tq = p.Tq; x.Tk = p.columns * p.page; x.total_q = p.B * p.Tq; x.total_k = (int)keys;

@@ -112,18 +112,23 @@ def filled(lens, page, columns, n_pages, hk, d, units, seed):
 
 
 U = 2.0 ** -24
-#: query rows to a key head from which the cache is unpacked for kla_attn's kernels
-LONG = 128
+#: query rows to a key head, and pairs of a query row and a key that the tables have room for,
+#: from which a bf16 cache is unpacked for kla_attn's kernels
+LONG, PAIRS = 128, 12 << 20
 
 
-def attention(q, k, v, scale):
+def unpacked(B, Tq, hq, hk, page, columns, dtype):
+    return dtype == torch.bfloat16 and Tq * hq // hk >= LONG and B * columns * page * Tq * hq >= PAIRS
+
+
+def attention(q, k, v, scale, unpacked=False):
     """One sequence, 64 bits: values and tolerances of o [Tq, Hq, d] and lse [Tq, Hq].
 
     q times k: products of fp16 parts are exact, their sums on the tensor cores are
     taken to be off by 2 u = 2^-23 an addition, and the parts of an fp32 q by 2^-22:
     e = (d + 8) 2 u max_ij sum_c |q_ic k_jc| scale.  p is off by 2 e, 2^-22 (the
-    exponential) and the rounding r of an operand (bf16 calls: fp16, 2^-11, and from
-    LONG rows to a key head on bf16, 2^-8, as in kla_attn; fp32: 2^-22); as an operand
+    exponential) and the rounding r of an operand (bf16 calls: fp16, 2^-11, and where
+    the cache is unpacked bf16, 2^-8, as in kla_attn; fp32: 2^-22); as an operand
     it has an absolute error too, 2^-25 (fp16's smallest step is 2^-24), and the largest
     p of a row is 2^7 or more: 2^-32 |v| for each key that is seen, which is all that is
     left of a row's o where the keys that matter have v = 0.  n products are summed with
@@ -131,7 +136,7 @@ def attention(q, k, v, scale):
     nq, hq, d = q.shape
     n, hk, _ = k.shape
     h, r = (2.0 ** -8, 2.0 ** -11) if q.dtype == torch.bfloat16 else (U, 2.0 ** -22)
-    if q.dtype == torch.bfloat16 and nq * hq // hk >= LONG:
+    if unpacked:
         r = 2.0 ** -8
     q = q.double().unflatten(1, (hk, hq // hk)).permute(1, 2, 0, 3)
     k, v = (x.transpose(0, 1)[:, None] for x in (k, v))

@@ -46,9 +46,11 @@ class Cache:
                         for old, x, u in zip(self.rows[s], (k, v), self.units.values())]
 
     def check(self, q, o, lse, scale):
+        (B, Tq, hq, _), hk, columns = q.shape, self.pool.shape[2], self.book[0].shape[1]
+        other = _cache.unpacked(B, Tq, hq, hk, self.page, columns, q.dtype)
         for s in range(len(q)):
             k, v = self.rows[s]
-            for got, (want, tol) in zip((o[s], lse[s]), _cache.attention(q[s].cpu(), k, v, scale)):
+            for got, (want, tol) in zip((o[s], lse[s]), _cache.attention(q[s].cpu(), k, v, scale, other)):
                 hard = ~torch.isfinite(want)
                 got = got.cpu().double()
                 assert torch.equal(got[hard], want[hard])
@@ -144,7 +146,7 @@ def test_drafted_tokens():
 def test_beside_the_dense_attention():
     """A cache's rows read back and given to kla_attn_fwd: the same within both tolerances."""
     B, n, hq, hk, d, page = 3, 400, 8, 2, 128, 64
-    c = Cache(B, 7, page, 25, hk, d)
+    c = Cache(B, 90, page, 25, hk, d)             # (100 tokens: unpacked)
     c.grow([n] * B)
     k, v, q = (_normal(B, n, h, d, seed=i) for i, h in ((1, hk), (2, hk), (3, hq)))
     kla.kla_kv4_append(k, v, c.pool[0], *c.book[:2], **c.units)
@@ -187,16 +189,16 @@ def _step(c, k, v, q, more, workspace=None):
     return kla.kla_kv4_attn(q, c.pool[0], *c.book[:2], **c.units, workspace=workspace)
 
 
-@pytest.mark.parametrize("Tq", [1, 40])
-def test_captured_steps(Tq):
+@pytest.mark.parametrize("Tq,columns", [(1, 12), (40, 12), (40, 900)])       # (900: unpacked)
+def test_captured_steps(Tq, columns):
     """A decode step captured once and replayed as the cache grows; two graphs on one workspace,
     one after the other."""
     B, hq, hk, d, page = 3, 8, 2, 64, 16
-    caches = [Cache(B, 12, page, 40, hk, d) for _ in range(2)]
+    caches = [Cache(B, columns, page, 40, hk, d) for _ in range(2)]
     k, v, q = (_normal(B, Tq, h, d, seed=i) for i, h in ((1, hk), (2, hk), (3, hq)))
     ks, vs, qs = (torch.empty_like(x) for x in (k, v, q))
     more = _ints([Tq] * B)
-    size = kla.kla_kv4_attn_workspace_size(B, Tq, hq, hk, d, page, 12)
+    size = kla.kla_kv4_attn_workspace_size(B, Tq, hq, hk, d, page, columns)
     ws = torch.empty(size, dtype=torch.uint8, device="cuda")
     for c in caches:                     # warm up, then empty again
         _step(c, k, v, q, more, ws)
@@ -272,16 +274,17 @@ def test_pool_beyond_32_bits():
     assert torch.equal(pool[n_pages - 3], pool[n_pages - 1])
 
 
-@pytest.mark.parametrize("Tq,hq,dtype", [(1, 4, BF16), (1, 4, torch.float32), (6, 4, BF16), (70, 4, BF16)])
-def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_exact(monkeypatch, Tq, hq, dtype):
+@pytest.mark.parametrize("Tq,hq,dtype,columns", [(1, 4, BF16, 63), (1, 4, torch.float32, 63), (6, 4, BF16, 63),
+                                                 (70, 4, BF16, 63), (70, 4, BF16, 320)])      # (320: unpacked)
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_exact(monkeypatch, Tq, hq, dtype, columns):
     """No hang and no fault: with KLA_TEST_LOST_WAIT set every warp gives up its first wait."""
     B, hk, d, page = 9, 2, 128, 16
-    c = Cache(B, 63, page, 600, hk, d)
+    c = Cache(B, columns, page, 600, hk, d)
     c.grow([1000, 3, 0, 640, 700, 1, 90, 900, 16])
     k, v = _normal(B, 1000, hk, d, seed=1), _normal(B, 1000, hk, d, seed=2)
     kla.kla_kv4_append(k, v, c.pool[0], *c.book[:2], **c.units)
     q = _normal(B, Tq, hq, d, seed=3).to(dtype)
-    size = kla.kla_kv4_attn_workspace_size(B, Tq, hq, hk, d, page, 63, 1 if dtype == BF16 else 0)
+    size = kla.kla_kv4_attn_workspace_size(B, Tq, hq, hk, d, page, columns, 1 if dtype == BF16 else 0)
     ws = torch.empty(size, dtype=torch.uint8, device="cuda")
     call = lambda: kla.kla_kv4_attn(q, c.pool[0], *c.book[:2], **c.units, workspace=ws, check_status=True)
     want = call()

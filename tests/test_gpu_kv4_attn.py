@@ -27,13 +27,15 @@ def _q(B, Tq, hq, d, dtype, seed):
     return torch.randn(B, Tq, hq, d, generator=torch.Generator().manual_seed(seed)).to(dtype)
 
 
-def _case(lens, Tq, hq, hk, d, page, dtype, units=(1.0, 0.5), scale=None, extra=2, seed=1):
-    columns = max(1, -(-max(lens) // page)) + 1
+def _case(lens, Tq, hq, hk, d, page, dtype, units=(1.0, 0.5), scale=None, extra=2, seed=1,
+          columns=0):
+    columns = max(columns, max(1, -(-max(lens) // page)) + 1)
     n_pages = sum(-(-n // page) for n in lens) + extra
     pool, table, held = _cache.filled(lens, page, columns, n_pages, hk, d, units, seed)
     q = _q(len(lens), Tq, hq, d, dtype, seed + 1)
     scale = scale or d ** -0.5
-    refs = [_cache.attention(x, *h, scale) for x, h in zip(q, held)]
+    other = _cache.unpacked(len(lens), Tq, hq, hk, page, columns, dtype)
+    refs = [_cache.attention(x, *h, scale, other) for x, h in zip(q, held)]
     return q, (pool.cuda(), table.cuda(), torch.tensor(lens).int().cuda()), refs, \
         dict(scale=scale, k_unit=units[0], v_unit=units[1])
 
@@ -69,6 +71,25 @@ def test_against_the_definition(lens, Tq, hq, hk, d, page, dtype):
     for b, ref in enumerate(refs):
         _check(o[b], ref[0], ("o", b))
         _check(lse[b], ref[1], ("lse", b))
+
+
+def _wide(B, Tq, hq, page):
+    """Columns from which on the cache is unpacked where there are rows enough."""
+    return -(-_cache.PAIRS // (B * Tq * hq * page))
+
+
+@pytest.mark.parametrize("lens,Tq,hq,hk,d,page", [x for x in SIZES if x[1] * x[2] // x[3] >= _cache.LONG])
+def test_unpacked_against_the_definition(lens, Tq, hq, hk, d, page):
+    """Many rows over tables of many columns, most of them empty; one column less is not unpacked."""
+    columns = _wide(len(lens), Tq, hq, page)
+    sizes = [kla.kla_kv4_attn_workspace_size(len(lens), Tq, hq, hk, d, page, c) for c in (columns - 1, columns)]
+    assert sizes[1] > len(lens) * columns * page * hk * d * 4 > sizes[0]
+    for n in (columns - 1, columns):
+        q, cache, refs, how = _case(lens, Tq, hq, hk, d, page, BF16, columns=n)
+        o, lse = kla.kla_kv4_attn(q.cuda(), *cache, **how, check_status=True)
+        for b, ref in enumerate(refs):
+            _check(o[b], ref[0], ("o", b))
+            _check(lse[b], ref[1], ("lse", b))
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
@@ -171,8 +192,12 @@ def test_bad_entries_are_reported_for_many_rows():
     _bad_entries(64)
 
 
-def _bad_entries(Tq):
-    q, (pool, table, lens), refs, how = _case([60, 40], Tq, 4, 2, 128, 16, BF16)
+def test_bad_entries_are_reported_where_the_cache_is_unpacked():
+    _bad_entries(64, _wide(2, 64, 4, 16))
+
+
+def _bad_entries(Tq, columns=0):
+    q, (pool, table, lens), refs, how = _case([60, 40], Tq, 4, 2, 128, 16, BF16, columns=columns)
     for bad in (-1, pool.shape[0], 1 << 30):
         t = table.clone()
         t[1, 1] = bad
