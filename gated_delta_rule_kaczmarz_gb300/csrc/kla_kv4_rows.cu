@@ -39,7 +39,10 @@ struct Work {
 };
 
 // Sequence and pair of a slot; false: a table that does not hold.  n rows lie in
-// n / 2 + 1 pairs at most, wherever they begin.
+// n / 2 + 1 pairs at most, wherever they begin.  WRITES: rows keep the positions that the
+// length gives them, and those behind the table's end are none; for reading a length is
+// clamped to what the table has.
+template <bool WRITES>
 __device__ __forceinline__ bool span_of(const Work &w, int slot, int &seq, int &pair, Span &s) {
     const Kv4Rows &p = w.p;
     if (p.cu) {
@@ -63,12 +66,15 @@ __device__ __forceinline__ bool span_of(const Work &w, int slot, int &seq, int &
     }
     const int most = p.columns * p.page;
     int len = p.lens[seq];
-    len = len < 0 ? 0 : (len < most ? len : most);
+    len = len < 0 ? 0 : len;
+    const int past = len > most ? len - most : 0;
+    if (!WRITES) len -= past;
     if (p.from_start) {
         s.pos0 = 0;
         s.rows = len < p.T ? len : p.T;
     } else {
         s.pos0 = len - s.rows;
+        if (WRITES) s.rows = s.rows > past ? s.rows - past : 0;
     }
     return true;
 }
@@ -207,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_const
     if (slot >= w.slots) return;
     int seq, pair;
     Span s;
-    if (!span_of(w, slot, seq, pair, s)) {
+    if (!span_of<true>(w, slot, seq, pair, s)) {
         if (p.status) *p.status = kDevBadSeqlens;
         return;
     }
@@ -291,7 +297,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
     if (slot >= w.slots) return;
     int seq, pair;
     Span s;
-    if (!span_of(w, slot, seq, pair, s)) {
+    if (!span_of<false>(w, slot, seq, pair, s)) {
         if (p.status) *p.status = kDevBadSeqlens;
         return;
     }

@@ -543,12 +543,13 @@ KLA_API int kla_attn_bwd_varlen(const void *q, long long q_stride, const void *k
  *
  * kla_kv4_append writes rows of k and v to the places of each sequence's last
  * positions: lens counts them already.  cu_seqlens NULL: k, v [B, T, Hk, d],
- * row i of sequence b goes to position lens[b] - T + i, and rows before position 0
- * are left out.  cu_seqlens (device int32 [B + 1]): packed rows [T, Hk, d], T the
- * total, sequence b's rows cu_seqlens[b] .. cu_seqlens[b+1]-1 likewise.  The table
- * must start with 0, not decrease and end with T; one that does not is reported,
- * and which rows are then written is unspecified.  Rows lie k_stride, v_stride
- * elements apart as in kla_attn_fwd.  The places must not be shared by sequences
+ * row i of sequence b goes to position lens[b] - T + i; rows before position 0 and
+ * rows that the table has no column for are left out, without a report (here a length
+ * is not clamped: no row takes another's place).  cu_seqlens (device int32 [B + 1]):
+ * packed rows [T, Hk, d], T the total, sequence b's rows cu_seqlens[b] ..
+ * cu_seqlens[b+1]-1 likewise.  The table must start with 0, not decrease and end with
+ * T; one that does not is reported, and which rows are then written is unspecified.
+ * Rows lie k_stride, v_stride elements apart as in kla_attn_fwd.  The places must not be shared by sequences
  * (kla_pages_grow sees to it); other positions keep their values.
  * kla_kv4_read is its inverse, rows before position 0 are zeros.  Read rows are
  * exact in both types.
