@@ -1079,11 +1079,14 @@ bool unpacked(const Kv4Attn &p, AttnProblem &x, Kv4Rows &r) {
     x.q = p.q; x.q_stride = p.q_stride; x.out = p.o; x.lse = p.lse; x.k_lens = p.lens;
     x.k_stride = x.v_stride = (long long)p.Hk * p.d;
     x.n_seq = p.B; x.Tq = p.Tq; x.Tk = p.columns * p.page; x.total_q = p.B * p.Tq; x.total_k = (int)keys;
-    x.Hq = p.Hq; x.Hk = p.Hk; x.d = p.d; x.dtype = p.dtype; x.scale = p.scale;
+    x.Hq = p.Hq; x.Hk = p.Hk; x.d = p.d; x.dtype = p.dtype;
+    // keys without their unit, which goes with the scale (both ways exact): fp32 holds the
+    // products of rows whose scores are in its range, whatever the unit
+    x.scale = p.scale * p.k_unit;
     r.k_stride = x.k_stride; r.v_stride = x.v_stride; r.from_start = true;
     r.pool = const_cast<void *>(p.pool); r.table = p.table; r.lens = p.lens; r.B = p.B; r.T = x.Tk;
     r.Hk = p.Hk; r.d = p.d; r.page = p.page; r.n_pages = p.n_pages; r.columns = p.columns;
-    r.dtype = p.dtype; r.k_unit = p.k_unit; r.v_unit = p.v_unit;
+    r.dtype = p.dtype; r.k_unit = 1.f; r.v_unit = p.v_unit;
     return !attn_too_large(x) && !kv4_rows_too_large(r);
 }
 // Keys' and values' places behind the attention's workspace.

@@ -575,7 +575,8 @@ KLA_API int kla_kv4_read(void *k, long long k_stride, void *v, long long v_strid
  * lse = -infinity.  What lies behind a sequence's last position may be anything; its
  * own rows must be finite for the queries before them to stay finite, as there.
  * o must not overlap q.
- * scale * k_unit from 1e-37 to 2e38.  Scores, statistics and sums are fp32;
+ * scale * k_unit from 1e-37 to 2e38.  Scores, statistics and sums are fp32, and
+ * <q, k / k_unit> and scale <q, k> have to be finite there;
  * exp(S - m) is rounded once as an operand of the second product (bf16: to fp16, or
  * to bf16 where many query rows go through kla_attn's kernels; fp32: to 22 bits), q
  * of fp32 to 22 bits; keys and values are exact.

@@ -1,4 +1,5 @@
-"""The paged 4-bit cache at its limits: rows behind the table's end."""
+"""The paged 4-bit cache at its limits: rows behind the table's end, and units at their ends
+where the cache is unpacked."""
 import pytest
 import torch
 
@@ -52,3 +53,46 @@ def test_rows_behind_the_tables_end_are_left_out(packed, dtype):
     kla.kla_kv4_append(kk, vv, dev, table.cuda(), _ints(lens), cu_seqlens=cu, check_status=True)
     _put_what_has_a_place(pool, table, lens, new, k, v, page)
     assert torch.equal(dev.cpu(), pool)
+
+
+class Long:
+    """A cache of normal rows, written by the append, and the rows' values."""
+
+    def __init__(self, lens, hk, d, page, dtype, columns=0, units=(1.0, 0.5), size=(1.0, 0.3)):
+        columns = max(columns, 1 + -(-max(lens) // page))
+        n_pages = sum(-(-n // page) for n in lens) + 1
+        table = _cache.book(lens, page, columns, n_pages, 1)
+        self.pool = _cache.garbage(n_pages, hk, page // 16, 18 * d, seed=2).cuda()
+        self.book = (table.cuda(), _ints(lens))
+        self.units = dict(k_unit=units[0], v_unit=units[1])
+        k, v = (x * _normal(sum(lens), hk, d, seed=s, dtype=FP32) for x, s in zip(size, (3, 4)))
+        k, v = k.to(dtype), v.to(dtype)
+        cu = _ints([0] + lens).cumsum(0).int()
+        kla.kla_kv4_append(k.cuda(), v.cuda(), self.pool, *self.book, cu_seqlens=cu, **self.units,
+                           check_status=True)
+        self.rows = list(zip(*(_cache.rounded(x, u).split(lens) for x, u in zip((k, v), units))))
+
+    def attn(self, q, **how):
+        return kla.kla_kv4_attn(q, self.pool, *self.book, **self.units, **how)
+
+    def check(self, q, scale, unpacked=False, got=None):
+        got = self.attn(q.cuda(), scale=scale, check_status=True) if got is None else got
+        for b, rows in enumerate(self.rows):
+            for x, (want, tol) in zip(got, _cache.attention(q[b], *rows, scale, unpacked)):
+                x, hard = x[b].cpu().double(), ~torch.isfinite(want)
+                assert torch.equal(x[hard], want[hard]), b
+                off = ((x - want).abs() / tol.clamp_min(1e-300))[~hard]
+                assert not off.numel() or float(off.max()) <= 1, (b, float(off.max()))
+        return got
+
+
+def test_units_where_the_cache_is_unpacked():
+    """Keys and queries whose products fp32 does not hold unless the keys' unit goes with the
+    scale: scale * k_unit is 2^-93."""
+    B, Tq, hq, hk, d, page = 1, 64, 4, 2, 64, 16
+    columns = -(-_cache.PAIRS // (B * Tq * hq * page))
+    c = Long([300], hk, d, page, BF16, columns, units=(2.0 ** 32, 2.0 ** -32),
+             size=(2.0 ** 33, 2.0 ** -32))
+    q = (_normal(B, Tq, hq, d, seed=5, dtype=FP32) * 2.0 ** 92).to(BF16)
+    assert _cache.unpacked(B, Tq, hq, hk, page, columns, BF16)
+    c.check(q, 2.0 ** -125, True)
