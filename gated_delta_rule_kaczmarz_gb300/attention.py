@@ -117,6 +117,8 @@ def _workspace(device, size, args, t, workspace):
     have = workspace.numel() * workspace.element_size()
     if workspace.get_device() != device:
         raise ValueError(f"workspace must be on cuda:{device}, got {workspace.device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     if have < need:
         raise ValueError(f"workspace needs {need} bytes")
     return workspace, have

@@ -229,6 +229,8 @@ def _mode(beta_mode) -> int:
 
 
 def _workspace(nbytes, device, workspace):
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     if nbytes == 0:
         # a path that needs none still records its status in a given workspace
         if workspace is None:

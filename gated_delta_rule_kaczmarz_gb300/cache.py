@@ -66,6 +66,8 @@ def _run(fn, dev, args, name, sizes, workspace, check):
         at, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         if workspace.get_device() != dev:
             raise ValueError(f"workspace must be on cuda:{dev}, got {workspace.device}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         if have < need:
             raise ValueError(f"workspace needs {need} bytes")
         need = have
