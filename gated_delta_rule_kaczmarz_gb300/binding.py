@@ -229,8 +229,11 @@ def _mode(beta_mode) -> int:
 
 
 def _workspace(nbytes, device, workspace):
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
+    if workspace is not None:
+        if workspace.device != device:
+            raise ValueError(f"workspace must be on {device}, got {workspace.device}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
     if nbytes == 0:
         # a path that needs none still records its status in a given workspace
         if workspace is None:

@@ -60,3 +60,12 @@ def test_workspaces_that_are_not_dense(name, need, monkeypatch):
     for bad in (_bytes(1).expand(1024), _bytes(2048)[::2], _bytes(32).view(1, 32).expand(32, 32)):
         with pytest.raises(ValueError, match="contiguous"):
             call(OnGpu(bad))
+
+
+@pytest.mark.parametrize("need", [512, 0])
+@pytest.mark.parametrize("name", ["cache", "attention", "binding"])
+def test_workspaces_on_another_device(name, need, monkeypatch):
+    call = _calls(monkeypatch, need)[name]
+    for device in (-1, 1):
+        with pytest.raises(ValueError, match="cuda:0"):
+            call(OnGpu(_bytes(1024), device))
