@@ -86,11 +86,6 @@ int simt_splits(const AttnProblem &p, long long blocks) {
     return cheapest_splits(blocks, ceil_div(p.total_k, (long long)p.n_seq * 64), 2 * sm_count(), 1, 1);
 }
 
-// The tensor cores take bf16 with groups that fit into a tile's 128 rows.
-bool on_tensor_cores(const AttnProblem &p) {
-    return p.dtype == 1 && p.Hq / p.Hk <= attn::kTile && p.total_k > 0 && attn_tc_ready();
-}
-
 // Parts of the key axis on the tensor cores, one CTA per SM: the number that
 // makes the whole launch shortest, counted in key tiles walked one after
 // another (waves of CTAs times the tiles of each, and 4 tiles' time for a
@@ -110,7 +105,7 @@ struct FwdPlan {
 FwdPlan fwd_plan(const AttnProblem &p) {
     FwdPlan f{};
     const int G = p.Hq / p.Hk;
-    f.tc = on_tensor_cores(p);
+    f.tc = attn_on_tensor_cores(p);
     if (f.tc) {
         f.q = side(p, false, 1, 2 * attn::tile_tokens(G));
         f.splits = tc_splits(p, f.q.items * p.Hk);
@@ -142,7 +137,7 @@ struct BwdPlan {
 BwdPlan bwd_plan(const AttnProblem &p) {
     BwdPlan b{};
     const int G = p.Hq / p.Hk;
-    b.tc = on_tensor_cores(p);
+    b.tc = attn_on_tensor_cores(p);
     if (b.tc) {
         b.q = side(p, false, 1, attn::tile_tokens(G));
         b.k = side(p, true, 1, attn::kTile);
@@ -220,6 +215,11 @@ cudaError_t allow_dynamic_smem(const void *kernel, size_t bytes) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e == cudaSuccess && n < kMost) asked[n++] = {kernel, dev};
     return e;
+}
+
+// The tensor cores take bf16 with groups that fit into a tile's 128 rows.
+bool attn_on_tensor_cores(const AttnProblem &p) {
+    return p.dtype == 1 && p.Hq / p.Hk <= attn::kTile && p.total_k > 0 && attn_tc_ready();
 }
 
 size_t attn_fwd_workspace_bytes(const AttnProblem &p) { return fwd_plan(p).bytes; }

@@ -125,6 +125,8 @@ struct AttnProblem {
     float scale;
     void *ws;                       // attn_*_workspace_bytes(p), the status word first
 };
+// Whether a forward or backward call runs on the tensor cores.
+bool attn_on_tensor_cores(const AttnProblem &p);
 size_t attn_fwd_workspace_bytes(const AttnProblem &p);
 size_t attn_bwd_workspace_bytes(const AttnProblem &p);
 bool attn_too_large(const AttnProblem &p);   // more blocks than a launch may have

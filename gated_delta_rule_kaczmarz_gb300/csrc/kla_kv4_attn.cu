@@ -1060,9 +1060,10 @@ int sm_count() {
 }
 
 // Many query rows: the cache's rows are unpacked into the workspace once and go
-// through the attention of dense rows, whose tcgen05 products take 128 rows (bf16;
-// in fp32 that runs on the CUDA cores, 4 to 8 times as long as here), where there is
-// enough to do for that way's launches.  Both, in us, with 16 + 4 heads of 128 over 32768 keys,
+// through the attention of dense rows, where that runs on the tensor cores (bf16, up to
+// 128 query heads to a key head; the CUDA cores take 4 to 8 times as long as the kernel here
+// in fp32, and 569 us for 49 with 256 + 1 heads of 128, a token over 65536 keys), whose tcgen05
+// products take 128 rows, and where there is enough to do for that way's launches.  Both, in us, with 16 + 4 heads of 128 over 32768 keys,
 // by tokens: 24 38 and 38, 32 46 and 40, 64 78 and 48, 512 529 and 157; over 4096 keys: 32 18 and 19,
 // 64 21 and 25, 128 29 and 29, 256 47 and 32; over 8 caches of 4096: 24 39 and 40, 32 47 and 42; 16 + 2 of
 // 64 over 4 caches of 16384: 12 28 and 28, 16 33 and 30, 64 100 and 54; 8 + 8 of 64 over 1024 keys: 64
@@ -1072,7 +1073,7 @@ constexpr long long kUnpackPairs = 12LL << 20;
 // Not where the unpacked rows, of the table's whole width, would take more than this.
 constexpr long long kUnpackBytes = 8LL << 30;
 bool unpacked(const Kv4Attn &p, AttnProblem &x, Kv4Rows &r) {
-    if (p.dtype != 1 || (long long)p.Hq / p.Hk * p.Tq < kUnpackRows) return false;
+    if ((long long)p.Hq / p.Hk * p.Tq < kUnpackRows) return false;
     const long long keys = (long long)p.B * p.columns * p.page;
     if (keys > INT32_MAX || keys * p.Hk * p.d * 4 > kUnpackBytes) return false;
     if (keys * ((long long)p.Tq * p.Hq) < kUnpackPairs) return false;       // (of the tables' whole width)
@@ -1087,7 +1088,7 @@ bool unpacked(const Kv4Attn &p, AttnProblem &x, Kv4Rows &r) {
     r.pool = const_cast<void *>(p.pool); r.table = p.table; r.lens = p.lens; r.B = p.B; r.T = x.Tk;
     r.Hk = p.Hk; r.d = p.d; r.page = p.page; r.n_pages = p.n_pages; r.columns = p.columns;
     r.dtype = p.dtype; r.k_unit = 1.f; r.v_unit = p.v_unit;
-    return !attn_too_large(x) && !kv4_rows_too_large(r);
+    return attn_on_tensor_cores(x) && !attn_too_large(x) && !kv4_rows_too_large(r);
 }
 // Keys' and values' places behind the attention's workspace.
 size_t unpacked_bytes(const AttnProblem &x, size_t &k, size_t &v) {

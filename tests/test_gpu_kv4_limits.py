@@ -1,5 +1,5 @@
-"""The paged 4-bit cache at its limits: rows behind the table's end, and units at their ends
-where the cache is unpacked."""
+"""The paged 4-bit cache at its limits: rows behind the table's end, units at their ends
+where the cache is unpacked, and more query heads to a key head than a tile has rows."""
 import pytest
 import torch
 
@@ -96,3 +96,14 @@ def test_units_where_the_cache_is_unpacked():
     q = (_normal(B, Tq, hq, d, seed=5, dtype=FP32) * 2.0 ** 92).to(BF16)
     assert _cache.unpacked(B, Tq, hq, hk, page, columns, BF16)
     c.check(q, 2.0 ** -125, True)
+
+
+@pytest.mark.parametrize("Tq,hq", [(1, 256), (2, 129)])
+def test_many_heads_over_many_keys(Tq, hq):
+    """More query heads to a key head than the dense attention's tensor cores take: such a cache
+    is not unpacked, however wide its table."""
+    page, d, lens = 64, 64, [3000, 70]
+    columns = -(-2 * _cache.PAIRS // (Tq * hq * page))
+    assert kla.kla_kv4_attn_workspace_size(2, Tq, hq, 1, d, page, columns) < columns * page * d * 4
+    c = Long(lens, 1, d, page, BF16, columns)
+    c.check(_normal(2, Tq, hq, d, seed=6, dtype=BF16), d ** -0.5)
