@@ -1019,9 +1019,11 @@ __global__ void __launch_bounds__(512) kv4_join_kernel(const __grid_constant__ A
     if (there) write_row<T, D>(a, out_row(a, own.seq, head, group * C::kRows + n), v, base, l);
 }
 
-// The unpacked path's check of the table, after the attention that writes the status word.
+// The unpacked path's check of the table, after the attention that writes the status word,
+// or cta_status where that is not the call's.
 __global__ void kv4_check_kernel(const __grid_constant__ Args a) {
     after_previous();
+    if (blockIdx.x == 0 && threadIdx.x == 0 && a.cta_status) atomicMax(a.status, *a.cta_status);
     const int b = blockIdx.x, page = a.blocks * kBlock, held = (int)(((long long)length(a, b) + page - 1) / page);
     for (int c = threadIdx.x; c < held; c += blockDim.x) {
         const int x = a.table[(long long)b * a.columns + c];
@@ -1060,42 +1062,69 @@ int sm_count() {
 }
 
 // Many query rows: the cache's rows are unpacked into the workspace once and go
-// through the attention of dense rows, where that runs on the tensor cores (bf16, up to
-// 128 query heads to a key head; the CUDA cores take 4 to 8 times as long as the kernel here
-// in fp32, and 569 us for 49 with 256 + 1 heads of 128, a token over 65536 keys), whose tcgen05
-// products take 128 rows, and where there is enough to do for that way's launches.  Both, in us, with 16 + 4 heads of 128 over 32768 keys,
-// by tokens: 24 38 and 38, 32 46 and 40, 64 78 and 48, 512 529 and 157; over 4096 keys: 32 18 and 19,
+// through the attention of dense rows, where that runs on the tensor cores (bf16, up
+// to 128 query heads to a key head; the CUDA cores take 4 to 8 times as long as the
+// kernel here in fp32, and 569 us for 49 with 256 + 1 heads of 128, a token over 65536
+// keys), whose tcgen05 products take 128 rows, and where there is enough to do for that
+// way's launches.  Both, in us, with 16 + 4 heads of 128 over 32768 keys, by tokens: 24
+// 38 and 38, 32 46 and 40, 64 78 and 48, 512 529 and 157; over 4096 keys: 32 18 and 19,
 // 64 21 and 25, 128 29 and 29, 256 47 and 32; over 8 caches of 4096: 24 39 and 40, 32 47 and 42; 16 + 2 of
 // 64 over 4 caches of 16384: 12 28 and 28, 16 33 and 30, 64 100 and 54; 8 + 8 of 64 over 1024 keys: 64
 // 10 and 15, 256 15 and 18, 512 19 and 20.  They are the same at 8 to 13 million pairs of a row and a key.
 constexpr int kUnpackRows = 128;
 constexpr long long kUnpackPairs = 12LL << 20;
-// Not where the unpacked rows, of the table's whole width, would take more than this.
-constexpr long long kUnpackBytes = 8LL << 30;
-bool unpacked(const Kv4Attn &p, AttnProblem &x, Kv4Rows &r) {
-    if ((long long)p.Hq / p.Hk * p.Tq < kUnpackRows) return false;
-    const long long keys = (long long)p.B * p.columns * p.page;
-    if (keys > INT32_MAX || keys * p.Hk * p.d * 4 > kUnpackBytes) return false;
-    if (keys * ((long long)p.Tq * p.Hq) < kUnpackPairs) return false;       // (of the tables' whole width)
-    x.q = p.q; x.q_stride = p.q_stride; x.out = p.o; x.lse = p.lse; x.k_lens = p.lens;
+// The unpacked rows, of the table's whole width: of as many sequences at a time as fit into
+// these bytes; not where one does not.  (A quarter of them: 8 sequences of 64 tokens, 32 + 8
+// heads of 128 over 32768 keys, 548 us in four turns and 444 in one; over 1000 keys in tables
+// as wide 184 and 111.)
+constexpr long long kUnpackBytes = 1LL << 30;
+// The n sequences from b0 on, unpacked (the workspace's places are not in it).
+void unpack_part(const Kv4Attn &p, int b0, int n, AttnProblem &x, Kv4Rows &r) {
+    const size_t es = p.dtype == 1 ? 2 : 4;
+    const long long row0 = (long long)b0 * p.Tq;
+    x.q = static_cast<const unsigned char *>(p.q) + row0 * p.q_stride * es;
+    x.out = static_cast<unsigned char *>(p.o) + row0 * p.Hq * p.d * es;
+    x.lse = p.lse ? p.lse + row0 * p.Hq : nullptr;
+    x.q_stride = p.q_stride;
     x.k_stride = x.v_stride = (long long)p.Hk * p.d;
-    x.n_seq = p.B; x.Tq = p.Tq; x.Tk = p.columns * p.page; x.total_q = p.B * p.Tq; x.total_k = (int)keys;
+    x.n_seq = n; x.Tq = p.Tq; x.Tk = p.columns * p.page; x.total_q = n * p.Tq; x.total_k = n * x.Tk;
     x.Hq = p.Hq; x.Hk = p.Hk; x.d = p.d; x.dtype = p.dtype;
     // keys without their unit, which goes with the scale (both ways exact): fp32 holds the
     // products of rows whose scores are in its range, whatever the unit
     x.scale = p.scale * p.k_unit;
     r.k_stride = x.k_stride; r.v_stride = x.v_stride; r.from_start = true;
-    r.pool = const_cast<void *>(p.pool); r.table = p.table; r.lens = p.lens; r.B = p.B; r.T = x.Tk;
-    r.Hk = p.Hk; r.d = p.d; r.page = p.page; r.n_pages = p.n_pages; r.columns = p.columns;
+    r.pool = const_cast<void *>(p.pool); r.table = p.table + (long long)b0 * p.columns; r.lens = p.lens + b0;
+    x.k_lens = r.lens;
+    r.B = n; r.T = x.Tk; r.Hk = p.Hk; r.d = p.d; r.page = p.page; r.n_pages = p.n_pages; r.columns = p.columns;
     r.dtype = p.dtype; r.k_unit = 1.f; r.v_unit = p.v_unit;
-    return attn_on_tensor_cores(x) && !attn_too_large(x) && !kv4_rows_too_large(r);
 }
-// Keys' and values' places behind the attention's workspace.
-size_t unpacked_bytes(const AttnProblem &x, size_t &k, size_t &v) {
-    const size_t rows = up256((size_t)x.total_k * x.Hk * x.d * (x.dtype == 1 ? 2 : 4));
-    k = up256(attn_fwd_workspace_bytes(x));
-    v = k + rows;
-    return v + rows;
+// How it is unpacked: `each` sequences at a time (0: it is not), and in the workspace the
+// attention's (its status word first), the keys and the values.
+struct Unpack {
+    int each;
+    size_t attn, k, v, bytes;
+};
+Unpack unpack_of(const Kv4Attn &p) {
+    Unpack u{};
+    const long long rows = (long long)p.columns * p.page, bytes = rows * p.Hk * p.d * 4;
+    if (rows == 0 || (long long)p.Hq / p.Hk * p.Tq < kUnpackRows || bytes > kUnpackBytes) return u;
+    if (rows * ((long long)p.B * p.Tq * p.Hq) < kUnpackPairs) return u;     // (of the tables' whole width)
+    const long long fit = kUnpackBytes / bytes, turns = (p.B + fit - 1) / fit;
+    const int each = (int)((p.B + turns - 1) / turns), last = (p.B - 1) % each + 1;
+    AttnProblem x{};
+    Kv4Rows r{};
+    unpack_part(p, 0, each, x, r);
+    if (!attn_on_tensor_cores(x) || attn_too_large(x) || kv4_rows_too_large(r)) return u;
+    size_t need = attn_fwd_workspace_bytes(x);
+    const size_t part = up256((size_t)each * bytes / 2);
+    unpack_part(p, 0, last, x, r);                   // (fewer sequences may have more parts)
+    if (attn_fwd_workspace_bytes(x) > need) need = attn_fwd_workspace_bytes(x);
+    u.each = each;
+    u.attn = each < p.B ? up256(kWsHeader) : 0;      // one turn: its status word is the call's
+    u.k = u.attn + up256(need);
+    u.v = u.k + part;
+    u.bytes = u.v + part;
+    return u;
 }
 
 struct Plan {
@@ -1154,10 +1183,8 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
 }  // namespace
 
 size_t kv4_attn_workspace_bytes(const Kv4Attn &p) {
-    AttnProblem x{};
-    Kv4Rows r{};
-    size_t k, v;
-    return p.columns > 0 && unpacked(p, x, r) ? unpacked_bytes(x, k, v) : plan_of(p).bytes;
+    const Unpack u = unpack_of(p);
+    return u.each ? u.bytes : plan_of(p).bytes;
 }
 
 bool kv4_attn_too_large(const Kv4Attn &p) {
@@ -1166,6 +1193,30 @@ bool kv4_attn_too_large(const Kv4Attn &p) {
     const long long items = (long long)p.Hk * ((p.Hq / p.Hk * (long long)p.Tq + 7) / 8);
     return rows > INT32_MAX || items > INT32_MAX || (items > 0 && tiles > INT32_MAX / items);
 }
+
+namespace {
+cudaError_t launch_unpacked(const Kv4Attn &p, const Unpack &u, cudaStream_t s) {
+    unsigned char *ws = static_cast<unsigned char *>(p.ws);
+    cudaError_t e = u.attn ? cudaMemsetAsync(ws, 0, sizeof(unsigned), s) : cudaSuccess;
+    for (int b0 = 0; b0 < p.B && e == cudaSuccess; b0 += u.each) {
+        const int n = p.B - b0 < u.each ? p.B - b0 : u.each;
+        AttnProblem x{};
+        Kv4Rows r{};
+        unpack_part(p, b0, n, x, r);
+        x.ws = ws + u.attn;
+        x.k = r.k_out = ws + u.k;
+        x.v = r.v_out = ws + u.v;
+        if ((e = launch_kv4_rows(r, true, s)) != cudaSuccess || (e = launch_attn_fwd(x, s)) != cudaSuccess) break;
+        Args a{};
+        a.table = r.table; a.lens = r.lens; a.columns = p.columns; a.blocks = p.page / kBlock;
+        a.n_pages = p.n_pages; a.status = static_cast<unsigned *>(p.ws);
+        a.cta_status = u.attn ? static_cast<unsigned *>(x.ws) : nullptr;
+        e = launch_next(kv4_check_kernel, n, 256, 0, 1, a, s);
+        note_launch();
+    }
+    return e;
+}
+}  // namespace
 
 cudaError_t launch_kv4_attn(const Kv4Attn &p, cudaStream_t s) {
     unsigned char *ws = static_cast<unsigned char *>(p.ws);
@@ -1177,23 +1228,8 @@ cudaError_t launch_kv4_attn(const Kv4Attn &p, cudaStream_t s) {
         note_launch();
         return cudaGetLastError();
     }
-    AttnProblem dense{};
-    Kv4Rows rows{};
-    if (unpacked(p, dense, rows)) {
-        size_t k, v;
-        unpacked_bytes(dense, k, v);
-        dense.ws = p.ws;
-        dense.k = rows.k_out = ws + k;
-        dense.v = rows.v_out = ws + v;
-        cudaError_t e = launch_kv4_rows(rows, true, s);
-        if (e != cudaSuccess || (e = launch_attn_fwd(dense, s)) != cudaSuccess) return e;
-        Args a{};
-        a.table = p.table; a.lens = p.lens; a.columns = p.columns; a.blocks = p.page / kBlock;
-        a.n_pages = p.n_pages; a.status = static_cast<unsigned *>(p.ws);
-        e = launch_next(kv4_check_kernel, p.B, 256, 0, 1, a, s);
-        note_launch();
-        return e;
-    }
+    const Unpack u = unpack_of(p);
+    if (u.each) return launch_unpacked(p, u, s);
     const Plan x = plan_of(p);
     Args a{};
     a.q = p.q; a.q_stride = p.q_stride; a.pool = static_cast<const unsigned char *>(p.pool);

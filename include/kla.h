@@ -581,7 +581,13 @@ KLA_API int kla_kv4_read(void *k, long long k_stride, void *v, long long v_strid
  * to bf16 where many query rows go through kla_attn's kernels; fp32: to 22 bits), q
  * of fp32 to 22 bits; keys and values are exact.
  * workspace: kla_kv4_attn_workspace_size(...) bytes, 256-byte aligned, the status
- * word first.  The size depends on the SM count of the current device.
+ * word first.  The size depends on the SM count of the current device.  Few query rows
+ * take some 20 MB at most.  Many (bf16; 128 and more to a key head, of up to 128 query
+ * heads; 12 * 2^20 pairs and more of a row and a position that the tables have columns
+ * for) go through kla_attn's kernels over unpacked keys and values: 4 Hk d bytes a
+ * position, of as many sequences at a time as 1 GiB holds, and where it does not hold
+ * one they are not unpacked.  The tables' width decides that, not the lengths, which only
+ * the device knows: tables much wider than their sequences cost such calls time and scratch.
  */
 KLA_API size_t kla_kv4_attn_workspace_size(int B, int Tq, int Hq, int Hk, int d, int page,
                                            int columns, int dtype);

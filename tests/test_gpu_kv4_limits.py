@@ -1,10 +1,14 @@
 """The paged 4-bit cache at its limits: rows behind the table's end, units at their ends
-where the cache is unpacked, and more query heads to a key head than a tile has rows."""
+where the cache is unpacked, more query heads to a key head than a tile has rows, and
+caches that are unpacked a few sequences at a time."""
+import random
+
 import pytest
 import torch
 
 import _cache
 import gated_delta_rule_kaczmarz_gb300 as kla
+from gated_delta_rule_kaczmarz_gb300 import binding
 
 pytestmark = pytest.mark.gpu
 BF16, FP32 = torch.bfloat16, torch.float32
@@ -107,3 +111,69 @@ def test_many_heads_over_many_keys(Tq, hq):
     assert kla.kla_kv4_attn_workspace_size(2, Tq, hq, 1, d, page, columns) < columns * page * d * 4
     c = Long(lens, 1, d, page, BF16, columns)
     c.check(_normal(2, Tq, hq, d, seed=6, dtype=BF16), d ** -0.5)
+
+
+def test_a_cache_is_unpacked_a_few_sequences_at_a_time():
+    """256 MiB of unpacked rows a sequence, 1 GiB at once: two turns of three."""
+    Tq, hq, lens = 16, 64, [700, 0, 2500, 33, 16, 900]
+    c = Long(lens, 8, 128, 64, BF16, 1024)
+    size = kla.kla_kv4_attn_workspace_size(len(lens), Tq, hq, 8, 128, 64, 1024)
+    assert 3 << 28 < size < 4 << 28
+    q = _normal(len(lens), Tq, hq, 128, seed=7, dtype=BF16)
+    wide = torch.zeros(len(lens), Tq, hq * 128 + 64, dtype=BF16, device="cuda")
+    part = wide[..., 64:].unflatten(-1, (hq, 128))
+    part.copy_(q)
+    got = c.check(q, 0.1, True, c.attn(part, scale=0.1, check_status=True))
+    alone, none = c.attn(q.cuda(), scale=0.1, return_lse=False)
+    assert none is None and torch.equal(alone, got[0])
+    # captured, on a workspace of its own
+    ws, q2 = torch.empty(size, dtype=torch.uint8, device="cuda"), q.cuda()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = c.attn(q2, scale=0.1, workspace=ws)
+    g.replay()
+    assert all(torch.equal(x, y) for x, y in zip(out, got))
+    # an entry that names no page, in each group
+    for b in (0, 2, 5):
+        table = c.book[0].clone()
+        table[b, 0] = -1
+        with pytest.raises(kla.KlaError) as e:
+            kla.kla_kv4_attn(q2, c.pool, table, c.book[1], scale=0.1, **c.units, workspace=ws, check_status=True)
+        assert e.value.status == binding.KLA_ERR_INVALID_ARG
+        o, _ = kla.kla_kv4_attn(q2, c.pool, table, c.book[1], scale=0.1, **c.units)
+        others = [s for s in range(len(lens)) if s != b]
+        assert torch.equal(o[others], got[0][others])
+    c.attn(q2, scale=0.1, workspace=ws, check_status=True)
+
+
+def test_a_wait_that_runs_out_in_any_group_is_reported(monkeypatch):
+    Tq, hq, lens = 16, 64, [700, 0, 2500, 33, 16, 900]
+    c = Long(lens, 8, 128, 64, BF16, 1024)
+    q = _normal(len(lens), Tq, hq, 128, seed=7, dtype=BF16).cuda()
+    want = c.attn(q)
+    monkeypatch.setenv("KLA_TEST_LOST_WAIT", "1")
+    with pytest.raises(kla.KlaError) as e:
+        c.attn(q, check_status=True)
+    assert e.value.status == binding.KLA_ERR_TIMEOUT
+    monkeypatch.delenv("KLA_TEST_LOST_WAIT")
+    assert all(torch.equal(x, y) for x, y in zip(c.attn(q, check_status=True), want))
+
+
+def test_a_last_turn_of_fewer_sequences():
+    """Of seven two turns, of four and of three."""
+    lens = [5, 300, 0, 64, 1000, 16, 129]
+    c = Long(lens, 8, 128, 64, BF16, 1024)
+    c.check(_normal(len(lens), 16, 64, 128, seed=8, dtype=BF16), 0.1, True)
+
+
+def test_workspaces_stay_small():
+    """Whatever the sizes: 1 GiB of unpacked rows, and the parts of the attention."""
+    r, largest = random.Random(1), 0
+    for _ in range(3000):
+        hk, d, page = r.choice([1, 2, 4, 8, 64]), r.choice([64, 128]), r.choice([16, 64, 128])
+        columns, B = 2 ** r.randint(0, 14), 2 ** r.randint(0, 8)
+        sizes = B, 2 ** r.randint(0, 10), hk * r.choice([1, 4, 7]), hk, d, page, columns
+        got = kla.kla_kv4_attn_workspace_size(*sizes)
+        largest = max(largest, got)
+        assert got < (1 << 30) + (256 << 20), sizes
+    assert largest > 1 << 30
