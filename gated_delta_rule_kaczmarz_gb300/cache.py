@@ -15,7 +15,7 @@ from __future__ import annotations
 
 import functools
 import math
-from operator import index
+from operator import attrgetter, index
 
 import torch
 
@@ -32,9 +32,21 @@ def _size(device, name, args):
         return getattr(load(), name)(*args)
 
 
+def _of_torch(name):
+    """A function of torch's own library that a small call is faster with; None where this torch
+    has none of that name, and torch.empty takes its place."""
+    try:
+        return attrgetter(name)(torch._C)
+    except AttributeError:
+        return None
+
+
 #: What compiled graphs take their buffers with, on the current device: 1.5 us of a small call
 #: where torch.empty takes 4.
-_empty = getattr(torch._C._dynamo.guards, "_empty_strided_cuda", None)
+_empty = _of_torch("_dynamo.guards._empty_strided_cuda")
+#: torch's allocator without a tensor around it: 0.7 us a call, not 5.
+_alloc = _of_torch("_cuda_cudaCachingAllocator_raw_alloc")
+_free = _of_torch("_cuda_cudaCachingAllocator_raw_delete")
 
 
 @functools.lru_cache(maxsize=1024)
@@ -71,19 +83,21 @@ def _run(fn, dev, args, name, sizes, workspace, check):
         if have < need:
             raise ValueError(f"workspace needs {need} bytes")
         need = have
-    elif need:
-        # torch's allocator without a tensor around it (0.7 us a call, not 5): given back
-        # once the call is enqueued, for what comes behind it in the stream
-        at = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream)
-    else:
+    elif not need:
         at = None
+    elif _alloc is None or _free is None:
+        kept = torch.empty(need, dtype=torch.uint8, device=dev)     # until the call is enqueued
+        at = kept.data_ptr()
+    else:
+        # given back once the call is enqueued, for what comes behind it in the stream
+        at = own = _alloc(need, stream)
     try:
         status = fn(*args, at, need, stream)
         if check and not status:
             status = load().kla_workspace_status(at, need, stream)
     finally:
         if own is not None:
-            torch._C._cuda_cudaCachingAllocator_raw_delete(own)
+            _free(own)
     if status:
         lib = load()
         raise KlaError(status, lib.kla_last_error_message().decode() or

@@ -8,7 +8,7 @@ import torch
 
 import _cache
 import gated_delta_rule_kaczmarz_gb300 as kla
-from gated_delta_rule_kaczmarz_gb300 import binding
+from gated_delta_rule_kaczmarz_gb300 import binding, cache
 
 pytestmark = pytest.mark.gpu
 BF16, FP32 = torch.bfloat16, torch.float32
@@ -177,3 +177,15 @@ def test_workspaces_stay_small():
         largest = max(largest, got)
         assert got < (1 << 30) + (256 << 20), sizes
     assert largest > 1 << 30
+
+
+@pytest.mark.parametrize("names", [("_empty",), ("_alloc",), ("_free",), ("_empty", "_alloc", "_free")])
+def test_a_torch_without_the_faster_allocations(names, monkeypatch):
+    """The same results, on outputs and workspaces that torch.empty makes."""
+    c = Long([100, 0, 33], 2, 64, 16, BF16)
+    q = _normal(3, 2, 4, 64, seed=9, dtype=BF16).cuda()
+    call = lambda: (*c.attn(q, check_status=True), *kla.kla_kv4_read(c.pool, *c.book, T=7, check_status=True))
+    want = call()
+    for name in names:
+        monkeypatch.setattr(cache, name, None)
+    assert all(torch.equal(x, y) for x, y in zip(call(), want))
