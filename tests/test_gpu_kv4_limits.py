@@ -8,18 +8,10 @@ import torch
 
 import _cache
 import gated_delta_rule_kaczmarz_gb300 as kla
+from _cache_rows import BF16, FP32, Long, ints, normal
 from gated_delta_rule_kaczmarz_gb300 import binding, cache
 
 pytestmark = pytest.mark.gpu
-BF16, FP32 = torch.bfloat16, torch.float32
-
-
-def _ints(x):
-    return torch.tensor(x, dtype=torch.int32, device="cuda")
-
-
-def _normal(*shape, seed, dtype):
-    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype)
 
 
 def _put_what_has_a_place(pool, table, lens, new, k, v, page):
@@ -48,46 +40,15 @@ def test_rows_behind_the_tables_end_are_left_out(packed, dtype):
     B = len(lens)
     table = torch.randperm(B * columns, generator=torch.Generator().manual_seed(1)).int().view(B, columns)
     pool = _cache.garbage(B * columns, hk, 1, 18 * d, seed=2)
-    k, v = (_normal(sum(new), hk, d, seed=s, dtype=dtype) for s in (3, 4))
+    k, v = (normal(sum(new), hk, d, seed=s, dtype=dtype) for s in (3, 4))
     dev, kk, vv, cu = pool.cuda(), k.cuda(), v.cuda(), None
     if packed:
-        cu = _ints([0] + new).cumsum(0).int()
+        cu = ints([0] + new).cumsum(0).int()
     else:
         kk, vv = (x.view(B, 5, hk, d) for x in (kk, vv))
-    kla.kla_kv4_append(kk, vv, dev, table.cuda(), _ints(lens), cu_seqlens=cu, check_status=True)
+    kla.kla_kv4_append(kk, vv, dev, table.cuda(), ints(lens), cu_seqlens=cu, check_status=True)
     _put_what_has_a_place(pool, table, lens, new, k, v, page)
     assert torch.equal(dev.cpu(), pool)
-
-
-class Long:
-    """A cache of normal rows, written by the append, and the rows' values."""
-
-    def __init__(self, lens, hk, d, page, dtype, columns=0, units=(1.0, 0.5), size=(1.0, 0.3)):
-        columns = max(columns, 1 + -(-max(lens) // page))
-        n_pages = sum(-(-n // page) for n in lens) + 1
-        table = _cache.book(lens, page, columns, n_pages, 1)
-        self.pool = _cache.garbage(n_pages, hk, page // 16, 18 * d, seed=2).cuda()
-        self.book = (table.cuda(), _ints(lens))
-        self.units = dict(k_unit=units[0], v_unit=units[1])
-        k, v = (x * _normal(sum(lens), hk, d, seed=s, dtype=FP32) for x, s in zip(size, (3, 4)))
-        k, v = k.to(dtype), v.to(dtype)
-        cu = _ints([0] + lens).cumsum(0).int()
-        kla.kla_kv4_append(k.cuda(), v.cuda(), self.pool, *self.book, cu_seqlens=cu, **self.units,
-                           check_status=True)
-        self.rows = list(zip(*(_cache.rounded(x, u).split(lens) for x, u in zip((k, v), units))))
-
-    def attn(self, q, **how):
-        return kla.kla_kv4_attn(q, self.pool, *self.book, **self.units, **how)
-
-    def check(self, q, scale, unpacked=False, got=None):
-        got = self.attn(q.cuda(), scale=scale, check_status=True) if got is None else got
-        for b, rows in enumerate(self.rows):
-            for x, (want, tol) in zip(got, _cache.attention(q[b], *rows, scale, unpacked)):
-                x, hard = x[b].cpu().double(), ~torch.isfinite(want)
-                assert torch.equal(x[hard], want[hard]), b
-                off = ((x - want).abs() / tol.clamp_min(1e-300))[~hard]
-                assert not off.numel() or float(off.max()) <= 1, (b, float(off.max()))
-        return got
 
 
 def test_units_where_the_cache_is_unpacked():
@@ -97,7 +58,7 @@ def test_units_where_the_cache_is_unpacked():
     columns = -(-_cache.PAIRS // (B * Tq * hq * page))
     c = Long([300], hk, d, page, BF16, columns, units=(2.0 ** 32, 2.0 ** -32),
              size=(2.0 ** 33, 2.0 ** -32))
-    q = (_normal(B, Tq, hq, d, seed=5, dtype=FP32) * 2.0 ** 92).to(BF16)
+    q = (normal(B, Tq, hq, d, seed=5, dtype=FP32) * 2.0 ** 92).to(BF16)
     assert _cache.unpacked(B, Tq, hq, hk, page, columns, BF16)
     c.check(q, 2.0 ** -125, True)
 
@@ -110,7 +71,7 @@ def test_many_heads_over_many_keys(Tq, hq):
     columns = -(-2 * _cache.PAIRS // (Tq * hq * page))
     assert kla.kla_kv4_attn_workspace_size(2, Tq, hq, 1, d, page, columns) < columns * page * d * 4
     c = Long(lens, 1, d, page, BF16, columns)
-    c.check(_normal(2, Tq, hq, d, seed=6, dtype=BF16), d ** -0.5)
+    c.check(normal(2, Tq, hq, d, seed=6, dtype=BF16), d ** -0.5)
 
 
 def test_a_cache_is_unpacked_a_few_sequences_at_a_time():
@@ -119,7 +80,7 @@ def test_a_cache_is_unpacked_a_few_sequences_at_a_time():
     c = Long(lens, 8, 128, 64, BF16, 1024)
     size = kla.kla_kv4_attn_workspace_size(len(lens), Tq, hq, 8, 128, 64, 1024)
     assert 3 << 28 < size < 4 << 28
-    q = _normal(len(lens), Tq, hq, 128, seed=7, dtype=BF16)
+    q = normal(len(lens), Tq, hq, 128, seed=7, dtype=BF16)
     wide = torch.zeros(len(lens), Tq, hq * 128 + 64, dtype=BF16, device="cuda")
     part = wide[..., 64:].unflatten(-1, (hq, 128))
     part.copy_(q)
@@ -149,7 +110,7 @@ def test_a_cache_is_unpacked_a_few_sequences_at_a_time():
 def test_a_wait_that_runs_out_in_any_group_is_reported(monkeypatch):
     Tq, hq, lens = 16, 64, [700, 0, 2500, 33, 16, 900]
     c = Long(lens, 8, 128, 64, BF16, 1024)
-    q = _normal(len(lens), Tq, hq, 128, seed=7, dtype=BF16).cuda()
+    q = normal(len(lens), Tq, hq, 128, seed=7, dtype=BF16).cuda()
     want = c.attn(q)
     monkeypatch.setenv("KLA_TEST_LOST_WAIT", "1")
     with pytest.raises(kla.KlaError) as e:
@@ -163,7 +124,7 @@ def test_a_last_turn_of_fewer_sequences():
     """Of seven two turns, of four and of three."""
     lens = [5, 300, 0, 64, 1000, 16, 129]
     c = Long(lens, 8, 128, 64, BF16, 1024)
-    c.check(_normal(len(lens), 16, 64, 128, seed=8, dtype=BF16), 0.1, True)
+    c.check(normal(len(lens), 16, 64, 128, seed=8, dtype=BF16), 0.1, True)
 
 
 def test_workspaces_stay_small():
@@ -183,7 +144,7 @@ def test_workspaces_stay_small():
 def test_a_torch_without_the_faster_allocations(names, monkeypatch):
     """The same results, on outputs and workspaces that torch.empty makes."""
     c = Long([100, 0, 33], 2, 64, 16, BF16)
-    q = _normal(3, 2, 4, 64, seed=9, dtype=BF16).cuda()
+    q = normal(3, 2, 4, 64, seed=9, dtype=BF16).cuda()
     call = lambda: (*c.attn(q, check_status=True), *kla.kla_kv4_read(c.pool, *c.book, T=7, check_status=True))
     want = call()
     for name in names:
