@@ -240,7 +240,8 @@ def kla_kv4_attn(q, pool, table, lens, scale=None, k_unit=1.0, v_unit=1.0, o=Non
     """Causal attention with grouped heads over a paged 4-bit cache.  q:
     [B,Tq,Hq,d], the last Tq positions of each sequence; query i sees the positions
     j <= i + lens - Tq; scale: 1/sqrt(d) unless given.  Returns (o, lse), o dense,
-    lse [B,Tq,Hq] fp32 (None with return_lse=False)."""
+    lse [B,Tq,Hq] fp32 (None with return_lse=False).  Many query rows in bf16 (128 to a
+    key head and more) take up to 1 GiB of workspace, by the table's width."""
     if stream is not None:
         with _given(stream, q):
             return kla_kv4_attn(q, pool, table, lens, scale, k_unit, v_unit, o, lse, return_lse,

@@ -51,8 +51,8 @@ using kv4::Layout;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 // p = 2^(s - m + kTop) with a base m that follows the maximum only when that is
-// kLag above it: p stays below 2^15 (fp16), and what is 2^-29 of the maximum is
-// still a normal number there.
+// kLag above it: a row's largest p is 2^7 to 2^15 (fp16 ends at 2^16), what is 2^-21 of
+// it is still a normal number, and below that p is off by 2^-32 of it at most.
 constexpr float kTop = 7.f, kLag = 8.f;
 // From so many tiles to a warp on an item counts as a tile more in the split.  Both, in us:
 // 16 contexts (14 tiles a warp) 46.9 and 47.1, 256 contexts (19) 61.7 and 60.0, drafted tokens

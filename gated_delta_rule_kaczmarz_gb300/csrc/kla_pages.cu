@@ -7,9 +7,9 @@
 // Each operator is one CTA, or one cluster of 8, that reads and changes the book
 // (its phases part at barriers, what they hand over goes through the workspace), and
 // where pages move a second kernel that copies those that the first listed.  The
-// first is bound by latency, a barrier and a round trip to L2 for each phase: 3 to 9
-// us.  The second is bound by HBM: 2048 pages of 36 KB in 4 layers 89 us, 0.99 of
-// measured bandwidth.
+// first is bound by latency, a barrier and a round trip to L2 for each phase: 2 to 9
+// us.  The second is bound by HBM: 2060 pages of 36 KB in 4 layers 99 us behind the
+// first, 0.91 of measured bandwidth (92 and 0.97 by itself, cold).
 #include "kla_internal.h"
 #include "kla_launch.cuh"
 
@@ -570,8 +570,8 @@ Book book_of(const Pages &p) {
 // of 64 entries 4.6 and 5.4, 40 5.9 and 5.3, 8 of 500 4.9 and 5.8.  Growth, by pages and
 // 128 for a sequence: 128 sequences among 16384 pages 5.7 and 6.8, 1024 among 131072 11.0
 // and 8.3; 256 that take 32 pages each among 16384, with the trimming behind it, 20.5 and 17.7.
-// Trimming, by sequences: 256 that lose a page or none 2.7 and 4.3, 25 pages
-// each 6.3 and 4.3.  Compaction, by pages and entries: 2048 pages with 32 x 64 6.4
+// Trimming, by sequences: 256 that lose a page or none 2.9 and 4.8, 25 pages each 8.1
+// and 6.1; 64 of 25 pages 3.8 and 5.4, 512 12.6 and 6.1.  Compaction, by pages and entries: 2048 pages with 32 x 64 6.4
 // and 8.8, 4096 with 64 x 64 8.2 and 9.1, 8192 with 64 x 64 9.9 and 9.2.
 constexpr long long kForkPieces = 32, kGrowEntries = 32768, kCompactEntries = 8192, kCopyEntries = 4096,
                     kTrimEntries = 256;

@@ -578,8 +578,9 @@ KLA_API int kla_kv4_read(void *k, long long k_stride, void *v, long long v_strid
  * scale * k_unit from 1e-37 to 2e38.  Scores, statistics and sums are fp32, and
  * <q, k / k_unit> and scale <q, k> have to be finite there;
  * exp(S - m) is rounded once as an operand of the second product (bf16: to fp16, or
- * to bf16 where many query rows go through kla_attn's kernels; fp32: to 22 bits), q
- * of fp32 to 22 bits; keys and values are exact.
+ * to bf16 where many query rows go through kla_attn's kernels; fp32: to 22 bits; what
+ * goes to fp16 is off by up to 2^-32 of its row's largest besides, and what is smaller
+ * counts in the sum alone), q of fp32 to 22 bits; keys and values are exact.
  * workspace: kla_kv4_attn_workspace_size(...) bytes, 256-byte aligned, the status
  * word first.  The size depends on the SM count of the current device.  Few query rows
  * take some 20 MB at most.  Many (bf16; 128 and more to a key head, of up to 128 query
