@@ -191,9 +191,9 @@ def kla_kv4_append(k, v, pool, table, lens, cu_seqlens=None, k_unit=1.0, v_unit=
     """Writes rows of keys and values to the places of each sequence's last
     positions (lens counts them already).  k, v: [B,T,Hk,d], or packed [total,Hk,d]
     with cu_seqlens int32 [B+1]; views of a fused projection's output among them.
-    Rows before position 0 and behind the table's last column are left out.  k_unit, v_unit: powers of two, the same
-    in every call on a cache.  check_status waits for the call and raises what the
-    device reports."""
+    Rows before position 0 and behind the table's last column are left out.  k_unit,
+    v_unit: powers of two, the same in every call on a cache.  check_status waits for
+    the call and raises what the device reports."""
     if stream is not None:
         with _given(stream, pool):
             return kla_kv4_append(k, v, pool, table, lens, cu_seqlens, k_unit, v_unit, workspace,

@@ -571,8 +571,9 @@ Book book_of(const Pages &p) {
 // 128 for a sequence: 128 sequences among 16384 pages 5.7 and 6.8, 1024 among 131072 11.0
 // and 8.3; 256 that take 32 pages each among 16384, with the trimming behind it, 20.5 and 17.7.
 // Trimming, by sequences: 256 that lose a page or none 2.9 and 4.8, 25 pages each 8.1
-// and 6.1; 64 of 25 pages 3.8 and 5.4, 512 12.6 and 6.1.  Compaction, by pages and entries: 2048 pages with 32 x 64 6.4
-// and 8.8, 4096 with 64 x 64 8.2 and 9.1, 8192 with 64 x 64 9.9 and 9.2.
+// and 6.1; 64 of 25 pages 3.8 and 5.4, 512 12.6 and 6.1.  Compaction, by pages and
+// entries: 2048 pages with 32 x 64 6.4 and 8.8, 4096 with 64 x 64 8.2 and 9.1, 8192 with
+// 64 x 64 9.9 and 9.2.
 constexpr long long kForkPieces = 32, kGrowEntries = 32768, kCompactEntries = 8192, kCopyEntries = 4096,
                     kTrimEntries = 256;
 

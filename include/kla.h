@@ -549,8 +549,8 @@ KLA_API int kla_attn_bwd_varlen(const void *q, long long q_stride, const void *k
  * packed rows [T, Hk, d], T the total, sequence b's rows cu_seqlens[b] ..
  * cu_seqlens[b+1]-1 likewise.  The table must start with 0, not decrease and end with
  * T; one that does not is reported, and which rows are then written is unspecified.
- * Rows lie k_stride, v_stride elements apart as in kla_attn_fwd.  The places must not be shared by sequences
- * (kla_pages_grow sees to it); other positions keep their values.
+ * Rows lie k_stride, v_stride elements apart as in kla_attn_fwd.  The places must not be
+ * shared by sequences (kla_pages_grow sees to it); other positions keep their values.
  * kla_kv4_read is its inverse, rows before position 0 are zeros.  Read rows are
  * exact in both types.
  * d in {64, 128}, Hk at most 1024.  The workspace may be NULL; 256 bytes or more
